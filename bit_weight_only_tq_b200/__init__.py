@@ -462,3 +462,10 @@ def tq_select_path(fmt: int, M: int, N: int, K: int, aligned: bool = True) -> in
 
 def tq_device_status() -> int:
     return int(lib.tq_device_status())
+
+
+# The mixture-of-experts calls (include/tq_moe.h); imported last, on top of the names above.
+from .moe import *  # noqa: E402,F401,F403
+from . import moe as _moe  # noqa: E402
+
+__all__ += _moe.__all__

@@ -26,7 +26,8 @@ def needs_build() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = sources() + [os.path.join(ROOT, "include", "tq.h"), __file__]
+    deps = sources() + [os.path.join(ROOT, "include", "tq.h"),
+                        os.path.join(ROOT, "include", "tq_moe.h"), __file__]
     return any(os.path.getmtime(p) > t for p in deps)
 
 

@@ -7,3 +7,6 @@
 #include "tq_batch.cu"
 #include "tq_tcbatch.cu"
 #include "tq_prefill.cu"
+#include "tq_moe.cu"
+#include "tq_experts.cu"
+#include "tq_moe_api.cu"
