@@ -83,9 +83,450 @@ static cudaError_t launch_experts_generic(const ExpertArgs& a, cudaStream_t s) {
   return launch_pdl(experts_generic_kernel<kInt4>, dim3(row_grid(a.R * ((a.N + 31) / 32), 8, 8)), dim3(256), 0, 1, s, a);
 }
 
+// ---------------------------------------------------------------------------------------------
+// The expert chunks of a launch: expert e's rows are cut into ceil(rows / TM) chunks of up to TM.
+// first[e] = chunks of the experts before e (E + 1 entries in shared memory), from the offsets
+// clamped to [0, R]; called by all nt threads of the CTA (nt <= 1024), scratch holds nt / 32 ints.
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ int expert_bound(const ExpertArgs& a, int e) {
+  const int64_t o = a.offsets[e];
+  return static_cast<int>(o < 0 ? 0 : (o < a.R ? o : a.R));
+}
+
+__device__ __forceinline__ void expert_chunks(const ExpertArgs& a, int TM, int* first, int* scratch, int nt) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int P = (a.E + nt - 1) / nt;
+  const int e0 = tid * P, e1 = e0 + P < a.E ? e0 + P : a.E;
+  int sum = 0;
+  int prev = e0 < a.E ? expert_bound(a, e0) : 0;
+  for (int e = e0; e < e1; ++e) {
+    const int next = expert_bound(a, e + 1);
+    first[e] = sum;
+    sum += next > prev ? (next - prev + TM - 1) / TM : 0;
+    prev = next;
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  int base = incl - sum, total = 0;
+  for (int w = 0; w < nt >> 5; ++w) {
+    if (w < warp) base += scratch[w];
+    total += scratch[w];
+  }
+  for (int e = e0; e < e1; ++e) first[e] += base;
+  if (tid == 0) first[a.E] = total;
+  __syncthreads();
+}
+
+// Work item `item` of a launch with `tiles` row tiles per expert: an expert's items run over its
+// chunks first, so that the chunks which share a weight tile run close together.
+struct ExpertItem {
+  int e, tile, row0, rows;  // expert, row tile of its weights, first sorted row, number of rows
+};
+__device__ __forceinline__ ExpertItem expert_item(const ExpertArgs& a, const int* first, int64_t item, int64_t tiles,
+                                                  int TM) {
+  int lo = 0, hi = a.E;  // first[lo] tiles <= item < first[lo + 1] tiles
+  const int chunk_at = static_cast<int>(item / tiles);
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= chunk_at)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int c = first[lo + 1] - first[lo];
+  const int local = static_cast<int>(item - first[lo] * tiles);
+  ExpertItem it;
+  it.e = lo;
+  it.tile = local / c;
+  const int b0 = expert_bound(a, lo), b1 = expert_bound(a, lo + 1);
+  it.row0 = b0 + (local - it.tile * c) * TM;
+  it.rows = b1 - it.row0 < TM ? b1 - it.row0 : TM;
+  return it;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Few rows per expert: bound by the packed weights' bytes.  Persistent CTAs; an item is 128 weight
+// rows of one expert times up to TM = 8 NT of its rows, all of K.  One producer warp keeps a ring
+// of stages full: 128 weight rows x 128 packed bytes by TMA (128-byte swizzle) and the rows' x by
+// one bulk copy each, running ahead across items.  Consumer warps form KG groups of four; group g
+// takes stages g, g + KG, ... of an item, warp w of it the 32 weight rows 32 w .. 32 w + 31, on
+// mma.sync m16n8k16 with the decoded weights as A (16 weight rows) and x as B (8 rows of x).
+//
+// The order of k within a product is free as long as both operands share it.  Lane (g, t) =
+// (lane / 4, lane % 4) takes 16 packed bytes of its weight rows -- 32 INT4 or 64 ternary codes of
+// consecutive k -- and the same k of x.  A 32-bit word is decoded with masks alone: nibbles (or
+// 2-bit codes) i and i + 4 (i + 8) land in the two halves of a register, in a place of the
+// fraction where their weight is 1 over a base of 1024, 256, 64 or 16; one fp16x2 subtraction
+// takes the base (and the zero-point) off, exactly.  x is brought into the same pairs by byte
+// permutes, once per warp for 32 weight rows.
+//
+// Bank conflicts: lane t's x starts 64 (128) bytes after lane t - 1's, so the lanes take their
+// words in an order that differs by t (word ^ 2 (t / 2); word ^ t for ternary) and x rows are 16
+// bytes apart modulo 128; weight row of lane group g is (g / 2) + 4 (g % 2), so that the two rows
+// of a quarter-warp access differ in the swizzle's top bit.
+// ---------------------------------------------------------------------------------------------
+constexpr int kERows = 128;       // weight rows per item
+constexpr int kEMaxRing = 8;
+constexpr int kEItems = 4;        // item descriptors in flight
+
+template <bool kInt4, int NT>
+struct SkinnyLayout {
+  static constexpr int TM = 8 * NT;
+  static constexpr int KG = NT == 1 ? 2 : 4;
+  static constexpr int kConsumers = 128 * KG;
+  static constexpr int kThreads = kConsumers + 32;
+  static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
+  static constexpr int KS = kInt4 ? 256 : 512;         // k per stage
+  static constexpr int kXRow = KS * 2 + 16;            // bytes between rows of x
+  static constexpr int kTileW = kERows * 128;
+  static constexpr int kTileX = TM * kXRow;
+  static constexpr int kPart = TM * 132 * 4;           // one group's sums [TM][132] fp32
+  static constexpr int kRing = NT == 1 ? 4 : (NT == 2 ? (kInt4 ? 6 : 5) : (kInt4 ? 4 : 3));
+  static constexpr int kOffX = kRing * kTileW;
+  static constexpr int kOffPart = kOffX + kRing * kTileX;
+  static constexpr int kOffBar = kOffPart + KG * kPart;
+  static constexpr int kOffItem = kOffBar + 2 * (kEMaxRing + kEItems) * 8;
+  static constexpr int kOffScan = kOffItem + kEItems * 32;  // descriptors of 32 bytes
+  static constexpr int kOffFirst = kOffScan + 32 * 4;
+  static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }  // 1024: alignment
+  static_assert(kRing <= kEMaxRing && kOffFirst + 1025 * 4 + 1024 <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t sel(bool c, uint32_t a, uint32_t b) { return c ? a : b; }
+
+template <bool kInt4, int NT>
+__global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayout<kInt4, NT>::kCtasPerSm)
+    experts_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w, const ExpertArgs a) {
+  using L = SkinnyLayout<kInt4, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
+  uint64_t* empty = full + kEMaxRing;
+  uint64_t* item_full = empty + kEMaxRing;
+  uint64_t* item_empty = item_full + kEItems;
+  int4* items = reinterpret_cast<int4*>(sm + L::kOffItem);  // [kEItems][2]: (e, tile, row0, rows), (row mask, ...)
+  int* scan = reinterpret_cast<int*>(sm + L::kOffScan);
+  int* first = reinterpret_cast<int*>(sm + L::kOffFirst);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_allow_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kRing; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 4);  // the four warps of the group that takes the stage
+    }
+    for (int i = 0; i < kEItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], 4 * L::KG);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tmap_w);
+  }
+  pdl_wait_prior_grids();
+  expert_chunks(a, L::TM, first, scan, L::kThreads);
+  const int64_t tiles = (a.N + kERows - 1) / kERows;
+  const int64_t total = static_cast<int64_t>(first[a.E]) * tiles;
+  const int nk = static_cast<int>((a.K + L::KS - 1) / L::KS);
+  bool ok = true;
+
+  if (warp == L::KG * 4) {
+    // ------------------------------------------------------------------ producer
+    int q = 0, n = 0;
+    for (int64_t item = blockIdx.x; item < total && ok; item += gridDim.x, ++n) {
+      const ExpertItem it = expert_item(a, first, item, tiles, L::TM);
+      int64_t xr = -1;
+      if (lane < it.rows) xr = expert_x_row(a, it.row0 + lane);
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, xr >= 0);
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x + (xr >= 0 ? xr * a.K : 0));
+      const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
+      const int d = n % kEItems;
+      if (n >= kEItems) ok = mbar_wait_warp(&item_empty[d], static_cast<uint32_t>(n / kEItems - 1) & 1u);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        items[d * 2] = make_int4(it.e, it.tile, it.row0, it.rows);
+        items[d * 2 + 1].x = static_cast<int>(mask);
+        mbar_arrive(&item_full[d]);
+      }
+      const int wrow = static_cast<int>(static_cast<int64_t>(it.e) * a.N + static_cast<int64_t>(it.tile) * kERows);
+      for (int kb = 0; kb < nk && ok; ++kb, ++q) {
+        const int s = q % L::kRing;
+        if (q >= L::kRing) ok = mbar_wait_warp(&empty[s], static_cast<uint32_t>(q / L::kRing - 1) & 1u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        const int64_t k0 = static_cast<int64_t>(kb) * L::KS;
+        const uint32_t xb = static_cast<uint32_t>((a.K - k0 < L::KS ? a.K - k0 : L::KS) * 2);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[s], L::kTileW + __popc(mask) * xb);
+          tma_load_2d(sm + s * L::kTileW, &tmap_w, &full[s], kb * 128, wrow);
+        }
+        __syncwarp();
+        if (xr >= 0 && !skipx)
+          bulk_load_1d(sm + L::kOffX + s * L::kTileX + lane * L::kXRow, src + k0 * 2, xb, &full[s]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ consumers
+    const int kg = warp >> 2, rg = warp & 3;
+    const int g = lane >> 2, t = lane & 3;
+    const int pg = (g >> 1) | ((g & 1) << 2);  // weight row of this lane group within 8
+    const int64_t G = a.K >> 7;
+    const bool sw = (t & 2) != 0, sw1 = (t & 1) != 0;
+    float* part = reinterpret_cast<float*>(sm + L::kOffPart);
+    int q0 = 0, n = 0;  // stages before this item; items before it
+    for (int64_t item = blockIdx.x; item < total; item += gridDim.x, ++n, q0 += nk) {
+      float acc[2][NT][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[m][b][c] = 0.0f;
+      const int d = n % kEItems;
+      if (ok) ok = mbar_wait_warp(&item_full[d], static_cast<uint32_t>(n / kEItems) & 1u);
+      const int4 it = items[d * 2];
+      const uint32_t rmask = static_cast<uint32_t>(items[d * 2 + 1].x);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[d]);
+      const int64_t n0 = static_cast<int64_t>(it.y) * kERows;
+      const int64_t en0 = static_cast<int64_t>(it.x) * a.N;
+      // the group scales (and zero-points) of this lane's four weight rows, loaded one of the
+      // group's stages ahead: two fp16 per register, the eight zero-points as nibbles of one
+      const __half* const sct = a.sc + (kInt4 && ok ? (en0 + n0) * G : 0);
+      const uint8_t* const zpt = kInt4 && a.zp ? a.zp + (ok ? (en0 + n0) * G : 0) : nullptr;
+      int rowG[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = rg * 32 + 8 * j + pg;
+        rowG[j] = ok && n0 + r < a.N ? static_cast<int>(r * G) : 0;  // past N: any scale, not stored
+      }
+      uint32_t sc[4] = {0u, 0u, 0u, 0u}, zp = 0x88888888u;
+      auto load_scales = [&](int kb) {
+        const int g0 = 2 * kb;
+        const bool two = g0 + 1 < G;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __half* p = sct + rowG[j] + g0;
+          sc[j] = __half_as_ushort(p[0]) | (two ? static_cast<uint32_t>(__half_as_ushort(p[1])) << 16 : 0u);
+        }
+        if (zpt) {
+          zp = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint8_t* p = zpt + rowG[j] + g0;
+            zp |= (p[0] & 15u) << (8 * j) | (two ? (p[1] & 15u) << (8 * j + 4) : 0u);
+          }
+        }
+      };
+      if (kInt4 && kg < nk) load_scales(kg);
+      for (int kb = kg; kb < nk && ok; kb += L::KG) {
+        const int q = q0 + kb, s = q % L::kRing;
+        uint32_t sc_now[4];
+        const uint32_t zp_now = zp;
+        if (kInt4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sc_now[j] = sc[j];
+          if (kb + L::KG < nk) load_scales(kb + L::KG);
+        }
+        ok = mbar_wait_warp(&full[s], static_cast<uint32_t>(q / L::kRing) & 1u);
+        if (!ok) break;
+        const uint8_t* wt = sm + s * L::kTileW + (rg * 32 + pg) * 128;
+        const uint8_t* xt = sm + L::kOffX + s * L::kTileX + g * L::kXRow;
+        // 16-byte chunks of a row that hold weights: all eight but in the last stage
+        const int64_t left = a.K - static_cast<int64_t>(kb) * L::KS;
+        const int live = left >= L::KS ? 8 : static_cast<int>(left / (kInt4 ? 32 : 64));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (4 * i >= live) break;
+          const bool in = 4 * i + t < live;  // always for INT4 (whole groups)
+          uint4 w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            w[j] = *reinterpret_cast<const uint4*>(wt + j * 8 * 128 + (((4 * i + t) ^ pg) << 4));
+            // word order of this lane: word ^ (2 (t / 2)), ternary word ^ t
+            const uint4 v = w[j];
+            const uint4 u = make_uint4(sel(sw, v.z, v.x), sel(sw, v.w, v.y), sel(sw, v.x, v.z), sel(sw, v.y, v.w));
+            w[j] = kInt4 ? u : make_uint4(sel(sw1, u.y, u.x), sel(sw1, u.x, u.y), sel(sw1, u.w, u.z), sel(sw1, u.z, u.w));
+          }
+          float grp[2][NT][4];
+          uint32_t zl[4], zh[4];  // 1024 + z and 64 + z
+          if (kInt4) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t z = ((zp_now >> (8 * j + 4 * i)) & 15u) * 0x00010001u;
+              zl[j] = 0x64006400u + z;
+              zh[j] = 0x54005400u + (z << 4);
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int b = 0; b < NT; ++b)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) grp[m][b][c] = 0.0f;
+          }
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            uint32_t wd[4] = {(&w[0].x)[p], (&w[1].x)[p], (&w[2].x)[p], (&w[3].x)[p]};
+            if (kInt4) {
+              uint32_t d[4][4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t v = wd[j], v8 = v >> 8;
+                d[j][0] = hsub2_u32((v & 0x000F000Fu) | 0x64006400u, zl[j]);
+                d[j][1] = hsub2_u32((v & 0x00F000F0u) | 0x54005400u, zh[j]);
+                d[j][2] = hsub2_u32((v8 & 0x000F000Fu) | 0x64006400u, zl[j]);
+                d[j][3] = hsub2_u32((v8 & 0x00F000F0u) | 0x54005400u, zh[j]);
+              }
+              const int piece = 4 * (4 * i + t) + (p ^ (t & 2));
+#pragma unroll
+              for (int b = 0; b < NT; ++b) {
+                const uint4 x = *reinterpret_cast<const uint4*>(xt + b * 8 * L::kXRow + piece * 16);
+                const uint32_t b0 = __byte_perm(x.x, x.z, 0x5410), b1 = __byte_perm(x.x, x.z, 0x7632);
+                const uint32_t b2 = __byte_perm(x.y, x.w, 0x5410), b3 = __byte_perm(x.y, x.w, 0x7632);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                  mma_16816(grp[m][b], d[2 * m][0], d[2 * m + 1][0], d[2 * m][1], d[2 * m + 1][1], b0, b1);
+                  mma_16816(grp[m][b], d[2 * m][2], d[2 * m + 1][2], d[2 * m][3], d[2 * m + 1][3], b2, b3);
+                }
+              }
+            } else {
+              const int piece = 8 * (4 * i + t) + 2 * (p ^ t);
+              uint4 x0[NT], x1[NT];
+#pragma unroll
+              for (int b = 0; b < NT; ++b) {
+                const uint8_t* xp = xt + b * 8 * L::kXRow + piece * 16;
+                x0[b] = in ? *reinterpret_cast<const uint4*>(xp) : make_uint4(0u, 0u, 0u, 0u);
+                x1[b] = in ? *reinterpret_cast<const uint4*>(xp + 16) : make_uint4(0u, 0u, 0u, 0u);
+              }
+              // codes j and j + 8 at bits 2 j and 16 + 2 j: j = 0..3 of v, then 4..7 of v >> 8
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t d[4][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t v = h ? wd[j] >> 8 : wd[j];
+                  d[j][0] = hsub2_u32((v & 0x00030003u) | 0x64006400u, 0x64016401u);  // 1024 + c - 1025
+                  d[j][1] = hsub2_u32((v & 0x000C000Cu) | 0x5C005C00u, 0x5C045C04u);  // 256 + c - 257
+                  d[j][2] = hsub2_u32((v & 0x00300030u) | 0x54005400u, 0x54105410u);  // 64 + c - 65
+                  d[j][3] = hsub2_u32((v & 0x00C000C0u) | 0x4C004C00u, 0x4C404C40u);  // 16 + c - 17
+                }
+#pragma unroll
+                for (int b = 0; b < NT; ++b) {
+                  const uint32_t xa = h ? x0[b].z : x0[b].x, xb = h ? x0[b].w : x0[b].y;
+                  const uint32_t ya = h ? x1[b].z : x1[b].x, yb = h ? x1[b].w : x1[b].y;
+                  const uint32_t b0 = __byte_perm(xa, ya, 0x5410), b1 = __byte_perm(xa, ya, 0x7632);
+                  const uint32_t b2 = __byte_perm(xb, yb, 0x5410), b3 = __byte_perm(xb, yb, 0x7632);
+#pragma unroll
+                  for (int m = 0; m < 2; ++m) {
+                    mma_16816(acc[m][b], d[2 * m][0], d[2 * m + 1][0], d[2 * m][1], d[2 * m + 1][1], b0, b1);
+                    mma_16816(acc[m][b], d[2 * m][2], d[2 * m + 1][2], d[2 * m][3], d[2 * m + 1][3], b2, b3);
+                  }
+                }
+              }
+            }
+          }
+          if (kInt4) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const float s0 = __half2float(__ushort_as_half(static_cast<uint16_t>(sc_now[2 * m] >> (16 * i))));
+              const float s1 = __half2float(__ushort_as_half(static_cast<uint16_t>(sc_now[2 * m + 1] >> (16 * i))));
+#pragma unroll
+              for (int b = 0; b < NT; ++b) {
+                acc[m][b][0] = fmaf(grp[m][b][0], s0, acc[m][b][0]);
+                acc[m][b][1] = fmaf(grp[m][b][1], s0, acc[m][b][1]);
+                acc[m][b][2] = fmaf(grp[m][b][2], s1, acc[m][b][2]);
+                acc[m][b][3] = fmaf(grp[m][b][3], s1, acc[m][b][3]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+      }
+      // the groups' sums, added in group order, then y
+      named_barrier_sync(1, L::kConsumers);  // the previous item's sums have been read
+      float* mine = part + kg * (L::kPart / 4);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            mine[(8 * b + 2 * t + (c & 1)) * 132 + rg * 32 + 16 * m + 8 * (c >> 1) + pg] = acc[m][b][c];
+      named_barrier_sync(1, L::kConsumers);
+      if (ok) {
+        const int64_t nn = n0 + 4 * lane;
+        float es[4] = {1.0f, 1.0f, 1.0f, 1.0f}, eb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (nn + c < a.N) {
+            if (!kInt4) es[c] = __half2float(a.sc[en0 + nn + c]);
+            if (a.bias) eb[c] = __half2float(a.bias[en0 + nn + c]);
+          }
+        }
+        for (int r = warp; r < it.w; r += 4 * L::KG) {
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if ((rmask >> r) & 1u) {  // a row outside x reads as zeros
+            v = *reinterpret_cast<const float4*>(part + r * 132 + 4 * lane);
+#pragma unroll
+            for (int k = 1; k < L::KG; ++k) {
+              const float4 u = *reinterpret_cast<const float4*>(part + k * (L::kPart / 4) + r * 132 + 4 * lane);
+              v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            }
+          }
+          __half o[4] = {__float2half_rn(fmaf(v.x, es[0], eb[0])), __float2half_rn(fmaf(v.y, es[1], eb[1])),
+                         __float2half_rn(fmaf(v.z, es[2], eb[2])), __float2half_rn(fmaf(v.w, es[3], eb[3]))};
+          __half* dst = a.y + (static_cast<int64_t>(it.z) + r) * a.N + nn;
+          if ((a.N & 3) == 0) {
+            if (nn < a.N) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (nn + c < a.N) dst[c] = o[c];
+          }
+        }
+      }
+    }
+  }
+}
+
+template <bool kInt4, int NT>
+static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
+  using L = SkinnyLayout<kInt4, NT>;
+  const uint64_t row_bytes = static_cast<uint64_t>(kInt4 ? a.K / 2 : a.K / 4);
+  CUtensorMap tw;
+  if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, row_bytes, static_cast<uint64_t>(a.E) * a.N, row_bytes, 128,
+                    kERows, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  auto* kern = experts_skinny_kernel<kInt4, NT>;
+  const int smem = L::bytes(a.E);
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  // at most min(R, E + R / TM) chunks
+  const int64_t by_rows = a.E + a.R / L::TM, chunks = a.R < by_rows ? a.R : by_rows;
+  const int64_t items = chunks * ((a.N + kERows - 1) / kERows);
+  return launch_pdl(kern, dim3(row_grid(items, 1, L::kCtasPerSm)), dim3(L::kThreads), static_cast<size_t>(smem), 1, s, tw,
+                    a);
+}
+
+template <bool kInt4>
+static cudaError_t launch_experts(int path, const ExpertArgs& a, cudaStream_t s) {
+  if (path == 3) return launch_experts_generic<kInt4>(a, s);
+  // rows per expert of an even spread; no expert has more than R rows
+  const int64_t avg = a.R / a.E;
+  if (a.R <= 8 || avg <= 4) return launch_experts_skinny<kInt4, 1>(a, s);
+  if (a.R <= 16 || avg <= 10) return launch_experts_skinny<kInt4, 2>(a, s);
+  return launch_experts_skinny<kInt4, 4>(a, s);
+}
+
 cudaError_t launch_gemm_experts(bool int4, int path, const ExpertArgs& a, cudaStream_t s) {
-  (void)path;
-  return int4 ? launch_experts_generic<true>(a, s) : launch_experts_generic<false>(a, s);
+  return int4 ? launch_experts<true>(path, a, s) : launch_experts<false>(path, a, s);
 }
 
 }  // namespace tq

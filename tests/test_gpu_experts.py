@@ -17,7 +17,7 @@ from gpu_util import bits, check_canaries, f16np, gpu, guarded_empty, need_cuda
 
 pytestmark = gpu
 FORMATS = ["ternary", "w4", "w4z"]
-PATHS = [tq.PATH_AUTO, tq.PATH_GENERIC]
+PATHS = [tq.PATH_AUTO, tq.PATH_GENERIC, tq.PATH_DECODE]
 
 
 def _gen(seed):
