@@ -23,6 +23,12 @@ struct ExpertArgs {
   int E, top_k;
 };
 
+// A named barrier of whole warps, each converged first (bar.sync is warp-aligned).
+__device__ __forceinline__ void warps_barrier(int id, int nthreads) {
+  __syncwarp();
+  named_barrier_sync(id, nthreads);
+}
+
 // The x row of sorted row r, or -1.
 __device__ __forceinline__ int64_t expert_x_row(const ExpertArgs& a, int64_t r) {
   const int64_t t = a.order ? a.order[r] / a.top_k : r;
@@ -128,6 +134,8 @@ __device__ __forceinline__ void expert_chunks(const ExpertArgs& a, int TM, int* 
 struct ExpertItem {
   int e, tile, row0, rows;  // expert, row tile of its weights, first sorted row, number of rows
 };
+// kEven: an expert's chunks hold about the same number of rows (a multiple of 16), else TM each.
+template <bool kEven>
 __device__ __forceinline__ ExpertItem expert_item(const ExpertArgs& a, const int* first, int64_t item, int64_t tiles,
                                                   int TM) {
   int lo = 0, hi = a.E;  // first[lo] tiles <= item < first[lo + 1] tiles
@@ -145,8 +153,9 @@ __device__ __forceinline__ ExpertItem expert_item(const ExpertArgs& a, const int
   it.e = lo;
   it.tile = local / c;
   const int b0 = expert_bound(a, lo), b1 = expert_bound(a, lo + 1);
-  it.row0 = b0 + (local - it.tile * c) * TM;
-  it.rows = b1 - it.row0 < TM ? b1 - it.row0 : TM;
+  const int size = kEven ? ((b1 - b0 + c - 1) / c + 15) / 16 * 16 : TM;
+  it.row0 = b0 + (local - it.tile * c) * size;
+  it.rows = b1 - it.row0 < size ? b1 - it.row0 : size;
   return it;
 }
 
@@ -154,9 +163,11 @@ __device__ __forceinline__ ExpertItem expert_item(const ExpertArgs& a, const int
 // Few rows per expert: bound by the packed weights' bytes.  Persistent CTAs; an item is 128 weight
 // rows of one expert times up to TM = 8 NT of its rows, all of K.  One producer warp keeps a ring
 // of stages full: 128 weight rows x 128 packed bytes by TMA (128-byte swizzle) and the rows' x by
-// one bulk copy each, running ahead across items.  Consumer warps form KG groups of four; group g
-// takes stages g, g + KG, ... of an item, warp w of it the 32 weight rows 32 w .. 32 w + 31, on
-// mma.sync m16n8k16 with the decoded weights as A (16 weight rows) and x as B (8 rows of x).
+// one bulk copy each, running ahead across items.  Consumer warps form KG groups of four that take
+// the CTA's stages in turn (the ring is a multiple of KG long, so that a slot has one consumer
+// group, which sees every phase of its barriers); warp w of a group takes the weight rows 32 w ..
+// 32 w + 31, on mma.sync m16n8k16 with the decoded weights as A (16 weight rows) and x as B (8
+// rows of x).
 //
 // The order of k within a product is free as long as both operands share it.  Lane (g, t) =
 // (lane / 4, lane % 4) takes 16 packed bytes of its weight rows -- 32 INT4 or 64 ternary codes of
@@ -187,7 +198,7 @@ struct SkinnyLayout {
   static constexpr int kTileW = kERows * 128;
   static constexpr int kTileX = TM * kXRow;
   static constexpr int kPart = TM * 132 * 4;           // one group's sums [TM][132] fp32
-  static constexpr int kRing = NT == 1 ? 4 : (NT == 2 ? (kInt4 ? 6 : 5) : (kInt4 ? 4 : 3));
+  static constexpr int kRing = 4;
   static constexpr int kOffX = kRing * kTileW;
   static constexpr int kOffPart = kOffX + kRing * kTileX;
   static constexpr int kOffBar = kOffPart + KG * kPart;
@@ -195,7 +206,7 @@ struct SkinnyLayout {
   static constexpr int kOffScan = kOffItem + kEItems * 32;  // descriptors of 32 bytes
   static constexpr int kOffFirst = kOffScan + 32 * 4;
   static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }  // 1024: alignment
-  static_assert(kRing <= kEMaxRing && kOffFirst + 1025 * 4 + 1024 <= 227 * 1024, "shared memory");
+  static_assert(kRing % KG == 0 && kRing <= kEMaxRing && kOffFirst + 1025 * 4 + 1024 <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ uint32_t sel(bool c, uint32_t a, uint32_t b) { return c ? a : b; }
@@ -239,7 +250,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
     // ------------------------------------------------------------------ producer
     int q = 0, n = 0;
     for (int64_t item = blockIdx.x; item < total && ok; item += gridDim.x, ++n) {
-      const ExpertItem it = expert_item(a, first, item, tiles, L::TM);
+      const ExpertItem it = expert_item<false>(a, first, item, tiles, L::TM);
       int64_t xr = -1;
       if (lane < it.rows) xr = expert_x_row(a, it.row0 + lane);
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, xr >= 0);
@@ -289,7 +300,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[m][b][c] = 0.0f;
       const int d = n % kEItems;
-      if (ok) ok = mbar_wait_warp(&item_full[d], static_cast<uint32_t>(n / kEItems) & 1u);
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&item_full[d], static_cast<uint32_t>(n / kEItems) & 1u));
       const int4 it = items[d * 2];
       const uint32_t rmask = static_cast<uint32_t>(items[d * 2 + 1].x);
       __syncwarp();
@@ -324,8 +335,9 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
           }
         }
       };
-      if (kInt4 && kg < nk) load_scales(kg);
-      for (int kb = kg; kb < nk && ok; kb += L::KG) {
+      const int kb0 = (kg + L::KG - q0 % L::KG) % L::KG;  // the group's first stage of the item
+      if (kInt4 && kb0 < nk) load_scales(kb0);
+      for (int kb = kb0; kb < nk && ok; kb += L::KG) {
         const int q = q0 + kb, s = q % L::kRing;
         uint32_t sc_now[4];
         const uint32_t zp_now = zp;
@@ -334,7 +346,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
           for (int j = 0; j < 4; ++j) sc_now[j] = sc[j];
           if (kb + L::KG < nk) load_scales(kb + L::KG);
         }
-        ok = mbar_wait_warp(&full[s], static_cast<uint32_t>(q / L::kRing) & 1u);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&full[s], static_cast<uint32_t>(q / L::kRing) & 1u));
         if (!ok) break;
         const uint8_t* wt = sm + s * L::kTileW + (rg * 32 + pg) * 128;
         const uint8_t* xt = sm + L::kOffX + s * L::kTileX + g * L::kXRow;
@@ -450,7 +462,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
         if (lane == 0) mbar_arrive(&empty[s]);
       }
       // the groups' sums, added in group order, then y
-      named_barrier_sync(1, L::kConsumers);  // the previous item's sums have been read
+      warps_barrier(1, L::kConsumers);  // the previous item's sums have been read
       float* mine = part + kg * (L::kPart / 4);
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -459,7 +471,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             mine[(8 * b + 2 * t + (c & 1)) * 132 + rg * 32 + 16 * m + 8 * (c >> 1) + pg] = acc[m][b][c];
-      named_barrier_sync(1, L::kConsumers);
+      warps_barrier(1, L::kConsumers);
       if (ok) {
         const int64_t nn = n0 + 4 * lane;
         float es[4] = {1.0f, 1.0f, 1.0f, 1.0f}, eb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -515,14 +527,421 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
                     a);
 }
 
+// ---------------------------------------------------------------------------------------------
+// Many rows per expert: a dense contraction, on tcgen05 with the decoded weights as A in tensor
+// memory (as in the prefill GEMM) and the rows of x as B in shared memory.  Persistent CTAs, one
+// per SM; an item is 128 weight rows of one expert times up to 192 of its rows, all of K.
+//
+// Tensor memory holds two accumulators of 192 columns and four slots of decoded weights (32
+// columns = 64 k), so that an item's epilogue runs under the next item's MMAs; the MMA's N is the
+// item's own number of rows rounded up to 16 (an expert's rows are cut evenly), so a ragged expert
+// costs its rows and not a full tile.  20 warps:
+//   warp 0      x of a stage (64 k, 128-byte swizzle): boxes of 32 sorted rows, or, through
+//               `order`, four rows per instruction (tile::gather4) issued by the whole warp;
+//   warp 1      allocates tensor memory; one lane issues the MMAs;
+//   warp 2      packed weights, 128 rows x 128 bytes per load (4 INT4 / 8 ternary stages);
+//   warp 3      finds the items (a search in the chunk table) and hands them to the others
+//               through a ring of descriptors, ahead of their use;
+//   warps 4-15  three groups of four that decode every third stage of the CTA (counted across
+//               items: having waited for the MMAs of the stage seven before, a group finds the
+//               slot's barrier in one of two phases); thread = weight row = tensor
+//               memory lane, 64 weights into 32 registers and one tcgen05.st; the row's next group
+//               scale (and zero-point) is loaded a stage ahead, the next item's first one an item
+//               ahead;
+//   warps 16-19 the epilogue: tcgen05.ld, row scale and bias, fp16, rows of y through a staging
+//               buffer.
+// One barrier per stage counts x's bytes and the four decode warps; one commit frees both.
+// ---------------------------------------------------------------------------------------------
+constexpr int kTTok = 192;       // rows of x per item (MMA N)
+constexpr int kTBox = 32;        // sorted rows per x load
+constexpr int kTRing = 4;        // stages of x and of decoded weights
+constexpr int kTPRing = 3;       // packed tiles
+constexpr int kTDec = 3;         // decode groups
+constexpr int kTThreads = 32 * (4 + 4 * kTDec + 4);
+constexpr int kTItems = 4;
+
+template <bool kInt4>
+struct ExpertTcLayout {
+  static constexpr int SPP = kInt4 ? 4 : 8;  // stages per packed tile
+  static constexpr int kTileX = kTTok * 128;
+  static constexpr int kTileP = kERows * 128;
+  static constexpr int kStage = 32 * kERows * 2;  // 32 rows of y, 128 columns
+  static constexpr int kOffX = 0;
+  static constexpr int kOffP = kTRing * kTileX;
+  static constexpr int kOffY = kOffP + kTPRing * kTileP;
+  static constexpr int kOffBar = kOffY + kStage;
+  // full[R], empty[R], fullP[RP], emptyP[RP], accFull[2], accEmpty[2], itemFull[I], itemEmpty[I]
+  static constexpr int kNumBars = 2 * kTRing + 2 * kTPRing + 4 + 2 * kTItems;
+  static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kOffMisc = kOffItem + kTItems * 16;  // TMEM slot, epilogue flags
+  static constexpr int kOffScan = kOffMisc + 32;
+  static constexpr int kOffFirst = kOffScan + 32 * 4;
+  static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }
+  static constexpr uint32_t kColA = 2 * kTTok;
+  static_assert(2 * kTTok + 32 * kTRing <= 512, "tensor memory");
+  static_assert(kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 && kOffFirst > 114 * 1024, "one CTA per SM");
+};
+
+template <bool kInt4, bool kOrder>
+__global__ void __launch_bounds__(kTThreads, 1)
+    experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                      const ExpertArgs a) {
+  using L = ExpertTcLayout<kInt4>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
+  uint64_t* empty = full + kTRing;
+  uint64_t* fullP = empty + kTRing;
+  uint64_t* emptyP = fullP + kTPRing;
+  uint64_t* acc_full = emptyP + kTPRing;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* item_full = acc_empty + 2;
+  uint64_t* item_empty = item_full + kTItems;
+  int4* items = reinterpret_cast<int4*>(sm + L::kOffItem);  // (e, tile, row0, rows)
+  uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kOffMisc);
+  int* first = reinterpret_cast<int*>(sm + L::kOffFirst);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_allow_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTRing; ++i) {
+      mbar_init(&full[i], 5);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kTPRing; ++i) {
+      mbar_init(&fullP[i], 1);
+      mbar_init(&emptyP[i], 4 * kTDec);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    for (int i = 0; i < kTItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], 3 + 4 * kTDec + 4);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tmap_x);
+    tma_prefetch_desc(&tmap_w);
+  }
+  if (threadIdx.x == 32) misc[1] = 0u;
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc(misc, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  pdl_wait_prior_grids();
+  expert_chunks(a, kTTok, first, reinterpret_cast<int*>(sm + L::kOffScan), kTThreads);  // synchronises
+  tc_fence_after_sync();
+  const uint32_t tmem = misc[0];
+  const int64_t tiles = (a.N + kERows - 1) / kERows;
+  const int64_t total = static_cast<int64_t>(first[a.E]) * tiles;
+  const int nk = static_cast<int>(a.K / 64);
+  const int npt = (nk + L::SPP - 1) / L::SPP;
+  // items of this CTA
+  const int count = static_cast<int>(total > blockIdx.x ? (total - blockIdx.x + gridDim.x - 1) / gridDim.x : 0);
+  bool ok = true;
+
+  // Item n of this CTA; every role but warp 3 reads each item once and releases it.
+  auto take_item = [&](int n, int4* it) {
+    const int d = n % kTItems;
+    const bool got = mbar_wait_warp(&item_full[d], static_cast<uint32_t>(n / kTItems) & 1u);
+    *it = items[d];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[d]);
+    return got;
+  };
+
+  if (warp == 3) {
+    // ------------------------------------------------------------------ items
+    for (int n = 0; n < count && ok; ++n) {
+      const ExpertItem it = expert_item<true>(a, first, blockIdx.x + static_cast<int64_t>(n) * gridDim.x, tiles, kTTok);
+      const int d = n % kTItems;
+      if (n >= kTItems) ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&item_empty[d], static_cast<uint32_t>(n / kTItems - 1) & 1u));
+      if (ok && lane == 0) {
+        items[d] = make_int4(it.e, it.tile, it.row0, it.rows);
+        mbar_arrive(&item_full[d]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 0) {
+    // ------------------------------------------------------------------ x
+    int q = 0;
+    const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
+    int4 nx;
+    int rows[8];  // kOrder: x rows of the four rows at 4 lane and 4 (lane + 32)
+    auto find_rows = [&](const int4& it) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        int r = 4 * (lane + 32 * (j >> 2)) + (j & 3);
+        r = it.z + (r < it.w ? r : it.w - 1);
+        const int64_t xr = expert_x_row(a, r);
+        rows[j] = xr < 0 ? 0 : static_cast<int>(xr);  // masked in the epilogue
+      }
+    };
+    if (count > 0) ok = __all_sync(0xFFFFFFFFu, take_item(0, &nx));
+    if (kOrder && count > 0 && ok) find_rows(nx);
+    for (int n = 0; n < count && ok; ++n) {
+      const int4 it = nx;
+      int now[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) now[j] = kOrder ? rows[j] : 0;
+      if (n + 1 < count) {  // the next item's rows are looked up under this item's loads
+        ok = __all_sync(0xFFFFFFFFu, take_item(n + 1, &nx));
+        if (!ok) break;
+        if (kOrder) find_rows(nx);
+      }
+      const int n16 = (it.w + 15) / 16 * 16;
+      const int boxes = (n16 + kTBox - 1) / kTBox;
+      for (int kb = 0; kb < nk && ok && !skipx; ++kb, ++q) {
+        const int s = q % kTRing;
+        if (q >= kTRing) ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&empty[s], static_cast<uint32_t>(q / kTRing - 1) & 1u));
+        if (!ok) break;
+        uint8_t* dst = sm + L::kOffX + s * L::kTileX;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], kOrder ? n16 * 128 : boxes * kTBox * 128);
+        __syncwarp();
+        if (kOrder) {
+          if (4 * lane < n16) tma_gather4(dst + lane * 512, &tmap_x, &full[s], kb * 64, now[0], now[1], now[2], now[3]);
+          if (4 * (lane + 32) < n16)
+            tma_gather4(dst + (lane + 32) * 512, &tmap_x, &full[s], kb * 64, now[4], now[5], now[6], now[7]);
+        } else if (lane < boxes) {
+          tma_load_2d(dst + lane * kTBox * 128, &tmap_x, &full[s], kb * 64, it.z + lane * kTBox);
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ packed weights
+    int pq = 0;
+    for (int n = 0; n < count && ok; ++n) {
+      int4 it;
+      ok = __all_sync(0xFFFFFFFFu, take_item(n, &it));
+      if (!ok) break;
+      const int row = static_cast<int>(static_cast<int64_t>(it.x) * a.N + static_cast<int64_t>(it.y) * kERows);
+      for (int pt = 0; pt < npt && ok; ++pt, ++pq) {
+        const int s = pq % kTPRing;
+        if (pq >= kTPRing) ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&emptyP[s], static_cast<uint32_t>(pq / kTPRing - 1) & 1u));
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&fullP[s], L::kTileP);
+          tma_load_2d(sm + L::kOffP + s * L::kTileP, &tmap_w, &fullP[s], pt * 128, row);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA
+    int q = 0;
+    const uint32_t x_base = smem_u32(sm + L::kOffX);
+    for (int n = 0; n < count && ok; ++n) {
+      int4 it;
+      ok = __all_sync(0xFFFFFFFFu, take_item(n, &it));
+      if (!ok) break;
+      if (lane == 0) {
+        const uint32_t idesc = idesc_f16_f32(kERows, static_cast<uint32_t>((it.w + 15) / 16 * 16));
+        const uint32_t acc = tmem + (n & 1) * kTTok;
+        if (n >= 2) ok = mbar_wait(&acc_empty[n & 1], static_cast<uint32_t>(n / 2 - 1) & 1u);
+        for (int kb = 0; kb < nk && ok; ++kb, ++q) {
+          const int s = q % kTRing;
+          ok = mbar_wait(&full[s], static_cast<uint32_t>(q / kTRing) & 1u);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint64_t bdesc = sdesc_kmajor_sw128(x_base + s * L::kTileX);
+#pragma unroll
+          for (int k16 = 0; k16 < 4; ++k16)
+            umma_f16_ts(acc, tmem + L::kColA + 32 * s + 8 * k16, bdesc + 2 * k16, idesc, (kb | k16) != 0 ? 1u : 0u);
+          umma_commit(&empty[s]);
+        }
+        if (ok) umma_commit(&acc_full[n & 1]);
+      }
+      __syncwarp();
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    }
+  } else if (warp < 4 + 4 * kTDec) {
+    // ------------------------------------------------------------------ decode
+    const int dg = (warp >> 2) - 1;
+    const int r = threadIdx.x & (kERows - 1);
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + L::kColA;
+    const int64_t G = a.K >> 7;
+    const uint8_t* prow0 = sm + L::kOffP + r * 128;
+    int4 nx;
+    const __half* scp = a.sc;   // scales / zero-points of this thread's weight row
+    const uint8_t* zpp = a.zp;
+    uint32_t sc_nxt = 0, zp_nxt = 8;
+    auto fetch = [&](int64_t gi) {  // group scale (both halves) and zero-point
+      const uint32_t h = __half_as_ushort(scp[gi]);
+      sc_nxt = h | (h << 16);
+      if (zpp) zp_nxt = zpp[gi] & 15u;
+    };
+    auto start_item = [&](const int4& it, int kb) {  // the group's first stage of the item is kb
+      const int64_t n = static_cast<int64_t>(it.y) * kERows + r;
+      const int64_t row = (static_cast<int64_t>(it.x) * a.N + (n < a.N ? n : 0)) * G;  // past N: not stored
+      scp = a.sc + row;
+      if (a.zp) zpp = a.zp + row;
+      fetch(kb >> 1);
+    };
+    int q0 = 0, pq = 0;
+    int qn = dg;         // the group's next stage
+    bool ready = false;  // its scale has been fetched
+    if (count > 0) ok = __all_sync(0xFFFFFFFFu, take_item(0, &nx));
+    for (int n = 0; n < count && ok; ++n, q0 += nk) {
+      const bool more = n + 1 < count;
+      if (kInt4 && !ready && qn < q0 + nk) start_item(nx, qn - q0);
+      ready = false;
+      if (more) ok = __all_sync(0xFFFFFFFFu, take_item(n + 1, &nx));
+      for (int pt = 0; pt < npt && ok; ++pt, ++pq) {
+        const int ps = pq % kTPRing;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&fullP[ps], static_cast<uint32_t>(pq / kTPRing) & 1u));
+        const uint8_t* prow = prow0 + ps * L::kTileP;
+        const int last = nk - pt * L::SPP < L::SPP ? nk - pt * L::SPP : L::SPP;
+        for (; qn < q0 + pt * L::SPP + last && ok; qn += kTDec) {
+          const int q = qn, kb = q - q0, ci = kb - pt * L::SPP, s = q % kTRing;
+          uint32_t v[32];
+          if (kInt4) {
+            const uint4 c0 = *reinterpret_cast<const uint4*>(prow + (((2 * ci) ^ (r & 7)) << 4));
+            const uint4 c1 = *reinterpret_cast<const uint4*>(prow + (((2 * ci + 1) ^ (r & 7)) << 4));
+            const uint32_t s2 = sc_nxt, zsub = w4_zero_pair(zp_nxt);
+            if (kb + kTDec < nk) {
+              fetch((kb + kTDec) >> 1);
+            } else if (more && kb + kTDec < 2 * nk) {
+              start_item(nx, kb + kTDec - nk);
+              ready = true;
+            }
+            const uint32_t pw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint4 d = decode_w4_8(pw[j], s2, zsub);
+              v[4 * j] = d.x;
+              v[4 * j + 1] = d.y;
+              v[4 * j + 2] = d.z;
+              v[4 * j + 3] = d.w;
+            }
+          } else {
+            const uint4 c0 = *reinterpret_cast<const uint4*>(prow + ((ci ^ (r & 7)) << 4));
+            const uint32_t pw[4] = {c0.x, c0.y, c0.z, c0.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint4 d = decode_tq_8(pw[j >> 1], j & 1);
+              v[4 * j] = d.x;
+              v[4 * j + 1] = d.y;
+              v[4 * j + 2] = d.z;
+              v[4 * j + 3] = d.w;
+            }
+          }
+          if (q >= kTRing) {
+            ok = mbar_wait_warp(&empty[s], static_cast<uint32_t>(q / kTRing - 1) & 1u);
+            tc_fence_after_sync();
+          }
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tmem_st_32x32b_x32(lane_base + 32 * s, v);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&emptyP[ps]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int r = threadIdx.x & (kERows - 1);
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    __half* stage = reinterpret_cast<__half*>(sm + L::kOffY);
+    const bool vec = (a.N & 7) == 0;  // y itself is 16-byte aligned
+    for (int n = 0; n < count; ++n) {
+      int4 it;
+      bool got = take_item(n, &it);
+      got = got && mbar_wait_warp(&acc_full[n & 1], static_cast<uint32_t>(n / 2) & 1u);
+      // the four warps go on together or not at all
+      if (!got && lane == 0) misc[1] = 1u;
+      warps_barrier(1, 128);
+      if (misc[1] != 0u) break;
+      tc_fence_after_sync();
+      const int64_t n0 = static_cast<int64_t>(it.y) * kERows, nr = n0 + r;
+      const int64_t en = static_cast<int64_t>(it.x) * a.N + nr;
+      float es = 1.0f, eb = 0.0f;
+      if (nr < a.N) {
+        if (!kInt4) es = __half2float(a.sc[en]);
+        if (a.bias) eb = __half2float(a.bias[en]);
+      }
+      for (int c = 0; c * 32 < it.w; ++c) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(lane_base + (n & 1) * kTTok + c * 32, v);
+        tmem_ld_wait();
+        const int cnt = it.w - c * 32 < 32 ? it.w - c * 32 : 32;
+        if ((c + 1) * 32 >= it.w) {  // the accumulator has been read
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[n & 1]);
+        }
+        uint32_t mask = 0xFFFFFFFFu;  // rows outside x read as zeros
+        if (kOrder) mask = __ballot_sync(0xFFFFFFFFu, lane < cnt && expert_x_row(a, it.z + c * 32 + lane) >= 0);
+        __half* yrow = a.y + (static_cast<int64_t>(it.z) + c * 32) * a.N + n0;
+        auto out = [&](int j) {
+          const float f = (mask >> j) & 1u ? __uint_as_float(v[j]) : 0.0f;
+          return __float2half_rn(fmaf(f, es, eb));
+        };
+        if (vec) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) stage[j * kERows + r] = out(j);
+          warps_barrier(1, 128);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const int i = r + 128 * p, tok = i >> 4, ch = i & 15;
+            if (tok < cnt && n0 + ch * 8 < a.N)
+              *reinterpret_cast<uint4*>(yrow + tok * a.N + ch * 8) =
+                  *reinterpret_cast<const uint4*>(stage + tok * kERows + ch * 8);
+          }
+          warps_barrier(1, 128);
+        } else if (nr < a.N) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j < cnt) yrow[j * a.N + r] = out(j);
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool kInt4>
+static cudaError_t launch_experts_tc(const ExpertArgs& a, cudaStream_t s) {
+  using L = ExpertTcLayout<kInt4>;
+  const uint64_t row_bytes = static_cast<uint64_t>(kInt4 ? a.K / 2 : a.K / 4);
+  CUtensorMap tx, tw;
+  if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, row_bytes, static_cast<uint64_t>(a.E) * a.N, row_bytes, 128,
+                    kERows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.x, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.X),
+                    static_cast<uint64_t>(a.K) * 2, 64, a.order ? 1 : kTBox, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  const int64_t by_rows = a.E + a.R / kTTok, chunks = a.R < by_rows ? a.R : by_rows;
+  const unsigned grid = row_grid(chunks * ((a.N + kERows - 1) / kERows), 1, 1);
+  const int smem = L::bytes(a.E);
+  auto run = [&](auto* kern) {
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(grid), dim3(kTThreads), static_cast<size_t>(smem), 1, s, tx, tw, a);
+  };
+  return a.order ? run(experts_tc_kernel<kInt4, true>) : run(experts_tc_kernel<kInt4, false>);
+}
+
 template <bool kInt4>
 static cudaError_t launch_experts(int path, const ExpertArgs& a, cudaStream_t s) {
-  if (path == 3) return launch_experts_generic<kInt4>(a, s);
+  if (path == 3 || a.X == 0) return launch_experts_generic<kInt4>(a, s);
+  if (path == 2) return launch_experts_tc<kInt4>(a, s);
   // rows per expert of an even spread; no expert has more than R rows
   const int64_t avg = a.R / a.E;
   if (a.R <= 8 || avg <= 4) return launch_experts_skinny<kInt4, 1>(a, s);
-  if (a.R <= 16 || avg <= 10) return launch_experts_skinny<kInt4, 2>(a, s);
-  return launch_experts_skinny<kInt4, 4>(a, s);
+  return launch_experts_skinny<kInt4, 2>(a, s);
 }
 
 cudaError_t launch_gemm_experts(bool int4, int path, const ExpertArgs& a, cudaStream_t s) {

@@ -139,7 +139,7 @@ int tq_experts_path(int fmt, int64_t R, int64_t E, int64_t N, int64_t K, int ali
   if (R < 0 || E < 1 || N < 0 || K <= 0) return TQ_ERR_SHAPE;
   if (fmt == TQ_FMT_W4G128 && K % 128 != 0) return TQ_ERR_SHAPE;
   if (R == 0 || N == 0 || !aligned || K % 64 != 0) return TQ_PATH_GENERIC;
-  return TQ_PATH_DECODE;
+  return R / E <= 32 ? TQ_PATH_DECODE : TQ_PATH_PREFILL;
 }
 
 }  // extern "C"

@@ -17,7 +17,7 @@ from gpu_util import bits, check_canaries, f16np, gpu, guarded_empty, need_cuda
 
 pytestmark = gpu
 FORMATS = ["ternary", "w4", "w4z"]
-PATHS = [tq.PATH_AUTO, tq.PATH_GENERIC, tq.PATH_DECODE]
+PATHS = [tq.PATH_AUTO, tq.PATH_GENERIC, tq.PATH_DECODE, tq.PATH_PREFILL]
 
 
 def _gen(seed):
@@ -237,3 +237,22 @@ def test_refusals():
         tq.w4g_gemm_experts(x, q, s, offsets, order=order, top_k=0)
     y = tq.w4g_gemm_experts(x, q, s, offsets, order=order[:0], top_k=2)      # no rows
     assert tuple(y.shape) == (0, 64)
+
+
+# more items than CTAs, with numbers of stages that do not divide by the groups and rings of any path
+@pytest.mark.parametrize("T,k,E,N,K", [(96, 2, 5, 7001, 384), (40, 3, 12, 4160, 640), (700, 4, 24, 2311, 896),
+                                       (1500, 1, 4, 5000, 1152)])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("path", [tq.PATH_DECODE, tq.PATH_PREFILL])
+@pytest.mark.parametrize("spread", [True, False])
+def test_many_items_per_cta(T, k, E, N, K, fmt, path, spread):
+    need_cuda()
+    cols = np.unique(np.concatenate([np.arange(0, N, 97), np.arange(N - 130, N)]))
+    _run(fmt, path, T, k, E, N, K, T + N, spread, bias=k == 3, cols=cols)
+
+
+@pytest.mark.parametrize("K", [64, 320, 448, 704])
+def test_ternary_many_items_of_odd_stage_counts(K):
+    need_cuda()
+    for path in (tq.PATH_DECODE, tq.PATH_PREFILL):
+        _run("ternary", path, 333, 2, 6, 4500, K, K, True, bias=True, cols=np.arange(0, 4500, 53))
