@@ -530,103 +530,110 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
 // ---------------------------------------------------------------------------------------------
 // Many rows per expert: a dense contraction, on tcgen05 with the decoded weights as A in tensor
 // memory (as in the prefill GEMM) and the rows of x as B in shared memory.  Persistent CTAs, one
-// per SM; an item is 128 weight rows of one expert times up to 192 of its rows, all of K.
+// per SM; an item is RT tiles of 128 weight rows of one expert times up to 192 of its rows, all of
+// K.  The MMA's N is the item's own number of rows rounded up to 16 (an expert's rows are cut
+// evenly), so a ragged expert costs its rows and not a full tile.
 //
-// Tensor memory holds two accumulators of 192 columns and four slots of decoded weights (32
-// columns = 64 k), so that an item's epilogue runs under the next item's MMAs; the MMA's N is the
-// item's own number of rows rounded up to 16 (an expert's rows are cut evenly), so a ragged expert
-// costs its rows and not a full tile.  20 warps:
-//   warp 0      x of a stage (64 k, 128-byte swizzle): boxes of 32 sorted rows, or, through
-//               `order`, four rows per instruction (tile::gather4) issued by the whole warp;
+// RT = 2: each stage of x (64 k) feeds two accumulators, which halves the x that crosses L2 per
+// MMA and gives the issuing thread eight MMAs per barrier test (a test stalls its MMA stream).
+// RT = 1 serves launches whose items would otherwise leave SMs idle.  20 warps:
+//   warp 0      x by TMA (64 k, 128-byte swizzle, boxes of 32 sorted rows); through `order`, warps 0
+//               and 3 copy the rows with 16-byte cp.async into the same layout (rows outside x
+//               zero-filled).  tile::gather4 loads were tried for this: 39 ns per four rows.
 //   warp 1      allocates tensor memory; one lane issues the MMAs;
-//   warp 2      packed weights, 128 rows x 128 bytes per load (4 INT4 / 8 ternary stages);
-//   warp 3      finds the items (a search in the chunk table) and hands them to the others
-//               through a ring of descriptors, ahead of their use;
-//   warps 4-15  three groups of four that decode every third stage of the CTA (counted across
-//               items: having waited for the MMAs of the stage seven before, a group finds the
-//               slot's barrier in one of two phases); thread = weight row = tensor
-//               memory lane, 64 weights into 32 registers and one tcgen05.st; the row's next group
-//               scale (and zero-point) is loaded a stage ahead, the next item's first one an item
-//               ahead;
-//   warps 16-19 the epilogue: tcgen05.ld, row scale and bias, fp16, rows of y through a staging
-//               buffer.
-// One barrier per stage counts x's bytes and the four decode warps; one commit frees both.
+//   warp 2      finds the items (a search in the chunk table), hands them to the other warps through
+//               a ring of descriptors one item ahead, and loads the packed weights, 128 rows x 128
+//               bytes per load (4 INT4 / 8 ternary stages);
+//   warps 4-19  four groups of four that decode, a row tile's stages in turn (thread = weight row =
+//               tensor memory lane: 64 weights into 32 registers and one tcgen05.st), then read the
+//               item's accumulator: row scale and bias, fp16, rows of y through staging buffers.
+//               INT4 group scales (and zero-points) are loaded a stage ahead, the next item's first
+//               one an item ahead.
+// A decode warp arrives on the stage's barrier only after the stage's x has landed, so the issuing
+// thread tests one barrier per stage; x and decoded weights are freed by separate commits.
 // ---------------------------------------------------------------------------------------------
 constexpr int kTTok = 192;       // rows of x per item (MMA N)
 constexpr int kTBox = 32;        // sorted rows per x load
-constexpr int kTRing = 4;        // stages of x and of decoded weights
+constexpr int kTXRing = 4;       // stages of x
 constexpr int kTPRing = 3;       // packed tiles
-constexpr int kTDec = 3;         // decode groups
-constexpr int kTThreads = 32 * (4 + 4 * kTDec + 4);
+constexpr int kTGroups = 4;      // decode groups
+constexpr int kTThreads = 32 * (4 + 4 * kTGroups);
 constexpr int kTItems = 4;
+constexpr int kTYTok = 16;       // rows of y per staging buffer
 
-template <bool kInt4>
+template <bool kInt4, int RT>
 struct ExpertTcLayout {
-  static constexpr int SPP = kInt4 ? 4 : 8;  // stages per packed tile
+  static constexpr int SPP = kInt4 ? 4 : 8;    // stages per packed tile
+  static constexpr int SG = kTGroups / RT;     // groups of a row tile = its slots of decoded weights
   static constexpr int kTileX = kTTok * 128;
-  static constexpr int kTileP = kERows * 128;
-  static constexpr int kStage = 32 * kERows * 2;  // 32 rows of y, 128 columns
-  static constexpr int kOffX = 0;
-  static constexpr int kOffP = kTRing * kTileX;
+  static constexpr int kTileP = RT * kERows * 128;
+  static constexpr int kStage = kTYTok * kERows * 2;
+  static constexpr int kOffP = kTXRing * kTileX;
   static constexpr int kOffY = kOffP + kTPRing * kTileP;
-  static constexpr int kOffBar = kOffY + kStage;
-  // full[R], empty[R], fullP[RP], emptyP[RP], accFull[2], accEmpty[2], itemFull[I], itemEmpty[I]
-  static constexpr int kNumBars = 2 * kTRing + 2 * kTPRing + 4 + 2 * kTItems;
+  static constexpr int kOffBar = kOffY + kTGroups * kStage;
+  // full[SG], emptyA[SG], fullX[RX], emptyX[RX], fullP[RP], emptyP[RP], accFull, accEmpty, itemFull[I],
+  // itemEmpty[I]
+  static constexpr int kNumBars = 2 * kTGroups + 2 * kTXRing + 2 * kTPRing + 2 + 2 * kTItems;
   static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
-  static constexpr int kOffMisc = kOffItem + kTItems * 16;  // TMEM slot, epilogue flags
+  static constexpr int kOffMisc = kOffItem + kTItems * 16;  // TMEM slot, the groups' failure flags
   static constexpr int kOffScan = kOffMisc + 32;
   static constexpr int kOffFirst = kOffScan + 32 * 4;
   static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }
   static constexpr uint32_t kColA = 2 * kTTok;
-  static_assert(2 * kTTok + 32 * kTRing <= 512, "tensor memory");
+  static_assert(2 * kTTok + 32 * kTGroups <= 512, "tensor memory");
   static_assert(kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 && kOffFirst > 114 * 1024, "one CTA per SM");
 };
 
-template <bool kInt4, bool kOrder>
+template <bool kInt4, bool kOrder, int RT>
 __global__ void __launch_bounds__(kTThreads, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                       const ExpertArgs a) {
-  using L = ExpertTcLayout<kInt4>;
+  using L = ExpertTcLayout<kInt4, RT>;
+  constexpr int SG = L::SG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
-  uint64_t* empty = full + kTRing;
-  uint64_t* fullP = empty + kTRing;
+  uint64_t* empty = full + kTGroups;
+  uint64_t* full_x = empty + kTGroups;
+  uint64_t* empty_x = full_x + kTXRing;
+  uint64_t* fullP = empty_x + kTXRing;
   uint64_t* emptyP = fullP + kTPRing;
   uint64_t* acc_full = emptyP + kTPRing;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* item_full = acc_empty + 2;
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* item_full = acc_empty + 1;
   uint64_t* item_empty = item_full + kTItems;
   int4* items = reinterpret_cast<int4*>(sm + L::kOffItem);  // (e, tile, row0, rows)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kOffMisc);
   int* first = reinterpret_cast<int*>(sm + L::kOffFirst);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kXWarps = kOrder ? 2 : 1;
 
   pdl_allow_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kTRing; ++i) {
-      mbar_init(&full[i], 5);
+    for (int i = 0; i < SG; ++i) {
+      mbar_init(&full[i], 4 * RT);
       mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kTXRing; ++i) {
+      mbar_init(&full_x[i], kXWarps);
+      mbar_init(&empty_x[i], 1);
     }
     for (int i = 0; i < kTPRing; ++i) {
       mbar_init(&fullP[i], 1);
-      mbar_init(&emptyP[i], 4 * kTDec);
+      mbar_init(&emptyP[i], 4 * kTGroups);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
-    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 4 * kTGroups);
     for (int i = 0; i < kTItems; ++i) {
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], 3 + 4 * kTDec + 4);
+      mbar_init(&item_empty[i], kXWarps + 1 + 4 * kTGroups);
     }
+    for (int i = 1; i < 8; ++i) misc[i] = 0u;
     fence_mbar_init();
     tma_prefetch_desc(&tmap_x);
     tma_prefetch_desc(&tmap_w);
   }
-  if (threadIdx.x == 32) misc[1] = 0u;
   if (warp == 1) {
-    __syncwarp();
     tmem_alloc(misc, 512);
     tmem_relinquish();
   }
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   expert_chunks(a, kTTok, first, reinterpret_cast<int*>(sm + L::kOffScan), kTThreads);  // synchronises
   tc_fence_after_sync();
   const uint32_t tmem = misc[0];
-  const int64_t tiles = (a.N + kERows - 1) / kERows;
+  const int64_t tiles = (a.N + RT * kERows - 1) / (RT * kERows);
   const int64_t total = static_cast<int64_t>(first[a.E]) * tiles;
   const int nk = static_cast<int>(a.K / 64);
   const int npt = (nk + L::SPP - 1) / L::SPP;
@@ -643,167 +650,191 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const int count = static_cast<int>(total > blockIdx.x ? (total - blockIdx.x + gridDim.x - 1) / gridDim.x : 0);
   bool ok = true;
 
-  // Item n of this CTA; every role but warp 3 reads each item once and releases it.
+  // Wait of a whole warp; the lanes agree on the outcome.
+  auto wait_all = [&](uint64_t* bar, int phase) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_warp(bar, static_cast<uint32_t>(phase) & 1u)) != 0;
+  };
+  // Item n of this CTA; every warp that uses items reads each once and releases it.
   auto take_item = [&](int n, int4* it) {
     const int d = n % kTItems;
-    const bool got = mbar_wait_warp(&item_full[d], static_cast<uint32_t>(n / kTItems) & 1u);
+    const bool got = wait_all(&item_full[d], n / kTItems);
     *it = items[d];
     __syncwarp();
     if (lane == 0) mbar_arrive(&item_empty[d]);
     return got;
   };
 
-  if (warp == 3) {
-    // ------------------------------------------------------------------ items
-    for (int n = 0; n < count && ok; ++n) {
+  if (warp == 2) {
+    // ------------------------------------------------------------------ items, packed weights
+    auto publish = [&](int n) {
       const ExpertItem it = expert_item<true>(a, first, blockIdx.x + static_cast<int64_t>(n) * gridDim.x, tiles, kTTok);
       const int d = n % kTItems;
-      if (n >= kTItems) ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&item_empty[d], static_cast<uint32_t>(n / kTItems - 1) & 1u));
+      if (n >= kTItems) ok = wait_all(&item_empty[d], n / kTItems - 1);
       if (ok && lane == 0) {
         items[d] = make_int4(it.e, it.tile, it.row0, it.rows);
         mbar_arrive(&item_full[d]);
       }
       __syncwarp();
-    }
-  } else if (warp == 0) {
-    // ------------------------------------------------------------------ x
-    int q = 0;
-    const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
-    int4 nx;
-    int rows[8];  // kOrder: x rows of the four rows at 4 lane and 4 (lane + 32)
-    auto find_rows = [&](const int4& it) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        int r = 4 * (lane + 32 * (j >> 2)) + (j & 3);
-        r = it.z + (r < it.w ? r : it.w - 1);
-        const int64_t xr = expert_x_row(a, r);
-        rows[j] = xr < 0 ? 0 : static_cast<int>(xr);  // masked in the epilogue
-      }
+      return static_cast<int>(static_cast<int64_t>(it.e) * a.N + static_cast<int64_t>(it.tile) * (RT * kERows));
     };
-    if (count > 0) ok = __all_sync(0xFFFFFFFFu, take_item(0, &nx));
-    if (kOrder && count > 0 && ok) find_rows(nx);
+    int pq = 0, row = 0;
+    if (count > 0) row = publish(0);
     for (int n = 0; n < count && ok; ++n) {
-      const int4 it = nx;
-      int now[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) now[j] = kOrder ? rows[j] : 0;
-      if (n + 1 < count) {  // the next item's rows are looked up under this item's loads
-        ok = __all_sync(0xFFFFFFFFu, take_item(n + 1, &nx));
-        if (!ok) break;
-        if (kOrder) find_rows(nx);
-      }
-      const int n16 = (it.w + 15) / 16 * 16;
-      const int boxes = (n16 + kTBox - 1) / kTBox;
-      for (int kb = 0; kb < nk && ok && !skipx; ++kb, ++q) {
-        const int s = q % kTRing;
-        if (q >= kTRing) ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&empty[s], static_cast<uint32_t>(q / kTRing - 1) & 1u));
-        if (!ok) break;
-        uint8_t* dst = sm + L::kOffX + s * L::kTileX;
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], kOrder ? n16 * 128 : boxes * kTBox * 128);
-        __syncwarp();
-        if (kOrder) {
-          if (4 * lane < n16) tma_gather4(dst + lane * 512, &tmap_x, &full[s], kb * 64, now[0], now[1], now[2], now[3]);
-          if (4 * (lane + 32) < n16)
-            tma_gather4(dst + (lane + 32) * 512, &tmap_x, &full[s], kb * 64, now[4], now[5], now[6], now[7]);
-        } else if (lane < boxes) {
-          tma_load_2d(dst + lane * kTBox * 128, &tmap_x, &full[s], kb * 64, it.z + lane * kTBox);
-        }
-      }
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------------ packed weights
-    int pq = 0;
-    for (int n = 0; n < count && ok; ++n) {
-      int4 it;
-      ok = __all_sync(0xFFFFFFFFu, take_item(n, &it));
-      if (!ok) break;
-      const int row = static_cast<int>(static_cast<int64_t>(it.x) * a.N + static_cast<int64_t>(it.y) * kERows);
+      const int row_next = n + 1 < count ? publish(n + 1) : 0;
       for (int pt = 0; pt < npt && ok; ++pt, ++pq) {
         const int s = pq % kTPRing;
-        if (pq >= kTPRing) ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&emptyP[s], static_cast<uint32_t>(pq / kTPRing - 1) & 1u));
+        if (pq >= kTPRing) ok = wait_all(&emptyP[s], pq / kTPRing - 1);
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(&fullP[s], L::kTileP);
-          tma_load_2d(sm + L::kOffP + s * L::kTileP, &tmap_w, &fullP[s], pt * 128, row);
+#pragma unroll
+          for (int h = 0; h < RT; ++h)
+            tma_load_2d(sm + L::kOffP + s * L::kTileP + h * kERows * 128, &tmap_w, &fullP[s], pt * 128, row + h * kERows);
         }
         __syncwarp();
       }
+      row = row_next;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
     int q = 0;
-    const uint32_t x_base = smem_u32(sm + L::kOffX);
+    const uint32_t x_base = smem_u32(sm);
     for (int n = 0; n < count && ok; ++n) {
       int4 it;
-      ok = __all_sync(0xFFFFFFFFu, take_item(n, &it));
+      ok = take_item(n, &it);
       if (!ok) break;
       if (lane == 0) {
         const uint32_t idesc = idesc_f16_f32(kERows, static_cast<uint32_t>((it.w + 15) / 16 * 16));
-        const uint32_t acc = tmem + (n & 1) * kTTok;
-        if (n >= 2) ok = mbar_wait(&acc_empty[n & 1], static_cast<uint32_t>(n / 2 - 1) & 1u);
+        if (n >= 1) ok = mbar_wait(acc_empty, static_cast<uint32_t>(n - 1) & 1u);
         for (int kb = 0; kb < nk && ok; ++kb, ++q) {
-          const int s = q % kTRing;
-          ok = mbar_wait(&full[s], static_cast<uint32_t>(q / kTRing) & 1u);
+          const int s = q % SG, sx = q % kTXRing;
+          ok = mbar_wait(&full[s], static_cast<uint32_t>(q / SG) & 1u);
           if (!ok) break;
           tc_fence_after_sync();
-          const uint64_t bdesc = sdesc_kmajor_sw128(x_base + s * L::kTileX);
+          const uint64_t bdesc = sdesc_kmajor_sw128(x_base + sx * L::kTileX);
 #pragma unroll
           for (int k16 = 0; k16 < 4; ++k16)
-            umma_f16_ts(acc, tmem + L::kColA + 32 * s + 8 * k16, bdesc + 2 * k16, idesc, (kb | k16) != 0 ? 1u : 0u);
+#pragma unroll
+            for (int h = 0; h < RT; ++h)
+              umma_f16_ts(tmem + h * kTTok, tmem + L::kColA + 32 * (h * SG + s) + 8 * k16, bdesc + 2 * k16, idesc,
+                          (kb | k16) != 0 ? 1u : 0u);
           umma_commit(&empty[s]);
+          umma_commit(&empty_x[sx]);
         }
-        if (ok) umma_commit(&acc_full[n & 1]);
+        if (ok) umma_commit(acc_full);
       }
       __syncwarp();
       ok = __all_sync(0xFFFFFFFFu, ok);
     }
-  } else if (warp < 4 + 4 * kTDec) {
-    // ------------------------------------------------------------------ decode
-    const int dg = (warp >> 2) - 1;
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ x
+    const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
+    int q = 0;
+    if (!kOrder) {
+      for (int n = 0; n < count && ok && warp == 0; ++n) {
+        int4 it;
+        ok = take_item(n, &it);
+        const int boxes = (it.w + kTBox - 1) / kTBox;
+        for (int kb = 0; kb < nk && ok && !skipx; ++kb, ++q) {
+          const int s = q % kTXRing;
+          if (q >= kTXRing) ok = wait_all(&empty_x[s], q / kTXRing - 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full_x[s], boxes * kTBox * 128);
+          __syncwarp();
+          if (lane < boxes)
+            tma_load_2d(sm + s * L::kTileX + lane * kTBox * 128, &tmap_x, &full_x[s], kb * 64, it.z + lane * kTBox);
+        }
+      }
+    } else {
+      // lane: 16-byte chunk lane % 8 of rows 8 i + 4 w + lane / 8
+      const int w = warp == 0 ? 0 : 1, sub = 4 * w + (lane >> 3), ch = lane & 7;
+      constexpr int kLag = 2;  // a stage is handed over when the second one after it has been issued
+      auto hand_over = [&](int qq) {
+        fence_proxy_async_smem();  // these copies are generic-proxy writes; the MMA reads by the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full_x[qq % kTXRing]);
+      };
+      for (int n = 0; n < count && ok; ++n) {
+        int4 it;
+        ok = take_item(n, &it);
+        int rows[kTTok / 8];
+#pragma unroll
+        for (int i = 0; i < kTTok / 8; ++i) {
+          const int r = 8 * i + sub;
+          rows[i] = ok && r < it.w ? static_cast<int>(expert_x_row(a, it.z + r)) : -1;
+        }
+        const int pieces = ((it.w + 15) / 16 * 16) / 8;
+        for (int kb = 0; kb < nk && ok && !skipx; ++kb, ++q) {
+          const int s = q % kTXRing;
+          if (q >= kTXRing) ok = wait_all(&empty_x[s], q / kTXRing - 1);
+          if (!ok) break;
+          uint8_t* dst = sm + s * L::kTileX + sub * 128 + ((ch ^ (sub & 7)) << 4);
+          const __half* src = a.x + kb * 64 + ch * 8;
+#pragma unroll
+          for (int i = 0; i < kTTok / 8; ++i)
+            if (i < pieces)
+              cp_async_16(dst + i * 1024, src + (rows[i] < 0 ? 0 : rows[i] * a.K), rows[i] < 0 ? 0u : 16u);
+          cp_async_commit();
+          if (q >= kLag) {
+            cp_async_wait<kLag>();
+            hand_over(q - kLag);
+          }
+        }
+      }
+      cp_async_wait<0>();
+      for (int qq = q - kLag < 0 ? 0 : q - kLag; qq < q; ++qq) hand_over(qq);
+    }
+  } else {
+    // ------------------------------------------------------------------ decode, epilogue
+    const int grp = (warp >> 2) - 1, h = grp / SG, sg = grp % SG;
     const int r = threadIdx.x & (kERows - 1);
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + L::kColA;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t a_slot = lane_base + L::kColA + 32 * (h * SG + sg);
     const int64_t G = a.K >> 7;
-    const uint8_t* prow0 = sm + L::kOffP + r * 128;
-    int4 nx;
-    const __half* scp = a.sc;   // scales / zero-points of this thread's weight row
+    const uint8_t* prow0 = sm + L::kOffP + (h * kERows + r) * 128;
+    __half* stage = reinterpret_cast<__half*>(sm + L::kOffY + grp * L::kStage);
+    const bool vec = (a.N & 7) == 0;  // y itself is 16-byte aligned
+    int4 nx = make_int4(0, 0, 0, 0);
+    const __half* scp = a.sc;  // scales / zero-points of this thread's weight row
     const uint8_t* zpp = a.zp;
     uint32_t sc_nxt = 0, zp_nxt = 8;
     auto fetch = [&](int64_t gi) {  // group scale (both halves) and zero-point
-      const uint32_t h = __half_as_ushort(scp[gi]);
-      sc_nxt = h | (h << 16);
+      const uint32_t v = __half_as_ushort(scp[gi]);
+      sc_nxt = v | (v << 16);
       if (zpp) zp_nxt = zpp[gi] & 15u;
     };
     auto start_item = [&](const int4& it, int kb) {  // the group's first stage of the item is kb
-      const int64_t n = static_cast<int64_t>(it.y) * kERows + r;
+      const int64_t n = static_cast<int64_t>(it.y) * (RT * kERows) + h * kERows + r;
       const int64_t row = (static_cast<int64_t>(it.x) * a.N + (n < a.N ? n : 0)) * G;  // past N: not stored
       scp = a.sc + row;
       if (a.zp) zpp = a.zp + row;
       fetch(kb >> 1);
     };
     int q0 = 0, pq = 0;
-    int qn = dg;         // the group's next stage
+    int qn = sg;         // the group's next stage, counted across items
     bool ready = false;  // its scale has been fetched
-    if (count > 0) ok = __all_sync(0xFFFFFFFFu, take_item(0, &nx));
+    if (count > 0) ok = take_item(0, &nx);
     for (int n = 0; n < count && ok; ++n, q0 += nk) {
+      const int4 it = nx;
       const bool more = n + 1 < count;
-      if (kInt4 && !ready && qn < q0 + nk) start_item(nx, qn - q0);
+      if (kInt4 && !ready && qn < q0 + nk) start_item(it, qn - q0);
       ready = false;
-      if (more) ok = __all_sync(0xFFFFFFFFu, take_item(n + 1, &nx));
+      if (more) ok = take_item(n + 1, &nx);
       for (int pt = 0; pt < npt && ok; ++pt, ++pq) {
         const int ps = pq % kTPRing;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&fullP[ps], static_cast<uint32_t>(pq / kTPRing) & 1u));
+        ok = wait_all(&fullP[ps], pq / kTPRing);
         const uint8_t* prow = prow0 + ps * L::kTileP;
-        const int last = nk - pt * L::SPP < L::SPP ? nk - pt * L::SPP : L::SPP;
-        for (; qn < q0 + pt * L::SPP + last && ok; qn += kTDec) {
-          const int q = qn, kb = q - q0, ci = kb - pt * L::SPP, s = q % kTRing;
+        const int end = q0 + (pt * L::SPP + L::SPP < nk ? pt * L::SPP + L::SPP : nk);
+        for (; qn < end && ok; qn += SG) {
+          const int kb = qn - q0, ci = kb - pt * L::SPP;
           uint32_t v[32];
           if (kInt4) {
             const uint4 c0 = *reinterpret_cast<const uint4*>(prow + (((2 * ci) ^ (r & 7)) << 4));
             const uint4 c1 = *reinterpret_cast<const uint4*>(prow + (((2 * ci + 1) ^ (r & 7)) << 4));
             const uint32_t s2 = sc_nxt, zsub = w4_zero_pair(zp_nxt);
-            if (kb + kTDec < nk) {
-              fetch((kb + kTDec) >> 1);
-            } else if (more && kb + kTDec < 2 * nk) {
-              start_item(nx, kb + kTDec - nk);
+            if (kb + SG < nk) {
+              fetch((kb + SG) >> 1);
+            } else if (more && kb + SG < 2 * nk) {
+              start_item(nx, kb + SG - nk);
               ready = true;
             }
             const uint32_t pw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
@@ -827,79 +858,73 @@ __global__ void __launch_bounds__(kTThreads, 1)
               v[4 * j + 3] = d.w;
             }
           }
-          if (q >= kTRing) {
-            ok = mbar_wait_warp(&empty[s], static_cast<uint32_t>(q / kTRing - 1) & 1u);
+          if (qn >= SG) {
+            ok = wait_all(&empty[sg], qn / SG - 1);
+            if (!ok) break;
             tc_fence_after_sync();
           }
-          ok = __all_sync(0xFFFFFFFFu, ok);
+          tmem_st_32x32b_x32(a_slot, v);
+          // the slot free, the MMAs of the stage SG before this one are done, so this stage's x
+          // barrier is in the awaited phase or past it
+          ok = wait_all(&full_x[qn % kTXRing], qn / kTXRing);
           if (!ok) break;
-          tmem_st_32x32b_x32(lane_base + 32 * s, v);
           tmem_st_wait();
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[s]);
+          if (lane == 0) mbar_arrive(&full[sg]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&emptyP[ps]);
       }
-    }
-  } else {
-    // ------------------------------------------------------------------ epilogue
-    const int r = threadIdx.x & (kERows - 1);
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    __half* stage = reinterpret_cast<__half*>(sm + L::kOffY);
-    const bool vec = (a.N & 7) == 0;  // y itself is 16-byte aligned
-    for (int n = 0; n < count; ++n) {
-      int4 it;
-      bool got = take_item(n, &it);
-      got = got && mbar_wait_warp(&acc_full[n & 1], static_cast<uint32_t>(n / 2) & 1u);
-      // the four warps go on together or not at all
-      if (!got && lane == 0) misc[1] = 1u;
-      warps_barrier(1, 128);
-      if (misc[1] != 0u) break;
+      // the item's sums: group sg of row tile h takes every SG-th 16 rows
+      const bool got = ok && wait_all(acc_full, n);
+      if (!got && lane == 0) misc[1 + grp] = 1u;  // the four warps of a group go on together or not at all
+      warps_barrier(1 + grp, 128);
+      ok = misc[1 + grp] == 0u;
+      if (!ok) break;
       tc_fence_after_sync();
-      const int64_t n0 = static_cast<int64_t>(it.y) * kERows, nr = n0 + r;
+      const int64_t n0 = static_cast<int64_t>(it.y) * (RT * kERows) + h * kERows, nr = n0 + r;
       const int64_t en = static_cast<int64_t>(it.x) * a.N + nr;
       float es = 1.0f, eb = 0.0f;
       if (nr < a.N) {
         if (!kInt4) es = __half2float(a.sc[en]);
         if (a.bias) eb = __half2float(a.bias[en]);
       }
-      for (int c = 0; c * 32 < it.w; ++c) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(lane_base + (n & 1) * kTTok + c * 32, v);
+      __syncwarp();
+      for (int c = sg; c * kTYTok < it.w; c += SG) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(lane_base + h * kTTok + c * kTYTok, v);
         tmem_ld_wait();
-        const int cnt = it.w - c * 32 < 32 ? it.w - c * 32 : 32;
-        if ((c + 1) * 32 >= it.w) {  // the accumulator has been read
+        if ((c + SG) * kTYTok >= it.w) {  // this group has read its share
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[n & 1]);
+          if (lane == 0) mbar_arrive(acc_empty);
         }
-        uint32_t mask = 0xFFFFFFFFu;  // rows outside x read as zeros
-        if (kOrder) mask = __ballot_sync(0xFFFFFFFFu, lane < cnt && expert_x_row(a, it.z + c * 32 + lane) >= 0);
-        __half* yrow = a.y + (static_cast<int64_t>(it.z) + c * 32) * a.N + n0;
-        auto out = [&](int j) {
-          const float f = (mask >> j) & 1u ? __uint_as_float(v[j]) : 0.0f;
-          return __float2half_rn(fmaf(f, es, eb));
-        };
+        const int cnt = it.w - c * kTYTok < kTYTok ? it.w - c * kTYTok : kTYTok;
+        __half* yrow = a.y + (static_cast<int64_t>(it.z) + c * kTYTok) * a.N + n0;
+        auto out = [&](int j) { return __float2half_rn(fmaf(__uint_as_float(v[j]), es, eb)); };
         if (vec) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) stage[j * kERows + r] = out(j);
-          warps_barrier(1, 128);
+          for (int j = 0; j < kTYTok; ++j) stage[j * kERows + r] = out(j);
+          warps_barrier(1 + grp, 128);
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const int i = r + 128 * p, tok = i >> 4, ch = i & 15;
-            if (tok < cnt && n0 + ch * 8 < a.N)
-              *reinterpret_cast<uint4*>(yrow + tok * a.N + ch * 8) =
-                  *reinterpret_cast<const uint4*>(stage + tok * kERows + ch * 8);
+          for (int p = 0; p < kTYTok / 8; ++p) {
+            const int i = r + 128 * p, tok = i >> 4, cc = i & 15;
+            if (tok < cnt && n0 + cc * 8 < a.N)
+              *reinterpret_cast<uint4*>(yrow + tok * a.N + cc * 8) =
+                  *reinterpret_cast<const uint4*>(stage + tok * kERows + cc * 8);
           }
-          warps_barrier(1, 128);
+          warps_barrier(1 + grp, 128);
         } else if (nr < a.N) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
+          for (int j = 0; j < kTYTok; ++j)
             if (j < cnt) yrow[j * a.N + r] = out(j);
         }
         __syncwarp();
+      }
+      if (sg * kTYTok >= it.w) {  // no share
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
       }
     }
   }
@@ -915,23 +940,26 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
 template <bool kInt4>
 static cudaError_t launch_experts_tc(const ExpertArgs& a, cudaStream_t s) {
-  using L = ExpertTcLayout<kInt4>;
   const uint64_t row_bytes = static_cast<uint64_t>(kInt4 ? a.K / 2 : a.K / 4);
   CUtensorMap tx, tw;
   if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, row_bytes, static_cast<uint64_t>(a.E) * a.N, row_bytes, 128,
                     kERows, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.x, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.X),
-                    static_cast<uint64_t>(a.K) * 2, 64, a.order ? 1 : kTBox, CU_TENSOR_MAP_SWIZZLE_128B))
+                    static_cast<uint64_t>(a.K) * 2, 64, kTBox, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const int64_t by_rows = a.E + a.R / kTTok, chunks = a.R < by_rows ? a.R : by_rows;
-  const unsigned grid = row_grid(chunks * ((a.N + kERows - 1) / kERows), 1, 1);
-  const int smem = L::bytes(a.E);
-  auto run = [&](auto* kern) {
+  auto run = [&](auto rt, auto ord) {
+    constexpr int RT = decltype(rt)::value;
+    auto* kern = experts_tc_kernel<kInt4, decltype(ord)::value, RT>;
+    const int smem = ExpertTcLayout<kInt4, RT>::bytes(a.E);
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(kTThreads), static_cast<size_t>(smem), 1, s, tx, tw, a);
+    const int64_t items = chunks * ((a.N + RT * kERows - 1) / (RT * kERows));
+    return launch_pdl(kern, dim3(row_grid(items, 1, 1)), dim3(kTThreads), static_cast<size_t>(smem), 1, s, tx, tw, a);
   };
-  return a.order ? run(experts_tc_kernel<kInt4, true>) : run(experts_tc_kernel<kInt4, false>);
+  const bool two = chunks * ((a.N + 2 * kERows - 1) / (2 * kERows)) >= current_device_info().num_sms;
+  if (a.order) return two ? run(std::integral_constant<int, 2>(), std::true_type()) : run(std::integral_constant<int, 1>(), std::true_type());
+  return two ? run(std::integral_constant<int, 2>(), std::false_type()) : run(std::integral_constant<int, 1>(), std::false_type());
 }
 
 template <bool kInt4>
