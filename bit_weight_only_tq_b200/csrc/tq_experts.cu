@@ -530,7 +530,7 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
 // ---------------------------------------------------------------------------------------------
 // Many rows per expert: a dense contraction, on tcgen05 with the decoded weights as A in tensor
 // memory (as in the prefill GEMM) and the rows of x as B in shared memory.  Persistent CTAs, one
-// per SM; an item is RT tiles of 128 weight rows of one expert times up to 192 of its rows, all of
+// per SM; an item is RT tiles of 128 weight rows of one expert times up to 128 of its rows, all of
 // K.  The MMA's N is the item's own number of rows rounded up to 16 (an expert's rows are cut
 // evenly), so a ragged expert costs its rows and not a full tile.
 //
@@ -550,11 +550,14 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
 //               INT4 group scales (and zero-points) are loaded a stage ahead, the next item's first
 //               one an item ahead.
 // A decode warp arrives on the stage's barrier only after the stage's x has landed, so the issuing
-// thread tests one barrier per stage; x and decoded weights are freed by separate commits.
+// thread tests one barrier per stage; x and decoded weights are freed by separate commits.  From
+// those commits to the next MMA on the same slot is a chain of barrier wake-ups and tensor memory
+// stores of about 0.8 us: the slots (four stages at RT = 2) are what keeps the MMAs running meanwhile.
 // ---------------------------------------------------------------------------------------------
-constexpr int kTTok = 192;       // rows of x per item (MMA N)
+constexpr int kTTok = 128;       // rows of x per item (MMA N)
 constexpr int kTBox = 32;        // sorted rows per x load
-constexpr int kTXRing = 4;       // stages of x
+constexpr int kTSlots = 8;       // slots of decoded weights, of all row tiles
+constexpr int kTMaxXRing = 8;
 constexpr int kTPRing = 3;       // packed tiles
 constexpr int kTGroups = 4;      // decode groups
 constexpr int kTThreads = 32 * (4 + 4 * kTGroups);
@@ -564,23 +567,26 @@ constexpr int kTYTok = 16;       // rows of y per staging buffer
 template <bool kInt4, int RT>
 struct ExpertTcLayout {
   static constexpr int SPP = kInt4 ? 4 : 8;    // stages per packed tile
-  static constexpr int SG = kTGroups / RT;     // groups of a row tile = its slots of decoded weights
+  static constexpr int SG = kTGroups / RT;     // decode groups of a row tile
+  static constexpr int AS = kTSlots / RT;      // its slots of decoded weights
+  static constexpr int RX = RT == 2 ? 6 : 8;   // stages of x
+  static_assert(RX % SG == 0 && RX <= kTMaxXRing && AS >= SG, "a group sees every phase of its x slots");
   static constexpr int kTileX = kTTok * 128;
   static constexpr int kTileP = RT * kERows * 128;
   static constexpr int kStage = kTYTok * kERows * 2;
-  static constexpr int kOffP = kTXRing * kTileX;
+  static constexpr int kOffP = RX * kTileX;
   static constexpr int kOffY = kOffP + kTPRing * kTileP;
   static constexpr int kOffBar = kOffY + kTGroups * kStage;
-  // full[SG], emptyA[SG], fullX[RX], emptyX[RX], fullP[RP], emptyP[RP], accFull, accEmpty, itemFull[I],
+  // full[AS], emptyA[AS], fullX[RX], emptyX[RX], fullP[RP], emptyP[RP], accFull, accEmpty, itemFull[I],
   // itemEmpty[I]
-  static constexpr int kNumBars = 2 * kTGroups + 2 * kTXRing + 2 * kTPRing + 2 + 2 * kTItems;
+  static constexpr int kNumBars = 2 * kTSlots + 2 * kTMaxXRing + 2 * kTPRing + 2 + 2 * kTItems;
   static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kOffMisc = kOffItem + kTItems * 16;  // TMEM slot, the groups' failure flags
   static constexpr int kOffScan = kOffMisc + 32;
   static constexpr int kOffFirst = kOffScan + 32 * 4;
   static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }
-  static constexpr uint32_t kColA = 2 * kTTok;
-  static_assert(2 * kTTok + 32 * kTGroups <= 512, "tensor memory");
+  static constexpr uint32_t kColA = RT * kTTok;
+  static_assert(RT * kTTok + 32 * kTSlots <= 512, "tensor memory");
   static_assert(kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 && kOffFirst > 114 * 1024, "one CTA per SM");
 };
 
@@ -589,14 +595,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                       const ExpertArgs a) {
   using L = ExpertTcLayout<kInt4, RT>;
-  constexpr int SG = L::SG;
+  constexpr int SG = L::SG, AS = L::AS, RX = L::RX;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
-  uint64_t* empty = full + kTGroups;
-  uint64_t* full_x = empty + kTGroups;
-  uint64_t* empty_x = full_x + kTXRing;
-  uint64_t* fullP = empty_x + kTXRing;
+  uint64_t* empty = full + kTSlots;
+  uint64_t* full_x = empty + kTSlots;
+  uint64_t* empty_x = full_x + kTMaxXRing;
+  uint64_t* fullP = empty_x + kTMaxXRing;
   uint64_t* emptyP = fullP + kTPRing;
   uint64_t* acc_full = emptyP + kTPRing;
   uint64_t* acc_empty = acc_full + 1;
@@ -610,11 +616,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
   pdl_allow_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < SG; ++i) {
+    for (int i = 0; i < AS; ++i) {
       mbar_init(&full[i], 4 * RT);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kTXRing; ++i) {
+    for (int i = 0; i < RX; ++i) {
       mbar_init(&full_x[i], kXWarps);
       mbar_init(&empty_x[i], 1);
     }
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   pdl_wait_prior_grids();
   expert_chunks(a, kTTok, first, reinterpret_cast<int*>(sm + L::kOffScan), kTThreads);  // synchronises
   tc_fence_after_sync();
-  const uint32_t tmem = misc[0];
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's: they start at 0
   const int64_t tiles = (a.N + RT * kERows - 1) / (RT * kERows);
   const int64_t total = static_cast<int64_t>(first[a.E]) * tiles;
   const int nk = static_cast<int>(a.K / 64);
@@ -696,34 +702,38 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
-    int q = 0;
-    const uint32_t x_base = smem_u32(sm);
+    // The whole warp runs the loop and one elected lane issues: the operands are then warp-uniform
+    // values, kept where the MMA takes them from; computed by a single lane they cost about 140
+    // cycles per MMA.
+    const uint32_t leader = elect_one() ? 1u : 0u;
+    const uint64_t xdesc = sdesc_kmajor_sw128(smem_u32(sm));
+    int s = 0, sx = 0, phase = 0;
     for (int n = 0; n < count && ok; ++n) {
       int4 it;
       ok = take_item(n, &it);
-      if (!ok) break;
-      if (lane == 0) {
-        const uint32_t idesc = idesc_f16_f32(kERows, static_cast<uint32_t>((it.w + 15) / 16 * 16));
-        if (n >= 1) ok = mbar_wait(acc_empty, static_cast<uint32_t>(n - 1) & 1u);
-        for (int kb = 0; kb < nk && ok; ++kb, ++q) {
-          const int s = q % SG, sx = q % kTXRing;
-          ok = mbar_wait(&full[s], static_cast<uint32_t>(q / SG) & 1u);
-          if (!ok) break;
-          tc_fence_after_sync();
-          const uint64_t bdesc = sdesc_kmajor_sw128(x_base + sx * L::kTileX);
+      if (ok && n >= 1) ok = wait_all(acc_empty, n - 1);
+      const uint32_t idesc = idesc_f16_f32(kERows, static_cast<uint32_t>((it.w + 15) / 16 * 16));
+      for (int kb = 0; kb < nk && ok; ++kb) {
+        ok = wait_all(&full[s], phase);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint64_t bdesc = xdesc + static_cast<uint64_t>(sx * (L::kTileX >> 4));
+        const uint32_t adst = L::kColA + 32 * s;
 #pragma unroll
-          for (int k16 = 0; k16 < 4; ++k16)
+        for (int k16 = 0; k16 < 4; ++k16)
 #pragma unroll
-            for (int h = 0; h < RT; ++h)
-              umma_f16_ts(tmem + h * kTTok, tmem + L::kColA + 32 * (h * SG + s) + 8 * k16, bdesc + 2 * k16, idesc,
-                          (kb | k16) != 0 ? 1u : 0u);
-          umma_commit(&empty[s]);
-          umma_commit(&empty_x[sx]);
+          for (int h = 0; h < RT; ++h)
+            umma_f16_ts_if(leader, h * kTTok, adst + 32 * h * AS + 8 * k16, bdesc + 2 * k16, idesc,
+                           (kb | k16) != 0 ? 1u : 0u);
+        umma_commit_if(leader, &empty[s]);
+        umma_commit_if(leader, &empty_x[sx]);
+        if (++s == AS) {
+          s = 0;
+          phase ^= 1;
         }
-        if (ok) umma_commit(acc_full);
+        if (++sx == RX) sx = 0;
       }
-      __syncwarp();
-      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (ok) umma_commit_if(leader, acc_full);
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------------ x
@@ -735,8 +745,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         ok = take_item(n, &it);
         const int boxes = (it.w + kTBox - 1) / kTBox;
         for (int kb = 0; kb < nk && ok && !skipx; ++kb, ++q) {
-          const int s = q % kTXRing;
-          if (q >= kTXRing) ok = wait_all(&empty_x[s], q / kTXRing - 1);
+          const int s = q % RX;
+          if (q >= RX) ok = wait_all(&empty_x[s], q / RX - 1);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&full_x[s], boxes * kTBox * 128);
           __syncwarp();
@@ -751,7 +761,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       auto hand_over = [&](int qq) {
         fence_proxy_async_smem();  // these copies are generic-proxy writes; the MMA reads by the async proxy
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full_x[qq % kTXRing]);
+        if (lane == 0) mbar_arrive(&full_x[qq % RX]);
       };
       for (int n = 0; n < count && ok; ++n) {
         int4 it;
@@ -764,8 +774,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         const int pieces = ((it.w + 15) / 16 * 16) / 8;
         for (int kb = 0; kb < nk && ok && !skipx; ++kb, ++q) {
-          const int s = q % kTXRing;
-          if (q >= kTXRing) ok = wait_all(&empty_x[s], q / kTXRing - 1);
+          const int s = q % RX;
+          if (q >= RX) ok = wait_all(&empty_x[s], q / RX - 1);
           if (!ok) break;
           uint8_t* dst = sm + s * L::kTileX + sub * 128 + ((ch ^ (sub & 7)) << 4);
           const __half* src = a.x + kb * 64 + ch * 8;
@@ -788,7 +798,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const int grp = (warp >> 2) - 1, h = grp / SG, sg = grp % SG;
     const int r = threadIdx.x & (kERows - 1);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t a_slot = lane_base + L::kColA + 32 * (h * SG + sg);
+    const uint32_t a_slots = lane_base + L::kColA + 32 * (h * AS);
     const int64_t G = a.K >> 7;
     const uint8_t* prow0 = sm + L::kOffP + (h * kERows + r) * 128;
     __half* stage = reinterpret_cast<__half*>(sm + L::kOffY + grp * L::kStage);
@@ -858,20 +868,17 @@ __global__ void __launch_bounds__(kTThreads, 1)
               v[4 * j + 3] = d.w;
             }
           }
-          if (qn >= SG) {
-            ok = wait_all(&empty[sg], qn / SG - 1);
-            if (!ok) break;
-            tc_fence_after_sync();
-          }
-          tmem_st_32x32b_x32(a_slot, v);
-          // the slot free, the MMAs of the stage SG before this one are done, so this stage's x
-          // barrier is in the awaited phase or past it
-          ok = wait_all(&full_x[qn % kTXRing], qn / kTXRing);
+          ok = wait_all(&full_x[qn % RX], qn / RX);
+          // the group has seen the MMAs of stage qn - SG - AS done, so those of qn - 2 AS are, and the
+          // slot's barrier is in the awaited phase or past it
+          if (ok && qn >= AS) ok = wait_all(&empty[qn % AS], qn / AS - 1);
           if (!ok) break;
+          tc_fence_after_sync();
+          tmem_st_32x32b_x32(a_slots + 32 * (qn % AS), v);
           tmem_st_wait();
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[sg]);
+          if (lane == 0) mbar_arrive(&full[qn % AS]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&emptyP[ps]);
