@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
       const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x + (xr >= 0 ? xr * a.K : 0));
       const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
       const int d = n % kEItems;
-      if (n >= kEItems) ok = mbar_wait_warp(&item_empty[d], static_cast<uint32_t>(n / kEItems - 1) & 1u);
+      if (n >= kEItems) ok = mbar_wait_quiet(&item_empty[d], static_cast<uint32_t>(n / kEItems - 1) & 1u);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       if (lane == 0) {
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
       const int wrow = static_cast<int>(static_cast<int64_t>(it.e) * a.N + static_cast<int64_t>(it.tile) * kERows);
       for (int kb = 0; kb < nk && ok; ++kb, ++q) {
         const int s = q % L::kRing;
-        if (q >= L::kRing) ok = mbar_wait_warp(&empty[s], static_cast<uint32_t>(q / L::kRing - 1) & 1u);
+        if (q >= L::kRing) ok = mbar_wait_quiet(&empty[s], static_cast<uint32_t>(q / L::kRing - 1) & 1u);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         const int64_t k0 = static_cast<int64_t>(kb) * L::KS;
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[m][b][c] = 0.0f;
       const int d = n % kEItems;
-      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&item_full[d], static_cast<uint32_t>(n / kEItems) & 1u));
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_quiet(&item_full[d], static_cast<uint32_t>(n / kEItems) & 1u));
       const int4 it = items[d * 2];
       const uint32_t rmask = static_cast<uint32_t>(items[d * 2 + 1].x);
       __syncwarp();
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
           for (int j = 0; j < 4; ++j) sc_now[j] = sc[j];
           if (kb + L::KG < nk) load_scales(kb + L::KG);
         }
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&full[s], static_cast<uint32_t>(q / L::kRing) & 1u));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_quiet(&full[s], static_cast<uint32_t>(q / L::kRing) & 1u));
         if (!ok) break;
         const uint8_t* wt = sm + s * L::kTileW + (rg * 32 + pg) * 128;
         const uint8_t* xt = sm + L::kOffX + s * L::kTileX + g * L::kXRow;
@@ -553,12 +553,14 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
 // thread tests one barrier per stage; x and decoded weights are freed by separate commits.  From
 // those commits to the next MMA on the same slot is a chain of barrier wake-ups and tensor memory
 // stores of about 0.8 us: the slots (four stages at RT = 2) are what keeps the MMAs running meanwhile.
+// The rings are walked in blocks of four stages, an item's last block filled up with empty stages, so
+// that slots and phases are constants of the unrolled code: the decode is bound by issue slots.
 // ---------------------------------------------------------------------------------------------
 constexpr int kTTok = 128;       // rows of x per item (MMA N)
 constexpr int kTBox = 32;        // sorted rows per x load
 constexpr int kTSlots = 8;       // slots of decoded weights, of all row tiles
-constexpr int kTMaxXRing = 8;
-constexpr int kTPRing = 3;       // packed tiles
+constexpr int kTXRing = 8;       // stages of x
+constexpr int kTBlock = 4;       // stages per block: the rings are walked in blocks, an item's last one filled up
 constexpr int kTGroups = 4;      // decode groups
 constexpr int kTThreads = 32 * (4 + 4 * kTGroups);
 constexpr int kTItems = 4;
@@ -569,17 +571,18 @@ struct ExpertTcLayout {
   static constexpr int SPP = kInt4 ? 4 : 8;    // stages per packed tile
   static constexpr int SG = kTGroups / RT;     // decode groups of a row tile
   static constexpr int AS = kTSlots / RT;      // its slots of decoded weights
-  static constexpr int RX = RT == 2 ? 6 : 8;   // stages of x
-  static_assert(RX % SG == 0 && RX <= kTMaxXRing && AS >= SG, "a group sees every phase of its x slots");
+  static constexpr int AB = AS / kTBlock;      // blocks of slots
+  static constexpr int RP = RT == 2 ? 2 : 3;   // packed tiles
+  static_assert(kTBlock % SG == 0 && AS % kTBlock == 0 && kTXRing == 2 * kTBlock, "a group sees every phase of its slots");
   static constexpr int kTileX = kTTok * 128;
   static constexpr int kTileP = RT * kERows * 128;
   static constexpr int kStage = kTYTok * kERows * 2;
-  static constexpr int kOffP = RX * kTileX;
-  static constexpr int kOffY = kOffP + kTPRing * kTileP;
+  static constexpr int kOffP = kTXRing * kTileX;
+  static constexpr int kOffY = kOffP + RP * kTileP;
   static constexpr int kOffBar = kOffY + kTGroups * kStage;
   // full[AS], emptyA[AS], fullX[RX], emptyX[RX], fullP[RP], emptyP[RP], accFull, accEmpty, itemFull[I],
   // itemEmpty[I]
-  static constexpr int kNumBars = 2 * kTSlots + 2 * kTMaxXRing + 2 * kTPRing + 2 + 2 * kTItems;
+  static constexpr int kNumBars = 2 * kTSlots + 2 * kTXRing + 2 * RP + 2 + 2 * kTItems;
   static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kOffMisc = kOffItem + kTItems * 16;  // TMEM slot, the groups' failure flags
   static constexpr int kOffScan = kOffMisc + 32;
@@ -590,21 +593,62 @@ struct ExpertTcLayout {
   static_assert(kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 && kOffFirst > 114 * 1024, "one CTA per SM");
 };
 
+// (v & mask) | base in one instruction: with both constants written out the compiler spends two.
+struct DecodeConsts {
+  uint32_t mask0, base0, mask1, base1;
+};
+__device__ __forceinline__ uint32_t opaque(uint32_t c) {
+  uint32_t r;
+  asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(c));
+  return r;
+}
+__device__ __forceinline__ DecodeConsts decode_consts(bool int4) {
+  DecodeConsts c;
+  c.mask0 = opaque(int4 ? 0x00F0000Fu : 0x000C0003u);
+  c.base0 = opaque(int4 ? 0x54006400u : 0x5C006400u);
+  c.mask1 = opaque(0x00C00030u);
+  c.base1 = opaque(0x4C005400u);
+  return c;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t base) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(base));
+  return r;
+}
+// 32 INT4 codes -> 16 registers of fp16 pairs (u - z) s, in natural order (as decode_w4_8).
+__device__ __forceinline__ void decode_stage_w4(const uint4& c, uint32_t s2, uint32_t zsub, const DecodeConsts& k,
+                                                uint32_t* v) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    v[i] = hmul2_u32(hsub2_u32(and_or(byte_to_halves(w[i >> 2], i & 3), k.mask0, k.base0), zsub), s2);
+}
+// 64 ternary codes -> 32 registers of fp16 pairs c - 1, in natural order (as decode_tq_8).
+__device__ __forceinline__ void decode_stage_tq(const uint4& c, const DecodeConsts& k, uint32_t* v) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t t = byte_to_halves(w[i >> 2], i & 3);
+    v[2 * i] = hsub2_u32(and_or(t, k.mask0, k.base0), 0x5C046401u);
+    v[2 * i + 1] = hsub2_u32(and_or(t, k.mask1, k.base1), 0x4C405410u);
+  }
+}
+
 template <bool kInt4, bool kOrder, int RT>
 __global__ void __launch_bounds__(kTThreads, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                       const ExpertArgs a) {
   using L = ExpertTcLayout<kInt4, RT>;
-  constexpr int SG = L::SG, AS = L::AS, RX = L::RX;
+  constexpr int SG = L::SG, AS = L::AS, AB = L::AB, RP = L::RP;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
   uint64_t* empty = full + kTSlots;
   uint64_t* full_x = empty + kTSlots;
-  uint64_t* empty_x = full_x + kTMaxXRing;
-  uint64_t* fullP = empty_x + kTMaxXRing;
-  uint64_t* emptyP = fullP + kTPRing;
-  uint64_t* acc_full = emptyP + kTPRing;
+  uint64_t* empty_x = full_x + kTXRing;
+  uint64_t* fullP = empty_x + kTXRing;
+  uint64_t* emptyP = fullP + RP;
+  uint64_t* acc_full = emptyP + RP;
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* item_full = acc_empty + 1;
   uint64_t* item_empty = item_full + kTItems;
@@ -620,11 +664,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
       mbar_init(&full[i], 4 * RT);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < RX; ++i) {
+    for (int i = 0; i < kTXRing; ++i) {
       mbar_init(&full_x[i], kXWarps);
       mbar_init(&empty_x[i], 1);
     }
-    for (int i = 0; i < kTPRing; ++i) {
+    for (int i = 0; i < RP; ++i) {
       mbar_init(&fullP[i], 1);
       mbar_init(&emptyP[i], 4 * kTGroups);
     }
@@ -651,6 +695,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const int64_t tiles = (a.N + RT * kERows - 1) / (RT * kERows);
   const int64_t total = static_cast<int64_t>(first[a.E]) * tiles;
   const int nk = static_cast<int>(a.K / 64);
+  const int nblk = (nk + kTBlock - 1) / kTBlock;
   const int npt = (nk + L::SPP - 1) / L::SPP;
   // items of this CTA
   const int count = static_cast<int>(total > blockIdx.x ? (total - blockIdx.x + gridDim.x - 1) / gridDim.x : 0);
@@ -658,7 +703,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
   // Wait of a whole warp; the lanes agree on the outcome.
   auto wait_all = [&](uint64_t* bar, int phase) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_warp(bar, static_cast<uint32_t>(phase) & 1u)) != 0;
+    return __all_sync(0xFFFFFFFFu, mbar_wait_quiet(bar, static_cast<uint32_t>(phase) & 1u)) != 0;
   };
   // Item n of this CTA; every warp that uses items reads each once and releases it.
   auto take_item = [&](int n, int4* it) {
@@ -688,8 +733,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
     for (int n = 0; n < count && ok; ++n) {
       const int row_next = n + 1 < count ? publish(n + 1) : 0;
       for (int pt = 0; pt < npt && ok; ++pt, ++pq) {
-        const int s = pq % kTPRing;
-        if (pq >= kTPRing) ok = wait_all(&emptyP[s], pq / kTPRing - 1);
+        const int s = pq % RP;
+        if (pq >= RP) ok = wait_all(&emptyP[s], pq / RP - 1);
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(&fullP[s], L::kTileP);
 #pragma unroll
@@ -707,31 +752,32 @@ __global__ void __launch_bounds__(kTThreads, 1)
     // cycles per MMA.
     const uint32_t leader = elect_one() ? 1u : 0u;
     const uint64_t xdesc = sdesc_kmajor_sw128(smem_u32(sm));
-    int s = 0, sx = 0, phase = 0;
+    int blk = 0;
     for (int n = 0; n < count && ok; ++n) {
       int4 it;
       ok = take_item(n, &it);
       if (ok && n >= 1) ok = wait_all(acc_empty, n - 1);
       const uint32_t idesc = idesc_f16_f32(kERows, static_cast<uint32_t>((it.w + 15) / 16 * 16));
-      for (int kb = 0; kb < nk && ok; ++kb) {
-        ok = wait_all(&full[s], phase);
-        if (!ok) break;
-        tc_fence_after_sync();
-        const uint64_t bdesc = xdesc + static_cast<uint64_t>(sx * (L::kTileX >> 4));
-        const uint32_t adst = L::kColA + 32 * s;
+      for (int b = 0; b < nblk && ok; ++b, ++blk) {
+        const int a0 = (blk % AB) * kTBlock, x0 = (blk & 1) * kTBlock;
 #pragma unroll
-        for (int k16 = 0; k16 < 4; ++k16)
+        for (int u = 0; u < kTBlock; ++u) {
+          ok = ok && wait_all(&full[a0 + u], blk / AB);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint64_t bdesc = xdesc + static_cast<uint64_t>((x0 + u) * (L::kTileX >> 4));
+          const uint32_t asrc = L::kColA + 32 * (a0 + u);
+          if (b * kTBlock + u < nk) {
 #pragma unroll
-          for (int h = 0; h < RT; ++h)
-            umma_f16_ts_if(leader, h * kTTok, adst + 32 * h * AS + 8 * k16, bdesc + 2 * k16, idesc,
-                           (kb | k16) != 0 ? 1u : 0u);
-        umma_commit_if(leader, &empty[s]);
-        umma_commit_if(leader, &empty_x[sx]);
-        if (++s == AS) {
-          s = 0;
-          phase ^= 1;
+            for (int k16 = 0; k16 < 4; ++k16)
+#pragma unroll
+              for (int h = 0; h < RT; ++h)
+                umma_f16_ts_if(leader, h * kTTok, asrc + 32 * h * AS + 8 * k16, bdesc + 2 * k16, idesc,
+                               (b | u | k16) != 0 ? 1u : 0u);
+          }
+          umma_commit_if(leader, &empty[a0 + u]);
+          umma_commit_if(leader, &empty_x[x0 + u]);
         }
-        if (++sx == RX) sx = 0;
       }
       if (ok) umma_commit_if(leader, acc_full);
     }
@@ -744,10 +790,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
         int4 it;
         ok = take_item(n, &it);
         const int boxes = (it.w + kTBox - 1) / kTBox;
-        for (int kb = 0; kb < nk && ok && !skipx; ++kb, ++q) {
-          const int s = q % RX;
-          if (q >= RX) ok = wait_all(&empty_x[s], q / RX - 1);
+        for (int kb = 0; kb < nblk * kTBlock && ok && !skipx; ++kb, ++q) {
+          const int s = q % kTXRing;
+          if (q >= kTXRing) ok = wait_all(&empty_x[s], q / kTXRing - 1);
           if (!ok) break;
+          if (kb >= nk) {  // fills up the block: nothing to load
+            if (lane == 0) mbar_arrive(&full_x[s]);
+            continue;
+          }
           if (lane == 0) mbar_arrive_expect_tx(&full_x[s], boxes * kTBox * 128);
           __syncwarp();
           if (lane < boxes)
@@ -761,7 +811,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       auto hand_over = [&](int qq) {
         fence_proxy_async_smem();  // these copies are generic-proxy writes; the MMA reads by the async proxy
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full_x[qq % RX]);
+        if (lane == 0) mbar_arrive(&full_x[qq % kTXRing]);
       };
       for (int n = 0; n < count && ok; ++n) {
         int4 it;
@@ -773,15 +823,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
           rows[i] = ok && r < it.w ? static_cast<int>(expert_x_row(a, it.z + r)) : -1;
         }
         const int pieces = ((it.w + 15) / 16 * 16) / 8;
-        for (int kb = 0; kb < nk && ok && !skipx; ++kb, ++q) {
-          const int s = q % RX;
-          if (q >= RX) ok = wait_all(&empty_x[s], q / RX - 1);
+        for (int kb = 0; kb < nblk * kTBlock && ok && !skipx; ++kb, ++q) {
+          const int s = q % kTXRing;
+          if (q >= kTXRing) ok = wait_all(&empty_x[s], q / kTXRing - 1);
           if (!ok) break;
           uint8_t* dst = sm + s * L::kTileX + sub * 128 + ((ch ^ (sub & 7)) << 4);
           const __half* src = a.x + kb * 64 + ch * 8;
 #pragma unroll
           for (int i = 0; i < kTTok / 8; ++i)
-            if (i < pieces)
+            if (i < pieces && kb < nk)
               cp_async_16(dst + i * 1024, src + (rows[i] < 0 ? 0 : rows[i] * a.K), rows[i] < 0 ? 0u : 16u);
           cp_async_commit();
           if (q >= kLag) {
@@ -804,84 +854,84 @@ __global__ void __launch_bounds__(kTThreads, 1)
     __half* stage = reinterpret_cast<__half*>(sm + L::kOffY + grp * L::kStage);
     const bool vec = (a.N & 7) == 0;  // y itself is 16-byte aligned
     int4 nx = make_int4(0, 0, 0, 0);
-    const __half* scp = a.sc;  // scales / zero-points of this thread's weight row
+    // The group scales (and zero-points) of this thread's weight row: a block of four stages has two
+    // groups of k, 2 b and 2 b + 1; both are loaded a block ahead.
+    const __half* scp = a.sc;
     const uint8_t* zpp = a.zp;
-    uint32_t sc_nxt = 0, zp_nxt = 8;
-    auto fetch = [&](int64_t gi) {  // group scale (both halves) and zero-point
-      const uint32_t v = __half_as_ushort(scp[gi]);
-      sc_nxt = v | (v << 16);
-      if (zpp) zp_nxt = zpp[gi] & 15u;
+    uint32_t sc_nxt = 0, zp_nxt = 0x0808u;
+    const bool pairs = (G & 1) == 0 && (reinterpret_cast<uintptr_t>(a.sc) & 3u) == 0;
+    auto fetch = [&](int b) {
+      if (pairs) {
+        sc_nxt = *reinterpret_cast<const uint32_t*>(scp + 2 * b);
+      } else {
+        sc_nxt = __half_as_ushort(scp[2 * b]);
+        if (2 * b + 1 < G) sc_nxt |= static_cast<uint32_t>(__half_as_ushort(scp[2 * b + 1])) << 16;
+      }
+      if (zpp) {
+        zp_nxt = zpp[2 * b];
+        if (2 * b + 1 < G) zp_nxt |= static_cast<uint32_t>(zpp[2 * b + 1]) << 8;
+      }
     };
-    auto start_item = [&](const int4& it, int kb) {  // the group's first stage of the item is kb
+    auto start_item = [&](const int4& it) {
       const int64_t n = static_cast<int64_t>(it.y) * (RT * kERows) + h * kERows + r;
       const int64_t row = (static_cast<int64_t>(it.x) * a.N + (n < a.N ? n : 0)) * G;  // past N: not stored
       scp = a.sc + row;
       if (a.zp) zpp = a.zp + row;
-      fetch(kb >> 1);
+      fetch(0);
     };
-    int q0 = 0, pq = 0;
-    int qn = sg;         // the group's next stage, counted across items
-    bool ready = false;  // its scale has been fetched
+    const DecodeConsts consts = decode_consts(kInt4);
+    int blk = 0, pq = 0;
     if (count > 0) ok = take_item(0, &nx);
-    for (int n = 0; n < count && ok; ++n, q0 += nk) {
+    if (kInt4 && ok && count > 0) start_item(nx);
+    for (int n = 0; n < count && ok; ++n) {
       const int4 it = nx;
       const bool more = n + 1 < count;
-      if (kInt4 && !ready && qn < q0 + nk) start_item(it, qn - q0);
-      ready = false;
       if (more) ok = take_item(n + 1, &nx);
-      for (int pt = 0; pt < npt && ok; ++pt, ++pq) {
-        const int ps = pq % kTPRing;
-        ok = wait_all(&fullP[ps], pq / kTPRing);
+      for (int b = 0; b < nblk && ok; ++b, ++blk) {
+        const int ps = pq % RP;
+        // a packed tile is one block of INT4 stages, two of ternary
+        const int half = kInt4 ? 0 : b & 1;
+        if (half == 0) ok = wait_all(&fullP[ps], pq / RP);
         const uint8_t* prow = prow0 + ps * L::kTileP;
-        const int end = q0 + (pt * L::SPP + L::SPP < nk ? pt * L::SPP + L::SPP : nk);
-        for (; qn < end && ok; qn += SG) {
-          const int kb = qn - q0, ci = kb - pt * L::SPP;
-          uint32_t v[32];
+        const uint32_t sc_now = sc_nxt, zp_now = zp_nxt;
+        if (kInt4 && ok) {
+          if (b + 1 < nblk)
+            fetch(b + 1);
+          else if (more)
+            start_item(nx);
+        }
+        const int a0 = (blk % AB) * kTBlock, x0 = (blk & 1) * kTBlock;
+#pragma unroll
+        for (int u = 0; u < kTBlock / SG; ++u) {
+          const int ci = u * SG + sg;
+          uint32_t v[32];  // a stage that fills up the block is decoded too, and not multiplied
           if (kInt4) {
             const uint4 c0 = *reinterpret_cast<const uint4*>(prow + (((2 * ci) ^ (r & 7)) << 4));
             const uint4 c1 = *reinterpret_cast<const uint4*>(prow + (((2 * ci + 1) ^ (r & 7)) << 4));
-            const uint32_t s2 = sc_nxt, zsub = w4_zero_pair(zp_nxt);
-            if (kb + SG < nk) {
-              fetch((kb + SG) >> 1);
-            } else if (more && kb + SG < 2 * nk) {
-              start_item(nx, kb + SG - nk);
-              ready = true;
-            }
-            const uint32_t pw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint4 d = decode_w4_8(pw[j], s2, zsub);
-              v[4 * j] = d.x;
-              v[4 * j + 1] = d.y;
-              v[4 * j + 2] = d.z;
-              v[4 * j + 3] = d.w;
-            }
+            const bool hi = SG == 2 ? u == 1 : sg >= 2;  // the second group of the block
+            const uint32_t s2 = __byte_perm(sc_now, sc_now, hi ? 0x3232 : 0x1010);
+            const uint32_t zsub = w4_zero_pair((hi ? zp_now >> 8 : zp_now) & 15u);
+            decode_stage_w4(c0, s2, zsub, consts, v);
+            decode_stage_w4(c1, s2, zsub, consts, v + 16);
           } else {
-            const uint4 c0 = *reinterpret_cast<const uint4*>(prow + ((ci ^ (r & 7)) << 4));
-            const uint32_t pw[4] = {c0.x, c0.y, c0.z, c0.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint4 d = decode_tq_8(pw[j >> 1], j & 1);
-              v[4 * j] = d.x;
-              v[4 * j + 1] = d.y;
-              v[4 * j + 2] = d.z;
-              v[4 * j + 3] = d.w;
-            }
+            const uint4 c0 = *reinterpret_cast<const uint4*>(prow + (((half * kTBlock + ci) ^ (r & 7)) << 4));
+            decode_stage_tq(c0, consts, v);
           }
-          ok = wait_all(&full_x[qn % RX], qn / RX);
-          // the group has seen the MMAs of stage qn - SG - AS done, so those of qn - 2 AS are, and the
-          // slot's barrier is in the awaited phase or past it
-          if (ok && qn >= AS) ok = wait_all(&empty[qn % AS], qn / AS - 1);
+          ok = ok && wait_all(&full_x[x0 + ci], blk >> 1);
+          if (ok && blk >= AB) ok = wait_all(&empty[a0 + ci], blk / AB - 1);
           if (!ok) break;
           tc_fence_after_sync();
-          tmem_st_32x32b_x32(a_slots + 32 * (qn % AS), v);
+          tmem_st_32x32b_x32(a_slots + 32 * (a0 + ci), v);
           tmem_st_wait();
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[qn % AS]);
+          if (lane == 0) mbar_arrive(&full[a0 + ci]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&emptyP[ps]);
+        if (kInt4 || half == 1 || b + 1 == nblk) {  // done with the packed tile
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&emptyP[ps]);
+          ++pq;
+        }
       }
       // the item's sums: group sg of row tile h takes every SG-th 16 rows
       const bool got = ok && wait_all(acc_full, n);
