@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
       const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x + (xr >= 0 ? xr * a.K : 0));
       const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
       const int d = n % kEItems;
-      if (n >= kEItems) ok = mbar_wait_quiet(&item_empty[d], static_cast<uint32_t>(n / kEItems - 1) & 1u);
+      if (n >= kEItems) ok = mbar_wait_warp(&item_empty[d], static_cast<uint32_t>(n / kEItems - 1) & 1u);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       if (lane == 0) {
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
       const int wrow = static_cast<int>(static_cast<int64_t>(it.e) * a.N + static_cast<int64_t>(it.tile) * kERows);
       for (int kb = 0; kb < nk && ok; ++kb, ++q) {
         const int s = q % L::kRing;
-        if (q >= L::kRing) ok = mbar_wait_quiet(&empty[s], static_cast<uint32_t>(q / L::kRing - 1) & 1u);
+        if (q >= L::kRing) ok = mbar_wait_warp(&empty[s], static_cast<uint32_t>(q / L::kRing - 1) & 1u);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         const int64_t k0 = static_cast<int64_t>(kb) * L::KS;
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[m][b][c] = 0.0f;
       const int d = n % kEItems;
-      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_quiet(&item_full[d], static_cast<uint32_t>(n / kEItems) & 1u));
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&item_full[d], static_cast<uint32_t>(n / kEItems) & 1u));
       const int4 it = items[d * 2];
       const uint32_t rmask = static_cast<uint32_t>(items[d * 2 + 1].x);
       __syncwarp();
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
           for (int j = 0; j < 4; ++j) sc_now[j] = sc[j];
           if (kb + L::KG < nk) load_scales(kb + L::KG);
         }
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_quiet(&full[s], static_cast<uint32_t>(q / L::kRing) & 1u));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&full[s], static_cast<uint32_t>(q / L::kRing) & 1u));
         if (!ok) break;
         const uint8_t* wt = sm + s * L::kTileW + (rg * 32 + pg) * 128;
         const uint8_t* xt = sm + L::kOffX + s * L::kTileX + g * L::kXRow;
@@ -549,8 +549,8 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
 //               item's accumulator: row scale and bias, fp16, rows of y through staging buffers.
 //               INT4 group scales (and zero-points) are loaded a stage ahead, the next item's first
 //               one an item ahead.
-// A decode warp arrives on the stage's barrier only after the stage's x has landed, so the issuing
-// thread tests one barrier per stage; x and decoded weights are freed by separate commits.  From
+// One of the eight (four) decode warps that arrive on a stage's barrier waits for the stage's x first,
+// so the issuing thread tests one barrier per stage; x and decoded weights are freed by separate commits.  From
 // those commits to the next MMA on the same slot is a chain of barrier wake-ups and tensor memory
 // stores of about 0.8 us: the slots (four stages at RT = 2) are what keeps the MMAs running meanwhile.
 // The rings are walked in blocks of four stages, an item's last block filled up with empty stages, so
@@ -703,7 +703,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
   // Wait of a whole warp; the lanes agree on the outcome.
   auto wait_all = [&](uint64_t* bar, int phase) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_quiet(bar, static_cast<uint32_t>(phase) & 1u)) != 0;
+    return __all_sync(0xFFFFFFFFu, mbar_wait_warp(bar, static_cast<uint32_t>(phase) & 1u)) != 0;
+  };
+  auto wait_ahead = [&](uint64_t* bar, int phase) {  // for the producers, which run ahead
+    return __all_sync(0xFFFFFFFFu, mbar_wait_relaxed(bar, static_cast<uint32_t>(phase) & 1u)) != 0;
   };
   // Item n of this CTA; every warp that uses items reads each once and releases it.
   auto take_item = [&](int n, int4* it) {
@@ -720,7 +723,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     auto publish = [&](int n) {
       const ExpertItem it = expert_item<true>(a, first, blockIdx.x + static_cast<int64_t>(n) * gridDim.x, tiles, kTTok);
       const int d = n % kTItems;
-      if (n >= kTItems) ok = wait_all(&item_empty[d], n / kTItems - 1);
+      if (n >= kTItems) ok = wait_ahead(&item_empty[d], n / kTItems - 1);
       if (ok && lane == 0) {
         items[d] = make_int4(it.e, it.tile, it.row0, it.rows);
         mbar_arrive(&item_full[d]);
@@ -734,7 +737,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int row_next = n + 1 < count ? publish(n + 1) : 0;
       for (int pt = 0; pt < npt && ok; ++pt, ++pq) {
         const int s = pq % RP;
-        if (pq >= RP) ok = wait_all(&emptyP[s], pq / RP - 1);
+        if (pq >= RP) ok = wait_ahead(&emptyP[s], pq / RP - 1);
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(&fullP[s], L::kTileP);
 #pragma unroll
@@ -792,7 +795,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const int boxes = (it.w + kTBox - 1) / kTBox;
         for (int kb = 0; kb < nblk * kTBlock && ok && !skipx; ++kb, ++q) {
           const int s = q % kTXRing;
-          if (q >= kTXRing) ok = wait_all(&empty_x[s], q / kTXRing - 1);
+          if (q >= kTXRing) ok = wait_ahead(&empty_x[s], q / kTXRing - 1);
           if (!ok) break;
           if (kb >= nk) {  // fills up the block: nothing to load
             if (lane == 0) mbar_arrive(&full_x[s]);
@@ -825,7 +828,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const int pieces = ((it.w + 15) / 16 * 16) / 8;
         for (int kb = 0; kb < nblk * kTBlock && ok && !skipx; ++kb, ++q) {
           const int s = q % kTXRing;
-          if (q >= kTXRing) ok = wait_all(&empty_x[s], q / kTXRing - 1);
+          if (q >= kTXRing) ok = wait_ahead(&empty_x[s], q / kTXRing - 1);
           if (!ok) break;
           uint8_t* dst = sm + s * L::kTileX + sub * 128 + ((ch ^ (sub & 7)) << 4);
           const __half* src = a.x + kb * 64 + ch * 8;
@@ -880,6 +883,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       fetch(0);
     };
     const DecodeConsts consts = decode_consts(kInt4);
+    const bool watch_x = h == 0 && (warp & 3) == 0;  // one warp of those that arrive for a stage
     int blk = 0, pq = 0;
     if (count > 0) ok = take_item(0, &nx);
     if (kInt4 && ok && count > 0) start_item(nx);
@@ -917,7 +921,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const uint4 c0 = *reinterpret_cast<const uint4*>(prow + (((half * kTBlock + ci) ^ (r & 7)) << 4));
             decode_stage_tq(c0, consts, v);
           }
-          ok = ok && wait_all(&full_x[x0 + ci], blk >> 1);
+          if (watch_x && ok) ok = wait_all(&full_x[x0 + ci], blk >> 1);
           if (ok && blk >= AB) ok = wait_all(&empty[a0 + ci], blk / AB - 1);
           if (!ok) break;
           tc_fence_after_sync();

@@ -105,16 +105,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// mbar_wait for kernels with many waiting warps: between two looks at the clock a run of tries that
-// issue nothing else, so that the waiting warps leave the issue slots to the working ones.
-__device__ __forceinline__ bool mbar_wait_quiet(uint64_t* bar, uint32_t parity) {
+// mbar_wait for a warp that runs ahead of its consumers: it sleeps between tries, since try_wait
+// returns within tens of cycles and a polling warp takes issue slots from the working ones.
+__device__ __forceinline__ bool mbar_wait_relaxed(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
   if (mbar_try_wait(a, parity)) return true;
   const long long t0 = clock64();
   while (true) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait_hint(a, parity, 20000u)) return true;
+    for (int i = 0; i < 16; ++i) {
+      __nanosleep(128);
+      if (mbar_try_wait(a, parity)) return true;
+    }
     if (clock64() - t0 > *reinterpret_cast<volatile long long*>(&g_tq_wait_limit)) {
       record_timeout();
       return false;
