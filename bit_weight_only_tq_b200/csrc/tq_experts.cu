@@ -534,81 +534,79 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
 // K.  The MMA's N is the item's own number of rows rounded up to 16 (an expert's rows are cut
 // evenly), so a ragged expert costs its rows and not a full tile.
 //
-// RT = 2: each stage of x (64 k) feeds two accumulators, which halves the x that crosses L2 per
-// MMA and gives the issuing thread eight MMAs per barrier test (a test stalls its MMA stream).
-// RT = 1 serves launches whose items would otherwise leave SMs idle.  20 warps:
-//   warp 0      x by TMA (64 k, 128-byte swizzle, boxes of 32 sorted rows); through `order`, warps 0
-//               and 3 copy the rows with 16-byte cp.async into the same layout (rows outside x
+// RT = 2: each stage of x (128 k) feeds two accumulators, which halves the x that crosses L2 per
+// MMA; RT = 1 serves launches whose items would otherwise leave SMs idle.  20 warps:
+//   warp 0      x: by TMA (two tiles of 64 k, 128-byte swizzle, boxes of 32 sorted rows), or, through
+//               `order` and with warp 3, by 16-byte cp.async into the same layout (rows outside x
 //               zero-filled).  tile::gather4 loads were tried for this: 39 ns per four rows.
-//   warp 1      allocates tensor memory; one lane issues the MMAs;
+//   warp 1      the MMAs (without `order` and with RT = 2 those of one row tile, warp 3 the other's): the
+//               whole warp runs the loop and one elected lane issues, so that the operands are
+//               warp-uniform values (computed by a single lane they cost about 140 cycles per MMA).  A
+//               barrier test costs the issuing warp 200 to 300 cycles whatever its outcome: hence
+//               eight MMAs per test, and one warp's tests under the other's MMAs.
 //   warp 2      finds the items (a search in the chunk table), hands them to the other warps through
 //               a ring of descriptors one item ahead, and loads the packed weights, 128 rows x 128
-//               bytes per load (4 INT4 / 8 ternary stages);
+//               bytes per load (2 INT4 / 4 ternary stages);
 //   warps 4-19  four groups of four that decode, a row tile's stages in turn (thread = weight row =
-//               tensor memory lane: 64 weights into 32 registers and one tcgen05.st), then read the
-//               item's accumulator: row scale and bias, fp16, rows of y through staging buffers.
-//               INT4 group scales (and zero-points) are loaded a stage ahead, the next item's first
-//               one an item ahead.
-// One of the eight (four) decode warps that arrive on a stage's barrier waits for the stage's x first,
-// so the issuing thread tests one barrier per stage; x and decoded weights are freed by separate commits.  From
-// those commits to the next MMA on the same slot is a chain of barrier wake-ups and tensor memory
-// stores of about 0.8 us: the slots (four stages at RT = 2) are what keeps the MMAs running meanwhile.
-// The rings are walked in blocks of four stages, an item's last block filled up with empty stages, so
-// that slots and phases are constants of the unrolled code: the decode is bound by issue slots.
+//               tensor memory lane: 128 weights into tensor memory, 32 registers at a time) and, one
+//               stage into the next item, read the item's accumulator: row scale and bias, fp16,
+//               straight to y.  INT4 group scales (and zero-points) are loaded a stage ahead.
+// A group has one slot of decoded weights.  One warp of a group also waits for the stage's x, after the
+// slot, so that the issuing warp tests one barrier per stage.  The chain from an MMA's end to the next
+// one on the same slot -- barrier wake-ups, tensor memory stores, the test -- takes about 0.8 us, and
+// each barrier wait of a decode warp 0.1 to 0.2 us: stages of 64 k with twice the slots lost more to it.
 // ---------------------------------------------------------------------------------------------
 constexpr int kTTok = 128;       // rows of x per item (MMA N)
 constexpr int kTBox = 32;        // sorted rows per x load
-constexpr int kTSlots = 8;       // slots of decoded weights, of all row tiles
-constexpr int kTXRing = 8;       // stages of x
-constexpr int kTBlock = 4;       // stages per block: the rings are walked in blocks, an item's last one filled up
+constexpr int kTK = 128;         // k per stage
 constexpr int kTGroups = 4;      // decode groups
 constexpr int kTThreads = 32 * (4 + 4 * kTGroups);
 constexpr int kTItems = 4;
-constexpr int kTYTok = 16;       // rows of y per staging buffer
+constexpr int kTMaxRing = 4;
 
-template <bool kInt4, int RT>
+template <bool kInt4, bool kOrder, int RT>
 struct ExpertTcLayout {
-  static constexpr int SPP = kInt4 ? 4 : 8;    // stages per packed tile
-  static constexpr int SG = kTGroups / RT;     // decode groups of a row tile
-  static constexpr int AS = kTSlots / RT;      // its slots of decoded weights
-  static constexpr int AB = AS / kTBlock;      // blocks of slots
-  static constexpr int RP = RT == 2 ? 2 : 3;   // packed tiles
-  static_assert(kTBlock % SG == 0 && AS % kTBlock == 0 && kTXRing == 2 * kTBlock, "a group sees every phase of its slots");
-  static constexpr int kTileX = kTTok * 128;
+  static constexpr int SPP = kInt4 ? 2 : 4;    // stages per packed tile
+  static constexpr int SG = kTGroups / RT;     // decode groups, and slots, of a row tile
+  static constexpr int MW = kOrder ? 1 : RT;   // MMA warps
+  static constexpr int XW = kOrder ? 2 : 1;    // x warps
+  static constexpr int RX = RT == 2 ? 3 : 4;   // stages of x
+  static constexpr int RP = 3;                 // packed tiles
+  // A decode warp tests the barrier of stage q's x knowing that the MMAs of stage q - SG are done: the
+  // slot's previous stage q - RX must be no later than that one.
+  static_assert(RX >= SG && RX <= kTMaxRing && SG <= kTMaxRing, "rings");
+  static constexpr int kSubX = kTTok * 128;    // 64 k of x
+  static constexpr int kTileX = 2 * kSubX;
   static constexpr int kTileP = RT * kERows * 128;
-  static constexpr int kStage = kTYTok * kERows * 2;
-  static constexpr int kOffP = kTXRing * kTileX;
-  static constexpr int kOffY = kOffP + RP * kTileP;
-  static constexpr int kOffBar = kOffY + kTGroups * kStage;
-  // full[AS], emptyA[AS], fullX[RX], emptyX[RX], fullP[RP], emptyP[RP], accFull, accEmpty, itemFull[I],
-  // itemEmpty[I]
-  static constexpr int kNumBars = 2 * kTSlots + 2 * kTXRing + 2 * RP + 2 + 2 * kTItems;
+  static constexpr int kOffP = RX * kTileX;
+  static constexpr int kOffBar = kOffP + RP * kTileP;
+  // full[MW][SG], empty[MW][SG], fullX[RX], emptyX[RX], fullP[RP], emptyP[RP], accFull[MW], accEmpty[MW],
+  // itemFull[I], itemEmpty[I]
+  static constexpr int kNumBars = 4 * kTMaxRing + 2 * kTMaxRing + 2 * RP + 4 + 2 * kTItems;
   static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
-  static constexpr int kOffMisc = kOffItem + kTItems * 16;  // TMEM slot, the groups' failure flags
+  static constexpr int kOffMisc = kOffItem + kTItems * 16;  // TMEM address, decode constants
   static constexpr int kOffScan = kOffMisc + 32;
   static constexpr int kOffFirst = kOffScan + 32 * 4;
   static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }
-  static constexpr uint32_t kColA = RT * kTTok;
-  static_assert(RT * kTTok + 32 * kTSlots <= 512, "tensor memory");
+  static constexpr uint32_t kColA = RT * kTTok;  // slots of 64 columns: 128 k
+  static_assert(RT * kTTok + 64 * RT * SG <= 512, "tensor memory");
   static_assert(kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 && kOffFirst > 114 * 1024, "one CTA per SM");
 };
 
-// (v & mask) | base in one instruction: with both constants written out the compiler spends two.
+// (v & mask) | base in one instruction: with both constants written out the compiler spends two, and
+// constants that it sees as uniform it moves into place for every use.  They come from shared memory.
 struct DecodeConsts {
   uint32_t mask0, base0, mask1, base1;
 };
-__device__ __forceinline__ uint32_t opaque(uint32_t c) {
-  uint32_t r;
-  asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(c));
-  return r;
+__device__ __forceinline__ void store_decode_consts(bool int4, uint32_t* c) {  // four words
+  c[0] = int4 ? 0x00F0000Fu : 0x000C0003u;
+  c[1] = int4 ? 0x54006400u : 0x5C006400u;
+  c[2] = 0x00C00030u;
+  c[3] = 0x4C005400u;
 }
-__device__ __forceinline__ DecodeConsts decode_consts(bool int4) {
-  DecodeConsts c;
-  c.mask0 = opaque(int4 ? 0x00F0000Fu : 0x000C0003u);
-  c.base0 = opaque(int4 ? 0x54006400u : 0x5C006400u);
-  c.mask1 = opaque(0x00C00030u);
-  c.base1 = opaque(0x4C005400u);
-  return c;
+__device__ __forceinline__ DecodeConsts load_decode_consts(const uint32_t* c) {
+  const volatile uint32_t* v = c;
+  return DecodeConsts{v[0], v[1], v[2], v[3]};
 }
 __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t base) {
   uint32_t r;
@@ -616,19 +614,18 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t b
   return r;
 }
 // 32 INT4 codes -> 16 registers of fp16 pairs (u - z) s, in natural order (as decode_w4_8).
-__device__ __forceinline__ void decode_stage_w4(const uint4& c, uint32_t s2, uint32_t zsub, const DecodeConsts& k,
-                                                uint32_t* v) {
+__device__ __forceinline__ void decode_piece_w4(const uint4& c, uint32_t s2, uint32_t zsub, const DecodeConsts& k,
+                                                uint32_t (&v)[16]) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     v[i] = hmul2_u32(hsub2_u32(and_or(byte_to_halves(w[i >> 2], i & 3), k.mask0, k.base0), zsub), s2);
 }
-// 64 ternary codes -> 32 registers of fp16 pairs c - 1, in natural order (as decode_tq_8).
-__device__ __forceinline__ void decode_stage_tq(const uint4& c, const DecodeConsts& k, uint32_t* v) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+// 32 ternary codes -> 16 registers of fp16 pairs c - 1, in natural order (as decode_tq_8).
+__device__ __forceinline__ void decode_piece_tq(const uint2& c, const DecodeConsts& k, uint32_t (&v)[16]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t t = byte_to_halves(w[i >> 2], i & 3);
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t t = byte_to_halves(i < 4 ? c.x : c.y, i & 3);
     v[2 * i] = hsub2_u32(and_or(t, k.mask0, k.base0), 0x5C046401u);
     v[2 * i + 1] = hsub2_u32(and_or(t, k.mask1, k.base1), 0x4C405410u);
   }
@@ -638,47 +635,48 @@ template <bool kInt4, bool kOrder, int RT>
 __global__ void __launch_bounds__(kTThreads, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                       const ExpertArgs a) {
-  using L = ExpertTcLayout<kInt4, RT>;
-  constexpr int SG = L::SG, AS = L::AS, AB = L::AB, RP = L::RP;
+  using L = ExpertTcLayout<kInt4, kOrder, RT>;
+  constexpr int SG = L::SG, MW = L::MW, RX = L::RX, RP = L::RP;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
-  uint64_t* empty = full + kTSlots;
-  uint64_t* full_x = empty + kTSlots;
-  uint64_t* empty_x = full_x + kTXRing;
-  uint64_t* fullP = empty_x + kTXRing;
+  uint64_t* empty = full + 2 * kTMaxRing;
+  uint64_t* full_x = empty + 2 * kTMaxRing;
+  uint64_t* empty_x = full_x + kTMaxRing;
+  uint64_t* fullP = empty_x + kTMaxRing;
   uint64_t* emptyP = fullP + RP;
   uint64_t* acc_full = emptyP + RP;
-  uint64_t* acc_empty = acc_full + 1;
-  uint64_t* item_full = acc_empty + 1;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* item_full = acc_empty + 2;
   uint64_t* item_empty = item_full + kTItems;
   int4* items = reinterpret_cast<int4*>(sm + L::kOffItem);  // (e, tile, row0, rows)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kOffMisc);
   int* first = reinterpret_cast<int*>(sm + L::kOffFirst);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kXWarps = kOrder ? 2 : 1;
 
   pdl_allow_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < AS; ++i) {
-      mbar_init(&full[i], 4 * RT);
+    for (int i = 0; i < MW * SG; ++i) {
+      mbar_init(&full[i], 4 * RT / MW);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kTXRing; ++i) {
-      mbar_init(&full_x[i], kXWarps);
-      mbar_init(&empty_x[i], 1);
+    for (int i = 0; i < RX; ++i) {
+      mbar_init(&full_x[i], L::XW);
+      mbar_init(&empty_x[i], MW);
     }
     for (int i = 0; i < RP; ++i) {
       mbar_init(&fullP[i], 1);
       mbar_init(&emptyP[i], 4 * kTGroups);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 4 * kTGroups);
+    for (int i = 0; i < MW; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4 * kTGroups / MW);
+    }
     for (int i = 0; i < kTItems; ++i) {
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], kXWarps + 1 + 4 * kTGroups);
+      mbar_init(&item_empty[i], L::XW + MW + 4 * kTGroups);
     }
-    for (int i = 1; i < 8; ++i) misc[i] = 0u;
+    store_decode_consts(kInt4, misc + 4);
     fence_mbar_init();
     tma_prefetch_desc(&tmap_x);
     tma_prefetch_desc(&tmap_w);
@@ -694,18 +692,17 @@ __global__ void __launch_bounds__(kTThreads, 1)
   constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's: they start at 0
   const int64_t tiles = (a.N + RT * kERows - 1) / (RT * kERows);
   const int64_t total = static_cast<int64_t>(first[a.E]) * tiles;
-  const int nk = static_cast<int>(a.K / 64);
-  const int nblk = (nk + kTBlock - 1) / kTBlock;
+  const int nk = static_cast<int>((a.K + kTK - 1) / kTK);  // the last stage may hold 64 k
   const int npt = (nk + L::SPP - 1) / L::SPP;
   // items of this CTA
   const int count = static_cast<int>(total > blockIdx.x ? (total - blockIdx.x + gridDim.x - 1) / gridDim.x : 0);
   bool ok = true;
 
-  // Wait of a whole warp; the lanes agree on the outcome.
+  // Waits of a whole warp; the lanes agree on the outcome.  wait_ahead: for the producers.
   auto wait_all = [&](uint64_t* bar, int phase) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_warp(bar, static_cast<uint32_t>(phase) & 1u)) != 0;
   };
-  auto wait_ahead = [&](uint64_t* bar, int phase) {  // for the producers, which run ahead
+  auto wait_ahead = [&](uint64_t* bar, int phase) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_relaxed(bar, static_cast<uint32_t>(phase) & 1u)) != 0;
   };
   // Item n of this CTA; every warp that uses items reads each once and releases it.
@@ -731,13 +728,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
       __syncwarp();
       return static_cast<int>(static_cast<int64_t>(it.e) * a.N + static_cast<int64_t>(it.tile) * (RT * kERows));
     };
-    int pq = 0, row = 0;
+    int s = 0, phase = -1, row = 0;  // packed slot; its previous load's phase
     if (count > 0) row = publish(0);
     for (int n = 0; n < count && ok; ++n) {
       const int row_next = n + 1 < count ? publish(n + 1) : 0;
-      for (int pt = 0; pt < npt && ok; ++pt, ++pq) {
-        const int s = pq % RP;
-        if (pq >= RP) ok = wait_ahead(&emptyP[s], pq / RP - 1);
+      for (int pt = 0; pt < npt && ok; ++pt) {
+        if (phase >= 0) ok = wait_ahead(&emptyP[s], phase);
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(&fullP[s], L::kTileP);
 #pragma unroll
@@ -745,248 +741,290 @@ __global__ void __launch_bounds__(kTThreads, 1)
             tma_load_2d(sm + L::kOffP + s * L::kTileP + h * kERows * 128, &tmap_w, &fullP[s], pt * 128, row + h * kERows);
         }
         __syncwarp();
+        if (++s == RP) {
+          s = 0;
+          ++phase;
+        }
       }
       row = row_next;
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || (MW == 2 && warp == 3)) {
     // ------------------------------------------------------------------ MMA
-    // The whole warp runs the loop and one elected lane issues: the operands are then warp-uniform
-    // values, kept where the MMA takes them from; computed by a single lane they cost about 140
-    // cycles per MMA.
+    const int m = warp >> 1;  // MMA warp: row tile m of two, or all of them
     const uint32_t leader = elect_one() ? 1u : 0u;
     const uint64_t xdesc = sdesc_kmajor_sw128(smem_u32(sm));
-    int blk = 0;
+    int s = 0, phase = 0, sx = 0;
     for (int n = 0; n < count && ok; ++n) {
       int4 it;
       ok = take_item(n, &it);
-      if (ok && n >= 1) ok = wait_all(acc_empty, n - 1);
+      if (ok && n >= 1) ok = wait_all(&acc_empty[m], n - 1);
       const uint32_t idesc = idesc_f16_f32(kERows, static_cast<uint32_t>((it.w + 15) / 16 * 16));
-      for (int b = 0; b < nblk && ok; ++b, ++blk) {
-        const int a0 = (blk % AB) * kTBlock, x0 = (blk & 1) * kTBlock;
+      for (int kb = 0; kb < nk && ok; ++kb) {
+        ok = wait_all(&full[m * SG + s], phase);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint64_t bdesc = xdesc + static_cast<uint64_t>(sx * (L::kTileX >> 4));
+        const uint32_t asrc = L::kColA + 64 * (m * SG + s);
+        const int steps = a.K - static_cast<int64_t>(kb) * kTK >= kTK ? 8 : 4;
 #pragma unroll
-        for (int u = 0; u < kTBlock; ++u) {
-          ok = ok && wait_all(&full[a0 + u], blk / AB);
-          if (!ok) break;
-          tc_fence_after_sync();
-          const uint64_t bdesc = xdesc + static_cast<uint64_t>((x0 + u) * (L::kTileX >> 4));
-          const uint32_t asrc = L::kColA + 32 * (a0 + u);
-          if (b * kTBlock + u < nk) {
+        for (int k16 = 0; k16 < 8; ++k16) {
+          if (k16 >= steps) break;
 #pragma unroll
-            for (int k16 = 0; k16 < 4; ++k16)
-#pragma unroll
-              for (int h = 0; h < RT; ++h)
-                umma_f16_ts_if(leader, h * kTTok, asrc + 32 * h * AS + 8 * k16, bdesc + 2 * k16, idesc,
-                               (b | u | k16) != 0 ? 1u : 0u);
-          }
-          umma_commit_if(leader, &empty[a0 + u]);
-          umma_commit_if(leader, &empty_x[x0 + u]);
+          for (int h = 0; h < RT / MW; ++h)
+            umma_f16_ts_if(leader, (m + h) * kTTok, asrc + 64 * h * SG + 8 * k16,
+                           bdesc + (k16 >> 2) * (L::kSubX >> 4) + 2 * (k16 & 3), idesc, (kb | k16) != 0 ? 1u : 0u);
         }
+        umma_commit_if(leader, &empty[m * SG + s]);
+        umma_commit_if(leader, &empty_x[sx]);
+        if (++s == SG) {
+          s = 0;
+          phase ^= 1;
+        }
+        if (++sx == RX) sx = 0;
       }
-      if (ok) umma_commit_if(leader, acc_full);
+      if (ok) umma_commit_if(leader, &acc_full[m]);
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------------ x
     const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
-    int q = 0;
+    int s = 0, phase = -1;              // x slot; its previous stage's phase
     if (!kOrder) {
       for (int n = 0; n < count && ok && warp == 0; ++n) {
         int4 it;
         ok = take_item(n, &it);
         const int boxes = (it.w + kTBox - 1) / kTBox;
-        for (int kb = 0; kb < nblk * kTBlock && ok && !skipx; ++kb, ++q) {
-          const int s = q % kTXRing;
-          if (q >= kTXRing) ok = wait_ahead(&empty_x[s], q / kTXRing - 1);
+        // lanes 0 .. 2 boxes - 1: box lane / 2 of 64-k tile lane % 2
+        const int sub = lane & 1, box = lane >> 1;
+        for (int kb = 0; kb < nk && ok && !skipx; ++kb) {
+          if (phase >= 0) ok = wait_ahead(&empty_x[s], phase);
           if (!ok) break;
-          if (kb >= nk) {  // fills up the block: nothing to load
-            if (lane == 0) mbar_arrive(&full_x[s]);
-            continue;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&full_x[s], boxes * kTBox * 128);
+          const bool two = a.K - static_cast<int64_t>(kb) * kTK >= kTK;
+          if (lane == 0) mbar_arrive_expect_tx(&full_x[s], boxes * kTBox * 128 * (two ? 2 : 1));
           __syncwarp();
-          if (lane < boxes)
-            tma_load_2d(sm + s * L::kTileX + lane * kTBox * 128, &tmap_x, &full_x[s], kb * 64, it.z + lane * kTBox);
+          if (box < boxes && (two || sub == 0))
+            tma_load_2d(sm + s * L::kTileX + sub * L::kSubX + box * kTBox * 128, &tmap_x, &full_x[s], kb * kTK + sub * 64,
+                        it.z + box * kTBox);
+          if (++s == RX) {
+            s = 0;
+            ++phase;
+          }
         }
       }
     } else {
-      // lane: 16-byte chunk lane % 8 of rows 8 i + 4 w + lane / 8
-      const int w = warp == 0 ? 0 : 1, sub = 4 * w + (lane >> 3), ch = lane & 7;
-      constexpr int kLag = 2;  // a stage is handed over when the second one after it has been issued
-      auto hand_over = [&](int qq) {
+      // lane: 16-byte chunk lane % 16 of the rows 4 i + 2 w + lane / 16; a stage is handed over when the
+      // next one has been issued
+      const int w = warp == 0 ? 0 : 1, sub = 2 * w + (lane >> 4), ch = lane & 15;
+      int s_done = 0;
+      bool pending = false;
+      auto hand_over = [&] {
         fence_proxy_async_smem();  // these copies are generic-proxy writes; the MMA reads by the async proxy
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full_x[qq % kTXRing]);
+        if (lane == 0) mbar_arrive(&full_x[s_done]);
+        if (++s_done == RX) s_done = 0;
       };
       for (int n = 0; n < count && ok; ++n) {
         int4 it;
         ok = take_item(n, &it);
-        int rows[kTTok / 8];
+        const int pieces = ((it.w + 15) / 16 * 16) / 4;
+        int rows[kTTok / 4];
 #pragma unroll
-        for (int i = 0; i < kTTok / 8; ++i) {
-          const int r = 8 * i + sub;
+        for (int i = 0; i < kTTok / 4; ++i) {
+          const int r = 4 * i + sub;
           rows[i] = ok && r < it.w ? static_cast<int>(expert_x_row(a, it.z + r)) : -1;
         }
-        const int pieces = ((it.w + 15) / 16 * 16) / 8;
-        for (int kb = 0; kb < nblk * kTBlock && ok && !skipx; ++kb, ++q) {
-          const int s = q % kTXRing;
-          if (q >= kTXRing) ok = wait_ahead(&empty_x[s], q / kTXRing - 1);
+        for (int kb = 0; kb < nk && ok && !skipx; ++kb) {
+          if (phase >= 0) ok = wait_ahead(&empty_x[s], phase);
           if (!ok) break;
-          uint8_t* dst = sm + s * L::kTileX + sub * 128 + ((ch ^ (sub & 7)) << 4);
-          const __half* src = a.x + kb * 64 + ch * 8;
+          const bool in = kb * static_cast<int64_t>(kTK) + ch * 8 < a.K;
+          uint8_t* dst = sm + s * L::kTileX + (ch >> 3) * L::kSubX + sub * 128;
+          const __half* src = a.x + (in ? static_cast<int64_t>(kb) * kTK + ch * 8 : 0);
 #pragma unroll
-          for (int i = 0; i < kTTok / 8; ++i)
-            if (i < pieces && kb < nk)
-              cp_async_16(dst + i * 1024, src + (rows[i] < 0 ? 0 : rows[i] * a.K), rows[i] < 0 ? 0u : 16u);
+          for (int i = 0; i < kTTok / 4; ++i)
+            if (i < pieces)
+              cp_async_16(dst + i * 512 + (((ch & 7) ^ ((4 * i + sub) & 7)) << 4), src + (rows[i] < 0 ? 0 : rows[i] * a.K),
+                          rows[i] < 0 || !in ? 0u : 16u);
           cp_async_commit();
-          if (q >= kLag) {
-            cp_async_wait<kLag>();
-            hand_over(q - kLag);
+          if (pending) {
+            cp_async_wait<1>();
+            hand_over();
+          }
+          pending = true;
+          if (++s == RX) {
+            s = 0;
+            ++phase;
           }
         }
       }
       cp_async_wait<0>();
-      for (int qq = q - kLag < 0 ? 0 : q - kLag; qq < q; ++qq) hand_over(qq);
+      if (pending) hand_over();
     }
   } else {
     // ------------------------------------------------------------------ decode, epilogue
     const int grp = (warp >> 2) - 1, h = grp / SG, sg = grp % SG;
+    const int m = MW == 1 ? 0 : h;  // the MMA warp that uses this row tile
     const int r = threadIdx.x & (kERows - 1);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t a_slots = lane_base + L::kColA + 32 * (h * AS);
+    const uint32_t slot = lane_base + L::kColA + 64 * grp;
+    uint64_t* const full_s = &full[m * SG + sg];
+    uint64_t* const empty_s = &empty[m * SG + sg];
     const int64_t G = a.K >> 7;
     const uint8_t* prow0 = sm + L::kOffP + (h * kERows + r) * 128;
-    __half* stage = reinterpret_cast<__half*>(sm + L::kOffY + grp * L::kStage);
-    const bool vec = (a.N & 7) == 0;  // y itself is 16-byte aligned
     int4 nx = make_int4(0, 0, 0, 0);
-    // The group scales (and zero-points) of this thread's weight row: a block of four stages has two
-    // groups of k, 2 b and 2 b + 1; both are loaded a block ahead.
+    // scales / zero-points of this thread's weight row: one group of k per stage
     const __half* scp = a.sc;
     const uint8_t* zpp = a.zp;
-    uint32_t sc_nxt = 0, zp_nxt = 0x0808u;
-    const bool pairs = (G & 1) == 0 && (reinterpret_cast<uintptr_t>(a.sc) & 3u) == 0;
-    auto fetch = [&](int b) {
-      if (pairs) {
-        sc_nxt = *reinterpret_cast<const uint32_t*>(scp + 2 * b);
-      } else {
-        sc_nxt = __half_as_ushort(scp[2 * b]);
-        if (2 * b + 1 < G) sc_nxt |= static_cast<uint32_t>(__half_as_ushort(scp[2 * b + 1])) << 16;
-      }
-      if (zpp) {
-        zp_nxt = zpp[2 * b];
-        if (2 * b + 1 < G) zp_nxt |= static_cast<uint32_t>(zpp[2 * b + 1]) << 8;
-      }
+    uint32_t sc_nxt = 0, zp_nxt = 8;
+    auto fetch = [&](int kb) {
+      sc_nxt = __half_as_ushort(scp[kb]);
+      if (zpp) zp_nxt = zpp[kb];
     };
-    auto start_item = [&](const int4& it) {
+    auto start_item = [&](const int4& it, int kb) {  // the group's first stage of the item is kb
       const int64_t n = static_cast<int64_t>(it.y) * (RT * kERows) + h * kERows + r;
       const int64_t row = (static_cast<int64_t>(it.x) * a.N + (n < a.N ? n : 0)) * G;  // past N: not stored
       scp = a.sc + row;
       if (a.zp) zpp = a.zp + row;
-      fetch(0);
+      fetch(kb);
     };
-    const DecodeConsts consts = decode_consts(kInt4);
-    const bool watch_x = h == 0 && (warp & 3) == 0;  // one warp of those that arrive for a stage
-    int blk = 0, pq = 0;
-    if (count > 0) ok = take_item(0, &nx);
-    if (kInt4 && ok && count > 0) start_item(nx);
-    for (int n = 0; n < count && ok; ++n) {
-      const int4 it = nx;
-      const bool more = n + 1 < count;
-      if (more) ok = take_item(n + 1, &nx);
-      for (int b = 0; b < nblk && ok; ++b, ++blk) {
-        const int ps = pq % RP;
-        // a packed tile is one block of INT4 stages, two of ternary
-        const int half = kInt4 ? 0 : b & 1;
-        if (half == 0) ok = wait_all(&fullP[ps], pq / RP);
-        const uint8_t* prow = prow0 + ps * L::kTileP;
-        const uint32_t sc_now = sc_nxt, zp_now = zp_nxt;
-        if (kInt4 && ok) {
-          if (b + 1 < nblk)
-            fetch(b + 1);
-          else if (more)
-            start_item(nx);
-        }
-        const int a0 = (blk % AB) * kTBlock, x0 = (blk & 1) * kTBlock;
-#pragma unroll
-        for (int u = 0; u < kTBlock / SG; ++u) {
-          const int ci = u * SG + sg;
-          uint32_t v[32];  // a stage that fills up the block is decoded too, and not multiplied
-          if (kInt4) {
-            const uint4 c0 = *reinterpret_cast<const uint4*>(prow + (((2 * ci) ^ (r & 7)) << 4));
-            const uint4 c1 = *reinterpret_cast<const uint4*>(prow + (((2 * ci + 1) ^ (r & 7)) << 4));
-            const bool hi = SG == 2 ? u == 1 : sg >= 2;  // the second group of the block
-            const uint32_t s2 = __byte_perm(sc_now, sc_now, hi ? 0x3232 : 0x1010);
-            const uint32_t zsub = w4_zero_pair((hi ? zp_now >> 8 : zp_now) & 15u);
-            decode_stage_w4(c0, s2, zsub, consts, v);
-            decode_stage_w4(c1, s2, zsub, consts, v + 16);
-          } else {
-            const uint4 c0 = *reinterpret_cast<const uint4*>(prow + (((half * kTBlock + ci) ^ (r & 7)) << 4));
-            decode_stage_tq(c0, consts, v);
-          }
-          if (watch_x && ok) ok = wait_all(&full_x[x0 + ci], blk >> 1);
-          if (ok && blk >= AB) ok = wait_all(&empty[a0 + ci], blk / AB - 1);
-          if (!ok) break;
-          tc_fence_after_sync();
-          tmem_st_32x32b_x32(a_slots + 32 * (a0 + ci), v);
-          tmem_st_wait();
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[a0 + ci]);
-        }
-        if (kInt4 || half == 1 || b + 1 == nblk) {  // done with the packed tile
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&emptyP[ps]);
-          ++pq;
-        }
-      }
-      // the item's sums: group sg of row tile h takes every SG-th 16 rows
-      const bool got = ok && wait_all(acc_full, n);
-      if (!got && lane == 0) misc[1 + grp] = 1u;  // the four warps of a group go on together or not at all
-      warps_barrier(1 + grp, 128);
-      ok = misc[1 + grp] == 0u;
-      if (!ok) break;
-      tc_fence_after_sync();
-      const int64_t n0 = static_cast<int64_t>(it.y) * (RT * kERows) + h * kERows, nr = n0 + r;
+    const DecodeConsts consts = load_decode_consts(misc + 4);
+    const bool watch_x = (warp & 3) == 0 && (MW == 2 || h == 0);  // looks after x for the MMA warp's barrier
+    int sx = sg, phase_x = 0;         // the slot of the group's next stage of x
+    int own = 0;                      // stages that the group has decoded
+    int kn = sg;                      // its next stage within the item
+    int ps = 0, phase_p = 0;          // packed slot
+    bool ready = false;               // the next stage's scale has been fetched
+
+    // The sums of item n: of its 32-row chunks group sg of row tile h takes every SG-th.  Read and
+    // rounded into registers first, so that the accumulator is free for the next item's MMAs, then
+    // stored: a warp's 32 weight rows of one row of y are 64 contiguous bytes.
+    auto epilogue = [&](int n, const int4& it) {
+      const int64_t nr = static_cast<int64_t>(it.y) * (RT * kERows) + h * kERows + r;
       const int64_t en = static_cast<int64_t>(it.x) * a.N + nr;
       float es = 1.0f, eb = 0.0f;
       if (nr < a.N) {
         if (!kInt4) es = __half2float(a.sc[en]);
         if (a.bias) eb = __half2float(a.bias[en]);
       }
-      __syncwarp();
-      for (int c = sg; c * kTYTok < it.w; c += SG) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(lane_base + h * kTTok + c * kTYTok, v);
-        tmem_ld_wait();
-        if ((c + SG) * kTYTok >= it.w) {  // this group has read its share
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(acc_empty);
-        }
-        const int cnt = it.w - c * kTYTok < kTYTok ? it.w - c * kTYTok : kTYTok;
-        __half* yrow = a.y + (static_cast<int64_t>(it.z) + c * kTYTok) * a.N + n0;
-        auto out = [&](int j) { return __float2half_rn(fmaf(__uint_as_float(v[j]), es, eb)); };
-        if (vec) {
+      if (!wait_all(&acc_full[m], n)) return false;
+      tc_fence_after_sync();
+      constexpr int kChunks = kTTok / 32 / SG;
+      uint32_t out[kChunks][16];
 #pragma unroll
-          for (int j = 0; j < kTYTok; ++j) stage[j * kERows + r] = out(j);
-          warps_barrier(1 + grp, 128);
+      for (int c = 0; c < kChunks; ++c) {
+        const int tok = (c * SG + sg) * 32;
+        if (tok < it.w) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(lane_base + h * kTTok + tok, v);
+          tmem_ld_wait();
 #pragma unroll
-          for (int p = 0; p < kTYTok / 8; ++p) {
-            const int i = r + 128 * p, tok = i >> 4, cc = i & 15;
-            if (tok < cnt && n0 + cc * 8 < a.N)
-              *reinterpret_cast<uint4*>(yrow + tok * a.N + cc * 8) =
-                  *reinterpret_cast<const uint4*>(stage + tok * kERows + cc * 8);
+          for (int j = 0; j < 16; ++j) {
+            const __half2 p = __floats2half2_rn(fmaf(__uint_as_float(v[2 * j]), es, eb),
+                                                fmaf(__uint_as_float(v[2 * j + 1]), es, eb));
+            out[c][j] = *reinterpret_cast<const uint32_t*>(&p);
           }
-          warps_barrier(1 + grp, 128);
-        } else if (nr < a.N) {
-#pragma unroll
-          for (int j = 0; j < kTYTok; ++j)
-            if (j < cnt) yrow[j * a.N + r] = out(j);
         }
-        __syncwarp();
       }
-      if (sg * kTYTok >= it.w) {  // no share
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[m]);
+      if (nr < a.N) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const int tok = (c * SG + sg) * 32, cnt = it.w - tok;
+          uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + (static_cast<int64_t>(it.z) + tok) * a.N + nr;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (2 * j < cnt) y[0] = static_cast<uint16_t>(out[c][j]);
+            if (2 * j + 1 < cnt) y[a.N] = static_cast<uint16_t>(out[c][j] >> 16);
+            y += 2 * a.N;
+          }
+        }
       }
+      __syncwarp();
+      return true;
+    };
+
+    // U steps per packed tile, at most one stage of the group in each; after an item's first step the
+    // previous item's sums are read (the group's second stage needs its slot back, and so the MMAs that
+    // wait for them).  A last round without stages reads the last item's.
+    constexpr int U = L::SPP > SG ? L::SPP / SG : 1;
+    if (count > 0) ok = take_item(0, &nx);
+    int4 it = nx;
+    for (int n = 0; n <= count && count > 0 && ok; ++n) {
+      const int4 prev = it;
+      it = nx;
+      const bool more = n + 1 < count;
+      if (kInt4 && !ready && n < count && kn < nk) start_item(it, kn);
+      ready = false;
+      if (more) ok = take_item(n + 1, &nx);
+      const int steps = n < count ? npt * U : 1;
+      for (int i = 0, u = 0, pt = 0; i < steps && ok; ++i) {
+        if (n < count) {
+          if (u == 0) ok = wait_all(&fullP[ps], phase_p);
+          const uint8_t* prow = prow0 + ps * L::kTileP;
+          const int end = pt * L::SPP + L::SPP < nk ? pt * L::SPP + L::SPP : nk;
+          if (kn < end && ok) {
+            const int ci = kn - pt * L::SPP;  // stage within the packed tile
+            uint32_t s2 = 0, zsub = 0;
+            uint4 pc[kInt4 ? 4 : 2];
+#pragma unroll
+            for (int c = 0; c < (kInt4 ? 4 : 2); ++c)
+              pc[c] = *reinterpret_cast<const uint4*>(prow + ((((kInt4 ? 4 : 2) * ci + c) ^ (r & 7)) << 4));
+            if (kInt4) {
+              s2 = sc_nxt | (sc_nxt << 16);
+              zsub = w4_zero_pair(zp_nxt & 15u);
+              if (kn + SG < nk) {
+                fetch(kn + SG);
+              } else if (more && kn + SG < 2 * nk) {
+                start_item(nx, kn + SG - nk);
+                ready = true;
+              }
+            }
+            // four pieces of 32 k; in a last stage of 64 k the last two are decoded too, and not multiplied
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t v[16];
+              if (kInt4)
+                decode_piece_w4(pc[q], s2, zsub, consts, v);
+              else
+                decode_piece_tq((q & 1) ? make_uint2(pc[q >> 1].z, pc[q >> 1].w) : make_uint2(pc[q >> 1].x, pc[q >> 1].y),
+                                consts, v);
+              if (q == 0) {
+                if (own > 0) ok = wait_all(empty_s, own - 1);
+                if (watch_x) {
+                  ok = ok && wait_all(&full_x[sx], phase_x);
+                  sx += SG;
+                  if (sx >= RX) {
+                    sx -= RX;
+                    phase_x ^= 1;
+                  }
+                }
+                if (!ok) break;
+                tc_fence_after_sync();
+              }
+              tmem_st_32x32b_x16(slot + 16 * q, v);
+            }
+            if (!ok) break;
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full_s);
+            ++own;
+            kn += SG;
+          }
+          if (++u == U) {  // done with the packed tile
+            u = 0;
+            ++pt;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&emptyP[ps]);
+            if (++ps == RP) {
+              ps = 0;
+              phase_p ^= 1;
+            }
+          }
+        }
+        if (i == 0 && n > 0 && ok) ok = epilogue(n - 1, prev);
+      }
+      kn -= nk;
     }
   }
 
@@ -1012,7 +1050,7 @@ static cudaError_t launch_experts_tc(const ExpertArgs& a, cudaStream_t s) {
   auto run = [&](auto rt, auto ord) {
     constexpr int RT = decltype(rt)::value;
     auto* kern = experts_tc_kernel<kInt4, decltype(ord)::value, RT>;
-    const int smem = ExpertTcLayout<kInt4, RT>::bytes(a.E);
+    const int smem = ExpertTcLayout<kInt4, decltype(ord)::value, RT>::bytes(a.E);
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     const int64_t items = chunks * ((a.N + RT * kERows - 1) / (RT * kERows));
