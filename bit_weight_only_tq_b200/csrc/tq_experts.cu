@@ -29,6 +29,8 @@ __device__ __forceinline__ void warps_barrier(int id, int nthreads) {
   named_barrier_sync(id, nthreads);
 }
 
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 // The x row of sorted row r, or -1.
 __device__ __forceinline__ int64_t expert_x_row(const ExpertArgs& a, int64_t r) {
   const int64_t t = a.order ? a.order[r] / a.top_k : r;
@@ -652,7 +654,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
   int4* items = reinterpret_cast<int4*>(sm + L::kOffItem);  // (e, tile, row0, rows)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kOffMisc);
   int* first = reinterpret_cast<int*>(sm + L::kOffFirst);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // values that steer the roles are broadcast, so that the compiler knows them to be warp-uniform
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   pdl_allow_dependents();
   if (threadIdx.x == 0) {
@@ -695,7 +698,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const int nk = static_cast<int>((a.K + kTK - 1) / kTK);  // the last stage may hold 64 k
   const int npt = (nk + L::SPP - 1) / L::SPP;
   // items of this CTA
-  const int count = static_cast<int>(total > blockIdx.x ? (total - blockIdx.x + gridDim.x - 1) / gridDim.x : 0);
+  const int count = uniform(static_cast<int>(total > blockIdx.x ? (total - blockIdx.x + gridDim.x - 1) / gridDim.x : 0));
   bool ok = true;
 
   // Waits of a whole warp; the lanes agree on the outcome.  wait_ahead: for the producers.
@@ -758,7 +761,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       int4 it;
       ok = take_item(n, &it);
       if (ok && n >= 1) ok = wait_all(&acc_empty[m], n - 1);
-      const uint32_t idesc = idesc_f16_f32(kERows, static_cast<uint32_t>((it.w + 15) / 16 * 16));
+      const uint32_t idesc = idesc_f16_f32(kERows, static_cast<uint32_t>((uniform(it.w) + 15) / 16 * 16));
       for (int kb = 0; kb < nk && ok; ++kb) {
         ok = wait_all(&full[m * SG + s], phase);
         if (!ok) break;
