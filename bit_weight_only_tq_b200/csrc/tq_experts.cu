@@ -19,6 +19,7 @@ struct ExpertArgs {
   __half* y;               // [R][N]
   const int32_t* offsets;  // [E + 1]
   const int32_t* order;    // [R] or null
+  __half* rows;            // [R][K] scratch, or null (PREFILL with order needs it)
   int64_t X, R, N, K;
   int E, top_k;
 };
@@ -89,6 +90,32 @@ __global__ void __launch_bounds__(256) experts_generic_kernel(const ExpertArgs a
 template <bool kInt4>
 static cudaError_t launch_experts_generic(const ExpertArgs& a, cudaStream_t s) {
   return launch_pdl(experts_generic_kernel<kInt4>, dim3(row_grid(a.R * ((a.N + 31) / 32), 8, 8)), dim3(256), 0, 1, s, a);
+}
+
+// rows[r] = x[row(r)], zeros for a row outside x, for r < offsets[E]: a warp per 2 KB.
+__global__ void __launch_bounds__(256) experts_rows_kernel(const ExpertArgs a) {
+  pdl_allow_dependents();
+  pdl_wait_prior_grids();
+  const int lane = threadIdx.x & 31;
+  const int64_t kept = a.offsets[a.E], nv = a.K / 8, segs = (nv + 127) / 128;
+  const int64_t tasks = (kept < a.R ? kept : a.R) * segs, step = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); w < tasks; w += step) {
+    const int64_t r = w / segs, v0 = (w - r * segs) * 128 + lane;
+    const int64_t xr = expert_x_row(a, r);
+    uint4 b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      b[u] = xr >= 0 && v0 + 32 * u < nv ? reinterpret_cast<const uint4*>(a.x)[xr * nv + v0 + 32 * u]
+                                         : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (v0 + 32 * u < nv) reinterpret_cast<uint4*>(a.rows)[r * nv + v0 + 32 * u] = b[u];
+  }
+}
+
+static cudaError_t launch_experts_rows(const ExpertArgs& a, cudaStream_t s) {
+  const int64_t segs = (a.K / 8 + 127) / 128;
+  return launch_pdl(experts_rows_kernel, dim3(row_grid(a.R * segs, 8, 8)), dim3(256), 0, 1, s, a);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -531,32 +558,33 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
 
 // ---------------------------------------------------------------------------------------------
 // Many rows per expert: a dense contraction, on tcgen05 with the decoded weights as A in tensor
-// memory (as in the prefill GEMM) and the rows of x as B in shared memory.  Persistent CTAs, one
-// per SM; an item is RT tiles of 128 weight rows of one expert times up to 128 of its rows, all of
+// memory (as in the prefill GEMM) and the sorted rows of x as B in shared memory.  Persistent CTAs,
+// one per SM; an item is RT tiles of 128 weight rows of one expert times up to 128 of its rows, all of
 // K.  The MMA's N is the item's own number of rows rounded up to 16 (an expert's rows are cut
 // evenly), so a ragged expert costs its rows and not a full tile.
-//
-// RT = 2: each stage of x (128 k) feeds two accumulators, which halves the x that crosses L2 per
-// MMA; RT = 1 serves launches whose items would otherwise leave SMs idle.  20 warps:
-//   warp 0      x: by TMA (two tiles of 64 k, 128-byte swizzle, boxes of 32 sorted rows), or, through
-//               `order` and with warp 3, by 16-byte cp.async into the same layout (rows outside x
-//               zero-filled).  tile::gather4 loads were tried for this: 39 ns per four rows.
-//   warp 1      the MMAs (without `order` and with RT = 2 those of one row tile, warp 3 the other's): the
-//               whole warp runs the loop and one elected lane issues, so that the operands are
-//               warp-uniform values (computed by a single lane they cost about 140 cycles per MMA).  A
-//               barrier test costs the issuing warp 200 to 300 cycles whatever its outcome: hence
-//               eight MMAs per test, and one warp's tests under the other's MMAs.
+// RT = 2: a stage of x (128 k) feeds two accumulators, which halves the x that crosses L2 per MMA (512
+// rows per expert, 4096 -> 7168: 240 us INT4, 203 us ternary; RT = 1: 311 and 266 us).  RT = 1 serves
+// launches whose items would otherwise leave SMs idle.
+// 20 warps:
+//   warp 0      x by TMA (tiles of 64 k, 128-byte swizzle, boxes of 32 rows);
+//   warp 1      the MMAs (with RT = 2 those of one row tile, warp 3 the other's): the whole warp runs
+//               the loop and one elected lane issues, so that the operands are warp-uniform values
+//               (computed by a single lane they cost about 140 cycles per MMA).  A barrier test costs
+//               the issuing warp 200 to 300 cycles whatever its outcome: hence eight MMAs per test,
+//               and one warp's tests under the other's MMAs;
 //   warp 2      finds the items (a search in the chunk table), hands them to the other warps through
 //               a ring of descriptors one item ahead, and loads the packed weights, 128 rows x 128
 //               bytes per load (2 INT4 / 4 ternary stages);
 //   warps 4-19  four groups of four that decode, a row tile's stages in turn (thread = weight row =
-//               tensor memory lane: 128 weights into tensor memory, 32 registers at a time) and, one
-//               stage into the next item, read the item's accumulator: row scale and bias, fp16,
-//               straight to y.  INT4 group scales (and zero-points) are loaded a stage ahead.
-// A group has one slot of decoded weights.  One warp of a group also waits for the stage's x, after the
-// slot, so that the issuing warp tests one barrier per stage.  The chain from an MMA's end to the next
-// one on the same slot -- barrier wake-ups, tensor memory stores, the test -- takes about 0.8 us, and
-// each barrier wait of a decode warp 0.1 to 0.2 us: stages of 64 k with twice the slots lost more to it.
+//               tensor memory lane: 128 weights into the group's slot) and, at the start of the next
+//               item, read the item's accumulator: row scale and bias, fp16, and rows of y by TMA
+//               stores from a staging buffer per warp (all CTAs reach this point together, and plain
+//               stores of 9.7 MB at once held the warps up for 2.7 us per item).  INT4 group scales
+//               (and zero-points) are loaded a stage ahead.
+// One barrier per stage counts the decode warps of the row tiles, one of which waits for the stage's x,
+// after the slot, so that the issuing warps test one barrier per stage.  The chain from an MMA's end to
+// the next one on the same slot -- barrier wake-ups, tensor memory stores, the test -- takes about 0.8
+// us, and each barrier wait of a decode warp 0.1 to 0.2 us: stages of 64 k lost more to it.
 // ---------------------------------------------------------------------------------------------
 constexpr int kTTok = 128;       // rows of x per item (MMA N)
 constexpr int kTBox = 32;        // sorted rows per x load
@@ -566,32 +594,32 @@ constexpr int kTThreads = 32 * (4 + 4 * kTGroups);
 constexpr int kTItems = 4;
 constexpr int kTMaxRing = 4;
 
-template <bool kInt4, bool kOrder, int RT>
+template <bool kInt4, int RT>
 struct ExpertTcLayout {
+  static constexpr int TN = kTTok;
   static constexpr int SPP = kInt4 ? 2 : 4;    // stages per packed tile
   static constexpr int SG = kTGroups / RT;     // decode groups, and slots, of a row tile
-  static constexpr int MW = kOrder ? 1 : RT;   // MMA warps
-  static constexpr int XW = kOrder ? 2 : 1;    // x warps
   static constexpr int RX = RT == 2 ? 3 : 4;   // stages of x
-  static constexpr int RP = 3;                 // packed tiles
-  // A decode warp tests the barrier of stage q's x knowing that the MMAs of stage q - SG are done: the
-  // slot's previous stage q - RX must be no later than that one.
-  static_assert(RX >= SG && RX <= kTMaxRing && SG <= kTMaxRing, "rings");
-  static constexpr int kSubX = kTTok * 128;    // 64 k of x
+  static constexpr int RP = RT == 2 ? 2 : 3;   // packed tiles
+  // A decode warp tests the barrier of stage q's x knowing that the MMAs of stage q - SG are done, and
+  // so that x of stage q - RX, the barrier's previous one, has landed.
+  static_assert(RX >= SG && RX <= kTMaxRing, "rings");
+  static constexpr int kSubX = TN * 128;       // 64 k of x
   static constexpr int kTileX = 2 * kSubX;
   static constexpr int kTileP = RT * kERows * 128;
   static constexpr int kOffP = RX * kTileX;
-  static constexpr int kOffBar = kOffP + RP * kTileP;
-  // full[MW][SG], empty[MW][SG], fullX[RX], emptyX[RX], fullP[RP], emptyP[RP], accFull[MW], accEmpty[MW],
-  // itemFull[I], itemEmpty[I]
-  static constexpr int kNumBars = 4 * kTMaxRing + 2 * kTMaxRing + 2 * RP + 4 + 2 * kTItems;
+  static constexpr int kOffY = kOffP + RP * kTileP;  // per decode warp: 32 rows of y, 32 columns
+  static constexpr int kOffBar = kOffY + 4 * kTGroups * 32 * 64;
+  // full[SG], empty[SG], fullX[RX], emptyX[RX][2] (by halves of 64 k), fullP[RP], emptyP[RP], accFull[RT],
+  // accEmpty[RT], itemFull[I], itemEmpty[I]
+  static constexpr int kNumBars = 5 * kTMaxRing + 2 * RP + 4 + 2 * kTItems;
   static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kOffMisc = kOffItem + kTItems * 16;  // TMEM address, decode constants
   static constexpr int kOffScan = kOffMisc + 32;
   static constexpr int kOffFirst = kOffScan + 32 * 4;
   static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }
-  static constexpr uint32_t kColA = RT * kTTok;  // slots of 64 columns: 128 k
-  static_assert(RT * kTTok + 64 * RT * SG <= 512, "tensor memory");
+  static constexpr uint32_t kColA = RT * TN;   // slots of 64 columns: 128 k
+  static_assert(RT * TN + 64 * RT * SG <= 512, "tensor memory");
   static_assert(kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 && kOffFirst > 114 * 1024, "one CTA per SM");
 };
 
@@ -617,14 +645,14 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t b
 }
 // 32 INT4 codes -> 16 registers of fp16 pairs (u - z) s, in natural order (as decode_w4_8).
 __device__ __forceinline__ void decode_piece_w4(const uint4& c, uint32_t s2, uint32_t zsub, const DecodeConsts& k,
-                                                uint32_t (&v)[16]) {
+                                                uint32_t* v) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     v[i] = hmul2_u32(hsub2_u32(and_or(byte_to_halves(w[i >> 2], i & 3), k.mask0, k.base0), zsub), s2);
 }
 // 32 ternary codes -> 16 registers of fp16 pairs c - 1, in natural order (as decode_tq_8).
-__device__ __forceinline__ void decode_piece_tq(const uint2& c, const DecodeConsts& k, uint32_t (&v)[16]) {
+__device__ __forceinline__ void decode_piece_tq(const uint2& c, const DecodeConsts& k, uint32_t* v) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t t = byte_to_halves(i < 4 ? c.x : c.y, i & 3);
@@ -633,19 +661,19 @@ __device__ __forceinline__ void decode_piece_tq(const uint2& c, const DecodeCons
   }
 }
 
-template <bool kInt4, bool kOrder, int RT>
+template <bool kInt4, int RT>
 __global__ void __launch_bounds__(kTThreads, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
-                      const ExpertArgs a) {
-  using L = ExpertTcLayout<kInt4, kOrder, RT>;
-  constexpr int SG = L::SG, MW = L::MW, RX = L::RX, RP = L::RP;
+                      const __grid_constant__ CUtensorMap tmap_y, const ExpertArgs a) {
+  using L = ExpertTcLayout<kInt4, RT>;
+  constexpr int SG = L::SG, RX = L::RX, RP = L::RP, TN = L::TN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
-  uint64_t* empty = full + 2 * kTMaxRing;
-  uint64_t* full_x = empty + 2 * kTMaxRing;
+  uint64_t* empty = full + kTMaxRing;
+  uint64_t* full_x = empty + kTMaxRing;
   uint64_t* empty_x = full_x + kTMaxRing;
-  uint64_t* fullP = empty_x + kTMaxRing;
+  uint64_t* fullP = empty_x + 2 * kTMaxRing;
   uint64_t* emptyP = fullP + RP;
   uint64_t* acc_full = emptyP + RP;
   uint64_t* acc_empty = acc_full + 2;
@@ -659,25 +687,23 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
   pdl_allow_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < MW * SG; ++i) {
-      mbar_init(&full[i], 4 * RT / MW);
-      mbar_init(&empty[i], 1);
+    for (int i = 0; i < SG; ++i) {
+      mbar_init(&full[i], 4 * RT);
+      mbar_init(&empty[i], RT);
     }
-    for (int i = 0; i < RX; ++i) {
-      mbar_init(&full_x[i], L::XW);
-      mbar_init(&empty_x[i], MW);
-    }
+    for (int i = 0; i < RX; ++i) mbar_init(&full_x[i], 2);
+    for (int i = 0; i < 2 * RX; ++i) mbar_init(&empty_x[i], RT);
     for (int i = 0; i < RP; ++i) {
       mbar_init(&fullP[i], 1);
       mbar_init(&emptyP[i], 4 * kTGroups);
     }
-    for (int i = 0; i < MW; ++i) {
+    for (int i = 0; i < RT; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4 * kTGroups / MW);
+      mbar_init(&acc_empty[i], 4 * SG);
     }
     for (int i = 0; i < kTItems; ++i) {
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], L::XW + MW + 4 * kTGroups);
+      mbar_init(&item_empty[i], 1 + RT + 4 * kTGroups);
     }
     store_decode_consts(kInt4, misc + 4);
     fence_mbar_init();
@@ -690,7 +716,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   }
   tc_fence_before_sync();
   pdl_wait_prior_grids();
-  expert_chunks(a, kTTok, first, reinterpret_cast<int*>(sm + L::kOffScan), kTThreads);  // synchronises
+  expert_chunks(a, TN, first, reinterpret_cast<int*>(sm + L::kOffScan), kTThreads);  // synchronises
   tc_fence_after_sync();
   constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's: they start at 0
   const int64_t tiles = (a.N + RT * kERows - 1) / (RT * kERows);
@@ -721,7 +747,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   if (warp == 2) {
     // ------------------------------------------------------------------ items, packed weights
     auto publish = [&](int n) {
-      const ExpertItem it = expert_item<true>(a, first, blockIdx.x + static_cast<int64_t>(n) * gridDim.x, tiles, kTTok);
+      const ExpertItem it = expert_item<true>(a, first, blockIdx.x + static_cast<int64_t>(n) * gridDim.x, tiles, TN);
       const int d = n % kTItems;
       if (n >= kTItems) ok = wait_ahead(&item_empty[d], n / kTItems - 1);
       if (ok && lane == 0) {
@@ -751,125 +777,82 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
       row = row_next;
     }
-  } else if (warp == 1 || (MW == 2 && warp == 3)) {
+  } else if (warp == 1 || (RT == 2 && warp == 3)) {
     // ------------------------------------------------------------------ MMA
-    const int m = warp >> 1;  // MMA warp: row tile m of two, or all of them
+    const int h = warp >> 1;  // row tile
     const uint32_t leader = elect_one() ? 1u : 0u;
     const uint64_t xdesc = sdesc_kmajor_sw128(smem_u32(sm));
     int s = 0, phase = 0, sx = 0;
     for (int n = 0; n < count && ok; ++n) {
       int4 it;
       ok = take_item(n, &it);
-      if (ok && n >= 1) ok = wait_all(&acc_empty[m], n - 1);
+      if (ok && n >= 1) ok = wait_all(&acc_empty[h], n - 1);
       const uint32_t idesc = idesc_f16_f32(kERows, static_cast<uint32_t>((uniform(it.w) + 15) / 16 * 16));
       for (int kb = 0; kb < nk && ok; ++kb) {
-        ok = wait_all(&full[m * SG + s], phase);
+        ok = wait_all(&full[s], phase);
         if (!ok) break;
         tc_fence_after_sync();
         const uint64_t bdesc = xdesc + static_cast<uint64_t>(sx * (L::kTileX >> 4));
-        const uint32_t asrc = L::kColA + 64 * (m * SG + s);
-        const int steps = a.K - static_cast<int64_t>(kb) * kTK >= kTK ? 8 : 4;
+        const uint32_t asrc = L::kColA + 64 * (h * SG + s);
+        const bool two = a.K - static_cast<int64_t>(kb) * kTK >= kTK;
 #pragma unroll
-        for (int k16 = 0; k16 < 8; ++k16) {
-          if (k16 >= steps) break;
+        for (int q = 0; q < 2; ++q) {
+          if (q == 0 || two) {
 #pragma unroll
-          for (int h = 0; h < RT / MW; ++h)
-            umma_f16_ts_if(leader, (m + h) * kTTok, asrc + 64 * h * SG + 8 * k16,
-                           bdesc + (k16 >> 2) * (L::kSubX >> 4) + 2 * (k16 & 3), idesc, (kb | k16) != 0 ? 1u : 0u);
+            for (int k16 = 0; k16 < 4; ++k16)
+              umma_f16_ts_if(leader, h * TN, asrc + 32 * q + 8 * k16, bdesc + q * (L::kSubX >> 4) + 2 * k16, idesc,
+                             (kb | q | k16) != 0 ? 1u : 0u);
+          }
+          umma_commit_if(leader, &empty_x[2 * sx + q]);
         }
-        umma_commit_if(leader, &empty[m * SG + s]);
-        umma_commit_if(leader, &empty_x[sx]);
+        umma_commit_if(leader, &empty[s]);
         if (++s == SG) {
           s = 0;
           phase ^= 1;
         }
         if (++sx == RX) sx = 0;
       }
-      if (ok) umma_commit_if(leader, &acc_full[m]);
+      if (ok) umma_commit_if(leader, &acc_full[h]);
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------------ x
     const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
     int s = 0, phase = -1;              // x slot; its previous stage's phase
-    if (!kOrder) {
-      for (int n = 0; n < count && ok && warp == 0; ++n) {
-        int4 it;
-        ok = take_item(n, &it);
-        const int boxes = (it.w + kTBox - 1) / kTBox;
-        // lanes 0 .. 2 boxes - 1: box lane / 2 of 64-k tile lane % 2
-        const int sub = lane & 1, box = lane >> 1;
-        for (int kb = 0; kb < nk && ok && !skipx; ++kb) {
-          if (phase >= 0) ok = wait_ahead(&empty_x[s], phase);
+    for (int n = 0; n < count && ok && warp == 0; ++n) {
+      int4 it;
+      ok = take_item(n, &it);
+      const int boxes = (it.w + kTBox - 1) / kTBox;
+      for (int kb = 0; kb < nk && ok && !skipx; ++kb) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (phase >= 0) ok = ok && wait_ahead(&empty_x[2 * s + q], phase);
           if (!ok) break;
-          const bool two = a.K - static_cast<int64_t>(kb) * kTK >= kTK;
-          if (lane == 0) mbar_arrive_expect_tx(&full_x[s], boxes * kTBox * 128 * (two ? 2 : 1));
-          __syncwarp();
-          if (box < boxes && (two || sub == 0))
-            tma_load_2d(sm + s * L::kTileX + sub * L::kSubX + box * kTBox * 128, &tmap_x, &full_x[s], kb * kTK + sub * 64,
-                        it.z + box * kTBox);
-          if (++s == RX) {
-            s = 0;
-            ++phase;
+          if (q == 0 || a.K - static_cast<int64_t>(kb) * kTK >= kTK) {
+            if (lane == 0) mbar_arrive_expect_tx(&full_x[s], boxes * kTBox * 128);
+            __syncwarp();
+            if (lane < boxes)
+              tma_load_2d(sm + s * L::kTileX + q * L::kSubX + lane * kTBox * 128, &tmap_x, &full_x[s], kb * kTK + q * 64,
+                          it.z + lane * kTBox);
+          } else if (lane == 0) {
+            mbar_arrive(&full_x[s]);
           }
+        }
+        if (++s == RX) {
+          s = 0;
+          ++phase;
         }
       }
-    } else {
-      // lane: 16-byte chunk lane % 16 of the rows 4 i + 2 w + lane / 16; a stage is handed over when the
-      // next one has been issued
-      const int w = warp == 0 ? 0 : 1, sub = 2 * w + (lane >> 4), ch = lane & 15;
-      int s_done = 0;
-      bool pending = false;
-      auto hand_over = [&] {
-        fence_proxy_async_smem();  // these copies are generic-proxy writes; the MMA reads by the async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full_x[s_done]);
-        if (++s_done == RX) s_done = 0;
-      };
-      for (int n = 0; n < count && ok; ++n) {
-        int4 it;
-        ok = take_item(n, &it);
-        const int pieces = ((it.w + 15) / 16 * 16) / 4;
-        int rows[kTTok / 4];
-#pragma unroll
-        for (int i = 0; i < kTTok / 4; ++i) {
-          const int r = 4 * i + sub;
-          rows[i] = ok && r < it.w ? static_cast<int>(expert_x_row(a, it.z + r)) : -1;
-        }
-        for (int kb = 0; kb < nk && ok && !skipx; ++kb) {
-          if (phase >= 0) ok = wait_ahead(&empty_x[s], phase);
-          if (!ok) break;
-          const bool in = kb * static_cast<int64_t>(kTK) + ch * 8 < a.K;
-          uint8_t* dst = sm + s * L::kTileX + (ch >> 3) * L::kSubX + sub * 128;
-          const __half* src = a.x + (in ? static_cast<int64_t>(kb) * kTK + ch * 8 : 0);
-#pragma unroll
-          for (int i = 0; i < kTTok / 4; ++i)
-            if (i < pieces)
-              cp_async_16(dst + i * 512 + (((ch & 7) ^ ((4 * i + sub) & 7)) << 4), src + (rows[i] < 0 ? 0 : rows[i] * a.K),
-                          rows[i] < 0 || !in ? 0u : 16u);
-          cp_async_commit();
-          if (pending) {
-            cp_async_wait<1>();
-            hand_over();
-          }
-          pending = true;
-          if (++s == RX) {
-            s = 0;
-            ++phase;
-          }
-        }
-      }
-      cp_async_wait<0>();
-      if (pending) hand_over();
     }
   } else {
     // ------------------------------------------------------------------ decode, epilogue
     const int grp = (warp >> 2) - 1, h = grp / SG, sg = grp % SG;
-    const int m = MW == 1 ? 0 : h;  // the MMA warp that uses this row tile
     const int r = threadIdx.x & (kERows - 1);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t slot = lane_base + L::kColA + 64 * grp;
-    uint64_t* const full_s = &full[m * SG + sg];
-    uint64_t* const empty_s = &empty[m * SG + sg];
+    uint64_t* const full_s = &full[sg];
+    uint64_t* const empty_s = &empty[sg];
+    const bool watch_x = h == 0 && (warp & 3) == 0;  // one of the warps that arrive for a stage
+    int sx = sg, phase_x = 0;                        // the barrier of x of the group's next stage
     const int64_t G = a.K >> 7;
     const uint8_t* prow0 = sm + L::kOffP + (h * kERows + r) * 128;
     int4 nx = make_int4(0, 0, 0, 0);
@@ -889,34 +872,69 @@ __global__ void __launch_bounds__(kTThreads, 1)
       fetch(kb);
     };
     const DecodeConsts consts = load_decode_consts(misc + 4);
-    const bool watch_x = (warp & 3) == 0 && (MW == 2 || h == 0);  // looks after x for the MMA warp's barrier
-    int sx = sg, phase_x = 0;         // the slot of the group's next stage of x
+    __half* const stage = reinterpret_cast<__half*>(sm + L::kOffY) + (warp - 4) * 32 * 32;
+    const bool vec = (a.N & 7) == 0;  // y itself is 16-byte aligned
     int own = 0;                      // stages that the group has decoded
     int kn = sg;                      // its next stage within the item
     int ps = 0, phase_p = 0;          // packed slot
     bool ready = false;               // the next stage's scale has been fetched
 
+    // 32 weight rows (n0 and on) x up to 32 rows of y (row and on; cnt of them) from packed pairs of rows.
+    auto store_chunk = [&](const uint32_t (&out)[16], int n0, int row, int cnt) {
+      if (cnt <= 0) return;
+      if (vec) {
+        if (lane == 0) tma_store_wait_read();  // the buffer's previous stores
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const __half2 p = *reinterpret_cast<const __half2*>(&out[j]);
+          stage[(2 * j) * 32 + lane] = __low2half(p);
+          stage[(2 * j + 1) * 32 + lane] = __high2half(p);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (cnt >= 16) tma_store_2d(&tmap_y, stage, n0, row);
+          if (cnt >= 32) tma_store_2d(&tmap_y, stage + 16 * 32, n0, row + 16);
+          tma_store_commit();
+        }
+        __syncwarp();
+      }
+      // what no store of 16 whole rows covers
+      const int from = vec ? (cnt < 32 ? cnt / 16 * 16 : 32) : 0;
+      uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + static_cast<int64_t>(row) * a.N + n0 + lane;
+      if (from < cnt && n0 + lane < a.N) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j >= from && j < cnt) y[j * a.N] = static_cast<uint16_t>((j & 1) ? out[j >> 1] >> 16 : out[j >> 1]);
+      }
+      __syncwarp();
+    };
     // The sums of item n: of its 32-row chunks group sg of row tile h takes every SG-th.  Read and
-    // rounded into registers first, so that the accumulator is free for the next item's MMAs, then
-    // stored: a warp's 32 weight rows of one row of y are 64 contiguous bytes.
+    // rounded into registers, so that the accumulator is free for the next item's MMAs; the second
+    // chunk is held there until the group's next stage is done and the first one's stores have been read.
+    constexpr int kChunks = TN / 32 / SG;
+    static_assert(kChunks <= 2, "one chunk is held");
+    uint32_t held[16];
+    int held_n0 = 0, held_row = 0, held_cnt = 0;
     auto epilogue = [&](int n, const int4& it) {
-      const int64_t nr = static_cast<int64_t>(it.y) * (RT * kERows) + h * kERows + r;
+      const int n0 = it.y * (RT * kERows) + h * kERows + (warp & 3) * 32;  // the warp's weight rows
+      const int nr = n0 + lane;
       const int64_t en = static_cast<int64_t>(it.x) * a.N + nr;
       float es = 1.0f, eb = 0.0f;
       if (nr < a.N) {
         if (!kInt4) es = __half2float(a.sc[en]);
         if (a.bias) eb = __half2float(a.bias[en]);
       }
-      if (!wait_all(&acc_full[m], n)) return false;
+      if (!wait_all(&acc_full[h], n)) return false;
       tc_fence_after_sync();
-      constexpr int kChunks = kTTok / 32 / SG;
       uint32_t out[kChunks][16];
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const int tok = (c * SG + sg) * 32;
         if (tok < it.w) {
           uint32_t v[32];
-          tmem_ld_32x32b_x32(lane_base + h * kTTok + tok, v);
+          tmem_ld_32x32b_x32(lane_base + h * TN + tok, v);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -928,27 +946,22 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[m]);
-      if (nr < a.N) {
+      if (lane == 0) mbar_arrive(&acc_empty[h]);
+      store_chunk(out[0], n0, it.z + sg * 32, it.w - sg * 32);
+      if (kChunks == 2) {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const int tok = (c * SG + sg) * 32, cnt = it.w - tok;
-          uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + (static_cast<int64_t>(it.z) + tok) * a.N + nr;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (2 * j < cnt) y[0] = static_cast<uint16_t>(out[c][j]);
-            if (2 * j + 1 < cnt) y[a.N] = static_cast<uint16_t>(out[c][j] >> 16);
-            y += 2 * a.N;
-          }
-        }
+        for (int j = 0; j < 16; ++j) held[j] = out[kChunks - 1][j];
+        held_n0 = n0;
+        held_row = it.z + (SG + sg) * 32;
+        held_cnt = it.w - (SG + sg) * 32;
       }
-      __syncwarp();
       return true;
     };
 
-    // U steps per packed tile, at most one stage of the group in each; after an item's first step the
-    // previous item's sums are read (the group's second stage needs its slot back, and so the MMAs that
-    // wait for them).  A last round without stages reads the last item's.
+    // U steps per packed tile, at most one stage of the group in each.  The previous item's sums are
+    // read after the group's first stage of the item (its second needs the slot back, and so the MMAs
+    // that wait for them), or, by the group whose slot the previous item's last MMAs use, before it.
+    // A last round without stages reads the last item's.
     constexpr int U = L::SPP > SG ? L::SPP / SG : 1;
     if (count > 0) ok = take_item(0, &nx);
     int4 it = nx;
@@ -959,9 +972,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (kInt4 && !ready && n < count && kn < nk) start_item(it, kn);
       ready = false;
       if (more) ok = take_item(n + 1, &nx);
-      const int steps = n < count ? npt * U : 1;
-      for (int i = 0, u = 0, pt = 0; i < steps && ok; ++i) {
-        if (n < count) {
+      const int steps = n < count ? npt * U : 0;
+      bool owed = n > 0;
+      for (int i = owed && (n == count || kn >= SG - 1) ? -1 : 0, u = 0, pt = 0; i < steps && ok; ++i) {
+        if (i >= 0) {
           if (u == 0) ok = wait_all(&fullP[ps], phase_p);
           const uint8_t* prow = prow0 + ps * L::kTileP;
           const int end = pt * L::SPP + L::SPP < nk ? pt * L::SPP + L::SPP : nk;
@@ -982,29 +996,30 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 ready = true;
               }
             }
-            // four pieces of 32 k; in a last stage of 64 k the last two are decoded too, and not multiplied
+            // two halves of 64 k, each decoded before the wait for its half of the slot; in a last stage of
+            // 64 k the second is decoded too, and not multiplied
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t v[16];
-              if (kInt4)
-                decode_piece_w4(pc[q], s2, zsub, consts, v);
-              else
-                decode_piece_tq((q & 1) ? make_uint2(pc[q >> 1].z, pc[q >> 1].w) : make_uint2(pc[q >> 1].x, pc[q >> 1].y),
-                                consts, v);
-              if (q == 0) {
-                if (own > 0) ok = wait_all(empty_s, own - 1);
-                if (watch_x) {
-                  ok = ok && wait_all(&full_x[sx], phase_x);
-                  sx += SG;
-                  if (sx >= RX) {
-                    sx -= RX;
-                    phase_x ^= 1;
-                  }
-                }
-                if (!ok) break;
-                tc_fence_after_sync();
+            for (int q = 0; q < 2; ++q) {
+              uint32_t v[32];
+              if (kInt4) {
+                decode_piece_w4(pc[2 * q], s2, zsub, consts, v);
+                decode_piece_w4(pc[2 * q + 1], s2, zsub, consts, v + 16);
+              } else {
+                decode_piece_tq(make_uint2(pc[q].x, pc[q].y), consts, v);
+                decode_piece_tq(make_uint2(pc[q].z, pc[q].w), consts, v + 16);
               }
-              tmem_st_32x32b_x16(slot + 16 * q, v);
+              if (own > 0 && q == 0) ok = ok && wait_all(empty_s, own - 1);
+              if (watch_x && q == 0) {
+                ok = ok && wait_all(&full_x[sx], phase_x);
+                sx += SG;
+                if (sx >= RX) {
+                  sx -= RX;
+                  phase_x ^= 1;
+                }
+              }
+              if (!ok) break;
+              tc_fence_after_sync();
+              tmem_st_32x32b_x32(slot + 32 * q, v);
             }
             if (!ok) break;
             tmem_st_wait();
@@ -1013,6 +1028,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
             if (lane == 0) mbar_arrive(full_s);
             ++own;
             kn += SG;
+            if (kChunks == 2 && held_cnt > 0 && !owed) {
+              store_chunk(held, held_n0, held_row, held_cnt);
+              held_cnt = 0;
+            }
           }
           if (++u == U) {  // done with the packed tile
             u = 0;
@@ -1025,10 +1044,19 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
           }
         }
-        if (i == 0 && n > 0 && ok) ok = epilogue(n - 1, prev);
+        if (owed && ok) {
+          owed = false;
+          if (kChunks == 2) {  // a group without a stage in the item before
+            store_chunk(held, held_n0, held_row, held_cnt);
+            held_cnt = 0;
+          }
+          ok = epilogue(n - 1, prev);
+        }
       }
       kn -= nk;
     }
+    if (kChunks == 2) store_chunk(held, held_n0, held_row, ok ? held_cnt : 0);
+    if (lane == 0) tma_store_wait();
   }
 
   __syncwarp();
@@ -1049,25 +1077,41 @@ static cudaError_t launch_experts_tc(const ExpertArgs& a, cudaStream_t s) {
       !make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.x, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.X),
                     static_cast<uint64_t>(a.K) * 2, 64, kTBox, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const int64_t by_rows = a.E + a.R / kTTok, chunks = a.R < by_rows ? a.R : by_rows;
-  auto run = [&](auto rt, auto ord) {
+  CUtensorMap ty = tx;  // not used when rows of y are not 16-byte aligned
+  if (a.N % 8 == 0 && !make_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.y, static_cast<uint64_t>(a.N),
+                                    static_cast<uint64_t>(a.R), static_cast<uint64_t>(a.N) * 2, 32, 16,
+                                    CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  const int64_t by_rows = a.E + a.R / kTTok, chunks = a.R < by_rows ? a.R : by_rows;  // at most
+  auto run = [&](auto rt) {
     constexpr int RT = decltype(rt)::value;
-    auto* kern = experts_tc_kernel<kInt4, decltype(ord)::value, RT>;
-    const int smem = ExpertTcLayout<kInt4, decltype(ord)::value, RT>::bytes(a.E);
+    auto* kern = experts_tc_kernel<kInt4, RT>;
+    const int smem = ExpertTcLayout<kInt4, RT>::bytes(a.E);
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     const int64_t items = chunks * ((a.N + RT * kERows - 1) / (RT * kERows));
-    return launch_pdl(kern, dim3(row_grid(items, 1, 1)), dim3(kTThreads), static_cast<size_t>(smem), 1, s, tx, tw, a);
+    return launch_pdl(kern, dim3(row_grid(items, 1, 1)), dim3(kTThreads), static_cast<size_t>(smem), 1, s, tx, tw, ty, a);
   };
-  const bool two = chunks * ((a.N + 2 * kERows - 1) / (2 * kERows)) >= current_device_info().num_sms;
-  if (a.order) return two ? run(std::integral_constant<int, 2>(), std::true_type()) : run(std::integral_constant<int, 1>(), std::true_type());
-  return two ? run(std::integral_constant<int, 2>(), std::false_type()) : run(std::integral_constant<int, 1>(), std::false_type());
+  if (chunks * ((a.N + 2 * kERows - 1) / (2 * kERows)) >= current_device_info().num_sms)
+    return run(std::integral_constant<int, 2>());
+  return run(std::integral_constant<int, 1>());
 }
 
 template <bool kInt4>
 static cudaError_t launch_experts(int path, const ExpertArgs& a, cudaStream_t s) {
   if (path == 3 || a.X == 0) return launch_experts_generic<kInt4>(a, s);
-  if (path == 2) return launch_experts_tc<kInt4>(a, s);
+  if (path == 2) {
+    if (!a.order) return launch_experts_tc<kInt4>(a, s);
+    // rows read through the order are copied into sorted order first: one pass over them at memory
+    // speed, where copies from inside the product's kernel slowed its MMAs by half
+    const cudaError_t e = launch_experts_rows(a, s);
+    if (e != cudaSuccess) return e;
+    ExpertArgs b = a;
+    b.x = a.rows;
+    b.X = a.R;
+    b.order = nullptr;
+    return launch_experts_tc<kInt4>(b, s);
+  }
   // rows per expert of an even spread; no expert has more than R rows
   const int64_t avg = a.R / a.E;
   if (a.R <= 8 || avg <= 4) return launch_experts_skinny<kInt4, 1>(a, s);

@@ -28,8 +28,8 @@ int check_route(int64_t T, int64_t E, int top_k, int dtype) {
 }
 
 int gemm_experts_impl(bool int4, const uint16_t* x, const void* w, const uint16_t* sc, const uint8_t* zeros,
-                      const uint16_t* bias, uint16_t* y, const int32_t* offsets, const int32_t* order, int64_t X,
-                      int64_t R, int64_t E, int64_t N, int64_t K, int top_k, int path, void* stream) {
+                      const uint16_t* bias, uint16_t* y, const int32_t* offsets, const int32_t* order, uint16_t* rows,
+                      int64_t X, int64_t R, int64_t E, int64_t N, int64_t K, int top_k, int path, void* stream) {
   if (X < 0 || R < 0 || X > kMoeMaxSlots || R > kMoeMaxSlots) return TQ_ERR_SHAPE;
   if (E < 1 || E > TQ_MOE_MAX_EXPERTS || N < 0 || N > kMoeMaxSlots / E) return TQ_ERR_SHAPE;
   if (K <= 0 || K > (int64_t(1) << 28) || top_k < 1) return TQ_ERR_SHAPE;
@@ -41,9 +41,11 @@ int gemm_experts_impl(bool int4, const uint16_t* x, const void* w, const uint16_
   const int fmt = int4 ? TQ_FMT_W4G128 : TQ_FMT_TERNARY;
   if (path == TQ_PATH_AUTO) {
     path = tq_experts_path(fmt, R, E, N, K, al ? 1 : 0);
+    if (path == TQ_PATH_PREFILL && order && (!rows || !aligned16(rows))) path = TQ_PATH_DECODE;
   } else if (path != TQ_PATH_GENERIC) {
     if (K % 64 != 0) return TQ_ERR_PATH;
-    if (!al) return TQ_ERR_ALIGN;
+    if (path == TQ_PATH_PREFILL && order && !rows) return TQ_ERR_NULL;
+    if (!al || (path == TQ_PATH_PREFILL && order && !aligned16(rows))) return TQ_ERR_ALIGN;
   }
   tq::ExpertArgs a = {};
   a.x = reinterpret_cast<const __half*>(x);
@@ -54,6 +56,7 @@ int gemm_experts_impl(bool int4, const uint16_t* x, const void* w, const uint16_
   a.y = reinterpret_cast<__half*>(y);
   a.offsets = offsets;
   a.order = order;
+  a.rows = reinterpret_cast<__half*>(rows);
   a.X = X;
   a.R = R;
   a.N = N;
@@ -123,15 +126,17 @@ int tq_moe_combine_backward(const void* dout, const void* y, int dtype, const in
 }
 
 int tq_gemm_experts(const uint16_t* x, const uint8_t* packed, const uint16_t* scale, const uint16_t* bias, uint16_t* y,
-                    const int32_t* offsets, const int32_t* order, int64_t X, int64_t R, int64_t E, int64_t N, int64_t K,
-                    int top_k, int path, void* stream) {
-  return gemm_experts_impl(false, x, packed, scale, nullptr, bias, y, offsets, order, X, R, E, N, K, top_k, path, stream);
+                    const int32_t* offsets, const int32_t* order, uint16_t* rows, int64_t X, int64_t R, int64_t E,
+                    int64_t N, int64_t K, int top_k, int path, void* stream) {
+  return gemm_experts_impl(false, x, packed, scale, nullptr, bias, y, offsets, order, rows, X, R, E, N, K, top_k, path,
+                           stream);
 }
 
 int w4g_gemm_experts(const uint16_t* x, const int32_t* qweight, const uint16_t* scales, const uint8_t* zeros,
-                     const uint16_t* bias, uint16_t* y, const int32_t* offsets, const int32_t* order, int64_t X,
-                     int64_t R, int64_t E, int64_t N, int64_t K, int top_k, int path, void* stream) {
-  return gemm_experts_impl(true, x, qweight, scales, zeros, bias, y, offsets, order, X, R, E, N, K, top_k, path, stream);
+                     const uint16_t* bias, uint16_t* y, const int32_t* offsets, const int32_t* order, uint16_t* rows,
+                     int64_t X, int64_t R, int64_t E, int64_t N, int64_t K, int top_k, int path, void* stream) {
+  return gemm_experts_impl(true, x, qweight, scales, zeros, bias, y, offsets, order, rows, X, R, E, N, K, top_k, path,
+                           stream);
 }
 
 int tq_experts_path(int fmt, int64_t R, int64_t E, int64_t N, int64_t K, int aligned) {

@@ -126,8 +126,8 @@ __device__ __forceinline__ bool mbar_wait_relaxed(uint64_t* bar, uint32_t parity
   const long long t0 = clock64();
   while (true) {
 #pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-      __nanosleep(128);
+    for (int i = 0; i < 32; ++i) {
+      __nanosleep(40);
       if (mbar_try_wait(a, parity)) return true;
     }
     if (clock64() - t0 > *reinterpret_cast<volatile long long*>(&g_tq_wait_limit)) {
@@ -206,6 +206,19 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
+
+// 2-D tile store shared -> global (async proxy; same 16-byte rule on c0, coordinates not negative).
+// The issuing thread commits it to a bulk group; tma_store_wait_read: the group's shared memory may
+// be written again; tma_store_wait: the group is complete.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(smem_src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // 1-D bulk copy global -> shared (no tensor map): both addresses 16-byte aligned, `bytes` a
 // multiple of 16 (below 2^20); its bytes complete transactions on `bar`.

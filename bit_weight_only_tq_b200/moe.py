@@ -18,7 +18,7 @@ import os
 
 import torch
 
-from . import PATH_AUTO, TQ_F16, TQ_F32, HEADER, _check, _i64, _int, _need, _ptr, _vp, header_functions, lib
+from . import FMT_TERNARY, FMT_W4G128, PATH_AUTO, PATH_PREFILL, TQ_F16, TQ_F32, HEADER, _check, _i64, _int, _need, _ptr, _vp, header_functions, lib
 
 __all__ = [
     "TQ_BF16", "tq_moe_route", "tq_moe_route_backward", "tq_moe_sort", "tq_moe_gather", "tq_moe_gather_backward",
@@ -35,8 +35,8 @@ _SIGS = {
     "tq_moe_gather": [_vp, _int, _vp, _vp, _vp, _i64, _i64, _int, _i64, _vp],
     "tq_moe_combine": [_vp, _int, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp],
     "tq_moe_combine_backward": [_vp, _vp, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp],
-    "tq_gemm_experts": [_vp] * 7 + [_i64] * 5 + [_int, _int, _vp],
-    "w4g_gemm_experts": [_vp] * 8 + [_i64] * 5 + [_int, _int, _vp],
+    "tq_gemm_experts": [_vp] * 8 + [_i64] * 5 + [_int, _int, _vp],
+    "w4g_gemm_experts": [_vp] * 9 + [_i64] * 5 + [_int, _int, _vp],
     "tq_experts_path": [_int, _i64, _i64, _i64, _i64, _int],
 }
 for _name, _args in _SIGS.items():
@@ -218,7 +218,7 @@ def tq_moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, pos: torch.Tens
     return dy, dweights
 
 
-def _experts(x, w, sc, zeros, offsets, order, top_k, bias, y, per_col, N, E, path, stream, fn, what):
+def _experts(x, w, sc, zeros, offsets, order, top_k, bias, y, per_col, N, E, path, stream, rows, fmt, fn, what):
     _need(x, torch.float16, "x", 2)
     _need(bias, torch.float16, "bias", 2)
     _need(offsets, torch.int32, "offsets", 1)
@@ -234,8 +234,15 @@ def _experts(x, w, sc, zeros, offsets, order, top_k, bias, y, per_col, N, E, pat
             y = torch.empty(R, N, dtype=torch.float16, device=x.device)
     _need(y, torch.float16, "y", 2)
     _shape(y, (R, N), "y")
-    _device(x, w, sc, zeros, offsets, order, bias, y)
-    tail = (_ptr(bias), y.data_ptr(), offsets.data_ptr(), _ptr(order), X, R, E, N, K, top_k, int(path), _raw(stream))
+    if order is not None and rows is None and (
+            path == PATH_PREFILL or path == PATH_AUTO and lib.tq_experts_path(fmt, R, E, N, K, 1) == PATH_PREFILL):
+        with _on(stream):
+            rows = torch.empty(R, K, dtype=torch.float16, device=x.device)
+    _need(rows, torch.float16, "rows", 2)
+    _shape(rows, (R, K), "rows")
+    _device(x, w, sc, zeros, offsets, order, bias, y, rows)
+    tail = (_ptr(bias), y.data_ptr(), offsets.data_ptr(), _ptr(order), _ptr(rows), X, R, E, N, K, top_k, int(path),
+            _raw(stream))
     if what == "w4g_gemm_experts":
         _check(fn(x.data_ptr(), w.data_ptr(), sc.data_ptr(), _ptr(zeros), *tail), what)
     else:
@@ -244,22 +251,23 @@ def _experts(x, w, sc, zeros, offsets, order, top_k, bias, y, per_col, N, E, pat
 
 
 def tq_gemm_experts(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, offsets: torch.Tensor, order=None,
-                    top_k: int = 1, bias=None, y=None, path: int = PATH_AUTO, stream=None) -> torch.Tensor:
+                    top_k: int = 1, bias=None, y=None, path: int = PATH_AUTO, stream=None, rows=None) -> torch.Tensor:
     """Each expert's rows times its ternary weights: y[r] = x[row(r)] . What_e^T (+ bias_e) for
     offsets[e] <= r < offsets[e + 1]; row(r) = order[r] // top_k with `order` (x holds the tokens), r
     without (x holds sorted rows).  packed uint8 [E, N, ceil(K/4)], scale fp16 [E, N], bias fp16 [E, N].
-    Rows from offsets[-1] on are left as they were (uninitialised when y is allocated here)."""
+    Rows from offsets[-1] on are left as they were (uninitialised when y is allocated here).
+    rows: fp16 [R, K] scratch for the path that copies the rows first (allocated here when it is needed)."""
     _need(packed, torch.uint8, "packed", 3)
     _need(scale, torch.float16, "scale", 2)
     E, N = packed.shape[:2]
     _shape(scale, (E, N), "scale")
-    return _experts(x, packed, scale, None, offsets, order, top_k, bias, y, 4, N, E, path, stream, lib.tq_gemm_experts,
-                    "tq_gemm_experts")
+    return _experts(x, packed, scale, None, offsets, order, top_k, bias, y, 4, N, E, path, stream, rows,
+                    FMT_TERNARY, lib.tq_gemm_experts, "tq_gemm_experts")
 
 
 def w4g_gemm_experts(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor, zeros=None,
                      order=None, top_k: int = 1, bias=None, y=None, path: int = PATH_AUTO,
-                     stream=None) -> torch.Tensor:
+                     stream=None, rows=None) -> torch.Tensor:
     """tq_gemm_experts with W4A16 weights: qweight int32 [E, N, K/8], scales fp16 [E, N, K/128], zeros
     uint8 [E, N, K/128] or None (symmetric)."""
     _need(qweight, torch.int32, "qweight", 3)
@@ -268,8 +276,8 @@ def w4g_gemm_experts(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tenso
     E, N = qweight.shape[:2]
     _shape(scales, (E, N, x.shape[1] // 128), "scales")
     _shape(zeros, scales.shape, "zeros")
-    return _experts(x, qweight, scales, zeros, offsets, order, top_k, bias, y, 8, N, E, path, stream,
-                    lib.w4g_gemm_experts, "w4g_gemm_experts")
+    return _experts(x, qweight, scales, zeros, offsets, order, top_k, bias, y, 8, N, E, path, stream, rows,
+                    FMT_W4G128, lib.w4g_gemm_experts, "w4g_gemm_experts")
 
 
 def tq_experts_path(fmt: int, R: int, E: int, N: int, K: int, aligned: bool = True) -> int:

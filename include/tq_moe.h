@@ -4,8 +4,8 @@
  *
  * The conventions of tq.h hold (device pointers owned by the caller, row-major contiguous
  * tensors, asynchronous on `stream` and the current device, argument errors returned before
- * anything is launched, no allocation, graph capturable), with two differences: the calls here
- * need no workspace, and their kernels read nothing -- weights included -- before the preceding
+ * anything is launched, no allocation, graph capturable), with one difference: the kernels
+ * here read nothing -- weights included -- before the preceding
  * work on the stream has finished.
  *
  * A layer of E experts, T tokens and top_k choices per token runs
@@ -120,6 +120,9 @@ TQ_API int tq_moe_combine_backward(const void* dout, const void* y, int dtype, c
  *            not overlap x.
  *   offsets  int32 [E + 1] (tq_moe_sort): non-decreasing, within [0, R].
  *   order    int32 [R] or NULL; a row(r) outside [0, X) reads as zeros.
+ *   rows     fp16 [R, K] scratch, 16-byte aligned, or NULL: the PREFILL path with `order` copies the
+ *            rows there in sorted order before the product.  Without it AUTO takes the DECODE path
+ *            (right, slower), and PREFILL returns TQ_ERR_NULL.  Not read or written otherwise.
  *   path     TQ_PATH_AUTO, or one path (tests): DECODE takes few rows per expert (mma.sync on
  *            in-register decode, up to 32 rows of an expert per pass over its weights), PREFILL
  *            many (tcgen05.mma), GENERIC any shape and alignment.  DECODE and PREFILL need
@@ -131,12 +134,13 @@ TQ_API int tq_moe_combine_backward(const void* dout, const void* y, int dtype, c
  * ------------------------------------------------------------------------------------------ */
 TQ_API int tq_gemm_experts(const uint16_t* x, const uint8_t* packed, const uint16_t* scale,
                            const uint16_t* bias, uint16_t* y, const int32_t* offsets,
-                           const int32_t* order, int64_t X, int64_t R, int64_t E, int64_t N,
-                           int64_t K, int top_k, int path, void* stream);
+                           const int32_t* order, uint16_t* rows, int64_t X, int64_t R, int64_t E,
+                           int64_t N, int64_t K, int top_k, int path, void* stream);
 TQ_API int w4g_gemm_experts(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
                             const uint8_t* zeros, const uint16_t* bias, uint16_t* y,
-                            const int32_t* offsets, const int32_t* order, int64_t X, int64_t R,
-                            int64_t E, int64_t N, int64_t K, int top_k, int path, void* stream);
+                            const int32_t* offsets, const int32_t* order, uint16_t* rows,
+                            int64_t X, int64_t R, int64_t E, int64_t N, int64_t K, int top_k,
+                            int path, void* stream);
 
 /* tq_experts_path -- the rule TQ_PATH_AUTO applies (host arithmetic only; fmt is a tq_format).
  * Returns a tq_path or a negative tq_status. */

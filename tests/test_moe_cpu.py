@@ -71,11 +71,11 @@ def test_row_argument_errors():
 def test_experts_argument_errors():
     t, w = tq.lib.tq_gemm_experts, tq.lib.w4g_gemm_experts
 
-    def tern(x=P, p=P, s=P, y=P, off=P, X=4, R=8, E=4, N=16, K=64, k=2, path=0):
-        return t(x, p, s, None, y, off, None, X, R, E, N, K, k, path, None)
+    def tern(x=P, p=P, s=P, y=P, off=P, X=4, R=8, E=4, N=16, K=64, k=2, path=0, order=None, rows=None):
+        return t(x, p, s, None, y, off, order, rows, X, R, E, N, K, k, path, None)
 
     def int4(K=128, **kw):
-        return w(P, P, P, None, None, P, P, None, kw.get("X", 4), kw.get("R", 8), 4, 16, K, 2, kw.get("path", 0), None)
+        return w(P, P, P, None, None, P, P, None, None, kw.get("X", 4), kw.get("R", 8), 4, 16, K, 2, kw.get("path", 0), None)
 
     for bad in (dict(X=-1), dict(R=-1), dict(R=2 ** 31), dict(E=0), dict(E=1025), dict(N=-1), dict(N=2 ** 30), dict(K=0),
                 dict(K=2 ** 28 + 1), dict(k=0)):
@@ -87,6 +87,11 @@ def test_experts_argument_errors():
     for path in (tq.PATH_DECODE, tq.PATH_PREFILL):
         assert tern(K=100, path=path) == -8                         # K % 64
         assert tern(x=Q, path=path) == -3 and tern(p=Q, path=path) == -3 and tern(y=Q, path=path) == -3
+
+
+    # PREFILL through `order` copies the rows first: it needs the scratch, aligned
+    assert tern(path=tq.PATH_PREFILL, order=P) == -1
+    assert tern(path=tq.PATH_PREFILL, order=P, rows=Q) == -3
 
 
 def test_experts_path_rule():
