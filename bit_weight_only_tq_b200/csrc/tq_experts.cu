@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
   int4* items = reinterpret_cast<int4*>(sm + L::kOffItem);  // [kEItems][2]: (e, tile, row0, rows), (row mask, ...)
   int* scan = reinterpret_cast<int*>(sm + L::kOffScan);
   int* first = reinterpret_cast<int*>(sm + L::kOffFirst);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // values that steer the roles are broadcast, so that the compiler knows them to be warp-uniform
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   pdl_allow_dependents();
   if (threadIdx.x == 0) {
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
   pdl_wait_prior_grids();
   expert_chunks(a, L::TM, first, scan, L::kThreads);
   const int64_t tiles = (a.N + kERows - 1) / kERows;
-  const int64_t total = static_cast<int64_t>(first[a.E]) * tiles;
+  const int64_t total = static_cast<int64_t>(uniform(first[a.E])) * tiles;
   const int nk = static_cast<int>((a.K + L::KS - 1) / L::KS);
   bool ok = true;
 
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
       const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x + (xr >= 0 ? xr * a.K : 0));
       const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
       const int d = n % kEItems;
-      if (n >= kEItems) ok = mbar_wait_warp(&item_empty[d], static_cast<uint32_t>(n / kEItems - 1) & 1u);
+      if (n >= kEItems) ok = mbar_wait_relaxed(&item_empty[d], static_cast<uint32_t>(n / kEItems - 1) & 1u);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       if (lane == 0) {
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
       const int wrow = static_cast<int>(static_cast<int64_t>(it.e) * a.N + static_cast<int64_t>(it.tile) * kERows);
       for (int kb = 0; kb < nk && ok; ++kb, ++q) {
         const int s = q % L::kRing;
-        if (q >= L::kRing) ok = mbar_wait_warp(&empty[s], static_cast<uint32_t>(q / L::kRing - 1) & 1u);
+        if (q >= L::kRing) ok = mbar_wait_relaxed(&empty[s], static_cast<uint32_t>(q / L::kRing - 1) & 1u);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         const int64_t k0 = static_cast<int64_t>(kb) * L::KS;
@@ -559,12 +560,13 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
 // ---------------------------------------------------------------------------------------------
 // Many rows per expert: a dense contraction, on tcgen05 with the decoded weights as A in tensor
 // memory (as in the prefill GEMM) and the sorted rows of x as B in shared memory.  Persistent CTAs,
-// one per SM; an item is RT tiles of 128 weight rows of one expert times up to 128 of its rows, all of
+// one per SM; an item is RT tiles of 128 weight rows of one expert times up to TN of its rows, all of
 // K.  The MMA's N is the item's own number of rows rounded up to 16 (an expert's rows are cut
 // evenly), so a ragged expert costs its rows and not a full tile.
 // RT = 2: a stage of x (128 k) feeds two accumulators, which halves the x that crosses L2 per MMA (512
 // rows per expert, 4096 -> 7168: 240 us INT4, 203 us ternary; RT = 1: 311 and 266 us).  RT = 1 serves
-// launches whose items would otherwise leave SMs idle.
+// launches whose items would otherwise leave SMs idle.  With few rows per expert the packed weights
+// bound it: TN = 64 leaves the shared memory of the wider x tiles to twice the packed tiles in flight.
 // 20 warps:
 //   warp 0      x by TMA (tiles of 64 k, 128-byte swizzle, boxes of 32 rows);
 //   warp 1      the MMAs (with RT = 2 those of one row tile, warp 3 the other's): the whole warp runs
@@ -586,7 +588,6 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
 // the next one on the same slot -- barrier wake-ups, tensor memory stores, the test -- takes about 0.8
 // us, and each barrier wait of a decode warp 0.1 to 0.2 us: stages of 64 k lost more to it.
 // ---------------------------------------------------------------------------------------------
-constexpr int kTTok = 128;       // rows of x per item (MMA N)
 constexpr int kTBox = 32;        // sorted rows per x load
 constexpr int kTK = 128;         // k per stage
 constexpr int kTGroups = 4;      // decode groups
@@ -594,13 +595,12 @@ constexpr int kTThreads = 32 * (4 + 4 * kTGroups);
 constexpr int kTItems = 4;
 constexpr int kTMaxRing = 4;
 
-template <bool kInt4, int RT>
+template <bool kInt4, int RT, int TN>
 struct ExpertTcLayout {
-  static constexpr int TN = kTTok;
   static constexpr int SPP = kInt4 ? 2 : 4;    // stages per packed tile
   static constexpr int SG = kTGroups / RT;     // decode groups, and slots, of a row tile
   static constexpr int RX = RT == 2 ? 3 : 4;   // stages of x
-  static constexpr int RP = RT == 2 ? 2 : 3;   // packed tiles
+  static constexpr int RP = RT == 2 ? (TN == 64 ? 4 : 2) : (TN == 64 ? 7 : 3);  // packed tiles
   // A decode warp tests the barrier of stage q's x knowing that the MMAs of stage q - SG are done, and
   // so that x of stage q - RX, the barrier's previous one, has landed.
   static_assert(RX >= SG && RX <= kTMaxRing, "rings");
@@ -661,12 +661,12 @@ __device__ __forceinline__ void decode_piece_tq(const uint2& c, const DecodeCons
   }
 }
 
-template <bool kInt4, int RT>
+template <bool kInt4, int RT, int TN>
 __global__ void __launch_bounds__(kTThreads, 1)
     experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                       const __grid_constant__ CUtensorMap tmap_y, const ExpertArgs a) {
-  using L = ExpertTcLayout<kInt4, RT>;
-  constexpr int SG = L::SG, RX = L::RX, RP = L::RP, TN = L::TN;
+  using L = ExpertTcLayout<kInt4, RT, TN>;
+  constexpr int SG = L::SG, RX = L::RX, RP = L::RP;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
@@ -913,7 +913,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     // The sums of item n: of its 32-row chunks group sg of row tile h takes every SG-th.  Read and
     // rounded into registers, so that the accumulator is free for the next item's MMAs; the second
     // chunk is held there until the group's next stage is done and the first one's stores have been read.
-    constexpr int kChunks = TN / 32 / SG;
+    constexpr int kChunks = TN / 32 > SG ? TN / 32 / SG : 1;
     static_assert(kChunks <= 2, "one chunk is held");
     uint32_t held[16];
     int held_n0 = 0, held_row = 0, held_cnt = 0;
@@ -1082,19 +1082,27 @@ static cudaError_t launch_experts_tc(const ExpertArgs& a, cudaStream_t s) {
                                     static_cast<uint64_t>(a.R), static_cast<uint64_t>(a.N) * 2, 32, 16,
                                     CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  const int64_t by_rows = a.E + a.R / kTTok, chunks = a.R < by_rows ? a.R : by_rows;  // at most
-  auto run = [&](auto rt) {
-    constexpr int RT = decltype(rt)::value;
-    auto* kern = experts_tc_kernel<kInt4, RT>;
-    const int smem = ExpertTcLayout<kInt4, RT>::bytes(a.E);
+  auto items = [&](int RT, int TN) {  // at most
+    const int64_t by_rows = a.E + a.R / TN, chunks = a.R < by_rows ? a.R : by_rows;
+    return chunks * ((a.N + RT * kERows - 1) / (RT * kERows));
+  };
+  auto run = [&](auto rt, auto tn) {
+    constexpr int RT = decltype(rt)::value, TN = decltype(tn)::value;
+    auto* kern = experts_tc_kernel<kInt4, RT, TN>;
+    const int smem = ExpertTcLayout<kInt4, RT, TN>::bytes(a.E);
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
-    const int64_t items = chunks * ((a.N + RT * kERows - 1) / (RT * kERows));
-    return launch_pdl(kern, dim3(row_grid(items, 1, 1)), dim3(kTThreads), static_cast<size_t>(smem), 1, s, tx, tw, ty, a);
+    return launch_pdl(kern, dim3(row_grid(items(RT, TN), 1, 1)), dim3(kTThreads), static_cast<size_t>(smem), 1, s, tx, tw,
+                      ty, a);
   };
-  if (chunks * ((a.N + 2 * kERows - 1) / (2 * kERows)) >= current_device_info().num_sms)
-    return run(std::integral_constant<int, 2>());
-  return run(std::integral_constant<int, 1>());
+  // 64 rows per item while uneven routing leaves most experts below that
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 2> two;
+  const std::integral_constant<int, 64> n64;
+  const std::integral_constant<int, 128> n128;
+  const int sms = current_device_info().num_sms;
+  if (a.R / a.E <= 48) return items(2, 64) >= sms ? run(two, n64) : run(one, n64);
+  return items(2, 128) >= sms ? run(two, n128) : run(one, n128);
 }
 
 template <bool kInt4>
