@@ -190,7 +190,7 @@ __device__ __forceinline__ ExpertItem expert_item(const ExpertArgs& a, const int
 
 // ---------------------------------------------------------------------------------------------
 // Few rows per expert: bound by the packed weights' bytes.  Persistent CTAs; an item is 128 weight
-// rows of one expert times up to TM = 8 NT of its rows, all of K.  One producer warp keeps a ring
+// rows of one expert times up to 8 of its rows, all of K.  One producer warp keeps a ring
 // of stages full: 128 weight rows x 128 packed bytes by TMA (128-byte swizzle) and the rows' x by
 // one bulk copy each, running ahead across items.  Consumer warps form KG groups of four that take
 // the CTA's stages in turn (the ring is a multiple of KG long, so that a slot has one consumer
@@ -212,16 +212,15 @@ __device__ __forceinline__ ExpertItem expert_item(const ExpertArgs& a, const int
 // of a quarter-warp access differ in the swizzle's top bit.
 // ---------------------------------------------------------------------------------------------
 constexpr int kERows = 128;       // weight rows per item
-constexpr int kEMaxRing = 8;
 constexpr int kEItems = 4;        // item descriptors in flight
 
-template <bool kInt4, int NT>
+template <bool kInt4>
 struct SkinnyLayout {
-  static constexpr int TM = 8 * NT;
-  static constexpr int KG = NT == 1 ? 2 : 4;
+  static constexpr int TM = 8;
+  static constexpr int KG = 2;                         // consumer groups
   static constexpr int kConsumers = 128 * KG;
   static constexpr int kThreads = kConsumers + 32;
-  static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
+  static constexpr int kCtasPerSm = 2;
   static constexpr int KS = kInt4 ? 256 : 512;         // k per stage
   static constexpr int kXRow = KS * 2 + 16;            // bytes between rows of x
   static constexpr int kTileW = kERows * 128;
@@ -231,24 +230,24 @@ struct SkinnyLayout {
   static constexpr int kOffX = kRing * kTileW;
   static constexpr int kOffPart = kOffX + kRing * kTileX;
   static constexpr int kOffBar = kOffPart + KG * kPart;
-  static constexpr int kOffItem = kOffBar + 2 * (kEMaxRing + kEItems) * 8;
+  static constexpr int kOffItem = kOffBar + 2 * (kRing + kEItems) * 8;
   static constexpr int kOffScan = kOffItem + kEItems * 32;  // descriptors of 32 bytes
   static constexpr int kOffFirst = kOffScan + 32 * 4;
   static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }  // 1024: alignment
-  static_assert(kRing % KG == 0 && kRing <= kEMaxRing && kOffFirst + 1025 * 4 + 1024 <= 227 * 1024, "shared memory");
+  static_assert(kRing % KG == 0 && kOffFirst + 1025 * 4 + 1024 <= 113 * 1024, "two CTAs per SM");
 };
 
 __device__ __forceinline__ uint32_t sel(bool c, uint32_t a, uint32_t b) { return c ? a : b; }
 
-template <bool kInt4, int NT>
-__global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayout<kInt4, NT>::kCtasPerSm)
+template <bool kInt4>
+__global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kInt4>::kCtasPerSm)
     experts_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w, const ExpertArgs a) {
-  using L = SkinnyLayout<kInt4, NT>;
+  using L = SkinnyLayout<kInt4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
-  uint64_t* empty = full + kEMaxRing;
-  uint64_t* item_full = empty + kEMaxRing;
+  uint64_t* empty = full + L::kRing;
+  uint64_t* item_full = empty + L::kRing;
   uint64_t* item_empty = item_full + kEItems;
   int4* items = reinterpret_cast<int4*>(sm + L::kOffItem);  // [kEItems][2]: (e, tile, row0, rows), (row mask, ...)
   int* scan = reinterpret_cast<int*>(sm + L::kOffScan);
@@ -322,13 +321,11 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
     float* part = reinterpret_cast<float*>(sm + L::kOffPart);
     int q0 = 0, n = 0;  // stages before this item; items before it
     for (int64_t item = blockIdx.x; item < total; item += gridDim.x, ++n, q0 += nk) {
-      float acc[2][NT][4];
+      float acc[2][4];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int b = 0; b < NT; ++b)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[m][b][c] = 0.0f;
+        for (int c = 0; c < 4; ++c) acc[m][c] = 0.0f;
       const int d = n % kEItems;
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&item_full[d], static_cast<uint32_t>(n / kEItems) & 1u));
       const int4 it = items[d * 2];
@@ -396,7 +393,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
             const uint4 u = make_uint4(sel(sw, v.z, v.x), sel(sw, v.w, v.y), sel(sw, v.x, v.z), sel(sw, v.y, v.w));
             w[j] = kInt4 ? u : make_uint4(sel(sw1, u.y, u.x), sel(sw1, u.x, u.y), sel(sw1, u.w, u.z), sel(sw1, u.z, u.w));
           }
-          float grp[2][NT][4];
+          float grp[2][4];
           uint32_t zl[4], zh[4];  // 1024 + z and 64 + z
           if (kInt4) {
 #pragma unroll
@@ -408,9 +405,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-              for (int b = 0; b < NT; ++b)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) grp[m][b][c] = 0.0f;
+              for (int c = 0; c < 4; ++c) grp[m][c] = 0.0f;
           }
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
@@ -426,26 +421,19 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
                 d[j][3] = hsub2_u32((v8 & 0x00F000F0u) | 0x54005400u, zh[j]);
               }
               const int piece = 4 * (4 * i + t) + (p ^ (t & 2));
+              const uint4 x = *reinterpret_cast<const uint4*>(xt + piece * 16);
+              const uint32_t b0 = __byte_perm(x.x, x.z, 0x5410), b1 = __byte_perm(x.x, x.z, 0x7632);
+              const uint32_t b2 = __byte_perm(x.y, x.w, 0x5410), b3 = __byte_perm(x.y, x.w, 0x7632);
 #pragma unroll
-              for (int b = 0; b < NT; ++b) {
-                const uint4 x = *reinterpret_cast<const uint4*>(xt + b * 8 * L::kXRow + piece * 16);
-                const uint32_t b0 = __byte_perm(x.x, x.z, 0x5410), b1 = __byte_perm(x.x, x.z, 0x7632);
-                const uint32_t b2 = __byte_perm(x.y, x.w, 0x5410), b3 = __byte_perm(x.y, x.w, 0x7632);
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                  mma_16816(grp[m][b], d[2 * m][0], d[2 * m + 1][0], d[2 * m][1], d[2 * m + 1][1], b0, b1);
-                  mma_16816(grp[m][b], d[2 * m][2], d[2 * m + 1][2], d[2 * m][3], d[2 * m + 1][3], b2, b3);
-                }
+              for (int m = 0; m < 2; ++m) {
+                mma_16816(grp[m], d[2 * m][0], d[2 * m + 1][0], d[2 * m][1], d[2 * m + 1][1], b0, b1);
+                mma_16816(grp[m], d[2 * m][2], d[2 * m + 1][2], d[2 * m][3], d[2 * m + 1][3], b2, b3);
               }
             } else {
               const int piece = 8 * (4 * i + t) + 2 * (p ^ t);
-              uint4 x0[NT], x1[NT];
-#pragma unroll
-              for (int b = 0; b < NT; ++b) {
-                const uint8_t* xp = xt + b * 8 * L::kXRow + piece * 16;
-                x0[b] = in ? *reinterpret_cast<const uint4*>(xp) : make_uint4(0u, 0u, 0u, 0u);
-                x1[b] = in ? *reinterpret_cast<const uint4*>(xp + 16) : make_uint4(0u, 0u, 0u, 0u);
-              }
+              const uint8_t* xp = xt + piece * 16;
+              const uint4 x0 = in ? *reinterpret_cast<const uint4*>(xp) : make_uint4(0u, 0u, 0u, 0u);
+              const uint4 x1 = in ? *reinterpret_cast<const uint4*>(xp + 16) : make_uint4(0u, 0u, 0u, 0u);
               // codes j and j + 8 at bits 2 j and 16 + 2 j: j = 0..3 of v, then 4..7 of v >> 8
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
@@ -458,17 +446,14 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
                   d[j][2] = hsub2_u32((v & 0x00300030u) | 0x54005400u, 0x54105410u);  // 64 + c - 65
                   d[j][3] = hsub2_u32((v & 0x00C000C0u) | 0x4C004C00u, 0x4C404C40u);  // 16 + c - 17
                 }
+                const uint32_t xa = h ? x0.z : x0.x, xb = h ? x0.w : x0.y;
+                const uint32_t ya = h ? x1.z : x1.x, yb = h ? x1.w : x1.y;
+                const uint32_t b0 = __byte_perm(xa, ya, 0x5410), b1 = __byte_perm(xa, ya, 0x7632);
+                const uint32_t b2 = __byte_perm(xb, yb, 0x5410), b3 = __byte_perm(xb, yb, 0x7632);
 #pragma unroll
-                for (int b = 0; b < NT; ++b) {
-                  const uint32_t xa = h ? x0[b].z : x0[b].x, xb = h ? x0[b].w : x0[b].y;
-                  const uint32_t ya = h ? x1[b].z : x1[b].x, yb = h ? x1[b].w : x1[b].y;
-                  const uint32_t b0 = __byte_perm(xa, ya, 0x5410), b1 = __byte_perm(xa, ya, 0x7632);
-                  const uint32_t b2 = __byte_perm(xb, yb, 0x5410), b3 = __byte_perm(xb, yb, 0x7632);
-#pragma unroll
-                  for (int m = 0; m < 2; ++m) {
-                    mma_16816(acc[m][b], d[2 * m][0], d[2 * m + 1][0], d[2 * m][1], d[2 * m + 1][1], b0, b1);
-                    mma_16816(acc[m][b], d[2 * m][2], d[2 * m + 1][2], d[2 * m][3], d[2 * m + 1][3], b2, b3);
-                  }
+                for (int m = 0; m < 2; ++m) {
+                  mma_16816(acc[m], d[2 * m][0], d[2 * m + 1][0], d[2 * m][1], d[2 * m + 1][1], b0, b1);
+                  mma_16816(acc[m], d[2 * m][2], d[2 * m + 1][2], d[2 * m][3], d[2 * m + 1][3], b2, b3);
                 }
               }
             }
@@ -478,13 +463,10 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
             for (int m = 0; m < 2; ++m) {
               const float s0 = __half2float(__ushort_as_half(static_cast<uint16_t>(sc_now[2 * m] >> (16 * i))));
               const float s1 = __half2float(__ushort_as_half(static_cast<uint16_t>(sc_now[2 * m + 1] >> (16 * i))));
-#pragma unroll
-              for (int b = 0; b < NT; ++b) {
-                acc[m][b][0] = fmaf(grp[m][b][0], s0, acc[m][b][0]);
-                acc[m][b][1] = fmaf(grp[m][b][1], s0, acc[m][b][1]);
-                acc[m][b][2] = fmaf(grp[m][b][2], s1, acc[m][b][2]);
-                acc[m][b][3] = fmaf(grp[m][b][3], s1, acc[m][b][3]);
-              }
+              acc[m][0] = fmaf(grp[m][0], s0, acc[m][0]);
+              acc[m][1] = fmaf(grp[m][1], s0, acc[m][1]);
+              acc[m][2] = fmaf(grp[m][2], s1, acc[m][2]);
+              acc[m][3] = fmaf(grp[m][3], s1, acc[m][3]);
             }
           }
         }
@@ -497,10 +479,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int b = 0; b < NT; ++b)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            mine[(8 * b + 2 * t + (c & 1)) * 132 + rg * 32 + 16 * m + 8 * (c >> 1) + pg] = acc[m][b][c];
+        for (int c = 0; c < 4; ++c) mine[(2 * t + (c & 1)) * 132 + rg * 32 + 16 * m + 8 * (c >> 1) + pg] = acc[m][c];
       warps_barrier(1, L::kConsumers);
       if (ok) {
         const int64_t nn = n0 + 4 * lane;
@@ -538,15 +517,15 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, NT>::kThreads, SkinnyLayou
   }
 }
 
-template <bool kInt4, int NT>
+template <bool kInt4>
 static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
-  using L = SkinnyLayout<kInt4, NT>;
+  using L = SkinnyLayout<kInt4>;
   const uint64_t row_bytes = static_cast<uint64_t>(kInt4 ? a.K / 2 : a.K / 4);
   CUtensorMap tw;
   if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, row_bytes, static_cast<uint64_t>(a.E) * a.N, row_bytes, 128,
                     kERows, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  auto* kern = experts_skinny_kernel<kInt4, NT>;
+  auto* kern = experts_skinny_kernel<kInt4>;
   const int smem = L::bytes(a.E);
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -1120,10 +1099,7 @@ static cudaError_t launch_experts(int path, const ExpertArgs& a, cudaStream_t s)
     b.order = nullptr;
     return launch_experts_tc<kInt4>(b, s);
   }
-  // rows per expert of an even spread; no expert has more than R rows
-  const int64_t avg = a.R / a.E;
-  if (a.R <= 8 || avg <= 4) return launch_experts_skinny<kInt4, 1>(a, s);
-  return launch_experts_skinny<kInt4, 2>(a, s);
+  return launch_experts_skinny<kInt4>(a, s);
 }
 
 cudaError_t launch_gemm_experts(bool int4, int path, const ExpertArgs& a, cudaStream_t s) {

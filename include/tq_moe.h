@@ -124,7 +124,7 @@ TQ_API int tq_moe_combine_backward(const void* dout, const void* y, int dtype, c
  *            rows there in sorted order before the product.  Without it AUTO takes the DECODE path
  *            (right, slower), and PREFILL returns TQ_ERR_NULL.  Not read or written otherwise.
  *   path     TQ_PATH_AUTO, or one path (tests): DECODE takes few rows per expert (mma.sync on
- *            in-register decode, up to 32 rows of an expert per pass over its weights), PREFILL
+ *            in-register decode, up to 8 rows of an expert per pass over its weights), PREFILL
  *            many (tcgen05.mma), GENERIC any shape and alignment.  DECODE and PREFILL need
  *            K % 64 == 0 (TQ_ERR_PATH) and 16-byte aligned x, weights and y (TQ_ERR_ALIGN).
  *            Every path is right for any numbers of rows per expert; AUTO goes by the average
