@@ -188,6 +188,44 @@ __device__ __forceinline__ ExpertItem expert_item(const ExpertArgs& a, const int
   return it;
 }
 
+// (v & mask) | base in one instruction: with both constants written out the compiler spends two, and
+// constants that it sees as uniform it moves into place for every use.  They come from shared memory.
+struct DecodeConsts {  // natural order, from a byte in both halves: see decode_tq_8, w4_zero_pair
+  uint32_t mask0, base0, mask1, base1;
+};
+__device__ __forceinline__ void store_decode_consts(bool int4, uint32_t* c) {  // four words
+  c[0] = int4 ? 0x00F0000Fu : 0x000C0003u;
+  c[1] = int4 ? 0x54006400u : 0x5C006400u;
+  c[2] = 0x00C00030u;
+  c[3] = 0x4C005400u;
+}
+__device__ __forceinline__ DecodeConsts load_decode_consts(const uint32_t* c) {
+  const volatile uint32_t* v = c;
+  return DecodeConsts{v[0], v[1], v[2], v[3]};
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t base) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(base));
+  return r;
+}
+struct FieldConsts {  // fields i and i + 4 (i + 8) of a word: mask and base of the i-th
+  uint32_t mask[4], base[4];
+};
+__device__ __forceinline__ void store_field_consts(bool int4, uint32_t* c) {  // eight words
+  c[0] = int4 ? 0x000F000Fu : 0x00030003u;
+  c[1] = int4 ? 0x00F000F0u : 0x000C000Cu;
+  c[2] = 0x00300030u;
+  c[3] = 0x00C000C0u;
+  c[4] = 0x64006400u;                          // 1024: unit in the lowest bits
+  c[5] = int4 ? 0x54005400u : 0x5C005C00u;     // 64 (four bits up) or 256 (two)
+  c[6] = 0x54005400u;
+  c[7] = 0x4C004C00u;                          // 16
+}
+__device__ __forceinline__ FieldConsts load_field_consts(const uint32_t* c) {
+  const volatile uint32_t* v = c;
+  return FieldConsts{{v[0], v[1], v[2], v[3]}, {v[4], v[5], v[6], v[7]}};
+}
+
 // ---------------------------------------------------------------------------------------------
 // Few rows per expert: bound by the packed weights' bytes.  Persistent CTAs; an item is 128 weight
 // rows of one expert times up to 8 of its rows, all of K.  One producer warp keeps a ring
@@ -232,7 +270,8 @@ struct SkinnyLayout {
   static constexpr int kOffBar = kOffPart + KG * kPart;
   static constexpr int kOffItem = kOffBar + 2 * (kRing + kEItems) * 8;
   static constexpr int kOffScan = kOffItem + kEItems * 32;  // descriptors of 32 bytes
-  static constexpr int kOffFirst = kOffScan + 32 * 4;
+  static constexpr int kOffConst = kOffScan + 32 * 4;       // FieldConsts
+  static constexpr int kOffFirst = kOffConst + 32;
   static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }  // 1024: alignment
   static_assert(kRing % KG == 0 && kOffFirst + 1025 * 4 + 1024 <= 113 * 1024, "two CTAs per SM");
 };
@@ -265,6 +304,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], 4 * L::KG);
     }
+    store_field_consts(kInt4, reinterpret_cast<uint32_t*>(sm + L::kOffConst));
     fence_mbar_init();
     tma_prefetch_desc(&tmap_w);
   }
@@ -318,6 +358,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
     const int pg = (g >> 1) | ((g & 1) << 2);  // weight row of this lane group within 8
     const int64_t G = a.K >> 7;
     const bool sw = (t & 2) != 0, sw1 = (t & 1) != 0;
+    const FieldConsts fc = load_field_consts(reinterpret_cast<const uint32_t*>(sm + L::kOffConst));
     float* part = reinterpret_cast<float*>(sm + L::kOffPart);
     int q0 = 0, n = 0;  // stages before this item; items before it
     for (int64_t item = blockIdx.x; item < total; item += gridDim.x, ++n, q0 += nk) {
@@ -415,10 +456,10 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const uint32_t v = wd[j], v8 = v >> 8;
-                d[j][0] = hsub2_u32((v & 0x000F000Fu) | 0x64006400u, zl[j]);
-                d[j][1] = hsub2_u32((v & 0x00F000F0u) | 0x54005400u, zh[j]);
-                d[j][2] = hsub2_u32((v8 & 0x000F000Fu) | 0x64006400u, zl[j]);
-                d[j][3] = hsub2_u32((v8 & 0x00F000F0u) | 0x54005400u, zh[j]);
+                d[j][0] = hsub2_u32(and_or(v, fc.mask[0], fc.base[0]), zl[j]);
+                d[j][1] = hsub2_u32(and_or(v, fc.mask[1], fc.base[1]), zh[j]);
+                d[j][2] = hsub2_u32(and_or(v8, fc.mask[0], fc.base[0]), zl[j]);
+                d[j][3] = hsub2_u32(and_or(v8, fc.mask[1], fc.base[1]), zh[j]);
               }
               const int piece = 4 * (4 * i + t) + (p ^ (t & 2));
               const uint4 x = *reinterpret_cast<const uint4*>(xt + piece * 16);
@@ -441,10 +482,10 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   const uint32_t v = h ? wd[j] >> 8 : wd[j];
-                  d[j][0] = hsub2_u32((v & 0x00030003u) | 0x64006400u, 0x64016401u);  // 1024 + c - 1025
-                  d[j][1] = hsub2_u32((v & 0x000C000Cu) | 0x5C005C00u, 0x5C045C04u);  // 256 + c - 257
-                  d[j][2] = hsub2_u32((v & 0x00300030u) | 0x54005400u, 0x54105410u);  // 64 + c - 65
-                  d[j][3] = hsub2_u32((v & 0x00C000C0u) | 0x4C004C00u, 0x4C404C40u);  // 16 + c - 17
+                  d[j][0] = hsub2_u32(and_or(v, fc.mask[0], fc.base[0]), 0x64016401u);  // 1024 + c - 1025
+                  d[j][1] = hsub2_u32(and_or(v, fc.mask[1], fc.base[1]), 0x5C045C04u);  // 256 + c - 257
+                  d[j][2] = hsub2_u32(and_or(v, fc.mask[2], fc.base[2]), 0x54105410u);  // 64 + c - 65
+                  d[j][3] = hsub2_u32(and_or(v, fc.mask[3], fc.base[3]), 0x4C404C40u);  // 16 + c - 17
                 }
                 const uint32_t xa = h ? x0.z : x0.x, xb = h ? x0.w : x0.y;
                 const uint32_t ya = h ? x1.z : x1.x, yb = h ? x1.w : x1.y;
@@ -602,26 +643,6 @@ struct ExpertTcLayout {
   static_assert(kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 && kOffFirst > 114 * 1024, "one CTA per SM");
 };
 
-// (v & mask) | base in one instruction: with both constants written out the compiler spends two, and
-// constants that it sees as uniform it moves into place for every use.  They come from shared memory.
-struct DecodeConsts {
-  uint32_t mask0, base0, mask1, base1;
-};
-__device__ __forceinline__ void store_decode_consts(bool int4, uint32_t* c) {  // four words
-  c[0] = int4 ? 0x00F0000Fu : 0x000C0003u;
-  c[1] = int4 ? 0x54006400u : 0x5C006400u;
-  c[2] = 0x00C00030u;
-  c[3] = 0x4C005400u;
-}
-__device__ __forceinline__ DecodeConsts load_decode_consts(const uint32_t* c) {
-  const volatile uint32_t* v = c;
-  return DecodeConsts{v[0], v[1], v[2], v[3]};
-}
-__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t base) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(base));
-  return r;
-}
 // 32 INT4 codes -> 16 registers of fp16 pairs (u - z) s, in natural order (as decode_w4_8).
 __device__ __forceinline__ void decode_piece_w4(const uint4& c, uint32_t s2, uint32_t zsub, const DecodeConsts& k,
                                                 uint32_t* v) {
