@@ -168,7 +168,9 @@ template <bool kEven>
 __device__ __forceinline__ ExpertItem expert_item(const ExpertArgs& a, const int* first, int64_t item, int64_t tiles,
                                                   int TM) {
   int lo = 0, hi = a.E;  // first[lo] tiles <= item < first[lo + 1] tiles
-  const int chunk_at = static_cast<int>(item / tiles);
+  const int chunk_at = (item | tiles) >> 31 == 0
+                           ? static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(tiles))
+                           : static_cast<int>(item / tiles);
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (first[mid] <= chunk_at)
@@ -244,9 +246,10 @@ __device__ __forceinline__ FieldConsts load_field_consts(const uint32_t* c) {
 // takes the base (and the zero-point) off, exactly.  x is brought into the same pairs by byte
 // permutes, once per warp for 32 weight rows.
 //
-// Bank conflicts: lane t's x starts 64 (128) bytes after lane t - 1's, so the lanes take their
-// words in an order that differs by t (word ^ 2 (t / 2); word ^ t for ternary) and x rows are 16
-// bytes apart modulo 128; weight row of lane group g is (g / 2) + 4 (g % 2), so that the two rows
+// Bank conflicts: rows of x are 16 bytes apart modulo 128, and lane t's x starts 64 (128) bytes after
+// lane t - 1's: two lanes share banks (four, and so the odd ternary lanes take their words in pairs
+// the other way round).  Ordering the words of all lanes apart took two selects per MMA, more than
+// the shared memory's extra cycles: it is the ALU that bounds this loop.  Weight row of lane group g is (g / 2) + 4 (g % 2), so that the two rows
 // of a quarter-warp access differ in the swizzle's top bit.
 // ---------------------------------------------------------------------------------------------
 constexpr int kERows = 128;       // weight rows per item
@@ -309,6 +312,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
     tma_prefetch_desc(&tmap_w);
   }
   pdl_wait_prior_grids();
+  const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
   expert_chunks(a, L::TM, first, scan, L::kThreads);
   const int64_t tiles = (a.N + kERows - 1) / kERows;
   const int64_t total = static_cast<int64_t>(uniform(first[a.E])) * tiles;
@@ -317,14 +321,22 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
 
   if (warp == L::KG * 4) {
     // ------------------------------------------------------------------ producer
+    // The first item's weights are requested before its rows are looked up; their barriers complete
+    // with the arrivals that add the rows' bytes.
     int q = 0, n = 0;
     for (int64_t item = blockIdx.x; item < total && ok; item += gridDim.x, ++n) {
       const ExpertItem it = expert_item<false>(a, first, item, tiles, L::TM);
+      const int wrow = static_cast<int>(static_cast<int64_t>(it.e) * a.N + static_cast<int64_t>(it.tile) * kERows);
+      const int early = n == 0 ? (nk < L::kRing ? nk : L::kRing) : 0;
+      if (lane < early) {
+        mbar_expect_tx(&full[lane], L::kTileW);
+        tma_load_2d(sm + lane * L::kTileW, &tmap_w, &full[lane], lane * 128, wrow);
+      }
+      __syncwarp();
       int64_t xr = -1;
       if (lane < it.rows) xr = expert_x_row(a, it.row0 + lane);
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, xr >= 0);
       const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x + (xr >= 0 ? xr * a.K : 0));
-      const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
       const int d = n % kEItems;
       if (n >= kEItems) ok = mbar_wait_relaxed(&item_empty[d], static_cast<uint32_t>(n / kEItems - 1) & 1u);
       ok = __all_sync(0xFFFFFFFFu, ok);
@@ -334,7 +346,6 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
         items[d * 2 + 1].x = static_cast<int>(mask);
         mbar_arrive(&item_full[d]);
       }
-      const int wrow = static_cast<int>(static_cast<int64_t>(it.e) * a.N + static_cast<int64_t>(it.tile) * kERows);
       for (int kb = 0; kb < nk && ok; ++kb, ++q) {
         const int s = q % L::kRing;
         if (q >= L::kRing) ok = mbar_wait_relaxed(&empty[s], static_cast<uint32_t>(q / L::kRing - 1) & 1u);
@@ -343,8 +354,8 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
         const int64_t k0 = static_cast<int64_t>(kb) * L::KS;
         const uint32_t xb = static_cast<uint32_t>((a.K - k0 < L::KS ? a.K - k0 : L::KS) * 2);
         if (lane == 0) {
-          mbar_arrive_expect_tx(&full[s], L::kTileW + __popc(mask) * xb);
-          tma_load_2d(sm + s * L::kTileW, &tmap_w, &full[s], kb * 128, wrow);
+          mbar_arrive_expect_tx(&full[s], (kb >= early ? L::kTileW : 0) + __popc(mask) * xb);
+          if (kb >= early) tma_load_2d(sm + s * L::kTileW, &tmap_w, &full[s], kb * 128, wrow);
         }
         __syncwarp();
         if (xr >= 0 && !skipx)
@@ -357,7 +368,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
     const int g = lane >> 2, t = lane & 3;
     const int pg = (g >> 1) | ((g & 1) << 2);  // weight row of this lane group within 8
     const int64_t G = a.K >> 7;
-    const bool sw = (t & 2) != 0, sw1 = (t & 1) != 0;
+    const bool odd = (t & 1) != 0;
     const FieldConsts fc = load_field_consts(reinterpret_cast<const uint32_t*>(sm + L::kOffConst));
     float* part = reinterpret_cast<float*>(sm + L::kOffPart);
     int q0 = 0, n = 0;  // stages before this item; items before it
@@ -429,10 +440,10 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             w[j] = *reinterpret_cast<const uint4*>(wt + j * 8 * 128 + (((4 * i + t) ^ pg) << 4));
-            // word order of this lane: word ^ (2 (t / 2)), ternary word ^ t
-            const uint4 v = w[j];
-            const uint4 u = make_uint4(sel(sw, v.z, v.x), sel(sw, v.w, v.y), sel(sw, v.x, v.z), sel(sw, v.y, v.w));
-            w[j] = kInt4 ? u : make_uint4(sel(sw1, u.y, u.x), sel(sw1, u.x, u.y), sel(sw1, u.w, u.z), sel(sw1, u.z, u.w));
+            if (!kInt4) {  // this lane takes word p ^ (t & 1)
+              const uint4 u = w[j];
+              w[j] = make_uint4(sel(odd, u.y, u.x), sel(odd, u.x, u.y), sel(odd, u.w, u.z), sel(odd, u.z, u.w));
+            }
           }
           float grp[2][4];
           uint32_t zl[4], zh[4];  // 1024 + z and 64 + z
@@ -461,7 +472,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
                 d[j][2] = hsub2_u32(and_or(v8, fc.mask[0], fc.base[0]), zl[j]);
                 d[j][3] = hsub2_u32(and_or(v8, fc.mask[1], fc.base[1]), zh[j]);
               }
-              const int piece = 4 * (4 * i + t) + (p ^ (t & 2));
+              const int piece = 4 * (4 * i + t) + p;
               const uint4 x = *reinterpret_cast<const uint4*>(xt + piece * 16);
               const uint32_t b0 = __byte_perm(x.x, x.z, 0x5410), b1 = __byte_perm(x.x, x.z, 0x7632);
               const uint32_t b2 = __byte_perm(x.y, x.w, 0x5410), b3 = __byte_perm(x.y, x.w, 0x7632);
@@ -471,7 +482,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
                 mma_16816(grp[m], d[2 * m][2], d[2 * m + 1][2], d[2 * m][3], d[2 * m + 1][3], b2, b3);
               }
             } else {
-              const int piece = 8 * (4 * i + t) + 2 * (p ^ t);
+              const int piece = 8 * (4 * i + t) + 2 * (p ^ (t & 1));
               const uint8_t* xp = xt + piece * 16;
               const uint4 x0 = in ? *reinterpret_cast<const uint4*>(xp) : make_uint4(0u, 0u, 0u, 0u);
               const uint4 x1 = in ? *reinterpret_cast<const uint4*>(xp + 16) : make_uint4(0u, 0u, 0u, 0u);
