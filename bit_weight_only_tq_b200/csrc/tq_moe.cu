@@ -76,6 +76,25 @@ __device__ __forceinline__ uint32_t route_key(float x) {
 __device__ __forceinline__ float route_unkey(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
+// The same of a 16-bit score, from its value: a 16-bit key.
+__device__ __forceinline__ uint32_t route_bits16(float x, __half) { return __half_as_ushort(__float2half_rn(x)); }
+__device__ __forceinline__ uint32_t route_bits16(float x, __nv_bfloat16) { return __float_as_uint(x) >> 16; }
+__device__ __forceinline__ uint32_t route_bits16(float, float) { return 0u; }  // not used
+__device__ __forceinline__ float route_value16(uint32_t b, __half) {
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(b)));
+}
+__device__ __forceinline__ float route_value16(uint32_t b, __nv_bfloat16) { return __uint_as_float(b << 16); }
+__device__ __forceinline__ float route_value16(uint32_t, float) { return 0.0f; }  // not used
+template <typename T>
+__device__ __forceinline__ uint32_t route_key16(float x) {
+  if (!(x > -INFINITY)) return 0u;
+  const uint32_t u = route_bits16(x + 0.0f, T());
+  return (u & 0x8000u) ? ~u & 0xFFFFu : u | 0x8000u;
+}
+template <typename T>
+__device__ __forceinline__ float route_unkey16(uint32_t k) {
+  return route_value16((k & 0x8000u) ? k & 0x7FFFu : ~k & 0xFFFFu, T());
+}
 // exp(x - m) for x <= m; 1 where they are equal, which at m = +inf is the limit.
 __device__ __forceinline__ float exp_below(float x, float m) { return x == m ? 1.0f : expf(x - m); }
 
@@ -112,44 +131,72 @@ __global__ void __launch_bounds__(kRouteThreads)
   if (t >= T_) return;
   float x[VPL];
   route_load<T, VPL, W>(logits + t * E, E, lane, x);
-  uint32_t key[VPL];
-  uint32_t bk = 0;
-  int bi = 0;
   auto expert = [&](int v) { return (v / W) * 32 * W + W * lane + v % W; };
-#pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    key[v] = route_key(x[v]);
-    if (key[v] > bk) {
-      bk = key[v];
-      bi = expert(v);
-    }
-  }
   uint32_t my_key = 0;  // lane j: the j-th choice
   int my_id = -1;
   uint32_t top = 0;
-  for (int j = 0; j < k; ++j) {
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, bk);
-    if (m == 0) break;
-    if (j == 0) top = m;
-    const int i = __reduce_min_sync(0xFFFFFFFFu, bk == m ? bi : 0x7FFFFFFF);
-    if (lane == j) {
-      my_key = m;
-      my_id = i;
-    }
-    if (j + 1 < k) {
-      bk = 0;
+  if (sizeof(T) == 2) {
+    // a 16-bit score's key fits the upper half of a word with the expert's complement below it: one
+    // maximum finds the largest score and the lowest expert among equals
+    uint32_t word[VPL], best = 0;
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        if (expert(v) == i) key[v] = 0;
-        if (key[v] > bk) {
-          bk = key[v];
-          bi = expert(v);
+    for (int v = 0; v < VPL; ++v) {
+      const uint32_t key = route_key16<T>(x[v]);
+      word[v] = key ? (key << 16) | (0xFFFFu - static_cast<uint32_t>(expert(v))) : 0u;
+      best = max(best, word[v]);
+    }
+    for (int j = 0; j < k; ++j) {
+      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+      if (m == 0) break;
+      if (j == 0) top = m;
+      if (lane == j) my_key = m;
+      if (j + 1 < k && best == m) {  // the lane that held it looks for its next
+        best = 0;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+          if (word[v] == m) word[v] = 0;
+          best = max(best, word[v]);
+        }
+      }
+    }
+    if (my_key) my_id = static_cast<int>(0xFFFFu - (my_key & 0xFFFFu));
+  } else {
+    uint32_t key[VPL];
+    uint32_t bk = 0;
+    int bi = 0;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      key[v] = route_key(x[v]);
+      if (key[v] > bk) {
+        bk = key[v];
+        bi = expert(v);
+      }
+    }
+    for (int j = 0; j < k; ++j) {
+      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, bk);
+      if (m == 0) break;
+      if (j == 0) top = m;
+      const int i = __reduce_min_sync(0xFFFFFFFFu, bk == m ? bi : 0x7FFFFFFF);
+      if (lane == j) {
+        my_key = m;
+        my_id = i;
+      }
+      if (j + 1 < k && bk == m && bi == i) {  // the lane that held it looks for its next
+        bk = 0;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+          if (expert(v) == i) key[v] = 0;
+          if (key[v] > bk) {
+            bk = key[v];
+            bi = expert(v);
+          }
         }
       }
     }
   }
-  const float mx = route_unkey(top);
-  float e = my_id >= 0 ? exp_below(route_unkey(my_key), mx) : 0.0f;
+  auto value = [](uint32_t m) { return sizeof(T) == 2 ? route_unkey16<T>(m >> 16) : route_unkey(m); };
+  const float mx = value(top);
+  float e = my_id >= 0 ? exp_below(value(my_key), mx) : 0.0f;
   float sum;
   if (renorm) {
     sum = warp_sum(e);
@@ -157,7 +204,7 @@ __global__ void __launch_bounds__(kRouteThreads)
     sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
-      if (route_key(x[v]) != 0u) sum += exp_below(x[v], mx);
+      if (x[v] > -INFINITY) sum += exp_below(x[v], mx);
     sum = warp_sum(sum);
   }
   if (lane < k) {
@@ -206,7 +253,7 @@ __global__ void __launch_bounds__(kRouteThreads)
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      x[v] = route_key(x[v]) != 0u ? exp_below(x[v], mx) : 0.0f;
+      x[v] = x[v] > -INFINITY ? exp_below(x[v], mx) : 0.0f;
       sum += x[v];
     }
     sum = warp_sum(sum);
@@ -339,11 +386,15 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32, 1)
   for (int e = tid * P; e < E && e < tid * P + P; ++e) {
     int before = 0, all = tot[e];
     if (C > 1) {
+      int v[kSortCluster];
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c)
+        v[c] = __float_as_int(ld_shared_cluster_f32(mapa_shared(smem_u32(&tot[e]), static_cast<uint32_t>(c))));
       all = 0;
-      for (int c = 0; c < C; ++c) {
-        const int v = __float_as_int(ld_shared_cluster_f32(mapa_shared(smem_u32(&tot[e]), static_cast<uint32_t>(c))));
-        before += c < rank ? v : 0;
-        all += v;
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c) {
+        before += c < rank ? v[c] : 0;
+        all += v[c];
       }
     }
     start[e] = sum + before;
@@ -413,38 +464,53 @@ cudaError_t launch_moe_sort(const int32_t* ids, int32_t* offsets, int32_t* order
 }
 
 // ---------------------------------------------------------------------------------------------
-// Rows.  A warp takes tasks (row, segment of 32 U vectors); bound by HBM at large sizes.
+// Rows.  A CTA of 128 threads takes one row (or token) at a time, each thread a 16-byte vector per
+// step, with the rows' loads of a step in flight together; 16 CTAs per SM keep enough of them in
+// flight for HBM, which bounds these kernels (a warp per segment of a row, with more loads per
+// thread and fewer threads, reached half the bandwidth).  With few rows a CTA takes one step of a row.
 // ---------------------------------------------------------------------------------------------
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 
-// Grid of a kernel whose warps take `tasks` tasks with a stride of the grid.
-static unsigned row_grid(int64_t tasks, int warps_per_cta, int ctas_per_sm) {
-  const int64_t want = (tasks + warps_per_cta - 1) / warps_per_cta;
+// Grid of a kernel whose CTAs take `tasks` tasks with a stride of the grid.
+static unsigned row_grid(int64_t tasks, int tasks_per_cta, int ctas_per_sm) {
+  const int64_t want = (tasks + tasks_per_cta - 1) / tasks_per_cta;
   const int64_t cap = static_cast<int64_t>(current_device_info().num_sms) * ctas_per_sm;
   return static_cast<unsigned>(want < cap ? (want > 0 ? want : 1) : cap);
 }
 
-template <typename V, int U>
+// How rows of `steps` steps are cut into tasks: whole rows, or single steps while the rows alone
+// would not give every SM a few CTAs.
+static int row_parts(int64_t rows, int steps) {
+  return rows < 4 * current_device_info().num_sms ? steps : 1;
+}
+
+template <typename V>
 __global__ void __launch_bounds__(kRowThreads)
     moe_gather_kernel(const V* __restrict__ x, const int32_t* __restrict__ order, const int32_t* __restrict__ offsets,
-                      V* __restrict__ rows, int64_t T_, int64_t R, int64_t nv, int64_t segs, int k, int E) {
+                      V* __restrict__ rows, int64_t T_, int64_t R, int nv, int parts, int k, int E) {
   pdl_allow_dependents();
   pdl_wait_prior_grids();
-  const int lane = threadIdx.x & 31;
-  const int64_t kept = offsets[E];
-  const int64_t tasks = (kept < R ? kept : R) * segs;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kRowThreads / 32);
-  for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5); w < tasks; w += step) {
-    const int64_t r = w / segs, v0 = (w - r * segs) * (32 * U) + lane;
-    const int64_t t = order[r] / k;
+  const int64_t kept = offsets[E] < R ? offsets[E] : R;
+  const int part = blockIdx.x % parts, per = (nv + parts - 1) / parts;
+  const int v0 = part * per + threadIdx.x, v1 = part * per + per < nv ? part * per + per : nv;
+  const int64_t step = gridDim.x / parts;
+  int64_t r = blockIdx.x / parts;
+  int slot = r < kept ? order[r] : 0;
+  for (; r < kept; r += step) {
+    const int64_t t = slot / k;
+    slot = r + step < kept ? order[r + step] : 0;  // the next row's, a row ahead
     if (t < 0 || t >= T_) continue;
-    V b[U];
+    const V* src = x + t * nv;
+    V* dst = rows + r * nv;
+    for (int v = v0; v < v1; v += 4 * kRowThreads) {
+      V b[4];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (v0 + 32 * u < nv) b[u] = x[t * nv + v0 + 32 * u];
+      for (int u = 0; u < 4; ++u)
+        if (v + u * kRowThreads < v1) b[u] = src[v + u * kRowThreads];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (v0 + 32 * u < nv) rows[r * nv + v0 + 32 * u] = b[u];
+      for (int u = 0; u < 4; ++u)
+        if (v + u * kRowThreads < v1) dst[v + u * kRowThreads] = b[u];
+    }
   }
 }
 
@@ -452,59 +518,59 @@ cudaError_t launch_moe_gather(const void* x, int elem, const int32_t* order, con
                               int64_t n, int64_t H, int k, int64_t E, cudaStream_t s) {
   const int64_t R = n * k, bytes = H * elem;
   const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(rows) | static_cast<uintptr_t>(bytes)) & 15u) == 0;
-  constexpr int U = 4;
   auto run = [&](auto v) {
     using V = decltype(v);
-    const int64_t nv = bytes / static_cast<int64_t>(sizeof(V)), segs = (nv + 32 * U - 1) / (32 * U);
-    return launch_pdl(moe_gather_kernel<V, U>, dim3(row_grid(R * segs, kRowThreads / 32, 8)), dim3(kRowThreads), 0, 1, s,
-                      static_cast<const V*>(x), order, offsets, static_cast<V*>(rows), n, R, nv, segs, k,
-                      static_cast<int>(E));
+    const int nv = static_cast<int>(bytes / static_cast<int64_t>(sizeof(V)));
+    const int parts = row_parts(R, (nv + kRowThreads - 1) / kRowThreads);
+    const unsigned grid = row_grid(R, 1, 16) * static_cast<unsigned>(parts);
+    return launch_pdl(moe_gather_kernel<V>, dim3(grid), dim3(kRowThreads), 0, 1, s, static_cast<const V*>(x), order, offsets,
+                      static_cast<V*>(rows), n, R, nv, parts, k, static_cast<int>(E));
   };
   if (vec) return run(uint4());
   return elem == 4 ? run(uint32_t()) : run(uint16_t());
 }
 
-// out[t] = sum_j w_j y[pos_j]: lane j of the warp holds (pos_j, w_j); eight rows' loads are in
-// flight at a time and added in the order of j.
-template <typename T, int VE>
+// out[t] = sum_j w_j y[pos_j], added in the order of j, KB rows at a time.
+template <typename T, int VE, int KB>
 __global__ void __launch_bounds__(kRowThreads)
     moe_combine_kernel(const T* __restrict__ y, const int32_t* __restrict__ pos, const float* __restrict__ weights,
-                       T* __restrict__ out, int64_t T_, int64_t R, int64_t H, int64_t segs, int k) {
+                       T* __restrict__ out, int64_t T_, int64_t R, int H, int parts, int k) {
   pdl_allow_dependents();
   pdl_wait_prior_grids();
-  const int lane = threadIdx.x & 31;
-  const int64_t tasks = T_ * segs, step = static_cast<int64_t>(gridDim.x) * (kRowThreads / 32);
-  for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5); w < tasks; w += step) {
-    const int64_t t = w / segs, h = ((w - t * segs) * 32 + lane) * VE;
-    int p = -1;
-    float wt = 0.0f;
-    if (lane < k) {
-      p = pos[t * k + lane];
-      if (p >= R) p = -1;
-      wt = weights ? weights[t * k + lane] : 1.0f;
-    }
-    float acc[VE];
+  const int steps = (H + kRowThreads * VE - 1) / (kRowThreads * VE);
+  const int part = blockIdx.x % parts, per = (steps + parts - 1) / parts * kRowThreads * VE;
+  const int h1 = part * per + per < H ? part * per + per : H;
+  const int64_t step = gridDim.x / parts;
+  for (int64_t t = blockIdx.x / parts; t < T_; t += step) {
+    int p[KB];
+    float w[KB];
+    auto take = [&](int j0) {
 #pragma unroll
-    for (int c = 0; c < VE; ++c) acc[c] = 0.0f;
-    for (int j0 = 0; j0 < k; j0 += 8) {
-      Vec<T, VE> v[8];
-      int pj[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        pj[j] = __shfl_sync(0xFFFFFFFFu, p, (j0 + j) & 31);
-        if (j0 + j >= k) pj[j] = -1;
-        if (pj[j] >= 0 && h < H) v[j] = *reinterpret_cast<const Vec<T, VE>*>(y + static_cast<int64_t>(pj[j]) * H + h);
+      for (int j = 0; j < KB; ++j) {
+        p[j] = j0 + j < k ? pos[t * k + j0 + j] : -1;
+        if (p[j] >= R) p[j] = -1;
+        w[j] = weights && j0 + j < k ? weights[t * k + j0 + j] : 1.0f;
       }
+    };
+    take(0);
+    for (int h = part * per + threadIdx.x * VE; h < h1; h += kRowThreads * VE) {
+      float acc[VE];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float wj = __shfl_sync(0xFFFFFFFFu, wt, (j0 + j) & 31);
-        if (pj[j] >= 0 && h < H) {
+      for (int c = 0; c < VE; ++c) acc[c] = 0.0f;
+      for (int j0 = 0; j0 < k; j0 += KB) {
+        if (k > KB) take(j0);
+        Vec<T, VE> v[KB];
 #pragma unroll
-          for (int c = 0; c < VE; ++c) acc[c] = fmaf(wj, to_f32(v[j].v[c]), acc[c]);
+        for (int j = 0; j < KB; ++j)
+          if (p[j] >= 0) v[j] = *reinterpret_cast<const Vec<T, VE>*>(y + static_cast<int64_t>(p[j]) * H + h);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if (p[j] >= 0) {
+#pragma unroll
+            for (int c = 0; c < VE; ++c) acc[c] = fmaf(w[j], to_f32(v[j].v[c]), acc[c]);
+          }
         }
       }
-    }
-    if (h < H) {
       Vec<T, VE> o;
 #pragma unroll
       for (int c = 0; c < VE; ++c) o.v[c] = from_f32<T>(acc[c]);
@@ -516,14 +582,12 @@ __global__ void __launch_bounds__(kRowThreads)
 // The gradients of one token by one CTA, KB choices at a time: each thread holds a vector of dout,
 // multiplies it into KB rows of y (dweights, reduced over the CTA at the end) and writes KB rows
 // of dy; the loads of all KB rows are in flight together.
-constexpr int kCombineBwdThreads = 128;
-
 template <typename T, int VE, int KB>
-__global__ void __launch_bounds__(kCombineBwdThreads)
+__global__ void __launch_bounds__(kRowThreads)
     moe_combine_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ y, const int32_t* __restrict__ pos,
                            const float* __restrict__ weights, T* __restrict__ dy, float* __restrict__ dweights,
                            int64_t T_, int64_t R, int64_t H, int k) {
-  __shared__ float part[2][kCombineBwdThreads / 32][KB];
+  __shared__ float part[2][kRowThreads / 32][KB];
   pdl_allow_dependents();
   pdl_wait_prior_grids();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -539,7 +603,7 @@ __global__ void __launch_bounds__(kCombineBwdThreads)
         sw[j] = dy && j0 + j < k ? weights[t * k + j0 + j] : 0.0f;
         dot[j] = 0.0f;
       }
-      for (int64_t h = static_cast<int64_t>(tid) * VE; h < H; h += kCombineBwdThreads * VE) {
+      for (int64_t h = static_cast<int64_t>(tid) * VE; h < H; h += kRowThreads * VE) {
         const Vec<T, VE> d = *reinterpret_cast<const Vec<T, VE>*>(dout + t * H + h);
         Vec<T, VE> v[KB];
         if (dweights) {
@@ -577,7 +641,7 @@ __global__ void __launch_bounds__(kCombineBwdThreads)
         __syncthreads();  // the other buffer's readers are past it when it is written again
         if (tid < KB && j0 + tid < k) {
           float s = 0.0f;
-          for (int w = 0; w < kCombineBwdThreads / 32; ++w) s += part[buf][w][tid];
+          for (int w = 0; w < kRowThreads / 32; ++w) s += part[buf][w][tid];
           dweights[t * k + j0 + tid] = s;
         }
       }
@@ -593,11 +657,17 @@ static bool rows_vectorised(int64_t H, uintptr_t ptrs) {
 template <typename T>
 static cudaError_t combine_t(const void* y, const int32_t* pos, const float* weights, void* out, int64_t n, int64_t R,
                              int64_t H, int k, cudaStream_t s) {
-  auto run = [&](auto ve) {
+  auto run2 = [&](auto ve, auto kb) {
     constexpr int VE = decltype(ve)::value;
-    const int64_t segs = (H + 32 * VE - 1) / (32 * VE);
-    return launch_pdl(moe_combine_kernel<T, VE>, dim3(row_grid(n * segs, kRowThreads / 32, 8)), dim3(kRowThreads), 0, 1, s,
-                      static_cast<const T*>(y), pos, weights, static_cast<T*>(out), n, R, H, segs, k);
+    const int parts = row_parts(n, static_cast<int>((H + kRowThreads * VE - 1) / (kRowThreads * VE)));
+    const unsigned grid = row_grid(n, 1, 16) * static_cast<unsigned>(parts);
+    return launch_pdl(moe_combine_kernel<T, VE, decltype(kb)::value>, dim3(grid), dim3(kRowThreads), 0, 1, s,
+                      static_cast<const T*>(y), pos, weights, static_cast<T*>(out), n, R, static_cast<int>(H), parts, k);
+  };
+  auto run = [&](auto ve) {
+    if (k <= 2) return run2(ve, std::integral_constant<int, 2>());
+    if (k <= 4) return run2(ve, std::integral_constant<int, 4>());
+    return run2(ve, std::integral_constant<int, 8>());
   };
   if (rows_vectorised<T>(H, reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)))
     return run(std::integral_constant<int, 16 / sizeof(T)>());
@@ -610,7 +680,7 @@ static cudaError_t combine_bwd_t(const void* dout, const void* y, const int32_t*
   auto run2 = [&](auto ve, auto kb) {
     const unsigned grid = row_grid(n, 1, 16);
     return launch_pdl(moe_combine_bwd_kernel<T, decltype(ve)::value, decltype(kb)::value>, dim3(grid),
-                      dim3(kCombineBwdThreads), 0, 1, s, static_cast<const T*>(dout), static_cast<const T*>(y), pos,
+                      dim3(kRowThreads), 0, 1, s, static_cast<const T*>(dout), static_cast<const T*>(y), pos,
                       weights, static_cast<T*>(dy), dweights, n, R, H, k);
   };
   auto run = [&](auto ve) {
