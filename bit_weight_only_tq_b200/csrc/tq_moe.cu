@@ -366,15 +366,26 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32, 1)
 #pragma unroll 4
   for (int64_t i = lo + lane; i < hi; i += 32) atomicAdd(&cnt[warp * B + bin(i)], 1);
   __syncthreads();
-  for (int e = tid; e < B; e += nt) {
+  for (int e = tid; e < B && W <= 8; e += nt) {  // few warps: a thread per bin
     int run = 0;
-#pragma unroll 8
+#pragma unroll 4
     for (int w = 0; w < W; ++w) {
       const int c = cnt[w * B + e];
       cnt[w * B + e] = run;
       run += c;
     }
     tot[e] = run;
+  }
+  for (int e = warp; e < B && W > 8; e += W) {  // a warp per bin, lane w: warp w's count
+    const int c = lane < W ? cnt[lane * B + e] : 0;
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane < W) cnt[lane * B + e] = incl - c;
+    if (lane == 31) tot[e] = incl;
   }
   if (C > 1)
     cluster_sync_all();
@@ -425,10 +436,9 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32, 1)
     start[E] = total + before;
     if (rank == 0) offsets[E] = total;
   }
-  if (C > 1)
-    cluster_sync_all();  // no CTA leaves while another reads its counts
-  else
-    __syncthreads();
+  // no CTA leaves while another reads its counts: the wait is at the end
+  if (C > 1) cluster_arrive();
+  __syncthreads();
   int* mine = cnt + warp * B;
   for (int64_t s0 = lo; s0 < hi; s0 += 32) {
     const int64_t i = s0 + lane;
@@ -445,6 +455,10 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32, 1)
       order[row] = static_cast<int32_t>(i);
       pos[i] = b < E ? row : -1;
     }
+  }
+  if (C > 1) {
+    __syncwarp();
+    cluster_wait();
   }
 }
 
