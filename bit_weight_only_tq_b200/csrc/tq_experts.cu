@@ -255,19 +255,20 @@ __device__ __forceinline__ FieldConsts load_field_consts(const uint32_t* c) {
 constexpr int kERows = 128;       // weight rows per item
 constexpr int kEItems = 4;        // item descriptors in flight
 
-template <bool kInt4>
+// Two CTAs per SM with KG = 2, or, for few items (a token's experts), one with KG = 4: an item then has
+// the warps of the whole SM.
+template <bool kInt4, int KG>
 struct SkinnyLayout {
   static constexpr int TM = 8;
-  static constexpr int KG = 2;                         // consumer groups
   static constexpr int kConsumers = 128 * KG;
   static constexpr int kThreads = kConsumers + 32;
-  static constexpr int kCtasPerSm = 2;
+  static constexpr int kCtasPerSm = 4 / KG;
   static constexpr int KS = kInt4 ? 256 : 512;         // k per stage
   static constexpr int kXRow = KS * 2 + 16;            // bytes between rows of x
   static constexpr int kTileW = kERows * 128;
   static constexpr int kTileX = TM * kXRow;
   static constexpr int kPart = TM * 132 * 4;           // one group's sums [TM][132] fp32
-  static constexpr int kRing = 4;
+  static constexpr int kRing = 2 * KG;
   static constexpr int kOffX = kRing * kTileW;
   static constexpr int kOffPart = kOffX + kRing * kTileX;
   static constexpr int kOffBar = kOffPart + KG * kPart;
@@ -276,15 +277,15 @@ struct SkinnyLayout {
   static constexpr int kOffConst = kOffScan + 32 * 4;       // FieldConsts
   static constexpr int kOffFirst = kOffConst + 32;
   static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }  // 1024: alignment
-  static_assert(kRing % KG == 0 && kOffFirst + 1025 * 4 + 1024 <= 113 * 1024, "two CTAs per SM");
+  static_assert(kRing % KG == 0 && kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 / kCtasPerSm, "shared memory");
 };
 
 __device__ __forceinline__ uint32_t sel(bool c, uint32_t a, uint32_t b) { return c ? a : b; }
 
-template <bool kInt4>
-__global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kInt4>::kCtasPerSm)
+template <bool kInt4, int KG>
+__global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayout<kInt4, KG>::kCtasPerSm)
     experts_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w, const ExpertArgs a) {
-  using L = SkinnyLayout<kInt4>;
+  using L = SkinnyLayout<kInt4, KG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
     }
     for (int i = 0; i < kEItems; ++i) {
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], 4 * L::KG);
+      mbar_init(&item_empty[i], 4 * KG);
     }
     store_field_consts(kInt4, reinterpret_cast<uint32_t*>(sm + L::kOffConst));
     fence_mbar_init();
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
   const int nk = static_cast<int>((a.K + L::KS - 1) / L::KS);
   bool ok = true;
 
-  if (warp == L::KG * 4) {
+  if (warp == KG * 4) {
     // ------------------------------------------------------------------ producer
     // The first item's weights are requested before its rows are looked up; their barriers complete
     // with the arrivals that add the rows' bytes.
@@ -414,16 +415,16 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
           }
         }
       };
-      const int kb0 = (kg + L::KG - q0 % L::KG) % L::KG;  // the group's first stage of the item
+      const int kb0 = (kg + KG - q0 % KG) % KG;  // the group's first stage of the item
       if (kInt4 && kb0 < nk) load_scales(kb0);
-      for (int kb = kb0; kb < nk && ok; kb += L::KG) {
+      for (int kb = kb0; kb < nk && ok; kb += KG) {
         const int q = q0 + kb, s = q % L::kRing;
         uint32_t sc_now[4];
         const uint32_t zp_now = zp;
         if (kInt4) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) sc_now[j] = sc[j];
-          if (kb + L::KG < nk) load_scales(kb + L::KG);
+          if (kb + KG < nk) load_scales(kb + KG);
         }
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&full[s], static_cast<uint32_t>(q / L::kRing) & 1u));
         if (!ok) break;
@@ -543,12 +544,12 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
             if (a.bias) eb[c] = __half2float(a.bias[en0 + nn + c]);
           }
         }
-        for (int r = warp; r < it.w; r += 4 * L::KG) {
+        for (int r = warp; r < it.w; r += 4 * KG) {
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if ((rmask >> r) & 1u) {  // a row outside x reads as zeros
             v = *reinterpret_cast<const float4*>(part + r * 132 + 4 * lane);
 #pragma unroll
-            for (int k = 1; k < L::KG; ++k) {
+            for (int k = 1; k < KG; ++k) {
               const float4 u = *reinterpret_cast<const float4*>(part + k * (L::kPart / 4) + r * 132 + 4 * lane);
               v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
             }
@@ -569,23 +570,33 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4>::kThreads, SkinnyLayout<kI
   }
 }
 
-template <bool kInt4>
-static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
-  using L = SkinnyLayout<kInt4>;
+template <bool kInt4, int KG>
+static cudaError_t launch_experts_skinny_t(const ExpertArgs& a, int64_t items, cudaStream_t s) {
+  using L = SkinnyLayout<kInt4, KG>;
   const uint64_t row_bytes = static_cast<uint64_t>(kInt4 ? a.K / 2 : a.K / 4);
   CUtensorMap tw;
   if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, row_bytes, static_cast<uint64_t>(a.E) * a.N, row_bytes, 128,
                     kERows, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  auto* kern = experts_skinny_kernel<kInt4>;
+  auto* kern = experts_skinny_kernel<kInt4, KG>;
   const int smem = L::bytes(a.E);
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  // at most min(R, E + R / TM) chunks
-  const int64_t by_rows = a.E + a.R / L::TM, chunks = a.R < by_rows ? a.R : by_rows;
-  const int64_t items = chunks * ((a.N + kERows - 1) / kERows);
   return launch_pdl(kern, dim3(row_grid(items, 1, L::kCtasPerSm)), dim3(L::kThreads), static_cast<size_t>(smem), 1, s, tw,
                     a);
+}
+
+template <bool kInt4>
+static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
+  // at most min(R, E + R / 8) chunks
+  const int64_t by_rows = a.E + a.R / 8, chunks = a.R < by_rows ? a.R : by_rows;
+  const int64_t items = chunks * ((a.N + kERows - 1) / kERows);
+  // One CTA per SM where its items run in one round, or where they are long (two rounds of short ones
+  // pay their fixed cost twice): 176 items of 28 ternary stages 44 us against 48, of 8 INT4 stages 16.8
+  // against 14.4.
+  const int64_t sms = current_device_info().num_sms, nk = a.K / SkinnyLayout<kInt4, 2>::KS;
+  if (items <= sms || (items <= 2 * sms && nk >= 16)) return launch_experts_skinny_t<kInt4, 4>(a, items, s);
+  return launch_experts_skinny_t<kInt4, 2>(a, items, s);
 }
 
 // ---------------------------------------------------------------------------------------------
