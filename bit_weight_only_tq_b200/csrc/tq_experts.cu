@@ -34,8 +34,9 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, 
 
 // The x row of sorted row r, or -1.
 __device__ __forceinline__ int64_t expert_x_row(const ExpertArgs& a, int64_t r) {
-  const int64_t t = a.order ? a.order[r] / a.top_k : r;
-  return t >= 0 && t < a.X ? t : -1;
+  if (!a.order) return r < a.X ? r : -1;
+  const int slot = a.order[r], t = slot / a.top_k;
+  return slot >= 0 && t < a.X ? t : -1;
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -511,9 +511,9 @@ __global__ void __launch_bounds__(kRowThreads)
   int64_t r = blockIdx.x / parts;
   int slot = r < kept ? order[r] : 0;
   for (; r < kept; r += step) {
-    const int64_t t = slot / k;
+    const int64_t t = slot >= 0 ? slot / k : T_;
     slot = r + step < kept ? order[r + step] : 0;  // the next row's, a row ahead
-    if (t < 0 || t >= T_) continue;
+    if (t >= T_) continue;
     const V* src = x + t * nv;
     V* dst = rows + r * nv;
     for (int v = v0; v < v1; v += 4 * kRowThreads) {

@@ -8,6 +8,7 @@ namespace {
 inline bool moe_dtype_ok(int d) { return d == TQ_F32 || d == TQ_F16 || d == TQ_BF16; }
 inline int moe_elem(int d) { return d == TQ_F32 ? 4 : 2; }
 constexpr int64_t kMoeMaxSlots = (int64_t(1) << 31) - 1;
+constexpr int64_t kMoeMaxRows = (int64_t(1) << 31) - 1024;  // a tile past the last weight row stays an int
 
 // T tokens of top_k choices
 int check_slots(int64_t T, int top_k) {
@@ -31,7 +32,7 @@ int gemm_experts_impl(bool int4, const uint16_t* x, const void* w, const uint16_
                       const uint16_t* bias, uint16_t* y, const int32_t* offsets, const int32_t* order, uint16_t* rows,
                       int64_t X, int64_t R, int64_t E, int64_t N, int64_t K, int top_k, int path, void* stream) {
   if (X < 0 || R < 0 || X > kMoeMaxSlots || R > kMoeMaxSlots) return TQ_ERR_SHAPE;
-  if (E < 1 || E > TQ_MOE_MAX_EXPERTS || N < 0 || N > kMoeMaxSlots / E) return TQ_ERR_SHAPE;
+  if (E < 1 || E > TQ_MOE_MAX_EXPERTS || N < 0 || N > kMoeMaxRows / E) return TQ_ERR_SHAPE;
   if (K <= 0 || K > (int64_t(1) << 28) || top_k < 1) return TQ_ERR_SHAPE;
   if (int4 && K % 128 != 0) return TQ_ERR_SHAPE;
   if (path < TQ_PATH_AUTO || path > TQ_PATH_GENERIC) return TQ_ERR_PATH;

@@ -4,9 +4,8 @@
  *
  * The conventions of tq.h hold (device pointers owned by the caller, row-major contiguous
  * tensors, asynchronous on `stream` and the current device, argument errors returned before
- * anything is launched, no allocation, graph capturable), with one difference: the kernels
- * here read nothing -- weights included -- before the preceding
- * work on the stream has finished.
+ * anything is launched, no allocation, graph capturable), with one difference: the kernels here
+ * read nothing, weights included, before the preceding work on the stream has finished.
  *
  * A layer of E experts, T tokens and top_k choices per token runs
  *
@@ -79,7 +78,7 @@ TQ_API int tq_moe_sort(const int32_t* ids, int32_t* offsets, int32_t* order, int
 
 /* --------------------------------------------------------------------------------------------
  * tq_moe_gather -- rows[r] = x[order[r] / top_k] for r < offsets[E]; rows from offsets[E] on are
- * left as they were.
+ * left as they were, and so is a row whose order is not a slot of the T tokens.
  *   x [T, H], rows [T top_k, H], both of `dtype`, not overlapping; order and offsets from
  *   tq_moe_sort.  Its gradient is tq_moe_combine without weights: dx[t] = sum_j drows[pos[t, j]].
  *
@@ -119,7 +118,7 @@ TQ_API int tq_moe_combine_backward(const void* dout, const void* y, int dtype, c
  *   y        fp16 [R, N], written for r < offsets[E]; later rows are left as they were.  Must
  *            not overlap x.
  *   offsets  int32 [E + 1] (tq_moe_sort): non-decreasing, within [0, R].
- *   order    int32 [R] or NULL; a row(r) outside [0, X) reads as zeros.
+ *   order    int32 [R] or NULL; a negative slot or a row(r) past X reads as zeros.
  *   rows     fp16 [R, K] scratch, 16-byte aligned, or NULL: the PREFILL path with `order` copies the
  *            rows there in sorted order before the product.  Without it AUTO takes the DECODE path
  *            (right, slower), and PREFILL returns TQ_ERR_NULL.  Not read or written otherwise.
@@ -129,7 +128,7 @@ TQ_API int tq_moe_combine_backward(const void* dout, const void* y, int dtype, c
  *            K % 64 == 0 (TQ_ERR_PATH) and 16-byte aligned x, weights and y (TQ_ERR_ALIGN).
  *            Every path is right for any numbers of rows per expert; AUTO goes by the average
  *            R / E, which the host knows.
- * 1 <= E <= 1024, N E < 2^31, 0 < K <= 2^28, top_k >= 1, 0 <= R < 2^31, 0 <= X < 2^31.
+ * 1 <= E <= 1024, N E <= 2^31 - 1024, 0 < K <= 2^28, top_k >= 1, 0 <= R < 2^31, 0 <= X < 2^31.
  * R == 0 or N == 0: nothing is launched.  Errors as in tq_gemm.
  * ------------------------------------------------------------------------------------------ */
 TQ_API int tq_gemm_experts(const uint16_t* x, const uint8_t* packed, const uint16_t* scale,

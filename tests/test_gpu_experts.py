@@ -24,6 +24,10 @@ def _gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 
 
+def _bits16(t):
+    return t.view(torch.int16)
+
+
 def _weights(fmt, E, N, K, seed):
     w = I.weights(E * N, K, seed, device="cuda", outlier_frac=0.0 if fmt == "ternary" else 0.001)
     if fmt == "ternary":
@@ -256,3 +260,89 @@ def test_ternary_many_items_of_odd_stage_counts(K):
     need_cuda()
     for path in (tq.PATH_DECODE, tq.PATH_PREFILL):
         _run("ternary", path, 333, 2, 6, 4500, K, K, True, bias=True, cols=np.arange(0, 4500, 53))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("path", PATHS)
+def test_every_negative_slot_reads_as_zeros(fmt, path):
+    """-1 is no slot of token 0, whatever a division that truncates makes of it."""
+    need_cuda()
+    T, k, E, N, K = 9, 4, 3, 70, 256
+    x, offsets, order, b, xrow = _problem(fmt, T, k, E, N, K, 6, True, True)
+    order = order.clone()
+    order[[0, 5, 6, 20]] = torch.tensor([-1, -3, -4, -2 ** 31], dtype=torch.int32, device="cuda")
+    xrow[[0, 5, 6, 20]] = -1
+    ws = _weights(fmt, E, N, K, 6)
+    y = _call(fmt, x, ws, offsets, order=order, top_k=k, bias=b, path=path)
+    _check(fmt, path, x, ws, b, offsets, y, xrow, K, N)
+
+
+# many rows per expert, beside experts with none or a few: items of 256 weight rows and up to 128 rows of x.  N
+# ending inside an item's first 128 rows, at its middle, inside its second half, odd; K of one stage and of many
+@pytest.mark.parametrize("N,K", [(2056, 128), (2176, 384), (2311, 640), (2424, 896), (2304, 1152)])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("counts", [[0, 1, 33, 700, 257, 513, 256], [1500, 0, 0, 0, 0, 0, 3, 30], [255, 161, 225]])
+def test_many_rows_per_expert(N, K, fmt, counts):
+    need_cuda()
+    ids = torch.cat([torch.full((c,), e, dtype=torch.int32) for e, c in enumerate(counts)])
+    ids = ids[torch.randperm(ids.numel(), generator=torch.Generator().manual_seed(N))].view(-1, 1).cuda()
+    cols = np.unique(np.concatenate([np.arange(0, N, 61), np.arange(N - 140, N)]))
+    _run(fmt, tq.PATH_PREFILL, ids.shape[0], 1, len(counts), N, K, N + K, True, bias=K == 640, ids=ids, cols=cols)
+
+
+@pytest.mark.parametrize("K", [64, 448, 704, 1344])
+def test_ternary_many_rows_per_expert_of_half_stages(K):
+    need_cuda()
+    cols = np.arange(0, 4096, 61)
+    _run("ternary", tq.PATH_PREFILL, 900, 2, 5, 4096, K, K, True, cols=cols)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,K", [(2, 1024), (300, 1024), (900, 512)])
+def test_wait_runs_out_then_recovers(T, K, fmt):
+    """Activation loads switched off and a wait limit of about a millisecond: every wait of the product
+    kernels runs out, the call reports it once, and the next one is as before."""
+    need_cuda()
+    k, E, N = 2, 4, 384 if T < 900 else 4096
+    x, offsets, order, b, _ = _problem(fmt, T, k, E, N, K, 8, True, True)
+    ws = _weights(fmt, E, N, K, 8)
+    run = lambda: _call(fmt, x, ws, offsets, order=order, top_k=k, bias=b)
+    ref = run()
+    assert tq.tq_device_status() == 0
+    assert tq.lib.tq_debug_set_wait_limit(2_000_000) == 0
+    assert tq.lib.tq_debug_skip_activation_loads(1) == 0
+    try:
+        run()
+        assert tq.tq_device_status() == -6
+    finally:
+        assert tq.lib.tq_debug_skip_activation_loads(0) == 0
+        assert tq.lib.tq_debug_set_wait_limit(0) == 0
+    assert tq.tq_device_status() == 0
+    assert torch.equal(_bits16(ref), _bits16(run()))
+    assert tq.tq_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_two_streams_at_once(fmt):
+    """Calls of both kernels on two streams, interleaved: no state is shared between them."""
+    need_cuda()
+    k, E, N, K = 2, 6, 2200, 1024
+    cases = []
+    for T in (3, 500):
+        x, offsets, order, b, _ = _problem(fmt, T, k, E, N, K, T, True, True)
+        ws = _weights(fmt, E, N, K, T)
+        cases.append((lambda s, y=None, x=x, ws=ws, offsets=offsets, order=order, b=b:
+                      _call(fmt, x, ws, offsets, order=order, top_k=k, bias=b, y=y, stream=s)))
+    ref = [c(None) for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    out = [[torch.empty_like(r) for r in ref for _ in range(6)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(12):
+        for j, s in enumerate(streams):
+            c = (i + j) % 2
+            cases[c](s, out[j][6 * c + i // 2])
+    torch.cuda.synchronize()
+    assert tq.tq_device_status() == 0
+    for o in out:
+        for i, y in enumerate(o):
+            assert torch.equal(_bits16(y), _bits16(ref[i // 6]))

@@ -303,3 +303,20 @@ def test_shape_and_type_refusals():
         tq.tq_moe_combine(x, pos, torch.zeros(4, 3, device="cuda"))
     with pytest.raises(ValueError):
         tq.tq_moe_combine_backward(x[:3], x, pos, torch.zeros(4, 2, device="cuda"))
+
+
+@pytest.mark.parametrize("H", [1, 64, 5000])
+def test_gather_leaves_rows_of_no_slot(H):
+    """order entries that are no slot of the tokens (negative, -1 among them, or past the last): row left as it was."""
+    need_cuda()
+    T, k, E = 5, 4, 3
+    _, (offsets, order, pos) = _plan(T, k, E, H, 0.0)
+    order = order.clone()
+    bad = torch.tensor([-1, -3, -2 ** 31, T * k, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    order[[0, 4, 9, 11, 19]] = bad
+    x = torch.randn(T, H, generator=_gen(H), device="cuda")
+    out = tq.tq_moe_gather(x, order, offsets, k, out=torch.full((T * k, H), 7.0, device="cuda"))
+    ok = (order >= 0) & (order < T * k)
+    want = torch.full((T * k, H), 7.0, device="cuda")
+    want[ok] = x[(order[ok] // k).long()]
+    assert torch.equal(out, want)
