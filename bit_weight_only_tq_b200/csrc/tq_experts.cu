@@ -250,8 +250,13 @@ __device__ __forceinline__ FieldConsts load_field_consts(const uint32_t* c) {
 // Bank conflicts: rows of x are 16 bytes apart modulo 128, and lane t's x starts 64 (128) bytes after
 // lane t - 1's: two lanes share banks (four, and so the odd ternary lanes take their words in pairs
 // the other way round).  Ordering the words of all lanes apart took two selects per MMA, more than
-// the shared memory's extra cycles: it is the ALU that bounds this loop.  Weight row of lane group g is (g / 2) + 4 (g % 2), so that the two rows
-// of a quarter-warp access differ in the swizzle's top bit.
+// the shared memory's extra cycles: it is the ALU that bounds this loop.  Weight row of lane group g is
+// (g / 2) + 4 (g % 2), so that the two rows of a quarter-warp access differ in the swizzle's top bit.
+//
+// One row for each of 8 experts, 4096 -> 14336: INT4 65 us, 3.7 TB/s of packed weights and scales,
+// ternary 51 us, 2.3 TB/s; issue 58 and 52 %, ALU 52 and 53 % busy.  A token's 8 of 64 experts,
+// 2048 -> 2816, INT4: 14.4 us, of which the weights' bytes take 3.7: launch, chunk table, first
+// loads and the last sums are not overlapped with anything.
 // ---------------------------------------------------------------------------------------------
 constexpr int kERows = 128;       // weight rows per item
 constexpr int kEItems = 4;        // item descriptors in flight
@@ -630,6 +635,14 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
 // after the slot, so that the issuing warps test one barrier per stage.  The chain from an MMA's end to
 // the next one on the same slot -- barrier wake-ups, tensor memory stores, the test -- takes about 0.8
 // us, and each barrier wait of a decode warp 0.1 to 0.2 us: stages of 64 k lost more to it.
+//
+// 4096 rows, 8 experts, 4096 -> 14336: INT4 402 us (1.20 PFLOP/s), ternary 341 us (1.41); tensor pipe
+// 63 and 73 %, issue 70 and 59 % busy.  A decode warp takes about 3100 (2650) cycles per stage, 1270
+// (750) of them decoding, the rest in the four waits and the sums; the MMAs ask for 2048.  Measured
+// and left out: pairs of CTAs sharing 256 x 256 items (cta_group::2; half the decoding per MMA, but
+// barriers across CTAs: 16384 rows 2044 us against 1729), rows copied in the pairs' order so that no
+// byte permutes are needed (no change), a warp of its own for x's barrier (registers fall to 80).
+// 16384 rows run at the power limit (990 W, 1440 MHz).
 // ---------------------------------------------------------------------------------------------
 constexpr int kTBox = 32;        // sorted rows per x load
 constexpr int kTK = 128;         // k per stage
