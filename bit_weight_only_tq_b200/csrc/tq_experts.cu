@@ -247,6 +247,10 @@ __device__ __forceinline__ FieldConsts load_field_consts(const uint32_t* c) {
 // takes the base (and the zero-point) off, exactly.  x is brought into the same pairs by byte
 // permutes, once per warp for 32 weight rows.
 //
+// An item may also be 64 weight rows with stages of twice the k (wide): the same bytes per stage, two
+// warps on each half of its k, whose sums are added with the groups'.  Half as many stages are in
+// flight then, since x takes twice the room.
+//
 // Bank conflicts: rows of x are 16 bytes apart modulo 128, and lane t's x starts 64 (128) bytes after
 // lane t - 1's: two lanes share banks (four, and so the odd ternary lanes take their words in pairs
 // the other way round).  Ordering the words of all lanes apart took two selects per MMA, more than
@@ -270,11 +274,13 @@ struct SkinnyLayout {
   static constexpr int kThreads = kConsumers + 32;
   static constexpr int kCtasPerSm = 4 / KG;
   static constexpr int KS = kInt4 ? 256 : 512;         // k per stage
+  static constexpr int kLogKS = kInt4 ? 8 : 9;
   static constexpr int kXRow = KS * 2 + 16;            // bytes between rows of x
   static constexpr int kTileW = kERows * 128;
   static constexpr int kTileX = TM * kXRow;
   static constexpr int kPart = TM * 132 * 4;           // one group's sums [TM][132] fp32
-  static constexpr int kRing = 2 * KG;
+  static constexpr int kRing = 2 * KG;                 // stages of an item of 128 weight rows; half for 64
+  static constexpr int kLogRing = KG == 4 ? 3 : 2;
   static constexpr int kOffX = kRing * kTileW;
   static constexpr int kOffPart = kOffX + kRing * kTileX;
   static constexpr int kOffBar = kOffPart + KG * kPart;
@@ -283,14 +289,15 @@ struct SkinnyLayout {
   static constexpr int kOffConst = kOffScan + 32 * 4;       // FieldConsts
   static constexpr int kOffFirst = kOffConst + 32;
   static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }  // 1024: alignment
-  static_assert(kRing % KG == 0 && kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 / kCtasPerSm, "shared memory");
+  static_assert(kRing == 1 << kLogRing && kRing / 2 % KG == 0 && (kRing / 2) * TM * (2 * KS * 2 + 16) <= kRing * kTileX && kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 / kCtasPerSm, "shared memory");
 };
 
 __device__ __forceinline__ uint32_t sel(bool c, uint32_t a, uint32_t b) { return c ? a : b; }
 
 template <bool kInt4, int KG>
 __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayout<kInt4, KG>::kCtasPerSm)
-    experts_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w, const ExpertArgs a) {
+    experts_skinny_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_h,
+                          const ExpertArgs a) {
   using L = SkinnyLayout<kInt4, KG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -317,14 +324,33 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayou
     store_field_consts(kInt4, reinterpret_cast<uint32_t*>(sm + L::kOffConst));
     fence_mbar_init();
     tma_prefetch_desc(&tmap_w);
+    tma_prefetch_desc(&tmap_h);
   }
   pdl_wait_prior_grids();
   const bool skipx = skip_x_loads();  // failure-path test hook: never set in normal use
   expert_chunks(a, L::TM, first, scan, L::kThreads);
-  const int64_t tiles = (a.N + kERows - 1) / kERows;
-  const int64_t total = static_cast<int64_t>(uniform(first[a.E])) * tiles;
-  const int nk = static_cast<int>((a.K + L::KS - 1) / L::KS);
+  // Tall items of 128 weight rows, or wide ones of 64 with stages of twice the k, where those end sooner:
+  // a round of wide items takes half as long (64 tall items of 14336 k: 34.5 -> 21.8 us INT4, 25.3 ->
+  // 15.2 us ternary; 160: 68 -> 57 and 50 -> 43 us).  Numbers of items fit 32 bits by far: y has to fit memory.
+  const uint32_t chunks = static_cast<uint32_t>(uniform(first[a.E])), n32 = static_cast<uint32_t>(a.N);
+  const uint32_t tall = chunks * ((n32 + kERows - 1) / kERows), wides = chunks * ((n32 + kERows / 2 - 1) / (kERows / 2));
+  const int wide = uniform((wides + gridDim.x - 1) / gridDim.x < 2 * ((tall + gridDim.x - 1) / gridDim.x) ? 1 : 0);
+  const int tile_rows = kERows >> wide, ring = L::kRing >> wide, xrow = wide ? 2 * L::KS * 2 + 16 : L::kXRow;
+  const int ks = L::KS << wide;  // k per stage
+  const int64_t tiles = (n32 + tile_rows - 1) >> (7 - wide);
+  const int64_t total = wide ? wides : tall;
+  const int nk = static_cast<int>((static_cast<uint32_t>(a.K) + ks - 1) >> (L::kLogKS + wide));
   bool ok = true;
+  // A stage's weights: 128 rows x 128 bytes, or (wide) two boxes of 64 rows side by side.
+  auto load_weights = [&](int s, int kb, int wrow) {
+    uint8_t* dst = sm + s * L::kTileW;
+    if (wide) {
+      tma_load_2d(dst, &tmap_h, &full[s], kb * 256, wrow);
+      tma_load_2d(dst + L::kTileW / 2, &tmap_h, &full[s], kb * 256 + 128, wrow);
+    } else {
+      tma_load_2d(dst, &tmap_w, &full[s], kb * 128, wrow);
+    }
+  };
 
   if (warp == KG * 4) {
     // ------------------------------------------------------------------ producer
@@ -333,11 +359,11 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayou
     int q = 0, n = 0;
     for (int64_t item = blockIdx.x; item < total && ok; item += gridDim.x, ++n) {
       const ExpertItem it = expert_item<false>(a, first, item, tiles, L::TM);
-      const int wrow = static_cast<int>(static_cast<int64_t>(it.e) * a.N + static_cast<int64_t>(it.tile) * kERows);
-      const int early = n == 0 ? (nk < L::kRing ? nk : L::kRing) : 0;
+      const int wrow = static_cast<int>(static_cast<int64_t>(it.e) * a.N + static_cast<int64_t>(it.tile) * tile_rows);
+      const int early = n == 0 ? (nk < ring ? nk : ring) : 0;
       if (lane < early) {
         mbar_expect_tx(&full[lane], L::kTileW);
-        tma_load_2d(sm + lane * L::kTileW, &tmap_w, &full[lane], lane * 128, wrow);
+        load_weights(lane, lane, wrow);
       }
       __syncwarp();
       int64_t xr = -1;
@@ -354,24 +380,26 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayou
         mbar_arrive(&item_full[d]);
       }
       for (int kb = 0; kb < nk && ok; ++kb, ++q) {
-        const int s = q % L::kRing;
-        if (q >= L::kRing) ok = mbar_wait_relaxed(&empty[s], static_cast<uint32_t>(q / L::kRing - 1) & 1u);
+        const int s = q & (ring - 1), lap = q >> (L::kLogRing - wide);
+        if (q >= ring) ok = mbar_wait_relaxed(&empty[s], static_cast<uint32_t>(lap - 1) & 1u);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        const int64_t k0 = static_cast<int64_t>(kb) * L::KS;
-        const uint32_t xb = static_cast<uint32_t>((a.K - k0 < L::KS ? a.K - k0 : L::KS) * 2);
+        const int64_t k0 = static_cast<int64_t>(kb) * ks;
+        const uint32_t xb = static_cast<uint32_t>((a.K - k0 < ks ? a.K - k0 : ks) * 2);
         if (lane == 0) {
           mbar_arrive_expect_tx(&full[s], (kb >= early ? L::kTileW : 0) + __popc(mask) * xb);
-          if (kb >= early) tma_load_2d(sm + s * L::kTileW, &tmap_w, &full[s], kb * 128, wrow);
+          if (kb >= early) load_weights(s, kb, wrow);
         }
         __syncwarp();
         if (xr >= 0 && !skipx)
-          bulk_load_1d(sm + L::kOffX + s * L::kTileX + lane * L::kXRow, src + k0 * 2, xb, &full[s]);
+          bulk_load_1d(sm + L::kOffX + (s * L::TM + lane) * xrow, src + k0 * 2, xb, &full[s]);
       }
     }
   } else {
     // ------------------------------------------------------------------ consumers
     const int kg = warp >> 2, rg = warp & 3;
+    // the warp's first weight row in the tile, and (wide) which half of the stage's k it takes
+    const int wr0 = wide ? (rg & 1) * 32 : rg * 32, kh = wide ? rg >> 1 : 0;
     const int g = lane >> 2, t = lane & 3;
     const int pg = (g >> 1) | ((g & 1) << 2);  // weight row of this lane group within 8
     const int64_t G = a.K >> 7;
@@ -391,7 +419,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayou
       const uint32_t rmask = static_cast<uint32_t>(items[d * 2 + 1].x);
       __syncwarp();
       if (lane == 0) mbar_arrive(&item_empty[d]);
-      const int64_t n0 = static_cast<int64_t>(it.y) * kERows;
+      const int64_t n0 = static_cast<int64_t>(it.y) * tile_rows;
       const int64_t en0 = static_cast<int64_t>(it.x) * a.N;
       // the group scales (and zero-points) of this lane's four weight rows, loaded one of the
       // group's stages ahead: two fp16 per register, the eight zero-points as nibbles of one
@@ -400,12 +428,13 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayou
       int rowG[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = rg * 32 + 8 * j + pg;
+        const int r = wr0 + 8 * j + pg;
         rowG[j] = ok && n0 + r < a.N ? static_cast<int>(r * G) : 0;  // past N: any scale, not stored
       }
       uint32_t sc[4] = {0u, 0u, 0u, 0u}, zp = 0x88888888u;
       auto load_scales = [&](int kb) {
-        const int g0 = 2 * kb;
+        const int g0 = 2 * ((kb << wide) + kh);
+        if (g0 >= G) return;  // nothing of the stage in this half
         const bool two = g0 + 1 < G;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -424,7 +453,7 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayou
       const int kb0 = (kg + KG - q0 % KG) % KG;  // the group's first stage of the item
       if (kInt4 && kb0 < nk) load_scales(kb0);
       for (int kb = kb0; kb < nk && ok; kb += KG) {
-        const int q = q0 + kb, s = q % L::kRing;
+        const int q = q0 + kb, s = q & (ring - 1), lap = q >> (L::kLogRing - wide);
         uint32_t sc_now[4];
         const uint32_t zp_now = zp;
         if (kInt4) {
@@ -432,13 +461,13 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayou
           for (int j = 0; j < 4; ++j) sc_now[j] = sc[j];
           if (kb + KG < nk) load_scales(kb + KG);
         }
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&full[s], static_cast<uint32_t>(q / L::kRing) & 1u));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_warp(&full[s], static_cast<uint32_t>(lap) & 1u));
         if (!ok) break;
-        const uint8_t* wt = sm + s * L::kTileW + (rg * 32 + pg) * 128;
-        const uint8_t* xt = sm + L::kOffX + s * L::kTileX + g * L::kXRow;
+        const uint8_t* wt = sm + s * L::kTileW + (rg * 32 + pg) * 128;  // either way: two boxes of 64 rows
+        const uint8_t* xt = sm + L::kOffX + (s * L::TM + g) * xrow + kh * (L::KS * 2);
         // 16-byte chunks of a row that hold weights: all eight but in the last stage
-        const int64_t left = a.K - static_cast<int64_t>(kb) * L::KS;
-        const int live = left >= L::KS ? 8 : static_cast<int>(left / (kInt4 ? 32 : 64));
+        const int64_t left = a.K - static_cast<int64_t>(kb) * ks - kh * L::KS;
+        const int live = left >= L::KS ? 8 : (left > 0 ? static_cast<int>(left / (kInt4 ? 32 : 64)) : 0);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (4 * i >= live) break;
@@ -560,6 +589,13 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayou
               v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
             }
           }
+          if (wide) {  // the halves of k: rows 0-63 of the tile in both halves of the columns
+            v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, 16);
+            v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, 16);
+            v.z += __shfl_xor_sync(0xFFFFFFFFu, v.z, 16);
+            v.w += __shfl_xor_sync(0xFFFFFFFFu, v.w, 16);
+            if (lane >= 16) continue;
+          }
           __half o[4] = {__float2half_rn(fmaf(v.x, es[0], eb[0])), __float2half_rn(fmaf(v.y, es[1], eb[1])),
                          __float2half_rn(fmaf(v.z, es[2], eb[2])), __float2half_rn(fmaf(v.w, es[3], eb[3]))};
           __half* dst = a.y + (static_cast<int64_t>(it.z) + r) * a.N + nn;
@@ -580,16 +616,19 @@ template <bool kInt4, int KG>
 static cudaError_t launch_experts_skinny_t(const ExpertArgs& a, int64_t items, cudaStream_t s) {
   using L = SkinnyLayout<kInt4, KG>;
   const uint64_t row_bytes = static_cast<uint64_t>(kInt4 ? a.K / 2 : a.K / 4);
-  CUtensorMap tw;
-  if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, row_bytes, static_cast<uint64_t>(a.E) * a.N, row_bytes, 128,
-                    kERows, CU_TENSOR_MAP_SWIZZLE_128B))
+  const uint64_t wrows = static_cast<uint64_t>(a.E) * a.N;
+  CUtensorMap tw, th;
+  if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, row_bytes, wrows, row_bytes, 128, kERows,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&th, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, row_bytes, wrows, row_bytes, 128, kERows / 2,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   auto* kern = experts_skinny_kernel<kInt4, KG>;
   const int smem = L::bytes(a.E);
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(row_grid(items, 1, L::kCtasPerSm)), dim3(L::kThreads), static_cast<size_t>(smem), 1, s, tw,
-                    a);
+  return launch_pdl(kern, dim3(row_grid(2 * items, 1, L::kCtasPerSm)), dim3(L::kThreads), static_cast<size_t>(smem), 1, s, tw,
+                    th, a);
 }
 
 template <bool kInt4>
@@ -598,8 +637,8 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
   const int64_t by_rows = a.E + a.R / 8, chunks = a.R < by_rows ? a.R : by_rows;
   const int64_t items = chunks * ((a.N + kERows - 1) / kERows);
   // One CTA per SM where its items run in one round, or where they are long (two rounds of short ones
-  // pay their fixed cost twice): 176 items of 28 ternary stages 44 us against 48, of 8 INT4 stages 16.8
-  // against 14.4.
+  // pay their fixed cost twice): 176 items of 28 ternary stages 44 us against 48, before wide items took
+  // them to 39, of 8 INT4 stages with zero-points 16.6 against 14.6.
   const int64_t sms = current_device_info().num_sms, nk = a.K / SkinnyLayout<kInt4, 2>::KS;
   if (items <= sms || (items <= 2 * sms && nk >= 16)) return launch_experts_skinny_t<kInt4, 4>(a, items, s);
   return launch_experts_skinny_t<kInt4, 2>(a, items, s);
