@@ -145,11 +145,13 @@ int tq_experts_path(int fmt, int64_t R, int64_t E, int64_t N, int64_t K, int ali
   if (R < 0 || E < 1 || N < 0 || K <= 0) return TQ_ERR_SHAPE;
   if (fmt == TQ_FMT_W4G128 && K % 128 != 0) return TQ_ERR_SHAPE;
   if (R == 0 || N == 0 || !aligned || K % 64 != 0) return TQ_PATH_GENERIC;
-  // The crossover by rows per expert of an even spread, the only such number the host knows: at 2 / 4 /
-  // 8 rows the decode kernel takes 65 / 81 / 116 us and the tensor-core kernel 82 / 87 / 98 us (INT4, 8
-  // experts of 4096 -> 14336; ternary 53 / 64 / 90 and 62 / 66 / 74 us).  One pass of the decode kernel
-  // covers 8 rows, so no more than 8 rows in all always take it.
-  return R <= 8 || R <= 4 * E ? TQ_PATH_DECODE : TQ_PATH_PREFILL;
+  // The crossover by rows per expert on average, the only such number the host knows (evenly random
+  // routing, INT4): at 4 / 6 / 8 / 10 rows the decode kernel takes 67 / 70 / 77 / 112 us and the tensor-core
+  // kernel 96 / 97 / 97 / 97 us with 8 experts of 4096 -> 14336, 52 / 57 / 72 / 81 and 68 / 69 / 69 / 69 us
+  // with 64 of 2048 -> 2816, 42 / 49 / 60 / 59 and 53 / 54 / 54 / 54 us with 32 of 4096 -> 2048; ternary
+  // crosses at the same numbers.  One pass of the decode kernel covers 8 rows, so no more than 8 rows in
+  // all always take it.
+  return R <= 8 || R <= 6 * E ? TQ_PATH_DECODE : TQ_PATH_PREFILL;
 }
 
 }  // extern "C"
