@@ -93,11 +93,13 @@ def _raw(stream, dev):
 
 
 def _empty(like, shape, dtype, stream):
-    """An output, allocated for the stream that writes it."""
+    """A contiguous output of one or two dims, allocated for the stream that writes it (empty_strided takes
+    the host 1.6 us, new_empty 2.0)."""
+    stride = (shape[1], 1) if len(shape) == 2 else (1,)
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty_strided(shape, stride, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty_strided(shape, stride, dtype=dtype, device=like.device)
 
 
 def _shape2(t, name, ndim=2):

@@ -346,3 +346,24 @@ def test_two_streams_at_once(fmt):
     for o in out:
         for i, y in enumerate(o):
             assert torch.equal(_bits16(y), _bits16(ref[i // 6]))
+
+
+# few items: 64 weight rows each, in stages of twice the k.  N around multiples of 64 and 128; K that ends in the
+# first half of such a stage, in its second half, and at either's end
+@pytest.mark.parametrize("N", [1, 63, 64, 65, 127, 191, 4033])
+@pytest.mark.parametrize("fmt,K", [("w4", 128), ("w4z", 384), ("w4", 640), ("w4z", 896), ("w4", 2176), ("ternary", 64),
+                                   ("ternary", 512), ("ternary", 576), ("ternary", 1536), ("ternary", 1600),
+                                   ("ternary", 4160)])
+def test_few_items(N, fmt, K):
+    need_cuda()
+    cols = None if N < 1000 else np.unique(np.concatenate([np.arange(0, N, 53), np.arange(N - 70, N)]))
+    _run(fmt, tq.PATH_DECODE, 2, 2, 3, N, K, N + K, True, bias=N % 2 == 1, cols=cols)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("E,N", [(1024, 96), (700, 257)])
+def test_many_experts(E, N, fmt):
+    """A token each for most experts, several for a few, none for the rest."""
+    need_cuda()
+    for path in (tq.PATH_DECODE, tq.PATH_PREFILL):
+        _run(fmt, path, 300, 4, E, N, 256, E, True)
