@@ -281,6 +281,7 @@ struct SkinnyLayout {
   static constexpr int kPart = TM * 132 * 4;           // one group's sums [TM][132] fp32
   static constexpr int kRing = 2 * KG;                 // stages of an item of 128 weight rows; half for 64
   static constexpr int kLogRing = KG == 4 ? 3 : 2;
+  static constexpr bool kWide = KG == 4;
   static constexpr int kOffX = kRing * kTileW;
   static constexpr int kOffPart = kOffX + kRing * kTileX;
   static constexpr int kOffBar = kOffPart + KG * kPart;
@@ -289,7 +290,9 @@ struct SkinnyLayout {
   static constexpr int kOffConst = kOffScan + 32 * 4;       // FieldConsts
   static constexpr int kOffFirst = kOffConst + 32;
   static constexpr int bytes(int E) { return kOffFirst + (E + 1) * 4 + 1024; }  // 1024: alignment
-  static_assert(kRing == 1 << kLogRing && kRing / 2 % KG == 0 && (kRing / 2) * TM * (2 * KS * 2 + 16) <= kRing * kTileX && kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 / kCtasPerSm, "shared memory");
+  static_assert(kRing == 1 << kLogRing && kRing % KG == 0, "ring");
+  static_assert(!kWide || (kRing / 2 % KG == 0 && kRing / 2 * TM * (2 * KS * 2 + 16) <= kRing * kTileX), "wide items");
+  static_assert(kOffFirst + 1025 * 4 + 1024 <= 227 * 1024 / kCtasPerSm, "shared memory");
 };
 
 __device__ __forceinline__ uint32_t sel(bool c, uint32_t a, uint32_t b) { return c ? a : b; }
@@ -331,10 +334,12 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayou
   expert_chunks(a, L::TM, first, scan, L::kThreads);
   // Tall items of 128 weight rows, or wide ones of 64 with stages of twice the k, where those end sooner:
   // a round of wide items takes half as long (64 tall items of 14336 k: 34.5 -> 21.8 us INT4, 25.3 ->
-  // 15.2 us ternary; 160: 68 -> 57 and 50 -> 43 us).  Numbers of items fit 32 bits by far: y has to fit memory.
+  // 15.2 us ternary; 160: 68 -> 57 and 50 -> 43 us).  Not with two CTAs per SM, which share it unevenly where
+  // one has an item more (896 items of 4096 k: 65 -> 70 us INT4).  Numbers of items fit 32 bits by far: y has
+  // to fit memory.
   const uint32_t chunks = static_cast<uint32_t>(uniform(first[a.E])), n32 = static_cast<uint32_t>(a.N);
   const uint32_t tall = chunks * ((n32 + kERows - 1) / kERows), wides = chunks * ((n32 + kERows / 2 - 1) / (kERows / 2));
-  const int wide = uniform((wides + gridDim.x - 1) / gridDim.x < 2 * ((tall + gridDim.x - 1) / gridDim.x) ? 1 : 0);
+  const int wide = L::kWide && uniform((wides + gridDim.x - 1) / gridDim.x < 2 * ((tall + gridDim.x - 1) / gridDim.x));
   const int tile_rows = kERows >> wide, ring = L::kRing >> wide, xrow = wide ? 2 * L::KS * 2 + 16 : L::kXRow;
   const int ks = L::KS << wide;  // k per stage
   const int64_t tiles = (n32 + tile_rows - 1) >> (7 - wide);
@@ -627,7 +632,7 @@ static cudaError_t launch_experts_skinny_t(const ExpertArgs& a, int64_t items, c
   const int smem = L::bytes(a.E);
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(row_grid(2 * items, 1, L::kCtasPerSm)), dim3(L::kThreads), static_cast<size_t>(smem), 1, s, tw,
+  return launch_pdl(kern, dim3(row_grid(L::kWide ? 2 * items : items, 1, L::kCtasPerSm)), dim3(L::kThreads), static_cast<size_t>(smem), 1, s, tw,
                     th, a);
 }
 
