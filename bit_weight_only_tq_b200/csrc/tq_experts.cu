@@ -257,9 +257,9 @@ __device__ __forceinline__ FieldConsts load_field_consts(const uint32_t* c) {
 // the shared memory's extra cycles: it is the ALU that bounds this loop.  Weight row of lane group g is
 // (g / 2) + 4 (g % 2), so that the two rows of a quarter-warp access differ in the swizzle's top bit.
 //
-// One row for each of 8 experts, 4096 -> 14336: INT4 65 us, 3.7 TB/s of packed weights and scales,
+// One row for each of 8 experts, 4096 -> 14336: INT4 62 us, 3.9 TB/s of packed weights and scales,
 // ternary 51 us, 2.3 TB/s; issue 58 and 52 %, ALU 52 and 53 % busy.  A token's 8 of 64 experts,
-// 2048 -> 2816, INT4: 14.4 us, of which the weights' bytes take 3.7: launch, chunk table, first
+// 2048 -> 2816, INT4 with zero-points: 13.2 us, of which the weights' bytes take 3.7: launch, chunk table, first
 // loads and the last sums are not overlapped with anything.
 // ---------------------------------------------------------------------------------------------
 constexpr int kERows = 128;       // weight rows per item
@@ -409,6 +409,9 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayou
     const int pg = (g >> 1) | ((g & 1) << 2);  // weight row of this lane group within 8
     const int64_t G = a.K >> 7;
     const bool odd = (t & 1) != 0;
+    // two groups' scales (zero-points) in one load: whole pairs per row, aligned
+    const bool pairs = (G & 1) == 0 && (reinterpret_cast<uintptr_t>(a.sc) & 3u) == 0 &&
+                       (reinterpret_cast<uintptr_t>(a.zp) & 1u) == 0;
     const FieldConsts fc = load_field_consts(reinterpret_cast<const uint32_t*>(sm + L::kOffConst));
     float* part = reinterpret_cast<float*>(sm + L::kOffPart);
     int q0 = 0, n = 0;  // stages before this item; items before it
@@ -440,6 +443,19 @@ __global__ void __launch_bounds__(SkinnyLayout<kInt4, KG>::kThreads, SkinnyLayou
       auto load_scales = [&](int kb) {
         const int g0 = 2 * ((kb << wide) + kh);
         if (g0 >= G) return;  // nothing of the stage in this half
+        if (pairs) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sc[j] = *reinterpret_cast<const uint32_t*>(sct + rowG[j] + g0);
+          if (zpt) {
+            zp = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t z = *reinterpret_cast<const uint16_t*>(zpt + rowG[j] + g0);
+              zp |= ((z & 15u) | ((z >> 4) & 0xF0u)) << (8 * j);
+            }
+          }
+          return;
+        }
         const bool two = g0 + 1 < G;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

@@ -367,3 +367,23 @@ def test_many_experts(E, N, fmt):
     need_cuda()
     for path in (tq.PATH_DECODE, tq.PATH_PREFILL):
         _run(fmt, path, 300, 4, E, N, 256, E, True)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("K", [512, 640])
+def test_scales_and_zeros_of_least_alignment(path, fmt, K):
+    """Scales, zero-points and bias may start at any element: only x, weights and y are 16-byte aligned."""
+    need_cuda()
+    T, k, E, N = 20, 2, 4, 333
+    x, offsets, order, b, xrow = _problem(fmt, T, k, E, N, K, K, True, True)
+
+    def shifted(t):
+        return None if t is None else torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)
+
+    ws = _weights(fmt, E, N, K, K)
+    off = (ws[0], shifted(ws[1]), shifted(ws[2]))
+    assert off[1].data_ptr() % 4 == 2 and (off[2] is None or off[2].data_ptr() % 2 == 1)
+    y = _call(fmt, x, off, offsets, order=order, top_k=k, bias=shifted(b), path=path)
+    assert tq.tq_device_status() == 0
+    _check(fmt, path, x, ws, b, offsets, y, xrow, K, N)
