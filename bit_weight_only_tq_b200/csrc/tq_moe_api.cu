@@ -146,12 +146,11 @@ int tq_experts_path(int fmt, int64_t R, int64_t E, int64_t N, int64_t K, int ali
   if (fmt == TQ_FMT_W4G128 && K % 128 != 0) return TQ_ERR_SHAPE;
   if (R == 0 || N == 0 || !aligned || K % 64 != 0) return TQ_PATH_GENERIC;
   // The crossover by rows per expert on average, the only such number the host knows (evenly random
-  // routing, INT4): at 4 / 6 / 8 / 10 rows the decode kernel takes 67 / 70 / 77 / 112 us and the tensor-core
-  // kernel 96 / 97 / 97 / 97 us with 8 experts of 4096 -> 14336, 52 / 57 / 72 / 81 and 68 / 69 / 69 / 69 us
-  // with 64 of 2048 -> 2816, 42 / 49 / 60 / 59 and 53 / 54 / 54 / 54 us with 32 of 4096 -> 2048; ternary
-  // crosses at the same numbers.  One pass of the decode kernel covers 8 rows, so no more than 8 rows in
-  // all always take it.
-  return R <= 8 || R <= 6 * E ? TQ_PATH_DECODE : TQ_PATH_PREFILL;
+  // routing, INT4): at 4 / 6 / 8 / 10 rows the decode kernel takes 63 / 72 / 72 / 105 us and the tensor-core
+  // kernel 96 us with 8 experts of 4096 -> 14336, 50 / 56 / 68 / 77 and 68 to 69 us with 64 of 2048 -> 2816,
+  // 40 / 46 / 56 / 56 and 53 to 54 us with 32 of 4096 -> 2048; ternary crosses at the same numbers.  One pass
+  // of the decode kernel covers 8 rows.
+  return R <= 8 * E ? TQ_PATH_DECODE : TQ_PATH_PREFILL;
 }
 
 }  // extern "C"

@@ -100,9 +100,9 @@ def test_experts_path_rule():
     assert tq.tq_experts_path(T, 8, 4, 64, 64, aligned=False) == tq.PATH_GENERIC
     assert tq.tq_experts_path(W, 8, 4, 64, 192) == -2
     for f in (T, W):
-        for R, E in ((1, 1), (8, 1), (8, 8), (48, 8), (384, 64)):
+        for R, E in ((1, 1), (8, 1), (8, 8), (64, 8), (512, 64)):
             assert tq.tq_experts_path(f, R, E, 1000, 1024) == tq.PATH_DECODE
-        for R, E in ((9, 1), (49, 8), (385, 64), (16384, 8)):
+        for R, E in ((9, 1), (65, 8), (513, 64), (16384, 8)):
             assert tq.tq_experts_path(f, R, E, 1000, 1024) == tq.PATH_PREFILL
     assert tq.tq_experts_path(5, 8, 4, 64, 128) == -8
     assert tq.tq_experts_path(T, -1, 4, 64, 128) == -2
