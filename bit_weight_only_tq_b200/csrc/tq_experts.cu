@@ -257,8 +257,8 @@ __device__ __forceinline__ FieldConsts load_field_consts(const uint32_t* c) {
 // the shared memory's extra cycles: it is the ALU that bounds this loop.  Weight row of lane group g is
 // (g / 2) + 4 (g % 2), so that the two rows of a quarter-warp access differ in the swizzle's top bit.
 //
-// One row for each of 8 experts, 4096 -> 14336: INT4 62 us, 3.9 TB/s of packed weights and scales,
-// ternary 51 us, 2.3 TB/s; issue 58 and 52 %, ALU 52 and 53 % busy.  A token's 8 of 64 experts,
+// One row for each of 8 experts, 4096 -> 14336: INT4 61 us, 4.0 TB/s of packed weights and scales,
+// ternary 51 us, 2.3 TB/s; issue 56 and 52 %, ALU 50 and 53 % busy.  A token's 8 of 64 experts,
 // 2048 -> 2816, INT4 with zero-points: 13.2 us, of which the weights' bytes take 3.7: launch, chunk table, first
 // loads and the last sums are not overlapped with anything.
 // ---------------------------------------------------------------------------------------------
