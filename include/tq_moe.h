@@ -122,6 +122,7 @@ TQ_API int tq_moe_combine_backward(const void* dout, const void* y, int dtype, c
  *   rows     fp16 [R, K] scratch, 16-byte aligned, or NULL: the PREFILL path with `order` copies the
  *            rows there in sorted order before the product.  Without it AUTO takes the DECODE path
  *            (right, slower), and PREFILL returns TQ_ERR_NULL.  Not read or written otherwise.
+ *            Calls (or captured graphs) that may run at once need a scratch each.
  *   path     TQ_PATH_AUTO, or one path (tests): DECODE takes few rows per expert (mma.sync on
  *            in-register decode, up to 8 rows of an expert per pass over its weights), PREFILL
  *            many (tcgen05.mma), GENERIC any shape and alignment.  DECODE and PREFILL need
