@@ -249,7 +249,9 @@ def w4g_gemm_experts(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tenso
                      order=None, top_k: int = 1, bias=None, y=None, path: int = PATH_AUTO,
                      stream=None, rows=None) -> torch.Tensor:
     """tq_gemm_experts with W4A16 weights: qweight int32 [E, N, K/8], scales fp16 [E, N, K/128], zeros
-    uint8 [E, N, K/128] or None (symmetric)."""
+    uint8 [E, N, K/128] or None (symmetric).  PATH_PREFILL, which PATH_AUTO takes for many rows per expert,
+    rounds each weight (u - z) * s to fp16 (infinite from 65520: scales up to 4364 are safe); PATH_DECODE
+    and PATH_GENERIC round no weight."""
     dev = _device()
     E, N, _ = _shape2(qweight, "qweight", 3)
     K = _shape2(x, "x")[1]

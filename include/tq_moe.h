@@ -21,7 +21,8 @@
  * the ids): it is sorted last, has position -1, and takes part in nothing.
  *
  * Types: TQ_F32, TQ_F16 and TQ_BF16 for scores and rows (`dtype`); the products are fp16 as in
- * tq.h.  Sums are in fp32; every output is rounded once.
+ * tq.h.  Sums are in fp32; every output is rounded once.  The one rounding besides is that of the
+ * INT4 weights on the PREFILL path (below).
  */
 #ifndef TQ_MOE_H
 #define TQ_MOE_H
@@ -106,7 +107,11 @@ TQ_API int tq_moe_combine_backward(const void* dout, const void* y, int dtype, c
  * tq_gemm_experts / w4g_gemm_experts -- each expert's rows times its packed weights: for
  * e < E and offsets[e] <= r < offsets[e + 1],
  *     y[r, :] = x[row(r), :] . What_e^T (+ bias[e, :]),     row(r) = order ? order[r] / top_k : r
- * What_e as in tq_gemm / w4g_gemm / w4g_gemm_zp (same formats, fp32 accumulation, one rounding).
+ * What_e as in tq_gemm / w4g_gemm / w4g_gemm_zp (same formats, fp32 accumulation).  Weights enter the
+ * sum exactly and the result is rounded once, except on the PREFILL path of w4g_gemm_experts: there, as
+ * on that of w4g_gemm, each weight (u - z) s is rounded to fp16 first (2^-11 of its value at most), and
+ * one of 65520 and above becomes infinite, so that scales must keep |(u - z) s| below that: any scale up
+ * to 4364 does.  AUTO may take that path; DECODE and GENERIC take any scale and round no weight.
  *
  *   x        fp16 [X, K]: X = T tokens with `order`, X = R sorted rows without.
  *   packed   ternary uint8 [E, N, ceil(K/4)] (tq_quantize_pack of the [E N, K] matrix)

@@ -1,0 +1,138 @@
+"""Experts' products at the ends of what their header allows, against the fp64 oracle.
+
+Tolerance per element, S = sum |x w|: half an fp16 step of the result (2^-11 |y|, 2^-25 among the
+subnormals); products are exact in fp32 and summed in fp32, at most K / 8 + 64 roundings of the running
+sum along the longest chain of any path, each 2^-23 of at most S; where the PREFILL path is taken, and
+only there, each INT4 weight rounded to fp16 (2^-11 S).
+"""
+import numpy as np
+import pytest
+import torch
+
+import bit_weight_only_tq_b200 as tq
+import oracle as O
+import tq_inputs as I
+from gpu_util import bits, check_canaries, f16np, gpu, guarded_empty, need_cuda
+
+pytestmark = gpu
+FORMATS = ["ternary", "w4", "w4z"]
+PATHS = [tq.PATH_AUTO, tq.PATH_GENERIC, tq.PATH_DECODE, tq.PATH_PREFILL]
+
+
+def _call(fmt, x, ws, offsets, **kw):
+    if fmt == "ternary":
+        return tq.tq_gemm_experts(x, ws[0], ws[1], offsets, **kw)
+    return tq.w4g_gemm_experts(x, ws[0], ws[1], offsets, zeros=ws[2], **kw)
+
+
+def _taken(fmt, path, R, E, N, K):
+    """The path that a call takes."""
+    f = tq.FMT_TERNARY if fmt == "ternary" else tq.FMT_W4G128
+    return tq.tq_experts_path(f, R, E, N, K) if path == tq.PATH_AUTO else path
+
+
+def _what(fmt, ws, e, K, cols):
+    """Rows `cols` of expert e's weights in fp64."""
+    q, s = ws[0][e][cols].cpu().numpy(), bits(ws[1][e][cols])
+    if fmt == "ternary":
+        return O.tq_unpack(q, s, K)
+    if ws[2] is None:
+        return O.w4g_unpack(q, s)
+    return O.w4z_unpack(q, s, ws[2][e][cols].cpu().numpy(), np.arange(K) // 128)
+
+
+def _tol(fmt, taken, ref, S, K):
+    rel = (K / 8 + 64) * 2.0 ** -23 + (2.0 ** -11 if fmt != "ternary" and taken == tq.PATH_PREFILL else 0.0)
+    return 2.0 ** -11 * (1 + 2.0 ** -10) * np.abs(ref) + rel * S + 2.0 ** -25
+
+
+def _check(fmt, path, x, ws, offsets, y, xrow, bias=None, cols=None):
+    """Every row of every expert against the oracle, at the weight rows `cols`."""
+    off, (R, N), K, E = offsets.cpu().numpy(), y.shape, x.shape[1], ws[0].shape[0]
+    taken = _taken(fmt, path, R, E, N, K)
+    cols = np.arange(N) if cols is None else cols
+    xn, yn = f16np(x).astype(np.float64), f16np(y).astype(np.float64)
+    for e in range(E):
+        rows = np.arange(off[e], off[e + 1])
+        if rows.size == 0:
+            continue
+        W = _what(fmt, ws, e, K, cols)
+        xs = xn[xrow[rows]]
+        ref, S = xs @ W.T, np.abs(xs) @ np.abs(W).T
+        if bias is not None:
+            b = f16np(bias)[e][cols].astype(np.float64)
+            ref, S = ref + b, S + np.abs(b)
+        err, tol = np.abs(yn[np.ix_(rows, cols)] - ref), _tol(fmt, taken, ref, S, K)
+        assert np.all(err <= tol), (fmt, path, e, float((err - tol).max()), np.argwhere(~(err <= tol))[:4])
+
+
+def _word(codes):
+    """Words of eight 4-bit codes, the first in the lowest bits."""
+    u = torch.as_tensor(codes, dtype=torch.int64).view(*np.shape(codes)[:-1], -1, 8)
+    q = (u << torch.arange(0, 32, 4)).sum(-1)
+    return torch.where(q >= 2 ** 31, q - 2 ** 32, q).to(torch.int32)
+
+
+# ------------------------------------------------------------------------- INT4 weights on each path
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("T", [1, 5, 40])
+@pytest.mark.parametrize("path", PATHS)
+def test_int4_weights_are_rounded_on_the_prefill_path_only(path, T, zeros):
+    """Products that cancel exactly, (7 s)(-3) + (3 s)(7), for scales whose multiples 7 s and 3 s are no
+    fp16 numbers: 0 wherever weights stay exact (every partial sum is one of integers times s, below 2^24),
+    and within the rounding of the weights on the PREFILL path."""
+    need_cuda()
+    E, N, K = 2, 70, 256
+    z = 6 if zeros else 8
+    codes = np.tile(np.array([z + 7, z + 3]), (E, N, K // 2))
+    ws = (_word(codes).cuda(), (0.5 + (2 * torch.arange(E * N * 2) + 1) * 2.0 ** -11).half().view(E, N, 2).cuda(),
+          torch.full((E, N, 2), z, dtype=torch.uint8, device="cuda") if zeros else None)
+    x = torch.tensor([-3.0, 7.0]).repeat(2 * T, K // 2).half().cuda()
+    offsets = torch.tensor([0, T, 2 * T], dtype=torch.int32, device="cuda")
+    y = _call("w4", x, ws, offsets, path=path)
+    assert tq.tq_device_status() == 0
+    if _taken("w4", path, 2 * T, E, N, K) == tq.PATH_PREFILL:
+        _check("w4", path, x, ws, offsets, y, np.arange(2 * T))
+    else:
+        assert (y == 0).all()
+
+
+@pytest.mark.parametrize("path,scale", [(p, 4364.0) for p in PATHS] + [(p, s) for p in (tq.PATH_GENERIC, tq.PATH_DECODE)
+                                                                       for s in (4368.0, 30000.0, 65504.0)])
+def test_int4_scales_up_to_the_documented_limit(path, scale):
+    """15 * 4364 = 65460 rounds to 65472, below the largest fp16, 65504; the next scale, 4368, gives 65520,
+    which rounds to infinity.  The paths that round no weight take any scale."""
+    need_cuda()
+    E, N, K, T = 3, 67, 384, 30
+    assert _taken("w4z", tq.PATH_AUTO, T, E, N, K) == tq.PATH_PREFILL
+    g = torch.Generator().manual_seed(7)
+    u = torch.randint(0, 16, (E, N, K), generator=g)
+    u[:, :, 5] = 15
+    ws = (_word(u).cuda(), torch.full((E, N, K // 128), scale, dtype=torch.float16, device="cuda"),
+          torch.zeros(E, N, K // 128, dtype=torch.uint8, device="cuda"))
+    # sums stay in fp16's range: K 15 scale |x| <= 384 * 15 * 65504 * 2^-14
+    x = (torch.rand(T, K, generator=g) * 2.0 ** -14 * torch.where(torch.rand(T, K, generator=g) < 0.5, -1.0, 1.0)).half().cuda()
+    offsets = torch.tensor([0, 11, 11, T], dtype=torch.int32, device="cuda")
+    y = _call("w4z", x, ws, offsets, path=path)
+    assert tq.tq_device_status() == 0 and torch.isfinite(y).all()
+    _check("w4z", path, x, ws, offsets, y, np.arange(T))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,E", [(6, 4), (24, 3), (25, 3), (90, 2)])
+def test_auto_is_as_exact_as_the_path_it_takes(T, E, fmt):
+    need_cuda()
+    N, K = 130, 640
+    w = I.weights(E * N, K, T, device="cuda", outlier_frac=0.0 if fmt == "ternary" else 0.001)
+    if fmt == "ternary":
+        p, s = tq.tq_quantize_pack(w)
+        ws = (p.view(E, N, -1), s.view(E, N), None)
+    else:
+        q, s, z, _ = tq.w4g_quantize_pack_ex(w, zero_point=fmt == "w4z")
+        ws = (q.view(E, N, -1), s.view(E, N, -1), None if z is None else z.view(E, N, -1))
+    ids = torch.randint(0, E, (T, 1), generator=torch.Generator().manual_seed(T)).int().cuda()
+    offsets, order, _ = tq.tq_moe_sort(ids, E)
+    x = I.activations(T, K, T, device="cuda", outlier_row_frac=0.02)
+    y = _call(fmt, x, ws, offsets, order=order, top_k=1)
+    assert tq.tq_device_status() == 0
+    _check(fmt, tq.PATH_AUTO, x, ws, offsets, y, order.cpu().numpy())
