@@ -393,10 +393,12 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32, 1)
     if (lane < W) cnt[lane * B + e] = incl - c;
     if (lane == 31) tot[e] = incl;
   }
-  if (C > 1)
-    cluster_sync_all();
-  else
+  if (C > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
     __syncthreads();
+  }
   // thread tid: the experts [tid P, tid P + P) of the scan over experts
   const int P = (E + nt - 1) / nt;
   int sum = 0;
@@ -462,10 +464,7 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32, 1)
       pos[i] = b < E ? row : -1;
     }
   }
-  if (C > 1) {
-    __syncwarp();
-    cluster_wait();
-  }
+  if (C > 1) cluster_wait();
 }
 
 cudaError_t launch_moe_sort(const int32_t* ids, int32_t* offsets, int32_t* order, int32_t* pos, int64_t R, int64_t E,
