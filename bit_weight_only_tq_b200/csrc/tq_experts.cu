@@ -138,7 +138,7 @@ __device__ __forceinline__ void expert_chunks(const ExpertArgs& a, int TM, int* 
   for (int e = e0; e < e1; ++e) {
     const int next = expert_bound(a, e + 1);
     first[e] = sum;
-    sum += next > prev ? (next - prev + TM - 1) / TM : 0;
+    sum += next > prev ? (next - prev - 1) / TM + 1 : 0;  // rows + TM - 1 could pass an int
     prev = next;
   }
   int incl = sum;
@@ -185,7 +185,7 @@ __device__ __forceinline__ ExpertItem expert_item(const ExpertArgs& a, const int
   it.e = lo;
   it.tile = local / c;
   const int b0 = expert_bound(a, lo), b1 = expert_bound(a, lo + 1);
-  const int size = kEven ? ((b1 - b0 + c - 1) / c + 15) / 16 * 16 : TM;
+  const int size = kEven ? ((b1 - b0 - 1) / c + 16) / 16 * 16 : TM;
   it.row0 = b0 + (local - it.tile * c) * size;
   it.rows = b1 - it.row0 < size ? b1 - it.row0 : size;
   return it;

@@ -136,3 +136,21 @@ def test_auto_is_as_exact_as_the_path_it_takes(T, E, fmt):
     y = _call(fmt, x, ws, offsets, order=order, top_k=1)
     assert tq.tq_device_status() == 0
     _check(fmt, tq.PATH_AUTO, x, ws, offsets, y, order.cpu().numpy())
+
+
+# ------------------------------------------------------------------------------------ most rows there can be
+def test_one_expert_with_every_row_there_can_be():
+    """2^31 - 1 slots of two tokens: an expert's rows plus a chunk's, less one, are past 32 bits.  13 GB."""
+    need_cuda()
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB of device memory")
+    R, k, K = 2 ** 31 - 1, 2 ** 30, 64
+    order = torch.arange(R, dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    x = torch.tensor([[1.0], [-2.0]]).repeat(1, K).half().cuda()
+    packed = torch.full((1, 1, K // 4), 0xAA, dtype=torch.uint8, device="cuda")      # every code +1
+    scale = torch.tensor([[0.5]]).half().cuda()
+    y = torch.full((R, 1), 7.0, dtype=torch.float16, device="cuda")
+    tq.tq_gemm_experts(x, packed, scale, offsets, order=order, top_k=k, y=y, path=tq.PATH_DECODE)
+    assert tq.tq_device_status() == 0
+    assert (y[:k] == 32.0).all() and (y[k:] == -64.0).all()
