@@ -39,6 +39,12 @@ __device__ __forceinline__ int64_t expert_x_row(const ExpertArgs& a, int64_t r) 
   return slot >= 0 && t < a.X ? t : -1;
 }
 
+// offsets[e], clamped to [0, R].
+__device__ __forceinline__ int expert_bound(const ExpertArgs& a, int e) {
+  const int64_t o = a.offsets[e];
+  return static_cast<int>(o < 0 ? 0 : (o < a.R ? o : a.R));
+}
+
 // ---------------------------------------------------------------------------------------------
 // Any shape and alignment: one warp per (row, 32 outputs), lanes over k.  Correct, not fast.
 // ---------------------------------------------------------------------------------------------
@@ -47,12 +53,12 @@ __global__ void __launch_bounds__(256) experts_generic_kernel(const ExpertArgs a
   pdl_allow_dependents();
   pdl_wait_prior_grids();
   const int lane = threadIdx.x & 31;
-  const int64_t nb = (a.N + 31) / 32, total = a.offsets[a.E];
-  const int64_t rows = total < a.R ? total : a.R, G = a.K / 128;
+  const int64_t nb = (a.N + 31) / 32, row0 = expert_bound(a, 0);
+  const int64_t rows = expert_bound(a, a.E) - row0, G = a.K / 128;
   const int64_t row_bytes = kInt4 ? a.K / 2 : (a.K + 3) / 4;
   const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
   for (int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); task < rows * nb; task += step) {
-    const int64_t r = task / nb, n0 = (task - r * nb) * 32;
+    const int64_t r = row0 + task / nb, n0 = task % nb * 32;
     int lo = 0, hi = a.E;  // the expert: offsets[lo] <= r < offsets[lo + 1]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -93,15 +99,15 @@ static cudaError_t launch_experts_generic(const ExpertArgs& a, cudaStream_t s) {
   return launch_pdl(experts_generic_kernel<kInt4>, dim3(row_grid(a.R * ((a.N + 31) / 32), 8, 8)), dim3(256), 0, 1, s, a);
 }
 
-// rows[r] = x[row(r)], zeros for a row outside x, for r < offsets[E]: a warp per 2 KB.
+// rows[r] = x[row(r)], zeros for a row outside x, for offsets[0] <= r < offsets[E]: a warp per 2 KB.
 __global__ void __launch_bounds__(256) experts_rows_kernel(const ExpertArgs a) {
   pdl_allow_dependents();
   pdl_wait_prior_grids();
   const int lane = threadIdx.x & 31;
-  const int64_t kept = a.offsets[a.E], nv = a.K / 8, segs = (nv + 127) / 128;
-  const int64_t tasks = (kept < a.R ? kept : a.R) * segs, step = static_cast<int64_t>(gridDim.x) * 8;
+  const int64_t row0 = expert_bound(a, 0), nv = a.K / 8, segs = (nv + 127) / 128;
+  const int64_t tasks = (expert_bound(a, a.E) - row0) * segs, step = static_cast<int64_t>(gridDim.x) * 8;
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); w < tasks; w += step) {
-    const int64_t r = w / segs, v0 = (w - r * segs) * 128 + lane;
+    const int64_t r = row0 + w / segs, v0 = w % segs * 128 + lane;
     const int64_t xr = expert_x_row(a, r);
     uint4 b[4];
 #pragma unroll
@@ -124,11 +130,6 @@ static cudaError_t launch_experts_rows(const ExpertArgs& a, cudaStream_t s) {
 // first[e] = chunks of the experts before e (E + 1 entries in shared memory), from the offsets
 // clamped to [0, R]; called by all nt threads of the CTA (nt <= 1024), scratch holds nt / 32 ints.
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ int expert_bound(const ExpertArgs& a, int e) {
-  const int64_t o = a.offsets[e];
-  return static_cast<int>(o < 0 ? 0 : (o < a.R ? o : a.R));
-}
-
 __device__ __forceinline__ void expert_chunks(const ExpertArgs& a, int TM, int* first, int* scratch, int nt) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = (a.E + nt - 1) / nt;

@@ -234,7 +234,8 @@ def tq_gemm_experts(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, 
     """Each expert's rows times its ternary weights: y[r] = x[row(r)] . What_e^T (+ bias_e) for
     offsets[e] <= r < offsets[e + 1]; row(r) = order[r] // top_k with `order` (x holds the tokens), r
     without (x holds sorted rows).  packed uint8 [E, N, ceil(K/4)], scale fp16 [E, N], bias fp16 [E, N].
-    Rows from offsets[-1] on are left as they were (uninitialised when y is allocated here).
+    Rows before offsets[0] and from offsets[-1] on are left as they were (uninitialised when y is allocated
+    here), so that E + 1 consecutive offsets of a sort of more experts do with the weights of those E.
     rows: fp16 [R, K] scratch for the path that copies the rows first (allocated here when it is needed)."""
     dev = _device()
     E, N, _ = _shape2(packed, "packed", 3)

@@ -120,9 +120,10 @@ TQ_API int tq_moe_combine_backward(const void* dout, const void* y, int dtype, c
  *   scales   fp16 [E, N, K/128]
  *   zeros    uint8 [E, N, K/128], values 0 .. 15, or NULL (symmetric)
  *   bias     fp16 [E, N] or NULL
- *   y        fp16 [R, N], written for r < offsets[E]; later rows are left as they were.  Must
- *            not overlap x.
- *   offsets  int32 [E + 1] (tq_moe_sort): non-decreasing, within [0, R].
+ *   y        fp16 [R, N], written for offsets[0] <= r < offsets[E]; other rows are left as they
+ *            were.  Must not overlap x.
+ *   offsets  int32 [E + 1] (tq_moe_sort, or E + 1 consecutive ones of a sort of more experts):
+ *            non-decreasing, within [0, R].
  *   order    int32 [R] or NULL; a negative slot or a row(r) past X reads as zeros.
  *   rows     fp16 [R, K] scratch, 16-byte aligned, or NULL: the PREFILL path with `order` copies the
  *            rows there in sorted order before the product.  Without it AUTO takes the DECODE path

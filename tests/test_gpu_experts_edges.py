@@ -154,3 +154,41 @@ def test_one_expert_with_every_row_there_can_be():
     tq.tq_gemm_experts(x, packed, scale, offsets, order=order, top_k=k, y=y, path=tq.PATH_DECODE)
     assert tq.tq_device_status() == 0
     assert (y[:k] == 32.0).all() and (y[k:] == -64.0).all()
+
+
+# -------------------------------------------------------------------------- a window of a larger sort's experts
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("lo,hi", [(0, 3), (2, 5), (3, 9), (8, 9)])
+@pytest.mark.parametrize("spread", [True, False])
+def test_a_window_of_the_experts(lo, hi, path, fmt, spread):
+    """offsets[lo:hi + 1] of a sort of nine experts with the weights of experts lo .. hi - 1: only their rows
+    are written, those before the first as well as those behind the last left as they were."""
+    need_cuda()
+    T, k, E, N, K = 70, 2, 9, 71 + lo % 2, 256
+    g = torch.Generator(device="cuda").manual_seed(lo)
+    offsets, order, _ = tq.tq_moe_sort(torch.randint(0, E, (T, k), generator=g, device="cuda").int(), E)
+    w = I.weights(E * N, K, 3, device="cuda", outlier_frac=0.0)
+    if fmt == "ternary":
+        p, s = tq.tq_quantize_pack(w)
+        ws = (p.view(E, N, -1)[lo:hi], s.view(E, N)[lo:hi], None)
+    else:
+        q, s, z, _ = tq.w4g_quantize_pack_ex(w, zero_point=fmt == "w4z")
+        ws = (q.view(E, N, -1)[lo:hi], s.view(E, N, -1)[lo:hi], None if z is None else z.view(E, N, -1)[lo:hi])
+    bias = I.bias((hi - lo) * N, 4, device="cuda").view(hi - lo, N)
+    x = I.activations(T, K, 5, device="cuda")
+    token = (order // k).long()
+    y, buf = guarded_empty(T * k, N)
+    window = offsets[lo:hi + 1]
+    if spread:
+        _call(fmt, x, ws, window, order=order, top_k=k, bias=bias, y=y, path=path)
+        _check(fmt, path, x, ws, window, y, token.cpu().numpy(), bias)
+    else:
+        rows = x[token].contiguous()
+        _call(fmt, rows, ws, window, bias=bias, y=y, path=path)
+        _check(fmt, path, rows, ws, window, y, np.arange(T * k), bias)
+    assert tq.tq_device_status() == 0
+    check_canaries(buf, T * k, N)
+    a, b = int(window[0]), int(window[-1])
+    left = y.view(torch.int16)
+    assert (left[:a] == 0x7E5A).all() and (left[b:] == 0x7E5A).all()
