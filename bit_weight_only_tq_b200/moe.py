@@ -218,6 +218,8 @@ def _experts(fmt, x, weights, offsets, order, top_k, bias, y, rows, E, N, path, 
     """What the two products share: checks, the output, and the arguments after the weights."""
     X, K = _shape2(x, "x")
     R = X if order is None else _shape2(order, "order", 1)[0]
+    if top_k >= 1 and R > X * top_k:  # top_k left out or too small: slots past the last token would read as zeros
+        raise ValueError(f"order has {R} slots, but {X} tokens of top_k = {top_k} have {X * top_k}")
     px = _arg(x, "x", torch.float16, (X, K), dev)
     if y is None:
         y = _empty(x, (R, N), torch.float16, stream)
@@ -233,7 +235,8 @@ def tq_gemm_experts(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, 
                     top_k: int = 1, bias=None, y=None, path: int = PATH_AUTO, stream=None, rows=None) -> torch.Tensor:
     """Each expert's rows times its ternary weights: y[r] = x[row(r)] . What_e^T (+ bias_e) for
     offsets[e] <= r < offsets[e + 1]; row(r) = order[r] // top_k with `order` (x holds the tokens), r
-    without (x holds sorted rows).  packed uint8 [E, N, ceil(K/4)], scale fp16 [E, N], bias fp16 [E, N].
+    without (x holds sorted rows); order holds at most x.shape[0] * top_k slots.  packed uint8
+    [E, N, ceil(K/4)], scale fp16 [E, N], bias fp16 [E, N].
     Rows before offsets[0] and from offsets[-1] on are left as they were (uninitialised when y is allocated
     here), so that E + 1 consecutive offsets of a sort of more experts do with the weights of those E.
     rows: fp16 [R, K] scratch for the path that copies the rows first (allocated here when it is needed)."""

@@ -192,3 +192,22 @@ def test_a_window_of_the_experts(lo, hi, path, fmt, spread):
     a, b = int(window[0]), int(window[-1])
     left = y.view(torch.int16)
     assert (left[:a] == 0x7E5A).all() and (left[b:] == 0x7E5A).all()
+
+
+def test_order_without_its_top_k_is_refused():
+    need_cuda()
+    T, k, E, N, K = 5, 3, 4, 40, 128
+    offsets, order, _ = tq.tq_moe_sort(torch.zeros(T, k, dtype=torch.int32, device="cuda"), E)
+    x = I.activations(T, K, 1, device="cuda")
+    p, s = tq.tq_quantize_pack(I.weights(E * N, K, 1, device="cuda"))
+    q, s4 = tq.w4g_quantize_pack(I.weights(E * N, K, 1, device="cuda"))
+    for top_k in (1, 2):
+        with pytest.raises(ValueError, match="15 slots"):
+            tq.tq_gemm_experts(x, p.view(E, N, -1), s.view(E, N), offsets, order=order, top_k=top_k)
+        with pytest.raises(ValueError, match="15 slots"):
+            tq.w4g_gemm_experts(x, q.view(E, N, -1), s4.view(E, N, -1), offsets, order=order, top_k=top_k)
+    ws = (p.view(E, N, -1), s.view(E, N), None)
+    offsets = offsets.clamp(max=7)
+    y = tq.tq_gemm_experts(x, *ws[:2], offsets, order=order[:7], top_k=k)           # the first slots alone
+    assert tuple(y.shape) == (7, N)
+    _check("ternary", tq.PATH_AUTO, x, ws, offsets, y, (order // k).cpu().numpy())

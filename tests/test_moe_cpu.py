@@ -123,3 +123,14 @@ def test_host_tensors_and_wrong_types_are_refused():
         tq.tq_moe_combine(x, ids)
     with pytest.raises(ValueError):
         tq.tq_gemm_experts(x.half(), torch.zeros(2, 4, 2, dtype=torch.uint8), torch.zeros(2, 4).half(), ids.view(-1))
+
+
+def test_an_order_of_more_slots_than_the_tokens_have_is_refused():
+    """top_k left out: the slots past the last token would all read as zeros."""
+    x, order = torch.zeros(4, 64).half(), torch.zeros(8, dtype=torch.int32)
+    for top_k, X in ((1, 4), (3, 2), (2, 0)):
+        with pytest.raises(ValueError, match="8 slots"):
+            moe._experts(tq.FMT_TERNARY, x[:X], (), order, order, top_k, None, None, None, 7, 16, tq.PATH_AUTO, None, 0)
+    for top_k, X in ((2, 4), (8, 1), (3, 4)):                        # refused for being on the host, and no earlier
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            moe._experts(tq.FMT_TERNARY, x[:X], (), order, order, top_k, None, None, None, 7, 16, tq.PATH_AUTO, None, 0)
