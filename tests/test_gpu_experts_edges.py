@@ -211,3 +211,44 @@ def test_order_without_its_top_k_is_refused():
     y = tq.tq_gemm_experts(x, *ws[:2], offsets, order=order[:7], top_k=k)           # the first slots alone
     assert tuple(y.shape) == (7, N)
     _check("ternary", tq.PATH_AUTO, x, ws, offsets, y, (order // k).cpu().numpy())
+
+
+# ------------------------------------------------- one CTA per SM with more than one item (few, long items)
+def _codes(fmt, E, N, K, seed):
+    """Random packed weights, without quantising a matrix of that size first."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if fmt == "ternary":
+        c = torch.randint(0, 3, (E, N, K // 4, 4), generator=g, device="cuda", dtype=torch.uint8)
+        q = c[..., 0] | (c[..., 1] << 2) | (c[..., 2] << 4) | (c[..., 3] << 6)
+        return q, (0.01 + 0.02 * torch.rand(E, N, generator=g, device="cuda")).half(), None
+    q = torch.randint(-2 ** 31, 2 ** 31, (E, N, K // 8), generator=g, device="cuda").int()
+    s = (0.002 + 0.004 * torch.rand(E, N, K // 128, generator=g, device="cuda")).half()
+    z = torch.randint(0, 16, (E, N, K // 128), generator=g, device="cuda", dtype=torch.uint8) if fmt == "w4z" else None
+    return q, s, z
+
+
+# Up to 296 items of 16 stages and more run on 148 CTAs of four consumer groups.  Stage counts (of 256 INT4 or 512
+# ternary k, the last one whole or not) that are and are no multiple of the groups and of the ring; with items of
+# half the rows, stages of twice the k.
+@pytest.mark.parametrize("fmt,K", [("w4", 4096), ("w4z", 4352), ("w4", 4480), ("w4", 4608), ("w4z", 4864), ("w4", 5376),
+                                   ("ternary", 8192), ("ternary", 8704), ("ternary", 8768), ("ternary", 9216),
+                                   ("ternary", 9728), ("ternary", 10752 + 320)])
+@pytest.mark.parametrize("counts,N", [([1, 1, 0, 1, 1, 1], 4001),         # 160 items, and so 315 of half the rows: 3 each
+                                      ([2, 1, 1, 0, 1, 1], 5600),         # 220: 440 halves, 3 each
+                                      ([1, 1, 1, 0, 1, 1], 6397),         # 250: whole items, two each
+                                      ([14], 18930)])                     # 296: two chunks of one expert, 8 and 6 rows
+def test_several_long_items_per_cta(counts, N, fmt, K):
+    need_cuda()
+    E, R = len(counts), sum(counts)
+    ws = _codes(fmt, E, N, K, N + K)
+    offsets = torch.tensor([0] + counts, device="cuda").cumsum(0).int()
+    x = I.activations(R, K, N, device="cuda")
+    bias = I.bias(E * N, K, device="cuda").view(E, N)
+    y, buf = guarded_empty(R, N)
+    _call(fmt, x, ws, offsets, bias=bias, y=y, path=tq.PATH_DECODE)
+    assert tq.tq_device_status() == 0
+    check_canaries(buf, R, N)
+    cols = np.unique(np.concatenate([np.arange(0, N, 61), np.arange(N - 130, N)]))
+    _check(fmt, tq.PATH_DECODE, x, ws, offsets, y, np.arange(R), bias, cols)
+    again = _call(fmt, x, ws, offsets, bias=bias, path=tq.PATH_DECODE)
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
