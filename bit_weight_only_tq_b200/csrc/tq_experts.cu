@@ -46,7 +46,9 @@ __device__ __forceinline__ int expert_bound(const ExpertArgs& a, int e) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Any shape and alignment: one warp per (row, 32 outputs), lanes over k.  Correct, not fast.
+// Any shape and alignment: one warp per (row, 32 outputs), lanes over k, one output at a time with the weights
+// read by bytes: shapes and addresses that the other kernels cannot take (K % 64, unaligned views), and their
+// check.  8 experts, 4096 -> 2048, 16 rows: 361 us INT4, 209 us ternary, where DECODE takes 15 and 13.
 // ---------------------------------------------------------------------------------------------
 template <bool kInt4>
 __global__ void __launch_bounds__(256) experts_generic_kernel(const ExpertArgs a) {
@@ -99,7 +101,8 @@ static cudaError_t launch_experts_generic(const ExpertArgs& a, cudaStream_t s) {
   return launch_pdl(experts_generic_kernel<kInt4>, dim3(row_grid(a.R * ((a.N + 31) / 32), 8, 8)), dim3(256), 0, 1, s, a);
 }
 
-// rows[r] = x[row(r)], zeros for a row outside x, for offsets[0] <= r < offsets[E]: a warp per 2 KB.
+// rows[r] = x[row(r)] for offsets[0] <= r < offsets[E]: a warp per 2 KB.  Not tq_moe_gather's kernel, which
+// leaves the row of a slot outside x as it was: here it has to read as zeros.
 __global__ void __launch_bounds__(256) experts_rows_kernel(const ExpertArgs a) {
   pdl_allow_dependents();
   pdl_wait_prior_grids();
@@ -231,7 +234,7 @@ __device__ __forceinline__ FieldConsts load_field_consts(const uint32_t* c) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Few rows per expert: bound by the packed weights' bytes.  Persistent CTAs; an item is 128 weight
+// Few rows per expert: the packed weights' bytes are the floor.  Persistent CTAs; an item is 128 weight
 // rows of one expert times up to 8 of its rows, all of K.  One producer warp keeps a ring
 // of stages full: 128 weight rows x 128 packed bytes by TMA (128-byte swizzle) and the rows' x by
 // one bulk copy each, running ahead across items.  Consumer warps form KG groups of four that take
@@ -254,12 +257,15 @@ __device__ __forceinline__ FieldConsts load_field_consts(const uint32_t* c) {
 //
 // Bank conflicts: rows of x are 16 bytes apart modulo 128, and lane t's x starts 64 (128) bytes after
 // lane t - 1's: two lanes share banks (four, and so the odd ternary lanes take their words in pairs
-// the other way round).  Ordering the words of all lanes apart took two selects per MMA, more than
-// the shared memory's extra cycles: it is the ALU that bounds this loop.  Weight row of lane group g is
-// (g / 2) + 4 (g % 2), so that the two rows of a quarter-warp access differ in the swizzle's top bit.
+// the other way round).  Ordering the words of all lanes apart took two selects per MMA, which cost more
+// than the shared memory's extra cycles.  Weight row of lane group g is (g / 2) + 4 (g % 2), so that the two
+// rows of a quarter-warp access differ in the swizzle's top bit.
 //
 // One row for each of 8 experts, 4096 -> 14336: INT4 61 us, 4.0 TB/s of packed weights and scales,
-// ternary 51 us, 2.3 TB/s; issue 56 and 52 %, ALU 50 and 53 % busy.  A token's 8 of 64 experts,
+// ternary 51 us, 2.3 TB/s; issue 57 and 52 %, ALU 50 and 53 % busy.  No unit is full: the four or so warps
+// of a scheduler wait for a stage, then decode at the same time.  Of 6.9 (7.0) warp cycles per instruction 1.2
+// (1.2) wait for a barrier, shared or global memory (long scoreboard), 1.2 (1.4) for the ALU, 1.4 (1.3) were
+// ready and not selected, 0.8 (0.7) are fixed latencies, 0.6 (0.7) dispatch.  A token's 8 of 64 experts,
 // 2048 -> 2816, INT4 with zero-points: 13.2 us, of which the weights' bytes take 3.7: launch, chunk table, first
 // loads and the last sums are not overlapped with anything.
 // ---------------------------------------------------------------------------------------------
@@ -658,9 +664,15 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
   // at most min(R, E + R / 8) chunks
   const int64_t by_rows = a.E + a.R / 8, chunks = a.R < by_rows ? a.R : by_rows;
   const int64_t items = chunks * ((a.N + kERows - 1) / kERows);
-  // One CTA per SM where its items run in one round, or where they are long (two rounds of short ones
-  // pay their fixed cost twice): 176 items of 28 ternary stages 44 us against 48, before wide items took
-  // them to 39, of 8 INT4 stages with zero-points 16.6 against 14.6.
+  // One CTA per SM where its items run in one round, or, up to twice as many, where they are long (two rounds
+  // of short ones pay their fixed cost twice).  `items` counts an expert for every row; rows that share one
+  // make fewer, and one round is where the single CTA gains most.  us with two CTAs | one, INT4 / ternary:
+  //   8 stages    120 items 11.0 |  9.6 / 15.8 | 12.0   176 items 12.0 | 13.3 / 16.8 | 16.6   296 13.3 | 15.6 / 17.6 | 19.9
+  //   16 stages             17.8 | 14.0 / 26.3 | 18.0             19.9 | 22.7 / 29.0 | 28.5       21.9 | 24.7 / 30.3 | 32.3
+  //   28 stages             26.7 | 19.9 / 40.0 | 27.4             31.4 | 32.8 / 47.6 | 43.2       33.6 | 36.3 / 48.7 | 50.7
+  //   56 stages             42.5 | 34.3 / 63.5 | 49.3             58.6 | 55.5 / 91.1 | 76.9       60.1 | 63.7 / 91.4 | 92.7
+  // so that from 16 stages the loss where every row has an expert of its own is 14 % at most and the gain
+  // where they share 19 to 32 %.
   const int64_t sms = current_device_info().num_sms, nk = a.K / SkinnyLayout<kInt4, 2>::KS;
   if (items <= sms || (items <= 2 * sms && nk >= 16)) return launch_experts_skinny_t<kInt4, 4>(a, items, s);
   return launch_experts_skinny_t<kInt4, 2>(a, items, s);
@@ -702,7 +714,9 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
 // (750) of them decoding, the rest in the four waits and the sums; the MMAs ask for 2048.  Measured
 // and left out: pairs of CTAs sharing 256 x 256 items (cta_group::2; half the decoding per MMA, but
 // barriers across CTAs: 16384 rows 2044 us against 1729), rows copied in the pairs' order so that no
-// byte permutes are needed (no change), a warp of its own for x's barrier (registers fall to 80).
+// byte permutes are needed (no change), a warp of its own for x's barrier (ptxas goes from 96 registers to 80 and
+// spills; the kernels here spill 32 to 80 bytes, <INT4, 2, 128> the most, and <ternary, 1, *> and <ternary, 2, 64>
+// none).
 // 16384 rows run at the power limit (990 W, 1440 MHz).
 // ---------------------------------------------------------------------------------------------
 constexpr int kTBox = 32;        // sorted rows per x load
@@ -1197,7 +1211,14 @@ static cudaError_t launch_experts_tc(const ExpertArgs& a, cudaStream_t s) {
     return launch_pdl(kern, dim3(row_grid(items(RT, TN), 1, 1)), dim3(kTThreads), static_cast<size_t>(smem), 1, s, tx, tw,
                       ty, a);
   };
-  // 64 rows per item while uneven routing leaves most experts below that
+  // 64 rows per item while uneven routing leaves most experts below that; 256 weight rows per item where such
+  // items (at most `items` of them) fill the SMs.  us, INT4 / ternary, rows spread at random:
+  //   TN = 64 | 128, RT = 2, 8 experts of 4096 -> 14336: 32 rows per expert 100 | 104 / 79 | 81, 48: 102 | 106 / 83 | 84,
+  //   64: 125 | 108 / 99 | 89, 96: 169 | 118 / 134 | 99; 64 experts of 2048 -> 2816 at 48: 73 | 77 / 61 | 63, at 64:
+  //   107 | 79 / 86 | 67.
+  //   RT = 1 | 2, 8 experts of 4096 -> N, 40 rows each: 104 items at most, 64 there 22.9 | 29.7 / 20.3 | 23.7; 130, 80
+  //   there 39.4 | 29.9 / 35.1 | 24.2; 182, 112 there 39.4 | 30.9 / 35.2 | 25.3; 416, 256 there 71 | 57 / 64 | 45: RT = 1
+  //   is the better one while its items, twice as many, take one round.
   const std::integral_constant<int, 1> one;
   const std::integral_constant<int, 2> two;
   const std::integral_constant<int, 64> n64;

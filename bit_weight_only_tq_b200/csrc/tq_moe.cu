@@ -64,9 +64,10 @@ static cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
 // Router.  One warp per token; lane l holds VPL scores in registers, in groups of W consecutive
 // ones (one load each): v -> expert (v / W) 32 W + W l + v % W, increasing in v.  The choices are k
 // rounds of a warp-wide maximum over each lane's best; only the lane that held the winner looks
-// through its scores again, so that a round costs one reduction.  Bound by instructions: 8192 tokens,
-// 256 experts, top 8, bf16, forward and gradient 14.4 us, where their bytes take 2.1; the ALU 72 %
-// busy forward (16384 tokens, 128 experts: 12.2 us).  16 tokens: 2.0 us, one launch.
+// through its scores again, so that a round costs one reduction (and that rescan: the warp waits for it).
+// 8192 tokens, 256 experts, top 8, bf16: 8.5 us, bound by instructions (the ALU 72 % busy), and the gradient
+// 5.9 (renormalised 4.4), a chain of shared-memory steps with one token per warp in flight (issue 35 %); their
+// bytes take 2.1.  16 tokens: 2.0 us, one launch.
 // ---------------------------------------------------------------------------------------------
 constexpr int kRouteThreads = 128;
 
@@ -341,9 +342,9 @@ cudaError_t launch_moe_route_bwd(const float* dw, const void* logits, int dtype,
 // CTAs (distributed shared memory) and over the experts give every (warp, expert) its first
 // sorted row; each warp then walks its run again, 32 slots at a time, and a slot's row is that
 // start plus the number of equal ids before it in the strip (match.any).  Stable and without
-// atomics whose order could show: the counting adds are integers.  Latency bounds it: 32768 slots of
-// 128 experts take 11 us, 104 slots 2.6; eight CTAs are what one portable cluster, and so one launch
-// without a workspace, can have.
+// atomics whose order could show: the counting adds are integers.  Latency bounds it; eight CTAs are what
+// one portable cluster, and so one launch without a workspace, can have.  us of 128 experts: 104 slots 2.3,
+// 2048 7.2 and 8192 13.7 (one CTA), 8193 8.5, 32768 10.5, 131072 25, 524288 82.
 // ---------------------------------------------------------------------------------------------
 constexpr int kSortMaxWarps = 32;
 constexpr int kSortCluster = 8;
@@ -489,7 +490,9 @@ cudaError_t launch_moe_sort(const int32_t* ids, int32_t* offsets, int32_t* order
 // thread and fewer threads, reached half the bandwidth).  With few rows a CTA takes one step of a row.
 // 8192 tokens, top 2, 4096 wide, bf16: the sum 31 us (6.5 TB/s), its gradients 54 us (6.2 TB/s).
 // 4096 tokens, top 8, 4096 wide, fp16: the gather writes 268 MB in 62 us, where a plain fill of as
-// much memory takes 73: writes bound it.
+// much memory takes 73: writes bound it.  Rows that are no multiple of 16 bytes go element by element: the sum
+// 114 us, its gradients 108 (8192 x top 2, 4097 wide), the gather 129 (4096 x top 8).  A token's gradients are one
+// CTA's work, since dweights sums over its row: 1 token, top 8, 4096 wide 4.8 us, the sum 1.7.
 // ---------------------------------------------------------------------------------------------
 constexpr int kRowThreads = 128;
 

@@ -145,11 +145,17 @@ int tq_experts_path(int fmt, int64_t R, int64_t E, int64_t N, int64_t K, int ali
   if (R < 0 || E < 1 || N < 0 || K <= 0) return TQ_ERR_SHAPE;
   if (fmt == TQ_FMT_W4G128 && K % 128 != 0) return TQ_ERR_SHAPE;
   if (R == 0 || N == 0 || !aligned || K % 64 != 0) return TQ_PATH_GENERIC;
-  // The crossover by rows per expert on average, the only such number the host knows (evenly random
-  // routing, INT4): at 4 / 6 / 8 / 10 rows the decode kernel takes 63 / 72 / 72 / 105 us and the tensor-core
-  // kernel 96 us with 8 experts of 4096 -> 14336, 50 / 56 / 68 / 77 and 68 to 69 us with 64 of 2048 -> 2816,
-  // 40 / 46 / 56 / 56 and 53 to 54 us with 32 of 4096 -> 2048; ternary crosses at the same numbers.  One pass
-  // of the decode kernel covers 8 rows.
+  // The crossover by rows per expert on average, the only such number the host knows; one pass of the decode
+  // kernel covers 8 rows.  us of the decode | tensor-core kernel, INT4 / ternary, rows spread at random:
+  //   rows per expert        6                     8                        10
+  //   8 of 4096 -> 14336     64 | 99 / 54 | 75     79 | 99 / 66 | 75        90 | 99 / 74 | 76
+  //   64 of 2048 -> 2816     53 | 69 / 45 | 54     68 | 70 / 56 | 54        79 | 70 / 66 | 55
+  //   32 of 4096 -> 2048     40 | 55 / 33 | 41     55.0 | 54.8 / 41 | 42    56 | 55 / 46 | 42
+  //   128 of 2048 -> 768     32 | 45 / 27 | 35     41 | 45 / 34 | 35        44 | 45 / 37 | 35
+  //   8 of 14336 -> 4096     64 | 104 / 51 | 89    90 | 104 / 72 | 89       119 | 104 / 95 | 89
+  // With half of the rows on one expert it moves by two rows at most (8 of 4096 -> 14336 at 8: 87 | 99 / 72 | 76,
+  // 128 of 2048 -> 768 at 10: 48 | 44 / 38 | 35).  R counts slots of no expert too: a caller who knows how many
+  // there are asks with its own number of rows (8 of 64 experts, 4096 -> 14336, 34 of 256 slots: 63 | 103 / 52 | 78).
   return R <= 8 * E ? TQ_PATH_DECODE : TQ_PATH_PREFILL;
 }
 

@@ -8,7 +8,8 @@ tokens and experts, and the experts' products with packed low-bit weights.
 
 Argument marshalling only, like the rest of the package; every tensor is contiguous, on one CUDA
 device, and that device is the current one.  Each forward call of the exchange has its gradient
-beside it; the products' weights are frozen and they have none.
+beside it; the products have none yet, for x either, so that a training step takes dx of the experts'
+rows from elsewhere.
 """
 from __future__ import annotations
 
@@ -268,5 +269,6 @@ def w4g_gemm_experts(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tenso
 
 
 def tq_experts_path(fmt: int, R: int, E: int, N: int, K: int, aligned: bool = True) -> int:
-    """The path PATH_AUTO takes for R sorted rows of E experts."""
+    """The path PATH_AUTO takes for R sorted rows of E experts.  A rank that holds some of the experts passes
+    the number of rows that it expects and hands the result to the product, whose own R counts every slot."""
     return int(lib.tq_experts_path(int(fmt), int(R), int(E), int(N), int(K), 1 if aligned else 0))

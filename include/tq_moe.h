@@ -134,7 +134,9 @@ TQ_API int tq_moe_combine_backward(const void* dout, const void* y, int dtype, c
  *            many (tcgen05.mma), GENERIC any shape and alignment.  DECODE and PREFILL need
  *            K % 64 == 0 (TQ_ERR_PATH) and 16-byte aligned x, weights and y (TQ_ERR_ALIGN).
  *            Every path is right for any numbers of rows per expert; AUTO goes by the average
- *            R / E, which the host knows.
+ *            R / E, which the host knows.  R counts the slots of other ranks' experts too: a rank
+ *            of an expert-parallel group takes the better path by passing what tq_experts_path
+ *            returns for the number of rows that it expects.
  * 1 <= E <= 1024, N E <= 2^31 - 1024, 0 < K <= 2^28, top_k >= 1, 0 <= R < 2^31, 0 <= X < 2^31.
  * R == 0 or N == 0: nothing is launched.  Errors as in tq_gemm.
  * ------------------------------------------------------------------------------------------ */
@@ -148,8 +150,8 @@ TQ_API int w4g_gemm_experts(const uint16_t* x, const int32_t* qweight, const uin
                             int64_t X, int64_t R, int64_t E, int64_t N, int64_t K, int top_k,
                             int path, void* stream);
 
-/* tq_experts_path -- the rule TQ_PATH_AUTO applies (host arithmetic only; fmt is a tq_format).
- * Returns a tq_path or a negative tq_status. */
+/* tq_experts_path -- the rule TQ_PATH_AUTO applies to R rows (host arithmetic only; fmt is a
+ * tq_format; aligned16: x, weights and y are 16-byte aligned).  Returns a tq_path or a negative tq_status. */
 TQ_API int tq_experts_path(int fmt, int64_t R, int64_t E, int64_t N, int64_t K, int aligned16);
 
 #ifdef __cplusplus
