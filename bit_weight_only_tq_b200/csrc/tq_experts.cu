@@ -667,10 +667,11 @@ static cudaError_t launch_experts_skinny(const ExpertArgs& a, cudaStream_t s) {
   // One CTA per SM where its items run in one round, or, up to twice as many, where they are long (two rounds
   // of short ones pay their fixed cost twice).  `items` counts an expert for every row; rows that share one
   // make fewer, and one round is where the single CTA gains most.  us with two CTAs | one, INT4 / ternary:
-  //   8 stages    120 items 11.0 |  9.6 / 15.8 | 12.0   176 items 12.0 | 13.3 / 16.8 | 16.6   296 13.3 | 15.6 / 17.6 | 19.9
-  //   16 stages             17.8 | 14.0 / 26.3 | 18.0             19.9 | 22.7 / 29.0 | 28.5       21.9 | 24.7 / 30.3 | 32.3
-  //   28 stages             26.7 | 19.9 / 40.0 | 27.4             31.4 | 32.8 / 47.6 | 43.2       33.6 | 36.3 / 48.7 | 50.7
-  //   56 stages             42.5 | 34.3 / 63.5 | 49.3             58.6 | 55.5 / 91.1 | 76.9       60.1 | 63.7 / 91.4 | 92.7
+  //               120 items                  176                        296
+  //   8 stages    11.0 |  9.6 / 15.8 | 12.0  12.0 | 13.3 / 16.8 | 16.6  13.3 | 15.6 / 17.6 | 19.9
+  //   16 stages   17.8 | 14.0 / 26.3 | 18.0  19.9 | 22.7 / 29.0 | 28.5  21.9 | 24.7 / 30.3 | 32.3
+  //   28 stages   26.7 | 19.9 / 40.0 | 27.4  31.4 | 32.8 / 47.6 | 43.2  33.6 | 36.3 / 48.7 | 50.7
+  //   56 stages   42.5 | 34.3 / 63.5 | 49.3  58.6 | 55.5 / 91.1 | 76.9  60.1 | 63.7 / 91.4 | 92.7
   // so that from 16 stages the loss where every row has an expert of its own is 14 % at most and the gain
   // where they share 19 to 32 %.
   const int64_t sms = current_device_info().num_sms, nk = a.K / SkinnyLayout<kInt4, 2>::KS;
@@ -1213,12 +1214,12 @@ static cudaError_t launch_experts_tc(const ExpertArgs& a, cudaStream_t s) {
   };
   // 64 rows per item while uneven routing leaves most experts below that; 256 weight rows per item where such
   // items (at most `items` of them) fill the SMs.  us, INT4 / ternary, rows spread at random:
-  //   TN = 64 | 128, RT = 2, 8 experts of 4096 -> 14336: 32 rows per expert 100 | 104 / 79 | 81, 48: 102 | 106 / 83 | 84,
-  //   64: 125 | 108 / 99 | 89, 96: 169 | 118 / 134 | 99; 64 experts of 2048 -> 2816 at 48: 73 | 77 / 61 | 63, at 64:
-  //   107 | 79 / 86 | 67.
-  //   RT = 1 | 2, 8 experts of 4096 -> N, 40 rows each: 104 items at most, 64 there 22.9 | 29.7 / 20.3 | 23.7; 130, 80
-  //   there 39.4 | 29.9 / 35.1 | 24.2; 182, 112 there 39.4 | 30.9 / 35.2 | 25.3; 416, 256 there 71 | 57 / 64 | 45: RT = 1
-  //   is the better one while its items, twice as many, take one round.
+  //   TN = 64 | 128, RT = 2, 8 experts of 4096 -> 14336: 32 rows per expert 100 | 104 / 79 | 81, 48: 102 | 106 /
+  //   83 | 84, 64: 125 | 108 / 99 | 89, 96: 169 | 118 / 134 | 99; 64 experts of 2048 -> 2816 at 48: 73 | 77 /
+  //   61 | 63, at 64: 107 | 79 / 86 | 67.
+  //   RT = 1 | 2, 8 experts of 4096 -> N, 40 rows each: 104 items at most, 64 there 22.9 | 29.7 / 20.3 | 23.7;
+  //   130, 80 there 39.4 | 29.9 / 35.1 | 24.2; 182, 112 there 39.4 | 30.9 / 35.2 | 25.3; 416, 256 there 71 | 57 /
+  //   64 | 45: RT = 1 is the better one while its items, twice as many, take one round.
   const std::integral_constant<int, 1> one;
   const std::integral_constant<int, 2> two;
   const std::integral_constant<int, 64> n64;
