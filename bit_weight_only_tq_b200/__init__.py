@@ -469,3 +469,9 @@ from .moe import *  # noqa: E402,F401,F403
 from . import moe as _moe  # noqa: E402
 
 __all__ += _moe.__all__
+
+# The adapters' calls (include/tq_lora.h).
+from .lora import *  # noqa: E402,F401,F403
+from . import lora as _lora  # noqa: E402
+
+__all__ += _lora.__all__

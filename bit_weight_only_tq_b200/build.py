@@ -27,7 +27,8 @@ def needs_build() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = sources() + [os.path.join(ROOT, "include", "tq.h"),
-                        os.path.join(ROOT, "include", "tq_moe.h"), __file__]
+                        os.path.join(ROOT, "include", "tq_moe.h"),
+                        os.path.join(ROOT, "include", "tq_lora.h"), __file__]
     return any(os.path.getmtime(p) > t for p in deps)
 
 

@@ -1,0 +1,198 @@
+// tq_lora_api.cu -- the extern "C" boundary of the adapters' calls (include/tq_lora.h): argument validation
+// and dispatch.
+#include "../../include/tq_lora.h"
+#include "tq_common.cuh"
+
+namespace {
+
+constexpr int64_t kLoraMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kLoraMaxWidth = int64_t(1) << 24;
+
+inline bool dtype16_ok(int d) { return d == TQ_F16 || d == TQ_BF16; }
+
+// The dropout of a call; false: p is not a probability that can be kept.
+bool drop_args(double p, const int64_t* rng, tq::DropArgs* d) {
+  if (!(p >= 0.0 && p < 1.0)) return false;
+  const uint32_t thr = static_cast<uint32_t>(p * 65536.0 + 0.5);
+  if (thr > 65535u) return false;
+  d->rng = rng;
+  d->thr = thr;
+  d->scale = static_cast<float>(65536.0 / (65536.0 - thr));
+  return true;
+}
+
+int check_lora(int dtype, int64_t M, int64_t L, int64_t N, int64_t K, int rank, int path, double p, const int64_t* rng,
+               tq::DropArgs* d) {
+  if (!dtype16_ok(dtype)) return TQ_ERR_DTYPE;
+  if (M < 0 || M > kLoraMaxRows || L < 1 || L > TQ_LORA_MAX_ADAPTERS) return TQ_ERR_SHAPE;
+  if (N < 0 || N > kLoraMaxWidth || K < 1 || K > kLoraMaxWidth) return TQ_ERR_SHAPE;
+  if (rank < 1 || rank > TQ_LORA_MAX_RANK || !drop_args(p, rng, d)) return TQ_ERR_SHAPE;
+  if (path < TQ_PATH_AUTO || path > TQ_PATH_GENERIC) return TQ_ERR_PATH;
+  return TQ_OK;
+}
+
+// 16-byte vectors along both widths.
+bool lora_fast_shape(int64_t N, int64_t K) { return N % 8 == 0 && K % 8 == 0; }
+
+// The sums of one call, W as A [rank, C] or as B [C, rank].
+tq::LoraArgs lora_sum(const void* P, const void* W, bool w_is_a, int64_t C, int rank, int64_t M, int64_t L, float* V,
+                      const float* scaling, const int32_t* offsets, const int32_t* order) {
+  tq::LoraArgs a = {};
+  a.P = P;
+  a.W = W;
+  a.V = V;
+  a.scaling = scaling;
+  a.offsets = offsets;
+  a.order = order;
+  a.M = M;
+  a.C = C;
+  a.wc = w_is_a ? 1 : rank;
+  a.wj = w_is_a ? C : 1;
+  a.ws = rank * C;
+  a.L = static_cast<int>(L);
+  a.rank = rank;
+  a.use_scaling = !w_is_a;
+  a.drop = tq::DropArgs{nullptr, 0u, 1.0f};
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tq_lora_path(int64_t M, int64_t L, int64_t N, int64_t K, int rank, int dropout, int aligned) {
+  if (M < 0 || L < 1 || N < 0 || K < 1 || rank < 1) return TQ_ERR_SHAPE;
+  if (M == 0 || N == 0 || !aligned || !lora_fast_shape(N, K)) return TQ_PATH_GENERIC;
+  return TQ_PATH_PREFILL;
+}
+
+int tq_lora(const void* x, int dtype, const void* a, const void* b, const float* scaling, const void* base, void* out,
+            float* v, const int32_t* offsets, const int32_t* order, double p, const int64_t* rng, int64_t M, int64_t L,
+            int64_t N, int64_t K, int rank, int path, void* stream) {
+  tq::DropArgs drop;
+  const int st = check_lora(dtype, M, L, N, K, rank, path, p, rng, &drop);
+  if (st != TQ_OK || M == 0 || N == 0) return st;
+  if (!x || !a || !b || !out || !offsets || (drop.thr && !rng)) return TQ_ERR_NULL;
+  const bool al = aligned16(x) && aligned16(a) && aligned16(b) && aligned16(base) && aligned16(out) && aligned16(v);
+  if (path == TQ_PATH_AUTO) {
+    path = tq_lora_path(M, L, N, K, rank, drop.thr != 0, al ? 1 : 0);
+  } else if (path != TQ_PATH_GENERIC) {
+    if (!lora_fast_shape(N, K) || (path == TQ_PATH_DECODE && drop.thr)) return TQ_ERR_PATH;
+    if (!al) return TQ_ERR_ALIGN;
+  }
+  if (!v) return TQ_ERR_NULL;
+  const bool bf16 = dtype == TQ_BF16;
+  tq::LoraArgs s = lora_sum(x, a, true, K, rank, M, L, v, scaling, offsets, order);
+  s.drop = drop;
+  const cudaError_t e = tq::launch_lora_reduce(bf16, path, s, as_stream(stream));
+  if (e != cudaSuccess) return to_status(e);
+  s = lora_sum(nullptr, b, false, N, rank, M, L, v, scaling, offsets, order);
+  s.base = base;
+  s.O = out;
+  return to_status(tq::launch_lora_expand(bf16, path, s, as_stream(stream)));
+}
+
+int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, const void* b, const float* scaling,
+                     const float* v, float* dv, const void* base_dx, void* dx, void* da, void* db,
+                     const int32_t* offsets, const int32_t* order, double p, const int64_t* rng, int64_t M, int64_t L,
+                     int64_t N, int64_t K, int rank, int path, void* stream) {
+  tq::DropArgs drop;
+  const int st = check_lora(dtype, M, L, N, K, rank, path, p, rng, &drop);
+  if (st != TQ_OK) return st;
+  if (path == TQ_PATH_DECODE) return TQ_ERR_PATH;
+  if (!dx && !da && !db) return TQ_OK;
+  if (!offsets || (drop.thr && !rng)) return TQ_ERR_NULL;
+  if (M > 0 && N > 0 && (!dy || !dv || !b || (db && !v) || (da && !x))) return TQ_ERR_NULL;
+  if (dx && M > 0 && !a) return TQ_ERR_NULL;
+  const bool al = aligned16(x) && aligned16(a) && aligned16(b) && aligned16(dy) && aligned16(v) && aligned16(dv) &&
+                  aligned16(base_dx) && aligned16(dx) && aligned16(da) && aligned16(db);
+  if (path == TQ_PATH_AUTO) {
+    path = al && lora_fast_shape(N, K) ? TQ_PATH_PREFILL : TQ_PATH_GENERIC;
+  } else if (path == TQ_PATH_PREFILL) {
+    if (!lora_fast_shape(N, K)) return TQ_ERR_PATH;
+    if (!al) return TQ_ERR_ALIGN;
+  }
+  const bool bf16 = dtype == TQ_BF16;
+  cudaStream_t s = as_stream(stream);
+  cudaError_t e = cudaSuccess;
+  if ((dx || da) && M > 0) {
+    tq::LoraArgs g = lora_sum(dy, b, false, N, rank, M, L, dv, scaling, offsets, order);
+    e = tq::launch_lora_reduce(bf16, path, g, s);
+  }
+  if (e == cudaSuccess && dx && M > 0) {
+    tq::LoraArgs g = lora_sum(nullptr, a, true, K, rank, M, L, dv, scaling, offsets, order);
+    g.base = base_dx;
+    g.O = dx;
+    g.drop = drop;
+    e = tq::launch_lora_expand(bf16, path, g, s);
+  }
+  if (e == cudaSuccess && da) {
+    tq::LoraArgs g = lora_sum(x, nullptr, true, K, rank, M, L, dv, scaling, offsets, order);
+    g.O = da;
+    g.drop = drop;
+    e = tq::launch_lora_wgrad(bf16, path, g, s);
+  }
+  if (e == cudaSuccess && db && N > 0) {
+    tq::LoraArgs g = lora_sum(dy, nullptr, false, N, rank, M, L, const_cast<float*>(v), scaling, offsets, order);
+    g.O = db;
+    e = tq::launch_lora_wgrad(bf16, path, g, s);
+  }
+  return to_status(e);
+}
+
+int tq_dropout(const void* x, int dtype, void* out, double p, const int64_t* rng, int64_t M, int64_t K, void* stream) {
+  if (!moe_dtype_ok(dtype)) return TQ_ERR_DTYPE;
+  tq::DropArgs drop;
+  if (M < 0 || M > kLoraMaxRows || K < 0 || K > (int64_t(1) << 28) || !drop_args(p, rng, &drop)) return TQ_ERR_SHAPE;
+  if (M == 0 || K == 0) return TQ_OK;
+  if (!x || !out || (drop.thr && !rng)) return TQ_ERR_NULL;
+  return to_status(tq::launch_dropout(x, dtype, out, drop, M, K, as_stream(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+int gemm_backward_impl(bool int4, const uint16_t* dy, const void* w, const uint16_t* sc, const uint8_t* zeros,
+                       uint16_t* dx, int64_t M, int64_t N, int64_t K, int path, void* stream) {
+  if (M < 0 || N < 0 || K <= 0 || M > (int64_t(1) << 31) || N > (int64_t(1) << 31) || K > (int64_t(1) << 28))
+    return TQ_ERR_SHAPE;
+  if (int4 && K % 128 != 0) return TQ_ERR_SHAPE;
+  if (path < TQ_PATH_AUTO || path > TQ_PATH_GENERIC || path == TQ_PATH_DECODE) return TQ_ERR_PATH;
+  if (M == 0) return TQ_OK;
+  if (!dx || (N > 0 && (!dy || !w || !sc))) return TQ_ERR_NULL;
+  const bool al = aligned16(dy) && aligned16(w) && aligned16(dx);
+  const bool fits = tq::dx_supported(N, K);
+  if (path == TQ_PATH_AUTO) {
+    path = al && fits ? TQ_PATH_PREFILL : TQ_PATH_GENERIC;
+  } else if (path == TQ_PATH_PREFILL) {
+    if (!fits) return TQ_ERR_PATH;
+    if (!al) return TQ_ERR_ALIGN;
+  }
+  tq::DxArgs a = {};
+  a.dy = reinterpret_cast<const __half*>(dy);
+  a.w = static_cast<const uint8_t*>(w);
+  a.sc = reinterpret_cast<const __half*>(sc);
+  a.zp = zeros;
+  a.dx = reinterpret_cast<__half*>(dx);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  return to_status(tq::launch_dx(int4, path, a, as_stream(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int tq_gemm_backward(const uint16_t* dy, const uint8_t* packed, const uint16_t* scale, uint16_t* dx, int64_t M,
+                     int64_t N, int64_t K, int path, void* stream) {
+  return gemm_backward_impl(false, dy, packed, scale, nullptr, dx, M, N, K, path, stream);
+}
+
+int w4g_gemm_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales, const uint8_t* zeros,
+                      uint16_t* dx, int64_t M, int64_t N, int64_t K, int path, void* stream) {
+  return gemm_backward_impl(true, dy, qweight, scales, zeros, dx, M, N, K, path, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,130 @@
+/*
+ * tq_lora.h -- C ABI of libtq.so, low-rank adapters beside the packed projections: the adapters' rows
+ * of many requests at once, their gradients, dropout from a counter-based generator, and the packed
+ * products' gradient for x.
+ *
+ * The conventions of tq.h hold (device pointers owned by the caller, row-major contiguous tensors,
+ * asynchronous on `stream` and the current device, argument errors returned before anything is
+ * launched, no allocation, graph capturable), with one difference: the kernels here read nothing,
+ * weights included, before the preceding work on the stream has finished.
+ *
+ * A frozen projection shared by all requests and L adapters of rank r:
+ *
+ *   y [M, N]    = x What^T                                   tq_gemm / w4g_gemm
+ *   out[m]      = y[m] + s_l (drop(x[m]) A_l^T) B_l^T        tq_lora,  l the adapter of row m
+ *
+ * and, from dy [M, N], a training step's gradients:
+ *
+ *   dx [M, K]   = dy What                                    tq_gemm_backward / w4g_gemm_backward
+ *   dx, dA, dB  of the adapters, dx added to the above       tq_lora_backward
+ *
+ * The adapter of each row comes as a plan that all layers of a step share: tq_moe_sort of the rows'
+ * adapter ids (a slot is a row here, top_k = 1) gives
+ *   order    int32 [M]: the row at each sorted position, rows of adapter 0 first, or NULL: row = position;
+ *   offsets  int32 [L + 1], non-decreasing, within [0, M]: adapter l has the positions offsets[l] .. offsets[l + 1] - 1.
+ * Positions before offsets[0] and from offsets[L] on belong to no adapter: their rows get the base alone.
+ * The rows that `order` names are distinct; an entry outside [0, M) names no row.
+ *
+ * Types: x, A, B, base, out, dy and the gradients have one dtype, TQ_F16 or TQ_BF16.  Sums are in fp32, v and dv
+ * are kept in fp32, and every output is rounded once.  Where v and dv enter a tensor-core product, each is
+ * the sum of two 16-bit numbers: 22 bits (fp16) or 16 bits (bf16) of it.
+ *
+ * Dropout: element e = k % 8 of the group i = m ceil(K / 8) + k / 8 of x [M, K] takes the 16 bits
+ *   (e even: low half, odd: high half) of word e / 2 of Philox4x32-10 (Salmon, Moraes, Dror, Shaw: Parallel
+ *   random numbers: as easy as 1, 2, 3; SC 2011) with the counter (i, offset) and the key seed, 64 bits
+ *   each, low word first.  It is dropped where they are below T = floor(65536 p + 1/2); what is kept is
+ *   multiplied by 65536 / (65536 - T).  A dropped element is zero whatever it holds.  No mask is stored:
+ *   every call that names the same p, seed, offset and shape drops the same elements.
+ *   rng      int64 [2] on the device: seed, offset.  A captured graph reads it when it runs, so that a
+ *            kernel which advances the offset between replays gives each its own mask.
+ *   0 <= p < 1 and T <= 65535 (TQ_ERR_SHAPE otherwise); p = 0 reads no rng (it may be NULL).
+ */
+#ifndef TQ_LORA_H
+#define TQ_LORA_H
+
+#include "tq_moe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define TQ_LORA_MAX_ADAPTERS 1024
+#define TQ_LORA_MAX_RANK 128
+
+/* --------------------------------------------------------------------------------------------
+ * tq_lora -- out[m] = base[m] + scaling[l] (drop(x[m]) A_l^T) B_l^T.
+ *
+ *   x        [M, K]
+ *   a        [L, rank, K], b [L, N, rank].  A rank above 128 is the sum of two calls, the second with
+ *            the first's out as base.
+ *   scaling  fp32 [L], or NULL for 1
+ *   base     [M, N], or NULL for zeros; may be `out`
+ *   out      [M, N], written in full.  Must not overlap x, a or b.
+ *   v        fp32 [M, rank], or NULL: drop(x) A^T by sorted position, without `scaling`, written for
+ *            the positions of adapters; tq_lora_backward reads it.  PREFILL and GENERIC need it
+ *            (TQ_ERR_NULL); AUTO without it takes DECODE where it can.
+ *            Calls (or captured graphs) that may run at once need one each.
+ *   path     TQ_PATH_AUTO, or one path (tests): DECODE takes few rows (one launch, up to 8 rows of an
+ *            adapter per pass over its weights), PREFILL many (tensor cores), GENERIC any shape and
+ *            alignment.  DECODE and PREFILL need K % 8 == 0 and N % 8 == 0 (TQ_ERR_PATH) and 16-byte aligned x, a,
+ *            b, base, out and v (TQ_ERR_ALIGN).  DECODE needs p = 0 (TQ_ERR_PATH).
+ *            Every path is right for any numbers of rows per adapter.
+ * 1 <= L <= 1024, 1 <= rank <= 128, 0 < K, N <= 2^24 (N = 0: nothing), 0 <= M < 2^31.
+ * M == 0 or N == 0: nothing is launched.
+ *
+ * tq_lora_path -- the rule TQ_PATH_AUTO applies (host arithmetic only; aligned16: all of the pointers
+ * that are not NULL are 16-byte aligned).  Returns a tq_path or a negative tq_status.
+ * ------------------------------------------------------------------------------------------ */
+TQ_API int tq_lora(const void* x, int dtype, const void* a, const void* b, const float* scaling, const void* base,
+                   void* out, float* v, const int32_t* offsets, const int32_t* order, double p, const int64_t* rng,
+                   int64_t M, int64_t L, int64_t N, int64_t K, int rank, int path, void* stream);
+TQ_API int tq_lora_path(int64_t M, int64_t L, int64_t N, int64_t K, int rank, int dropout, int aligned16);
+
+/* --------------------------------------------------------------------------------------------
+ * tq_lora_backward -- the gradients of tq_lora, from dy [M, N] and the forward call's x, a, b, scaling,
+ * plan, p, rng and v:
+ *   dv[r]    = scaling[l] dy[m] B_l              scratch fp32 [M, rank], by sorted position
+ *   dx[m]    = base_dx[m] + drop'(dv[r] A_l)     drop': zero where drop(x) dropped, else times the same factor
+ *   da_l     = sum over its rows of dv[r]^T drop(x[m])             [L, rank, K]
+ *   db_l     = scaling[l] sum over its rows of dy[m]^T v[r]        [L, N, rank]
+ *   (r: sorted position, m: its row).  An adapter without rows gets zeros.
+ *   base_dx  [M, K], or NULL for zeros; may be `dx` (the projection's own gradient for x, to which this adds)
+ *   dx, da, db  each may be NULL (not wanted).  None may overlap what the call reads (dx may be base_dx).
+ *   path     AUTO, PREFILL or GENERIC, with the conditions of tq_lora on all of the tensors.
+ * The gradient for base is dy itself; `scaling` has none.  Sums are taken in a fixed order.
+ * ------------------------------------------------------------------------------------------ */
+TQ_API int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, const void* b,
+                            const float* scaling, const float* v, float* dv, const void* base_dx, void* dx, void* da,
+                            void* db, const int32_t* offsets, const int32_t* order, double p, const int64_t* rng,
+                            int64_t M, int64_t L, int64_t N, int64_t K, int rank, int path, void* stream);
+
+/* --------------------------------------------------------------------------------------------
+ * tq_dropout -- out = drop(x), x and out [M, K] of `dtype` (TQ_F32, TQ_F16, TQ_BF16); out may be x.  Its
+ * gradient is the same call on the gradient of out.
+ * 0 <= M < 2^31, 0 <= K <= 2^28.
+ * ------------------------------------------------------------------------------------------ */
+TQ_API int tq_dropout(const void* x, int dtype, void* out, double p, const int64_t* rng, int64_t M, int64_t K,
+                      void* stream);
+
+/* --------------------------------------------------------------------------------------------
+ * tq_gemm_backward / w4g_gemm_backward -- dx = dy What, the gradient for x of tq_gemm / w4g_gemm / w4g_gemm_zp
+ * (that of bias is the sum of dy's rows; the packed weights have none).
+ *   dy       fp16 [M, N]
+ *   packed, scale / qweight, scales, zeros   as in the products (zeros NULL: symmetric)
+ *   dx       fp16 [M, K], written in full.  Must not overlap dy.
+ *   path     TQ_PATH_AUTO, PREFILL (tensor cores) or GENERIC (any shape and alignment; weights enter the sum
+ *            exactly).  PREFILL needs K % 64 == 0, N % 8 == 0 (TQ_ERR_PATH), 16-byte aligned dy, weights and
+ *            dx (TQ_ERR_ALIGN).  There a ternary weight enters exactly and an INT4 weight (u - z) s is rounded to fp16,
+ *            as on that path of w4g_gemm (scales must keep it below 65520).
+ * Shapes and errors as in tq_gemm / w4g_gemm.
+ * ------------------------------------------------------------------------------------------ */
+TQ_API int tq_gemm_backward(const uint16_t* dy, const uint8_t* packed, const uint16_t* scale, uint16_t* dx, int64_t M,
+                            int64_t N, int64_t K, int path, void* stream);
+TQ_API int w4g_gemm_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales, const uint8_t* zeros,
+                             uint16_t* dx, int64_t M, int64_t N, int64_t K, int path, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* TQ_LORA_H */
