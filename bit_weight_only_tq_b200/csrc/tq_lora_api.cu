@@ -162,7 +162,7 @@ int gemm_backward_impl(bool int4, const uint16_t* dy, const void* w, const uint1
   if (M == 0) return TQ_OK;
   if (!dx || (N > 0 && (!dy || !w || !sc))) return TQ_ERR_NULL;
   const bool al = aligned16(dy) && aligned16(w) && aligned16(dx);
-  const bool fits = tq::dx_supported(N, K);
+  const bool fits = tq::dx_supported(M, N, K);
   if (path == TQ_PATH_AUTO) {
     path = al && fits ? TQ_PATH_PREFILL : TQ_PATH_GENERIC;
   } else if (path == TQ_PATH_PREFILL) {

@@ -133,7 +133,8 @@ def test_gradient_for_x(M, N, K, fmt):
     assert tq.tq_device_status() == 0
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 5, 7), (9, 33, 130), (17, 100, 64), (1, 1, 1), (40, 9, 192)])
+@pytest.mark.parametrize("M,N,K", [(3, 5, 7), (9, 33, 130), (17, 100, 64), (1, 1, 1), (40, 9, 192), (40, 16, 192),
+                                   (300, 72, 64)])
 def test_gradient_for_x_ternary_odd_sizes(M, N, K):
     need_cuda()
     t, w64 = _weights(N, K, M + N, "ternary")
