@@ -270,16 +270,6 @@ static cudaError_t lora_generic_wgrad(bool bf16, const LoraArgs& a, cudaStream_t
   });
 }
 
-cudaError_t launch_lora_reduce(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {
-  return lora_generic_reduce(bf16, a, s);
-}
-cudaError_t launch_lora_expand(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {
-  return lora_generic_expand(bf16, a, s);
-}
-cudaError_t launch_lora_wgrad(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {
-  return lora_generic_wgrad(bf16, a, s);
-}
-
 // ---------------------------------------------------------------------------------------------
 // Dropout
 // ---------------------------------------------------------------------------------------------
