@@ -42,7 +42,15 @@ struct LoraArgs {
   int64_t wc, wj, ws;
   int L, rank;
   bool use_scaling;         // f includes scaling[l]
+  // Tensor-core wgrad scales V by one power of two per adapter, from the largest magnitude that reduce found in each tile of V and
+  // of V2 (kLoraMostPer slots per tile, of which its most_n CTAs write one each); null: not wanted
+  const float* V2;
+  float* most;
+  float* most2;
+  int most_n;
 };
+
+constexpr int kLoraMostPer = 8;
 
 // ---------------------------------------------------------------------------------------------
 // Philox4x32-10: ten rounds of two 32 x 32 -> 64 bit products, the key advanced by two odd constants

@@ -92,9 +92,14 @@ int tq_lora(const void* x, int dtype, const void* a, const void* b, const float*
   return to_status(tq::launch_lora_expand(bf16, path, s, as_stream(stream)));
 }
 
+size_t tq_lora_workspace_size(int64_t M, int64_t L, int rank) {
+  if (M < 0 || M > kLoraMaxRows || L < 1 || L > TQ_LORA_MAX_ADAPTERS || rank < 1 || rank > TQ_LORA_MAX_RANK) return 0;
+  return static_cast<size_t>(tq::lora_workspace_floats(M, rank) + 2 * tq::lora_most_floats(M, L)) * sizeof(float);
+}
+
 int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, const void* b, const float* scaling,
-                     const float* v, float* dv, const void* base_dx, void* dx, void* da, void* db,
-                     const int32_t* offsets, const int32_t* order, double p, const int64_t* rng, int64_t M, int64_t L,
+                     const float* v, void* workspace, size_t workspace_bytes, const void* base_dx, void* dx, void* da,
+                     void* db, const int32_t* offsets, const int32_t* order, double p, const int64_t* rng, int64_t M, int64_t L,
                      int64_t N, int64_t K, int rank, int path, void* stream) {
   tq::DropArgs drop;
   const int st = check_lora(dtype, M, L, N, K, rank, path, p, rng, &drop);
@@ -102,9 +107,10 @@ int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, co
   if (path == TQ_PATH_DECODE) return TQ_ERR_PATH;
   if (!dx && !da && !db) return TQ_OK;
   if (!offsets || (drop.thr && !rng)) return TQ_ERR_NULL;
-  if (M > 0 && N > 0 && (!dy || !dv || !b || (db && !v) || (da && !x))) return TQ_ERR_NULL;
-  if (dx && M > 0 && !a) return TQ_ERR_NULL;
-  const bool al = aligned16(x) && aligned16(a) && aligned16(b) && aligned16(dy) && aligned16(v) && aligned16(dv) &&
+  if (M > 0 && (!workspace || (N > 0 && (!dy || !b)) || !v || (da && !x) || (dx && !a))) return TQ_ERR_NULL;
+  if (!aligned16(workspace)) return TQ_ERR_ALIGN;
+  if (M > 0 && workspace_bytes < tq_lora_workspace_size(M, L, rank)) return TQ_ERR_SHAPE;
+  const bool al = aligned16(x) && aligned16(a) && aligned16(b) && aligned16(dy) && aligned16(v) &&
                   aligned16(base_dx) && aligned16(dx) && aligned16(da) && aligned16(db);
   if (path == TQ_PATH_AUTO) {
     path = al && lora_fast_shape(N, K) ? TQ_PATH_PREFILL : TQ_PATH_GENERIC;
@@ -115,8 +121,18 @@ int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, co
   const bool bf16 = dtype == TQ_BF16;
   cudaStream_t s = as_stream(stream);
   cudaError_t e = cudaSuccess;
-  if ((dx || da) && M > 0) {
+  float* dv = static_cast<float*>(workspace);
+  // fp16 on the tensor cores: the largest |v| and |dv| of each tile, for the powers of two of da and db
+  const bool most = path != TQ_PATH_GENERIC && !bf16;
+  float* most_v = most ? dv + tq::lora_workspace_floats(M, rank) : nullptr;
+  float* most_dv = most ? most_v + tq::lora_most_floats(M, L) : nullptr;
+  int most_n = 0;
+  if (M > 0 && (dx || da || most)) {
     tq::LoraArgs g = lora_sum(dy, b, false, N, rank, M, L, dv, scaling, offsets, order);
+    g.V2 = v;
+    g.most = most_dv;
+    g.most2 = most_v;
+    most_n = tq::lora_reduce_split(g);
     e = tq::launch_lora_reduce(bf16, path, g, s);
   }
   if (e == cudaSuccess && dx && M > 0) {
@@ -130,11 +146,15 @@ int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, co
     tq::LoraArgs g = lora_sum(x, nullptr, true, K, rank, M, L, dv, scaling, offsets, order);
     g.O = da;
     g.drop = drop;
+    g.most = most_dv;
+    g.most_n = most_n;
     e = tq::launch_lora_wgrad(bf16, path, g, s);
   }
   if (e == cudaSuccess && db && N > 0) {
     tq::LoraArgs g = lora_sum(dy, nullptr, false, N, rank, M, L, const_cast<float*>(v), scaling, offsets, order);
     g.O = db;
+    g.most = most_v;
+    g.most_n = most_n;
     e = tq::launch_lora_wgrad(bf16, path, g, s);
   }
   return to_status(e);

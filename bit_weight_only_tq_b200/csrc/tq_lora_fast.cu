@@ -376,16 +376,500 @@ static cudaError_t lora_fast_expand(bool bf16, const LoraArgs& a, cudaStream_t s
   });
 }
 
+// ---------------------------------------------------------------------------------------------
+// reduce and wgrad on tcgen05: D (128 x up to 256 fp32, tensor memory) += A B^T over stages in shared memory.
+//   reduce  D[position, j]  A: the tile's rows of P, 128 x 64 columns (K-major)
+//                           B: W, as A [rank, C] 64 columns of each j (K-major), as B [C, rank] 64 rows (MN-major)
+//   wgrad   D[c, j]         A: 64 rows x 128 columns of P (MN-major)
+//                           B: 64 rows of V, hi and lo side by side (MN-major); their sums are added at the end
+// Both read P once and little else: HBM bounds them (2 rank FLOPs per byte of P; the tensor pipe is busy for at most the
+// share that rank 128 takes, 512 of the 712 cycles that a stage of P takes from HBM).  P is fetched row by row through `order`
+// with 16-byte cp.async (a row's 128 or 256 bytes are consecutive lanes), which also masks, zero-fills and needs no tensor map,
+// by eight loader warps that stay up to six stages ahead; with dropout each thread masks what it copied before it hands the stage on.
+// The summation (columns, rows) is split over a cluster of S CTAs while tiles leave SMs idle; partial sums go through distributed
+// shared memory and are added in rank order.
+// One CTA per SM (its shared memory keeps every other kernel with tensor memory out), so that none waits for tensor memory that a
+// CTA holds which itself waits for a cluster.
+// ---------------------------------------------------------------------------------------------
+constexpr int kLtcLoaders = 256;
+constexpr int kLtcThreads = kLtcLoaders + 32;
+enum { kReduceA = 0, kReduceB = 1, kWgrad = 2 };
+
+template <int kMode, int RP>
+struct LoraTcLayout {
+  static constexpr int kN = kMode == kWgrad ? 2 * RP : RP;                  // MMA columns
+  static constexpr int kTileP = 128 * 128;
+  static constexpr int kTileW = kMode == kReduceA ? (RP < 64 ? 8192 : RP * 128) : (kN + 63) / 64 * 8192;
+  static constexpr int kStage = kTileP + kTileW;
+  static constexpr int kRing = 192 * 1024 / kStage;
+  static constexpr int kLag = kRing - 2;                                    // stages between request and hand-over
+  static constexpr int kOffBar = kRing * kStage;                            // full[R], empty[R], accFull
+  static constexpr int kOffRow = kOffBar + (2 * kRing + 1) * 8 + 8;         // TMEM slot before it
+  static constexpr int kOffMost = kOffRow + (kMode == kWgrad ? kRing * 64 : 128) * 4;
+  static constexpr int kAlloc = kOffMost + 128 + 1024;
+  static constexpr uint32_t kTmemCols = kN <= 32 ? 32u : (kN <= 64 ? 64u : (kN <= 128 ? 128u : 256u));
+  static_assert(kRing >= 4 && kAlloc > 116 * 1024 && kAlloc <= 227 * 1024, "one CTA per SM");
+  static_assert(128 * RP * 4 <= kRing * kStage, "partial sums fit");
+};
+
+// Shared-memory descriptor of an MN-major operand, 128-byte swizzle: planes of 64 elements along M / N, 8192 bytes apart (leading
+// byte offset), each of 128-byte rows of one k, groups of eight rows 1024 bytes apart (stride byte offset).
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(8192u >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+// The number of the first tile of adapter l (lora_tile); run by a whole warp.
+__device__ __forceinline__ int lora_first_tile(const int32_t* offsets, int64_t M, int l) {
+  int sum = 0;
+  for (int i = threadIdx.x & 31; i < l; i += 32) {
+    const int64_t n = clamp_pos(offsets[i + 1], M) - clamp_pos(offsets[i], M);
+    sum += n > 0 ? static_cast<int>((n + kLoraTile - 1) / kLoraTile) : 0;
+  }
+  return warp_sum(sum);
+}
+
+template <typename T, int kMode, int RP, bool kDrop>
+__global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs a, const int S) {
+  using L = LoraTcLayout<kMode, RP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
+  uint64_t* empty = full + L::kRing;
+  uint64_t* accFull = empty + L::kRing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accFull + 1);
+  int* rowbuf = reinterpret_cast<int*>(sm + L::kOffRow);  // reduce: the tile's rows; wgrad: a ring of the stages' rows
+  float* mostbuf = reinterpret_cast<float*>(sm + L::kOffMost);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(blockIdx.z);
+  pdl_wait_prior_grids();
+
+  // the work of this cluster: positions [pos0, pos0 + cnt) of adapter l; columns from c0 (wgrad); stages [s0, s0 + ns)
+  int l, ns_all, tile0;
+  int64_t pos0, cnt, c0 = 0;
+  if (kMode != kWgrad) {
+    const LoraTile t = lora_tile(a.offsets, a.L, a.M, blockIdx.x);
+    if (t.l < 0) return;  // the whole cluster
+    l = t.l;
+    pos0 = t.pos;
+    cnt = t.cnt;
+    tile0 = static_cast<int>(blockIdx.x);
+    ns_all = static_cast<int>((a.C + 63) / 64);
+  } else {
+    l = static_cast<int>(blockIdx.y);
+    pos0 = clamp_pos(a.offsets[l], a.M);
+    cnt = clamp_pos(a.offsets[l + 1], a.M) - pos0;
+    c0 = static_cast<int64_t>(blockIdx.x) * 128;
+    if (cnt <= 0) {  // no rows: zeros (the whole cluster returns)
+      T* out = static_cast<T*>(a.O) + l * a.ws;
+      if (rank == 0)
+        for (int i = tid; i < 128 * a.rank; i += kLtcThreads) {
+          const int64_t c = c0 + (a.wc == 1 ? i & 127 : i / a.rank);
+          const int j = a.wc == 1 ? i >> 7 : i % a.rank;
+          if (c < a.C) out[c * a.wc + j * a.wj] = from_f32<T>(0.0f);
+        }
+      return;
+    }
+    ns_all = static_cast<int>((cnt + 63) / 64);
+    tile0 = 0;
+  }
+  const int s0 = static_cast<int>(static_cast<int64_t>(rank) * ns_all / S);
+  const int ns = static_cast<int>(static_cast<int64_t>(rank + 1) * ns_all / S) - s0;  // may be 0 (wgrad)
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kRing; ++i) {
+      mbar_init(&full[i], kLtcLoaders / 32);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(accFull, 1);
+    fence_mbar_init();
+  }
+  if (warp == kLtcLoaders / 32) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  if (kMode != kWgrad && tid < 128) rowbuf[tid] = tid < cnt ? static_cast<int>(lora_row(a, pos0 + tid)) : -1;
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  pdl_allow_dependents();
+  const uint32_t tmem = *tmem_slot;
+  const PhiloxKey key = kDrop ? philox_key(a.drop) : PhiloxKey{0u, 0u, 0u, 0u};
+  const uint16_t* P = static_cast<const uint16_t*>(a.P);
+  const uint16_t* W = static_cast<const uint16_t*>(a.W) + l * a.ws;
+  float f = lora_factor(a, l);
+  float vscale = 1.0f;
+  if (kMode == kWgrad && std::is_same<T, __half>::value && a.most) {
+    const int t0 = lora_first_tile(a.offsets, a.M, l), nt = static_cast<int>((cnt + kLoraTile - 1) / kLoraTile);
+    float most = 0.0f;
+    for (int i = lane; i < nt * a.most_n; i += 32) {
+      const int t = i / a.most_n;
+      most = fmaxf(most, a.most[(t0 + t) * kLoraMostPer + i - t * a.most_n]);
+    }
+    float inv;
+    vscale = split_scale<T>(warp_max(most), inv);
+    f *= inv;
+  }
+
+  bool ok = true;
+  if (warp < kLtcLoaders / 32) {
+    // ------------------------------------------------------------------ loaders
+    constexpr int kQ = kMode == kWgrad ? (RP + 31) / 32 : 1;  // chunks of V per thread and stage
+    constexpr int kWPer = (RP * 8 + kLtcLoaders - 1) / kLtcLoaders;
+    const bool bvec = (a.rank & 7) == 0, vvec = (a.rank & 3) == 0;
+    // P: 16-byte chunk pch of rows prow + 32 i (reduce) or + 16 i (wgrad), i = 0 .. 3
+    const int prow = kMode == kWgrad ? tid >> 4 : tid >> 3, pch = kMode == kWgrad ? tid & 15 : tid & 7;
+    constexpr int kStep = kMode == kWgrad ? 16 : 32;
+    const uint32_t pdst = (kMode == kWgrad ? (pch >> 3) * 8192 : 0) + prow * 128 + (((pch & 7) ^ (prow & 7)) << 4);
+    int64_t m[4];
+    float qv[kQ][8];
+    auto fetch_rows = [&](int i) {  // wgrad: rows and V of stage i, one stage ahead of their use
+      const int64_t r0 = static_cast<int64_t>(s0 + i) * 64;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t r = r0 + prow + 16 * k;
+        m[k] = r < cnt ? lora_row(a, pos0 + r) : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < kQ; ++k) {
+        const int q = tid + kLtcLoaders * k, row = q / (RP / 8), ch = q % (RP / 8);
+        const bool there = q < RP * 8 && r0 + row < cnt;
+        const float* src = a.V + (pos0 + r0 + row) * a.rank + 8 * ch;
+        if (vvec) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 x = there && 8 * ch + 4 * h < a.rank ? *reinterpret_cast<const float4*>(src + 4 * h)
+                                                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            qv[k][4 * h] = x.x;
+            qv[k][4 * h + 1] = x.y;
+            qv[k][4 * h + 2] = x.z;
+            qv[k][4 * h + 3] = x.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) qv[k][e] = there && 8 * ch + e < a.rank ? src[e] : 0.0f;
+        }
+      }
+    };
+    if (kMode == kWgrad) {
+      if (ns > 0) fetch_rows(0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m[k] = rowbuf[prow + 32 * k];
+    }
+    for (int i = 0; i < ns + L::kLag && ok; ++i) {
+      if (i < ns) {
+        const int s = i % L::kRing;
+        if (i >= L::kRing) {
+          ok = mbar_wait(&empty[s], static_cast<uint32_t>((i / L::kRing) - 1) & 1u);
+          if (!ok) break;
+        }
+        uint8_t* st = sm + s * L::kStage;
+        const int64_t c = (kMode == kWgrad ? c0 : static_cast<int64_t>(s0 + i) * 64) + 8 * pch;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool there = m[k] >= 0 && c < a.C;
+          cp_async_16(st + pdst + k * kStep * 128, P + (there ? m[k] * a.C + c : 0), there ? 16u : 0u);
+        }
+        if (kMode == kWgrad) {
+          if (kDrop && pch == 0)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) rowbuf[s * 64 + prow + 16 * k] = static_cast<int>(m[k]);
+#pragma unroll
+          for (int k = 0; k < kQ; ++k) {
+            const int q = tid + kLtcLoaders * k, row = q / (RP / 8), ch = q % (RP / 8);
+            if (q >= RP * 8) continue;
+            uint4 hi, lo;
+            split2<T>(vscale * qv[k][0], vscale * qv[k][1], hi.x, lo.x);
+            split2<T>(vscale * qv[k][2], vscale * qv[k][3], hi.y, lo.y);
+            split2<T>(vscale * qv[k][4], vscale * qv[k][5], hi.z, lo.z);
+            split2<T>(vscale * qv[k][6], vscale * qv[k][7], hi.w, lo.w);
+            uint8_t* wd = st + L::kTileP + row * 128;
+            const int c2 = RP / 8 + ch;
+            *reinterpret_cast<uint4*>(wd + (ch >> 3) * 8192 + (((ch & 7) ^ (row & 7)) << 4)) = hi;
+            *reinterpret_cast<uint4*>(wd + (c2 >> 3) * 8192 + (((c2 & 7) ^ (row & 7)) << 4)) = lo;
+          }
+          if (i + 1 < ns) fetch_rows(i + 1);
+        } else {
+          const int64_t cs = static_cast<int64_t>(s0 + i) * 64;
+#pragma unroll
+          for (int k = 0; k < kWPer; ++k) {
+            const int q = tid + kLtcLoaders * k;
+            if (q >= RP * 8) continue;
+            if (kMode == kReduceA) {
+              const int j = q >> 3, ch = q & 7;
+              const bool there = j < a.rank && cs + 8 * ch < a.C;
+              cp_async_16(st + L::kTileP + j * 128 + ((ch ^ (j & 7)) << 4), W + (there ? j * a.C + cs + 8 * ch : 0),
+                          there ? 16u : 0u);
+            } else {
+              const int row = q / (RP / 8), ch = q % (RP / 8);
+              uint8_t* wd = st + L::kTileP + (ch >> 3) * 8192 + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+              const bool there = cs + row < a.C && 8 * ch < a.rank;
+              const uint16_t* src = W + (there ? (cs + row) * a.rank : 0);
+              if (bvec)
+                cp_async_16(wd, src + (there ? 8 * ch : 0), there ? 16u : 0u);
+              else
+                *reinterpret_cast<uint4*>(wd) = there ? load8(src, 8 * ch, a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
+      }
+      cp_async_commit();
+      const int d = i - L::kLag;
+      if (d < 0) continue;
+      cp_async_wait<L::kLag>();
+      if (kDrop) {
+        uint8_t* st = sm + (d % L::kRing) * L::kStage;
+        const int64_t c = (kMode == kWgrad ? c0 : static_cast<int64_t>(s0 + d) * 64) + 8 * pch;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t mk = kMode == kWgrad ? rowbuf[(d % L::kRing) * 64 + prow + 16 * k] : m[k];
+          uint4* x = reinterpret_cast<uint4*>(st + pdst + k * kStep * 128);
+          if (mk >= 0 && c < a.C) *x = and4(*x, drop_mask16((mk * a.C + c) >> 3, key, a.drop.thr));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[d % L::kRing]);
+    }
+    cp_async_wait<0>();
+    if (ns > 0) ok = ok && mbar_wait(accFull, 0u);
+  } else if (lane == 0) {
+    // ------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
+    constexpr uint32_t kMajor = kMode == kReduceA ? 0u : (kMode == kReduceB ? 1u << 16 : (1u << 15) | (1u << 16));
+    constexpr uint32_t kIdesc = idesc_f16_f32(128, L::kN) | kType | kMajor;
+    constexpr uint32_t kStepA = kMode == kWgrad ? 128u : 2u, kStepB = kMode == kReduceA ? 2u : 128u;
+    const uint32_t base = smem_u32(sm);
+    for (int i = 0; i < ns && ok; ++i) {
+      const int s = i % L::kRing;
+      ok = mbar_wait(&full[s], static_cast<uint32_t>(i / L::kRing) & 1u);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint32_t pa = base + s * L::kStage, wa = pa + L::kTileP;
+      const uint64_t ad = kMode == kWgrad ? sdesc_mnmajor_sw128(pa) : sdesc_kmajor_sw128(pa);
+      const uint64_t bd = kMode == kReduceA ? sdesc_kmajor_sw128(wa) : sdesc_mnmajor_sw128(wa);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) umma_f16(tmem, ad + kStepA * q, bd + kStepB * q, kIdesc, (i | q) != 0 ? 1u : 0u);
+      umma_commit(&empty[s]);
+    }
+    if (ok && ns > 0) umma_commit(accFull);
+  }
+  __syncwarp();
+  tc_fence_after_sync();
+
+  // ------------------------------------------------------------------ sums out of tensor memory
+  // Loader warp w has lanes 32 (w % 4) .. + 31 (position or column r of the tile) and half w / 4 of the inner columns.
+  const int r = tid & 127;
+  float most = 0.0f, most2 = 0.0f;
+  auto emit = [&](int j, float v) {
+    if (j >= a.rank) return;
+    if (kMode == kWgrad) {
+      if (c0 + r < a.C) (static_cast<T*>(a.O) + l * a.ws)[(c0 + r) * a.wc + j * a.wj] = from_f32<T>(f * v);
+    } else if (r < cnt) {
+      const int64_t at = (pos0 + r) * a.rank + j;
+      a.V[at] = f * v;
+      most = fmaxf(most, fabsf(f * v));
+      if (a.most2) most2 = fmaxf(most2, fabsf(a.V2[at]));
+    }
+  };
+  auto sums = [&](int j0, float (&v)[8]) {
+    const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + j0;
+    uint32_t x[8], y[8];
+    if (ok && ns > 0) {
+      tmem_ld_32x32b_x8(at, x);
+      if (kMode == kWgrad) tmem_ld_32x32b_x8(at + RP, y);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[e]) + (kMode == kWgrad ? __uint_as_float(y[e]) : 0.0f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    }
+  };
+  if (S == 1) {
+    if (warp < kLtcLoaders / 32)
+#pragma unroll 1
+      for (int j0 = (warp >> 2) * (RP / 2); j0 < (warp >> 2) * (RP / 2) + RP / 2; j0 += 8) {
+        float v[8];
+        sums(j0, v);
+        if (kMode != kWgrad && (a.rank & 3) == 0) {  // whole float4s of a position's row
+          if (r < cnt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (j0 + 4 * h >= a.rank) continue;
+              const int64_t at = (pos0 + r) * a.rank + j0 + 4 * h;
+              const float4 o = make_float4(f * v[4 * h], f * v[4 * h + 1], f * v[4 * h + 2], f * v[4 * h + 3]);
+              *reinterpret_cast<float4*>(a.V + at) = o;
+              most = fmaxf(fmaxf(fmaxf(fabsf(o.x), fabsf(o.y)), fmaxf(fabsf(o.z), fabsf(o.w))), most);
+              if (a.most2) {
+                const float4 p = *reinterpret_cast<const float4*>(a.V2 + at);
+                most2 = fmaxf(fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(p.z), fabsf(p.w))), most2);
+              }
+            }
+        } else if (kMode == kWgrad && a.wj == 1 && (a.rank & 7) == 0) {  // dB: eight consecutive elements of a row
+          if (c0 + r < a.C && j0 < a.rank) {
+            Vec<T, 8> o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o.v[e] = from_f32<T>(f * v[e]);
+            *reinterpret_cast<Vec<T, 8>*>(static_cast<T*>(a.O) + l * a.ws + (c0 + r) * a.rank + j0) = o;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) emit(j0 + e, v[e]);
+        }
+      }
+  } else {
+    // inner columns [q RP / S, (q + 1) RP / S) are added up by CTA q: partial sums [source][column][128]
+    const int cpo = RP / S;
+    float* red = reinterpret_cast<float*>(sm);
+    const uint32_t red_local = smem_u32(red);
+    cluster_arrive();  // every CTA of the cluster is past its main loop: the rings are free
+    cluster_wait();
+    if (warp < kLtcLoaders / 32)
+#pragma unroll 1
+      for (int j0 = (warp >> 2) * (RP / 2); j0 < (warp >> 2) * (RP / 2) + RP / 2; j0 += 8) {
+        float v[8];
+        sums(j0, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int q = (j0 + e) / cpo;
+          const uint32_t dst = red_local + 4u * static_cast<uint32_t>((rank * cpo + (j0 + e) - q * cpo) * 128 + r);
+          st_shared_cluster_f32(mapa_shared(dst, static_cast<uint32_t>(q)), v[e]);
+        }
+      }
+    cluster_arrive();  // all partial sums have landed
+    cluster_wait();
+    if (warp < kLtcLoaders / 32)
+      for (int j = tid >> 7; j < cpo; j += 2) {
+        float v = 0.0f;
+        for (int src = 0; src < S; ++src) v += red[(src * cpo + j) * 128 + r];
+        emit(rank * cpo + j, v);
+      }
+  }
+  if (kMode != kWgrad && a.most) {
+    most = warp_max(most);
+    most2 = warp_max(most2);
+    if (lane == 0 && warp < kLtcLoaders / 32) {
+      mostbuf[warp] = most;
+      mostbuf[16 + warp] = most2;
+    }
+    __syncthreads();
+    if (tid < 2) {
+      float x = 0.0f;
+      for (int i = 0; i < kLtcLoaders / 32; ++i) x = fmaxf(x, mostbuf[16 * tid + i]);
+      float* to = tid == 0 ? a.most : a.most2;
+      if (to) to[tile0 * kLoraMostPer + rank] = x;
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kLtcLoaders / 32) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+// CTAs per cluster for `ctas` tiles of `stages` stages: time goes as (waves of CTAs) / S, and a split must leave each CTA eight
+// stages to be worth the exchange.
+static int lora_split(int64_t ctas, int64_t stages, int rp) {
+  const int64_t sms = current_device_info().num_sms;
+  int best = 1;
+  double cost = static_cast<double>((ctas + sms - 1) / sms);
+  for (int S = 2; S <= 8 && S * 8 <= stages && rp / S >= 2; S *= 2) {
+    const double c = static_cast<double>((ctas * S + sms - 1) / sms) / S;
+    if (c < 0.95 * cost) {
+      cost = c;
+      best = S;
+    }
+  }
+  return best;
+}
+
+static int lora_pad_rank(int rank) { return rank <= 16 ? 16 : (rank <= 32 ? 32 : (rank <= 64 ? 64 : 128)); }
+
+template <typename T, int kMode, int RP, bool kDrop>
+static cudaError_t launch_lora_tc(const LoraArgs& a, dim3 grid, cudaStream_t s) {
+  auto* kern = lora_tc_kernel<T, kMode, RP, kDrop>;
+  constexpr int kAlloc = LoraTcLayout<kMode, RP>::kAlloc;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kAlloc);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kLtcThreads);
+  cfg.dynamicSmemBytes = kAlloc;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = grid.z;
+  cfg.attrs = attr;
+  cfg.numAttrs = grid.z > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, static_cast<int>(grid.z));
+}
+
+// Clusters that reduce a call's tiles (the maxima of its tiles have one slot per CTA).
+static int lora_reduce_split(const LoraArgs& a) {
+  return lora_split((a.M + kLoraTile - 1) / kLoraTile, (a.C + 63) / 64, lora_pad_rank(a.rank));
+}
+
+static cudaError_t lora_fast_reduce(bool bf16, const LoraArgs& a, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(lora_max_tiles(a.M, a.L)), 1, static_cast<unsigned>(lora_reduce_split(a)));
+  return with_type16(bf16, [&](auto t) {
+    using T = decltype(t);
+    return with_rank(a.rank, [&](auto rp) {
+      constexpr int RP = decltype(rp)::value;
+      if (a.wc != 1) return launch_lora_tc<T, kReduceB, RP, false>(a, grid, s);
+      return a.drop.thr ? launch_lora_tc<T, kReduceA, RP, true>(a, grid, s)
+                        : launch_lora_tc<T, kReduceA, RP, false>(a, grid, s);
+    });
+  });
+}
+
+static cudaError_t lora_fast_wgrad(bool bf16, const LoraArgs& a, cudaStream_t s) {
+  const int64_t ct = (a.C + 127) / 128, some = a.L < a.M ? a.L : (a.M < 1 ? 1 : a.M);
+  const int S = lora_split(ct * some, a.M / some / 64, lora_pad_rank(a.rank));
+  const dim3 grid(static_cast<unsigned>(ct), static_cast<unsigned>(a.L), static_cast<unsigned>(S));
+  return with_type16(bf16, [&](auto t) {
+    using T = decltype(t);
+    return with_rank(a.rank, [&](auto rp) {
+      constexpr int RP = decltype(rp)::value;
+      return a.drop.thr ? launch_lora_tc<T, kWgrad, RP, true>(a, grid, s)
+                        : launch_lora_tc<T, kWgrad, RP, false>(a, grid, s);
+    });
+  });
+}
+
 constexpr int kLoraGeneric = 3;  // TQ_PATH_GENERIC
 
 cudaError_t launch_lora_reduce(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {
-  return lora_generic_reduce(bf16, a, s);
+  return path == kLoraGeneric ? lora_generic_reduce(bf16, a, s) : lora_fast_reduce(bf16, a, s);
 }
 cudaError_t launch_lora_expand(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {
   return path == kLoraGeneric ? lora_generic_expand(bf16, a, s) : lora_fast_expand(bf16, a, s);
 }
 cudaError_t launch_lora_wgrad(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {
-  return lora_generic_wgrad(bf16, a, s);
+  return path == kLoraGeneric ? lora_generic_wgrad(bf16, a, s) : lora_fast_wgrad(bf16, a, s);
 }
+
+// Workspace of the gradients: dv fp32 [M, rank], then the tiles' maxima of v and of dv.
+int64_t lora_workspace_floats(int64_t M, int64_t rank) { return (M * rank + 3) / 4 * 4; }
+int64_t lora_most_floats(int64_t M, int64_t L) { return lora_max_tiles(M, L) * kLoraMostPer; }
 
 }  // namespace tq

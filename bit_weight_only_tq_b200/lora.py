@@ -20,7 +20,7 @@ import torch
 from . import HEADER, PATH_AUTO, PATH_DECODE, TQ_F16, _check, _i64, _int, _vp, header_functions, lib
 from .moe import TQ_BF16, _arg, _device, _dtype, _empty, _opt, _raw, _shape2
 
-__all__ = ["tq_lora", "tq_lora_backward", "tq_lora_path", "tq_dropout", "tq_gemm_backward", "w4g_gemm_backward"]
+__all__ = ["tq_lora", "tq_lora_backward", "tq_lora_path", "tq_lora_workspace_size", "tq_dropout", "tq_gemm_backward", "w4g_gemm_backward"]
 
 LORA_HEADER = os.path.join(os.path.dirname(HEADER), "tq_lora.h")
 
@@ -28,7 +28,8 @@ _f64 = ctypes.c_double
 _SIGS = {
     "tq_lora": [_vp, _int] + [_vp] * 8 + [_f64, _vp] + [_i64] * 4 + [_int, _int, _vp],
     "tq_lora_path": [_i64] * 4 + [_int] * 3,
-    "tq_lora_backward": [_vp, _vp, _int] + [_vp] * 11 + [_f64, _vp] + [_i64] * 4 + [_int, _int, _vp],
+    "tq_lora_workspace_size": [_i64, _i64, _int],
+    "tq_lora_backward": [_vp, _vp, _int] + [_vp] * 5 + [ctypes.c_size_t] + [_vp] * 6 + [_f64, _vp] + [_i64] * 4 + [_int, _int, _vp],
     "tq_dropout": [_vp, _int, _vp, _f64, _vp, _i64, _i64, _vp],
     "tq_gemm_backward": [_vp] * 4 + [_i64] * 3 + [_int, _vp],
     "w4g_gemm_backward": [_vp] * 5 + [_i64] * 3 + [_int, _vp],
@@ -36,7 +37,7 @@ _SIGS = {
 for _name, _args in _SIGS.items():
     _f = getattr(lib, _name)
     _f.argtypes = _args
-    _f.restype = ctypes.c_int
+    _f.restype = ctypes.c_size_t if _name == "tq_lora_workspace_size" else ctypes.c_int
 
 _DTYPES16 = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
 
@@ -97,11 +98,12 @@ def tq_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, base, offsets: to
 
 
 def tq_lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, v: torch.Tensor, base_dx,
-                     offsets: torch.Tensor, order=None, scaling=None, p: float = 0.0, rng=None, dv=None, dx=None,
-                     da=None, db=None, need_dx: bool = True, need_ab: bool = True, path: int = PATH_AUTO, stream=None):
+                     offsets: torch.Tensor, order=None, scaling=None, p: float = 0.0, rng=None, workspace=None,
+                     dx=None, da=None, db=None, need_dx: bool = True, need_ab: bool = True, path: int = PATH_AUTO, stream=None):
     """Gradients of tq_lora from dy [M, N], the call's inputs and its v -> (dx [M, K], da like a, db like b), each None
     where it is not wanted.  dx is base_dx [M, K] (the projection's gradient for x; None: zeros) plus the adapters'
-    part and may be base_dx; an adapter without rows gets zeros.  dv: fp32 [M, rank] scratch."""
+    part and may be base_dx; an adapter without rows gets zeros.  workspace: uint8, tq_lora_workspace_size(M, L, rank) bytes
+    or more (allocated here when it is left out)."""
     dt, dev = _dtype16(x, "x"), _device()
     M, K, L, r, N = _adapters(x, a, b)
     d = x.dtype
@@ -112,11 +114,14 @@ def tq_lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torc
         da = _empty3(a, stream)
     if need_ab and db is None:
         db = _empty3(b, stream)
-    if dv is None:
-        dv = _empty(x, (M, r), torch.float32, stream)
+    if workspace is None:
+        workspace = _empty(x, (lib.tq_lora_workspace_size(M, L, r),), torch.uint8, stream)
+    elif workspace.dim() != 1:
+        raise ValueError("workspace must have 1 dims")
     _check(lib.tq_lora_backward(pd, _arg(x, "x", d, (M, K), dev), dt, _arg(a, "a", d, (L, r, K), dev),
                                 _arg(b, "b", d, (L, N, r), dev), _opt(scaling, "scaling", torch.float32, (L,), dev),
-                                _arg(v, "v", torch.float32, (M, r), dev), _arg(dv, "dv", torch.float32, (M, r), dev),
+                                _arg(v, "v", torch.float32, (M, r), dev),
+                                _arg(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(),
                                 _opt(base_dx, "base_dx", d, (M, K), dev), _opt(dx, "dx", d, (M, K), dev),
                                 _opt(da, "da", d, (L, r, K), dev), _opt(db, "db", d, (L, N, r), dev),
                                 _arg(offsets, "offsets", torch.int32, (L + 1,), dev),
@@ -135,6 +140,11 @@ def _empty3(like, stream):
 def tq_lora_path(M: int, L: int, N: int, K: int, rank: int, dropout: bool = False, aligned: bool = True) -> int:
     """The path PATH_AUTO takes for M rows of L adapters."""
     return int(lib.tq_lora_path(int(M), int(L), int(N), int(K), int(rank), 1 if dropout else 0, 1 if aligned else 0))
+
+
+def tq_lora_workspace_size(M: int, L: int, rank: int) -> int:
+    """Bytes of workspace that tq_lora_backward needs (0: invalid sizes)."""
+    return int(lib.tq_lora_workspace_size(int(M), int(L), int(rank)))
 
 
 def tq_dropout(x: torch.Tensor, p: float, rng, out=None, stream=None) -> torch.Tensor:

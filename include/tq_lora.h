@@ -83,20 +83,26 @@ TQ_API int tq_lora_path(int64_t M, int64_t L, int64_t N, int64_t K, int rank, in
 /* --------------------------------------------------------------------------------------------
  * tq_lora_backward -- the gradients of tq_lora, from dy [M, N] and the forward call's x, a, b, scaling,
  * plan, p, rng and v:
- *   dv[r]    = scaling[l] dy[m] B_l              scratch fp32 [M, rank], by sorted position
+ *   dv[r]    = scaling[l] dy[m] B_l              fp32 [M, rank], by sorted position, in the workspace
  *   dx[m]    = base_dx[m] + drop'(dv[r] A_l)     drop': zero where drop(x) dropped, else times the same factor
  *   da_l     = sum over its rows of dv[r]^T drop(x[m])             [L, rank, K]
  *   db_l     = scaling[l] sum over its rows of dy[m]^T v[r]        [L, N, rank]
  *   (r: sorted position, m: its row).  An adapter without rows gets zeros.
+ *   v        fp32 [M, rank], as tq_lora left it
+ *   workspace  tq_lora_workspace_size() bytes or more (TQ_ERR_SHAPE), 16-byte aligned (TQ_ERR_ALIGN); nothing in it lasts
+ *            from call to call.  Calls (or captured graphs) that may run at once need one each.
  *   base_dx  [M, K], or NULL for zeros; may be `dx` (the projection's own gradient for x, to which this adds)
  *   dx, da, db  each may be NULL (not wanted).  None may overlap what the call reads (dx may be base_dx).
  *   path     AUTO, PREFILL or GENERIC, with the conditions of tq_lora on all of the tensors.
  * The gradient for base is dy itself; `scaling` has none.  Sums are taken in a fixed order.
  * ------------------------------------------------------------------------------------------ */
 TQ_API int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, const void* b,
-                            const float* scaling, const float* v, float* dv, const void* base_dx, void* dx, void* da,
-                            void* db, const int32_t* offsets, const int32_t* order, double p, const int64_t* rng,
+                            const float* scaling, const float* v, void* workspace, size_t workspace_bytes,
+                            const void* base_dx, void* dx, void* da, void* db, const int32_t* offsets, const int32_t* order, double p, const int64_t* rng,
                             int64_t M, int64_t L, int64_t N, int64_t K, int rank, int path, void* stream);
+
+/* Bytes of workspace that tq_lora_backward needs (host arithmetic only; 0: invalid sizes). */
+TQ_API size_t tq_lora_workspace_size(int64_t M, int64_t L, int rank);
 
 /* --------------------------------------------------------------------------------------------
  * tq_dropout -- out = drop(x), x and out [M, K] of `dtype` (TQ_F32, TQ_F16, TQ_BF16); out may be x.  Its

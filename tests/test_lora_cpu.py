@@ -27,10 +27,10 @@ def _fwd(x=P, dtype=1, a=P, b=P, scaling=None, base=P, out=P, v=P, off=P, order=
     return tq.lib.tq_lora(x, dtype, a, b, scaling, base, out, v, off, order, p, rng, M, L, N, K, rank, path, None)
 
 
-def _bwd(dy=P, x=P, dtype=1, a=P, b=P, scaling=None, v=P, dv=P, base_dx=P, dx=P, da=P, db=P, off=P, order=None, p=0.0, rng=None,
+def _bwd(dy=P, x=P, dtype=1, a=P, b=P, scaling=None, v=P, ws=P, ws_bytes=1 << 30, base_dx=P, dx=P, da=P, db=P, off=P, order=None, p=0.0, rng=None,
          M=4, L=2, N=64, K=64, rank=8, path=0):
-    return tq.lib.tq_lora_backward(dy, x, dtype, a, b, scaling, v, dv, base_dx, dx, da, db, off, order, p, rng, M, L, N, K, rank,
-                                   path, None)
+    return tq.lib.tq_lora_backward(dy, x, dtype, a, b, scaling, v, ws, ws_bytes, base_dx, dx, da, db, off, order, p, rng, M, L, N,
+                                   K, rank, path, None)
 
 
 @pytest.mark.parametrize("f", [_fwd, _bwd])
@@ -56,13 +56,17 @@ def test_forward_argument_errors():
 
 
 def test_backward_argument_errors():
-    for name in ("dy", "x", "b", "dv", "v", "a"):
+    for name in ("dy", "x", "b", "ws", "v", "a"):
         assert _bwd(**{name: None}) == -1, name
     assert _bwd(dx=None, da=None, db=None, off=None) == 0           # nothing wanted
     assert _bwd(path=tq.PATH_DECODE) == -8
     assert _bwd(K=63, path=tq.PATH_PREFILL) == -8 and _bwd(N=62, path=tq.PATH_PREFILL) == -8
-    for name in ("dy", "x", "a", "b", "v", "dv", "base_dx", "dx", "da", "db"):
+    for name in ("dy", "x", "a", "b", "v", "ws", "base_dx", "dx", "da", "db"):
         assert _bwd(**{name: Q}, path=tq.PATH_PREFILL) == -3, name
+    need = tq.tq_lora_workspace_size(4, 2, 8)
+    assert need >= 4 * 4 * 8 and _bwd(ws_bytes=need - 1) == -2
+    for M, L, r in ((-1, 2, 8), (4, 0, 8), (4, 1025, 8), (4, 2, 0), (4, 2, 129), (2 ** 31, 2, 8)):
+        assert tq.tq_lora_workspace_size(M, L, r) == 0
 
 
 def test_dropout_argument_errors():
