@@ -63,6 +63,7 @@ extern "C" {
 int tq_lora_path(int64_t M, int64_t L, int64_t N, int64_t K, int rank, int dropout, int aligned) {
   if (M < 0 || L < 1 || N < 0 || K < 1 || rank < 1) return TQ_ERR_SHAPE;
   if (M == 0 || N == 0 || !aligned || !lora_fast_shape(N, K)) return TQ_PATH_GENERIC;
+  if (!dropout && M <= 64) return TQ_PATH_DECODE;
   return TQ_PATH_PREFILL;
 }
 
@@ -76,12 +77,19 @@ int tq_lora(const void* x, int dtype, const void* a, const void* b, const float*
   const bool al = aligned16(x) && aligned16(a) && aligned16(b) && aligned16(base) && aligned16(out) && aligned16(v);
   if (path == TQ_PATH_AUTO) {
     path = tq_lora_path(M, L, N, K, rank, drop.thr != 0, al ? 1 : 0);
+    if (path == TQ_PATH_PREFILL && !v && !drop.thr && M <= tq::kLoraFewMaxRows) path = TQ_PATH_DECODE;
   } else if (path != TQ_PATH_GENERIC) {
-    if (!lora_fast_shape(N, K) || (path == TQ_PATH_DECODE && drop.thr)) return TQ_ERR_PATH;
+    if (!lora_fast_shape(N, K)) return TQ_ERR_PATH;
+    if (path == TQ_PATH_DECODE && (drop.thr || M > tq::kLoraFewMaxRows)) return TQ_ERR_PATH;
     if (!al) return TQ_ERR_ALIGN;
   }
-  if (!v) return TQ_ERR_NULL;
   const bool bf16 = dtype == TQ_BF16;
+  if (path == TQ_PATH_DECODE)
+    return to_status(tq::launch_lora_few(
+        bf16,
+        tq::LoraFewArgs{x, a, b, base, out, v, scaling, offsets, order, M, N, K, static_cast<int>(L), rank},
+        as_stream(stream)));
+  if (!v) return TQ_ERR_NULL;
   tq::LoraArgs s = lora_sum(x, a, true, K, rank, M, L, v, scaling, offsets, order);
   s.drop = drop;
   const cudaError_t e = tq::launch_lora_reduce(bf16, path, s, as_stream(stream));

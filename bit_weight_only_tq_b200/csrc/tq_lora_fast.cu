@@ -856,6 +856,239 @@ static cudaError_t lora_fast_wgrad(bool bf16, const LoraArgs& a, cudaStream_t s)
   });
 }
 
+// ---------------------------------------------------------------------------------------------
+// Few rows: one launch.  A cluster of eight CTAs takes up to eight positions of one adapter: each CTA sums an eighth of the columns
+// of x (m16n8k16: 16 inner columns x 8 positions), the partial sums meet through distributed shared memory in rank order,
+// and each CTA then computes an eighth of the columns of out (16 x 8: 8 positions, rows 8 .. 15 unused, x 8 columns).
+// Bound by the latency of this chain and, with many adapters, by reading each one's A and B once from HBM: B is asked into L2 before
+// A is read, and a warp holds the first 32 columns of its part of B and base in registers before the partial sums meet.
+// Operand fragments come straight from memory: within 32 k, lane t of a quad takes the eight consecutive k = 8 t .. 8 t + 7 (both
+// operands the same, so the order within the sum does not matter) in one 16-byte load.
+// ---------------------------------------------------------------------------------------------
+constexpr int kFewThreads = 256;
+constexpr int kFewRows = 8;
+constexpr int kFewCluster = 8;
+
+struct LoraFewArgs {
+  const void* x;
+  const void* A;
+  const void* B;
+  const void* base;
+  void* out;
+  float* V;  // may be null
+  const float* scaling;
+  const int32_t* offsets;
+  const int32_t* order;
+  int64_t M, N, K;
+  int L, rank;
+};
+
+// adapter_of by a whole warp: two dependent loads (1024 adapters take at most 33 steps of 32 offsets).
+__device__ __forceinline__ int adapter_of_warp(const int32_t* offsets, int L, int64_t r) {
+  const int lane = threadIdx.x & 31;
+  const int step = (L + 32) / 32;  // 32 steps cover the L + 1 offsets
+  const int i0 = lane * step;
+  const uint32_t below = __ballot_sync(0xFFFFFFFFu, i0 <= L && offsets[i0 <= L ? i0 : L] <= r);
+  if (!below) return -1;
+  const int seg = (31 - __clz(below)) * step;
+  int last = seg;
+  for (int j = 1; j < step; j += 32) {
+    const int i = seg + j + lane;
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, j + lane < step && i <= L && offsets[i <= L ? i : L] <= r);
+    if (b) last = seg + j + (31 - __clz(b));
+  }
+  return last < L ? last : -1;
+}
+
+template <typename T, int RP>
+__global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const LoraFewArgs a) {
+  constexpr int RT = RP / 16;                 // tiles of 16 inner columns
+  constexpr int KG = RP < 32 ? 1 : RP / 32;   // groups of 32 inner columns (RP = 16: one of 16)
+  __shared__ float red[8][RP * kFewRows];     // partial sums of the warps: [inner column][position]
+  __shared__ float part[RP * kFewRows];       // of the CTA
+  __shared__ float vs[kFewRows][RP];
+  pdl_allow_dependents();
+  pdl_wait_prior_grids();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int rank = static_cast<int>(blockIdx.x);  // in the cluster
+  const int64_t r = blockIdx.y;
+  const int l = adapter_of_warp(a.offsets, a.L, r);
+  // columns of out of this CTA, in blocks of 32
+  const int64_t nblk = (a.N + 31) / 32;
+  const int64_t b0 = rank * nblk / kFewCluster, b1 = (rank + 1) * nblk / kFewCluster;
+  auto row_of = [&](int64_t q) {
+    const int64_t m = a.order ? static_cast<int64_t>(a.order[q]) : q;
+    return m >= 0 && m < a.M ? m : -1;
+  };
+  if (l < 0) {  // a row of no adapter: base alone
+    const int64_t m = row_of(r);
+    if (m < 0 || a.base == a.out) return;
+    const int64_t c1 = b1 * 32 < a.N ? b1 * 32 : a.N;
+    for (int64_t c = b0 * 32 + 8 * tid; c < c1; c += 8 * kFewThreads)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + m * a.N + c) =
+          a.base ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.base) + m * a.N + c)
+                 : make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  const int64_t first = a.offsets[l] < 0 ? 0 : a.offsets[l];
+  if ((r - first) % kFewRows != 0) return;  // another cluster's
+  const int64_t end = a.offsets[l + 1] < a.M ? a.offsets[l + 1] : a.M;
+  const int cnt = static_cast<int>(end - r < kFewRows ? end - r : kFewRows);
+  const int64_t m = g < cnt ? row_of(r + g) : -1;  // of this lane's position
+  const T* A = static_cast<const T*>(a.A) + static_cast<int64_t>(l) * a.rank * a.K;
+  const T* B = static_cast<const T*>(a.B) + static_cast<int64_t>(l) * a.rank * a.N;
+  const bool bvec = (a.rank & 7) == 0;
+  {
+    const char* p0 = reinterpret_cast<const char*>(B + b0 * 32 * a.rank);
+    const char* p1 = reinterpret_cast<const char*>(B + (b1 * 32 < a.N ? b1 * 32 : a.N) * a.rank);
+    for (const char* p = p0 + 128 * tid; p < p1; p += 128 * kFewThreads)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+  }
+
+  // ---- an eighth of x A^T, groups of 32 columns dealt to the warps
+  float acc[RT][4] = {};
+  const int64_t ng = (a.K + 31) / 32, g0 = rank * ng / kFewCluster, g1 = (rank + 1) * ng / kFewCluster;
+  const T* xrow = static_cast<const T*>(a.x) + (m >= 0 ? m * a.K : 0);
+#pragma unroll 2
+  for (int64_t q = g0 + warp; q < g1; q += 8) {
+    const int64_t k = 32 * q + 8 * t;
+    const uint4 xv = m >= 0 ? load8(xrow, k, a.K, true) : make_uint4(0u, 0u, 0u, 0u);
+    uint4 lo[RT], hi[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int j = 16 * i + g;
+      lo[i] = j < a.rank ? load8(A + j * a.K, k, a.K, true) : make_uint4(0u, 0u, 0u, 0u);
+      hi[i] = j + 8 < a.rank ? load8(A + (j + 8) * a.K, k, a.K, true) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      mma16(acc[i], lo[i].x, hi[i].x, lo[i].y, hi[i].y, xv.x, xv.y, T());
+      mma16(acc[i], lo[i].z, hi[i].z, lo[i].w, hi[i].w, xv.z, xv.w, T());
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    *reinterpret_cast<float2*>(&red[warp][(16 * i + g) * kFewRows + 2 * t]) = make_float2(acc[i][0], acc[i][1]);
+    *reinterpret_cast<float2*>(&red[warp][(16 * i + g + 8) * kFewRows + 2 * t]) = make_float2(acc[i][2], acc[i][3]);
+  }
+
+  // ---- B and base of this warp's first 32 columns, while the partial sums meet
+  uint4 bw[KG][4], yv;
+  auto load_block = [&](int64_t blk) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // column 8 (g / 2) + 2 j + g % 2 of the block is column g of tile j
+      const int64_t n = 32 * blk + 8 * (g >> 1) + 2 * j + (g & 1);
+      const bool there = blk < b1 && n < a.N;
+      const T* row = B + (there ? n * a.rank : 0);
+#pragma unroll
+      for (int q = 0; q < KG; ++q) {
+        if (RP >= 32) {
+          bw[q][j] = there ? load8(row, 32 * q + 8 * t, a.rank, bvec) : make_uint4(0u, 0u, 0u, 0u);
+        } else {  // k = 4 t .. 4 t + 3
+          uint16_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            h[e] = there && 4 * t + e < a.rank ? reinterpret_cast<const uint16_t*>(row)[4 * t + e] : static_cast<uint16_t>(0);
+          bw[q][j] = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), 0u, 0u);
+          if ((a.rank & 3) == 0) {
+            const uint2 w = there && 4 * t < a.rank ? *reinterpret_cast<const uint2*>(row + 4 * t) : make_uint2(0u, 0u);
+            bw[q][j] = make_uint4(w.x, w.y, 0u, 0u);
+          }
+        }
+      }
+    }
+    const int64_t c = 32 * blk + 8 * t;
+    yv = a.base && m >= 0 && blk < b1 && c < a.N
+             ? *reinterpret_cast<const uint4*>(static_cast<const T*>(a.base) + m * a.N + c)
+             : make_uint4(0u, 0u, 0u, 0u);
+  };
+  int64_t blk = b0 + warp;
+  load_block(blk);
+
+  __syncthreads();
+  for (int i = tid; i < RP * kFewRows; i += kFewThreads) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += red[w][i];
+    part[i] = s;
+  }
+  cluster_arrive();
+  cluster_wait();
+  for (int i = tid; i < RP * kFewRows; i += kFewThreads) {
+    const uint32_t at = smem_u32(&part[i]);
+    float p[kFewCluster], s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kFewCluster; ++q) p[q] = ld_shared_cluster_f32(mapa_shared(at, static_cast<uint32_t>(q)));
+#pragma unroll
+    for (int q = 0; q < kFewCluster; ++q) s += p[q];
+    const int j = i / kFewRows, pos = i % kFewRows;
+    vs[pos][j] = s;
+    if (a.V && rank == 0 && pos < cnt && j < a.rank) a.V[(r + pos) * a.rank + j] = s;
+  }
+  cluster_arrive();  // this CTA has read the others' partial sums; waited for at the end
+  __syncthreads();
+
+  // ---- fragments of v: position g, hi and lo, in the order of k of load_block
+  uint32_t hi[KG][4], lo[KG][4];
+  float f;
+  {
+    float most = 0.0f, v[KG][8];
+#pragma unroll
+    for (int q = 0; q < KG; ++q)
+#pragma unroll
+      for (int e = 0; e < (RP < 32 ? 4 : 8); ++e) {
+        const int j = RP < 32 ? 4 * t + e : 32 * q + 8 * t + e;
+        v[q][e] = j < a.rank ? vs[g][j] : 0.0f;
+        most = fmaxf(most, fabsf(v[q][e]));
+      }
+    most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+    most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+    const float s = split_scale<T>(most, f);
+    if (a.scaling) f *= a.scaling[l];
+#pragma unroll
+    for (int q = 0; q < KG; ++q)
+#pragma unroll
+      for (int e = 0; e < (RP < 32 ? 2 : 4); ++e) split2<T>(s * v[q][2 * e], s * v[q][2 * e + 1], hi[q][e], lo[q][e]);
+  }
+  while (blk < b1) {
+    float d[4][4] = {};
+#pragma unroll
+    for (int q = 0; q < KG; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mma16(d[j], hi[q][0], 0u, hi[q][1], 0u, bw[q][j].x, bw[q][j].y, T());
+        mma16(d[j], lo[q][0], 0u, lo[q][1], 0u, bw[q][j].x, bw[q][j].y, T());
+        if (RP >= 32) {
+          mma16(d[j], hi[q][2], 0u, hi[q][3], 0u, bw[q][j].z, bw[q][j].w, T());
+          mma16(d[j], lo[q][2], 0u, lo[q][3], 0u, bw[q][j].z, bw[q][j].w, T());
+        }
+      }
+    Vec<T, 8> y = *reinterpret_cast<const Vec<T, 8>*>(&yv);
+    const int64_t c = 32 * blk + 8 * t;
+    blk += 8;
+    load_block(blk);
+    if (m >= 0 && c < a.N) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y.v[e] = from_f32<T>(fmaf(f, d[e >> 1][e & 1], to_f32(y.v[e])));
+      *reinterpret_cast<Vec<T, 8>*>(static_cast<T*>(a.out) + m * a.N + c) = y;
+    }
+  }
+  cluster_wait();  // the others may still be reading this CTA's partial sums
+}
+
+// Rows that one launch of the kernel above may cover (grid y).
+constexpr int64_t kLoraFewMaxRows = 65535;
+
+cudaError_t launch_lora_few(bool bf16, const LoraFewArgs& a, cudaStream_t s) {
+  return with_type16(bf16, [&](auto t) {
+    using T = decltype(t);
+    return with_rank(a.rank, [&](auto rp) {
+      return launch_pdl(lora_few_kernel<T, decltype(rp)::value>,
+                        dim3(kFewCluster, static_cast<unsigned>(a.M)), dim3(kFewThreads), 0, kFewCluster, s, a);
+    });
+  });
+}
+
 constexpr int kLoraGeneric = 3;  // TQ_PATH_GENERIC
 
 cudaError_t launch_lora_reduce(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {

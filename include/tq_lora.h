@@ -67,7 +67,7 @@ extern "C" {
  *   path     TQ_PATH_AUTO, or one path (tests): DECODE takes few rows (one launch, up to 8 rows of an
  *            adapter per pass over its weights), PREFILL many (tensor cores), GENERIC any shape and
  *            alignment.  DECODE and PREFILL need K % 8 == 0 and N % 8 == 0 (TQ_ERR_PATH) and 16-byte aligned x, a,
- *            b, base, out and v (TQ_ERR_ALIGN).  DECODE needs p = 0 (TQ_ERR_PATH).
+ *            b, base, out and v (TQ_ERR_ALIGN).  DECODE needs p = 0 and M <= 65535 (TQ_ERR_PATH).
  *            Every path is right for any numbers of rows per adapter.
  * 1 <= L <= 1024, 1 <= rank <= 128, 0 < K, N <= 2^24 (N = 0: nothing), 0 <= M < 2^31.
  * M == 0 or N == 0: nothing is launched.
