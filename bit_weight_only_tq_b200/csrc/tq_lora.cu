@@ -42,12 +42,14 @@ struct LoraArgs {
   int64_t wc, wj, ws;
   int L, rank;
   bool use_scaling;         // f includes scaling[l]
-  // Tensor-core wgrad scales V by one power of two per adapter, from the largest magnitude that reduce found in each tile of V and
-  // of V2 (kLoraMostPer slots per tile, of which its most_n CTAs write one each); null: not wanted
+  // Tensor-core reduce: the largest magnitude that each CTA of a tile wrote to V (most) and found in V2 (most2), kLoraMostPer slots
+  // per tile; null: not wanted
   const float* V2;
   float* most;
   float* most2;
-  int most_n;
+  // Tensor-core wgrad: V as hi and lo [M, 2 padded rank], scaled by 1 / inv[l]
+  const void* Q;
+  const float* inv;
 };
 
 constexpr int kLoraMostPer = 8;

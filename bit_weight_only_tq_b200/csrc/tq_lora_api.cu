@@ -102,7 +102,7 @@ int tq_lora(const void* x, int dtype, const void* a, const void* b, const float*
 
 size_t tq_lora_workspace_size(int64_t M, int64_t L, int rank) {
   if (M < 0 || M > kLoraMaxRows || L < 1 || L > TQ_LORA_MAX_ADAPTERS || rank < 1 || rank > TQ_LORA_MAX_RANK) return 0;
-  return static_cast<size_t>(tq::lora_workspace_floats(M, rank) + 2 * tq::lora_most_floats(M, L)) * sizeof(float);
+  return tq::lora_workspace(nullptr, M, L, rank).bytes;
 }
 
 int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, const void* b, const float* scaling,
@@ -129,40 +129,42 @@ int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, co
   const bool bf16 = dtype == TQ_BF16;
   cudaStream_t s = as_stream(stream);
   cudaError_t e = cudaSuccess;
-  float* dv = static_cast<float*>(workspace);
-  // fp16 on the tensor cores: the largest |v| and |dv| of each tile, for the powers of two of da and db
-  const bool most = path != TQ_PATH_GENERIC && !bf16;
-  float* most_v = most ? dv + tq::lora_workspace_floats(M, rank) : nullptr;
-  float* most_dv = most ? most_v + tq::lora_most_floats(M, L) : nullptr;
-  int most_n = 0;
-  if (M > 0 && (dx || da || most)) {
-    tq::LoraArgs g = lora_sum(dy, b, false, N, rank, M, L, dv, scaling, offsets, order);
-    g.V2 = v;
-    g.most = most_dv;
-    g.most2 = most_v;
-    most_n = tq::lora_reduce_split(g);
+  const tq::LoraWorkspace w = tq::lora_workspace(workspace, M, L, rank);
+  const bool tc = path != TQ_PATH_GENERIC;
+  const bool scaled = tc && !bf16;  // the powers of two of v and dv are found on the way
+  if (M > 0 && (dx || da || scaled)) {
+    tq::LoraArgs g = lora_sum(dy, b, false, N, rank, M, L, w.dv, scaling, offsets, order);
+    if (scaled) {
+      g.V2 = v;
+      g.most2 = w.most[0];
+      g.most = w.most[1];
+    }
     e = tq::launch_lora_reduce(bf16, path, g, s);
+    if (e == cudaSuccess && tc && (da || db))
+      e = tq::launch_lora_split(bf16, da != nullptr, w, v, offsets, M, L, rank, tq::lora_reduce_split(g), s);
+  } else if (M > 0 && tc && db) {
+    e = tq::launch_lora_split(bf16, false, w, v, offsets, M, L, rank, 1, s);
   }
   if (e == cudaSuccess && dx && M > 0) {
-    tq::LoraArgs g = lora_sum(nullptr, a, true, K, rank, M, L, dv, scaling, offsets, order);
+    tq::LoraArgs g = lora_sum(nullptr, a, true, K, rank, M, L, w.dv, scaling, offsets, order);
     g.base = base_dx;
     g.O = dx;
     g.drop = drop;
     e = tq::launch_lora_expand(bf16, path, g, s);
   }
   if (e == cudaSuccess && da) {
-    tq::LoraArgs g = lora_sum(x, nullptr, true, K, rank, M, L, dv, scaling, offsets, order);
+    tq::LoraArgs g = lora_sum(x, nullptr, true, K, rank, M, L, w.dv, scaling, offsets, order);
     g.O = da;
     g.drop = drop;
-    g.most = most_dv;
-    g.most_n = most_n;
+    g.Q = w.Q[1];
+    g.inv = w.inv[1];
     e = tq::launch_lora_wgrad(bf16, path, g, s);
   }
   if (e == cudaSuccess && db && N > 0) {
     tq::LoraArgs g = lora_sum(dy, nullptr, false, N, rank, M, L, const_cast<float*>(v), scaling, offsets, order);
     g.O = db;
-    g.most = most_v;
-    g.most_n = most_n;
+    g.Q = w.Q[0];
+    g.inv = w.inv[0];
     e = tq::launch_lora_wgrad(bf16, path, g, s);
   }
   return to_status(e);

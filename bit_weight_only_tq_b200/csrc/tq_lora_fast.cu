@@ -34,6 +34,11 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 4-byte copy global -> shared, in the thread's current group of copies.
+__device__ __forceinline__ void cp_async_4(void* smem_dst, const void* gmem_src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(gmem_src) : "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(T a, T b) {
   Vec<T, 2> v;
@@ -175,8 +180,9 @@ static int64_t lora_max_tiles(int64_t M, int64_t L) {
 // straight between memory and the registers that hold the sums.  A CTA takes a tile's 128 positions (16 per warp) and a range of
 // columns in blocks of 64; V stays in registers as fragments, W goes through two shared-memory buffers.
 // m16n8k16 gives a lane columns 2t, 2t + 1 of each n8 tile; W's columns are dealt to four n8 tiles so that these are
-// eight consecutive columns: column c = 8 u + 2 j + e of a block of 32 is column 2 u + e of tile j.  W as B [C, rank]: rows are
-// picked so in the ldmatrix addresses; W as A [rank, C]: pairs of columns are placed so when they are stored to shared memory.
+// eight consecutive columns: column c = 8 u + 2 j + e of a block of 32 is column 2 u + e of tile j.  W is placed so when it is stored
+// to shared memory: as B [C, rank] row c becomes row 8 j + 2 u + e (a tile's eight rows are neighbours, which ldmatrix reads without
+// conflicts), as A [rank, C] pairs of columns are moved.
 // ---------------------------------------------------------------------------------------------
 constexpr int kExpThreads = 256;
 constexpr int kExpCols = 64;
@@ -281,7 +287,8 @@ __global__ void __launch_bounds__(kExpThreads) lora_expand_kernel(const LoraArgs
         dst[12] = wpre[i].w;
       } else {
         const int c = q / (RP / 8), ch = q % (RP / 8);
-        *reinterpret_cast<uint4*>(buf + c * kStride + ch * 16) = wpre[i];
+        const int row = (c & ~31) + 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3) + (c & 1);
+        *reinterpret_cast<uint4*>(buf + row * kStride + ch * 16) = wpre[i];
       }
     }
   };
@@ -299,7 +306,7 @@ __global__ void __launch_bounds__(kExpThreads) lora_expand_kernel(const LoraArgs
   const uint32_t sbase = smem_u32(sm);
   const int mq = lane >> 3, mr = lane & 7;  // matrix and row of this lane's ldmatrix address
   const uint32_t frag = kWA ? ((mq & 1) * 8 + mr) * kStride + (mq >> 1) * 16
-                            : (8 * (mr >> 1) + 2 * (mq >> 1) + (mr & 1)) * kStride + (mq & 1) * 16;
+                            : (8 * (mq >> 1) + mr) * kStride + (mq & 1) * 16;
   int it = 0;
   for (int64_t c0 = c_begin; c0 < c_end; c0 += kExpCols, ++it) {
     store_w(sm + (it & 1) * kBuf);
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(kExpThreads) lora_expand_kernel(const LoraArgs
           if (kWA)
             ldmatrix_x4_trans(buf + 16 * k * kStride + half * 64 + j * 16, b);
           else
-            ldmatrix_x4(buf + (32 * half + 2 * j) * kStride + 32 * k, b);
+            ldmatrix_x4(buf + (32 * half + 8 * j) * kStride + 32 * k, b);
           mma16(acc[j], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b[0], b[1], T());
           mma16(acc[j + 1], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b[2], b[3], T());
           mma16(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b[0], b[1], T());
@@ -378,46 +385,58 @@ static cudaError_t lora_fast_expand(bool bf16, const LoraArgs& a, cudaStream_t s
 
 // ---------------------------------------------------------------------------------------------
 // reduce and wgrad on tcgen05: D (128 x up to 256 fp32, tensor memory) += A B^T over stages in shared memory.
-//   reduce  D[position, j]  A: the tile's rows of P, 128 x 64 columns (K-major)
-//                           B: W, as A [rank, C] 64 columns of each j (K-major), as B [C, rank] 64 rows (MN-major)
+//   reduce  D[position, j]  A: the tile's rows of P, 128 x 128 columns (K-major; 64 columns for ranks above 64)
+//                           B: W, as A [rank, C] those columns of each j (K-major), as B [C, rank] those rows (MN-major)
 //   wgrad   D[c, j]         A: 64 rows x 128 columns of P (MN-major)
 //                           B: 64 rows of V, hi and lo side by side (MN-major); their sums are added at the end
-// Both read P once and little else: HBM bounds them (2 rank FLOPs per byte of P; the tensor pipe is busy for at most the
-// share that rank 128 takes, 512 of the 712 cycles that a stage of P takes from HBM).  P is fetched row by row through `order`
-// with 16-byte cp.async (a row's 128 or 256 bytes are consecutive lanes), which also masks, zero-fills and needs no tensor map,
-// by eight loader warps that stay up to six stages ahead; with dropout each thread masks what it copied before it hands the stage on.
+// Both read P once and little else, so HBM bounds them (2 rank FLOPs per element of P leave the tensor pipe idle most of the
+// time).  P is fetched row by row through `order` with 16-byte cp.async (a row's 128 or 256 bytes are consecutive lanes), which
+// zero-fills too and needs no tensor map, by sixteen loader warps: a stage costs a warp some 100 dependent
+// instructions, and with eight warps their latency, not memory, set the pace.  With dropout each thread masks what it copied before it
+// hands the stage on.
 // The summation (columns, rows) is split over a cluster of S CTAs while tiles leave SMs idle; partial sums go through distributed
 // shared memory and are added in rank order.
 // One CTA per SM (its shared memory keeps every other kernel with tensor memory out), so that none waits for tensor memory that a
 // CTA holds which itself waits for a cluster.
 // ---------------------------------------------------------------------------------------------
-constexpr int kLtcLoaders = 256;
+constexpr int kLtcWarps = 16;  // loaders
+constexpr int kLtcLoaders = 32 * kLtcWarps;
 constexpr int kLtcThreads = kLtcLoaders + 32;
+constexpr int kLtcEpiWarps = 8;  // of the loaders, read the sums
 enum { kReduceA = 0, kReduceB = 1, kWgrad = 2 };
 
 template <int kMode, int RP>
 struct LoraTcLayout {
-  static constexpr int kN = kMode == kWgrad ? 2 * RP : RP;                  // MMA columns
-  static constexpr int kTileP = 128 * 128;
-  static constexpr int kTileW = kMode == kReduceA ? (RP < 64 ? 8192 : RP * 128) : (kN + 63) / 64 * 8192;
+  static constexpr bool kW = kMode == kWgrad;
+  static constexpr int kN = kW ? 2 * RP : RP;                               // MMA columns
+  static constexpr int kSub = kW || RP > 64 ? 1 : 2;                        // reduce: planes of 64 columns per stage
+  static constexpr int kTileP = kW ? 16384 : kSub * 16384;
+  static constexpr int kPlaneW = kMode == kReduceA ? RP * 128 : (kW ? 64 : 64 * kSub) * 128;
+  static constexpr int kTileW = kMode == kReduceA ? kSub * kPlaneW : (kN + 63) / 64 * kPlaneW;
   static constexpr int kStage = kTileP + kTileW;
-  static constexpr int kRing = 192 * 1024 / kStage;
+  static constexpr int kRing = 208 * 1024 / kStage < 8 ? 208 * 1024 / kStage : 8;
   static constexpr int kLag = kRing - 2;                                    // stages between request and hand-over
-  static constexpr int kOffBar = kRing * kStage;                            // full[R], empty[R], accFull
-  static constexpr int kOffRow = kOffBar + (2 * kRing + 1) * 8 + 8;         // TMEM slot before it
-  static constexpr int kOffMost = kOffRow + (kMode == kWgrad ? kRing * 64 : 128) * 4;
+  static constexpr int kChunks = kW ? 16 : 8 * kSub;                        // 16-byte chunks of a row of P per stage
+  static constexpr int kStep = kLtcLoaders / kChunks;                       // rows between a thread's chunks
+  static constexpr int kPer = (kW ? 64 : 128) / kStep;                      // chunks of P per thread
+  static constexpr int kChunksW = kW ? 16 * RP : RP * 8 * kSub;             // chunks of the B operand per stage
+  static constexpr int kPerW = (kChunksW + kLtcLoaders - 1) / kLtcLoaders;
+  static constexpr int kOffBar = kRing * kStage;                            // full[R], empty[R], accFull, TMEM slot
+  static constexpr int kOffRow = kOffBar + (2 * kRing + 2) * 8;
+  static constexpr int kRowRing = 2 * kLag + 2;                             // wgrad: stages whose rows are kept
+  static constexpr int kOffMost = kOffRow + (kW ? kRowRing * 64 : 128) * 4;
   static constexpr int kAlloc = kOffMost + 128 + 1024;
   static constexpr uint32_t kTmemCols = kN <= 32 ? 32u : (kN <= 64 ? 64u : (kN <= 128 ? 128u : 256u));
   static_assert(kRing >= 4 && kAlloc > 116 * 1024 && kAlloc <= 227 * 1024, "one CTA per SM");
-  static_assert(128 * RP * 4 <= kRing * kStage, "partial sums fit");
+  static_assert(128 * (RP + 8) * 4 <= kRing * kStage, "partial sums fit");
 };
 
-// Shared-memory descriptor of an MN-major operand, 128-byte swizzle: planes of 64 elements along M / N, 8192 bytes apart (leading
+// Shared-memory descriptor of an MN-major operand, 128-byte swizzle: planes of 64 elements along M / N, `plane` bytes apart (leading
 // byte offset), each of 128-byte rows of one k, groups of eight rows 1024 bytes apart (stride byte offset).
-__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t smem_addr) {
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t smem_addr, uint32_t plane) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(8192u >> 4) << 16;
+  d |= static_cast<uint64_t>(plane >> 4) << 16;
   d |= static_cast<uint64_t>(1024u >> 4) << 32;
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
@@ -430,19 +449,10 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
                : "r"(taddr));
 }
 
-// The number of the first tile of adapter l (lora_tile); run by a whole warp.
-__device__ __forceinline__ int lora_first_tile(const int32_t* offsets, int64_t M, int l) {
-  int sum = 0;
-  for (int i = threadIdx.x & 31; i < l; i += 32) {
-    const int64_t n = clamp_pos(offsets[i + 1], M) - clamp_pos(offsets[i], M);
-    sum += n > 0 ? static_cast<int>((n + kLoraTile - 1) / kLoraTile) : 0;
-  }
-  return warp_sum(sum);
-}
-
 template <typename T, int kMode, int RP, bool kDrop>
 __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs a, const int S) {
   using L = LoraTcLayout<kMode, RP>;
+  constexpr bool kW = kMode == kWgrad;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
@@ -457,16 +467,15 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
   pdl_wait_prior_grids();
 
   // the work of this cluster: positions [pos0, pos0 + cnt) of adapter l; columns from c0 (wgrad); stages [s0, s0 + ns)
-  int l, ns_all, tile0;
+  int l, ns_all;
   int64_t pos0, cnt, c0 = 0;
-  if (kMode != kWgrad) {
+  if (!kW) {
     const LoraTile t = lora_tile(a.offsets, a.L, a.M, blockIdx.x);
     if (t.l < 0) return;  // the whole cluster
     l = t.l;
     pos0 = t.pos;
     cnt = t.cnt;
-    tile0 = static_cast<int>(blockIdx.x);
-    ns_all = static_cast<int>((a.C + 63) / 64);
+    ns_all = static_cast<int>((a.C + 64 * L::kSub - 1) / (64 * L::kSub));
   } else {
     l = static_cast<int>(blockIdx.y);
     pos0 = clamp_pos(a.offsets[l], a.M);
@@ -483,24 +492,23 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
       return;
     }
     ns_all = static_cast<int>((cnt + 63) / 64);
-    tile0 = 0;
   }
   const int s0 = static_cast<int>(static_cast<int64_t>(rank) * ns_all / S);
-  const int ns = static_cast<int>(static_cast<int64_t>(rank + 1) * ns_all / S) - s0;  // may be 0 (wgrad)
+  const int ns = static_cast<int>(static_cast<int64_t>(rank + 1) * ns_all / S) - s0;  // may be 0
 
   if (tid == 0) {
     for (int i = 0; i < L::kRing; ++i) {
-      mbar_init(&full[i], kLtcLoaders / 32);
+      mbar_init(&full[i], kLtcWarps);
       mbar_init(&empty[i], 1);
     }
     mbar_init(accFull, 1);
     fence_mbar_init();
   }
-  if (warp == kLtcLoaders / 32) {
+  if (warp == kLtcWarps) {
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
-  if (kMode != kWgrad && tid < 128) rowbuf[tid] = tid < cnt ? static_cast<int>(lora_row(a, pos0 + tid)) : -1;
+  if (!kW && tid < 128) rowbuf[tid] = tid < cnt ? static_cast<int>(lora_row(a, pos0 + tid)) : -1;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -508,142 +516,146 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
   const uint32_t tmem = *tmem_slot;
   const PhiloxKey key = kDrop ? philox_key(a.drop) : PhiloxKey{0u, 0u, 0u, 0u};
   const uint16_t* P = static_cast<const uint16_t*>(a.P);
-  const uint16_t* W = static_cast<const uint16_t*>(a.W) + l * a.ws;
   float f = lora_factor(a, l);
-  float vscale = 1.0f;
-  if (kMode == kWgrad && std::is_same<T, __half>::value && a.most) {
-    const int t0 = lora_first_tile(a.offsets, a.M, l), nt = static_cast<int>((cnt + kLoraTile - 1) / kLoraTile);
-    float most = 0.0f;
-    for (int i = lane; i < nt * a.most_n; i += 32) {
-      const int t = i / a.most_n;
-      most = fmaxf(most, a.most[(t0 + t) * kLoraMostPer + i - t * a.most_n]);
-    }
-    float inv;
-    vscale = split_scale<T>(warp_max(most), inv);
-    f *= inv;
-  }
+  if (kW) f *= a.inv[l];
 
   bool ok = true;
-  if (warp < kLtcLoaders / 32) {
+  if (warp < kLtcWarps) {
     // ------------------------------------------------------------------ loaders
-    constexpr int kQ = kMode == kWgrad ? (RP + 31) / 32 : 1;  // chunks of V per thread and stage
-    constexpr int kWPer = (RP * 8 + kLtcLoaders - 1) / kLtcLoaders;
-    const bool bvec = (a.rank & 7) == 0, vvec = (a.rank & 3) == 0;
-    // P: 16-byte chunk pch of rows prow + 32 i (reduce) or + 16 i (wgrad), i = 0 .. 3
-    const int prow = kMode == kWgrad ? tid >> 4 : tid >> 3, pch = kMode == kWgrad ? tid & 15 : tid & 7;
-    constexpr int kStep = kMode == kWgrad ? 16 : 32;
-    const uint32_t pdst = (kMode == kWgrad ? (pch >> 3) * 8192 : 0) + prow * 128 + (((pch & 7) ^ (prow & 7)) << 4);
-    int64_t m[4];
-    float qv[kQ][8];
-    auto fetch_rows = [&](int i) {  // wgrad: rows and V of stage i, one stage ahead of their use
-      const int64_t r0 = static_cast<int64_t>(s0 + i) * 64;
+    const int prow = tid / L::kChunks, pch = tid % L::kChunks;  // chunk pch of rows prow + kStep k, k < kPer
+    const uint32_t pdst = (pch >> 3) * (kW ? 8192 : 16384) + prow * 128 + (((pch & 7) ^ (prow & 7)) << 4);
+    // reduce: each chunk's address in the first stage (a position without a row reads row 0, and its sums are not used)
+    // wgrad: the rows of a stage are requested kLag + 1 stages ahead of their use by the first lane of each row, in the same groups of
+    // copies, and kept until the stage is handed over
+    const uint16_t* src[L::kPer];
+    int m[L::kPer];
+    auto row_slot = [&](int slot, int k) { return rowbuf + slot * 64 + prow + L::kStep * k; };
+    auto request_rows = [&](int i, int slot) {
+      if (pch != 0) return;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t r = r0 + prow + 16 * k;
-        m[k] = r < cnt ? lora_row(a, pos0 + r) : -1;
-      }
-#pragma unroll
-      for (int k = 0; k < kQ; ++k) {
-        const int q = tid + kLtcLoaders * k, row = q / (RP / 8), ch = q % (RP / 8);
-        const bool there = q < RP * 8 && r0 + row < cnt;
-        const float* src = a.V + (pos0 + r0 + row) * a.rank + 8 * ch;
-        if (vvec) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 x = there && 8 * ch + 4 * h < a.rank ? *reinterpret_cast<const float4*>(src + 4 * h)
-                                                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            qv[k][4 * h] = x.x;
-            qv[k][4 * h + 1] = x.y;
-            qv[k][4 * h + 2] = x.z;
-            qv[k][4 * h + 3] = x.w;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) qv[k][e] = there && 8 * ch + e < a.rank ? src[e] : 0.0f;
-        }
+      for (int k = 0; k < L::kPer; ++k) {
+        const int64_t r = static_cast<int64_t>(s0 + i) * 64 + prow + L::kStep * k;
+        if (r >= cnt)
+          *row_slot(slot, k) = -1;
+        else if (!a.order)
+          *row_slot(slot, k) = static_cast<int>(pos0 + r);
+        else
+          cp_async_4(row_slot(slot, k), a.order + pos0 + r);
       }
     };
-    if (kMode == kWgrad) {
-      if (ns > 0) fetch_rows(0);
+    int64_t c = kW ? c0 + 8 * pch : static_cast<int64_t>(s0) * 64 * L::kSub + 8 * pch;  // this thread's column
+    if (kW) {
+      for (int i = 0; i <= L::kLag && i < ns; ++i) request_rows(i, i);
+      cp_async_commit();
+      cp_async_wait<0>();
+      __syncwarp();
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) m[k] = rowbuf[prow + 32 * k];
+      for (int k = 0; k < L::kPer; ++k) {
+        m[k] = rowbuf[prow + L::kStep * k];
+        src[k] = P + (m[k] >= 0 ? static_cast<int64_t>(m[k]) * a.C : 0) + c;
+      }
     }
+    // the B operand: chunks tid + 512 k of the stage
+    const uint16_t* wsrc[L::kPerW];
+    uint32_t wdst[L::kPerW], wsize[L::kPerW];
+    int wrow[L::kPerW];  // summation index within the stage, for the zeros past its end
+    const bool bvec = (a.rank & 7) == 0;
+#pragma unroll
+    for (int k = 0; k < L::kPerW; ++k) {
+      const int q = tid + kLtcLoaders * k;
+      const bool mine = q < L::kChunksW;
+      int row, ch;
+      if (kMode == kReduceA) {  // row: j; 8 kSub chunks of its columns
+        row = q / (8 * L::kSub);
+        ch = q % (8 * L::kSub);
+        wdst[k] = (ch >> 3) * L::kPlaneW + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+        wsize[k] = mine && row < a.rank ? 16u : 0u;
+        wrow[k] = 8 * ch;
+        wsrc[k] = static_cast<const uint16_t*>(a.W) + l * a.ws + (wsize[k] ? row * a.C : 0) +
+                  static_cast<int64_t>(s0) * 64 * L::kSub + 8 * ch;
+      } else {                  // row: summation index; RP / 8 (wgrad: RP / 4, hi and lo) chunks
+        constexpr int kRowChunks = kW ? RP / 4 : RP / 8;
+        row = q / kRowChunks;
+        ch = q % kRowChunks;
+        wdst[k] = (ch >> 3) * L::kPlaneW + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+        wsize[k] = mine && (kW || 8 * ch < a.rank) ? 16u : 0u;
+        wrow[k] = row;
+        wsrc[k] = kW ? static_cast<const uint16_t*>(a.Q) + (pos0 + static_cast<int64_t>(s0) * 64 + row) * (2 * RP) + 8 * ch
+                     : static_cast<const uint16_t*>(a.W) + l * a.ws +
+                           (static_cast<int64_t>(s0) * 64 * L::kSub + row) * a.rank + 8 * ch;
+      }
+    }
+    const int64_t wadvance = kMode == kReduceA ? 64 * L::kSub : (kW ? 64 * 2 * RP : 64 * L::kSub * a.rank);
+    // summation indexes left from the current stage on (columns or positions)
+    int64_t left = kW ? cnt - static_cast<int64_t>(s0) * 64 : a.C - static_cast<int64_t>(s0) * 64 * L::kSub;
+    int s = 0, hs = 0;       // ring slots of the stage requested and of the one handed over
+    int rs = 0, rh = 0, rn = L::kLag + 1;  // slots of the rows of those two and of the ones requested
+    int64_t hc = c;
+    uint32_t parity = 1u;    // of the phase of empty[s] to wait for
     for (int i = 0; i < ns + L::kLag && ok; ++i) {
       if (i < ns) {
-        const int s = i % L::kRing;
         if (i >= L::kRing) {
-          ok = mbar_wait(&empty[s], static_cast<uint32_t>((i / L::kRing) - 1) & 1u);
+          ok = mbar_wait(&empty[s], parity);
           if (!ok) break;
         }
         uint8_t* st = sm + s * L::kStage;
-        const int64_t c = (kMode == kWgrad ? c0 : static_cast<int64_t>(s0 + i) * 64) + 8 * pch;
+        if (kW) {
+          const bool in = c < a.C;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool there = m[k] >= 0 && c < a.C;
-          cp_async_16(st + pdst + k * kStep * 128, P + (there ? m[k] * a.C + c : 0), there ? 16u : 0u);
-        }
-        if (kMode == kWgrad) {
-          if (kDrop && pch == 0)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) rowbuf[s * 64 + prow + 16 * k] = static_cast<int>(m[k]);
-#pragma unroll
-          for (int k = 0; k < kQ; ++k) {
-            const int q = tid + kLtcLoaders * k, row = q / (RP / 8), ch = q % (RP / 8);
-            if (q >= RP * 8) continue;
-            uint4 hi, lo;
-            split2<T>(vscale * qv[k][0], vscale * qv[k][1], hi.x, lo.x);
-            split2<T>(vscale * qv[k][2], vscale * qv[k][3], hi.y, lo.y);
-            split2<T>(vscale * qv[k][4], vscale * qv[k][5], hi.z, lo.z);
-            split2<T>(vscale * qv[k][6], vscale * qv[k][7], hi.w, lo.w);
-            uint8_t* wd = st + L::kTileP + row * 128;
-            const int c2 = RP / 8 + ch;
-            *reinterpret_cast<uint4*>(wd + (ch >> 3) * 8192 + (((ch & 7) ^ (row & 7)) << 4)) = hi;
-            *reinterpret_cast<uint4*>(wd + (c2 >> 3) * 8192 + (((c2 & 7) ^ (row & 7)) << 4)) = lo;
+          for (int k = 0; k < L::kPer; ++k) {
+            const int64_t mk = *row_slot(rs, k);
+            const bool there = in && mk >= 0 && mk < a.M;
+            cp_async_16(st + pdst + k * L::kStep * 128, P + (there ? mk * a.C + c : 0), there ? 16u : 0u);
           }
-          if (i + 1 < ns) fetch_rows(i + 1);
+          if (i + L::kLag + 1 < ns) request_rows(i + L::kLag + 1, rn);
+          if (++rs == L::kRowRing) rs = 0;
+          if (++rn == L::kRowRing) rn = 0;
         } else {
-          const int64_t cs = static_cast<int64_t>(s0 + i) * 64;
+          const uint32_t size = 8 * pch < left ? 16u : 0u;
 #pragma unroll
-          for (int k = 0; k < kWPer; ++k) {
-            const int q = tid + kLtcLoaders * k;
-            if (q >= RP * 8) continue;
-            if (kMode == kReduceA) {
-              const int j = q >> 3, ch = q & 7;
-              const bool there = j < a.rank && cs + 8 * ch < a.C;
-              cp_async_16(st + L::kTileP + j * 128 + ((ch ^ (j & 7)) << 4), W + (there ? j * a.C + cs + 8 * ch : 0),
-                          there ? 16u : 0u);
-            } else {
-              const int row = q / (RP / 8), ch = q % (RP / 8);
-              uint8_t* wd = st + L::kTileP + (ch >> 3) * 8192 + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-              const bool there = cs + row < a.C && 8 * ch < a.rank;
-              const uint16_t* src = W + (there ? (cs + row) * a.rank : 0);
-              if (bvec)
-                cp_async_16(wd, src + (there ? 8 * ch : 0), there ? 16u : 0u);
-              else
-                *reinterpret_cast<uint4*>(wd) = there ? load8(src, 8 * ch, a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
-            }
+          for (int k = 0; k < L::kPer; ++k) {
+            cp_async_16(st + pdst + k * L::kStep * 128, size ? src[k] : P, size);
+            src[k] += 64 * L::kSub;
           }
+        }
+#pragma unroll
+        for (int k = 0; k < L::kPerW; ++k) {
+          if (L::kChunksW % kLtcLoaders != 0 && tid + kLtcLoaders * k >= L::kChunksW) continue;
+          const uint32_t size = wrow[k] < left ? wsize[k] : 0u;
+          uint8_t* dst = st + L::kTileP + wdst[k];
+          if (kMode != kReduceB || bvec) {
+            cp_async_16(dst, size ? wsrc[k] : P, size);
+          } else {  // rows of B that are not whole 16-byte vectors
+            const int ch = (tid + kLtcLoaders * k) % (RP / 8);
+            *reinterpret_cast<uint4*>(dst) =
+                size ? load8(wsrc[k] - 8 * ch, 8 * ch, a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
+          }
+          wsrc[k] += wadvance;
+        }
+        left -= kW ? 64 : 64 * L::kSub;
+        if (++s == L::kRing) {
+          s = 0;
+          parity ^= 1u;
         }
       }
       cp_async_commit();
-      const int d = i - L::kLag;
-      if (d < 0) continue;
+      if (i < L::kLag) continue;
       cp_async_wait<L::kLag>();
       if (kDrop) {
-        uint8_t* st = sm + (d % L::kRing) * L::kStage;
-        const int64_t c = (kMode == kWgrad ? c0 : static_cast<int64_t>(s0 + d) * 64) + 8 * pch;
-        __syncwarp();
+        uint8_t* st = sm + hs * L::kStage + pdst;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int64_t mk = kMode == kWgrad ? rowbuf[(d % L::kRing) * 64 + prow + 16 * k] : m[k];
-          uint4* x = reinterpret_cast<uint4*>(st + pdst + k * kStep * 128);
-          if (mk >= 0 && c < a.C) *x = and4(*x, drop_mask16((mk * a.C + c) >> 3, key, a.drop.thr));
+        for (int k = 0; k < L::kPer; ++k) {
+          const int64_t mk = kW ? *row_slot(rh, k) : m[k];
+          uint4* x = reinterpret_cast<uint4*>(st + k * L::kStep * 128);
+          if (mk >= 0 && mk < a.M && hc < a.C) *x = and4(*x, drop_mask16((mk * a.C + hc) >> 3, key, a.drop.thr));
         }
+        if (!kW) hc += 64 * L::kSub;
+        if (kW && ++rh == L::kRowRing) rh = 0;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[d % L::kRing]);
+      __syncwarp();  // also: the rows that came with this group of copies are there for the whole warp
+      if (lane == 0) mbar_arrive(&full[hs]);
+      if (++hs == L::kRing) hs = 0;
     }
     cp_async_wait<0>();
     if (ns > 0) ok = ok && mbar_wait(accFull, 0u);
@@ -652,19 +664,34 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
     constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
     constexpr uint32_t kMajor = kMode == kReduceA ? 0u : (kMode == kReduceB ? 1u << 16 : (1u << 15) | (1u << 16));
     constexpr uint32_t kIdesc = idesc_f16_f32(128, L::kN) | kType | kMajor;
-    constexpr uint32_t kStepA = kMode == kWgrad ? 128u : 2u, kStepB = kMode == kReduceA ? 2u : 128u;
     const uint32_t base = smem_u32(sm);
+    int s = 0;
+    uint32_t parity = 0u;
     for (int i = 0; i < ns && ok; ++i) {
-      const int s = i % L::kRing;
-      ok = mbar_wait(&full[s], static_cast<uint32_t>(i / L::kRing) & 1u);
+      ok = mbar_wait(&full[s], parity);
       if (!ok) break;
+      // The stage was written by other threads' cp.async and stores, ordered before this point by the barrier.  The fence that makes
+      // it visible to the tensor core is here, not in the loaders: there it also waits for the thread's copies in
+      // flight, and each stage then takes a whole memory latency (wgrad of 8192 x 4096, rank 64: 38 us).
+      fence_proxy_async_smem();
       tc_fence_after_sync();
       const uint32_t pa = base + s * L::kStage, wa = pa + L::kTileP;
-      const uint64_t ad = kMode == kWgrad ? sdesc_mnmajor_sw128(pa) : sdesc_kmajor_sw128(pa);
-      const uint64_t bd = kMode == kReduceA ? sdesc_kmajor_sw128(wa) : sdesc_mnmajor_sw128(wa);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) umma_f16(tmem, ad + kStepA * q, bd + kStepB * q, kIdesc, (i | q) != 0 ? 1u : 0u);
+      for (int p = 0; p < L::kSub; ++p) {
+        const uint64_t ad = kW ? sdesc_mnmajor_sw128(pa, 8192u) : sdesc_kmajor_sw128(pa + p * 16384);
+        const uint64_t bd = kMode == kReduceA ? sdesc_kmajor_sw128(wa + p * L::kPlaneW)
+                                              : sdesc_mnmajor_sw128(wa + p * 8192, L::kPlaneW);
+        // 16 of the summation index: 32 bytes of a K-major row, 16 rows of 128 bytes of an MN-major plane
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          umma_f16(tmem, ad + (kW ? 128u : 2u) * q, bd + (kMode == kReduceA ? 2u : 128u) * q, kIdesc,
+                   (i | p | q) != 0 ? 1u : 0u);
+      }
       umma_commit(&empty[s]);
+      if (++s == L::kRing) {
+        s = 0;
+        parity ^= 1u;
+      }
     }
     if (ok && ns > 0) umma_commit(accFull);
   }
@@ -672,17 +699,21 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
   tc_fence_after_sync();
 
   // ------------------------------------------------------------------ sums out of tensor memory
-  // Loader warp w has lanes 32 (w % 4) .. + 31 (position or column r of the tile) and half w / 4 of the inner columns.
+  // Warp w < 8 has lanes 32 (w % 4) .. + 31 (position or column r of the tile) and half w / 4 of the inner columns.
   const int r = tid & 127;
+  const bool epi = warp < kLtcEpiWarps;
+  if (!kW && rowbuf[r] < 0) f = 0.0f;  // a position without a row
+  const bool none = !kW && rowbuf[r] < 0;
   float most = 0.0f, most2 = 0.0f;
   auto emit = [&](int j, float v) {
     if (j >= a.rank) return;
-    if (kMode == kWgrad) {
+    if (kW) {
       if (c0 + r < a.C) (static_cast<T*>(a.O) + l * a.ws)[(c0 + r) * a.wc + j * a.wj] = from_f32<T>(f * v);
     } else if (r < cnt) {
       const int64_t at = (pos0 + r) * a.rank + j;
-      a.V[at] = f * v;
-      most = fmaxf(most, fabsf(f * v));
+      const float o = none ? 0.0f : f * v;
+      a.V[at] = o;
+      most = fmaxf(most, fabsf(o));
       if (a.most2) most2 = fmaxf(most2, fabsf(a.V2[at]));
     }
   };
@@ -691,28 +722,29 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
     uint32_t x[8], y[8];
     if (ok && ns > 0) {
       tmem_ld_32x32b_x8(at, x);
-      if (kMode == kWgrad) tmem_ld_32x32b_x8(at + RP, y);
+      if (kW) tmem_ld_32x32b_x8(at + RP, y);
       tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[e]) + (kMode == kWgrad ? __uint_as_float(y[e]) : 0.0f);
+      for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[e]) + (kW ? __uint_as_float(y[e]) : 0.0f);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = 0.0f;
     }
   };
   if (S == 1) {
-    if (warp < kLtcLoaders / 32)
+    if (epi)
 #pragma unroll 1
       for (int j0 = (warp >> 2) * (RP / 2); j0 < (warp >> 2) * (RP / 2) + RP / 2; j0 += 8) {
         float v[8];
         sums(j0, v);
-        if (kMode != kWgrad && (a.rank & 3) == 0) {  // whole float4s of a position's row
+        if (!kW && (a.rank & 3) == 0) {  // whole float4s of a position's row
           if (r < cnt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if (j0 + 4 * h >= a.rank) continue;
               const int64_t at = (pos0 + r) * a.rank + j0 + 4 * h;
-              const float4 o = make_float4(f * v[4 * h], f * v[4 * h + 1], f * v[4 * h + 2], f * v[4 * h + 3]);
+              float4 o = make_float4(f * v[4 * h], f * v[4 * h + 1], f * v[4 * h + 2], f * v[4 * h + 3]);
+              if (none) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               *reinterpret_cast<float4*>(a.V + at) = o;
               most = fmaxf(fmaxf(fmaxf(fabsf(o.x), fabsf(o.y)), fmaxf(fabsf(o.z), fabsf(o.w))), most);
               if (a.most2) {
@@ -720,7 +752,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
                 most2 = fmaxf(fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(p.z), fabsf(p.w))), most2);
               }
             }
-        } else if (kMode == kWgrad && a.wj == 1 && (a.rank & 7) == 0) {  // dB: eight consecutive elements of a row
+        } else if (kW && a.wj == 1 && (a.rank & 7) == 0) {  // dB: eight consecutive elements of a row
           if (c0 + r < a.C && j0 < a.rank) {
             Vec<T, 8> o;
 #pragma unroll
@@ -733,13 +765,13 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
         }
       }
   } else {
-    // inner columns [q RP / S, (q + 1) RP / S) are added up by CTA q: partial sums [source][column][128]
-    const int cpo = RP / S;
+    // inner columns [q cpo, (q + 1) cpo) are added up by CTA q: partial sums [source][column][128]
+    const int cpo = (RP + S - 1) / S;
     float* red = reinterpret_cast<float*>(sm);
     const uint32_t red_local = smem_u32(red);
     cluster_arrive();  // every CTA of the cluster is past its main loop: the rings are free
     cluster_wait();
-    if (warp < kLtcLoaders / 32)
+    if (epi)
 #pragma unroll 1
       for (int j0 = (warp >> 2) * (RP / 2); j0 < (warp >> 2) * (RP / 2) + RP / 2; j0 += 8) {
         float v[8];
@@ -753,43 +785,108 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
       }
     cluster_arrive();  // all partial sums have landed
     cluster_wait();
-    if (warp < kLtcLoaders / 32)
-      for (int j = tid >> 7; j < cpo; j += 2) {
+    if (warp < kLtcWarps)
+      for (int j = tid >> 7; j < cpo && rank * cpo + j < RP; j += kLtcLoaders / 128) {
         float v = 0.0f;
-        for (int src = 0; src < S; ++src) v += red[(src * cpo + j) * 128 + r];
+        for (int q = 0; q < S; ++q) v += red[(q * cpo + j) * 128 + r];
         emit(rank * cpo + j, v);
       }
   }
-  if (kMode != kWgrad && a.most) {
+  if (!kW && a.most) {
     most = warp_max(most);
     most2 = warp_max(most2);
-    if (lane == 0 && warp < kLtcLoaders / 32) {
+    if (lane == 0 && warp < kLtcWarps) {
       mostbuf[warp] = most;
       mostbuf[16 + warp] = most2;
     }
     __syncthreads();
     if (tid < 2) {
       float x = 0.0f;
-      for (int i = 0; i < kLtcLoaders / 32; ++i) x = fmaxf(x, mostbuf[16 * tid + i]);
+      for (int i = 0; i < kLtcWarps; ++i) x = fmaxf(x, mostbuf[16 * tid + i]);
       float* to = tid == 0 ? a.most : a.most2;
-      if (to) to[tile0 * kLoraMostPer + rank] = x;
+      if (to) to[static_cast<int64_t>(blockIdx.x) * kLoraMostPer + rank] = x;
     }
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == kLtcLoaders / 32) {
+  if (warp == kLtcWarps) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, L::kTmemCols);
   }
 }
 
-// CTAs per cluster for `ctas` tiles of `stages` stages: time goes as (waves of CTAs) / S, and a split must leave each CTA eight
+// V [M, rank] fp32 -> hi and lo [M, 2 RP] (zeros past the rank), scaled by the adapter's power of two, whose inverse goes to inv[l]:
+// once for all columns of wgrad, which would repeat it for each 128 of them.  A CTA per tile; grid y: v and dv.
+struct LoraSplitArgs {
+  const float* V[2];
+  const float* most[2];  // or null (bf16)
+  void* Q[2];
+  float* inv[2];
+  const int32_t* offsets;
+  int64_t M;
+  int L, rank, most_n;
+};
+
+template <typename T, int RP>
+__global__ void __launch_bounds__(256) lora_split_kernel(const LoraSplitArgs a) {
+  pdl_allow_dependents();
+  pdl_wait_prior_grids();
+  const int lane = threadIdx.x & 31;
+  const bool y = blockIdx.y != 0;
+  const float* const V = y ? a.V[1] : a.V[0];
+  const float* const tiles = y ? a.most[1] : a.most[0];
+  uint4* const Q = static_cast<uint4*>(y ? a.Q[1] : a.Q[0]);
+  const LoraTile t = lora_tile(a.offsets, a.L, a.M, blockIdx.x);
+  if (t.l < 0) return;
+  float scale = 1.0f, inv = 1.0f;
+  if (std::is_same<T, __half>::value) {
+    const int64_t n = clamp_pos(a.offsets[t.l + 1], a.M) - clamp_pos(a.offsets[t.l], a.M);
+    const int64_t slots = (n + kLoraTile - 1) / kLoraTile * a.most_n;
+    float most = 0.0f;
+    for (int64_t i = lane; i < slots; i += 32) {
+      const int64_t k = i / a.most_n;
+      most = fmaxf(most, tiles[(t.first + k) * kLoraMostPer + i - k * a.most_n]);
+    }
+    scale = split_scale<T>(warp_max(most), inv);
+  }
+  if (threadIdx.x == 0 && static_cast<int>(blockIdx.x) == t.first) (y ? a.inv[1] : a.inv[0])[t.l] = inv;
+  const bool vec = (a.rank & 3) == 0;
+  for (int q = threadIdx.x; q < t.cnt * (RP / 8); q += 256) {
+    const int row = q / (RP / 8), ch = q % (RP / 8);
+    const float* src = V + (t.pos + row) * a.rank + 8 * ch;
+    float v[8];
+    if (vec) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 x = 8 * ch + 4 * h < a.rank ? *reinterpret_cast<const float4*>(src + 4 * h)
+                                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        v[4 * h] = x.x;
+        v[4 * h + 1] = x.y;
+        v[4 * h + 2] = x.z;
+        v[4 * h + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 8 * ch + e < a.rank ? src[e] : 0.0f;
+    }
+    uint4 hi, lo;
+    split2<T>(scale * v[0], scale * v[1], hi.x, lo.x);
+    split2<T>(scale * v[2], scale * v[3], hi.y, lo.y);
+    split2<T>(scale * v[4], scale * v[5], hi.z, lo.z);
+    split2<T>(scale * v[6], scale * v[7], hi.w, lo.w);
+    uint4* dst = Q + (t.pos + row) * (RP / 4);
+    dst[ch] = hi;
+    dst[RP / 8 + ch] = lo;
+  }
+}
+
+// CTAs per cluster for `ctas` tiles of `stages` stages: time goes as (waves of CTAs) / S, and a split must leave each CTA four
 // stages to be worth the exchange.
-static int lora_split(int64_t ctas, int64_t stages, int rp) {
+static int lora_split(int64_t ctas, int64_t stages) {
   const int64_t sms = current_device_info().num_sms;
   int best = 1;
   double cost = static_cast<double>((ctas + sms - 1) / sms);
-  for (int S = 2; S <= 8 && S * 8 <= stages && rp / S >= 2; S *= 2) {
+  for (int S = 2; S <= kLoraMostPer && S * 4 <= stages; ++S) {
     const double c = static_cast<double>((ctas * S + sms - 1) / sms) / S;
     if (c < 0.95 * cost) {
       cost = c;
@@ -799,7 +896,7 @@ static int lora_split(int64_t ctas, int64_t stages, int rp) {
   return best;
 }
 
-static int lora_pad_rank(int rank) { return rank <= 16 ? 16 : (rank <= 32 ? 32 : (rank <= 64 ? 64 : 128)); }
+static int lora_pad_rank(int64_t rank) { return rank <= 16 ? 16 : (rank <= 32 ? 32 : (rank <= 64 ? 64 : 128)); }
 
 template <typename T, int kMode, int RP, bool kDrop>
 static cudaError_t launch_lora_tc(const LoraArgs& a, dim3 grid, cudaStream_t s) {
@@ -824,9 +921,11 @@ static cudaError_t launch_lora_tc(const LoraArgs& a, dim3 grid, cudaStream_t s) 
   return cudaLaunchKernelEx(&cfg, kern, a, static_cast<int>(grid.z));
 }
 
-// Clusters that reduce a call's tiles (the maxima of its tiles have one slot per CTA).
+// CTAs that reduce a tile together (the maxima of a tile have one slot for each).
 static int lora_reduce_split(const LoraArgs& a) {
-  return lora_split((a.M + kLoraTile - 1) / kLoraTile, (a.C + 63) / 64, lora_pad_rank(a.rank));
+  const int64_t full = (a.M + kLoraTile - 1) / kLoraTile;
+  const int64_t part = a.L > 1 ? (a.L < full ? a.L : full) : 0;  // tiles that adapters may begin besides
+  return lora_split(full + part, (a.C + 127) / 128);
 }
 
 static cudaError_t lora_fast_reduce(bool bf16, const LoraArgs& a, cudaStream_t s) {
@@ -844,7 +943,7 @@ static cudaError_t lora_fast_reduce(bool bf16, const LoraArgs& a, cudaStream_t s
 
 static cudaError_t lora_fast_wgrad(bool bf16, const LoraArgs& a, cudaStream_t s) {
   const int64_t ct = (a.C + 127) / 128, some = a.L < a.M ? a.L : (a.M < 1 ? 1 : a.M);
-  const int S = lora_split(ct * some, a.M / some / 64, lora_pad_rank(a.rank));
+  const int S = lora_split(ct * some, a.M / some / 64);
   const dim3 grid(static_cast<unsigned>(ct), static_cast<unsigned>(a.L), static_cast<unsigned>(S));
   return with_type16(bf16, [&](auto t) {
     using T = decltype(t);
@@ -852,6 +951,58 @@ static cudaError_t lora_fast_wgrad(bool bf16, const LoraArgs& a, cudaStream_t s)
       constexpr int RP = decltype(rp)::value;
       return a.drop.thr ? launch_lora_tc<T, kWgrad, RP, true>(a, grid, s)
                         : launch_lora_tc<T, kWgrad, RP, false>(a, grid, s);
+    });
+  });
+}
+
+// Workspace of the gradients: dv fp32 [M, rank]; the tiles' maxima of v and of dv; the inverse scales; v and dv as hi and lo.
+struct LoraWorkspace {
+  float* dv;
+  float* most[2];
+  float* inv[2];
+  uint16_t* Q[2];
+  size_t bytes;
+};
+
+LoraWorkspace lora_workspace(void* base, int64_t M, int64_t L, int64_t rank) {
+  LoraWorkspace w;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    void* p = static_cast<char*>(base) + at;
+    at += (bytes + 15) / 16 * 16;
+    return p;
+  };
+  w.dv = static_cast<float*>(take(static_cast<size_t>(M) * rank * 4));
+  for (int i = 0; i < 2; ++i) {
+    w.most[i] = static_cast<float*>(take(static_cast<size_t>(lora_max_tiles(M, L)) * kLoraMostPer * 4));
+    w.inv[i] = static_cast<float*>(take(static_cast<size_t>(L) * 4));
+    w.Q[i] = static_cast<uint16_t*>(take(static_cast<size_t>(M) * 2 * lora_pad_rank(rank) * 2));
+  }
+  w.bytes = at;
+  return w;
+}
+
+// hi and lo of v (into Q[0]) and, with `both`, of dv (Q[1]).
+cudaError_t launch_lora_split(bool bf16, bool both, const LoraWorkspace& w, const float* v, const int32_t* offsets,
+                              int64_t M, int64_t L, int rank, int most_n, cudaStream_t s) {
+  LoraSplitArgs a = {};
+  a.V[0] = v;
+  a.V[1] = w.dv;
+  for (int i = 0; i < 2; ++i) {
+    a.most[i] = bf16 ? nullptr : w.most[i];
+    a.Q[i] = w.Q[i];
+    a.inv[i] = w.inv[i];
+  }
+  a.offsets = offsets;
+  a.M = M;
+  a.L = static_cast<int>(L);
+  a.rank = rank;
+  a.most_n = most_n;
+  const dim3 grid(static_cast<unsigned>(lora_max_tiles(M, L)), both ? 2 : 1);
+  return with_type16(bf16, [&](auto t) {
+    using T = decltype(t);
+    return with_rank(rank, [&](auto rp) {
+      return launch_pdl(lora_split_kernel<T, decltype(rp)::value>, grid, dim3(256), 0, 1, s, a);
     });
   });
 }
@@ -1100,9 +1251,5 @@ cudaError_t launch_lora_expand(bool bf16, int path, const LoraArgs& a, cudaStrea
 cudaError_t launch_lora_wgrad(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {
   return path == kLoraGeneric ? lora_generic_wgrad(bf16, a, s) : lora_fast_wgrad(bf16, a, s);
 }
-
-// Workspace of the gradients: dv fp32 [M, rank], then the tiles' maxima of v and of dv.
-int64_t lora_workspace_floats(int64_t M, int64_t rank) { return (M * rank + 3) / 4 * 4; }
-int64_t lora_most_floats(int64_t M, int64_t L) { return lora_max_tiles(M, L) * kLoraMostPer; }
 
 }  // namespace tq
