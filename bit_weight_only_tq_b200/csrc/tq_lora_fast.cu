@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "tq_common.cuh"
 
 namespace tq {
@@ -68,23 +70,6 @@ __device__ __forceinline__ float split_scale(float most, float& inv) {
   e = e > 126 ? 126 : e;
   inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-}
-
-__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-__device__ __forceinline__ uint4 and4(const uint4& a, const uint4& b) {
-  return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
 }
 
 // Eight consecutive 16-bit elements of a row of `width` from column c (zero past it); vec: whole and aligned.
@@ -174,183 +159,10 @@ static int64_t lora_max_tiles(int64_t M, int64_t L) {
   return t < M ? t : M;
 }
 
-// ---------------------------------------------------------------------------------------------
-// expand: O[m, c] = base[m, c] + f sum_j V[r, j] W_l(c, j).
-// Bound by the rows of base and O (rank FLOPs per byte moved and column, 16-bit), so each is touched once, with 16-byte accesses
-// straight between memory and the registers that hold the sums.  A CTA takes a tile's 128 positions (16 per warp) and a range of
-// columns in blocks of 64; V stays in registers as fragments, W goes through two shared-memory buffers.
-// m16n8k16 gives a lane columns 2t, 2t + 1 of each n8 tile; W's columns are dealt to four n8 tiles so that these are
-// eight consecutive columns: column c = 8 u + 2 j + e of a block of 32 is column 2 u + e of tile j.  W is placed so when it is stored
-// to shared memory: as B [C, rank] row c becomes row 8 j + 2 u + e (a tile's eight rows are neighbours, which ldmatrix reads without
-// conflicts), as A [rank, C] pairs of columns are moved.
-// ---------------------------------------------------------------------------------------------
-constexpr int kExpThreads = 256;
-constexpr int kExpCols = 64;
-
-template <typename T, int RP, bool kWA, bool kDrop>
-__global__ void __launch_bounds__(kExpThreads) lora_expand_kernel(const LoraArgs a, const int cols_per_cta) {
-  constexpr int KT = RP / 16;
-  constexpr int kStride = kWA ? kExpCols * 2 + 16 : RP * 2 + 16;  // bytes per row; the 16 keep ldmatrix free of conflicts
-  constexpr int kBuf = (kWA ? RP : kExpCols) * kStride;
-  constexpr int kChunks = RP * kExpCols / 8;                      // 16-byte chunks of a block of W
-  constexpr int kPer = (kChunks + kExpThreads - 1) / kExpThreads;
-  __shared__ __align__(16) uint8_t sm[2 * kBuf];
-  pdl_allow_dependents();
-  pdl_wait_prior_grids();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const LoraTile tile = lora_tile(a.offsets, a.L, a.M, blockIdx.x);
-  if (tile.l == -2) return;
-  const int64_t c_begin = static_cast<int64_t>(blockIdx.y) * cols_per_cta;
-  const int64_t c_end = c_begin + cols_per_cta < a.C ? c_begin + cols_per_cta : a.C;
-  const T* base = static_cast<const T*>(a.base);
-  T* out = static_cast<T*>(a.O);
-
-  if (tile.l < 0) {  // rows of no adapter: base alone
-    if (base == out) return;
-    const int64_t head = clamp_pos(a.offsets[0], a.M), at = clamp_pos(a.offsets[a.L], a.M);
-    const int vecs = static_cast<int>((c_end - c_begin) >> 3);
-    for (int i = warp; i < tile.cnt; i += kExpThreads / 32) {
-      const int64_t q = tile.pos + i, m = lora_row(a, q < head ? q : q - head + at);
-      if (m < 0) continue;
-      uint4* dst = reinterpret_cast<uint4*>(out + m * a.C + c_begin);
-      const uint4* src = reinterpret_cast<const uint4*>(base + m * a.C + c_begin);
-#pragma unroll 4
-      for (int j = lane; j < vecs; j += 32) dst[j] = base ? src[j] : make_uint4(0u, 0u, 0u, 0u);
-    }
-    return;
-  }
-
-  const T* W = static_cast<const T*>(a.W) + tile.l * a.ws;
-  const bool wvec = kWA || (a.rank & 7) == 0;
-  const PhiloxKey key = philox_key(a.drop);
-  // the rows of this lane: positions 16 warp + g and + 8 of the tile
-  int64_t m[2];
-  float f[2];
-  uint32_t hi[KT][4], lo[KT][4];
-  {
-    float v[KT][8];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 16 * warp + g + 8 * h;
-      m[h] = i < tile.cnt ? lora_row(a, tile.pos + i) : -1;
-      const float* row = a.V + (tile.pos + i) * a.rank;
-      float most = 0.0f;
-#pragma unroll
-      for (int k = 0; k < KT; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 16 * k + 2 * t + (e & 1) + 8 * (e >> 1);
-          const float x = m[h] >= 0 && j < a.rank ? row[j] : 0.0f;
-          v[k][4 * h + e] = x;
-          most = fmaxf(most, fabsf(x));
-        }
-      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-      float inv;
-      const float s = split_scale<T>(most, inv);
-      f[h] = inv * lora_factor(a, tile.l);
-#pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        split2<T>(s * v[k][4 * h], s * v[k][4 * h + 1], hi[k][h], lo[k][h]);
-        split2<T>(s * v[k][4 * h + 2], s * v[k][4 * h + 3], hi[k][2 + h], lo[k][2 + h]);
-      }
-    }
-  }
-
-  uint4 wpre[kPer], ynow[4], ynext[4];
-  auto load_w = [&](int64_t c0) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int q = threadIdx.x + kExpThreads * i;
-      wpre[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (q >= kChunks) continue;
-      if (kWA) {
-        const int j = q / (kExpCols / 8), ch = q % (kExpCols / 8);
-        if (j < a.rank) wpre[i] = load8(W + j * a.C, c0 + 8 * ch, a.C, true);
-      } else {
-        const int c = q / (RP / 8), ch = q % (RP / 8);
-        if (c0 + c < a.C) wpre[i] = load8(W + (c0 + c) * a.rank, 8 * ch, a.rank, wvec);
-      }
-    }
-  };
-  auto store_w = [&](uint8_t* buf) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int q = threadIdx.x + kExpThreads * i;
-      if (q >= kChunks) continue;
-      if (kWA) {
-        const int j = q / (kExpCols / 8), ch = q % (kExpCols / 8);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(buf + j * kStride + (ch >> 2) * 64 + (ch & 3) * 4);
-        dst[0] = wpre[i].x;
-        dst[4] = wpre[i].y;
-        dst[8] = wpre[i].z;
-        dst[12] = wpre[i].w;
-      } else {
-        const int c = q / (RP / 8), ch = q % (RP / 8);
-        const int row = (c & ~31) + 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3) + (c & 1);
-        *reinterpret_cast<uint4*>(buf + row * kStride + ch * 16) = wpre[i];
-      }
-    }
-  };
-  auto load_y = [&](int64_t c0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // i = 2 half + row
-      const int64_t c = c0 + 32 * (i >> 1) + 8 * t;
-      ynext[i] = base && m[i & 1] >= 0 && c < c_end ? *reinterpret_cast<const uint4*>(base + m[i & 1] * a.C + c)
-                                                    : make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-
-  load_w(c_begin);
-  load_y(c_begin);
-  const uint32_t sbase = smem_u32(sm);
-  const int mq = lane >> 3, mr = lane & 7;  // matrix and row of this lane's ldmatrix address
-  const uint32_t frag = kWA ? ((mq & 1) * 8 + mr) * kStride + (mq >> 1) * 16
-                            : (8 * (mq >> 1) + mr) * kStride + (mq & 1) * 16;
-  int it = 0;
-  for (int64_t c0 = c_begin; c0 < c_end; c0 += kExpCols, ++it) {
-    store_w(sm + (it & 1) * kBuf);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ynow[i] = ynext[i];
-    if (c0 + kExpCols < c_end) {
-      load_w(c0 + kExpCols);
-      load_y(c0 + kExpCols);
-    }
-    const uint32_t buf = sbase + (it & 1) * kBuf + frag;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float acc[4][4] = {};
-#pragma unroll
-      for (int k = 0; k < KT; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          uint32_t b[4];
-          if (kWA)
-            ldmatrix_x4_trans(buf + 16 * k * kStride + half * 64 + j * 16, b);
-          else
-            ldmatrix_x4(buf + (32 * half + 8 * j) * kStride + 32 * k, b);
-          mma16(acc[j], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b[0], b[1], T());
-          mma16(acc[j + 1], hi[k][0], hi[k][1], hi[k][2], hi[k][3], b[2], b[3], T());
-          mma16(acc[j], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b[0], b[1], T());
-          mma16(acc[j + 1], lo[k][0], lo[k][1], lo[k][2], lo[k][3], b[2], b[3], T());
-        }
-      const int64_t c = c0 + 32 * half + 8 * t;
-      if (c >= c_end) continue;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (m[h] < 0) continue;
-        Vec<T, 8> y = *reinterpret_cast<const Vec<T, 8>*>(&ynow[2 * half + h]);
-        const uint4 bits = kDrop ? philox((m[h] * a.C + c) >> 3, key) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float s = acc[e >> 1][2 * h + (e & 1)], b = to_f32(y.v[e]);
-          y.v[e] = from_f32<T>(kDrop && !drop_keeps(bits, e, a.drop.thr) ? b : fmaf(f[h], s, b));
-        }
-        *reinterpret_cast<Vec<T, 8>*>(out + m[h] * a.C + c) = y;
-      }
-    }
-  }
+// Tiles that a plan of M rows and L adapters has in all likelihood (some adapters end in a part-filled one).
+static int64_t lora_likely_tiles(int64_t M, int64_t L) {
+  const int64_t full = (M + kLoraTile - 1) / kLoraTile;
+  return L > 1 ? full + (L < full ? L : full) : full;
 }
 
 // The smallest padded rank of 16, 32, 64 or 128 (a multiple of an MMA's 16 k).
@@ -360,27 +172,6 @@ static cudaError_t with_rank(int rank, F fn) {
   if (rank <= 32) return fn(std::integral_constant<int, 32>());
   if (rank <= 64) return fn(std::integral_constant<int, 64>());
   return fn(std::integral_constant<int, 128>());
-}
-
-static cudaError_t lora_fast_expand(bool bf16, const LoraArgs& a, cudaStream_t s) {
-  const int64_t tiles = lora_max_tiles(a.M, a.L), full = (a.M + kLoraTile - 1) / kLoraTile;
-  const int64_t blocks = (a.C + kExpCols - 1) / kExpCols;
-  // columns split until the tiles with rows give each SM four CTAs or a CTA is left with two blocks
-  int64_t split = (4 * current_device_info().num_sms + full - 1) / full;
-  if (split > (blocks + 1) / 2) split = (blocks + 1) / 2;
-  if (split < 1) split = 1;
-  const int64_t per = (blocks + split - 1) / split;
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((blocks + per - 1) / per));
-  const int cols = static_cast<int>(per) * kExpCols;
-  return with_type16(bf16, [&](auto t) {
-    using T = decltype(t);
-    return with_rank(a.rank, [&](auto rp) {
-      constexpr int RP = decltype(rp)::value;
-      auto* kern = a.wc == 1 ? (a.drop.thr ? lora_expand_kernel<T, RP, true, true> : lora_expand_kernel<T, RP, true, false>)
-                             : lora_expand_kernel<T, RP, false, false>;
-      return launch_pdl(kern, grid, dim3(kExpThreads), 0, 1, s, a, cols);
-    });
-  });
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -524,7 +315,8 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
     // ------------------------------------------------------------------ loaders
     const int prow = tid / L::kChunks, pch = tid % L::kChunks;  // chunk pch of rows prow + kStep k, k < kPer
     const uint32_t pdst = (pch >> 3) * (kW ? 8192 : 16384) + prow * 128 + (((pch & 7) ^ (prow & 7)) << 4);
-    // reduce: each chunk's address in the first stage (a position without a row reads row 0, and its sums are not used)
+    // reduce: each chunk's address in the first stage (nothing is copied for a position without a row: its sums are not used, and no
+    // other sum reads what the stage holds for it)
     // wgrad: the rows of a stage are requested kLag + 1 stages ahead of their use by the first lane of each row, in the same groups of
     // copies, and kept until the stage is handed over
     const uint16_t* src[L::kPer];
@@ -615,7 +407,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
           const uint32_t size = 8 * pch < left ? 16u : 0u;
 #pragma unroll
           for (int k = 0; k < L::kPer; ++k) {
-            cp_async_16(st + pdst + k * L::kStep * 128, size ? src[k] : P, size);
+            if (m[k] >= 0) cp_async_16(st + pdst + k * L::kStep * 128, size ? src[k] : P, size);
             src[k] += 64 * L::kSub;
           }
         }
@@ -648,7 +440,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
         for (int k = 0; k < L::kPer; ++k) {
           const int64_t mk = kW ? *row_slot(rh, k) : m[k];
           uint4* x = reinterpret_cast<uint4*>(st + k * L::kStep * 128);
-          if (mk >= 0 && mk < a.M && hc < a.C) *x = and4(*x, drop_mask16((mk * a.C + hc) >> 3, key, a.drop.thr));
+          if (mk >= 0 && mk < a.M && hc < a.C) *x = drop_apply16(*x, (mk * a.C + hc) >> 3, key, a.drop.thr);
         }
         if (!kW) hc += 64 * L::kSub;
         if (kW && ++rh == L::kRowRing) rh = 0;
@@ -880,15 +672,46 @@ __global__ void __launch_bounds__(256) lora_split_kernel(const LoraSplitArgs a) 
   }
 }
 
-// CTAs per cluster for `ctas` tiles of `stages` stages: time goes as (waves of CTAs) / S, and a split must leave each CTA four
-// stages to be worth the exchange.
-static int lora_split(int64_t ctas, int64_t stages) {
-  const int64_t sms = current_device_info().num_sms;
+// Clusters of S CTAs that can be resident at once (a cluster lies in one GPC, so the GPCs bound them below SMs / S: on a B200 148, 74,
+// 45, 33, 26, 22, 15 and 15 for S = 1 .. 8), queried once per device and S.
+static int lora_cluster_capacity(const DeviceInfo& di, int S) {
+  static std::atomic<int> cache[kPfMaxDevices][kLoraMostPer + 1];
+  if (S == 1) return di.num_sms;
+  if (di.device < 0 || di.device >= kPfMaxDevices) return di.num_sms / S;
+  int n = cache[di.device][S].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  auto* kern = lora_tc_kernel<__half, kReduceA, 64, false>;
+  constexpr int kAlloc = LoraTcLayout<kReduceA, 64>::kAlloc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, 1, static_cast<unsigned>(S));
+  cfg.blockDim = dim3(kLtcThreads);
+  cfg.dynamicSmemBytes = kAlloc;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = static_cast<unsigned>(S);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (ensure_smem_attr(reinterpret_cast<const void*>(kern), kAlloc) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+    (void)cudaGetLastError();
+    return di.num_sms / S;
+  }
+  cache[di.device][S].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// CTAs per cluster for `tiles` tiles of `stages` stages: a wave costs a CTA its share of the stages, the time of about seven for its
+// start and end, and of three more for the exchange between CTAs.
+static int lora_split(int64_t tiles, int64_t stages) {
+  const DeviceInfo di = current_device_info();
   int best = 1;
-  double cost = static_cast<double>((ctas + sms - 1) / sms);
-  for (int S = 2; S <= kLoraMostPer && S * 4 <= stages; ++S) {
-    const double c = static_cast<double>((ctas * S + sms - 1) / sms) / S;
-    if (c < 0.95 * cost) {
+  double cost = 0.0;
+  for (int S = 1; S <= kLoraMostPer && (S == 1 || S * 2 <= stages); ++S) {
+    const int64_t cap = lora_cluster_capacity(di, S);
+    const double c = static_cast<double>((tiles + cap - 1) / cap) * (static_cast<double>(stages) / S + (S > 1 ? 10.0 : 7.0));
+    if (S == 1 || c < 0.97 * cost) {
       cost = c;
       best = S;
     }
@@ -923,9 +746,7 @@ static cudaError_t launch_lora_tc(const LoraArgs& a, dim3 grid, cudaStream_t s) 
 
 // CTAs that reduce a tile together (the maxima of a tile have one slot for each).
 static int lora_reduce_split(const LoraArgs& a) {
-  const int64_t full = (a.M + kLoraTile - 1) / kLoraTile;
-  const int64_t part = a.L > 1 ? (a.L < full ? a.L : full) : 0;  // tiles that adapters may begin besides
-  return lora_split(full + part, (a.C + 127) / 128);
+  return lora_split(lora_likely_tiles(a.M, a.L), (a.C + 127) / 128);
 }
 
 static cudaError_t lora_fast_reduce(bool bf16, const LoraArgs& a, cudaStream_t s) {
@@ -1003,6 +824,362 @@ cudaError_t launch_lora_split(bool bf16, bool both, const LoraWorkspace& w, cons
     using T = decltype(t);
     return with_rank(rank, [&](auto rp) {
       return launch_pdl(lora_split_kernel<T, decltype(rp)::value>, grid, dim3(256), 0, 1, s, a);
+    });
+  });
+}
+
+// ---------------------------------------------------------------------------------------------
+// expand on tcgen05: O[m, c] = base[m, c] + f sum_j V[r, j] W_l(c, j).
+//   D[position, c] (128 x 128, four buffers in tensor memory) = [hi | lo] of V (shared memory, K-major, kept for the CTA's whole range of
+//   columns) x W (four stages of 128 columns)
+// Bound by the rows of base and O, each touched once with 16-byte accesses straight between memory and the registers that hold the
+// sums.  Sixteen epilogue warps, each with 32 positions and 32 columns of a block, read D in the fragment layout of m16n8
+// (16x256b), which gives a lane columns 2 t, 2 t + 1 of each n8 tile; W's columns are dealt to four n8 tiles so that these are eight
+// consecutive ones: column c = 8 u + 2 j + e of a block of 32 is column 2 u + e of tile j.  base is requested two blocks ahead.
+// Four loader warps bring W: as B [C, rank] a column's 16-byte pieces with cp.async, as A [rank, C] through registers, since pairs
+// of columns part ways (4-byte cp.async took 78 cycles an instruction).  Only barriers of single stages tie the warps.
+// mma.sync on the same fragments, two CTAs per SM, was bound by the MMA rate from rank 64 on (rank 128, 8192 x 8192: 150 us; this 93).
+// ---------------------------------------------------------------------------------------------
+constexpr int kXpEpi = 16;     // epilogue warps
+constexpr int kXpLoad = 4;     // loader warps; the first also issues the MMAs (20 warps leave 96 registers a thread, 21 only 80)
+constexpr int kXpThreads = 32 * (kXpEpi + kXpLoad);
+constexpr int kXpCols = 128;   // columns per block (MMA N)
+constexpr int kXpRing = 4;     // stages of W, and of D
+
+template <int RP, bool kWA>
+struct LoraXpLayout {
+  static constexpr int kPlanesV = 2 * RP <= 64 ? 1 : 2 * RP / 64;     // planes of 64 k: hi then lo
+  static constexpr int kTileV = kPlanesV * 16384;
+  static constexpr int kPlaneW = kWA ? RP * 128 : kXpCols * 128;      // A: 64 columns x RP k; B: 128 columns x 64 k
+  static constexpr int kTileW = kWA ? 2 * kPlaneW : (RP + 63) / 64 * kPlaneW;
+  static constexpr int kLag = kWA ? 0 : kXpRing - 2;                  // stages between request and hand-over (B)
+  static constexpr int kOffW = kTileV;
+  static constexpr int kOffBar = kOffW + kXpRing * kTileW;            // wfull, wempty, dfull, dempty, vfull; TMEM slot
+  static constexpr int kOffF = kOffBar + (4 * kXpRing + 2) * 8;       // fp32 factor of each position
+  static constexpr int kBytes = kOffF + 128 * 4 + 1024;
+  static constexpr int kAlloc = kBytes > 116 * 1024 + 64 ? kBytes : 116 * 1024 + 64;  // one CTA per SM, as above
+  static_assert(kAlloc <= 227 * 1024 && kTileW % 1024 == 0, "shared memory");
+};
+
+// 16 lanes x 32 columns of tensor memory in the fragment layout of m16n8: r[4 j + i] is element i of the n8 tile j.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+template <typename T, int RP, bool kWA, bool kDrop>
+__global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const LoraArgs a, const int blocks_per_cta) {
+  using L = LoraXpLayout<RP, kWA>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
+  uint64_t* wempty = wfull + kXpRing;
+  uint64_t* dfull = wempty + kXpRing;
+  uint64_t* dempty = dfull + kXpRing;
+  uint64_t* vfull = dempty + kXpRing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vfull + 1);
+  float* rowf = reinterpret_cast<float*>(sm + L::kOffF);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait_prior_grids();
+  const LoraTile tile = lora_tile(a.offsets, a.L, a.M, blockIdx.x);
+  if (tile.l == -2) return;
+  const int64_t c_begin = static_cast<int64_t>(blockIdx.y) * blocks_per_cta * kXpCols;
+  const int64_t c_end = c_begin + static_cast<int64_t>(blocks_per_cta) * kXpCols < a.C
+                            ? c_begin + static_cast<int64_t>(blocks_per_cta) * kXpCols
+                            : a.C;
+  const T* base = static_cast<const T*>(a.base);
+  T* out = static_cast<T*>(a.O);
+  if (tile.l < 0) {  // rows of no adapter: base alone
+    if (base == out) return;
+    const int64_t head = clamp_pos(a.offsets[0], a.M), at = clamp_pos(a.offsets[a.L], a.M);
+    const int vecs = static_cast<int>((c_end - c_begin) >> 3);
+    for (int i = warp; i < tile.cnt; i += kXpThreads / 32) {
+      const int64_t q = tile.pos + i, m = lora_row(a, q < head ? q : q - head + at);
+      if (m < 0) continue;
+      uint4* dst = reinterpret_cast<uint4*>(out + m * a.C + c_begin);
+      const uint4* src = reinterpret_cast<const uint4*>(base + m * a.C + c_begin);
+#pragma unroll 4
+      for (int j = lane; j < vecs; j += 32) dst[j] = base ? src[j] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    return;
+  }
+  const int nb = static_cast<int>((c_end - c_begin + kXpCols - 1) / kXpCols);
+
+  if (tid == 0) {
+    for (int i = 0; i < kXpRing; ++i) {
+      mbar_init(&wfull[i], kXpLoad);
+      mbar_init(&wempty[i], 1);
+      mbar_init(&dfull[i], 1);
+      mbar_init(&dempty[i], kXpEpi);
+    }
+    mbar_init(vfull, kXpEpi);
+    fence_mbar_init();
+  }
+  if (warp == kXpEpi) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  pdl_allow_dependents();
+  const uint32_t tmem = *tmem_slot;
+
+  bool ok = true;
+  if (warp < kXpEpi) {
+    // ------------------------------------------------------------------ epilogue
+    const int g = lane >> 2, t = lane & 3, r0 = (warp & 3) * 32 + g;
+    int m[4];  // rows of positions r0 + 8 i
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m[i] = r0 + 8 * i < tile.cnt ? static_cast<int>(lora_row(a, tile.pos + r0 + 8 * i)) : -1;
+    int64_t c = c_begin + (warp >> 2) * 32 + 8 * t;  // this lane's eight columns
+    uint4 y[2][4];
+    auto load_base = [&](uint4 (&to)[4], int64_t at) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        to[i] = base && m[i] >= 0 && at < c_end ? *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(m[i]) * a.C + at)
+                                                : make_uint4(0u, 0u, 0u, 0u);
+    };
+    load_base(y[0], c);
+    load_base(y[1], c + kXpCols);
+    {
+      // V of the tile as hi and lo, four threads per position
+      const int row = tid >> 2, part = tid & 3;
+      constexpr int kE = RP / 4;  // inner columns per thread
+      const bool there = row < tile.cnt;
+      const float* src = a.V + (tile.pos + row) * a.rank;
+      float most = 0.0f;
+      float v[kE];
+      if ((a.rank & 3) == 0) {
+#pragma unroll
+        for (int e = 0; e < kE; e += 4) {
+          const int j = part * kE + e;
+          const float4 x = there && j < a.rank ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          v[e] = x.x;
+          v[e + 1] = x.y;
+          v[e + 2] = x.z;
+          v[e + 3] = x.w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) v[e] = there && part * kE + e < a.rank ? src[part * kE + e] : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < kE; ++e) most = fmaxf(most, fabsf(v[e]));
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+      float inv;
+      const float sc = split_scale<T>(most, inv);
+#pragma unroll
+      for (int e = 0; e < kE; e += 4) {
+        uint2 hi, lo;
+        split2<T>(sc * v[e], sc * v[e + 1], hi.x, lo.x);
+        split2<T>(sc * v[e + 2], sc * v[e + 3], hi.y, lo.y);
+        const int kh = part * kE + e, kl = RP + kh;  // k of hi and of lo
+        *reinterpret_cast<uint2*>(sm + (kh >> 6) * 16384 + row * 128 + ((((kh >> 3) & 7) ^ (row & 7)) << 4) + (kh & 4) * 2) = hi;
+        *reinterpret_cast<uint2*>(sm + (kl >> 6) * 16384 + row * 128 + ((((kl >> 3) & 7) ^ (row & 7)) << 4) + (kl & 4) * 2) = lo;
+      }
+      if (part == 0) rowf[row] = inv * lora_factor(a, tile.l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(vfull);
+    }
+    const PhiloxKey key = kDrop ? philox_key(a.drop) : PhiloxKey{0u, 0u, 0u, 0u};
+    named_barrier_sync(1, 32 * kXpEpi);  // rowf
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = rowf[r0 + 8 * i];
+    int s = 0;
+    uint32_t parity = 0u;
+    auto block = [&](uint4 (&yb)[4]) {
+      ok = ok && mbar_wait(&dfull[s], parity);
+      if (!ok) return;
+      tc_fence_after_sync();
+      const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + s * kXpCols + (warp >> 2) * 32;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // positions r0 + 16 h and + 8
+        uint32_t acc[16];
+        tmem_ld_16x256b_x4(at + (static_cast<uint32_t>(16 * h) << 16), acc);
+        tmem_ld_wait();
+        if (h == 1) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&dempty[s]);
+        }
+        if (c >= c_end) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (m[2 * h + i] < 0) continue;
+          const int64_t at_row = static_cast<int64_t>(m[2 * h + i]) * a.C + c;
+          Vec<T, 8> o = *reinterpret_cast<const Vec<T, 8>*>(&yb[2 * h + i]);
+          const uint4 bits = kDrop ? philox(at_row >> 3, key) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x = __uint_as_float(acc[4 * (e >> 1) + 2 * i + (e & 1)]), z = to_f32(o.v[e]);
+            o.v[e] = from_f32<T>(kDrop && !drop_keeps(bits, e, a.drop.thr) ? z : fmaf(f[2 * h + i], x, z));
+          }
+          *reinterpret_cast<Vec<T, 8>*>(out + at_row) = o;
+        }
+      }
+      if (++s == kXpRing) {
+        s = 0;
+        parity ^= 1u;
+      }
+    };
+    for (int b = 0; b < nb && ok; b += 2) {
+      block(y[0]);
+      load_base(y[0], c + 2 * kXpCols);
+      c += kXpCols;
+      if (b + 1 < nb) {
+        block(y[1]);
+        load_base(y[1], c + 2 * kXpCols);
+        c += kXpCols;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ loaders of W; the first warp also issues the MMAs
+    const int w = tid - 32 * kXpEpi;  // 0 .. 127
+    const uint16_t* W = static_cast<const uint16_t*>(a.W) + tile.l * a.ws;
+    const bool bvec = (a.rank & 7) == 0;
+    constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
+    constexpr uint32_t kIdesc = idesc_f16_f32(128, kXpCols) | kType | (kWA ? 1u << 16 : 0u);
+    const uint32_t base_v = smem_u32(sm);
+    int s = 0, hs = 0;
+    uint32_t parity = 1u, hparity = 0u;
+    // A: chunk (row j = w / 16 + 8 i, eight columns from 8 (w % 16)) of a block, a block ahead in registers
+    constexpr int kPerA = kWA ? RP / 8 : 1;
+    uint4 pre[kPerA];
+    const int ach = w & 15, aj = w >> 4;
+    auto load_a = [&](int b) {
+      const int64_t at = c_begin + static_cast<int64_t>(b) * kXpCols + 8 * ach;
+#pragma unroll
+      for (int i = 0; i < kPerA; ++i)
+        pre[i] = at < a.C && aj + 8 * i < a.rank ? *reinterpret_cast<const uint4*>(W + (aj + 8 * i) * a.C + at)
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+    };
+    if (kWA) load_a(0);
+    for (int b = 0; b < nb + L::kLag && ok; ++b) {
+      if (b < nb) {
+        if (b >= kXpRing) {
+          ok = mbar_wait(&wempty[s], parity);
+          if (!ok) break;
+        }
+        uint8_t* st = sm + L::kOffW + s * L::kTileW;
+        if (kWA) {
+          // columns 8 u + 2 j + e of a block of 32 to 8 j + 2 u + e: piece j of the chunk to 16-byte chunk j of the block
+          const int hb = ach >> 2;
+          uint8_t* dst = st + (hb >> 1) * L::kPlaneW + aj * 128 + 4 * (ach & 3);
+#pragma unroll
+          for (int i = 0; i < kPerA; ++i) {
+            const uint32_t word[4] = {pre[i].x, pre[i].y, pre[i].z, pre[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint32_t*>(dst + i * 1024 + (((4 * (hb & 1) + j) ^ (aj & 7)) << 4)) = word[j];
+          }
+          if (b + 1 < nb) load_a(b + 1);
+        } else {
+          // column c of 128 to its place, RP / 8 pieces
+          const int64_t c0 = c_begin + static_cast<int64_t>(b) * kXpCols;
+          const int c = w, pos = (c & ~31) + 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3) + (c & 1);
+          const bool there = c0 + c < a.C;
+          const uint16_t* src = W + (there ? (c0 + c) * a.rank : 0);
+#pragma unroll
+          for (int ch = 0; ch < RP / 8; ++ch) {
+            uint8_t* dst = st + (ch >> 3) * L::kPlaneW + pos * 128 + (((ch & 7) ^ (pos & 7)) << 4);
+            const bool in = there && 8 * ch < a.rank;
+            if (bvec)
+              cp_async_16(dst, in ? src + 8 * ch : W, in ? 16u : 0u);
+            else
+              *reinterpret_cast<uint4*>(dst) = in ? load8(src, 8 * ch, a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        if (++s == kXpRing) {
+          s = 0;
+          parity ^= 1u;
+        }
+      }
+      if (!kWA) {
+        cp_async_commit();
+        if (b < L::kLag) continue;
+        cp_async_wait<L::kLag>();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&wfull[hs]);
+      if (warp == kXpEpi) {
+        // the MMAs of the block handed over: four buffers of D keep the epilogue busy while this warp waits
+        const int d = b - L::kLag;
+        ok = (d > 0 || mbar_wait(vfull, 0u)) && mbar_wait(&wfull[hs], hparity) &&
+             (d < kXpRing || mbar_wait(&dempty[hs], hparity ^ 1u));
+        if (!ok) break;
+        if (lane == 0) {
+          fence_proxy_async_smem();  // for the copies and stores of the other warps, which the barriers order before this point
+          tc_fence_after_sync();
+          const uint32_t wa = base_v + L::kOffW + hs * L::kTileW;
+#pragma unroll
+          for (int part = 0; part < 2; ++part)  // hi, lo
+#pragma unroll
+            for (int q = 0; q < RP / 16; ++q) {
+              const int kv = part * RP + 16 * q;
+              const uint64_t ad = sdesc_kmajor_sw128(base_v + (kv >> 6) * 16384) + 2 * ((kv & 63) >> 4);
+              const uint64_t bd = kWA ? sdesc_mnmajor_sw128(wa, L::kPlaneW) + 128 * q
+                                      : sdesc_kmajor_sw128(wa + (q >> 2) * L::kPlaneW) + 2 * (q & 3);
+              umma_f16(tmem + hs * kXpCols, ad, bd, kIdesc, (part | q) != 0 ? 1u : 0u);
+            }
+          umma_commit(&wempty[hs]);
+          umma_commit(&dfull[hs]);
+        }
+        __syncwarp();
+      }
+      if (++hs == kXpRing) {
+        hs = 0;
+        hparity ^= 1u;
+      }
+    }
+    cp_async_wait<0>();
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kXpEpi) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int RP, bool kWA, bool kDrop>
+static cudaError_t launch_lora_expand_tc(const LoraArgs& a, int64_t tiles, int64_t est, cudaStream_t s) {
+  auto* kern = lora_expand_tc_kernel<T, RP, kWA, kDrop>;
+  constexpr int kAlloc = LoraXpLayout<RP, kWA>::kAlloc;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kAlloc);
+  if (e != cudaSuccess) return e;
+  // columns split so that waves of CTAs cost least, a CTA's start and end counted as eight blocks
+  const int64_t sms = current_device_info().num_sms, blocks = (a.C + kXpCols - 1) / kXpCols;
+  int64_t per = blocks, cost = -1;
+  for (int64_t split = 1; split <= blocks && split <= 64; ++split) {
+    const int64_t p = (blocks + split - 1) / split;
+    const int64_t c = (est * ((blocks + p - 1) / p) + sms - 1) / sms * (p + 8);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      per = p;
+    }
+  }
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((blocks + per - 1) / per));
+  return launch_pdl(kern, grid, dim3(kXpThreads), kAlloc, 1, s, a, static_cast<int>(per));
+}
+
+static cudaError_t lora_fast_expand(bool bf16, const LoraArgs& a, cudaStream_t s) {
+  const int64_t tiles = lora_max_tiles(a.M, a.L), est = lora_likely_tiles(a.M, a.L);
+  return with_type16(bf16, [&](auto t) {
+    using T = decltype(t);
+    return with_rank(a.rank, [&](auto rp) {
+      constexpr int RP = decltype(rp)::value;
+      if (a.wc != 1) return launch_lora_expand_tc<T, RP, false, false>(a, tiles, est, s);
+      return a.drop.thr ? launch_lora_expand_tc<T, RP, true, true>(a, tiles, est, s)
+                        : launch_lora_expand_tc<T, RP, true, false>(a, tiles, est, s);
     });
   });
 }
