@@ -36,9 +36,9 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 4-byte copy global -> shared, in the thread's current group of copies.
-__device__ __forceinline__ void cp_async_4(void* smem_dst, const void* gmem_src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(gmem_src) : "memory");
+// cp_async_16 to a shared-memory address.
+__device__ __forceinline__ void cp_async_16s(uint32_t smem_dst, const void* gmem_src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gmem_src), "r"(src_bytes) : "memory");
 }
 
 template <typename T>
@@ -154,15 +154,25 @@ __device__ __forceinline__ LoraTile lora_tile(const int32_t* offsets, int L, int
   return r;
 }
 
+// The number of tiles of a plan; run by a whole warp.
+__device__ __forceinline__ int64_t lora_tiles(const int32_t* offsets, int L, int64_t M) {
+  int64_t sum = 0;
+  for (int l = threadIdx.x & 31; l < L; l += 32) {
+    const int64_t n = clamp_pos(offsets[l + 1], M) - clamp_pos(offsets[l], M);
+    sum += n > 0 ? (n + kLoraTile - 1) / kLoraTile : 0;
+  }
+  const int64_t none = clamp_pos(offsets[0], M) + M - clamp_pos(offsets[L], M);
+  return warp_sum(sum) + (none + kLoraTile - 1) / kLoraTile;
+}
+
 static int64_t lora_max_tiles(int64_t M, int64_t L) {
   const int64_t t = M / kLoraTile + L + 1;
   return t < M ? t : M;
 }
 
-// Tiles that a plan of M rows and L adapters has in all likelihood (some adapters end in a part-filled one).
+// Tiles to expect of a plan of M rows and L adapters: each adapter that has rows ends in a part-filled one.
 static int64_t lora_likely_tiles(int64_t M, int64_t L) {
-  const int64_t full = (M + kLoraTile - 1) / kLoraTile;
-  return L > 1 ? full + (L < full ? L : full) : full;
+  return L > 1 ? M / kLoraTile + (L < M ? L : M) : (M + kLoraTile - 1) / kLoraTile;
 }
 
 // The smallest padded rank of 16, 32, 64 or 128 (a multiple of an MMA's 16 k).
@@ -182,8 +192,8 @@ static cudaError_t with_rank(int rank, F fn) {
 //                           B: 64 rows of V, hi and lo side by side (MN-major); their sums are added at the end
 // Both read P once and little else, so HBM bounds them (2 rank FLOPs per element of P leave the tensor pipe idle most of the
 // time).  P is fetched row by row through `order` with 16-byte cp.async (a row's 128 or 256 bytes are consecutive lanes), which
-// zero-fills too and needs no tensor map, by sixteen loader warps: a stage costs a warp some 100 dependent
-// instructions, and with eight warps their latency, not memory, set the pace.  With dropout each thread masks what it copied before it
+// zero-fills too and needs no tensor map, by sixteen loader warps: with eight, or with three times the
+// instructions per stage, the latency of a warp's own instructions set the pace, not memory.  With dropout each thread masks what it copied before it
 // hands the stage on.
 // The summation (columns, rows) is split over a cluster of S CTAs while tiles leave SMs idle; partial sums go through distributed
 // shared memory and are added in rank order.
@@ -196,6 +206,8 @@ constexpr int kLtcThreads = kLtcLoaders + 32;
 constexpr int kLtcEpiWarps = 8;  // of the loaders, read the sums
 enum { kReduceA = 0, kReduceB = 1, kWgrad = 2 };
 
+constexpr int kRowStages = 16;    // wgrad: stages whose rows are fetched together (two such sets are kept)
+
 template <int kMode, int RP>
 struct LoraTcLayout {
   static constexpr bool kW = kMode == kWgrad;
@@ -205,7 +217,7 @@ struct LoraTcLayout {
   static constexpr int kPlaneW = kMode == kReduceA ? RP * 128 : (kW ? 64 : 64 * kSub) * 128;
   static constexpr int kTileW = kMode == kReduceA ? kSub * kPlaneW : (kN + 63) / 64 * kPlaneW;
   static constexpr int kStage = kTileP + kTileW;
-  static constexpr int kRing = 208 * 1024 / kStage < 8 ? 208 * 1024 / kStage : 8;
+  static constexpr int kRing = 200 * 1024 / kStage < 8 ? 200 * 1024 / kStage : 8;
   static constexpr int kLag = kRing - 2;                                    // stages between request and hand-over
   static constexpr int kChunks = kW ? 16 : 8 * kSub;                        // 16-byte chunks of a row of P per stage
   static constexpr int kStep = kLtcLoaders / kChunks;                       // rows between a thread's chunks
@@ -214,8 +226,7 @@ struct LoraTcLayout {
   static constexpr int kPerW = (kChunksW + kLtcLoaders - 1) / kLtcLoaders;
   static constexpr int kOffBar = kRing * kStage;                            // full[R], empty[R], accFull, TMEM slot
   static constexpr int kOffRow = kOffBar + (2 * kRing + 2) * 8;
-  static constexpr int kRowRing = 2 * kLag + 2;                             // wgrad: stages whose rows are kept
-  static constexpr int kOffMost = kOffRow + (kW ? kRowRing * 64 : 128) * 4;
+  static constexpr int kOffMost = kOffRow + (kW ? 2 * kRowStages * 64 : 128) * 4;
   static constexpr int kAlloc = kOffMost + 128 + 1024;
   static constexpr uint32_t kTmemCols = kN <= 32 ? 32u : (kN <= 64 ? 64u : (kN <= 128 ? 128u : 256u));
   static_assert(kRing >= 4 && kAlloc > 116 * 1024 && kAlloc <= 227 * 1024, "one CTA per SM");
@@ -250,7 +261,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
   uint64_t* empty = full + L::kRing;
   uint64_t* accFull = empty + L::kRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accFull + 1);
-  int* rowbuf = reinterpret_cast<int*>(sm + L::kOffRow);  // reduce: the tile's rows; wgrad: a ring of the stages' rows
+  int* rowbuf = reinterpret_cast<int*>(sm + L::kOffRow);  // reduce: the tile's rows; wgrad: those of two sets of stages
   float* mostbuf = reinterpret_cast<float*>(sm + L::kOffMost);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -315,39 +326,33 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
     // ------------------------------------------------------------------ loaders
     const int prow = tid / L::kChunks, pch = tid % L::kChunks;  // chunk pch of rows prow + kStep k, k < kPer
     const uint32_t pdst = (pch >> 3) * (kW ? 8192 : 16384) + prow * 128 + (((pch & 7) ^ (prow & 7)) << 4);
+    const uint32_t ring0 = smem_u32(sm), ring1 = ring0 + L::kRing * L::kStage;
+    int64_t c = kW ? c0 + 8 * pch : static_cast<int64_t>(s0) * 64 * L::kSub + 8 * pch;  // this thread's column
     // reduce: each chunk's address in the first stage (nothing is copied for a position without a row: its sums are not used, and no
     // other sum reads what the stage holds for it)
-    // wgrad: the rows of a stage are requested kLag + 1 stages ahead of their use by the first lane of each row, in the same groups of
-    // copies, and kept until the stage is handed over
-    const uint16_t* src[L::kPer];
+    const uint16_t* src[kW ? 1 : L::kPer];
     int m[L::kPer];
-    auto row_slot = [&](int slot, int k) { return rowbuf + slot * 64 + prow + L::kStep * k; };
-    auto request_rows = [&](int i, int slot) {
-      if (pch != 0) return;
-#pragma unroll
-      for (int k = 0; k < L::kPer; ++k) {
-        const int64_t r = static_cast<int64_t>(s0 + i) * 64 + prow + L::kStep * k;
-        if (r >= cnt)
-          *row_slot(slot, k) = -1;
-        else if (!a.order)
-          *row_slot(slot, k) = static_cast<int>(pos0 + r);
-        else
-          cp_async_4(row_slot(slot, k), a.order + pos0 + r);
-      }
-    };
-    int64_t c = kW ? c0 + 8 * pch : static_cast<int64_t>(s0) * 64 * L::kSub + 8 * pch;  // this thread's column
-    if (kW) {
-      for (int i = 0; i <= L::kLag && i < ns; ++i) request_rows(i, i);
-      cp_async_commit();
-      cp_async_wait<0>();
-      __syncwarp();
-    } else {
+    if (!kW) {
 #pragma unroll
       for (int k = 0; k < L::kPer; ++k) {
         m[k] = rowbuf[prow + L::kStep * k];
         src[k] = P + (m[k] >= 0 ? static_cast<int64_t>(m[k]) * a.C : 0) + c;
       }
     }
+    // wgrad: the rows (-1: none) of kRowStages stages at a time, the next set's in registers half a set ahead
+    const bool pin = c < a.C;
+    const uint16_t* pcol = P + (pin ? c : 0);
+    const uint32_t psize = pin ? 16u : 0u;
+    constexpr int kRowPer = kRowStages * 64 / kLtcLoaders;
+    int rnext[kRowPer];
+    auto fetch_rows = [&](int i) {  // of the set that begins with stage i
+#pragma unroll
+      for (int k = 0; k < kRowPer; ++k) {
+        const int64_t r = static_cast<int64_t>(s0 + i) * 64 + tid + kLtcLoaders * k;
+        rnext[k] = r < cnt ? static_cast<int>(lora_row(a, pos0 + r)) : -1;
+      }
+    };
+    if (kW && ns > 0) fetch_rows(0);
     // the B operand: chunks tid + 512 k of the stage
     const uint16_t* wsrc[L::kPerW];
     uint32_t wdst[L::kPerW], wsize[L::kPerW];
@@ -361,7 +366,6 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
       if (kMode == kReduceA) {  // row: j; 8 kSub chunks of its columns
         row = q / (8 * L::kSub);
         ch = q % (8 * L::kSub);
-        wdst[k] = (ch >> 3) * L::kPlaneW + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
         wsize[k] = mine && row < a.rank ? 16u : 0u;
         wrow[k] = 8 * ch;
         wsrc[k] = static_cast<const uint16_t*>(a.W) + l * a.ws + (wsize[k] ? row * a.C : 0) +
@@ -370,86 +374,102 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
         constexpr int kRowChunks = kW ? RP / 4 : RP / 8;
         row = q / kRowChunks;
         ch = q % kRowChunks;
-        wdst[k] = (ch >> 3) * L::kPlaneW + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
         wsize[k] = mine && (kW || 8 * ch < a.rank) ? 16u : 0u;
         wrow[k] = row;
         wsrc[k] = kW ? static_cast<const uint16_t*>(a.Q) + (pos0 + static_cast<int64_t>(s0) * 64 + row) * (2 * RP) + 8 * ch
                      : static_cast<const uint16_t*>(a.W) + l * a.ws +
                            (static_cast<int64_t>(s0) * 64 * L::kSub + row) * a.rank + 8 * ch;
       }
+      wdst[k] = L::kTileP + (ch >> 3) * L::kPlaneW + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
     }
     const int64_t wadvance = kMode == kReduceA ? 64 * L::kSub : (kW ? 64 * 2 * RP : 64 * L::kSub * a.rank);
     // summation indexes left from the current stage on (columns or positions)
     int64_t left = kW ? cnt - static_cast<int64_t>(s0) * 64 : a.C - static_cast<int64_t>(s0) * 64 * L::kSub;
-    int s = 0, hs = 0;       // ring slots of the stage requested and of the one handed over
-    int rs = 0, rh = 0, rn = L::kLag + 1;  // slots of the rows of those two and of the ones requested
-    int64_t hc = c;
-    uint32_t parity = 1u;    // of the phase of empty[s] to wait for
-    for (int i = 0; i < ns + L::kLag && ok; ++i) {
-      if (i < ns) {
-        if (i >= L::kRing) {
-          ok = mbar_wait(&empty[s], parity);
-          if (!ok) break;
-        }
-        uint8_t* st = sm + s * L::kStage;
-        if (kW) {
-          const bool in = c < a.C;
-#pragma unroll
-          for (int k = 0; k < L::kPer; ++k) {
-            const int64_t mk = *row_slot(rs, k);
-            const bool there = in && mk >= 0 && mk < a.M;
-            cp_async_16(st + pdst + k * L::kStep * 128, P + (there ? mk * a.C + c : 0), there ? 16u : 0u);
-          }
-          if (i + L::kLag + 1 < ns) request_rows(i + L::kLag + 1, rn);
-          if (++rs == L::kRowRing) rs = 0;
-          if (++rn == L::kRowRing) rn = 0;
-        } else {
-          const uint32_t size = 8 * pch < left ? 16u : 0u;
-#pragma unroll
-          for (int k = 0; k < L::kPer; ++k) {
-            if (m[k] >= 0) cp_async_16(st + pdst + k * L::kStep * 128, size ? src[k] : P, size);
-            src[k] += 64 * L::kSub;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < L::kPerW; ++k) {
-          if (L::kChunksW % kLtcLoaders != 0 && tid + kLtcLoaders * k >= L::kChunksW) continue;
-          const uint32_t size = wrow[k] < left ? wsize[k] : 0u;
-          uint8_t* dst = st + L::kTileP + wdst[k];
-          if (kMode != kReduceB || bvec) {
-            cp_async_16(dst, size ? wsrc[k] : P, size);
-          } else {  // rows of B that are not whole 16-byte vectors
-            const int ch = (tid + kLtcLoaders * k) % (RP / 8);
-            *reinterpret_cast<uint4*>(dst) =
-                size ? load8(wsrc[k] - 8 * ch, 8 * ch, a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
-          }
-          wsrc[k] += wadvance;
-        }
-        left -= kW ? 64 : 64 * L::kSub;
-        if (++s == L::kRing) {
-          s = 0;
-          parity ^= 1u;
-        }
-      }
-      cp_async_commit();
-      if (i < L::kLag) continue;
-      cp_async_wait<L::kLag>();
-      if (kDrop) {
-        uint8_t* st = sm + hs * L::kStage + pdst;
+    // One stage; kTail: some of its summation indexes are past the end, and zeros.
+    auto request = [&](auto tail, int i, uint32_t st) {
+      constexpr bool kTail = decltype(tail)::value;
+      if (kW) {
+        const int* rows = rowbuf + (i % (2 * kRowStages)) * 64 + prow;
 #pragma unroll
         for (int k = 0; k < L::kPer; ++k) {
-          const int64_t mk = kW ? *row_slot(rh, k) : m[k];
-          uint4* x = reinterpret_cast<uint4*>(st + k * L::kStep * 128);
-          if (mk >= 0 && mk < a.M && hc < a.C) *x = drop_apply16(*x, (mk * a.C + hc) >> 3, key, a.drop.thr);
+          const int mk = rows[L::kStep * k];
+          cp_async_16s(st + pdst + k * L::kStep * 128, pcol + static_cast<int64_t>(mk < 0 ? 0 : mk) * a.C,
+                       mk < 0 ? 0u : psize);
         }
-        if (!kW) hc += 64 * L::kSub;
-        if (kW && ++rh == L::kRowRing) rh = 0;
+      } else {
+        const uint32_t size = !kTail || 8 * pch < left ? 16u : 0u;
+#pragma unroll
+        for (int k = 0; k < L::kPer; ++k) {
+          if (m[k] >= 0) cp_async_16s(st + pdst + k * L::kStep * 128, size ? src[k] : P, size);
+          src[k] += 64 * L::kSub;
+        }
       }
-      __syncwarp();  // also: the rows that came with this group of copies are there for the whole warp
+#pragma unroll
+      for (int k = 0; k < L::kPerW; ++k) {
+        if (L::kChunksW % kLtcLoaders != 0 && tid + kLtcLoaders * k >= L::kChunksW) continue;
+        const uint32_t size = !kTail || wrow[k] < left ? wsize[k] : 0u;
+        if (kMode != kReduceB || bvec) {
+          cp_async_16s(st + wdst[k], size ? wsrc[k] : P, size);
+        } else {  // rows of B that are not whole 16-byte vectors
+          const int ch = (tid + kLtcLoaders * k) % (RP / 8);
+          *reinterpret_cast<uint4*>(sm + (st - ring0) + wdst[k]) =
+              size ? load8(wsrc[k] - 8 * ch, 8 * ch, a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        wsrc[k] += wadvance;
+      }
+      left -= kW ? 64 : 64 * L::kSub;
+    };
+    int hd = 0, hs = 0;  // the stage to hand over and its slot
+    auto hand_over = [&]() {
+      if (kDrop) {
+        uint8_t* st = sm + hs * L::kStage + pdst;
+        const int64_t hc = kW ? c : c + static_cast<int64_t>(hd) * 64 * L::kSub;
+        if (hc < a.C)
+#pragma unroll
+          for (int k = 0; k < L::kPer; ++k) {
+            const int64_t mk = kW ? rowbuf[(hd % (2 * kRowStages)) * 64 + prow + L::kStep * k] : m[k];
+            uint4* x = reinterpret_cast<uint4*>(st + k * L::kStep * 128);
+            if (mk >= 0) *x = drop_apply16(*x, (mk * a.C + hc) >> 3, key, a.drop.thr);
+          }
+      }
+      __syncwarp();
       if (lane == 0) mbar_arrive(&full[hs]);
+      ++hd;
       if (++hs == L::kRing) hs = 0;
+    };
+    uint32_t st = ring0, parity = 1u;  // the slot of the stage requested, and the parity of its last release
+    uint64_t* release = empty;
+    for (int i = 0; i < ns; ++i) {
+      if (kW && i % kRowStages == 0) {
+        // The set before last is not read any more: a warp is at most a ring ahead of another.
+#pragma unroll
+        for (int k = 0; k < kRowPer; ++k) rowbuf[(i % (2 * kRowStages)) * 64 + tid + kLtcLoaders * k] = rnext[k];
+        named_barrier_sync(1, kLtcLoaders);
+      }
+      if (kW && i % kRowStages == kRowStages / 2 && i + kRowStages / 2 < ns) fetch_rows(i + kRowStages / 2);
+      if (i >= L::kRing) {
+        ok = mbar_wait(release, parity);
+        if (!ok) break;
+      }
+      if (left >= (kW ? 64 : 64 * L::kSub))
+        request(std::false_type(), i, st);
+      else
+        request(std::true_type(), i, st);
+      st += L::kStage;
+      ++release;
+      if (st == ring1) {
+        st = ring0;
+        release = empty;
+        parity ^= 1u;
+      }
+      cp_async_commit();
+      if (i >= L::kLag) {
+        cp_async_wait<L::kLag>();
+        hand_over();
+      }
     }
     cp_async_wait<0>();
+    while (hd < ns && ok) hand_over();
     if (ns > 0) ok = ok && mbar_wait(accFull, 0u);
   } else if (lane == 0) {
     // ------------------------------------------------------------------ MMA issuer
@@ -838,6 +858,8 @@ cudaError_t launch_lora_split(bool bf16, bool both, const LoraWorkspace& w, cons
 // consecutive ones: column c = 8 u + 2 j + e of a block of 32 is column 2 u + e of tile j.  base is requested two blocks ahead.
 // Four loader warps bring W: as B [C, rank] a column's 16-byte pieces with cp.async, as A [rank, C] through registers, since pairs
 // of columns part ways (4-byte cp.async took 78 cycles an instruction).  Only barriers of single stages tie the warps.
+// All tiles' blocks in a row are dealt to the CTAs, one per SM, in equal runs, which cross from tile to tile where they must: with a CTA
+// per tile and range of columns, SMs were idle for a third of the time (4096 rows, 6 adapters, rank 32, 18944 columns: 81 us).
 // mma.sync on the same fragments, two CTAs per SM, was bound by the MMA rate from rank 64 on (rank 128, 8192 x 8192: 150 us; this 93).
 // ---------------------------------------------------------------------------------------------
 constexpr int kXpEpi = 16;     // epilogue warps
@@ -845,6 +867,7 @@ constexpr int kXpLoad = 4;     // loader warps; the first also issues the MMAs (
 constexpr int kXpThreads = 32 * (kXpEpi + kXpLoad);
 constexpr int kXpCols = 128;   // columns per block (MMA N)
 constexpr int kXpRing = 4;     // stages of W, and of D
+constexpr int kXpCopy = 8;     // vectors per lane and round where rows of no adapter are copied
 
 template <int RP, bool kWA>
 struct LoraXpLayout {
@@ -856,7 +879,7 @@ struct LoraXpLayout {
   static constexpr int kOffW = kTileV;
   static constexpr int kOffBar = kOffW + kXpRing * kTileW;            // wfull, wempty, dfull, dempty, vfull; TMEM slot
   static constexpr int kOffF = kOffBar + (4 * kXpRing + 2) * 8;       // fp32 factor of each position
-  static constexpr int kBytes = kOffF + 128 * 4 + 1024;
+  static constexpr int kBytes = kOffF + 2 * 128 * 4 + 1024;
   static constexpr int kAlloc = kBytes > 116 * 1024 + 64 ? kBytes : 116 * 1024 + 64;  // one CTA per SM, as above
   static_assert(kAlloc <= 227 * 1024 && kTileW % 1024 == 0, "shared memory");
 };
@@ -871,7 +894,7 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
 }
 
 template <typename T, int RP, bool kWA, bool kDrop>
-__global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const LoraArgs a, const int blocks_per_cta) {
+__global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const LoraArgs a) {
   using L = LoraXpLayout<RP, kWA>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -885,29 +908,11 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait_prior_grids();
-  const LoraTile tile = lora_tile(a.offsets, a.L, a.M, blockIdx.x);
-  if (tile.l == -2) return;
-  const int64_t c_begin = static_cast<int64_t>(blockIdx.y) * blocks_per_cta * kXpCols;
-  const int64_t c_end = c_begin + static_cast<int64_t>(blocks_per_cta) * kXpCols < a.C
-                            ? c_begin + static_cast<int64_t>(blocks_per_cta) * kXpCols
-                            : a.C;
+  const int64_t nblk = (a.C + kXpCols - 1) / kXpCols, total = lora_tiles(a.offsets, a.L, a.M) * nblk;
+  const int64_t run0 = total * blockIdx.x / gridDim.x, run1 = total * (blockIdx.x + 1) / gridDim.x;
+  if (run0 == run1) return;
   const T* base = static_cast<const T*>(a.base);
   T* out = static_cast<T*>(a.O);
-  if (tile.l < 0) {  // rows of no adapter: base alone
-    if (base == out) return;
-    const int64_t head = clamp_pos(a.offsets[0], a.M), at = clamp_pos(a.offsets[a.L], a.M);
-    const int vecs = static_cast<int>((c_end - c_begin) >> 3);
-    for (int i = warp; i < tile.cnt; i += kXpThreads / 32) {
-      const int64_t q = tile.pos + i, m = lora_row(a, q < head ? q : q - head + at);
-      if (m < 0) continue;
-      uint4* dst = reinterpret_cast<uint4*>(out + m * a.C + c_begin);
-      const uint4* src = reinterpret_cast<const uint4*>(base + m * a.C + c_begin);
-#pragma unroll 4
-      for (int j = lane; j < vecs; j += 32) dst[j] = base ? src[j] : make_uint4(0u, 0u, 0u, 0u);
-    }
-    return;
-  }
-  const int nb = static_cast<int>((c_end - c_begin + kXpCols - 1) / kXpCols);
 
   if (tid == 0) {
     for (int i = 0; i < kXpRing; ++i) {
@@ -933,6 +938,36 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
   if (warp < kXpEpi) {
     // ------------------------------------------------------------------ epilogue
     const int g = lane >> 2, t = lane & 3, r0 = (warp & 3) * 32 + g;
+    const PhiloxKey key = kDrop ? philox_key(a.drop) : PhiloxKey{0u, 0u, 0u, 0u};
+    int s = 0, seg = 0;
+    uint32_t parity = 0u;
+    for (int64_t run = run0; run < run1 && ok;) {
+    const int64_t tn = run / nblk, c_begin = (run - tn * nblk) * kXpCols;
+    const int nb = static_cast<int>(run1 - run < nblk * (tn + 1) - run ? run1 - run : nblk * (tn + 1) - run);
+    const int64_t c_end = c_begin + static_cast<int64_t>(nb) * kXpCols < a.C ? c_begin + static_cast<int64_t>(nb) * kXpCols : a.C;
+    run += nb;
+    const LoraTile tile = lora_tile(a.offsets, a.L, a.M, static_cast<int>(tn));
+    if (tile.l < 0) {  // rows of no adapter: base alone
+      if (base == out) continue;
+      const int64_t head = clamp_pos(a.offsets[0], a.M), at = clamp_pos(a.offsets[a.L], a.M);
+      const int vecs = static_cast<int>((c_end - c_begin) >> 3);
+      for (int i = warp; i < tile.cnt; i += kXpEpi) {
+        const int64_t q = tile.pos + i, m = lora_row(a, q < head ? q : q - head + at);
+        if (m < 0) continue;
+        uint4* dst = reinterpret_cast<uint4*>(out + m * a.C + c_begin);
+        const uint4* src = reinterpret_cast<const uint4*>(base + m * a.C + c_begin);
+        for (int j = lane; j < vecs; j += 32 * kXpCopy) {  // all loads of a round before its stores
+          uint4 x[kXpCopy];
+#pragma unroll
+          for (int k = 0; k < kXpCopy; ++k)
+            x[k] = base && j + 32 * k < vecs ? src[j + 32 * k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int k = 0; k < kXpCopy; ++k)
+            if (j + 32 * k < vecs) dst[j + 32 * k] = x[k];
+        }
+      }
+      continue;
+    }
     int m[4];  // rows of positions r0 + 8 i
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -948,7 +983,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     load_base(y[0], c);
     load_base(y[1], c + kXpCols);
     {
-      // V of the tile as hi and lo, four threads per position
+      // V of the tile as hi and lo, four threads per position (the last run's MMAs have read theirs: this warp has seen their sums)
       const int row = tid >> 2, part = tid & 3;
       constexpr int kE = RP / 4;  // inner columns per thread
       const bool there = row < tile.cnt;
@@ -984,17 +1019,14 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
         *reinterpret_cast<uint2*>(sm + (kh >> 6) * 16384 + row * 128 + ((((kh >> 3) & 7) ^ (row & 7)) << 4) + (kh & 4) * 2) = hi;
         *reinterpret_cast<uint2*>(sm + (kl >> 6) * 16384 + row * 128 + ((((kl >> 3) & 7) ^ (row & 7)) << 4) + (kl & 4) * 2) = lo;
       }
-      if (part == 0) rowf[row] = inv * lora_factor(a, tile.l);
+      if (part == 0) rowf[(seg & 1) * 128 + row] = inv * lora_factor(a, tile.l);
       __syncwarp();
       if (lane == 0) mbar_arrive(vfull);
     }
-    const PhiloxKey key = kDrop ? philox_key(a.drop) : PhiloxKey{0u, 0u, 0u, 0u};
-    named_barrier_sync(1, 32 * kXpEpi);  // rowf
+    named_barrier_sync(1, 32 * kXpEpi);  // rowf; two of them, since a warp may be done with a short run before another reads this one's
     float f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = rowf[r0 + 8 * i];
-    int s = 0;
-    uint32_t parity = 0u;
+    for (int i = 0; i < 4; ++i) f[i] = rowf[(seg & 1) * 128 + r0 + 8 * i];
     auto block = [&](uint4 (&yb)[4]) {
       ok = ok && mbar_wait(&dfull[s], parity);
       if (!ok) return;
@@ -1040,16 +1072,25 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
         c += kXpCols;
       }
     }
+    ++seg;
+    }
   } else {
     // ------------------------------------------------------------------ loaders of W; the first warp also issues the MMAs
     const int w = tid - 32 * kXpEpi;  // 0 .. 127
-    const uint16_t* W = static_cast<const uint16_t*>(a.W) + tile.l * a.ws;
     const bool bvec = (a.rank & 7) == 0;
     constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
     constexpr uint32_t kIdesc = idesc_f16_f32(128, kXpCols) | kType | (kWA ? 1u << 16 : 0u);
     const uint32_t base_v = smem_u32(sm);
-    int s = 0, hs = 0;
+    int s = 0, hs = 0, seg = 0;
     uint32_t parity = 1u, hparity = 0u;
+    int64_t done = 0;  // blocks requested in earlier runs
+    for (int64_t run = run0; run < run1 && ok;) {
+    const int64_t tn = run / nblk, c_begin = (run - tn * nblk) * kXpCols;
+    const int nb = static_cast<int>(run1 - run < nblk * (tn + 1) - run ? run1 - run : nblk * (tn + 1) - run);
+    run += nb;
+    const LoraTile tile = lora_tile(a.offsets, a.L, a.M, static_cast<int>(tn));
+    if (tile.l < 0) continue;
+    const uint16_t* W = static_cast<const uint16_t*>(a.W) + tile.l * a.ws;
     // A: chunk (row j = w / 16 + 8 i, eight columns from 8 (w % 16)) of a block, a block ahead in registers
     constexpr int kPerA = kWA ? RP / 8 : 1;
     uint4 pre[kPerA];
@@ -1064,7 +1105,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     if (kWA) load_a(0);
     for (int b = 0; b < nb + L::kLag && ok; ++b) {
       if (b < nb) {
-        if (b >= kXpRing) {
+        if (done + b >= kXpRing) {
           ok = mbar_wait(&wempty[s], parity);
           if (!ok) break;
         }
@@ -1112,8 +1153,8 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
       if (warp == kXpEpi) {
         // the MMAs of the block handed over: four buffers of D keep the epilogue busy while this warp waits
         const int d = b - L::kLag;
-        ok = (d > 0 || mbar_wait(vfull, 0u)) && mbar_wait(&wfull[hs], hparity) &&
-             (d < kXpRing || mbar_wait(&dempty[hs], hparity ^ 1u));
+        ok = (d > 0 || mbar_wait(vfull, static_cast<uint32_t>(seg & 1))) && mbar_wait(&wfull[hs], hparity) &&
+             (done + d < kXpRing || mbar_wait(&dempty[hs], hparity ^ 1u));
         if (!ok) break;
         if (lane == 0) {
           fence_proxy_async_smem();  // for the copies and stores of the other warps, which the barriers order before this point
@@ -1139,6 +1180,9 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
         hparity ^= 1u;
       }
     }
+    done += nb;
+    ++seg;
+    }
     cp_async_wait<0>();
   }
   __syncwarp();
@@ -1151,35 +1195,25 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
 }
 
 template <typename T, int RP, bool kWA, bool kDrop>
-static cudaError_t launch_lora_expand_tc(const LoraArgs& a, int64_t tiles, int64_t est, cudaStream_t s) {
+static cudaError_t launch_lora_expand_tc(const LoraArgs& a, cudaStream_t s) {
   auto* kern = lora_expand_tc_kernel<T, RP, kWA, kDrop>;
   constexpr int kAlloc = LoraXpLayout<RP, kWA>::kAlloc;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kAlloc);
   if (e != cudaSuccess) return e;
-  // columns split so that waves of CTAs cost least, a CTA's start and end counted as eight blocks
-  const int64_t sms = current_device_info().num_sms, blocks = (a.C + kXpCols - 1) / kXpCols;
-  int64_t per = blocks, cost = -1;
-  for (int64_t split = 1; split <= blocks && split <= 64; ++split) {
-    const int64_t p = (blocks + split - 1) / split;
-    const int64_t c = (est * ((blocks + p - 1) / p) + sms - 1) / sms * (p + 8);
-    if (cost < 0 || c < cost) {
-      cost = c;
-      per = p;
-    }
-  }
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((blocks + per - 1) / per));
-  return launch_pdl(kern, grid, dim3(kXpThreads), kAlloc, 1, s, a, static_cast<int>(per));
+  // a CTA per SM, fewer where that would leave them a single block
+  const int64_t sms = current_device_info().num_sms;
+  const int64_t runs = (lora_max_tiles(a.M, a.L) * ((a.C + kXpCols - 1) / kXpCols) + 1) / 2;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(runs < sms ? runs : sms)), dim3(kXpThreads), kAlloc, 1, s, a);
 }
 
 static cudaError_t lora_fast_expand(bool bf16, const LoraArgs& a, cudaStream_t s) {
-  const int64_t tiles = lora_max_tiles(a.M, a.L), est = lora_likely_tiles(a.M, a.L);
   return with_type16(bf16, [&](auto t) {
     using T = decltype(t);
     return with_rank(a.rank, [&](auto rp) {
       constexpr int RP = decltype(rp)::value;
-      if (a.wc != 1) return launch_lora_expand_tc<T, RP, false, false>(a, tiles, est, s);
-      return a.drop.thr ? launch_lora_expand_tc<T, RP, true, true>(a, tiles, est, s)
-                        : launch_lora_expand_tc<T, RP, true, false>(a, tiles, est, s);
+      if (a.wc != 1) return launch_lora_expand_tc<T, RP, false, false>(a, s);
+      return a.drop.thr ? launch_lora_expand_tc<T, RP, true, true>(a, s)
+                        : launch_lora_expand_tc<T, RP, true, false>(a, s);
     });
   });
 }
