@@ -86,7 +86,7 @@ __device__ __forceinline__ uint4 load8(const void* row, int64_t c, int64_t width
 // ---------------------------------------------------------------------------------------------
 // Tiles.  Tile t of a plan: the tiles of adapter 0, of adapter 1, ..., then those of the positions of no adapter (l = -1),
 // which are counted on from the ones before offsets[0] to the ones from offsets[L] on.  Run by a whole warp, all of
-// whose lanes get the result.  A plan has at most lora_max_tiles().
+// whose lanes get the result.  A plan has at most lora_max_tiles(); kTile positions each.
 // ---------------------------------------------------------------------------------------------
 struct LoraTile {
   int l;        // adapter, -1: none, -2: past the last tile
@@ -97,6 +97,7 @@ struct LoraTile {
 
 __device__ __forceinline__ int64_t clamp_pos(int64_t o, int64_t M) { return o < 0 ? 0 : (o < M ? o : M); }
 
+template <int kTile = kLoraTile>
 __device__ __forceinline__ LoraTile lora_tile(const int32_t* offsets, int L, int64_t M, int t) {
   const int lane = threadIdx.x & 31;
   LoraTile r = {-2, 0, 0, 0};
@@ -111,7 +112,7 @@ __device__ __forceinline__ LoraTile lora_tile(const int32_t* offsets, int L, int
     int n[4], sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      n[i] = o[i + 1] > o[i] ? static_cast<int>((o[i + 1] - o[i] + kLoraTile - 1) / kLoraTile) : 0;
+      n[i] = o[i + 1] > o[i] ? static_cast<int>((o[i + 1] - o[i] + kTile - 1) / kTile) : 0;
       sum += n[i];
     }
     int incl = sum;
@@ -130,8 +131,8 @@ __device__ __forceinline__ LoraTile lora_tile(const int32_t* offsets, int L, int
         if (mine && t >= before && t < before + n[i]) {
           f.l = l0 + 4 * lane + i;
           f.first = before;
-          f.pos = o[i] + static_cast<int64_t>(t - before) * kLoraTile;
-          f.cnt = static_cast<int>(o[i + 1] - f.pos < kLoraTile ? o[i + 1] - f.pos : kLoraTile);
+          f.pos = o[i] + static_cast<int64_t>(t - before) * kTile;
+          f.cnt = static_cast<int>(o[i + 1] - f.pos < kTile ? o[i + 1] - f.pos : kTile);
         }
         before += n[i];
       }
@@ -145,11 +146,11 @@ __device__ __forceinline__ LoraTile lora_tile(const int32_t* offsets, int L, int
     done += total;
   }
   const int64_t head = clamp_pos(offsets[0], M), tail = M - clamp_pos(offsets[L], M);
-  r.pos = static_cast<int64_t>(t - done) * kLoraTile;
+  r.pos = static_cast<int64_t>(t - done) * kTile;
   if (r.pos < head + tail) {
     r.l = -1;
     r.first = done;
-    r.cnt = static_cast<int>(head + tail - r.pos < kLoraTile ? head + tail - r.pos : kLoraTile);
+    r.cnt = static_cast<int>(head + tail - r.pos < kTile ? head + tail - r.pos : kTile);
   }
   return r;
 }
@@ -165,8 +166,8 @@ __device__ __forceinline__ int64_t lora_tiles(const int32_t* offsets, int L, int
   return warp_sum(sum) + (none + kLoraTile - 1) / kLoraTile;
 }
 
-static int64_t lora_max_tiles(int64_t M, int64_t L) {
-  const int64_t t = M / kLoraTile + L + 1;
+static int64_t lora_max_tiles(int64_t M, int64_t L, int tile = kLoraTile) {
+  const int64_t t = M / tile + L + 1;
   return t < M ? t : M;
 }
 
@@ -1222,14 +1223,28 @@ static cudaError_t lora_fast_expand(bool bf16, const LoraArgs& a, cudaStream_t s
 // Few rows: one launch.  A cluster of eight CTAs takes up to eight positions of one adapter: each CTA sums an eighth of the columns
 // of x (m16n8k16: 16 inner columns x 8 positions), the partial sums meet through distributed shared memory in rank order,
 // and each CTA then computes an eighth of the columns of out (16 x 8: 8 positions, rows 8 .. 15 unused, x 8 columns).
-// Bound by the latency of this chain and, with many adapters, by reading each one's A and B once from HBM: B is asked into L2 before
-// A is read, and a warp holds the first 32 columns of its part of B and base in registers before the partial sums meet.
-// Operand fragments come straight from memory: within 32 k, lane t of a quad takes the eight consecutive k = 8 t .. 8 t + 7 (both
-// operands the same, so the order within the sum does not matter) in one 16-byte load.
+// Bound by the latency of this chain and, with many adapters, by reading each one's A and B once from HBM.  So B does not wait for
+// the chain: 32 rows of B are one piece of memory, and each warp keeps the next two or three such blocks in flight into
+// shared memory of its own by bulk copies from the start on.  (B ahead in registers spilled; asked into L2 by prefetches, these
+// held up the warps that made them for up to 6 us.)
+// Within 32 k, lane t of a quad takes the eight consecutive k = 8 t .. 8 t + 7 (both operands the same, so the order within the sum
+// does not matter) in one 16-byte load.
 // ---------------------------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kFewRows = 8;
 constexpr int kFewCluster = 8;
+
+template <int RP>
+struct LoraFewLayout {
+  static constexpr int kSlots = RP <= 32 ? 3 : 2;       // blocks of B in flight per warp
+  static constexpr int kSlot = 32 * RP * 2;
+  static constexpr int kOffRed = kFewWarps * kSlots * kSlot;             // partial sums of the warps [inner column][position]
+  static constexpr int kOffPart = kOffRed + kFewWarps * RP * kFewRows * 4;  // of the CTA
+  static constexpr int kOffV = kOffPart + RP * kFewRows * 4;             // v [position][inner column]
+  static constexpr int kOffBar = kOffV + RP * kFewRows * 4;
+  static constexpr int kBytes = kOffBar + kFewWarps * kSlots * 8;
+};
 
 struct LoraFewArgs {
   const void* x;
@@ -1245,133 +1260,125 @@ struct LoraFewArgs {
   int L, rank;
 };
 
-// adapter_of by a whole warp: two dependent loads (1024 adapters take at most 33 steps of 32 offsets).
-__device__ __forceinline__ int adapter_of_warp(const int32_t* offsets, int L, int64_t r) {
-  const int lane = threadIdx.x & 31;
-  const int step = (L + 32) / 32;  // 32 steps cover the L + 1 offsets
-  const int i0 = lane * step;
-  const uint32_t below = __ballot_sync(0xFFFFFFFFu, i0 <= L && offsets[i0 <= L ? i0 : L] <= r);
-  if (!below) return -1;
-  const int seg = (31 - __clz(below)) * step;
-  int last = seg;
-  for (int j = 1; j < step; j += 32) {
-    const int i = seg + j + lane;
-    const uint32_t b = __ballot_sync(0xFFFFFFFFu, j + lane < step && i <= L && offsets[i <= L ? i : L] <= r);
-    if (b) last = seg + j + (31 - __clz(b));
-  }
-  return last < L ? last : -1;
-}
-
-template <typename T, int RP>
-__global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const LoraFewArgs a) {
+// kVec: rows of B in whole 16-byte vectors (8-byte ones for RP = 16).
+template <typename T, int RP, bool kVec>
+__global__ void __launch_bounds__(kFewThreads, RP <= 64 ? 2 : 1) lora_few_kernel(const LoraFewArgs a) {
+  using L = LoraFewLayout<RP>;
   constexpr int RT = RP / 16;                 // tiles of 16 inner columns
   constexpr int KG = RP < 32 ? 1 : RP / 32;   // groups of 32 inner columns (RP = 16: one of 16)
-  __shared__ float red[8][RP * kFewRows];     // partial sums of the warps: [inner column][position]
-  __shared__ float part[RP * kFewRows];       // of the CTA
-  __shared__ float vs[kFewRows][RP];
+  extern __shared__ __align__(128) uint8_t few_smem[];
+  uint8_t* sm = few_smem;
+  float* part = reinterpret_cast<float*>(sm + L::kOffPart);
+  float* vs = reinterpret_cast<float*>(sm + L::kOffV);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  float* red = reinterpret_cast<float*>(sm + L::kOffRed) + warp * RP * kFewRows;
+  uint8_t* slots = sm + warp * L::kSlots * L::kSlot;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kOffBar) + warp * L::kSlots;
+  if (lane == 0) {
+    for (int i = 0; i < L::kSlots; ++i) mbar_init(&bars[i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   pdl_allow_dependents();
   pdl_wait_prior_grids();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x);  // in the cluster
-  const int64_t r = blockIdx.y;
-  const int l = adapter_of_warp(a.offsets, a.L, r);
+  const LoraTile chunk = lora_tile<kFewRows>(a.offsets, a.L, a.M, blockIdx.y);
+  if (chunk.l == -2) return;  // (the whole cluster, as below)
+  const int64_t r = chunk.pos;
+  const int l = chunk.l, cnt = chunk.cnt;
   // columns of out of this CTA, in blocks of 32
-  const int64_t nblk = (a.N + 31) / 32;
-  const int64_t b0 = rank * nblk / kFewCluster, b1 = (rank + 1) * nblk / kFewCluster;
+  const int nblk = static_cast<int>((a.N + 31) / 32);
+  const int parts = kFewCluster * static_cast<int>(gridDim.z), part_id = static_cast<int>(blockIdx.z) * kFewCluster + rank;
+  const int b0 = static_cast<int>(static_cast<int64_t>(part_id) * nblk / parts);
+  const int b1 = static_cast<int>(static_cast<int64_t>(part_id + 1) * nblk / parts);
   auto row_of = [&](int64_t q) {
     const int64_t m = a.order ? static_cast<int64_t>(a.order[q]) : q;
     return m >= 0 && m < a.M ? m : -1;
   };
-  if (l < 0) {  // a row of no adapter: base alone
-    const int64_t m = row_of(r);
-    if (m < 0 || a.base == a.out) return;
-    const int64_t c1 = b1 * 32 < a.N ? b1 * 32 : a.N;
-    for (int64_t c = b0 * 32 + 8 * tid; c < c1; c += 8 * kFewThreads)
+  if (l < 0) {  // rows of no adapter: base alone, a warp each
+    if (a.base == a.out || warp >= cnt) return;
+    const int64_t head = clamp_pos(a.offsets[0], a.M), q = r + warp;
+    const int64_t m = row_of(q < head ? q : q - head + clamp_pos(a.offsets[a.L], a.M));
+    if (m < 0) return;
+    const int c1 = b1 * 32 < a.N ? b1 * 32 : static_cast<int>(a.N);
+    for (int c = b0 * 32 + 8 * lane; c < c1; c += 8 * 32)
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + m * a.N + c) =
           a.base ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.base) + m * a.N + c)
                  : make_uint4(0u, 0u, 0u, 0u);
     return;
   }
-  const int64_t first = a.offsets[l] < 0 ? 0 : a.offsets[l];
-  if ((r - first) % kFewRows != 0) return;  // another cluster's
-  const int64_t end = a.offsets[l + 1] < a.M ? a.offsets[l + 1] : a.M;
-  const int cnt = static_cast<int>(end - r < kFewRows ? end - r : kFewRows);
   const int64_t m = g < cnt ? row_of(r + g) : -1;  // of this lane's position
   const T* A = static_cast<const T*>(a.A) + static_cast<int64_t>(l) * a.rank * a.K;
   const T* B = static_cast<const T*>(a.B) + static_cast<int64_t>(l) * a.rank * a.N;
-  const bool bvec = (a.rank & 7) == 0;
+  // Block blk of B into slot s of this warp (whole 16-byte pieces: N is a multiple of 8); one lane.
+  auto request = [&](int blk, int s) {
+    const int64_t n0 = static_cast<int64_t>(blk) * 32, n = a.N - n0 < 32 ? a.N - n0 : 32;
+    const uint32_t bytes = static_cast<uint32_t>(n * a.rank * 2);
+    mbar_arrive_expect_tx(&bars[s], bytes);
+    bulk_load_1d(slots + s * L::kSlot, B + n0 * a.rank, bytes, &bars[s]);
+  };
+  if (lane == 0)
+    for (int i = 0; i < L::kSlots; ++i)
+      if (b0 + warp + kFewWarps * i < b1) request(b0 + warp + kFewWarps * i, i);
+
+  // ---- an eighth of x A^T, groups of 32 columns dealt to the warps.  No load of A depends on a bound: where a row or column is past
+  // the end the address is one within the same matrix row, and what is read there meets a zero of x or goes to an unused sum.
+  const int K = static_cast<int>(a.K), ng = (K + 31) / 32, g0 = rank * ng / kFewCluster, g1 = (rank + 1) * ng / kFewCluster;
   {
-    const char* p0 = reinterpret_cast<const char*>(B + b0 * 32 * a.rank);
-    const char* p1 = reinterpret_cast<const char*>(B + (b1 * 32 < a.N ? b1 * 32 : a.N) * a.rank);
-    for (const char* p = p0 + 128 * tid; p < p1; p += 128 * kFewThreads)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-  }
-
-  // ---- an eighth of x A^T, groups of 32 columns dealt to the warps
-  float acc[RT][4] = {};
-  const int64_t ng = (a.K + 31) / 32, g0 = rank * ng / kFewCluster, g1 = (rank + 1) * ng / kFewCluster;
-  const T* xrow = static_cast<const T*>(a.x) + (m >= 0 ? m * a.K : 0);
-#pragma unroll 2
-  for (int64_t q = g0 + warp; q < g1; q += 8) {
-    const int64_t k = 32 * q + 8 * t;
-    const uint4 xv = m >= 0 ? load8(xrow, k, a.K, true) : make_uint4(0u, 0u, 0u, 0u);
-    uint4 lo[RT], hi[RT];
+    float acc[RT][4] = {};
+    const T* xrow = static_cast<const T*>(a.x) + (m >= 0 ? m * a.K : 0);
+    constexpr int kU = RP <= 32 ? 2 : 1;  // groups whose loads a warp has in flight
+    for (int q = g0 + warp; q < g1; q += kFewWarps * kU) {
+      uint4 xv[kU], lo[kU][RT], hi[kU][RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int j = 16 * i + g;
-      lo[i] = j < a.rank ? load8(A + j * a.K, k, a.K, true) : make_uint4(0u, 0u, 0u, 0u);
-      hi[i] = j + 8 < a.rank ? load8(A + (j + 8) * a.K, k, a.K, true) : make_uint4(0u, 0u, 0u, 0u);
-    }
+      for (int u = 0; u < kU; ++u) {
+        int k = 32 * (q + kFewWarps * u) + 8 * t;
+        const bool in = m >= 0 && q + kFewWarps * u < g1 && k < K;
+        if (k >= K) k = 0;
+        xv[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (in) xv[u] = *reinterpret_cast<const uint4*>(xrow + k);
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      mma16(acc[i], lo[i].x, hi[i].x, lo[i].y, hi[i].y, xv.x, xv.y, T());
-      mma16(acc[i], lo[i].z, hi[i].z, lo[i].w, hi[i].w, xv.z, xv.w, T());
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    *reinterpret_cast<float2*>(&red[warp][(16 * i + g) * kFewRows + 2 * t]) = make_float2(acc[i][0], acc[i][1]);
-    *reinterpret_cast<float2*>(&red[warp][(16 * i + g + 8) * kFewRows + 2 * t]) = make_float2(acc[i][2], acc[i][3]);
-  }
-
-  // ---- B and base of this warp's first 32 columns, while the partial sums meet
-  uint4 bw[KG][4], yv;
-  auto load_block = [&](int64_t blk) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {  // column 8 (g / 2) + 2 j + g % 2 of the block is column g of tile j
-      const int64_t n = 32 * blk + 8 * (g >> 1) + 2 * j + (g & 1);
-      const bool there = blk < b1 && n < a.N;
-      const T* row = B + (there ? n * a.rank : 0);
-#pragma unroll
-      for (int q = 0; q < KG; ++q) {
-        if (RP >= 32) {
-          bw[q][j] = there ? load8(row, 32 * q + 8 * t, a.rank, bvec) : make_uint4(0u, 0u, 0u, 0u);
-        } else {  // k = 4 t .. 4 t + 3
-          uint16_t h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            h[e] = there && 4 * t + e < a.rank ? reinterpret_cast<const uint16_t*>(row)[4 * t + e] : static_cast<uint16_t>(0);
-          bw[q][j] = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), 0u, 0u);
-          if ((a.rank & 3) == 0) {
-            const uint2 w = there && 4 * t < a.rank ? *reinterpret_cast<const uint2*>(row + 4 * t) : make_uint2(0u, 0u);
-            bw[q][j] = make_uint4(w.x, w.y, 0u, 0u);
-          }
+        for (int i = 0; i < RT; ++i) {
+          const int j = 16 * i + g;
+          const uint32_t j0 = static_cast<uint32_t>(j < a.rank ? j : a.rank - 1);
+          const uint32_t j1 = static_cast<uint32_t>(j + 8 < a.rank ? j + 8 : a.rank - 1);
+          lo[u][i] = *reinterpret_cast<const uint4*>(A + (j0 * static_cast<uint32_t>(K) + static_cast<uint32_t>(k)));
+          hi[u][i] = *reinterpret_cast<const uint4*>(A + (j1 * static_cast<uint32_t>(K) + static_cast<uint32_t>(k)));
         }
       }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          mma16(acc[i], lo[u][i].x, hi[u][i].x, lo[u][i].y, hi[u][i].y, xv[u].x, xv[u].y, T());
+          mma16(acc[i], lo[u][i].z, hi[u][i].z, lo[u][i].w, hi[u][i].w, xv[u].z, xv[u].w, T());
+        }
     }
-    const int64_t c = 32 * blk + 8 * t;
-    yv = a.base && m >= 0 && blk < b1 && c < a.N
-             ? *reinterpret_cast<const uint4*>(static_cast<const T*>(a.base) + m * a.N + c)
-             : make_uint4(0u, 0u, 0u, 0u);
-  };
-  int64_t blk = b0 + warp;
-  load_block(blk);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      *reinterpret_cast<float2*>(&red[(16 * i + g) * kFewRows + 2 * t]) = make_float2(acc[i][0], acc[i][1]);
+      *reinterpret_cast<float2*>(&red[(16 * i + g + 8) * kFewRows + 2 * t]) = make_float2(acc[i][2], acc[i][3]);
+    }
+  }
 
+  // ---- base of this warp's first blocks, and the partial sums meet
+  constexpr int kY = 2;
+  uint4 yv[kY];
+  const T* yrow = static_cast<const T*>(a.base) + (m >= 0 ? m * a.N : 0);
+  auto load_y = [&](int blk) {
+    const int c = 32 * blk + 8 * t;
+    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+    if (a.base && m >= 0 && blk < b1 && c < a.N) y = *reinterpret_cast<const uint4*>(yrow + c);
+    return y;
+  };
+#pragma unroll
+  for (int i = 0; i < kY; ++i) yv[i] = load_y(b0 + warp + kFewWarps * i);
   __syncthreads();
   for (int i = tid; i < RP * kFewRows; i += kFewThreads) {
+    const float* p = reinterpret_cast<const float*>(sm + L::kOffRed) + i;
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) s += red[w][i];
+    for (int w = 0; w < kFewWarps; ++w) s += p[w * RP * kFewRows];
     part[i] = s;
   }
   cluster_arrive();
@@ -1384,13 +1391,14 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const LoraFewArgs
 #pragma unroll
     for (int q = 0; q < kFewCluster; ++q) s += p[q];
     const int j = i / kFewRows, pos = i % kFewRows;
-    vs[pos][j] = s;
-    if (a.V && rank == 0 && pos < cnt && j < a.rank) a.V[(r + pos) * a.rank + j] = s;
+    vs[pos * RP + j] = s;
+    if (a.V && part_id == 0 && pos < cnt && j < a.rank) a.V[(r + pos) * a.rank + j] = s;
   }
   cluster_arrive();  // this CTA has read the others' partial sums; waited for at the end
   __syncthreads();
 
-  // ---- fragments of v: position g, hi and lo, in the order of k of load_block
+  // ---- fragments of v: position g, hi and lo, lane's k as in the blocks of B (zeros past the rank)
+  const int kc = RP < 32 ? 4 * t : 8 * t;
   uint32_t hi[KG][4], lo[KG][4];
   float f;
   {
@@ -1399,8 +1407,8 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const LoraFewArgs
     for (int q = 0; q < KG; ++q)
 #pragma unroll
       for (int e = 0; e < (RP < 32 ? 4 : 8); ++e) {
-        const int j = RP < 32 ? 4 * t + e : 32 * q + 8 * t + e;
-        v[q][e] = j < a.rank ? vs[g][j] : 0.0f;
+        const int j = 32 * q + kc + e;
+        v[q][e] = j < a.rank ? vs[g * RP + j] : 0.0f;
         most = fmaxf(most, fabsf(v[q][e]));
       }
     most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
@@ -1412,27 +1420,48 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const LoraFewArgs
 #pragma unroll
       for (int e = 0; e < (RP < 32 ? 2 : 4); ++e) split2<T>(s * v[q][2 * e], s * v[q][2 * e + 1], hi[q][e], lo[q][e]);
   }
-  while (blk < b1) {
+  // column 8 (g / 2) + 2 j + g % 2 of a block is column g of tile j, so that a lane ends with eight consecutive ones
+  const uint32_t brow = static_cast<uint32_t>(8 * (g >> 1) + (g & 1)) * static_cast<uint32_t>(a.rank);
+  T* orow = static_cast<T*>(a.out) + (m >= 0 ? m * a.N : 0);
+  int slot = 0;
+  uint32_t parity = 0u;
+  bool ok = true;
+  for (int blk = b0 + warp; blk < b1 && ok; blk += kFewWarps) {
+    const T* bs = reinterpret_cast<const T*>(slots + slot * L::kSlot);
+    const uint4 ycur = yv[0];
+    yv[0] = yv[1];
+    yv[1] = load_y(blk + kY * kFewWarps);
+    ok = mbar_wait(&bars[slot], parity);
+    if (!ok) break;
     float d[4][4] = {};
 #pragma unroll
     for (int q = 0; q < KG; ++q)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        mma16(d[j], hi[q][0], 0u, hi[q][1], 0u, bw[q][j].x, bw[q][j].y, T());
-        mma16(d[j], lo[q][0], 0u, lo[q][1], 0u, bw[q][j].x, bw[q][j].y, T());
+        const T* row = bs + brow + 2 * j * a.rank;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (!kVec) w = load8(row, 32 * q + kc, a.rank, false);
+        else if (RP >= 32) w = *reinterpret_cast<const uint4*>(row + (32 * q + kc < a.rank ? 32 * q + kc : 0));
+        else *reinterpret_cast<uint2*>(&w) = *reinterpret_cast<const uint2*>(row + (kc < a.rank ? kc : 0));
+        mma16(d[j], hi[q][0], 0u, hi[q][1], 0u, w.x, w.y, T());
+        mma16(d[j], lo[q][0], 0u, lo[q][1], 0u, w.x, w.y, T());
         if (RP >= 32) {
-          mma16(d[j], hi[q][2], 0u, hi[q][3], 0u, bw[q][j].z, bw[q][j].w, T());
-          mma16(d[j], lo[q][2], 0u, lo[q][3], 0u, bw[q][j].z, bw[q][j].w, T());
+          mma16(d[j], hi[q][2], 0u, hi[q][3], 0u, w.z, w.w, T());
+          mma16(d[j], lo[q][2], 0u, lo[q][3], 0u, w.z, w.w, T());
         }
       }
-    Vec<T, 8> y = *reinterpret_cast<const Vec<T, 8>*>(&yv);
-    const int64_t c = 32 * blk + 8 * t;
-    blk += 8;
-    load_block(blk);
+    __syncwarp();  // the block has been read
+    if (lane == 0 && blk + kFewWarps * L::kSlots < b1) request(blk + kFewWarps * L::kSlots, slot);
+    if (++slot == L::kSlots) {
+      slot = 0;
+      parity ^= 1u;
+    }
+    const int c = 32 * blk + 8 * t;
     if (m >= 0 && c < a.N) {
+      Vec<T, 8> y = *reinterpret_cast<const Vec<T, 8>*>(&ycur);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y.v[e] = from_f32<T>(fmaf(f, d[e >> 1][e & 1], to_f32(y.v[e])));
-      *reinterpret_cast<Vec<T, 8>*>(static_cast<T*>(a.out) + m * a.N + c) = y;
+      *reinterpret_cast<Vec<T, 8>*>(orow + c) = y;
     }
   }
   cluster_wait();  // the others may still be reading this CTA's partial sums
@@ -1442,11 +1471,22 @@ __global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const LoraFewArgs
 constexpr int64_t kLoraFewMaxRows = 65535;
 
 cudaError_t launch_lora_few(bool bf16, const LoraFewArgs& a, cudaStream_t s) {
+  const int64_t chunks = lora_max_tiles(a.M, a.L, kFewRows);
+  // Few chunks: several clusters each, which all sum x A^T and share the columns of out, while there are SMs for them and a warp has
+  // more than a block of columns (one row of rank 64, 4096 -> 14336: 12.5 us by one cluster, 7.7 by four).
+  int64_t q = current_device_info().num_sms / (kFewCluster * chunks);
+  const int64_t most = (a.N + 32 * 64 - 1) / (32 * 64);
+  q = q > most ? most : q;
+  const dim3 grid(kFewCluster, static_cast<unsigned>(chunks), static_cast<unsigned>(q < 1 ? 1 : q));
   return with_type16(bf16, [&](auto t) {
     using T = decltype(t);
     return with_rank(a.rank, [&](auto rp) {
-      return launch_pdl(lora_few_kernel<T, decltype(rp)::value>,
-                        dim3(kFewCluster, static_cast<unsigned>(a.M)), dim3(kFewThreads), 0, kFewCluster, s, a);
+      constexpr int RP = decltype(rp)::value;
+      auto* kern = a.rank % (RP < 32 ? 4 : 8) == 0 ? lora_few_kernel<T, RP, true> : lora_few_kernel<T, RP, false>;
+      constexpr int kBytes = LoraFewLayout<RP>::kBytes;
+      const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kBytes);
+      if (e != cudaSuccess) return e;
+      return launch_pdl(kern, grid, dim3(kFewThreads), kBytes, kFewCluster, s, a);
     });
   });
 }
