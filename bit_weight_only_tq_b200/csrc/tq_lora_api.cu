@@ -63,8 +63,19 @@ extern "C" {
 int tq_lora_path(int64_t M, int64_t L, int64_t N, int64_t K, int rank, int dropout, int aligned) {
   if (M < 0 || L < 1 || N < 0 || K < 1 || rank < 1) return TQ_ERR_SHAPE;
   if (M == 0 || N == 0 || !aligned || !lora_fast_shape(N, K)) return TQ_PATH_GENERIC;
-  if (!dropout && M <= 64) return TQ_PATH_DECODE;
-  return TQ_PATH_PREFILL;
+  if (dropout) return TQ_PATH_PREFILL;
+  // DECODE reads an adapter's weights once per eight rows, PREFILL once per 128 and has two launches' worth of start and end.
+  // us of DECODE | PREFILL, rows spread over the adapters at random, fp16:
+  //   rows x adapters         256 x 1      512 x 1      1024 x 1     256 x 64     1024 x 64     2048 x 64
+  //   4096 -> 4096, 16         7 | 14      13 | 15      19 | 15      13 | 30       27 | 35       43 | 42
+  //   4096 -> 14336, 16       11 | 15      20 | 17      33 | 26      23 | 60       44 | 71       71 | 81
+  //   14336 -> 4096, 32       13 | 20      23 | 21      44 | 24      29 | 53       57 | 57       95 | 74
+  //   4096 -> 4096, 64        14 | 17      26 | 19      46 | 19      29 | 41       57 | 44       96 | 50
+  //   4096 -> 14336, 64       16 | 19      31 | 22      60 | 33      41 | 83       79 | 91      135 | 101
+  //   4096 -> 4096, 128       30 | 23      50 | 25      89 | 25      62 | 60      120 | 63      204 | 71
+  const int64_t some = L < M ? (L < 128 ? L : 128) : M;
+  const int64_t most = 32000 + (rank <= 64 ? 800 * (some - 1) : 0);
+  return M <= tq::kLoraFewMaxRows && M * (rank + 32) <= most ? TQ_PATH_DECODE : TQ_PATH_PREFILL;
 }
 
 int tq_lora(const void* x, int dtype, const void* a, const void* b, const float* scaling, const void* base, void* out,

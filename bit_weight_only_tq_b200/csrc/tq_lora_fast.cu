@@ -1262,7 +1262,7 @@ struct LoraFewArgs {
 
 // kVec: rows of B in whole 16-byte vectors (8-byte ones for RP = 16).
 template <typename T, int RP, bool kVec>
-__global__ void __launch_bounds__(kFewThreads, RP <= 64 ? 2 : 1) lora_few_kernel(const LoraFewArgs a) {
+__global__ void __launch_bounds__(kFewThreads, RP <= 16 ? 3 : (RP <= 64 ? 2 : 1)) lora_few_kernel(const LoraFewArgs a) {
   using L = LoraFewLayout<RP>;
   constexpr int RT = RP / 16;                 // tiles of 16 inner columns
   constexpr int KG = RP < 32 ? 1 : RP / 32;   // groups of 32 inner columns (RP = 16: one of 16)

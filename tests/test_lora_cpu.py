@@ -69,6 +69,18 @@ def test_backward_argument_errors():
         assert tq.tq_lora_workspace_size(M, L, r) == 0
 
 
+def test_path_rule():
+    for M, L, N, K, r in ((1, 1, 4096, 4096, 16), (250, 1, 4096, 4096, 64), (61, 32, 14336, 4096, 64), (1024, 64, 4096, 4096, 16),
+                          (190, 4, 512, 512, 128)):
+        assert tq.tq_lora_path(M, L, N, K, r) == tq.PATH_DECODE
+        assert tq.tq_lora_path(M, L, N, K, r, dropout=True) == tq.PATH_PREFILL
+        assert tq.tq_lora_path(M, L, N, K, r, aligned=False) == tq.PATH_GENERIC
+        assert tq.tq_lora_path(M, L, N + 1, K, r) == tq.PATH_GENERIC and tq.tq_lora_path(M, L, N, K + 4, r) == tq.PATH_GENERIC
+    for M, L, r in ((1024, 1, 16), (512, 1, 64), (2048, 64, 64), (256, 64, 128), (100000, 1024, 1)):
+        assert tq.tq_lora_path(M, L, 4096, 4096, r) == tq.PATH_PREFILL
+    assert tq.tq_lora_path(0, 1, 64, 64, 8) == tq.PATH_GENERIC and tq.tq_lora_path(-1, 1, 64, 64, 8) == -2
+
+
 def test_dropout_argument_errors():
     f = tq.lib.tq_dropout
     assert f(P, 3, P, 0.5, P, 4, 8, None) == -4
