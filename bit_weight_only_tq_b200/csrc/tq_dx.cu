@@ -166,7 +166,7 @@ __device__ __forceinline__ void dx_decode_w4(uint32_t w, const uint4& zs0, const
 template <bool kInt4, int TN>
 __global__ void __launch_bounds__(kXThreads, 1)
     dx_tc_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant__ CUtensorMap tmap_w, const DxArgs a,
-                 const int S) {
+                 const int S, const int kt0) {
   using L = DxLayout<kInt4, TN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kOffTmemSlot);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kXM, m0 = static_cast<int64_t>(blockIdx.y) * TN;
+  const int kt = kt0 + static_cast<int>(blockIdx.x);  // tile of columns
+  const int64_t k0 = static_cast<int64_t>(kt) * kXM, m0 = static_cast<int64_t>(blockIdx.y) * TN;
   const int ns_all = static_cast<int>((a.N + kXN - 1) / kXN);
   const int rank = static_cast<int>(blockIdx.z);  // slice of n = rank in the cluster
   const int s0 = static_cast<int>((static_cast<int64_t>(rank) * ns_all) / S);
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
           if (!ok) break;
         }
         mbar_arrive_expect_tx(&fullP[s], L::kTileP);
-        tma_load_2d(sm + L::kOffP + s * L::kTileP, &tmap_w, &fullP[s], static_cast<int32_t>(blockIdx.x) * L::kRowBytes,
+        tma_load_2d(sm + L::kOffP + s * L::kTileP, &tmap_w, &fullP[s], kt * L::kRowBytes,
                     (s0 + pt * kXSPP) * kXN);
       }
     }
@@ -528,17 +529,29 @@ static cudaError_t launch_dx_tc(const DxArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const DeviceInfo di = current_device_info();
   const int64_t kt = (a.K + kXM - 1) / kXM, mt = (a.M + TN - 1) / TN, ns = (a.N + kXN - 1) / kXN;
-  // n split over a cluster while the tiles leave SMs idle and all clusters are resident at once, as in the products
+  auto capacity = [&](int cs) { return dx_cluster_capacity<kInt4, TN>(di.device, cs); };
+  auto run = [&](int64_t first, int64_t last, int S) {
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = dx_config<kInt4, TN>(
+        dim3(static_cast<unsigned>(last - first), static_cast<unsigned>(mt), static_cast<unsigned>(S)), s, attr);
+    return cudaLaunchKernelEx(&cfg, kern, td, tw, a, S, static_cast<int>(first));
+  };
+  // n split over a cluster while the tiles leave SMs idle and all clusters are resident at once, and a nearly empty last wave
+  // split off into a launch of its own, as in the products
   int S = 1;
   while (S < 8 && kt * mt * S * 2 <= di.num_sms && S * 2 <= ns) {
-    const int cap = dx_cluster_capacity<kInt4, TN>(di.device, S * 2);
+    const int cap = capacity(S * 2);
     if (cap > 0 && kt * mt > cap) break;
     S *= 2;
   }
-  cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = dx_config<kInt4, TN>(
-      dim3(static_cast<unsigned>(kt), static_cast<unsigned>(mt), static_cast<unsigned>(S)), s, attr);
-  return cudaLaunchKernelEx(&cfg, kern, td, tw, a, S);
+  if (S == 1) {
+    const PrefillTailPlan tp = prefill_tail_plan(kt, mt, static_cast<int>(ns), di.num_sms, capacity);
+    if (tp.rows_main > 0) {
+      e = run(0, tp.rows_main, tp.Sm);
+      return e != cudaSuccess ? e : run(tp.rows_main, kt, tp.St);
+    }
+  }
+  return run(0, kt, S);
 }
 
 bool dx_supported(int64_t M, int64_t N, int64_t K) {

@@ -86,7 +86,7 @@ def tq_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, base, offsets: to
     px = _arg(x, "x", d, (M, K), dev)
     if out is None:
         out = _empty(x, (M, N), d, stream)
-    if v is None and lib.tq_lora_path(M, L, N, K, r, 1 if p else 0, 1) != PATH_DECODE or v is None and path != PATH_AUTO:
+    if v is None and (path != PATH_AUTO or p or lib.tq_lora_path(M, L, N, K, r, 0, 1) != PATH_DECODE):
         v = _empty(x, (M, r), torch.float32, stream)
     _check(lib.tq_lora(px, dt, _arg(a, "a", d, (L, r, K), dev), _arg(b, "b", d, (L, N, r), dev),
                        _opt(scaling, "scaling", torch.float32, (L,), dev), _opt(base, "base", d, (M, N), dev),

@@ -119,7 +119,8 @@ def _dx_check(dy, w64, out, rounded):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 8, 128), (7, 72, 128), (61, 1024, 256), (64, 128, 384), (129, 200, 640), (130, 520, 1152),
-                                   (257, 1000, 512), (300, 64, 2304), (5, 4096, 128), (520, 264, 128)])
+                                   (257, 1000, 512), (300, 64, 2304), (5, 4096, 128), (520, 264, 128),
+                                   (2816, 1024, 1792)])  # 154 tiles: the last six in a launch of their own
 @pytest.mark.parametrize("fmt", ["ternary", "w4", "w4z"])
 def test_gradient_for_x(M, N, K, fmt):
     need_cuda()
