@@ -47,6 +47,7 @@ struct LoraArgs {
   const float* V2;
   float* most;
   float* most2;
+  bool behind;  // tensor-core wgrad: the preceding kernels on the stream are this call's own
   // Tensor-core wgrad: V as hi and lo [M, 2 padded rank], scaled by 1 / inv[l]
   const void* Q;
   const float* inv;

@@ -169,6 +169,7 @@ int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, co
     g.drop = drop;
     g.Q = w.Q[1];
     g.inv = w.inv[1];
+    g.behind = M > 0;
     e = tq::launch_lora_wgrad(bf16, path, g, s);
   }
   if (e == cudaSuccess && db && N > 0) {
@@ -176,6 +177,7 @@ int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, co
     g.O = db;
     g.Q = w.Q[0];
     g.inv = w.inv[0];
+    g.behind = M > 0;
     e = tq::launch_lora_wgrad(bf16, path, g, s);
   }
   return to_status(e);

@@ -267,7 +267,9 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.z);
-  pdl_wait_prior_grids();
+  // wgrad follows kernels of the same call, which let it start only after the work before the call had finished: all but Q and inv may
+  // be read before the wait.
+  if (!kW || !a.behind) pdl_wait_prior_grids();
 
   // the work of this cluster: positions [pos0, pos0 + cnt) of adapter l; columns from c0 (wgrad); stages [s0, s0 + ns)
   int l, ns_all;
@@ -292,6 +294,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
           const int j = a.wc == 1 ? i >> 7 : i % a.rank;
           if (c < a.C) out[c * a.wc + j * a.wj] = from_f32<T>(0.0f);
         }
+      if (a.behind) pdl_wait_prior_grids();
       return;
     }
     ns_all = static_cast<int>((cnt + 63) / 64);
@@ -320,7 +323,6 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
   const PhiloxKey key = kDrop ? philox_key(a.drop) : PhiloxKey{0u, 0u, 0u, 0u};
   const uint16_t* P = static_cast<const uint16_t*>(a.P);
   float f = lora_factor(a, l);
-  if (kW) f *= a.inv[l];
 
   bool ok = true;
   if (warp < kLtcWarps) {
@@ -438,6 +440,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
       ++hd;
       if (++hs == L::kRing) hs = 0;
     };
+    if (kW && a.behind) pdl_wait_prior_grids();
     uint32_t st = ring0, parity = 1u;  // the slot of the stage requested, and the parity of its last release
     uint64_t* release = empty;
     for (int i = 0; i < ns; ++i) {
@@ -513,6 +516,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
 
   // ------------------------------------------------------------------ sums out of tensor memory
   // Warp w < 8 has lanes 32 (w % 4) .. + 31 (position or column r of the tile) and half w / 4 of the inner columns.
+  if (kW) f *= a.inv[l];  // (the loaders have waited for the kernel that wrote it)
   const int r = tid & 127;
   const bool epi = warp < kLtcEpiWarps;
   if (!kW && rowbuf[r] < 0) f = 0.0f;  // a position without a row
@@ -908,10 +912,14 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
   float* rowf = reinterpret_cast<float*>(sm + L::kOffF);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait_prior_grids();
+  // The preceding kernel is this call's reduction (or one behind it), which let this one start only after the work before the call
+  // had finished: everything but V may be read at once.
   const int64_t nblk = (a.C + kXpCols - 1) / kXpCols, total = lora_tiles(a.offsets, a.L, a.M) * nblk;
   const int64_t run0 = total * blockIdx.x / gridDim.x, run1 = total * (blockIdx.x + 1) / gridDim.x;
-  if (run0 == run1) return;
+  if (run0 == run1) {
+    pdl_wait_prior_grids();  // no CTA ends before the kernels ahead of it: the next one takes this grid's end for theirs
+    return;
+  }
   const T* base = static_cast<const T*>(a.base);
   T* out = static_cast<T*>(a.O);
 
@@ -942,6 +950,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     const PhiloxKey key = kDrop ? philox_key(a.drop) : PhiloxKey{0u, 0u, 0u, 0u};
     int s = 0, seg = 0;
     uint32_t parity = 0u;
+    bool waited = false;
     for (int64_t run = run0; run < run1 && ok;) {
     const int64_t tn = run / nblk, c_begin = (run - tn * nblk) * kXpCols;
     const int nb = static_cast<int>(run1 - run < nblk * (tn + 1) - run ? run1 - run : nblk * (tn + 1) - run);
@@ -991,6 +1000,8 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
       const float* src = a.V + (tile.pos + row) * a.rank;
       float most = 0.0f;
       float v[kE];
+      if (!waited) pdl_wait_prior_grids();
+      waited = true;
       if ((a.rank & 3) == 0) {
 #pragma unroll
         for (int e = 0; e < kE; e += 4) {
@@ -1075,6 +1086,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     }
     ++seg;
     }
+    if (!waited) pdl_wait_prior_grids();
   } else {
     // ------------------------------------------------------------------ loaders of W; the first warp also issues the MMAs
     const int w = tid - 32 * kXpEpi;  // 0 .. 127
