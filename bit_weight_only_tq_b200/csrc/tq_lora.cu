@@ -42,6 +42,9 @@ struct LoraArgs {
   int64_t wc, wj, ws;
   int L, rank;
   bool use_scaling;         // f includes scaling[l]
+  // tensor-core kernels: rows of P, of W and of base and O in whole, aligned 16-byte vectors (element by element otherwise); wgrad: O
+  // aligned to them
+  bool pvec, wvec, yvec;
   // Tensor-core reduce: the largest magnitude that each CTA of a tile wrote to V (most) and found in V2 (most2), kLoraMostPer slots
   // per tile; null: not wanted
   const float* V2;

@@ -31,8 +31,8 @@ int check_lora(int dtype, int64_t M, int64_t L, int64_t N, int64_t K, int rank, 
   return TQ_OK;
 }
 
-// 16-byte vectors along both widths.
-bool lora_fast_shape(int64_t N, int64_t K) { return N % 8 == 0 && K % 8 == 0; }
+// The kernel for few rows takes 16-byte vectors along both widths.
+bool lora_few_shape(int64_t M, int64_t N, int64_t K) { return N % 8 == 0 && K % 8 == 0 && M <= tq::kLoraFewMaxRows; }
 
 // The sums of one call, W as A [rank, C] or as B [C, rank].
 tq::LoraArgs lora_sum(const void* P, const void* W, bool w_is_a, int64_t C, int rank, int64_t M, int64_t L, float* V,
@@ -62,8 +62,8 @@ extern "C" {
 
 int tq_lora_path(int64_t M, int64_t L, int64_t N, int64_t K, int rank, int dropout, int aligned) {
   if (M < 0 || L < 1 || N < 0 || K < 1 || rank < 1) return TQ_ERR_SHAPE;
-  if (M == 0 || N == 0 || !aligned || !lora_fast_shape(N, K)) return TQ_PATH_GENERIC;
-  if (dropout) return TQ_PATH_PREFILL;
+  if (M == 0 || N == 0) return TQ_PATH_GENERIC;
+  if (dropout || !aligned || !lora_few_shape(M, N, K)) return TQ_PATH_PREFILL;
   // DECODE reads an adapter's weights once per eight rows, PREFILL once per 128 and has two launches' worth of start and end.
   // us of DECODE | PREFILL, rows spread over the adapters at random, fp16:
   //   rows x adapters         256 x 1      512 x 1      1024 x 1     256 x 64     1024 x 64     2048 x 64
@@ -75,7 +75,7 @@ int tq_lora_path(int64_t M, int64_t L, int64_t N, int64_t K, int rank, int dropo
   //   4096 -> 4096, 128       30 | 23      50 | 25      89 | 25      62 | 60      120 | 63      204 | 71
   const int64_t some = L < M ? (L < 128 ? L : 128) : M;
   const int64_t most = 32000 + (rank <= 64 ? 800 * (some - 1) : 0);
-  return M <= tq::kLoraFewMaxRows && M * (rank + 32) <= most ? TQ_PATH_DECODE : TQ_PATH_PREFILL;
+  return M * (rank + 32) <= most ? TQ_PATH_DECODE : TQ_PATH_PREFILL;
 }
 
 int tq_lora(const void* x, int dtype, const void* a, const void* b, const float* scaling, const void* base, void* out,
@@ -86,13 +86,16 @@ int tq_lora(const void* x, int dtype, const void* a, const void* b, const float*
   if (st != TQ_OK || M == 0 || N == 0) return st;
   if (!x || !a || !b || !out || !offsets || (drop.thr && !rng)) return TQ_ERR_NULL;
   const bool al = aligned16(x) && aligned16(a) && aligned16(b) && aligned16(base) && aligned16(out) && aligned16(v);
+  const bool few = !drop.thr && lora_few_shape(M, N, K);
   if (path == TQ_PATH_AUTO) {
     path = tq_lora_path(M, L, N, K, rank, drop.thr != 0, al ? 1 : 0);
-    if (path == TQ_PATH_PREFILL && !v && !drop.thr && M <= tq::kLoraFewMaxRows) path = TQ_PATH_DECODE;
-  } else if (path != TQ_PATH_GENERIC) {
-    if (!lora_fast_shape(N, K)) return TQ_ERR_PATH;
-    if (path == TQ_PATH_DECODE && (drop.thr || M > tq::kLoraFewMaxRows)) return TQ_ERR_PATH;
+    if (path == TQ_PATH_PREFILL && !v && few && al) path = TQ_PATH_DECODE;
+    if (path == TQ_PATH_PREFILL && !aligned16(v)) path = TQ_PATH_GENERIC;
+  } else if (path == TQ_PATH_DECODE) {
+    if (!few) return TQ_ERR_PATH;
     if (!al) return TQ_ERR_ALIGN;
+  } else if (path == TQ_PATH_PREFILL && !aligned16(v)) {
+    return TQ_ERR_ALIGN;
   }
   const bool bf16 = dtype == TQ_BF16;
   if (path == TQ_PATH_DECODE)
@@ -129,14 +132,8 @@ int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, co
   if (M > 0 && (!workspace || (N > 0 && (!dy || !b)) || !v || (da && !x) || (dx && !a))) return TQ_ERR_NULL;
   if (!aligned16(workspace)) return TQ_ERR_ALIGN;
   if (M > 0 && workspace_bytes < tq_lora_workspace_size(M, L, rank)) return TQ_ERR_SHAPE;
-  const bool al = aligned16(x) && aligned16(a) && aligned16(b) && aligned16(dy) && aligned16(v) &&
-                  aligned16(base_dx) && aligned16(dx) && aligned16(da) && aligned16(db);
-  if (path == TQ_PATH_AUTO) {
-    path = al && lora_fast_shape(N, K) ? TQ_PATH_PREFILL : TQ_PATH_GENERIC;
-  } else if (path == TQ_PATH_PREFILL) {
-    if (!lora_fast_shape(N, K)) return TQ_ERR_PATH;
-    if (!al) return TQ_ERR_ALIGN;
-  }
+  if (path == TQ_PATH_AUTO) path = aligned16(v) ? TQ_PATH_PREFILL : TQ_PATH_GENERIC;
+  if (path == TQ_PATH_PREFILL && !aligned16(v)) return TQ_ERR_ALIGN;
   const bool bf16 = dtype == TQ_BF16;
   cudaStream_t s = as_stream(stream);
   cudaError_t e = cudaSuccess;

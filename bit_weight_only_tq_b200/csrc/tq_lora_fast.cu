@@ -1,5 +1,5 @@
-// tq_lora_fast.cu -- low-rank adapters (include/tq_lora.h) with 16-byte vectors along both widths: the sums over many
-// rows (reduce and wgrad on tcgen05, expand on mma.sync) and the single launch for few rows.
+// tq_lora_fast.cu -- low-rank adapters (include/tq_lora.h): the sums over many rows (reduce, wgrad and expand on tcgen05, with
+// 16-byte accesses where rows are made of whole vectors and element by element otherwise) and the single launch for few rows.
 //
 // Work is cut by adapter: a tile is up to 128 sorted positions of one adapter, found on the device from
 // the offsets, so that one captured graph serves any plan.
@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
   pdl_allow_dependents();
   const uint32_t tmem = *tmem_slot;
   const PhiloxKey key = kDrop ? philox_key(a.drop) : PhiloxKey{0u, 0u, 0u, 0u};
+  const int64_t groups = (a.C + 7) >> 3;
   const uint16_t* P = static_cast<const uint16_t*>(a.P);
   float f = lora_factor(a, l);
 
@@ -360,7 +361,6 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
     const uint16_t* wsrc[L::kPerW];
     uint32_t wdst[L::kPerW], wsize[L::kPerW];
     int wrow[L::kPerW];  // summation index within the stage, for the zeros past its end
-    const bool bvec = (a.rank & 7) == 0;
 #pragma unroll
     for (int k = 0; k < L::kPerW; ++k) {
       const int q = tid + kLtcLoaders * k;
@@ -396,14 +396,24 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
 #pragma unroll
         for (int k = 0; k < L::kPer; ++k) {
           const int mk = rows[L::kStep * k];
-          cp_async_16s(st + pdst + k * L::kStep * 128, pcol + static_cast<int64_t>(mk < 0 ? 0 : mk) * a.C,
-                       mk < 0 ? 0u : psize);
+          const uint32_t dst = st + pdst + k * L::kStep * 128;
+          if (a.pvec)
+            cp_async_16s(dst, pcol + static_cast<int64_t>(mk < 0 ? 0 : mk) * a.C, mk < 0 ? 0u : psize);
+          else
+            *reinterpret_cast<uint4*>(sm + (dst - ring0)) =
+                mk < 0 ? make_uint4(0u, 0u, 0u, 0u) : load8(P + static_cast<int64_t>(mk) * a.C, c, a.C, false);
         }
       } else {
         const uint32_t size = !kTail || 8 * pch < left ? 16u : 0u;
 #pragma unroll
         for (int k = 0; k < L::kPer; ++k) {
-          if (m[k] >= 0) cp_async_16s(st + pdst + k * L::kStep * 128, size ? src[k] : P, size);
+          const uint32_t dst = st + pdst + k * L::kStep * 128;
+          if (a.pvec) {
+            if (m[k] >= 0) cp_async_16s(dst, size ? src[k] : P, size);
+          } else if (m[k] >= 0) {
+            const int64_t ci = c + static_cast<int64_t>(i) * 64 * L::kSub;
+            *reinterpret_cast<uint4*>(sm + (dst - ring0)) = load8(src[k] - ci, ci, a.C, false);
+          }
           src[k] += 64 * L::kSub;
         }
       }
@@ -411,12 +421,13 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
       for (int k = 0; k < L::kPerW; ++k) {
         if (L::kChunksW % kLtcLoaders != 0 && tid + kLtcLoaders * k >= L::kChunksW) continue;
         const uint32_t size = !kTail || wrow[k] < left ? wsize[k] : 0u;
-        if (kMode != kReduceB || bvec) {
+        if (kW || a.wvec) {
           cp_async_16s(st + wdst[k], size ? wsrc[k] : P, size);
-        } else {  // rows of B that are not whole 16-byte vectors
-          const int ch = (tid + kLtcLoaders * k) % (RP / 8);
+        } else {  // from the row's start: wc0 columns (or inner columns) before this chunk
+          const int64_t wc0 = kMode == kReduceA ? (static_cast<int64_t>(s0) + i) * 64 * L::kSub + wrow[k]
+                                                : 8 * ((tid + kLtcLoaders * k) % (RP / 8));
           *reinterpret_cast<uint4*>(sm + (st - ring0) + wdst[k]) =
-              size ? load8(wsrc[k] - 8 * ch, 8 * ch, a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
+              size ? load8(wsrc[k] - wc0, wc0, kMode == kReduceA ? a.C : a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
         }
         wsrc[k] += wadvance;
       }
@@ -432,7 +443,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
           for (int k = 0; k < L::kPer; ++k) {
             const int64_t mk = kW ? rowbuf[(hd % (2 * kRowStages)) * 64 + prow + L::kStep * k] : m[k];
             uint4* x = reinterpret_cast<uint4*>(st + k * L::kStep * 128);
-            if (mk >= 0) *x = drop_apply16(*x, (mk * a.C + hc) >> 3, key, a.drop.thr);
+            if (mk >= 0) *x = drop_apply16(*x, mk * groups + (hc >> 3), key, a.drop.thr);
           }
       }
       __syncwarp();
@@ -569,7 +580,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
                 most2 = fmaxf(fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(p.z), fabsf(p.w))), most2);
               }
             }
-        } else if (kW && a.wj == 1 && (a.rank & 7) == 0) {  // dB: eight consecutive elements of a row
+        } else if (kW && a.wj == 1 && (a.rank & 7) == 0 && a.yvec) {  // dB: eight consecutive elements of a row
           if (c0 + r < a.C && j0 < a.rank) {
             Vec<T, 8> o;
 #pragma unroll
@@ -948,6 +959,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     // ------------------------------------------------------------------ epilogue
     const int g = lane >> 2, t = lane & 3, r0 = (warp & 3) * 32 + g;
     const PhiloxKey key = kDrop ? philox_key(a.drop) : PhiloxKey{0u, 0u, 0u, 0u};
+    const int64_t groups = (a.C + 7) >> 3;
     int s = 0, seg = 0;
     uint32_t parity = 0u;
     bool waited = false;
@@ -964,6 +976,11 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
       for (int i = warp; i < tile.cnt; i += kXpEpi) {
         const int64_t q = tile.pos + i, m = lora_row(a, q < head ? q : q - head + at);
         if (m < 0) continue;
+        if (!a.yvec) {
+          for (int64_t c = c_begin + lane; c < c_end; c += 32)
+            out[m * a.C + c] = base ? base[m * a.C + c] : from_f32<T>(0.0f);
+          continue;
+        }
         uint4* dst = reinterpret_cast<uint4*>(out + m * a.C + c_begin);
         const uint4* src = reinterpret_cast<const uint4*>(base + m * a.C + c_begin);
         for (int j = lane; j < vecs; j += 32 * kXpCopy) {  // all loads of a round before its stores
@@ -987,7 +1004,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     auto load_base = [&](uint4 (&to)[4], int64_t at) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        to[i] = base && m[i] >= 0 && at < c_end ? *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(m[i]) * a.C + at)
+        to[i] = base && m[i] >= 0 && at < c_end ? load8(base + static_cast<int64_t>(m[i]) * a.C, at, a.C, a.yvec)
                                                 : make_uint4(0u, 0u, 0u, 0u);
     };
     load_base(y[0], c);
@@ -1060,13 +1077,17 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
           if (m[2 * h + i] < 0) continue;
           const int64_t at_row = static_cast<int64_t>(m[2 * h + i]) * a.C + c;
           Vec<T, 8> o = *reinterpret_cast<const Vec<T, 8>*>(&yb[2 * h + i]);
-          const uint4 bits = kDrop ? philox(at_row >> 3, key) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 bits = kDrop ? philox(m[2 * h + i] * groups + (c >> 3), key) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float x = __uint_as_float(acc[4 * (e >> 1) + 2 * i + (e & 1)]), z = to_f32(o.v[e]);
             o.v[e] = from_f32<T>(kDrop && !drop_keeps(bits, e, a.drop.thr) ? z : fmaf(f[2 * h + i], x, z));
           }
-          *reinterpret_cast<Vec<T, 8>*>(out + at_row) = o;
+          if (a.yvec) {
+            *reinterpret_cast<Vec<T, 8>*>(out + at_row) = o;
+          } else {
+            for (int e = 0; e < 8 && c + e < a.C; ++e) out[at_row + e] = o.v[e];
+          }
         }
       }
       if (++s == kXpRing) {
@@ -1090,7 +1111,6 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
   } else {
     // ------------------------------------------------------------------ loaders of W; the first warp also issues the MMAs
     const int w = tid - 32 * kXpEpi;  // 0 .. 127
-    const bool bvec = (a.rank & 7) == 0;
     constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
     constexpr uint32_t kIdesc = idesc_f16_f32(128, kXpCols) | kType | (kWA ? 1u << 16 : 0u);
     const uint32_t base_v = smem_u32(sm);
@@ -1112,8 +1132,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
       const int64_t at = c_begin + static_cast<int64_t>(b) * kXpCols + 8 * ach;
 #pragma unroll
       for (int i = 0; i < kPerA; ++i)
-        pre[i] = at < a.C && aj + 8 * i < a.rank ? *reinterpret_cast<const uint4*>(W + (aj + 8 * i) * a.C + at)
-                                                 : make_uint4(0u, 0u, 0u, 0u);
+        pre[i] = at < a.C && aj + 8 * i < a.rank ? load8(W + (aj + 8 * i) * a.C, at, a.C, a.wvec) : make_uint4(0u, 0u, 0u, 0u);
     };
     if (kWA) load_a(0);
     for (int b = 0; b < nb + L::kLag && ok; ++b) {
@@ -1145,7 +1164,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
           for (int ch = 0; ch < RP / 8; ++ch) {
             uint8_t* dst = st + (ch >> 3) * L::kPlaneW + pos * 128 + (((ch & 7) ^ (pos & 7)) << 4);
             const bool in = there && 8 * ch < a.rank;
-            if (bvec)
+            if (a.wvec)
               cp_async_16(dst, in ? src + 8 * ch : W, in ? 16u : 0u);
             else
               *reinterpret_cast<uint4*>(dst) = in ? load8(src, 8 * ch, a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
@@ -1505,14 +1524,24 @@ cudaError_t launch_lora_few(bool bf16, const LoraFewArgs& a, cudaStream_t s) {
 
 constexpr int kLoraGeneric = 3;  // TQ_PATH_GENERIC
 
+static bool lora_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+static LoraArgs lora_vectors(LoraArgs a) {
+  const bool rows = a.C % 8 == 0;
+  a.pvec = rows && lora_aligned(a.P);
+  a.wvec = (a.wc == 1 ? rows : a.rank % 8 == 0) && lora_aligned(a.W);
+  a.yvec = lora_aligned(a.O) && (a.P || (rows && lora_aligned(a.base)));  // (wgrad has P, and only O)
+  return a;
+}
+
 cudaError_t launch_lora_reduce(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {
-  return path == kLoraGeneric ? lora_generic_reduce(bf16, a, s) : lora_fast_reduce(bf16, a, s);
+  return path == kLoraGeneric ? lora_generic_reduce(bf16, a, s) : lora_fast_reduce(bf16, lora_vectors(a), s);
 }
 cudaError_t launch_lora_expand(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {
-  return path == kLoraGeneric ? lora_generic_expand(bf16, a, s) : lora_fast_expand(bf16, a, s);
+  return path == kLoraGeneric ? lora_generic_expand(bf16, a, s) : lora_fast_expand(bf16, lora_vectors(a), s);
 }
 cudaError_t launch_lora_wgrad(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {
-  return path == kLoraGeneric ? lora_generic_wgrad(bf16, a, s) : lora_fast_wgrad(bf16, a, s);
+  return path == kLoraGeneric ? lora_generic_wgrad(bf16, a, s) : lora_fast_wgrad(bf16, lora_vectors(a), s);
 }
 
 }  // namespace tq

@@ -86,12 +86,14 @@ def tq_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, base, offsets: to
     px = _arg(x, "x", d, (M, K), dev)
     if out is None:
         out = _empty(x, (M, N), d, stream)
-    if v is None and (path != PATH_AUTO or p or lib.tq_lora_path(M, L, N, K, r, 0, 1) != PATH_DECODE):
-        v = _empty(x, (M, r), torch.float32, stream)
-    _check(lib.tq_lora(px, dt, _arg(a, "a", d, (L, r, K), dev), _arg(b, "b", d, (L, N, r), dev),
-                       _opt(scaling, "scaling", torch.float32, (L,), dev), _opt(base, "base", d, (M, N), dev),
-                       _arg(out, "out", d, (M, N), dev), _opt(v, "v", torch.float32, (M, r), dev),
-                       _arg(offsets, "offsets", torch.int32, (L + 1,), dev),
+    pa, pb = _arg(a, "a", d, (L, r, K), dev), _arg(b, "b", d, (L, N, r), dev)
+    pbase, po = _opt(base, "base", d, (M, N), dev), _arg(out, "out", d, (M, N), dev)
+    if v is None:
+        aligned = 0 if (px | pa | pb | (pbase or 0) | po) & 15 else 1
+        if path != PATH_AUTO or p or lib.tq_lora_path(M, L, N, K, r, 0, aligned) != PATH_DECODE:
+            v = _empty(x, (M, r), torch.float32, stream)
+    _check(lib.tq_lora(px, dt, pa, pb, _opt(scaling, "scaling", torch.float32, (L,), dev), pbase, po,
+                       _opt(v, "v", torch.float32, (M, r), dev), _arg(offsets, "offsets", torch.int32, (L + 1,), dev),
                        _opt(order, "order", torch.int32, (M,), dev), p, _rng(p, rng, dev), M, L, N, K, r, int(path),
                        _raw(stream, dev)), "tq_lora")
     return out

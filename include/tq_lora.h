@@ -65,14 +65,15 @@ extern "C" {
  *            (TQ_ERR_NULL); AUTO without it takes DECODE where it can.
  *            Calls (or captured graphs) that may run at once need one each.
  *   path     TQ_PATH_AUTO, or one path (tests): DECODE takes few rows (one launch, up to 8 rows of an
- *            adapter per pass over its weights), PREFILL many (tensor cores), GENERIC any shape and
- *            alignment.  DECODE and PREFILL need K % 8 == 0 and N % 8 == 0 (TQ_ERR_PATH) and 16-byte aligned x, a,
- *            b, base, out and v (TQ_ERR_ALIGN).  DECODE needs p = 0 and M <= 65535 (TQ_ERR_PATH).
+ *            adapter per pass over its weights), PREFILL many (tensor cores), GENERIC is the plain form.
+ *            DECODE needs p = 0, M <= 65535, K % 8 == 0 and N % 8 == 0 (TQ_ERR_PATH) and 16-byte aligned x, a, b, base,
+ *            out and v (TQ_ERR_ALIGN).  PREFILL needs a 16-byte aligned v (TQ_ERR_ALIGN); widths that are multiples of 8
+ *            and aligned tensors are read in whole vectors, others element by element.
  *            Every path is right for any numbers of rows per adapter.
  * 1 <= L <= 1024, 1 <= rank <= 128, 0 < K, N <= 2^24 (N = 0: nothing), 0 <= M < 2^31.
  * M == 0 or N == 0: nothing is launched.
  *
- * tq_lora_path -- the rule TQ_PATH_AUTO applies (host arithmetic only; aligned16: all of the pointers
+ * tq_lora_path -- the rule TQ_PATH_AUTO applies with a v (host arithmetic only; aligned16: all of the pointers
  * that are not NULL are 16-byte aligned).  Returns a tq_path or a negative tq_status.
  * ------------------------------------------------------------------------------------------ */
 TQ_API int tq_lora(const void* x, int dtype, const void* a, const void* b, const float* scaling, const void* base,
@@ -93,7 +94,7 @@ TQ_API int tq_lora_path(int64_t M, int64_t L, int64_t N, int64_t K, int rank, in
  *            from call to call.  Calls (or captured graphs) that may run at once need one each.
  *   base_dx  [M, K], or NULL for zeros; may be `dx` (the projection's own gradient for x, to which this adds)
  *   dx, da, db  each may be NULL (not wanted).  None may overlap what the call reads (dx may be base_dx).
- *   path     AUTO, PREFILL or GENERIC, with the conditions of tq_lora on all of the tensors.
+ *   path     AUTO, PREFILL (16-byte aligned v: TQ_ERR_ALIGN) or GENERIC.
  * The gradient for base is dy itself; `scaling` has none.  Sums are taken in a fixed order.
  * ------------------------------------------------------------------------------------------ */
 TQ_API int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, const void* b,

@@ -40,16 +40,21 @@ def factor(p):
 
 def kept(M, K, p, seed, offset):
     """The elements of [M, K] that dropout keeps."""
+    return kept_rows(M, K, p, seed, offset, 0)
+
+
+def kept_rows(M, K, p, seed, offset, first):
+    """Rows first .. M - 1 of the same."""
     if threshold(p) == 0:
-        return np.ones((M, K), dtype=bool)
+        return np.ones((M - first, K), dtype=bool)
     low = 0xFFFFFFFF
     seed, offset = seed & (2 ** 64 - 1), offset & (2 ** 64 - 1)
     G = -(-K // 8)
-    i = np.arange(M * G, dtype=np.uint64)
+    i = np.arange(first * G, M * G, dtype=np.uint64)
     w = philox([i & np.uint64(low), i >> np.uint64(32), np.full_like(i, offset & low), np.full_like(i, offset >> 32)],
                [seed & low, seed >> 32])
     e = np.stack([w[j // 2] >> np.uint64(16) if j % 2 else w[j // 2] & np.uint64(0xFFFF) for j in range(8)], -1)
-    return (e >= threshold(p)).reshape(M, G * 8)[:, :K]
+    return (e >= threshold(p)).reshape(M - first, G * 8)[:, :K]
 
 
 def segments(offsets, order, M):

@@ -69,7 +69,8 @@ def _check_v(v, want, tol, segs):
 SHAPES = [(1, 1, 8, 8, 1), (1, 3, 64, 24, 16), (7, 2, 136, 8, 8), (8, 8, 512, 72, 16), (9, 4, 1000, 200, 32),
           (33, 5, 72, 264, 64), (61, 32, 256, 1032, 24), (130, 1, 264, 136, 128), (129, 3, 2048, 40, 4), (300, 7, 520, 520, 40),
           (1, 2, 8200, 16, 128), (257, 2, 128, 4096, 100)]
-ODD = [(5, 2, 7, 3, 5), (19, 3, 101, 67, 12), (70, 2, 33, 129, 33), (3, 1, 1, 1, 1)]
+ODD = [(5, 2, 7, 3, 5), (19, 3, 101, 67, 12), (70, 2, 33, 129, 33), (3, 1, 1, 1, 1), (300, 4, 1001, 264, 16), (260, 2, 128, 515, 64),
+       (140, 3, 650, 1026, 128)]
 
 
 def _paths(M, p=0.0):
@@ -103,13 +104,15 @@ def test_forward_odd_sizes(shape, dtype):
     M, L, K, N, r = shape
     x, a, b, base, s, offsets, order = _case(M, L, K, N, r, dtype, M)
     want, tol, v64, tv, segs = _forward64(x, a, b, base, s, offsets, order)
-    v = torch.empty(M, r, device="cuda")
-    O.check(tq.tq_lora(x, a, b, base, offsets, order=order, scaling=s, v=v), want, tol)
-    _check_v(v, v64, tv, segs)
-    for path in (TC, FEW):
-        if K % 8 or N % 8:
-            with pytest.raises(tq.TQError):
-                tq.tq_lora(x, a, b, base, offsets, order=order, scaling=s, path=path)
+    for path in (tq.PATH_AUTO, ANY, TC):
+        v = torch.empty(M, r, device="cuda")
+        O.check(tq.tq_lora(x, a, b, base, offsets, order=order, scaling=s, v=v, path=path), want, tol)
+        _check_v(v, v64, tv, segs)
+        again = base.clone()
+        assert torch.equal(tq.tq_lora(x, a, b, again, offsets, order=order, scaling=s, out=again, path=path),
+                           tq.tq_lora(x, a, b, base, offsets, order=order, scaling=s, path=path))
+    with pytest.raises(tq.TQError):
+        tq.tq_lora(x, a, b, base, offsets, order=order, scaling=s, path=FEW)
 
 
 @pytest.mark.parametrize("path", [ANY, TC, FEW])
@@ -275,12 +278,13 @@ def test_backward_odd_sizes(shape):
     x, a, b, base, s, offsets, order = _case(M, L, K, N, r, H, M)
     dy = (0.1 * torch.randn(M, N, generator=_gen(9), device="cuda")).half()
     rng = torch.tensor([11, 12], dtype=torch.int64, device="cuda")
-    v = torch.zeros(M, r, device="cuda")
-    tq.tq_lora(x, a, b, None, offsets, order=order, scaling=s, p=0.25, rng=rng, v=v)
-    want = _backward64(dy, x, a, b, v, None, s, offsets, order, 0.25, 11, 12)
-    got = tq.tq_lora_backward(dy, x, a, b, v, None, offsets, order=order, scaling=s, p=0.25, rng=rng)
-    for g, (w, t), name in zip(got, want, ("dx", "da", "db")):
-        O.check(g, w, t, name)
+    for path in (ANY, TC):
+        v = torch.zeros(M, r, device="cuda")
+        tq.tq_lora(x, a, b, None, offsets, order=order, scaling=s, p=0.25, rng=rng, v=v, path=path)
+        want = _backward64(dy, x, a, b, v, None, s, offsets, order, 0.25, 11, 12)
+        got = tq.tq_lora_backward(dy, x, a, b, v, None, offsets, order=order, scaling=s, p=0.25, rng=rng, path=path)
+        for g, (w, t), name in zip(got, want, ("dx", "da", "db")):
+            O.check(g, w, t, f"{name}, path {path}")
 
 
 @pytest.mark.parametrize("path", [ANY, TC])
@@ -314,6 +318,155 @@ def test_small_and_large_gradients(path):
         for g, (w, t), name in zip(got, want, ("dx", "da", "db")):
             fits = np.abs(w) < 60000
             O.check(np.where(fits, O.f64(g), 0), np.where(fits, w, 0), t, name)
+
+
+def _shifted(t):
+    """The same values two bytes past a 16-byte boundary."""
+    buf = torch.empty(t.numel() + 8, dtype=t.dtype, device=t.device)
+    out = buf[1:1 + t.numel()].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+def test_misaligned_tensors():
+    """Rows that are no aligned vectors are read and written element by element: the same results."""
+    need_cuda()
+    M, L, K, N, r = 150, 3, 136, 264, 24
+    x, a, b, base, s, offsets, order = _case(M, L, K, N, r, B, 77)
+    rng = torch.tensor([1, 2], dtype=torch.int64, device="cuda")
+    dy, base_dx = (base * 0.1), (x * 0.1)
+    v = torch.zeros(M, r, device="cuda")
+    kw = dict(order=order, scaling=s, p=0.2, rng=rng, path=TC)
+    out = tq.tq_lora(x, a, b, base, offsets, v=v, **kw)
+    grads = tq.tq_lora_backward(dy, x, a, b, v, base_dx, offsets, **kw)
+    w = torch.zeros(M, r, device="cuda")
+    dest = _shifted(torch.zeros_like(base))
+    got = tq.tq_lora(_shifted(x), _shifted(a), _shifted(b), _shifted(base), offsets, v=w, out=dest, **kw)
+    assert got is dest and torch.equal(got, out) and torch.equal(v, w)
+    more = tq.tq_lora_backward(_shifted(dy), _shifted(x), _shifted(a), _shifted(b), w, _shifted(base_dx), offsets,
+                               dx=_shifted(x), da=_shifted(a), db=_shifted(b), **kw)
+    assert all(torch.equal(g, h) for g, h in zip(more, grads))
+    plain = tq.tq_lora(_shifted(x), a, b, base, offsets, order=order, scaling=s)
+    want, tol, *_ = _forward64(x, a, b, base, s, offsets, order)
+    O.check(plain, want, tol)
+    with pytest.raises(tq.TQError):
+        tq.tq_lora(_shifted(x), a, b, base, offsets, order=order, scaling=s, path=FEW)
+
+
+def test_two_streams_at_once_and_two_captured_graphs():
+    """Calls with scratch of their own may run at once, eager and replayed."""
+    need_cuda()
+    cases = [_case(400, 4, 512, 768, 32, H, 90 + i) for i in range(2)]
+    dys = [(c[3] * 0.1) for c in cases]
+    vs = [torch.zeros(400, 32, device="cuda") for _ in cases]
+    ws = [torch.empty(tq.tq_lora_workspace_size(400, 4, 32), dtype=torch.uint8, device="cuda") for _ in cases]
+
+    def step(i):
+        x, a, b, base, s, offsets, order = cases[i]
+        out = tq.tq_lora(x, a, b, base, offsets, order=order, scaling=s, v=vs[i], path=TC)
+        few = tq.tq_lora(x, a, b, base, offsets, order=order, scaling=s, path=FEW)
+        return (out, few, *tq.tq_lora_backward(dys[i], x, a, b, vs[i], None, offsets, order=order, scaling=s, workspace=ws[i]))
+
+    want = [tuple(t.clone() for t in step(i)) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        got = []
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append(step(i))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for g, w in zip(got, want) for p, q in zip(g, w))
+    graphs, outs = [], []
+    for i, st in enumerate(streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            outs.append(step(i))
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for g, w in zip(outs, want) for p, q in zip(g, w))
+    assert tq.tq_device_status() == 0
+
+
+def test_a_captured_graph_serves_any_plan():
+    need_cuda()
+    M, L, K, N, r = 96, 5, 256, 320, 16
+    x, a, b, base, s, offsets, order = _case(M, L, K, N, r, H, 50)
+    ids = torch.zeros(M, 1, dtype=torch.int32, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+
+    def step(path):
+        o, w, _ = tq.tq_moe_sort(ids, L)
+        return tq.tq_lora(x, a, b, base, o, order=w, scaling=s, path=path)
+
+    with torch.cuda.stream(st):
+        step(TC), step(FEW)
+    st.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        outs = [step(TC), step(FEW)]
+    for seed, how in ((1, "spread"), (2, "none"), (3, "one"), (4, "runs")):
+        offsets, order = _plan(M, L, seed, how)
+        new = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+        for l in range(L):
+            new[order[offsets[l]:offsets[l + 1]].long()] = l
+        ids.copy_(new.view(M, 1))
+        g.replay()
+        torch.cuda.synchronize()
+        want, tol, *_ = _forward64(x, a, b, base, s, offsets, order)
+        for out in outs:
+            O.check(out, want, tol, how)
+
+
+def test_many_adapters_and_highest_rank():
+    """1024 adapters, most without rows, of rank 128."""
+    need_cuda()
+    M, L, K, N, r = 40, 1024, 64, 72, 128
+    x, a, b, base, s, offsets, order = _case(M, L, K, N, r, B, 60)
+    want, tol, *_ = _forward64(x, a, b, base, s, offsets, order)
+    for path in (ANY, TC, FEW):
+        O.check(tq.tq_lora(x, a, b, base, offsets, order=order, scaling=s, path=path), want, tol, f"path {path}")
+    v = torch.zeros(M, r, device="cuda")
+    tq.tq_lora(x, a, b, None, offsets, order=order, scaling=s, v=v, path=TC)
+    w = _backward64(base, x, a, b, v, None, s, offsets, order, 0.0, 0, 0)
+    for g, (want, tol), name in zip(tq.tq_lora_backward(base, x, a, b, v, None, offsets, order=order, scaling=s), w, ("dx", "da", "db")):
+        O.check(g, want, tol, name)
+
+
+def test_rows_past_two_to_the_31_elements():
+    """Offsets of rows in x and base past 2^31 elements, on the tensor cores and element offsets of dropout with them."""
+    need_cuda()
+    M, L, K, N, r = 140000, 2, 16384, 16, 8
+    x = torch.zeros(M, K, dtype=H, device="cuda")
+    last = torch.randn(64, K, generator=_gen(1), device="cuda").half()
+    x[-64:] = last
+    _, a, b, base, s, _, _ = _case(64, L, K, N, r, H, 1)
+    offsets = torch.tensor([0, M - 30, M], dtype=torch.int32, device="cuda")
+    small = torch.tensor([0, 34, 64], dtype=torch.int32, device="cuda")
+    out = tq.tq_lora(x, a, b, None, offsets, scaling=s)
+    want, tol, *_ = _forward64(last, a, b, None, s, small, None)
+    O.check(out[-64:], want, tol)
+    assert not out[:-64].any()
+    rng = torch.tensor([4, 4], dtype=torch.int64, device="cuda")
+    y = tq.tq_dropout(x, 0.5, rng)
+    tail = O.kept_rows(M, K, 0.5, 4, 4, M - 64)
+    assert np.array_equal(O.f64(y[-64:]) != 0, tail & (O.f64(last) != 0))
+    v = torch.zeros(M, r, device="cuda")
+    tq.tq_lora(x, a, b, None, offsets, scaling=s, p=0.5, rng=rng, v=v, path=TC)
+    xd = O.f64(last) * tail * 2.0
+    for l, lo, hi in ((0, 0, 34), (1, 34, 64)):
+        w = xd[lo:hi] @ O.f64(a[l]).T
+        mag = np.abs(xd[lo:hi]) @ np.abs(O.f64(a[l])).T
+        O.check(O.f64(v[-64:])[lo:hi], w, _sum_tol(K) * mag + 2.0 ** -149, "v")
 
 
 def test_same_results_on_every_run():

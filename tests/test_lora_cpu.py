@@ -48,11 +48,11 @@ def test_forward_argument_errors():
         assert _fwd(**{name: None}) == -1, name
     assert _fwd(M=0, x=None, out=None, off=None) == 0 and _fwd(N=0, out=None) == 0
     assert _fwd(v=None, path=tq.PATH_GENERIC) == -1 and _fwd(v=None, path=tq.PATH_PREFILL) == -1
-    for path in (tq.PATH_DECODE, tq.PATH_PREFILL):
-        assert _fwd(K=63, path=path) == -8 and _fwd(N=62, path=path) == -8
-        for name in ("x", "a", "b", "base", "out", "v"):
-            assert _fwd(**{name: Q}, path=path) == -3, name
-    assert _fwd(path=tq.PATH_DECODE, p=0.5, rng=P) == -8
+    assert _fwd(K=63, path=tq.PATH_DECODE) == -8 and _fwd(N=62, path=tq.PATH_DECODE) == -8
+    assert _fwd(M=65536, path=tq.PATH_DECODE) == -8 and _fwd(path=tq.PATH_DECODE, p=0.5, rng=P) == -8
+    for name in ("x", "a", "b", "base", "out", "v"):
+        assert _fwd(**{name: Q}, path=tq.PATH_DECODE) == -3, name
+    assert _fwd(v=Q, path=tq.PATH_PREFILL) == -3
 
 
 def test_backward_argument_errors():
@@ -60,9 +60,7 @@ def test_backward_argument_errors():
         assert _bwd(**{name: None}) == -1, name
     assert _bwd(dx=None, da=None, db=None, off=None) == 0           # nothing wanted
     assert _bwd(path=tq.PATH_DECODE) == -8
-    assert _bwd(K=63, path=tq.PATH_PREFILL) == -8 and _bwd(N=62, path=tq.PATH_PREFILL) == -8
-    for name in ("dy", "x", "a", "b", "v", "ws", "base_dx", "dx", "da", "db"):
-        assert _bwd(**{name: Q}, path=tq.PATH_PREFILL) == -3, name
+    assert _bwd(v=Q, path=tq.PATH_PREFILL) == -3 and _bwd(ws=Q) == -3
     need = tq.tq_lora_workspace_size(4, 2, 8)
     assert need >= 4 * 4 * 8 and _bwd(ws_bytes=need - 1) == -2
     for M, L, r in ((-1, 2, 8), (4, 0, 8), (4, 1025, 8), (4, 2, 0), (4, 2, 129), (2 ** 31, 2, 8)):
@@ -74,8 +72,8 @@ def test_path_rule():
                           (190, 4, 512, 512, 128)):
         assert tq.tq_lora_path(M, L, N, K, r) == tq.PATH_DECODE
         assert tq.tq_lora_path(M, L, N, K, r, dropout=True) == tq.PATH_PREFILL
-        assert tq.tq_lora_path(M, L, N, K, r, aligned=False) == tq.PATH_GENERIC
-        assert tq.tq_lora_path(M, L, N + 1, K, r) == tq.PATH_GENERIC and tq.tq_lora_path(M, L, N, K + 4, r) == tq.PATH_GENERIC
+        assert tq.tq_lora_path(M, L, N, K, r, aligned=False) == tq.PATH_PREFILL
+        assert tq.tq_lora_path(M, L, N + 1, K, r) == tq.PATH_PREFILL and tq.tq_lora_path(M, L, N, K + 4, r) == tq.PATH_PREFILL
     for M, L, r in ((1024, 1, 16), (512, 1, 64), (2048, 64, 64), (256, 64, 128), (100000, 1024, 1)):
         assert tq.tq_lora_path(M, L, 4096, 4096, r) == tq.PATH_PREFILL
     assert tq.tq_lora_path(0, 1, 64, 64, 8) == tq.PATH_GENERIC and tq.tq_lora_path(-1, 1, 64, 64, 8) == -2
