@@ -98,7 +98,7 @@ __device__ __forceinline__ uint4 philox(uint64_t group, const PhiloxKey& key) {
 // Whether element e of the group is kept.
 __device__ __forceinline__ bool drop_keeps(const uint4& w, int e, uint32_t thr) {
   const uint32_t word = (e >> 1) == 0 ? w.x : ((e >> 1) == 1 ? w.y : ((e >> 1) == 2 ? w.z : w.w));
-  return ((e & 1) ? word >> 16 : word & 0xFFFFu) >= thr;
+  return ((e & 1) ? word : word << 16) >= thr << 16;  // thr <= 65535
 }
 
 // Eight 16-bit elements of a group with the dropped ones zero.  (Comparing whole words decides the high halves, shifted ones the low
@@ -296,49 +296,77 @@ static cudaError_t lora_generic_wgrad(bool bf16, const LoraArgs& a, cudaStream_t
 // ---------------------------------------------------------------------------------------------
 constexpr int kDropThreads = 256;
 
-// A thread per group of eight columns.  kVec: groups are whole and aligned to their size.
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kDropThreads)
-    dropout_kernel(const T* x, T* out, const DropArgs d, int64_t M, int64_t K) {
+// Whole, aligned groups: a thread per group of eight columns.  16384 x 4096 in bf16: 48 us, 0.85 of the copy rate; with two groups per
+// thread in flight 54.
+template <typename T>
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const T* x, T* out, const DropArgs d, int64_t total) {
   pdl_allow_dependents();
   pdl_wait_prior_grids();
-  const int64_t groups = (K + 7) >> 3, total = M * groups;
   const PhiloxKey key = philox_key(d);
   const float f = d.thr ? d.scale : 1.0f;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kDropThreads + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * kDropThreads) {
-    if (kVec) {
-      constexpr int kW = 16 / sizeof(T);  // elements per 16 bytes
-      Vec<T, kW> v[8 / kW];
+    constexpr int kW = 16 / sizeof(T);  // elements per 16 bytes
+    Vec<T, kW> v[8 / kW];
 #pragma unroll
-      for (int q = 0; q < 8 / kW; ++q) v[q] = reinterpret_cast<const Vec<T, kW>*>(x)[i * (8 / kW) + q];
-      const uint4 bits = d.thr ? philox(i, key) : make_uint4(~0u, ~0u, ~0u, ~0u);
+    for (int q = 0; q < 8 / kW; ++q) v[q] = reinterpret_cast<const Vec<T, kW>*>(x)[i * (8 / kW) + q];
+    const uint4 bits = d.thr ? philox(i, key) : make_uint4(~0u, ~0u, ~0u, ~0u);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        T& t = v[e / kW].v[e % kW];
-        t = from_f32<T>(drop_keeps(bits, e, d.thr) ? f * to_f32(t) : 0.0f);
-      }
+    for (int e = 0; e < 8; ++e) {
+      T& t = v[e / kW].v[e % kW];
+      t = from_f32<T>(drop_keeps(bits, e, d.thr) ? f * to_f32(t) : 0.0f);
+    }
 #pragma unroll
-      for (int q = 0; q < 8 / kW; ++q) reinterpret_cast<Vec<T, kW>*>(out)[i * (8 / kW) + q] = v[q];
-    } else {
-      const int64_t m = i / groups, c0 = 8 * (i - m * groups);
-      const uint4 bits = d.thr ? philox(i, key) : make_uint4(~0u, ~0u, ~0u, ~0u);
+    for (int q = 0; q < 8 / kW; ++q) reinterpret_cast<Vec<T, kW>*>(out)[i * (8 / kW) + q] = v[q];
+  }
+}
+
+// Any width and alignment: a warp per 256 columns of a row.  Each lane draws for one group, and the elements are taken in the order
+// of memory, their truth values from the lane that drew them.
+template <typename T>
+__global__ void __launch_bounds__(kDropThreads)
+    dropout_any_kernel(const T* x, T* out, const DropArgs d, int64_t M, int64_t K) {
+  pdl_allow_dependents();
+  pdl_wait_prior_grids();
+  const int lane = threadIdx.x & 31;
+  const int64_t groups = (K + 7) >> 3, segments = (K + 255) >> 8, total = M * segments;
+  const PhiloxKey key = philox_key(d);
+  const float f = d.thr ? d.scale : 1.0f;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kDropThreads + threadIdx.x) >> 5; i < total;
+       i += (static_cast<int64_t>(gridDim.x) * kDropThreads) >> 5) {
+    const int64_t m = i / segments, c0 = (i - m * segments) << 8;
+    const T* src = x + m * K + c0;
+    T v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c0 + e < K)
-          out[m * K + c0 + e] = from_f32<T>(drop_keeps(bits, e, d.thr) ? f * to_f32(x[m * K + c0 + e]) : 0.0f);
+    for (int e = 0; e < 8; ++e)
+      if (c0 + 32 * e + lane < K) v[e] = src[32 * e + lane];
+    uint32_t kept = 0xFFu;
+    if (d.thr) {
+      const uint4 bits = philox(m * groups + (c0 >> 3) + lane, key);
+      kept = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) kept |= drop_keeps(bits, e, d.thr) ? 1u << e : 0u;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t k = __shfl_sync(0xFFFFFFFFu, kept, 4 * e + (lane >> 3));
+      if (c0 + 32 * e + lane < K)
+        out[m * K + c0 + 32 * e + lane] = from_f32<T>((k >> (lane & 7)) & 1u ? f * to_f32(v[e]) : 0.0f);
     }
   }
 }
 
 cudaError_t launch_dropout(const void* x, int dtype, void* out, const DropArgs& d, int64_t M, int64_t K,
                            cudaStream_t s) {
-  const unsigned grid = lora_grid((M * ((K + 7) >> 3) + kDropThreads - 1) / kDropThreads, 32);
+  const int64_t groups = M * ((K + 7) >> 3);
   const bool vec = K % 8 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+  const dim3 grid(lora_grid((groups + kDropThreads - 1) / kDropThreads, 32));
   auto run = [&](auto t) {
     using T = decltype(t);
-    return launch_pdl(vec ? dropout_kernel<T, true> : dropout_kernel<T, false>, dim3(grid), dim3(kDropThreads), 0, 1, s,
-                      static_cast<const T*>(x), static_cast<T*>(out), d, M, K);
+    const T* xt = static_cast<const T*>(x);
+    T* ot = static_cast<T*>(out);
+    if (vec) return launch_pdl(dropout_kernel<T>, grid, dim3(kDropThreads), 0, 1, s, xt, ot, d, groups);
+    return launch_pdl(dropout_any_kernel<T>, grid, dim3(kDropThreads), 0, 1, s, xt, ot, d, M, K);
   };
   return dtype == 0 ? run(float()) : (dtype == 1 ? run(__half()) : run(__nv_bfloat16()));
 }
