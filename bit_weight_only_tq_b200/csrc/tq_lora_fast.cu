@@ -72,15 +72,21 @@ __device__ __forceinline__ float split_scale(float most, float& inv) {
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
+// Eight consecutive 16-bit elements of which `left` are there (zero past them), one by one; out of line, since what runs beside it
+// is slower for the code.
+__device__ __noinline__ uint4 load8_any(const uint16_t* p, int64_t left) {
+  uint16_t h[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h[e] = e < left ? p[e] : static_cast<uint16_t>(0);
+  return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+}
+
 // Eight consecutive 16-bit elements of a row of `width` from column c (zero past it); vec: whole and aligned.
 __device__ __forceinline__ uint4 load8(const void* row, int64_t c, int64_t width, bool vec) {
   const uint16_t* p = static_cast<const uint16_t*>(row) + c;
   if (c >= width) return make_uint4(0u, 0u, 0u, 0u);
   if (vec) return *reinterpret_cast<const uint4*>(p);
-  uint16_t h[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) h[e] = c + e < width ? p[e] : static_cast<uint16_t>(0);
-  return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+  return load8_any(p, width - c);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -252,10 +258,12 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
                : "r"(taddr));
 }
 
-template <typename T, int kMode, int RP, bool kDrop>
+// kVec: all rows in whole, aligned vectors; without it kDrop is decided at run time where it is set.
+template <typename T, int kMode, int RP, bool kDrop, bool kVec>
 __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs a, const int S) {
   using L = LoraTcLayout<kMode, RP>;
   constexpr bool kW = kMode == kWgrad;
+  const bool pvec = kVec || a.pvec, wvec = kVec || a.wvec, yvec = kVec || a.yvec, drop = kDrop && (kVec || a.drop.thr != 0);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
@@ -397,7 +405,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
         for (int k = 0; k < L::kPer; ++k) {
           const int mk = rows[L::kStep * k];
           const uint32_t dst = st + pdst + k * L::kStep * 128;
-          if (a.pvec)
+          if (pvec)
             cp_async_16s(dst, pcol + static_cast<int64_t>(mk < 0 ? 0 : mk) * a.C, mk < 0 ? 0u : psize);
           else
             *reinterpret_cast<uint4*>(sm + (dst - ring0)) =
@@ -408,7 +416,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
 #pragma unroll
         for (int k = 0; k < L::kPer; ++k) {
           const uint32_t dst = st + pdst + k * L::kStep * 128;
-          if (a.pvec) {
+          if (pvec) {
             if (m[k] >= 0) cp_async_16s(dst, size ? src[k] : P, size);
           } else if (m[k] >= 0) {
             const int64_t ci = c + static_cast<int64_t>(i) * 64 * L::kSub;
@@ -421,7 +429,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
       for (int k = 0; k < L::kPerW; ++k) {
         if (L::kChunksW % kLtcLoaders != 0 && tid + kLtcLoaders * k >= L::kChunksW) continue;
         const uint32_t size = !kTail || wrow[k] < left ? wsize[k] : 0u;
-        if (kW || a.wvec) {
+        if (kW || wvec) {
           cp_async_16s(st + wdst[k], size ? wsrc[k] : P, size);
         } else {  // from the row's start: wc0 columns (or inner columns) before this chunk
           const int64_t wc0 = kMode == kReduceA ? (static_cast<int64_t>(s0) + i) * 64 * L::kSub + wrow[k]
@@ -435,7 +443,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
     };
     int hd = 0, hs = 0;  // the stage to hand over and its slot
     auto hand_over = [&]() {
-      if (kDrop) {
+      if (drop) {
         uint8_t* st = sm + hs * L::kStage + pdst;
         const int64_t hc = kW ? c : c + static_cast<int64_t>(hd) * 64 * L::kSub;
         if (hc < a.C)
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
                 most2 = fmaxf(fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(p.z), fabsf(p.w))), most2);
               }
             }
-        } else if (kW && a.wj == 1 && (a.rank & 7) == 0 && a.yvec) {  // dB: eight consecutive elements of a row
+        } else if (kW && a.wj == 1 && (a.rank & 7) == 0 && yvec) {  // dB: eight consecutive elements of a row
           if (c0 + r < a.C && j0 < a.rank) {
             Vec<T, 8> o;
 #pragma unroll
@@ -716,7 +724,7 @@ static int lora_cluster_capacity(const DeviceInfo& di, int S) {
   if (di.device < 0 || di.device >= kPfMaxDevices) return di.num_sms / S;
   int n = cache[di.device][S].load(std::memory_order_relaxed);
   if (n > 0) return n;
-  auto* kern = lora_tc_kernel<__half, kReduceA, 64, false>;
+  auto* kern = lora_tc_kernel<__half, kReduceA, 64, false, true>;
   constexpr int kAlloc = LoraTcLayout<kReduceA, 64>::kAlloc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1, 1, static_cast<unsigned>(S));
@@ -759,7 +767,8 @@ static int lora_pad_rank(int64_t rank) { return rank <= 16 ? 16 : (rank <= 32 ? 
 
 template <typename T, int kMode, int RP, bool kDrop>
 static cudaError_t launch_lora_tc(const LoraArgs& a, dim3 grid, cudaStream_t s) {
-  auto* kern = lora_tc_kernel<T, kMode, RP, kDrop>;
+  const bool vec = a.pvec && (a.wvec || kMode == kWgrad) && (a.yvec || kMode != kWgrad);
+  auto* kern = vec ? lora_tc_kernel<T, kMode, RP, kDrop, true> : lora_tc_kernel<T, kMode, RP, kMode != kReduceB, false>;
   constexpr int kAlloc = LoraTcLayout<kMode, RP>::kAlloc;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kAlloc);
   if (e != cudaSuccess) return e;
@@ -909,9 +918,10 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
-template <typename T, int RP, bool kWA, bool kDrop>
+template <typename T, int RP, bool kWA, bool kDrop, bool kVec>  // kVec, kDrop as in lora_tc_kernel
 __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const LoraArgs a) {
   using L = LoraXpLayout<RP, kWA>;
+  const bool wvec = kVec || a.wvec, yvec = kVec || a.yvec, drop = kDrop && (kVec || a.drop.thr != 0);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* wfull = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
@@ -976,7 +986,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
       for (int i = warp; i < tile.cnt; i += kXpEpi) {
         const int64_t q = tile.pos + i, m = lora_row(a, q < head ? q : q - head + at);
         if (m < 0) continue;
-        if (!a.yvec) {
+        if (!yvec) {
           for (int64_t c = c_begin + lane; c < c_end; c += 32)
             out[m * a.C + c] = base ? base[m * a.C + c] : from_f32<T>(0.0f);
           continue;
@@ -1004,7 +1014,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     auto load_base = [&](uint4 (&to)[4], int64_t at) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        to[i] = base && m[i] >= 0 && at < c_end ? load8(base + static_cast<int64_t>(m[i]) * a.C, at, a.C, a.yvec)
+        to[i] = base && m[i] >= 0 && at < c_end ? load8(base + static_cast<int64_t>(m[i]) * a.C, at, a.C, yvec)
                                                 : make_uint4(0u, 0u, 0u, 0u);
     };
     load_base(y[0], c);
@@ -1077,13 +1087,13 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
           if (m[2 * h + i] < 0) continue;
           const int64_t at_row = static_cast<int64_t>(m[2 * h + i]) * a.C + c;
           Vec<T, 8> o = *reinterpret_cast<const Vec<T, 8>*>(&yb[2 * h + i]);
-          const uint4 bits = kDrop ? philox(m[2 * h + i] * groups + (c >> 3), key) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 bits = drop ? philox(m[2 * h + i] * groups + (c >> 3), key) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float x = __uint_as_float(acc[4 * (e >> 1) + 2 * i + (e & 1)]), z = to_f32(o.v[e]);
-            o.v[e] = from_f32<T>(kDrop && !drop_keeps(bits, e, a.drop.thr) ? z : fmaf(f[2 * h + i], x, z));
+            o.v[e] = from_f32<T>(drop && !drop_keeps(bits, e, a.drop.thr) ? z : fmaf(f[2 * h + i], x, z));
           }
-          if (a.yvec) {
+          if (yvec) {
             *reinterpret_cast<Vec<T, 8>*>(out + at_row) = o;
           } else {
             for (int e = 0; e < 8 && c + e < a.C; ++e) out[at_row + e] = o.v[e];
@@ -1132,7 +1142,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
       const int64_t at = c_begin + static_cast<int64_t>(b) * kXpCols + 8 * ach;
 #pragma unroll
       for (int i = 0; i < kPerA; ++i)
-        pre[i] = at < a.C && aj + 8 * i < a.rank ? load8(W + (aj + 8 * i) * a.C, at, a.C, a.wvec) : make_uint4(0u, 0u, 0u, 0u);
+        pre[i] = at < a.C && aj + 8 * i < a.rank ? load8(W + (aj + 8 * i) * a.C, at, a.C, wvec) : make_uint4(0u, 0u, 0u, 0u);
     };
     if (kWA) load_a(0);
     for (int b = 0; b < nb + L::kLag && ok; ++b) {
@@ -1164,7 +1174,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
           for (int ch = 0; ch < RP / 8; ++ch) {
             uint8_t* dst = st + (ch >> 3) * L::kPlaneW + pos * 128 + (((ch & 7) ^ (pos & 7)) << 4);
             const bool in = there && 8 * ch < a.rank;
-            if (a.wvec)
+            if (wvec)
               cp_async_16(dst, in ? src + 8 * ch : W, in ? 16u : 0u);
             else
               *reinterpret_cast<uint4*>(dst) = in ? load8(src, 8 * ch, a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
@@ -1228,7 +1238,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
 
 template <typename T, int RP, bool kWA, bool kDrop>
 static cudaError_t launch_lora_expand_tc(const LoraArgs& a, cudaStream_t s) {
-  auto* kern = lora_expand_tc_kernel<T, RP, kWA, kDrop>;
+  auto* kern = a.wvec && a.yvec ? lora_expand_tc_kernel<T, RP, kWA, kDrop, true> : lora_expand_tc_kernel<T, RP, kWA, kWA, false>;
   constexpr int kAlloc = LoraXpLayout<RP, kWA>::kAlloc;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kAlloc);
   if (e != cudaSuccess) return e;
