@@ -1,18 +1,20 @@
 // tq_dx.cu -- the packed products' gradient for x, dx[m, k] = sum_n dy[m, n] What[n, k] (include/tq_lora.h).
 //
-// The products sum over the packed dimension k; this sums over the rows n, so each decoded weight is needed with n, not k,
-// running along the tensor core's summation index.  On the tensor-core path What^T is the A operand in tensor
+// The products sum over the packed dimension k; this sums over the rows n, so each decoded weight is needed with n,
+// not k, running along the tensor core's summation index.  On the tensor-core path What^T is the A operand in tensor
 // memory and dy the B operand:
 //   D[k, m] (TMEM, fp32) += A[k, n] (TMEM, fp16) * B[m, n]^T (smem, dy tile, K-major)
-// A TMEM lane holds one k and its columns hold pairs of n, while a packed word holds 8 (INT4) or 16 (ternary) k of one n.
+// A TMEM lane holds one k and its columns hold pairs of n, while a packed word holds 8 (INT4) or 16 (ternary) k of
+// one n.
 // Eight (sixteen) lanes of a decode warp load the words of as many rows n and exchange them by a butterfly (three or
-// four shuffles, each followed by a byte permute or a shift and a mask), after which each lane's word holds its own k for 8 (16)
-// consecutive n, in order; it is then decoded as in the products.  That costs 8 instructions per 8 INT4 weights and
-// 11 per 16 ternary ones, against a load per weight without the exchange, and no shared-memory traffic beyond the
-// packed bytes: a decoded tile in shared memory (MN-major, needing no exchange) would be written and read again there, and
-// shared memory already carries the dy tile twice at the tensor core's full rate.
+// four shuffles, each followed by a byte permute or a shift and a mask), after which each lane's word holds its own k
+// for 8 (16) consecutive n, in order; it is then decoded as in the products.  That costs 8 instructions per 8 INT4
+// weights and 11 per 16 ternary ones, against a load per weight without the exchange, and no shared-memory traffic
+// beyond the packed bytes: a decoded tile in shared memory (MN-major, needing no exchange) would be written and read
+// again there, and shared memory already carries the dy tile twice at the tensor core's full rate.
 //
-// Scales run along n here, two per TMEM column: (c - 1) s is exact in fp16 (ternary); fp16((u - z) s) is one rounding per
+// Scales run along n here, two per TMEM column: (c - 1) s is exact in fp16 (ternary); fp16((u - z) s) is one rounding
+// per
 // INT4 weight, as in the products' tensor-core path.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -106,10 +108,10 @@ static cudaError_t launch_dx_generic(bool int4, const DxArgs& a, cudaStream_t s)
 
 // ---------------------------------------------------------------------------------------------
 // Tensor cores.  One CTA = 128 columns k x TN tokens x a range of n, in stages of 64 n:
-//   warp 0: TMA of the dy tile (TN tokens x 64 n, 128-byte swizzle); warp 2: TMA of the packed weights, 256 rows x 32 bytes
-//   (ternary) or 64 bytes (INT4) per tile, swizzled so that the decode warps' loads meet no (INT4) or two-way (ternary) bank
-//   conflicts; warp 3: the scales (and zero-points) of those 256 rows, as pairs; warp 1: tensor memory and the MMAs;
-//   warps 4-11: two groups of four decode warps on alternate stages.  All twelve run the epilogue.
+//   warp 0: TMA of the dy tile (TN tokens x 64 n, 128-byte swizzle); warp 2: TMA of the packed weights, 256 rows x 32
+//   bytes (ternary) or 64 bytes (INT4) per tile, swizzled so that the decode warps' loads meet no (INT4) or two-way
+//   (ternary) bank conflicts; warp 3: the scales (and zero-points) of those 256 rows, as pairs; warp 1: tensor memory
+//   and the MMAs; warps 4-11: two groups of four decode warps on alternate stages.  All twelve run the epilogue.
 // Every wait is bounded, as in the products.
 // ---------------------------------------------------------------------------------------------
 constexpr int kXM = 128;        // columns k per CTA (UMMA M, TMEM lanes)
@@ -126,7 +128,7 @@ struct DxLayout {
   static constexpr int kRowBytes = kInt4 ? 64 : 32;              // packed bytes of 128 k of a row
   static constexpr int kTileD = TN * kXN * 2;
   static constexpr int kTileP = kXTileN * kRowBytes;
-  static constexpr int kTileS = kXTileN / 2 * (kInt4 ? 8 : 4);   // per pair of n: {zero pair, scale pair} or {scale pair}
+  static constexpr int kTileS = kXTileN / 2 * (kInt4 ? 8 : 4);   // per pair of n: {zero pair,} scale pair
   static constexpr int kRing = TN == 256 ? 4 : 8;                // stages: dy tile in shared memory, weights in TMEM
   static constexpr int kOffP = kRing * kTileD;
   static constexpr int kOffS = kOffP + kXPRing * kTileP;
@@ -145,8 +147,9 @@ struct DxLayout {
   static_assert(kOffP % 1024 == 0 && kTileP % 1024 == 0 && kTileS % 16 == 0 && kAlloc <= 227 * 1024, "shared memory");
 };
 
-// One step of a transposition of w-bit fields across lanes: of the pair (x, partner's y) the lane keeps the fields of its
-// own side.  16 and 8 bits: a byte permute with a selector of the lane's side; 4 and 2 bits: a rotation and a select.
+// One step of a transposition of w-bit fields across lanes: of the pair (x, partner's y) the lane keeps the fields of
+// its own side.  16 and 8 bits: a byte permute with a selector of the lane's side; 4 and 2 bits: a rotation and a
+// select.
 __device__ __forceinline__ uint32_t exchange_bytes(uint32_t x, int d, uint32_t sel) {
   return __byte_perm(x, __shfl_xor_sync(0xFFFFFFFFu, x, d), sel);
 }
@@ -165,8 +168,8 @@ __device__ __forceinline__ void dx_decode_w4(uint32_t w, const uint4& zs0, const
 
 template <bool kInt4, int TN>
 __global__ void __launch_bounds__(kXThreads, 1)
-    dx_tc_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant__ CUtensorMap tmap_w, const DxArgs a,
-                 const int S, const int kt0) {
+    dx_tc_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant__ CUtensorMap tmap_w,
+                 const DxArgs a, const int S, const int kt0) {
   using L = DxLayout<kInt4, TN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -361,8 +364,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
   }
 
   // ------------------------------------------------------------------ epilogue (all warps)
-  // Groups of four warps take 32-token chunks of the accumulator in turn; a warp reads TMEM lanes 32 (warp % 4) .. + 31,
-  // i.e. column k0 + threadIdx.x % 128.
+  // Groups of four warps take 32-token chunks of the accumulator in turn; a warp reads TMEM lanes 32 (warp % 4) .. +
+  // 31, i.e. column k0 + threadIdx.x % 128.
   if (threadIdx.x == 128) tmem_slot[1] = acc_flag ? 1u : 0u;
   __syncwarp();
   named_barrier_sync(1 + kXEpiGroups, kXThreads);
@@ -372,7 +375,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int grp = ((warp >> 2) + kXEpiGroups - 1) % kXEpiGroups;
     const int r = threadIdx.x & (kXM - 1);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    // dx[m0 + t0 + t, k0 ..] for t < cnt (<= 32) from this group's staging buffer [cnt][128] fp16; K is a multiple of 64
+    // dx[m0 + t0 + t, k0 ..] for t < cnt (<= 32) from this group's staging buffer [cnt][128] fp16; K is a multiple of
+    // 64
     auto store_staged = [&](const __half* stage, int t0, int cnt) {
       named_barrier_sync(1 + grp, 128);
 #pragma unroll
@@ -404,9 +408,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
         store_staged(stage, c * 32, 32);
       }
     } else {
-      // the tokens are split over the S CTAs of the cluster (TN / S each); each CTA sends its partial sums of the others'
-      // tokens into their shared memory, [source rank][token / 4][k][token % 4] fp32, and adds those of its own in
-      // rank order
+      // the tokens are split over the S CTAs of the cluster (TN / S each); each CTA sends its partial sums of the
+      // others' tokens into their shared memory, [source rank][token / 4][k][token % 4] fp32, and adds those of its
+      // own in rank order
       const int tpo = TN / S, own0 = rank * tpo, own1 = own0 + tpo;
       float* red = reinterpret_cast<float*>(sm);
       const uint32_t red_local = smem_u32(red);
@@ -423,7 +427,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
           const int tok = c * 32 + j, q = tok / tpo;
           if (q != rank) {
             const uint32_t dst = red_local + 4u * static_cast<uint32_t>(slot(rank, tok - q * tpo));
-            st_shared_cluster_v4_f32(mapa_shared(dst, static_cast<uint32_t>(q)), rr[j], rr[j + 1], rr[j + 2], rr[j + 3]);
+            st_shared_cluster_v4_f32(mapa_shared(dst, static_cast<uint32_t>(q)), rr[j], rr[j + 1], rr[j + 2],
+                                     rr[j + 3]);
           }
         }
       }
@@ -536,8 +541,8 @@ static cudaError_t launch_dx_tc(const DxArgs& a, cudaStream_t s) {
         dim3(static_cast<unsigned>(last - first), static_cast<unsigned>(mt), static_cast<unsigned>(S)), s, attr);
     return cudaLaunchKernelEx(&cfg, kern, td, tw, a, S, static_cast<int>(first));
   };
-  // n split over a cluster while the tiles leave SMs idle and all clusters are resident at once, and a nearly empty last wave
-  // split off into a launch of its own, as in the products
+  // n split over a cluster while the tiles leave SMs idle and all clusters are resident at once, and a nearly empty
+  // last wave split off into a launch of its own, as in the products
   int S = 1;
   while (S < 8 && kt * mt * S * 2 <= di.num_sms && S * 2 <= ns) {
     const int cap = capacity(S * 2);
@@ -563,7 +568,8 @@ cudaError_t launch_dx(bool int4, int path, const DxArgs& a, cudaStream_t s) {
   if (path != 2) return launch_dx_generic(int4, a, s);
   const int tn = prefill_tile_tokens(a.M);
   if (int4)
-    return tn == 64 ? launch_dx_tc<true, 64>(a, s) : (tn == 128 ? launch_dx_tc<true, 128>(a, s) : launch_dx_tc<true, 256>(a, s));
+    return tn == 64 ? launch_dx_tc<true, 64>(a, s)
+                    : (tn == 128 ? launch_dx_tc<true, 128>(a, s) : launch_dx_tc<true, 256>(a, s));
   return tn == 64 ? launch_dx_tc<false, 64>(a, s)
                   : (tn == 128 ? launch_dx_tc<false, 128>(a, s) : launch_dx_tc<false, 256>(a, s));
 }

@@ -3,8 +3,8 @@
 //
 // Forward and backward are four forms of three sums, over the rows m(r) of the sorted positions r of each adapter l:
 //   reduce   V[r, j]  = f sum_c P[m, c] W_l(c, j)        v: P = drop(x), W = A;     dv: P = dy, W = B
-//   expand   O[m, c]  = base[m, c] + f sum_j V[r, j] W_l(c, j)   out: V = v, W = B;  dx: V = dv, W = A, dropout of the result
-//   wgrad    G_l(c, j) = f sum_r P[m, c] V[r, j]         dA: P = drop(x), V = dv;   dB: P = dy, V = v
+//   expand   O[m, c]  = base[m, c] + f sum_j V[r, j] W_l(c, j)   out: V = v, W = B;  dx: V = dv, W = A, dropout of
+//   the result wgrad    G_l(c, j) = f sum_r P[m, c] V[r, j]         dA: P = drop(x), V = dv;   dB: P = dy, V = v
 // with W(c, j) stored as A [rank, C] (column c of row j) or as B [C, rank].  The factors that do not depend on the
 // summation index (scaling, 1 / (1 - p)) are applied to the fp32 sum.
 #include <cuda_bf16.h>
@@ -42,11 +42,11 @@ struct LoraArgs {
   int64_t wc, wj, ws;
   int L, rank;
   bool use_scaling;         // f includes scaling[l]
-  // tensor-core kernels: rows of P, of W and of base and O in whole, aligned 16-byte vectors (element by element otherwise); wgrad: O
-  // aligned to them
+  // tensor-core kernels: rows of P, of W and of base and O in whole, aligned 16-byte vectors (element by element
+  // otherwise); wgrad: O aligned to them
   bool pvec, wvec, yvec;
-  // Tensor-core reduce: the largest magnitude that each CTA of a tile wrote to V (most) and found in V2 (most2), kLoraMostPer slots
-  // per tile; null: not wanted
+  // Tensor-core reduce: the largest magnitude that each CTA of a tile wrote to V (most) and found in V2 (most2),
+  // kLoraMostPer slots per tile; null: not wanted
   const float* V2;
   float* most;
   float* most2;
@@ -101,8 +101,8 @@ __device__ __forceinline__ bool drop_keeps(const uint4& w, int e, uint32_t thr) 
   return ((e & 1) ? word : word << 16) >= thr << 16;  // thr <= 65535
 }
 
-// Eight 16-bit elements of a group with the dropped ones zero.  (Comparing whole words decides the high halves, shifted ones the low
-// halves: 32 cycles of a warp beside the generator's 115; the packed 16-bit comparison takes 45.)
+// Eight 16-bit elements of a group with the dropped ones zero.  (Comparing whole words decides the high halves,
+// shifted ones the low halves: 32 cycles of a warp beside the generator's 115; the packed 16-bit comparison takes 45.)
 __device__ __forceinline__ uint32_t drop_word16(uint32_t x, uint32_t bits, uint32_t thr) {
   const uint32_t t = thr << 16;
   if (bits < t) x &= 0x0000FFFFu;
@@ -296,8 +296,8 @@ static cudaError_t lora_generic_wgrad(bool bf16, const LoraArgs& a, cudaStream_t
 // ---------------------------------------------------------------------------------------------
 constexpr int kDropThreads = 256;
 
-// Whole, aligned groups: a thread per group of eight columns.  16384 x 4096 in bf16: 48 us, 0.85 of the copy rate; with two groups per
-// thread in flight 54.
+// Whole, aligned groups: a thread per group of eight columns.  16384 x 4096 in bf16: 48 us, 0.85 of the copy rate;
+// with two groups per thread in flight 54.
 template <typename T>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const T* x, T* out, const DropArgs d, int64_t total) {
   pdl_allow_dependents();
@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const T* x, T* ou
   }
 }
 
-// Any width and alignment: a warp per 256 columns of a row.  Each lane draws for one group, and the elements are taken in the order
-// of memory, their truth values from the lane that drew them.
+// Any width and alignment: a warp per 256 columns of a row.  Each lane draws for one group, and the elements are
+// taken in the order of memory, their truth values from the lane that drew them.
 template <typename T>
 __global__ void __launch_bounds__(kDropThreads)
     dropout_any_kernel(const T* x, T* out, const DropArgs d, int64_t M, int64_t K) {

@@ -64,8 +64,8 @@ int tq_lora_path(int64_t M, int64_t L, int64_t N, int64_t K, int rank, int dropo
   if (M < 0 || L < 1 || N < 0 || K < 1 || rank < 1) return TQ_ERR_SHAPE;
   if (M == 0 || N == 0) return TQ_PATH_GENERIC;
   if (dropout || !aligned || !lora_few_shape(M, N, K)) return TQ_PATH_PREFILL;
-  // DECODE reads an adapter's weights once per eight rows, PREFILL once per 128 and has two launches' worth of start and end.
-  // us of DECODE | PREFILL, rows spread over the adapters at random, fp16:
+  // DECODE reads an adapter's weights once per eight rows, PREFILL once per 128 and has two launches' worth of start
+  // and end. us of DECODE | PREFILL, rows spread over the adapters at random, fp16:
   //   rows x adapters         256 x 1      512 x 1      1024 x 1     256 x 64     1024 x 64     2048 x 64
   //   4096 -> 4096, 16         7 | 14      13 | 15      19 | 15      13 | 30       27 | 35       43 | 42
   //   4096 -> 14336, 16       11 | 15      20 | 17      33 | 26      23 | 60       44 | 71       71 | 81
@@ -121,7 +121,8 @@ size_t tq_lora_workspace_size(int64_t M, int64_t L, int rank) {
 
 int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, const void* b, const float* scaling,
                      const float* v, void* workspace, size_t workspace_bytes, const void* base_dx, void* dx, void* da,
-                     void* db, const int32_t* offsets, const int32_t* order, double p, const int64_t* rng, int64_t M, int64_t L,
+                     void* db, const int32_t* offsets, const int32_t* order, double p, const int64_t* rng,
+                     int64_t M, int64_t L,
                      int64_t N, int64_t K, int rank, int path, void* stream) {
   tq::DropArgs drop;
   const int st = check_lora(dtype, M, L, N, K, rank, path, p, rng, &drop);

@@ -1,12 +1,13 @@
-// tq_lora_fast.cu -- low-rank adapters (include/tq_lora.h): the sums over many rows (reduce, wgrad and expand on tcgen05, with
-// 16-byte accesses where rows are made of whole vectors and element by element otherwise) and the single launch for few rows.
+// tq_lora_fast.cu -- low-rank adapters (include/tq_lora.h): the sums over many rows (reduce, wgrad and expand on
+// tcgen05, with 16-byte accesses where rows are made of whole vectors and element by element otherwise) and the
+// single launch for few rows.
 //
 // Work is cut by adapter: a tile is up to 128 sorted positions of one adapter, found on the device from
 // the offsets, so that one captured graph serves any plan.
 //
-// v and dv are fp32.  As operands of a 16-bit product they are split, v s = hi + lo with hi = round(v s), lo = round(v s - hi) and s
-// a power of two (fp16 only: bf16 has the exponents of fp32), which keeps 22 (fp16) or 16 (bf16) bits; hi and lo enter the
-// same fp32 sum, and 1 / s is applied to it, exactly.
+// v and dv are fp32.  As operands of a 16-bit product they are split, v s = hi + lo with hi = round(v s), lo =
+// round(v s - hi) and s a power of two (fp16 only: bf16 has the exponents of fp32), which keeps 22 (fp16) or 16
+// (bf16) bits; hi and lo enter the same fp32 sum, and 1 / s is applied to it, exactly.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,7 +39,8 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
 
 // cp_async_16 to a shared-memory address.
 __device__ __forceinline__ void cp_async_16s(uint32_t smem_dst, const void* gmem_src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gmem_src), "r"(src_bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gmem_src), "r"(src_bytes)
+               : "memory");
 }
 
 template <typename T>
@@ -49,7 +51,8 @@ __device__ __forceinline__ uint32_t pack2(T a, T b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Two fp32 numbers, already scaled, as hi and lo pairs.  What is not finite has no lo part (infinity less itself is NaN).
+// Two fp32 numbers, already scaled, as hi and lo pairs.  What is not finite has no lo part (infinity less itself is
+// NaN).
 template <typename T>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   const T ha = from_f32<T>(a), hb = from_f32<T>(b);
@@ -60,8 +63,8 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = pack2<T>(from_f32<T>(la), from_f32<T>(lb));
 }
 
-// The power of two that brings `most` to [2^14, 2^15) (fp16), so that the largest value fits and the smallest ones keep their bits; 1
-// for bf16, for zero and for what is not finite.  inv: its inverse.
+// The power of two that brings `most` to [2^14, 2^15) (fp16), so that the largest value fits and the smallest ones
+// keep their bits; 1 for bf16, for zero and for what is not finite.  inv: its inverse.
 template <typename T>
 __device__ __forceinline__ float split_scale(float most, float& inv) {
   inv = 1.0f;
@@ -72,8 +75,8 @@ __device__ __forceinline__ float split_scale(float most, float& inv) {
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
-// Eight consecutive 16-bit elements of which `left` are there (zero past them), one by one; out of line, since what runs beside it
-// is slower for the code.
+// Eight consecutive 16-bit elements of which `left` are there (zero past them), one by one; out of line, since what
+// runs beside it is slower for the code.
 __device__ __noinline__ uint4 load8_any(const uint16_t* p, int64_t left) {
   uint16_t h[8];
 #pragma unroll
@@ -90,9 +93,9 @@ __device__ __forceinline__ uint4 load8(const void* row, int64_t c, int64_t width
 }
 
 // ---------------------------------------------------------------------------------------------
-// Tiles.  Tile t of a plan: the tiles of adapter 0, of adapter 1, ..., then those of the positions of no adapter (l = -1),
-// which are counted on from the ones before offsets[0] to the ones from offsets[L] on.  Run by a whole warp, all of
-// whose lanes get the result.  A plan has at most lora_max_tiles(); kTile positions each.
+// Tiles.  Tile t of a plan: the tiles of adapter 0, of adapter 1, ..., then those of the positions of no adapter (l =
+// -1), which are counted on from the ones before offsets[0] to the ones from offsets[L] on.  Run by a whole warp, all
+// of whose lanes get the result.  A plan has at most lora_max_tiles(); kTile positions each.
 // ---------------------------------------------------------------------------------------------
 struct LoraTile {
   int l;        // adapter, -1: none, -2: past the last tile
@@ -194,17 +197,18 @@ static cudaError_t with_rank(int rank, F fn) {
 // ---------------------------------------------------------------------------------------------
 // reduce and wgrad on tcgen05: D (128 x up to 256 fp32, tensor memory) += A B^T over stages in shared memory.
 //   reduce  D[position, j]  A: the tile's rows of P, 128 x 128 columns (K-major; 64 columns for ranks above 64)
-//                           B: W, as A [rank, C] those columns of each j (K-major), as B [C, rank] those rows (MN-major)
-//   wgrad   D[c, j]         A: 64 rows x 128 columns of P (MN-major)
+//                           B: W, as A [rank, C] those columns of each j (K-major), as B [C, rank] those rows
+//   (MN-major) wgrad   D[c, j]         A: 64 rows x 128 columns of P (MN-major)
 //                           B: 64 rows of V, hi and lo side by side (MN-major); their sums are added at the end
-// Both read P once and little else, so HBM bounds them (2 rank FLOPs per element of P leave the tensor pipe idle most of the
-// time).  P is fetched row by row through `order` with 16-byte cp.async (a row's 128 or 256 bytes are consecutive lanes), which
-// zero-fills too and needs no tensor map, by sixteen loader warps: with eight, or with three times the
-// instructions per stage, the latency of a warp's own instructions set the pace, not memory.  With dropout each thread masks what it copied before it
-// hands the stage on.
-// The summation (columns, rows) is split over a cluster of S CTAs while tiles leave SMs idle; partial sums go through distributed
-// shared memory and are added in rank order.
-// One CTA per SM (its shared memory keeps every other kernel with tensor memory out), so that none waits for tensor memory that a
+// Both read P once and little else, so HBM bounds them (2 rank FLOPs per element of P leave the tensor pipe idle most
+// of the time).  P is fetched row by row through `order` with 16-byte cp.async (a row's 128 or 256 bytes are
+// consecutive lanes), which zero-fills too and needs no tensor map, by sixteen loader warps: with eight, or with
+// three times the instructions per stage, the latency of a warp's own instructions set the pace, not memory.  With
+// dropout each thread masks what it copied before it hands the stage on.
+// The summation (columns, rows) is split over a cluster of S CTAs while tiles leave SMs idle; partial sums go through
+// distributed shared memory and are added in rank order.
+// One CTA per SM (its shared memory keeps every other kernel with tensor memory out), so that none waits for tensor
+// memory that a
 // CTA holds which itself waits for a cluster.
 // ---------------------------------------------------------------------------------------------
 constexpr int kLtcWarps = 16;  // loaders
@@ -240,8 +244,9 @@ struct LoraTcLayout {
   static_assert(128 * (RP + 8) * 4 <= kRing * kStage, "partial sums fit");
 };
 
-// Shared-memory descriptor of an MN-major operand, 128-byte swizzle: planes of 64 elements along M / N, `plane` bytes apart (leading
-// byte offset), each of 128-byte rows of one k, groups of eight rows 1024 bytes apart (stride byte offset).
+// Shared-memory descriptor of an MN-major operand, 128-byte swizzle: planes of 64 elements along M / N, `plane` bytes
+// apart (leading byte offset), each of 128-byte rows of one k, groups of eight rows 1024 bytes apart (stride byte
+// offset).
 __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t smem_addr, uint32_t plane) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
@@ -263,7 +268,8 @@ template <typename T, int kMode, int RP, bool kDrop, bool kVec>
 __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs a, const int S) {
   using L = LoraTcLayout<kMode, RP>;
   constexpr bool kW = kMode == kWgrad;
-  const bool pvec = kVec || a.pvec, wvec = kVec || a.wvec, yvec = kVec || a.yvec, drop = kDrop && (kVec || a.drop.thr != 0);
+  const bool pvec = kVec || a.pvec, wvec = kVec || a.wvec, yvec = kVec || a.yvec;
+  const bool drop = kDrop && (kVec || a.drop.thr != 0);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
@@ -275,8 +281,8 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.z);
-  // wgrad follows kernels of the same call, which let it start only after the work before the call had finished: all but Q and inv may
-  // be read before the wait.
+  // wgrad follows kernels of the same call, which let it start only after the work before the call had finished: all
+  // but Q and inv may be read before the wait.
   if (!kW || !a.behind) pdl_wait_prior_grids();
 
   // the work of this cluster: positions [pos0, pos0 + cnt) of adapter l; columns from c0 (wgrad); stages [s0, s0 + ns)
@@ -340,8 +346,8 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
     const uint32_t pdst = (pch >> 3) * (kW ? 8192 : 16384) + prow * 128 + (((pch & 7) ^ (prow & 7)) << 4);
     const uint32_t ring0 = smem_u32(sm), ring1 = ring0 + L::kRing * L::kStage;
     int64_t c = kW ? c0 + 8 * pch : static_cast<int64_t>(s0) * 64 * L::kSub + 8 * pch;  // this thread's column
-    // reduce: each chunk's address in the first stage (nothing is copied for a position without a row: its sums are not used, and no
-    // other sum reads what the stage holds for it)
+    // reduce: each chunk's address in the first stage (nothing is copied for a position without a row: its sums are
+    // not used, and no other sum reads what the stage holds for it)
     const uint16_t* src[kW ? 1 : L::kPer];
     int m[L::kPer];
     if (!kW) {
@@ -387,7 +393,8 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
         ch = q % kRowChunks;
         wsize[k] = mine && (kW || 8 * ch < a.rank) ? 16u : 0u;
         wrow[k] = row;
-        wsrc[k] = kW ? static_cast<const uint16_t*>(a.Q) + (pos0 + static_cast<int64_t>(s0) * 64 + row) * (2 * RP) + 8 * ch
+        wsrc[k] = kW ? static_cast<const uint16_t*>(a.Q) +
+                           (pos0 + static_cast<int64_t>(s0) * 64 + row) * (2 * RP) + 8 * ch
                      : static_cast<const uint16_t*>(a.W) + l * a.ws +
                            (static_cast<int64_t>(s0) * 64 * L::kSub + row) * a.rank + 8 * ch;
       }
@@ -505,9 +512,8 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
     for (int i = 0; i < ns && ok; ++i) {
       ok = mbar_wait(&full[s], parity);
       if (!ok) break;
-      // The stage was written by other threads' cp.async and stores, ordered before this point by the barrier.  The fence that makes
-      // it visible to the tensor core is here, not in the loaders: there it also waits for the thread's copies in
-      // flight, and each stage then takes a whole memory latency (wgrad of 8192 x 4096, rank 64: 38 us).
+      // The stage was written by other threads' cp.async and stores, which the barrier orders before this point; the
+      // fence makes them visible to the tensor core, once a stage instead of once a loader.
       fence_proxy_async_smem();
       tc_fence_after_sync();
       const uint32_t pa = base + s * L::kStage, wa = pa + L::kTileP;
@@ -651,8 +657,9 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
   }
 }
 
-// V [M, rank] fp32 -> hi and lo [M, 2 RP] (zeros past the rank), scaled by the adapter's power of two, whose inverse goes to inv[l]:
-// once for all columns of wgrad, which would repeat it for each 128 of them.  A CTA per tile; grid y: v and dv.
+// V [M, rank] fp32 -> hi and lo [M, 2 RP] (zeros past the rank), scaled by the adapter's power of two, whose inverse
+// goes to inv[l]: once for all columns of wgrad, which would repeat it for each 128 of them.  A CTA per tile; grid y:
+// v and dv.
 struct LoraSplitArgs {
   const float* V[2];
   const float* most[2];  // or null (bf16)
@@ -716,8 +723,8 @@ __global__ void __launch_bounds__(256) lora_split_kernel(const LoraSplitArgs a) 
   }
 }
 
-// Clusters of S CTAs that can be resident at once (a cluster lies in one GPC, so the GPCs bound them below SMs / S: on a B200 148, 74,
-// 45, 33, 26, 22, 15 and 15 for S = 1 .. 8), queried once per device and S.
+// Clusters of S CTAs that can be resident at once (a cluster lies in one GPC, so the GPCs bound them below SMs / S:
+// on a B200 148, 74, 45, 33, 26, 22, 15 and 15 for S = 1 .. 8), queried once per device and S.
 static int lora_cluster_capacity(const DeviceInfo& di, int S) {
   static std::atomic<int> cache[kPfMaxDevices][kLoraMostPer + 1];
   if (S == 1) return di.num_sms;
@@ -746,15 +753,16 @@ static int lora_cluster_capacity(const DeviceInfo& di, int S) {
   return n;
 }
 
-// CTAs per cluster for `tiles` tiles of `stages` stages: a wave costs a CTA its share of the stages, the time of about seven for its
-// start and end, and of three more for the exchange between CTAs.
+// CTAs per cluster for `tiles` tiles of `stages` stages: a wave costs a CTA its share of the stages, the time of
+// about seven for its start and end, and of three more for the exchange between CTAs.
 static int lora_split(int64_t tiles, int64_t stages) {
   const DeviceInfo di = current_device_info();
   int best = 1;
   double cost = 0.0;
   for (int S = 1; S <= kLoraMostPer && (S == 1 || S * 2 <= stages); ++S) {
     const int64_t cap = lora_cluster_capacity(di, S);
-    const double c = static_cast<double>((tiles + cap - 1) / cap) * (static_cast<double>(stages) / S + (S > 1 ? 10.0 : 7.0));
+    const double c = static_cast<double>((tiles + cap - 1) / cap) *
+                     (static_cast<double>(stages) / S + (S > 1 ? 10.0 : 7.0));
     if (S == 1 || c < 0.97 * cost) {
       cost = c;
       best = S;
@@ -821,7 +829,8 @@ static cudaError_t lora_fast_wgrad(bool bf16, const LoraArgs& a, cudaStream_t s)
   });
 }
 
-// Workspace of the gradients: dv fp32 [M, rank]; the tiles' maxima of v and of dv; the inverse scales; v and dv as hi and lo.
+// Workspace of the gradients: dv fp32 [M, rank]; the tiles' maxima of v and of dv; the inverse scales; v and dv as hi
+// and lo.
 struct LoraWorkspace {
   float* dv;
   float* most[2];
@@ -875,20 +884,24 @@ cudaError_t launch_lora_split(bool bf16, bool both, const LoraWorkspace& w, cons
 
 // ---------------------------------------------------------------------------------------------
 // expand on tcgen05: O[m, c] = base[m, c] + f sum_j V[r, j] W_l(c, j).
-//   D[position, c] (128 x 128, four buffers in tensor memory) = [hi | lo] of V (shared memory, K-major, kept for the CTA's whole range of
-//   columns) x W (four stages of 128 columns)
-// Bound by the rows of base and O, each touched once with 16-byte accesses straight between memory and the registers that hold the
-// sums.  Sixteen epilogue warps, each with 32 positions and 32 columns of a block, read D in the fragment layout of m16n8
-// (16x256b), which gives a lane columns 2 t, 2 t + 1 of each n8 tile; W's columns are dealt to four n8 tiles so that these are eight
-// consecutive ones: column c = 8 u + 2 j + e of a block of 32 is column 2 u + e of tile j.  base is requested two blocks ahead.
-// Four loader warps bring W: as B [C, rank] a column's 16-byte pieces with cp.async, as A [rank, C] through registers, since pairs
-// of columns part ways (4-byte cp.async took 78 cycles an instruction).  Only barriers of single stages tie the warps.
-// All tiles' blocks in a row are dealt to the CTAs, one per SM, in equal runs, which cross from tile to tile where they must: with a CTA
-// per tile and range of columns, SMs were idle for a third of the time (4096 rows, 6 adapters, rank 32, 18944 columns: 81 us).
-// mma.sync on the same fragments, two CTAs per SM, was bound by the MMA rate from rank 64 on (rank 128, 8192 x 8192: 150 us; this 93).
+//   D[position, c] (128 x 128, four buffers in tensor memory) = [hi | lo] of V (shared memory, K-major, kept for the
+//   CTA's whole range of columns) x W (four stages of 128 columns)
+// Bound by the rows of base and O, each touched once with 16-byte accesses straight between memory and the registers
+// that hold the sums.  Sixteen epilogue warps, each with 32 positions and 32 columns of a block, read D in the
+// fragment layout of m16n8 (16x256b), which gives a lane columns 2 t, 2 t + 1 of each n8 tile; W's columns are dealt
+// to four n8 tiles so that these are eight consecutive ones: column c = 8 u + 2 j + e of a block of 32 is column 2 u
+// + e of tile j.  base is requested two blocks ahead.
+// Four loader warps bring W: as B [C, rank] a column's 16-byte pieces with cp.async, as A [rank, C] through
+// registers, since pairs of columns part ways (4-byte cp.async took 78 cycles an instruction).  Only barriers of
+// single stages tie the warps.
+// All tiles' blocks in a row are dealt to the CTAs, one per SM, in equal runs, which cross from tile to tile where
+// they must: with a CTA per tile and range of columns, SMs were idle for a third of the time (4096 rows, 6 adapters,
+// rank 32, 18944 columns: 81 us). mma.sync on the same fragments, two CTAs per SM, was bound by the MMA rate from
+// rank 64 on (rank 128, 8192 x 8192, no base: 150 us; this 79, rank 64 72 and 50, rank 16 44 and 35, the rate of
+// plain writes).
 // ---------------------------------------------------------------------------------------------
 constexpr int kXpEpi = 16;     // epilogue warps
-constexpr int kXpLoad = 4;     // loader warps; the first also issues the MMAs (20 warps leave 96 registers a thread, 21 only 80)
+constexpr int kXpLoad = 4;     // loader warps; the first also issues the MMAs (20 warps: 96 registers a thread, 21: 80)
 constexpr int kXpThreads = 32 * (kXpEpi + kXpLoad);
 constexpr int kXpCols = 128;   // columns per block (MMA N)
 constexpr int kXpRing = 4;     // stages of W, and of D
@@ -933,12 +946,12 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
   float* rowf = reinterpret_cast<float*>(sm + L::kOffF);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // The preceding kernel is this call's reduction (or one behind it), which let this one start only after the work before the call
-  // had finished: everything but V may be read at once.
+  // The preceding kernel is this call's reduction (or one behind it), which let this one start only after the work
+  // before the call had finished: everything but V may be read at once.
   const int64_t nblk = (a.C + kXpCols - 1) / kXpCols, total = lora_tiles(a.offsets, a.L, a.M) * nblk;
   const int64_t run0 = total * blockIdx.x / gridDim.x, run1 = total * (blockIdx.x + 1) / gridDim.x;
   if (run0 == run1) {
-    pdl_wait_prior_grids();  // no CTA ends before the kernels ahead of it: the next one takes this grid's end for theirs
+    pdl_wait_prior_grids();  // no CTA ends before the kernels ahead of it: the next takes this grid's end for theirs
     return;
   }
   const T* base = static_cast<const T*>(a.base);
@@ -974,152 +987,159 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     uint32_t parity = 0u;
     bool waited = false;
     for (int64_t run = run0; run < run1 && ok;) {
-    const int64_t tn = run / nblk, c_begin = (run - tn * nblk) * kXpCols;
-    const int nb = static_cast<int>(run1 - run < nblk * (tn + 1) - run ? run1 - run : nblk * (tn + 1) - run);
-    const int64_t c_end = c_begin + static_cast<int64_t>(nb) * kXpCols < a.C ? c_begin + static_cast<int64_t>(nb) * kXpCols : a.C;
-    run += nb;
-    const LoraTile tile = lora_tile(a.offsets, a.L, a.M, static_cast<int>(tn));
-    if (tile.l < 0) {  // rows of no adapter: base alone
-      if (base == out) continue;
-      const int64_t head = clamp_pos(a.offsets[0], a.M), at = clamp_pos(a.offsets[a.L], a.M);
-      const int vecs = static_cast<int>((c_end - c_begin) >> 3);
-      for (int i = warp; i < tile.cnt; i += kXpEpi) {
-        const int64_t q = tile.pos + i, m = lora_row(a, q < head ? q : q - head + at);
-        if (m < 0) continue;
-        if (!yvec) {
-          for (int64_t c = c_begin + lane; c < c_end; c += 32)
-            out[m * a.C + c] = base ? base[m * a.C + c] : from_f32<T>(0.0f);
-          continue;
-        }
-        uint4* dst = reinterpret_cast<uint4*>(out + m * a.C + c_begin);
-        const uint4* src = reinterpret_cast<const uint4*>(base + m * a.C + c_begin);
-        for (int j = lane; j < vecs; j += 32 * kXpCopy) {  // all loads of a round before its stores
-          uint4 x[kXpCopy];
+      const int64_t tn = run / nblk, c_begin = (run - tn * nblk) * kXpCols;
+      const int nb = static_cast<int>(run1 - run < nblk * (tn + 1) - run ? run1 - run : nblk * (tn + 1) - run);
+      const int64_t c_stop = c_begin + static_cast<int64_t>(nb) * kXpCols, c_end = c_stop < a.C ? c_stop : a.C;
+      run += nb;
+      const LoraTile tile = lora_tile(a.offsets, a.L, a.M, static_cast<int>(tn));
+      if (tile.l < 0) {  // rows of no adapter: base alone
+        if (base == out) continue;
+        const int64_t head = clamp_pos(a.offsets[0], a.M), at = clamp_pos(a.offsets[a.L], a.M);
+        const int vecs = static_cast<int>((c_end - c_begin) >> 3);
+        for (int i = warp; i < tile.cnt; i += kXpEpi) {
+          const int64_t q = tile.pos + i, m = lora_row(a, q < head ? q : q - head + at);
+          if (m < 0) continue;
+          if (!yvec) {
+            for (int64_t c = c_begin + lane; c < c_end; c += 32)
+              out[m * a.C + c] = base ? base[m * a.C + c] : from_f32<T>(0.0f);
+            continue;
+          }
+          uint4* dst = reinterpret_cast<uint4*>(out + m * a.C + c_begin);
+          const uint4* src = reinterpret_cast<const uint4*>(base + m * a.C + c_begin);
+          for (int j = lane; j < vecs; j += 32 * kXpCopy) {  // all loads of a round before its stores
+            uint4 x[kXpCopy];
 #pragma unroll
-          for (int k = 0; k < kXpCopy; ++k)
-            x[k] = base && j + 32 * k < vecs ? src[j + 32 * k] : make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < kXpCopy; ++k)
+              x[k] = base && j + 32 * k < vecs ? src[j + 32 * k] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-          for (int k = 0; k < kXpCopy; ++k)
-            if (j + 32 * k < vecs) dst[j + 32 * k] = x[k];
+            for (int k = 0; k < kXpCopy; ++k)
+              if (j + 32 * k < vecs) dst[j + 32 * k] = x[k];
+          }
         }
+        continue;
       }
-      continue;
-    }
-    int m[4];  // rows of positions r0 + 8 i
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      m[i] = r0 + 8 * i < tile.cnt ? static_cast<int>(lora_row(a, tile.pos + r0 + 8 * i)) : -1;
-    int64_t c = c_begin + (warp >> 2) * 32 + 8 * t;  // this lane's eight columns
-    uint4 y[2][4];
-    auto load_base = [&](uint4 (&to)[4], int64_t at) {
+      int m[4];  // rows of positions r0 + 8 i
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        to[i] = base && m[i] >= 0 && at < c_end ? load8(base + static_cast<int64_t>(m[i]) * a.C, at, a.C, yvec)
-                                                : make_uint4(0u, 0u, 0u, 0u);
-    };
-    load_base(y[0], c);
-    load_base(y[1], c + kXpCols);
-    {
-      // V of the tile as hi and lo, four threads per position (the last run's MMAs have read theirs: this warp has seen their sums)
-      const int row = tid >> 2, part = tid & 3;
-      constexpr int kE = RP / 4;  // inner columns per thread
-      const bool there = row < tile.cnt;
-      const float* src = a.V + (tile.pos + row) * a.rank;
-      float most = 0.0f;
-      float v[kE];
-      if (!waited) pdl_wait_prior_grids();
-      waited = true;
-      if ((a.rank & 3) == 0) {
+        m[i] = r0 + 8 * i < tile.cnt ? static_cast<int>(lora_row(a, tile.pos + r0 + 8 * i)) : -1;
+      int64_t c = c_begin + (warp >> 2) * 32 + 8 * t;  // this lane's eight columns
+      uint4 y[2][4];
+      auto load_base = [&](uint4 (&to)[4], int64_t at) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          to[i] = base && m[i] >= 0 && at < c_end ? load8(base + static_cast<int64_t>(m[i]) * a.C, at, a.C, yvec)
+                                                  : make_uint4(0u, 0u, 0u, 0u);
+      };
+      load_base(y[0], c);
+      load_base(y[1], c + kXpCols);
+      {
+        // V of the tile as hi and lo, four threads per position (the last run's MMAs have read theirs: this warp has
+        // seen their sums)
+        const int row = tid >> 2, part = tid & 3;
+        constexpr int kE = RP / 4;  // inner columns per thread
+        const bool there = row < tile.cnt;
+        const float* src = a.V + (tile.pos + row) * a.rank;
+        float most = 0.0f;
+        float v[kE];
+        if (!waited) pdl_wait_prior_grids();
+        waited = true;
+        if ((a.rank & 3) == 0) {
+#pragma unroll
+          for (int e = 0; e < kE; e += 4) {
+            const int j = part * kE + e;
+            const float4 x = there && j < a.rank ? *reinterpret_cast<const float4*>(src + j)
+                                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            v[e] = x.x;
+            v[e + 1] = x.y;
+            v[e + 2] = x.z;
+            v[e + 3] = x.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) v[e] = there && part * kE + e < a.rank ? src[part * kE + e] : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < kE; ++e) most = fmaxf(most, fabsf(v[e]));
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+        float inv;
+        const float sc = split_scale<T>(most, inv);
 #pragma unroll
         for (int e = 0; e < kE; e += 4) {
-          const int j = part * kE + e;
-          const float4 x = there && j < a.rank ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          v[e] = x.x;
-          v[e + 1] = x.y;
-          v[e + 2] = x.z;
-          v[e + 3] = x.w;
+          uint2 hi, lo;
+          split2<T>(sc * v[e], sc * v[e + 1], hi.x, lo.x);
+          split2<T>(sc * v[e + 2], sc * v[e + 3], hi.y, lo.y);
+          const int kh = part * kE + e, kl = RP + kh;  // k of hi and of lo
+          auto at = [&](int k) {
+            return sm + (k >> 6) * 16384 + row * 128 + ((((k >> 3) & 7) ^ (row & 7)) << 4) + (k & 4) * 2;
+          };
+          *reinterpret_cast<uint2*>(at(kh)) = hi;
+          *reinterpret_cast<uint2*>(at(kl)) = lo;
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) v[e] = there && part * kE + e < a.rank ? src[part * kE + e] : 0.0f;
+        if (part == 0) rowf[(seg & 1) * 128 + row] = inv * lora_factor(a, tile.l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vfull);
       }
+      // rowf, of which there are two, since a warp may be done with a short run before another reads this one's
+      named_barrier_sync(1, 32 * kXpEpi);
+      float f[4];
 #pragma unroll
-      for (int e = 0; e < kE; ++e) most = fmaxf(most, fabsf(v[e]));
-      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-      float inv;
-      const float sc = split_scale<T>(most, inv);
+      for (int i = 0; i < 4; ++i) f[i] = rowf[(seg & 1) * 128 + r0 + 8 * i];
+      auto block = [&](uint4 (&yb)[4]) {
+        ok = ok && mbar_wait(&dfull[s], parity);
+        if (!ok) return;
+        tc_fence_after_sync();
+        const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + s * kXpCols + (warp >> 2) * 32;
 #pragma unroll
-      for (int e = 0; e < kE; e += 4) {
-        uint2 hi, lo;
-        split2<T>(sc * v[e], sc * v[e + 1], hi.x, lo.x);
-        split2<T>(sc * v[e + 2], sc * v[e + 3], hi.y, lo.y);
-        const int kh = part * kE + e, kl = RP + kh;  // k of hi and of lo
-        *reinterpret_cast<uint2*>(sm + (kh >> 6) * 16384 + row * 128 + ((((kh >> 3) & 7) ^ (row & 7)) << 4) + (kh & 4) * 2) = hi;
-        *reinterpret_cast<uint2*>(sm + (kl >> 6) * 16384 + row * 128 + ((((kl >> 3) & 7) ^ (row & 7)) << 4) + (kl & 4) * 2) = lo;
-      }
-      if (part == 0) rowf[(seg & 1) * 128 + row] = inv * lora_factor(a, tile.l);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(vfull);
-    }
-    named_barrier_sync(1, 32 * kXpEpi);  // rowf; two of them, since a warp may be done with a short run before another reads this one's
-    float f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = rowf[(seg & 1) * 128 + r0 + 8 * i];
-    auto block = [&](uint4 (&yb)[4]) {
-      ok = ok && mbar_wait(&dfull[s], parity);
-      if (!ok) return;
-      tc_fence_after_sync();
-      const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + s * kXpCols + (warp >> 2) * 32;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // positions r0 + 16 h and + 8
-        uint32_t acc[16];
-        tmem_ld_16x256b_x4(at + (static_cast<uint32_t>(16 * h) << 16), acc);
-        tmem_ld_wait();
-        if (h == 1) {
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&dempty[s]);
-        }
-        if (c >= c_end) continue;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (m[2 * h + i] < 0) continue;
-          const int64_t at_row = static_cast<int64_t>(m[2 * h + i]) * a.C + c;
-          Vec<T, 8> o = *reinterpret_cast<const Vec<T, 8>*>(&yb[2 * h + i]);
-          const uint4 bits = drop ? philox(m[2 * h + i] * groups + (c >> 3), key) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = __uint_as_float(acc[4 * (e >> 1) + 2 * i + (e & 1)]), z = to_f32(o.v[e]);
-            o.v[e] = from_f32<T>(drop && !drop_keeps(bits, e, a.drop.thr) ? z : fmaf(f[2 * h + i], x, z));
+        for (int h = 0; h < 2; ++h) {  // positions r0 + 16 h and + 8
+          uint32_t acc[16];
+          tmem_ld_16x256b_x4(at + (static_cast<uint32_t>(16 * h) << 16), acc);
+          tmem_ld_wait();
+          if (h == 1) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&dempty[s]);
           }
-          if (yvec) {
-            *reinterpret_cast<Vec<T, 8>*>(out + at_row) = o;
-          } else {
-            for (int e = 0; e < 8 && c + e < a.C; ++e) out[at_row + e] = o.v[e];
+          if (c >= c_end) continue;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (m[2 * h + i] < 0) continue;
+            const int64_t at_row = static_cast<int64_t>(m[2 * h + i]) * a.C + c;
+            Vec<T, 8> o = *reinterpret_cast<const Vec<T, 8>*>(&yb[2 * h + i]);
+            const uint4 bits = drop ? philox(m[2 * h + i] * groups + (c >> 3), key) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float x = __uint_as_float(acc[4 * (e >> 1) + 2 * i + (e & 1)]), z = to_f32(o.v[e]);
+              o.v[e] = from_f32<T>(drop && !drop_keeps(bits, e, a.drop.thr) ? z : fmaf(f[2 * h + i], x, z));
+            }
+            if (yvec) {
+              *reinterpret_cast<Vec<T, 8>*>(out + at_row) = o;
+            } else {
+              for (int e = 0; e < 8 && c + e < a.C; ++e) out[at_row + e] = o.v[e];
+            }
           }
         }
-      }
-      if (++s == kXpRing) {
-        s = 0;
-        parity ^= 1u;
-      }
-    };
-    for (int b = 0; b < nb && ok; b += 2) {
-      block(y[0]);
-      load_base(y[0], c + 2 * kXpCols);
-      c += kXpCols;
-      if (b + 1 < nb) {
-        block(y[1]);
-        load_base(y[1], c + 2 * kXpCols);
+        if (++s == kXpRing) {
+          s = 0;
+          parity ^= 1u;
+        }
+      };
+      for (int b = 0; b < nb && ok; b += 2) {
+        block(y[0]);
+        load_base(y[0], c + 2 * kXpCols);
         c += kXpCols;
+        if (b + 1 < nb) {
+          block(y[1]);
+          load_base(y[1], c + 2 * kXpCols);
+          c += kXpCols;
+        }
       }
-    }
-    ++seg;
+      ++seg;
     }
     if (!waited) pdl_wait_prior_grids();
   } else {
-    // ------------------------------------------------------------------ loaders of W; the first warp also issues the MMAs
+    // ------------------------------------------------------------------ loaders of W; the first warp also issues the
+    // MMAs
     const int w = tid - 32 * kXpEpi;  // 0 .. 127
     constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
     constexpr uint32_t kIdesc = idesc_f16_f32(128, kXpCols) | kType | (kWA ? 1u << 16 : 0u);
@@ -1128,102 +1148,104 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     uint32_t parity = 1u, hparity = 0u;
     int64_t done = 0;  // blocks requested in earlier runs
     for (int64_t run = run0; run < run1 && ok;) {
-    const int64_t tn = run / nblk, c_begin = (run - tn * nblk) * kXpCols;
-    const int nb = static_cast<int>(run1 - run < nblk * (tn + 1) - run ? run1 - run : nblk * (tn + 1) - run);
-    run += nb;
-    const LoraTile tile = lora_tile(a.offsets, a.L, a.M, static_cast<int>(tn));
-    if (tile.l < 0) continue;
-    const uint16_t* W = static_cast<const uint16_t*>(a.W) + tile.l * a.ws;
-    // A: chunk (row j = w / 16 + 8 i, eight columns from 8 (w % 16)) of a block, a block ahead in registers
-    constexpr int kPerA = kWA ? RP / 8 : 1;
-    uint4 pre[kPerA];
-    const int ach = w & 15, aj = w >> 4;
-    auto load_a = [&](int b) {
-      const int64_t at = c_begin + static_cast<int64_t>(b) * kXpCols + 8 * ach;
+      const int64_t tn = run / nblk, c_begin = (run - tn * nblk) * kXpCols;
+      const int nb = static_cast<int>(run1 - run < nblk * (tn + 1) - run ? run1 - run : nblk * (tn + 1) - run);
+      run += nb;
+      const LoraTile tile = lora_tile(a.offsets, a.L, a.M, static_cast<int>(tn));
+      if (tile.l < 0) continue;
+      const uint16_t* W = static_cast<const uint16_t*>(a.W) + tile.l * a.ws;
+      // A: chunk (row j = w / 16 + 8 i, eight columns from 8 (w % 16)) of a block, a block ahead in registers
+      constexpr int kPerA = kWA ? RP / 8 : 1;
+      uint4 pre[kPerA];
+      const int ach = w & 15, aj = w >> 4;
+      auto load_a = [&](int b) {
+        const int64_t at = c_begin + static_cast<int64_t>(b) * kXpCols + 8 * ach;
 #pragma unroll
-      for (int i = 0; i < kPerA; ++i)
-        pre[i] = at < a.C && aj + 8 * i < a.rank ? load8(W + (aj + 8 * i) * a.C, at, a.C, wvec) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    if (kWA) load_a(0);
-    for (int b = 0; b < nb + L::kLag && ok; ++b) {
-      if (b < nb) {
-        if (done + b >= kXpRing) {
-          ok = mbar_wait(&wempty[s], parity);
-          if (!ok) break;
-        }
-        uint8_t* st = sm + L::kOffW + s * L::kTileW;
-        if (kWA) {
-          // columns 8 u + 2 j + e of a block of 32 to 8 j + 2 u + e: piece j of the chunk to 16-byte chunk j of the block
-          const int hb = ach >> 2;
-          uint8_t* dst = st + (hb >> 1) * L::kPlaneW + aj * 128 + 4 * (ach & 3);
-#pragma unroll
-          for (int i = 0; i < kPerA; ++i) {
-            const uint32_t word[4] = {pre[i].x, pre[i].y, pre[i].z, pre[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint32_t*>(dst + i * 1024 + (((4 * (hb & 1) + j) ^ (aj & 7)) << 4)) = word[j];
+        for (int i = 0; i < kPerA; ++i)
+          pre[i] = at < a.C && aj + 8 * i < a.rank ? load8(W + (aj + 8 * i) * a.C, at, a.C, wvec)
+                                                   : make_uint4(0u, 0u, 0u, 0u);
+      };
+      if (kWA) load_a(0);
+      for (int b = 0; b < nb + L::kLag && ok; ++b) {
+        if (b < nb) {
+          if (done + b >= kXpRing) {
+            ok = mbar_wait(&wempty[s], parity);
+            if (!ok) break;
           }
-          if (b + 1 < nb) load_a(b + 1);
-        } else {
-          // column c of 128 to its place, RP / 8 pieces
-          const int64_t c0 = c_begin + static_cast<int64_t>(b) * kXpCols;
-          const int c = w, pos = (c & ~31) + 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3) + (c & 1);
-          const bool there = c0 + c < a.C;
-          const uint16_t* src = W + (there ? (c0 + c) * a.rank : 0);
+          uint8_t* st = sm + L::kOffW + s * L::kTileW;
+          if (kWA) {
+            // columns 8 u + 2 j + e of a block of 32 to 8 j + 2 u + e: piece j of the chunk to 16-byte chunk j of the
+            // block
+            const int hb = ach >> 2;
+            uint8_t* dst = st + (hb >> 1) * L::kPlaneW + aj * 128 + 4 * (ach & 3);
 #pragma unroll
-          for (int ch = 0; ch < RP / 8; ++ch) {
-            uint8_t* dst = st + (ch >> 3) * L::kPlaneW + pos * 128 + (((ch & 7) ^ (pos & 7)) << 4);
-            const bool in = there && 8 * ch < a.rank;
-            if (wvec)
-              cp_async_16(dst, in ? src + 8 * ch : W, in ? 16u : 0u);
-            else
-              *reinterpret_cast<uint4*>(dst) = in ? load8(src, 8 * ch, a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-        if (++s == kXpRing) {
-          s = 0;
-          parity ^= 1u;
-        }
-      }
-      if (!kWA) {
-        cp_async_commit();
-        if (b < L::kLag) continue;
-        cp_async_wait<L::kLag>();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&wfull[hs]);
-      if (warp == kXpEpi) {
-        // the MMAs of the block handed over: four buffers of D keep the epilogue busy while this warp waits
-        const int d = b - L::kLag;
-        ok = (d > 0 || mbar_wait(vfull, static_cast<uint32_t>(seg & 1))) && mbar_wait(&wfull[hs], hparity) &&
-             (done + d < kXpRing || mbar_wait(&dempty[hs], hparity ^ 1u));
-        if (!ok) break;
-        if (lane == 0) {
-          fence_proxy_async_smem();  // for the copies and stores of the other warps, which the barriers order before this point
-          tc_fence_after_sync();
-          const uint32_t wa = base_v + L::kOffW + hs * L::kTileW;
+            for (int i = 0; i < kPerA; ++i) {
+              const uint32_t word[4] = {pre[i].x, pre[i].y, pre[i].z, pre[i].w};
 #pragma unroll
-          for (int part = 0; part < 2; ++part)  // hi, lo
-#pragma unroll
-            for (int q = 0; q < RP / 16; ++q) {
-              const int kv = part * RP + 16 * q;
-              const uint64_t ad = sdesc_kmajor_sw128(base_v + (kv >> 6) * 16384) + 2 * ((kv & 63) >> 4);
-              const uint64_t bd = kWA ? sdesc_mnmajor_sw128(wa, L::kPlaneW) + 128 * q
-                                      : sdesc_kmajor_sw128(wa + (q >> 2) * L::kPlaneW) + 2 * (q & 3);
-              umma_f16(tmem + hs * kXpCols, ad, bd, kIdesc, (part | q) != 0 ? 1u : 0u);
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint32_t*>(dst + i * 1024 + (((4 * (hb & 1) + j) ^ (aj & 7)) << 4)) = word[j];
             }
-          umma_commit(&wempty[hs]);
-          umma_commit(&dfull[hs]);
+            if (b + 1 < nb) load_a(b + 1);
+          } else {
+            // column c of 128 to its place, RP / 8 pieces
+            const int64_t c0 = c_begin + static_cast<int64_t>(b) * kXpCols;
+            const int c = w, pos = (c & ~31) + 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3) + (c & 1);
+            const bool there = c0 + c < a.C;
+            const uint16_t* src = W + (there ? (c0 + c) * a.rank : 0);
+#pragma unroll
+            for (int ch = 0; ch < RP / 8; ++ch) {
+              uint8_t* dst = st + (ch >> 3) * L::kPlaneW + pos * 128 + (((ch & 7) ^ (pos & 7)) << 4);
+              const bool in = there && 8 * ch < a.rank;
+              if (wvec)
+                cp_async_16(dst, in ? src + 8 * ch : W, in ? 16u : 0u);
+              else
+                *reinterpret_cast<uint4*>(dst) = in ? load8(src, 8 * ch, a.rank, false) : make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          if (++s == kXpRing) {
+            s = 0;
+            parity ^= 1u;
+          }
+        }
+        if (!kWA) {
+          cp_async_commit();
+          if (b < L::kLag) continue;
+          cp_async_wait<L::kLag>();
         }
         __syncwarp();
+        if (lane == 0) mbar_arrive(&wfull[hs]);
+        if (warp == kXpEpi) {
+          // the MMAs of the block handed over: four buffers of D keep the epilogue busy while this warp waits
+          const int d = b - L::kLag;
+          ok = (d > 0 || mbar_wait(vfull, static_cast<uint32_t>(seg & 1))) && mbar_wait(&wfull[hs], hparity) &&
+               (done + d < kXpRing || mbar_wait(&dempty[hs], hparity ^ 1u));
+          if (!ok) break;
+          if (lane == 0) {
+            fence_proxy_async_smem();  // for the other warps' copies and stores, which the barriers order before this
+            tc_fence_after_sync();
+            const uint32_t wa = base_v + L::kOffW + hs * L::kTileW;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)  // hi, lo
+#pragma unroll
+              for (int q = 0; q < RP / 16; ++q) {
+                const int kv = part * RP + 16 * q;
+                const uint64_t ad = sdesc_kmajor_sw128(base_v + (kv >> 6) * 16384) + 2 * ((kv & 63) >> 4);
+                const uint64_t bd = kWA ? sdesc_mnmajor_sw128(wa, L::kPlaneW) + 128 * q
+                                        : sdesc_kmajor_sw128(wa + (q >> 2) * L::kPlaneW) + 2 * (q & 3);
+                umma_f16(tmem + hs * kXpCols, ad, bd, kIdesc, (part | q) != 0 ? 1u : 0u);
+              }
+            umma_commit(&wempty[hs]);
+            umma_commit(&dfull[hs]);
+          }
+          __syncwarp();
+        }
+        if (++hs == kXpRing) {
+          hs = 0;
+          hparity ^= 1u;
+        }
       }
-      if (++hs == kXpRing) {
-        hs = 0;
-        hparity ^= 1u;
-      }
-    }
-    done += nb;
-    ++seg;
+      done += nb;
+      ++seg;
     }
     cp_async_wait<0>();
   }
@@ -1238,7 +1260,8 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
 
 template <typename T, int RP, bool kWA, bool kDrop>
 static cudaError_t launch_lora_expand_tc(const LoraArgs& a, cudaStream_t s) {
-  auto* kern = a.wvec && a.yvec ? lora_expand_tc_kernel<T, RP, kWA, kDrop, true> : lora_expand_tc_kernel<T, RP, kWA, kWA, false>;
+  auto* kern = a.wvec && a.yvec ? lora_expand_tc_kernel<T, RP, kWA, kDrop, true>
+                                : lora_expand_tc_kernel<T, RP, kWA, kWA, false>;
   constexpr int kAlloc = LoraXpLayout<RP, kWA>::kAlloc;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kAlloc);
   if (e != cudaSuccess) return e;
@@ -1261,15 +1284,16 @@ static cudaError_t lora_fast_expand(bool bf16, const LoraArgs& a, cudaStream_t s
 }
 
 // ---------------------------------------------------------------------------------------------
-// Few rows: one launch.  A cluster of eight CTAs takes up to eight positions of one adapter: each CTA sums an eighth of the columns
-// of x (m16n8k16: 16 inner columns x 8 positions), the partial sums meet through distributed shared memory in rank order,
-// and each CTA then computes an eighth of the columns of out (16 x 8: 8 positions, rows 8 .. 15 unused, x 8 columns).
-// Bound by the latency of this chain and, with many adapters, by reading each one's A and B once from HBM.  So B does not wait for
-// the chain: 32 rows of B are one piece of memory, and each warp keeps the next two or three such blocks in flight into
-// shared memory of its own by bulk copies from the start on.  (B ahead in registers spilled; asked into L2 by prefetches, these
-// held up the warps that made them for up to 6 us.)
-// Within 32 k, lane t of a quad takes the eight consecutive k = 8 t .. 8 t + 7 (both operands the same, so the order within the sum
-// does not matter) in one 16-byte load.
+// Few rows: one launch.  A cluster of eight CTAs takes up to eight positions of one adapter: each CTA sums an eighth
+// of the columns of x (m16n8k16: 16 inner columns x 8 positions), the partial sums meet through distributed shared
+// memory in rank order, and each CTA then computes an eighth of the columns of out (16 x 8: 8 positions, rows 8 .. 15
+// unused, x 8 columns).
+// Bound by the latency of this chain and, with many adapters, by reading each one's A and B once from HBM.  So B does
+// not wait for the chain: 32 rows of B are one piece of memory, and each warp keeps the next two or three such blocks
+// in flight into shared memory of its own by bulk copies from the start on.  (B ahead in registers spilled; asked
+// into L2 by prefetches, these held up the warps that made them for up to 6 us.)
+// Within 32 k, lane t of a quad takes the eight consecutive k = 8 t .. 8 t + 7 (both operands the same, so the order
+// within the sum does not matter) in one 16-byte load.
 // ---------------------------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
@@ -1280,7 +1304,7 @@ template <int RP>
 struct LoraFewLayout {
   static constexpr int kSlots = RP <= 32 ? 3 : 2;       // blocks of B in flight per warp
   static constexpr int kSlot = 32 * RP * 2;
-  static constexpr int kOffRed = kFewWarps * kSlots * kSlot;             // partial sums of the warps [inner column][position]
+  static constexpr int kOffRed = kFewWarps * kSlots * kSlot;             // the warps' partial sums [column][position]
   static constexpr int kOffPart = kOffRed + kFewWarps * RP * kFewRows * 4;  // of the CTA
   static constexpr int kOffV = kOffPart + RP * kFewRows * 4;             // v [position][inner column]
   static constexpr int kOffBar = kOffV + RP * kFewRows * 4;
@@ -1329,7 +1353,8 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 16 ? 3 : (RP <= 64 ? 2 : 1)
   const int l = chunk.l, cnt = chunk.cnt;
   // columns of out of this CTA, in blocks of 32
   const int nblk = static_cast<int>((a.N + 31) / 32);
-  const int parts = kFewCluster * static_cast<int>(gridDim.z), part_id = static_cast<int>(blockIdx.z) * kFewCluster + rank;
+  const int parts = kFewCluster * static_cast<int>(gridDim.z);
+  const int part_id = static_cast<int>(blockIdx.z) * kFewCluster + rank;
   const int b0 = static_cast<int>(static_cast<int64_t>(part_id) * nblk / parts);
   const int b1 = static_cast<int>(static_cast<int64_t>(part_id + 1) * nblk / parts);
   auto row_of = [&](int64_t q) {
@@ -1362,9 +1387,11 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 16 ? 3 : (RP <= 64 ? 2 : 1)
     for (int i = 0; i < L::kSlots; ++i)
       if (b0 + warp + kFewWarps * i < b1) request(b0 + warp + kFewWarps * i, i);
 
-  // ---- an eighth of x A^T, groups of 32 columns dealt to the warps.  No load of A depends on a bound: where a row or column is past
-  // the end the address is one within the same matrix row, and what is read there meets a zero of x or goes to an unused sum.
-  const int K = static_cast<int>(a.K), ng = (K + 31) / 32, g0 = rank * ng / kFewCluster, g1 = (rank + 1) * ng / kFewCluster;
+  // ---- an eighth of x A^T, groups of 32 columns dealt to the warps.  No load of A depends on a bound: where a row
+  // or column is past the end the address is one within the same matrix row, and what is read there meets a zero of x
+  // or goes to an unused sum.
+  const int K = static_cast<int>(a.K), ng = (K + 31) / 32;
+  const int g0 = rank * ng / kFewCluster, g1 = (rank + 1) * ng / kFewCluster;
   {
     float acc[RT][4] = {};
     const T* xrow = static_cast<const T*>(a.x) + (m >= 0 ? m * a.K : 0);
@@ -1513,8 +1540,9 @@ constexpr int64_t kLoraFewMaxRows = 65535;
 
 cudaError_t launch_lora_few(bool bf16, const LoraFewArgs& a, cudaStream_t s) {
   const int64_t chunks = lora_max_tiles(a.M, a.L, kFewRows);
-  // Few chunks: several clusters each, which all sum x A^T and share the columns of out, while there are SMs for them and a warp has
-  // more than a block of columns (one row of rank 64, 4096 -> 14336: 12.5 us by one cluster, 7.7 by four).
+  // Few chunks: several clusters each, which all sum x A^T and share the columns of out, while there are SMs for them
+  // and a warp has more than a block of columns (one row of rank 64, 4096 -> 14336: 12.5 us by one cluster, 7.7 by
+  // four).
   int64_t q = current_device_info().num_sms / (kFewCluster * chunks);
   const int64_t most = (a.N + 32 * 64 - 1) / (32 * 64);
   q = q > most ? most : q;

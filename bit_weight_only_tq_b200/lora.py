@@ -20,7 +20,10 @@ import torch
 from . import HEADER, PATH_AUTO, PATH_DECODE, TQ_F16, _check, _i64, _int, _vp, header_functions, lib
 from .moe import TQ_BF16, _arg, _device, _dtype, _empty, _opt, _raw, _shape2
 
-__all__ = ["tq_lora", "tq_lora_backward", "tq_lora_path", "tq_lora_workspace_size", "tq_dropout", "tq_gemm_backward", "w4g_gemm_backward"]
+__all__ = [
+    "tq_lora", "tq_lora_backward", "tq_lora_path", "tq_lora_workspace_size", "tq_dropout", "tq_gemm_backward",
+    "w4g_gemm_backward",
+]
 
 LORA_HEADER = os.path.join(os.path.dirname(HEADER), "tq_lora.h")
 
@@ -29,7 +32,8 @@ _SIGS = {
     "tq_lora": [_vp, _int] + [_vp] * 8 + [_f64, _vp] + [_i64] * 4 + [_int, _int, _vp],
     "tq_lora_path": [_i64] * 4 + [_int] * 3,
     "tq_lora_workspace_size": [_i64, _i64, _int],
-    "tq_lora_backward": [_vp, _vp, _int] + [_vp] * 5 + [ctypes.c_size_t] + [_vp] * 6 + [_f64, _vp] + [_i64] * 4 + [_int, _int, _vp],
+    "tq_lora_backward": [_vp, _vp, _int] + [_vp] * 5 + [ctypes.c_size_t] + [_vp] * 6 + [_f64, _vp] + [_i64] * 4 +
+    [_int, _int, _vp],
     "tq_dropout": [_vp, _int, _vp, _f64, _vp, _i64, _i64, _vp],
     "tq_gemm_backward": [_vp] * 4 + [_i64] * 3 + [_int, _vp],
     "w4g_gemm_backward": [_vp] * 5 + [_i64] * 3 + [_int, _vp],
@@ -101,11 +105,12 @@ def tq_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, base, offsets: to
 
 def tq_lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, v: torch.Tensor, base_dx,
                      offsets: torch.Tensor, order=None, scaling=None, p: float = 0.0, rng=None, workspace=None,
-                     dx=None, da=None, db=None, need_dx: bool = True, need_ab: bool = True, path: int = PATH_AUTO, stream=None):
+                     dx=None, da=None, db=None, need_dx: bool = True, need_ab: bool = True, path: int = PATH_AUTO,
+                     stream=None):
     """Gradients of tq_lora from dy [M, N], the call's inputs and its v -> (dx [M, K], da like a, db like b), each None
     where it is not wanted.  dx is base_dx [M, K] (the projection's gradient for x; None: zeros) plus the adapters'
-    part and may be base_dx; an adapter without rows gets zeros.  workspace: uint8, tq_lora_workspace_size(M, L, rank) bytes
-    or more (allocated here when it is left out)."""
+    part and may be base_dx; an adapter without rows gets zeros.  workspace: uint8, at least
+    tq_lora_workspace_size(M, L, rank) bytes (allocated here when it is left out)."""
     dt, dev = _dtype16(x, "x"), _device()
     M, K, L, r, N = _adapters(x, a, b)
     d = x.dtype

@@ -21,7 +21,8 @@
  * The adapter of each row comes as a plan that all layers of a step share: tq_moe_sort of the rows'
  * adapter ids (a slot is a row here, top_k = 1) gives
  *   order    int32 [M]: the row at each sorted position, rows of adapter 0 first, or NULL: row = position;
- *   offsets  int32 [L + 1], non-decreasing, within [0, M]: adapter l has the positions offsets[l] .. offsets[l + 1] - 1.
+ *   offsets  int32 [L + 1], non-decreasing, within [0, M]: adapter l has the positions from offsets[l] to
+ *            offsets[l + 1] - 1.
  * Positions before offsets[0] and from offsets[L] on belong to no adapter: their rows get the base alone.
  * The rows that `order` names are distinct; an entry outside [0, M) names no row.
  *
@@ -67,8 +68,8 @@ extern "C" {
  *   path     TQ_PATH_AUTO, or one path (tests): DECODE takes few rows (one launch, up to 8 rows of an
  *            adapter per pass over its weights), PREFILL many (tensor cores), GENERIC is the plain form.
  *            DECODE needs p = 0, M <= 65535, K % 8 == 0 and N % 8 == 0 (TQ_ERR_PATH) and 16-byte aligned x, a, b, base,
- *            out and v (TQ_ERR_ALIGN).  PREFILL needs a 16-byte aligned v (TQ_ERR_ALIGN); widths that are multiples of 8
- *            and aligned tensors are read in whole vectors, others element by element.
+ *            out and v (TQ_ERR_ALIGN).  PREFILL needs a 16-byte aligned v (TQ_ERR_ALIGN); widths that are multiples
+ *            of 8 and aligned tensors are read in whole vectors, others element by element.
  *            Every path is right for any numbers of rows per adapter.
  * 1 <= L <= 1024, 1 <= rank <= 128, 0 < K, N <= 2^24 (N = 0: nothing), 0 <= M < 2^31.
  * M == 0 or N == 0: nothing is launched.
@@ -90,8 +91,8 @@ TQ_API int tq_lora_path(int64_t M, int64_t L, int64_t N, int64_t K, int rank, in
  *   db_l     = scaling[l] sum over its rows of dy[m]^T v[r]        [L, N, rank]
  *   (r: sorted position, m: its row).  An adapter without rows gets zeros.
  *   v        fp32 [M, rank], as tq_lora left it
- *   workspace  tq_lora_workspace_size() bytes or more (TQ_ERR_SHAPE), 16-byte aligned (TQ_ERR_ALIGN); nothing in it lasts
- *            from call to call.  Calls (or captured graphs) that may run at once need one each.
+ *   workspace  tq_lora_workspace_size() bytes or more (TQ_ERR_SHAPE), 16-byte aligned (TQ_ERR_ALIGN); nothing in it
+ *            lasts from call to call.  Calls (or captured graphs) that may run at once need one each.
  *   base_dx  [M, K], or NULL for zeros; may be `dx` (the projection's own gradient for x, to which this adds)
  *   dx, da, db  each may be NULL (not wanted).  None may overlap what the call reads (dx may be base_dx).
  *   path     AUTO, PREFILL (16-byte aligned v: TQ_ERR_ALIGN) or GENERIC.
@@ -99,8 +100,9 @@ TQ_API int tq_lora_path(int64_t M, int64_t L, int64_t N, int64_t K, int rank, in
  * ------------------------------------------------------------------------------------------ */
 TQ_API int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, const void* b,
                             const float* scaling, const float* v, void* workspace, size_t workspace_bytes,
-                            const void* base_dx, void* dx, void* da, void* db, const int32_t* offsets, const int32_t* order, double p, const int64_t* rng,
-                            int64_t M, int64_t L, int64_t N, int64_t K, int rank, int path, void* stream);
+                            const void* base_dx, void* dx, void* da, void* db, const int32_t* offsets,
+                            const int32_t* order, double p, const int64_t* rng, int64_t M, int64_t L, int64_t N,
+                            int64_t K, int rank, int path, void* stream);
 
 /* Bytes of workspace that tq_lora_backward needs (host arithmetic only; 0: invalid sizes). */
 TQ_API size_t tq_lora_workspace_size(int64_t M, int64_t L, int rank);
