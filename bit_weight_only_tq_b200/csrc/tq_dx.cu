@@ -33,8 +33,11 @@ struct DxArgs {
   const __half* sc;   // ternary [N]; W4A16 [N][K / 128]
   const uint8_t* zp;  // W4A16 zero-points [N][K / 128], or null (symmetric)
   __half* dx;
+  __half* rows;       // [M][dx_padded(N)] copies of dy's rows (tensor cores, rows that TMA cannot address), or null
   int64_t M, N, K;
 };
+
+inline int64_t dx_padded(int64_t N) { return (N + 7) / 8 * 8; }
 
 // ---------------------------------------------------------------------------------------------
 // Any shape and alignment: a thread per byte (ternary, four columns) or word (INT4, eight columns) of a
@@ -499,6 +502,24 @@ static cudaLaunchConfig_t dx_config(dim3 grid, cudaStream_t s, cudaLaunchAttribu
   return cfg;
 }
 
+// rows[m, 0 .. padded) = dy[m, 0 .. N), zeros: a warp per 256 elements.
+__global__ void __launch_bounds__(256) dx_rows_kernel(const __half* dy, __half* rows, int64_t M, int64_t N,
+                                                      int64_t padded) {
+  pdl_allow_dependents();
+  pdl_wait_prior_grids();
+  const int lane = threadIdx.x & 31;
+  const int64_t segments = (padded + 255) >> 8;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5; i < M * segments;
+       i += (static_cast<int64_t>(gridDim.x) * 256) >> 5) {
+    const int64_t m = i / segments, c0 = (i - m * segments) << 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t c = c0 + 32 * e + lane;
+      if (c < padded) rows[m * padded + c] = c < N ? dy[m * N + c] : __float2half_rn(0.0f);
+    }
+  }
+}
+
 // Clusters of S CTAs that can be resident at once, queried once per device and S; 0 when unknown.
 template <bool kInt4, int TN>
 static int dx_cluster_capacity(int device, int S) {
@@ -525,10 +546,17 @@ static cudaError_t launch_dx_tc(const DxArgs& a, cudaStream_t s) {
   auto* kern = dx_tc_kernel<kInt4, TN>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), L::kAlloc);
   if (e != cudaSuccess) return e;
+  const __half* dy = a.rows ? a.rows : a.dy;
+  const int64_t width = a.rows ? dx_padded(a.N) : a.N;
+  if (a.rows) {
+    e = launch_pdl(dx_rows_kernel, dim3(lora_grid((a.M * ((width + 255) >> 8) + 7) / 8, 16)), dim3(256), 0, 1, s, a.dy,
+                   a.rows, a.M, a.N, width);
+    if (e != cudaSuccess) return e;
+  }
   CUtensorMap td, tw;
   const uint64_t kbytes = static_cast<uint64_t>(a.K) / (kInt4 ? 2 : 4);
-  if (!make_tmap_2d(&td, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.dy, static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.M),
-                    static_cast<uint64_t>(a.N) * 2, kXN, TN, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!make_tmap_2d(&td, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dy, static_cast<uint64_t>(width), static_cast<uint64_t>(a.M),
+                    static_cast<uint64_t>(width) * 2, kXN, TN, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, kbytes, static_cast<uint64_t>(a.N), kbytes, L::kRowBytes,
                     kXTileN, kInt4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B))
     return cudaErrorInvalidValue;
@@ -560,7 +588,7 @@ static cudaError_t launch_dx_tc(const DxArgs& a, cudaStream_t s) {
 }
 
 bool dx_supported(int64_t M, int64_t N, int64_t K) {
-  return N > 0 && N % 8 == 0 && K % 64 == 0 && (M + 63) / 64 <= 65535;
+  return N > 0 && K % 64 == 0 && (M + 63) / 64 <= 65535;
 }
 
 // Tiles of 64, 128 or 256 tokens, as in the products: an MMA of fewer columns costs as much as one of 64.

@@ -141,7 +141,8 @@ int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, co
   const tq::LoraWorkspace w = tq::lora_workspace(workspace, M, L, rank);
   const bool tc = path != TQ_PATH_GENERIC;
   const bool scaled = tc && !bf16;  // the powers of two of v and dv are found on the way
-  if (M > 0 && (dx || da || scaled)) {
+  const bool reduced = M > 0 && (dx || da || scaled);
+  if (reduced) {
     tq::LoraArgs g = lora_sum(dy, b, false, N, rank, M, L, w.dv, scaling, offsets, order);
     if (scaled) {
       g.V2 = v;
@@ -167,7 +168,7 @@ int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, co
     g.drop = drop;
     g.Q = w.Q[1];
     g.inv = w.inv[1];
-    g.behind = M > 0;
+    g.behind = reduced;
     e = tq::launch_lora_wgrad(bf16, path, g, s);
   }
   if (e == cudaSuccess && db && N > 0) {
@@ -175,7 +176,7 @@ int tq_lora_backward(const void* dy, const void* x, int dtype, const void* a, co
     g.O = db;
     g.Q = w.Q[0];
     g.inv = w.inv[0];
-    g.behind = M > 0;
+    g.behind = reduced;
     e = tq::launch_lora_wgrad(bf16, path, g, s);
   }
   return to_status(e);
@@ -195,23 +196,26 @@ int tq_dropout(const void* x, int dtype, void* out, double p, const int64_t* rng
 namespace {
 
 int gemm_backward_impl(bool int4, const uint16_t* dy, const void* w, const uint16_t* sc, const uint8_t* zeros,
-                       uint16_t* dx, int64_t M, int64_t N, int64_t K, int path, void* stream) {
+                       uint16_t* dx, uint16_t* rows, int64_t M, int64_t N, int64_t K, int path, void* stream) {
   if (M < 0 || N < 0 || K <= 0 || M > (int64_t(1) << 31) || N > (int64_t(1) << 31) || K > (int64_t(1) << 28))
     return TQ_ERR_SHAPE;
   if (int4 && K % 128 != 0) return TQ_ERR_SHAPE;
   if (path < TQ_PATH_AUTO || path > TQ_PATH_GENERIC || path == TQ_PATH_DECODE) return TQ_ERR_PATH;
   if (M == 0) return TQ_OK;
   if (!dx || (N > 0 && (!dy || !w || !sc))) return TQ_ERR_NULL;
-  const bool al = aligned16(dy) && aligned16(w) && aligned16(dx);
-  const bool fits = tq::dx_supported(M, N, K);
+  const bool copied = N % 8 != 0 || !aligned16(dy);  // rows of dy that TMA cannot address
+  const bool al = aligned16(w) && aligned16(dx) && (!copied || aligned16(rows));
+  const bool fits = tq::dx_supported(M, N, K) && (!copied || rows);
   if (path == TQ_PATH_AUTO) {
     path = al && fits ? TQ_PATH_PREFILL : TQ_PATH_GENERIC;
   } else if (path == TQ_PATH_PREFILL) {
-    if (!fits) return TQ_ERR_PATH;
+    if (!tq::dx_supported(M, N, K)) return TQ_ERR_PATH;
+    if (copied && !rows) return TQ_ERR_NULL;
     if (!al) return TQ_ERR_ALIGN;
   }
   tq::DxArgs a = {};
   a.dy = reinterpret_cast<const __half*>(dy);
+  a.rows = copied ? reinterpret_cast<__half*>(rows) : nullptr;
   a.w = static_cast<const uint8_t*>(w);
   a.sc = reinterpret_cast<const __half*>(sc);
   a.zp = zeros;
@@ -226,14 +230,14 @@ int gemm_backward_impl(bool int4, const uint16_t* dy, const void* w, const uint1
 
 extern "C" {
 
-int tq_gemm_backward(const uint16_t* dy, const uint8_t* packed, const uint16_t* scale, uint16_t* dx, int64_t M,
-                     int64_t N, int64_t K, int path, void* stream) {
-  return gemm_backward_impl(false, dy, packed, scale, nullptr, dx, M, N, K, path, stream);
+int tq_gemm_backward(const uint16_t* dy, const uint8_t* packed, const uint16_t* scale, uint16_t* dx, uint16_t* rows,
+                     int64_t M, int64_t N, int64_t K, int path, void* stream) {
+  return gemm_backward_impl(false, dy, packed, scale, nullptr, dx, rows, M, N, K, path, stream);
 }
 
 int w4g_gemm_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales, const uint8_t* zeros,
-                      uint16_t* dx, int64_t M, int64_t N, int64_t K, int path, void* stream) {
-  return gemm_backward_impl(true, dy, qweight, scales, zeros, dx, M, N, K, path, stream);
+                      uint16_t* dx, uint16_t* rows, int64_t M, int64_t N, int64_t K, int path, void* stream) {
+  return gemm_backward_impl(true, dy, qweight, scales, zeros, dx, rows, M, N, K, path, stream);
 }
 
 }  // extern "C"

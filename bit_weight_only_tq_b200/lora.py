@@ -17,7 +17,7 @@ import os
 
 import torch
 
-from . import HEADER, PATH_AUTO, PATH_DECODE, TQ_F16, _check, _i64, _int, _vp, header_functions, lib
+from . import HEADER, PATH_AUTO, PATH_DECODE, PATH_GENERIC, TQ_F16, _check, _i64, _int, _vp, header_functions, lib
 from .moe import TQ_BF16, _arg, _device, _dtype, _empty, _opt, _raw, _shape2
 
 __all__ = [
@@ -35,8 +35,8 @@ _SIGS = {
     "tq_lora_backward": [_vp, _vp, _int] + [_vp] * 5 + [ctypes.c_size_t] + [_vp] * 6 + [_f64, _vp] + [_i64] * 4 +
     [_int, _int, _vp],
     "tq_dropout": [_vp, _int, _vp, _f64, _vp, _i64, _i64, _vp],
-    "tq_gemm_backward": [_vp] * 4 + [_i64] * 3 + [_int, _vp],
-    "w4g_gemm_backward": [_vp] * 5 + [_i64] * 3 + [_int, _vp],
+    "tq_gemm_backward": [_vp] * 5 + [_i64] * 3 + [_int, _vp],
+    "w4g_gemm_backward": [_vp] * 6 + [_i64] * 3 + [_int, _vp],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(lib, _name)
@@ -168,9 +168,20 @@ def tq_dropout(x: torch.Tensor, p: float, rng, out=None, stream=None) -> torch.T
     return out
 
 
+def _rows(dy, pd, M, N, K, path, rows, stream, dev):
+    """The address of the scratch where the tensor-core path copies rows that it cannot read in place, or None."""
+    if rows is None:
+        if N % 8 == 0 and pd & 15 == 0 or K % 64 or path == PATH_GENERIC:
+            return None
+        rows = _empty(dy, (M, (N + 7) // 8 * 8), torch.float16, stream)
+    return _arg(rows, "rows", torch.float16, (M, (N + 7) // 8 * 8), dev)
+
+
 def tq_gemm_backward(dy: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, K=None, dx=None,
-                     path: int = PATH_AUTO, stream=None) -> torch.Tensor:
-    """Gradient for x of tq_gemm: dx [M, K] = dy [M, N] What, fp16 (K: 4 packed.shape[1] unless given)."""
+                     path: int = PATH_AUTO, stream=None, rows=None) -> torch.Tensor:
+    """Gradient for x of tq_gemm: dx [M, K] = dy [M, N] What, fp16 (K: 4 packed.shape[1] unless given).  rows: fp16
+    [M, N rounded up to a multiple of 8] scratch for rows of dy that are no whole 16-byte vectors (allocated here when
+    it is needed)."""
     dev = _device()
     M, N = _shape2(dy, "dy")
     KB = _shape2(packed, "packed")[1]
@@ -180,14 +191,16 @@ def tq_gemm_backward(dy: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor
         dx = _empty(dy, (M, K), torch.float16, stream)
     _check(lib.tq_gemm_backward(pd, _arg(packed, "packed", torch.uint8, (N, (K + 3) // 4), dev),
                                 _arg(scale, "scale", torch.float16, (N,), dev),
-                                _arg(dx, "dx", torch.float16, (M, K), dev), M, N, K, int(path), _raw(stream, dev)),
-           "tq_gemm_backward")
+                                _arg(dx, "dx", torch.float16, (M, K), dev),
+                                _rows(dy, pd, M, N, K, path, rows, stream, dev), M, N, K, int(path),
+                                _raw(stream, dev)), "tq_gemm_backward")
     return dx
 
 
 def w4g_gemm_backward(dy: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros=None, dx=None,
-                      path: int = PATH_AUTO, stream=None) -> torch.Tensor:
-    """Gradient for x of w4g_gemm (zeros: of w4g_gemm_zp): dx [M, K] = dy [M, N] What, fp16."""
+                      path: int = PATH_AUTO, stream=None, rows=None) -> torch.Tensor:
+    """Gradient for x of w4g_gemm (zeros: of w4g_gemm_zp): dx [M, K] = dy [M, N] What, fp16.  rows: as in
+    tq_gemm_backward."""
     dev = _device()
     M, N = _shape2(dy, "dy")
     K = 8 * _shape2(qweight, "qweight")[1]
@@ -197,6 +210,7 @@ def w4g_gemm_backward(dy: torch.Tensor, qweight: torch.Tensor, scales: torch.Ten
     _check(lib.w4g_gemm_backward(pd, _arg(qweight, "qweight", torch.int32, (N, K // 8), dev),
                                  _arg(scales, "scales", torch.float16, (N, K // 128), dev),
                                  _opt(zeros, "zeros", torch.uint8, (N, K // 128), dev),
-                                 _arg(dx, "dx", torch.float16, (M, K), dev), M, N, K, int(path), _raw(stream, dev)),
-           "w4g_gemm_backward")
+                                 _arg(dx, "dx", torch.float16, (M, K), dev),
+                                 _rows(dy, pd, M, N, K, path, rows, stream, dev), M, N, K, int(path),
+                                 _raw(stream, dev)), "w4g_gemm_backward")
     return dx

@@ -121,16 +121,20 @@ TQ_API int tq_dropout(const void* x, int dtype, void* out, double p, const int64
  *   dy       fp16 [M, N]
  *   packed, scale / qweight, scales, zeros   as in the products (zeros NULL: symmetric)
  *   dx       fp16 [M, K], written in full.  Must not overlap dy.
+ *   rows     fp16 [M, N rounded up to a multiple of 8] scratch, 16-byte aligned, or NULL: PREFILL copies the rows of
+ *            dy there first where N % 8 != 0 or dy is not 16-byte aligned (without it: AUTO takes GENERIC, PREFILL
+ *            returns TQ_ERR_NULL).  Not read or written otherwise.  Calls that may run at once need one each.
  *   path     TQ_PATH_AUTO, PREFILL (tensor cores) or GENERIC (any shape and alignment; weights enter the sum
- *            exactly).  PREFILL needs K % 64 == 0, N % 8 == 0 (TQ_ERR_PATH), 16-byte aligned dy, weights and
- *            dx (TQ_ERR_ALIGN).  There a ternary weight enters exactly and an INT4 weight (u - z) s is rounded to fp16,
- *            as on that path of w4g_gemm (scales must keep it below 65520).
+ *            exactly).  PREFILL needs K % 64 == 0 (TQ_ERR_PATH) and 16-byte aligned weights and dx (TQ_ERR_ALIGN).
+ *            There a ternary weight enters exactly and an INT4 weight (u - z) s is rounded to fp16, as on that path
+ *            of w4g_gemm (scales must keep it below 65520).
  * Shapes and errors as in tq_gemm / w4g_gemm.
  * ------------------------------------------------------------------------------------------ */
-TQ_API int tq_gemm_backward(const uint16_t* dy, const uint8_t* packed, const uint16_t* scale, uint16_t* dx, int64_t M,
-                            int64_t N, int64_t K, int path, void* stream);
+TQ_API int tq_gemm_backward(const uint16_t* dy, const uint8_t* packed, const uint16_t* scale, uint16_t* dx,
+                            uint16_t* rows, int64_t M, int64_t N, int64_t K, int path, void* stream);
 TQ_API int w4g_gemm_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales, const uint8_t* zeros,
-                             uint16_t* dx, int64_t M, int64_t N, int64_t K, int path, void* stream);
+                             uint16_t* dx, uint16_t* rows, int64_t M, int64_t N, int64_t K, int path,
+                             void* stream);
 
 #ifdef __cplusplus
 }

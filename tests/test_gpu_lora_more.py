@@ -140,10 +140,14 @@ def test_gradient_for_x_ternary_odd_sizes(M, N, K):
     need_cuda()
     t, w64 = _weights(N, K, M + N, "ternary")
     dy = torch.randn(M, N, generator=_gen(K), device="cuda").half()
-    _dx_check(dy, w64, _backward(dy, t, "ternary", K), False)
-    if K % 64 or N % 8:
-        with pytest.raises(tq.TQError):
-            _backward(dy, t, "ternary", K, path=tq.PATH_PREFILL)
+    for path in (tq.PATH_AUTO, tq.PATH_GENERIC, tq.PATH_PREFILL):
+        if K % 64 and path == tq.PATH_PREFILL:
+            with pytest.raises(tq.TQError):
+                _backward(dy, t, "ternary", K, path=path)
+            continue
+        dx, buf = guarded_empty(M, K)
+        _dx_check(dy, w64, _backward(dy, t, "ternary", K, dx=dx, path=path), False)
+        check_canaries(buf, M, K)
 
 
 @pytest.mark.parametrize("fmt", ["ternary", "w4"])
@@ -153,9 +157,21 @@ def test_gradient_for_x_of_misaligned_rows(fmt):
     t, w64 = _weights(N, K, 1, fmt)
     buf = torch.randn(M * N + 1, generator=_gen(1), device="cuda").half()
     dy = buf[1:].view(M, N)
-    _dx_check(dy, w64, _backward(dy, t, fmt, K), False)
-    with pytest.raises(tq.TQError):
-        _backward(dy, t, fmt, K, path=tq.PATH_PREFILL)
+    _dx_check(dy, w64, _backward(dy, t, fmt, K, path=tq.PATH_GENERIC), False)
+    for path in (tq.PATH_AUTO, tq.PATH_PREFILL):
+        _dx_check(dy, w64, _backward(dy, t, fmt, K, path=path), fmt != "ternary")
+
+
+@pytest.mark.parametrize("fmt", ["w4", "w4z"])
+@pytest.mark.parametrize("M,N,K", [(70, 101, 256), (300, 1003, 384), (1, 9, 128)])
+def test_gradient_for_x_int4_odd_rows(fmt, M, N, K):
+    need_cuda()
+    t, w64 = _weights(N, K, M, fmt)
+    dy = torch.randn(M, N, generator=_gen(1), device="cuda").half()
+    rows = torch.full((M, (N + 7) // 8 * 8), float("nan"), dtype=torch.float16, device="cuda")
+    _dx_check(dy, w64, _backward(dy, t, fmt, K, path=tq.PATH_PREFILL, rows=rows), True)
+    with pytest.raises(ValueError, match="rows"):
+        _backward(dy, t, fmt, K, rows=rows[:, :-1].contiguous())
 
 
 def test_gradient_for_x_of_nothing():

@@ -90,11 +90,11 @@ def test_dropout_argument_errors():
 
 
 def test_gemm_backward_argument_errors():
-    def tern(dy=P, w=P, s=P, dx=P, M=4, N=64, K=64, path=0):
-        return tq.lib.tq_gemm_backward(dy, w, s, dx, M, N, K, path, None)
+    def tern(dy=P, w=P, s=P, dx=P, rows=None, M=4, N=64, K=64, path=0):
+        return tq.lib.tq_gemm_backward(dy, w, s, dx, rows, M, N, K, path, None)
 
-    def int4(dy=P, w=P, s=P, z=None, dx=P, M=4, N=64, K=128, path=0):
-        return tq.lib.w4g_gemm_backward(dy, w, s, z, dx, M, N, K, path, None)
+    def int4(dy=P, w=P, s=P, z=None, dx=P, rows=None, M=4, N=64, K=128, path=0):
+        return tq.lib.w4g_gemm_backward(dy, w, s, z, dx, rows, M, N, K, path, None)
 
     for f in (tern, int4):
         for bad in (dict(M=-1), dict(N=-1), dict(K=0), dict(M=2 ** 31 + 1), dict(N=2 ** 31 + 1), dict(K=2 ** 28 + 128)):
@@ -103,8 +103,9 @@ def test_gemm_backward_argument_errors():
             assert f(**{name: None}) == -1, name
         assert f(M=0, dy=None, dx=None) == 0
         assert f(path=4) == -8 and f(path=tq.PATH_DECODE) == -8
-        assert f(N=60, path=tq.PATH_PREFILL) == -8
-        for name in ("dy", "w", "dx"):
+        assert f(N=60, path=tq.PATH_PREFILL) == -1 and f(dy=Q, path=tq.PATH_PREFILL) == -1      # no room for copies
+        assert f(N=60, rows=Q, path=tq.PATH_PREFILL) == -3
+        for name in ("w", "dx"):
             assert f(**{name: Q}, path=tq.PATH_PREFILL) == -3, name
     assert int4(K=192) == -2 and tern(K=100, path=tq.PATH_PREFILL) == -8
 
