@@ -28,7 +28,9 @@
  *
  * Types: x, A, B, base, out, dy and the gradients have one dtype, TQ_F16 or TQ_BF16.  Sums are in fp32, v and dv
  * are kept in fp32, and every output is rounded once.  Where v and dv enter a tensor-core product, each is
- * the sum of two 16-bit numbers: 22 bits (fp16) or 16 bits (bf16) of it.
+ * the sum of two 16-bit numbers: 22 bits (fp16) or 16 bits (bf16) of it.  A tensor core cuts its fp32 sum off
+ * after every 16 products instead of rounding it: on PREFILL a sum of n products comes out smaller by up to about
+ * n 2^-29 of its value (v of 16384 columns: 2e-5; a split over CTAs divides that).
  *
  * Dropout: element e = k % 8 of the group i = m ceil(K / 8) + k / 8 of x [M, K] takes the 16 bits
  *   (e even: low half, odd: high half) of word e / 2 of Philox4x32-10 (Salmon, Moraes, Dror, Shaw: Parallel

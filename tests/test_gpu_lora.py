@@ -302,6 +302,20 @@ def test_backward_of_no_rows(path):
 
 
 @pytest.mark.parametrize("path", [ANY, TC])
+@pytest.mark.parametrize("dtype", [H, B])
+def test_no_output_columns(path, dtype):
+    """N = 0: nothing to write forward, the projection's part alone backward."""
+    need_cuda()
+    M, L, K, r = 20, 2, 64, 8
+    x, a, b, base, s, offsets, order = _case(M, L, K, 8, r, dtype, 8)
+    b, base = b[:, :0].contiguous(), base[:, :0].contiguous()
+    assert tq.tq_lora(x, a, b, base, offsets, order=order, scaling=s, path=path).shape == (M, 0)
+    v = torch.zeros(M, r, device="cuda")
+    dx, da, db = tq.tq_lora_backward(base, x, a, b, v, x, offsets, order=order, scaling=s, path=path)
+    assert torch.equal(dx, x) and not da.any() and db.shape == b.shape
+
+
+@pytest.mark.parametrize("path", [ANY, TC])
 def test_small_and_large_gradients(path):
     """dv far outside the range of fp16: it is scaled by powers of two where it enters a tensor-core product."""
     need_cuda()
