@@ -5,12 +5,12 @@
 // memory and dy the B operand:
 //   D[k, m] (TMEM, fp32) += A[k, n] (TMEM, fp16) * B[m, n]^T (smem, dy tile, K-major)
 // A TMEM lane holds one k and its columns hold pairs of n, while a packed word holds 8 (INT4) or 16 (ternary) k of
-// one n.  Eight (sixteen) lanes of a decode warp load the words of as many rows n and exchange them by a butterfly (three or
-// four shuffles, each followed by a byte permute or a shift and a mask), after which each lane's word holds its own k
-// for 8 (16) consecutive n, in order; it is then decoded as in the products.  That costs 8 instructions per 8 INT4
-// weights and 11 per 16 ternary ones, against a load per weight without the exchange, and no shared-memory traffic
-// beyond the packed bytes: a decoded tile in shared memory (MN-major, needing no exchange) would be written and read
-// again there, and shared memory already carries the dy tile twice at the tensor core's full rate.
+// one n.  Eight (sixteen) lanes of a decode warp load the words of as many rows n and exchange them by a butterfly
+// (three or four shuffles, each followed by a byte permute or a shift and a mask), after which each lane's word holds
+// its own k for 8 (16) consecutive n, in order; it is then decoded as in the products.  That costs 8 instructions per
+// 8 INT4 weights and 11 per 16 ternary ones, against a load per weight without the exchange, and no shared-memory
+// traffic beyond the packed bytes: a decoded tile in shared memory (MN-major, needing no exchange) would be written
+// and read again there, and shared memory already carries the dy tile twice at the tensor core's full rate.
 //
 // Scales run along n here, two per TMEM column: (c - 1) s is exact in fp16 (ternary); fp16((u - z) s) is one rounding
 // per INT4 weight, as in the products' tensor-core path.

@@ -197,7 +197,7 @@ static cudaError_t with_rank(int rank, F fn) {
 // ---------------------------------------------------------------------------------------------
 // reduce and wgrad on tcgen05: D (128 x up to 256 fp32, tensor memory) += A B^T over stages in shared memory.
 //   reduce  D[position, j]  A: the tile's rows of P, 128 x 128 columns (K-major; 64 columns for ranks above 64)
-//                           B: W, as A [rank, C] those columns of each j (K-major), as B [C, rank] those rows (MN-major)
+//                           B: W, as A [rank, C] those columns of each j (K-major), as B [C, rank] those rows (MN)
 //   wgrad   D[c, j]         A: 64 rows x 128 columns of P (MN-major)
 //                           B: 64 rows of V, hi and lo side by side (MN-major); their sums are added at the end
 // Both read P once and little else, so HBM bounds them (2 rank FLOPs per element of P leave the tensor pipe idle most
@@ -209,8 +209,8 @@ static cudaError_t with_rank(int rank, F fn) {
 // distributed shared memory and are added in rank order.
 // One CTA per SM (its shared memory keeps every other kernel with tensor memory out), so that none waits for tensor
 // memory that a CTA holds which itself waits for a cluster.
-// 8192 rows, rank 64, each kernel alone and cold: reduce of 8192 columns 34 us and of 2048 17 (6.1 TB/s between them, 12 us
-// of start and end; with dropout 2.3 times that slope: Philox), dv of 4096 23, wgrad of 4096 30, with dropout 44.
+// 8192 rows, rank 64, each kernel alone and cold: reduce of 8192 columns 34 us and of 2048 17 (6.1 TB/s between them,
+// 12 us of start and end; with dropout 2.3 times that slope: Philox), dv of 4096 23, wgrad of 4096 30, with dropout 44.
 // ---------------------------------------------------------------------------------------------
 constexpr int kLtcWarps = 16;  // loaders
 constexpr int kLtcLoaders = 32 * kLtcWarps;
@@ -264,11 +264,21 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
                : "r"(taddr));
 }
 
+// The sums of one launch: one, or both weight gradients (the same plan and rank), whose tiles of columns follow each
+// other.
+struct LoraSums {
+  LoraArgs a[2];
+  int first;  // wgrad: tiles of columns of a[0]
+};
+
 // kVec: all rows in whole, aligned vectors; without it kDrop is decided at run time where it is set.
 template <typename T, int kMode, int RP, bool kDrop, bool kVec>
-__global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs a, const int S) {
+__global__ void __launch_bounds__(kLtcThreads, 1)
+lora_tc_kernel(const __grid_constant__ LoraSums sums_of, const int S) {
   using L = LoraTcLayout<kMode, RP>;
   constexpr bool kW = kMode == kWgrad;
+  const bool second = kW && static_cast<int>(blockIdx.x) >= sums_of.first;
+  const LoraArgs& a = sums_of.a[second ? 1 : 0];
   const bool pvec = kVec || a.pvec, wvec = kVec || a.wvec, yvec = kVec || a.yvec;
   const bool drop = kDrop && (kVec || a.drop.thr != 0);
   extern __shared__ uint8_t smem_raw[];
@@ -300,7 +310,7 @@ __global__ void __launch_bounds__(kLtcThreads, 1) lora_tc_kernel(const LoraArgs 
     l = static_cast<int>(blockIdx.y);
     pos0 = clamp_pos(a.offsets[l], a.M);
     cnt = clamp_pos(a.offsets[l + 1], a.M) - pos0;
-    c0 = static_cast<int64_t>(blockIdx.x) * 128;
+    c0 = (static_cast<int64_t>(blockIdx.x) - (second ? sums_of.first : 0)) * 128;
     if (cnt <= 0) {  // no rows: zeros (the whole cluster returns)
       T* out = static_cast<T*>(a.O) + l * a.ws;
       if (rank == 0)
@@ -775,8 +785,9 @@ static int lora_split(int64_t tiles, int64_t stages) {
 static int lora_pad_rank(int64_t rank) { return rank <= 16 ? 16 : (rank <= 32 ? 32 : (rank <= 64 ? 64 : 128)); }
 
 template <typename T, int kMode, int RP, bool kDrop>
-static cudaError_t launch_lora_tc(const LoraArgs& a, dim3 grid, cudaStream_t s) {
-  const bool vec = a.pvec && (a.wvec || kMode == kWgrad) && (a.yvec || kMode != kWgrad);
+static cudaError_t launch_lora_tc(const LoraSums& sums, dim3 grid, cudaStream_t s) {
+  bool vec = true;
+  for (const LoraArgs& a : sums.a) vec = vec && a.pvec && (a.wvec || kMode == kWgrad) && (a.yvec || kMode != kWgrad);
   auto* kern = vec ? lora_tc_kernel<T, kMode, RP, kDrop, true> : lora_tc_kernel<T, kMode, RP, kMode != kReduceB, false>;
   constexpr int kAlloc = LoraTcLayout<kMode, RP>::kAlloc;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kAlloc);
@@ -795,7 +806,7 @@ static cudaError_t launch_lora_tc(const LoraArgs& a, dim3 grid, cudaStream_t s) 
   attr[1].val.clusterDim.z = grid.z;
   cfg.attrs = attr;
   cfg.numAttrs = grid.z > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, static_cast<int>(grid.z));
+  return cudaLaunchKernelEx(&cfg, kern, sums, static_cast<int>(grid.z));
 }
 
 // CTAs that reduce a tile together (the maxima of a tile have one slot for each).
@@ -804,28 +815,32 @@ static int lora_reduce_split(const LoraArgs& a) {
 }
 
 static cudaError_t lora_fast_reduce(bool bf16, const LoraArgs& a, cudaStream_t s) {
+  const LoraSums sums = {{a, a}, 0};
   const dim3 grid(static_cast<unsigned>(lora_max_tiles(a.M, a.L)), 1, static_cast<unsigned>(lora_reduce_split(a)));
   return with_type16(bf16, [&](auto t) {
     using T = decltype(t);
     return with_rank(a.rank, [&](auto rp) {
       constexpr int RP = decltype(rp)::value;
-      if (a.wc != 1) return launch_lora_tc<T, kReduceB, RP, false>(a, grid, s);
-      return a.drop.thr ? launch_lora_tc<T, kReduceA, RP, true>(a, grid, s)
-                        : launch_lora_tc<T, kReduceA, RP, false>(a, grid, s);
+      if (a.wc != 1) return launch_lora_tc<T, kReduceB, RP, false>(sums, grid, s);
+      return a.drop.thr ? launch_lora_tc<T, kReduceA, RP, true>(sums, grid, s)
+                        : launch_lora_tc<T, kReduceA, RP, false>(sums, grid, s);
     });
   });
 }
 
-static cudaError_t lora_fast_wgrad(bool bf16, const LoraArgs& a, cudaStream_t s) {
-  const int64_t ct = (a.C + 127) / 128, some = a.L < a.M ? a.L : (a.M < 1 ? 1 : a.M);
+// b: the other gradient in the same launch, or null.
+static cudaError_t lora_fast_wgrad(bool bf16, const LoraArgs& a, const LoraArgs* b, cudaStream_t s) {
+  const int64_t first = (a.C + 127) / 128, ct = first + (b ? (b->C + 127) / 128 : 0);
+  const LoraSums sums = {{a, b ? *b : a}, static_cast<int>(first)};
+  const int64_t some = a.L < a.M ? a.L : (a.M < 1 ? 1 : a.M);
   const int S = lora_split(ct * some, a.M / some / 64);
   const dim3 grid(static_cast<unsigned>(ct), static_cast<unsigned>(a.L), static_cast<unsigned>(S));
   return with_type16(bf16, [&](auto t) {
     using T = decltype(t);
     return with_rank(a.rank, [&](auto rp) {
       constexpr int RP = decltype(rp)::value;
-      return a.drop.thr ? launch_lora_tc<T, kWgrad, RP, true>(a, grid, s)
-                        : launch_lora_tc<T, kWgrad, RP, false>(a, grid, s);
+      return a.drop.thr ? launch_lora_tc<T, kWgrad, RP, true>(sums, grid, s)
+                        : launch_lora_tc<T, kWgrad, RP, false>(sums, grid, s);
     });
   });
 }
@@ -897,8 +912,8 @@ cudaError_t launch_lora_split(bool bf16, bool both, const LoraWorkspace& w, cons
 // single stages tie the warps.
 // All tiles' blocks in a row are dealt to the CTAs, one per SM, in equal runs, which cross from tile to tile where
 // they must: with a CTA per tile and range of columns, SMs were idle for a third of the time (4096 rows, 6 adapters,
-// rank 32, 18944 columns: 81 us, now 71).  mma.sync on the same fragments, two CTAs per SM, was bound by the MMA rate from
-// rank 64 on (rank 128, 8192 x 8192, no base: 150 us; this 79, rank 64 72 and 50, rank 16 44 and 35, the rate of
+// rank 32, 18944 columns: 81 us, now 71).  mma.sync on the same fragments, two CTAs per SM, was bound by the MMA rate
+// from rank 64 on (rank 128, 8192 x 8192, no base: 150 us; this 79, rank 64 72 and 50, rank 16 44 and 35, the rate of
 // plain writes).
 // ---------------------------------------------------------------------------------------------
 constexpr int kXpEpi = 16;     // epilogue warps
@@ -1293,8 +1308,8 @@ static cudaError_t lora_fast_expand(bool bf16, const LoraArgs& a, cudaStream_t s
 // not wait for the chain: 32 rows of B are one piece of memory, and each warp keeps the next two or three such blocks
 // in flight into shared memory of its own by bulk copies from the start on.  (B ahead in registers spilled; asked
 // into L2 by prefetches, these held up the warps that made them for up to 6 us.)
-// One row, rank 16, 4096 -> 4096: 4.5 us; 61 rows of 32 adapters of rank 64, 4096 -> 14336: 19 us for 66 MB (10 us at the
-// copy rate); 250 rows of 100 adapters of rank 8, 3584 -> 512: 11 us.
+// One row, rank 16, 4096 -> 4096: 4.5 us; 61 rows of 32 adapters of rank 64, 4096 -> 14336: 19 us for 66 MB (10 us at
+// the copy rate); 250 rows of 100 adapters of rank 8, 3584 -> 512: 11 us.
 // Within 32 k, lane t of a quad takes the eight consecutive k = 8 t .. 8 t + 7 (both operands the same, so the order
 // within the sum does not matter) in one 16-byte load.
 // ---------------------------------------------------------------------------------------------
@@ -1582,7 +1597,16 @@ cudaError_t launch_lora_expand(bool bf16, int path, const LoraArgs& a, cudaStrea
   return path == kLoraGeneric ? lora_generic_expand(bf16, a, s) : lora_fast_expand(bf16, lora_vectors(a), s);
 }
 cudaError_t launch_lora_wgrad(bool bf16, int path, const LoraArgs& a, cudaStream_t s) {
-  return path == kLoraGeneric ? lora_generic_wgrad(bf16, a, s) : lora_fast_wgrad(bf16, lora_vectors(a), s);
+  return path == kLoraGeneric ? lora_generic_wgrad(bf16, a, s) : lora_fast_wgrad(bf16, lora_vectors(a), nullptr, s);
+}
+// Both gradients of the weights, no dropout.
+cudaError_t launch_lora_wgrad_both(bool bf16, int path, const LoraArgs& a, const LoraArgs& b, cudaStream_t s) {
+  if (path == kLoraGeneric) {
+    const cudaError_t e = lora_generic_wgrad(bf16, a, s);
+    return e != cudaSuccess ? e : lora_generic_wgrad(bf16, b, s);
+  }
+  const LoraArgs other = lora_vectors(b);
+  return lora_fast_wgrad(bf16, lora_vectors(a), &other, s);
 }
 
 }  // namespace tq
