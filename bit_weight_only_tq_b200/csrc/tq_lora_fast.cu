@@ -411,6 +411,9 @@ lora_tc_kernel(const __grid_constant__ LoraSums sums_of, const int S) {
       }
       wdst[k] = L::kTileP + (ch >> 3) * L::kPlaneW + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
     }
+    // what a copy of zeros names: the start of the operand itself, since an address must be a multiple of 16 bytes
+    // whatever is read there, and P has only its type's alignment where pvec is false
+    const uint16_t* const wzero = static_cast<const uint16_t*>(kW ? a.Q : a.W);
     const int64_t wadvance = kMode == kReduceA ? 64 * L::kSub : (kW ? 64 * 2 * RP : 64 * L::kSub * a.rank);
     // summation indexes left from the current stage on (columns or positions)
     int64_t left = kW ? cnt - static_cast<int64_t>(s0) * 64 : a.C - static_cast<int64_t>(s0) * 64 * L::kSub;
@@ -448,7 +451,7 @@ lora_tc_kernel(const __grid_constant__ LoraSums sums_of, const int S) {
         if (L::kChunksW % kLtcLoaders != 0 && tid + kLtcLoaders * k >= L::kChunksW) continue;
         const uint32_t size = !kTail || wrow[k] < left ? wsize[k] : 0u;
         if (kW || wvec) {
-          cp_async_16s(st + wdst[k], size ? wsrc[k] : P, size);
+          cp_async_16s(st + wdst[k], size ? wsrc[k] : wzero, size);
         } else {  // from the row's start: wc0 columns (or inner columns) before this chunk
           const int64_t wc0 = kMode == kReduceA ? (static_cast<int64_t>(s0) + i) * 64 * L::kSub + wrow[k]
                                                 : 8 * ((tid + kLtcLoaders * k) % (RP / 8));
