@@ -113,7 +113,7 @@ static cudaError_t launch_dx_generic(bool int4, const DxArgs& a, cudaStream_t s)
 //   bytes (ternary) or 64 bytes (INT4) per tile, swizzled so that the decode warps' loads meet no (INT4) or two-way
 //   (ternary) bank conflicts; warp 3: the scales (and zero-points) of those 256 rows, as pairs; warp 1: tensor memory
 //   and the MMAs; warps 4-11: two groups of four decode warps on alternate stages.  All twelve run the epilogue.
-// Every wait is bounded, as in the products.
+// Every wait is bounded, as in the products; a whole warp's wait has one result (warp_wait).
 // 8192 x 14336 -> 4096 ternary: 680 us, 1414 TFLOP/s (tensor pipe 80 % busy, SM clock 1540 MHz at the power limit);
 // 4096 x 4096 -> 14336 INT4 with zero-points: 414 us, 1160 TFLOP/s (64 % busy: a stage's decode ends after its MMAs);
 // 61 x 1024 -> 4096 INT4: 8.4 us.  Four groups of decode warps (92 registers instead of 128) are 1 to 10 % slower.
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         zp[i] = kInt4 && a.zp && n < a.N ? static_cast<uint32_t>(a.zp[n * G + gi]) : 8u;
       }
       if (pt >= kXPRing) {
-        ok = mbar_wait_relaxed(&emptyP[s], static_cast<uint32_t>((pt / kXPRing) - 1) & 1u);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_relaxed(&emptyP[s], static_cast<uint32_t>((pt / kXPRing) - 1) & 1u)) != 0;
         if (!ok) break;
       }
       uint4* dst = reinterpret_cast<uint4*>(sm + L::kOffS + s * L::kTileS);
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     for (int i = dg; i < ns && ok; i += kXGroups) {
       const int s = i % L::kRing, pt = i / kXSPP, ci = i - pt * kXSPP, ps = pt % kXPRing;
       if (ci == dg) {  // this group's first stage of the packed tile
-        ok = mbar_wait(&fullP[ps], static_cast<uint32_t>(pt / kXPRing) & 1u);
+        ok = warp_wait(&fullP[ps], static_cast<uint32_t>(pt / kXPRing) & 1u);
         if (!ok) break;
       }
       constexpr int kWords = kInt4 ? 8 : 4;          // words per lane and stage, of 8 or 16 n each
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if (lane == 0) mbar_arrive(&emptyP[ps]);
       }
       if (i >= L::kRing) {
-        ok = mbar_wait(&empty[s], static_cast<uint32_t>((i / L::kRing) - 1) & 1u);
+        ok = warp_wait(&empty[s], static_cast<uint32_t>((i / L::kRing) - 1) & 1u);
         if (!ok) break;
         tc_fence_after_sync();
       }
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
     }
-    acc_flag = ok && mbar_wait(accFull, 0u);
+    acc_flag = ok && warp_wait(accFull, 0u);
   }
 
   // ------------------------------------------------------------------ epilogue (all warps)

@@ -43,6 +43,12 @@ __device__ __forceinline__ void cp_async_16s(uint32_t smem_dst, const void* gmem
                : "memory");
 }
 
+// A bounded wait by a whole warp, with one result for all its lanes: lanes that each went by a result of their own could
+// part before an instruction that takes the whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity)) != 0;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(T a, T b) {
   Vec<T, 2> v;
@@ -350,7 +356,10 @@ lora_tc_kernel(const __grid_constant__ LoraSums sums_of, const int S) {
   const uint16_t* P = static_cast<const uint16_t*>(a.P);
   float f = lora_factor(a, l);
 
-  bool ok = true;
+  // A wait that runs out is recorded, and whoever waited goes on with what there is, waits no more and comes to every
+  // barrier like the others: one that left the loop would leave them at a barrier for good, and lanes that went by
+  // results of their own would part before an instruction that takes the whole warp.
+  bool ok = !(warp == kLtcWarps && skip_x_loads());  // failure-path test hook (no MMA is issued), else true
   if (warp < kLtcWarps) {
     // ------------------------------------------------------------------ loaders
     const int prow = tid / L::kChunks, pch = tid % L::kChunks;  // chunk pch of rows prow + kStep k, k < kPer
@@ -488,13 +497,11 @@ lora_tc_kernel(const __grid_constant__ LoraSums sums_of, const int S) {
         // The set before last is not read any more: a warp is at most a ring ahead of another.
 #pragma unroll
         for (int k = 0; k < kRowPer; ++k) rowbuf[(i % (2 * kRowStages)) * 64 + tid + kLtcLoaders * k] = rnext[k];
+        __syncwarp();
         named_barrier_sync(1, kLtcLoaders);
       }
       if (kW && i % kRowStages == kRowStages / 2 && i + kRowStages / 2 < ns) fetch_rows(i + kRowStages / 2);
-      if (i >= L::kRing) {
-        ok = mbar_wait(release, parity);
-        if (!ok) break;
-      }
+      if (ok && i >= L::kRing) ok = mbar_wait(release, parity);
       if (left >= (kW ? 64 : 64 * L::kSub))
         request(std::false_type(), i, st);
       else
@@ -513,8 +520,8 @@ lora_tc_kernel(const __grid_constant__ LoraSums sums_of, const int S) {
       }
     }
     cp_async_wait<0>();
-    while (hd < ns && ok) hand_over();
-    if (ns > 0) ok = ok && mbar_wait(accFull, 0u);
+    while (hd < ns) hand_over();
+    if (ns > 0) ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(accFull, 0u)) != 0;
   } else if (lane == 0) {
     // ------------------------------------------------------------------ MMA issuer
     constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
@@ -996,7 +1003,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
   pdl_allow_dependents();
   const uint32_t tmem = *tmem_slot;
 
-  bool ok = true;
+  bool ok = !(warp == kXpEpi && skip_x_loads());  // as in lora_tc_kernel
   if (warp < kXpEpi) {
     // ------------------------------------------------------------------ epilogue
     const int g = lane >> 2, t = lane & 3, r0 = (warp & 3) * 32 + g;
@@ -1005,7 +1012,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     int s = 0, seg = 0;
     uint32_t parity = 0u;
     bool waited = false;
-    for (int64_t run = run0; run < run1 && ok;) {
+    for (int64_t run = run0; run < run1;) {
       const int64_t tn = run / nblk, c_begin = (run - tn * nblk) * kXpCols;
       const int nb = static_cast<int>(run1 - run < nblk * (tn + 1) - run ? run1 - run : nblk * (tn + 1) - run);
       const int64_t c_stop = c_begin + static_cast<int64_t>(nb) * kXpCols, c_end = c_stop < a.C ? c_stop : a.C;
@@ -1105,8 +1112,8 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = rowf[(seg & 1) * 128 + r0 + 8 * i];
       auto block = [&](uint4 (&yb)[4]) {
-        ok = ok && mbar_wait(&dfull[s], parity);
-        if (!ok) return;
+        ok = ok && mbar_wait(&dfull[s], parity);  // (a vote here costs registers that the bf16 kernels do not have)
+        __syncwarp();
         tc_fence_after_sync();
         const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + s * kXpCols + (warp >> 2) * 32;
 #pragma unroll
@@ -1119,7 +1126,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
             __syncwarp();
             if (lane == 0) mbar_arrive(&dempty[s]);
           }
-          if (c >= c_end) continue;
+          if (c >= c_end || !ok) continue;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (m[2 * h + i] < 0) continue;
@@ -1143,7 +1150,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
           parity ^= 1u;
         }
       };
-      for (int b = 0; b < nb && ok; b += 2) {
+      for (int b = 0; b < nb; b += 2) {
         block(y[0]);
         load_base(y[0], c + 2 * kXpCols);
         c += kXpCols;
@@ -1166,7 +1173,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     int s = 0, hs = 0, seg = 0;
     uint32_t parity = 1u, hparity = 0u;
     int64_t done = 0;  // blocks requested in earlier runs
-    for (int64_t run = run0; run < run1 && ok;) {
+    for (int64_t run = run0; run < run1;) {
       const int64_t tn = run / nblk, c_begin = (run - tn * nblk) * kXpCols;
       const int nb = static_cast<int>(run1 - run < nblk * (tn + 1) - run ? run1 - run : nblk * (tn + 1) - run);
       run += nb;
@@ -1185,12 +1192,9 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
                                                    : make_uint4(0u, 0u, 0u, 0u);
       };
       if (kWA) load_a(0);
-      for (int b = 0; b < nb + L::kLag && ok; ++b) {
+      for (int b = 0; b < nb + L::kLag; ++b) {
         if (b < nb) {
-          if (done + b >= kXpRing) {
-            ok = mbar_wait(&wempty[s], parity);
-            if (!ok) break;
-          }
+          if (ok && done + b >= kXpRing) ok = mbar_wait(&wempty[s], parity);
           uint8_t* st = sm + L::kOffW + s * L::kTileW;
           if (kWA) {
             // columns 8 u + 2 j + e of a block of 32 to 8 j + 2 u + e: piece j of the chunk to 16-byte chunk j of the
@@ -1236,10 +1240,9 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
         if (warp == kXpEpi) {
           // the MMAs of the block handed over: four buffers of D keep the epilogue busy while this warp waits
           const int d = b - L::kLag;
-          ok = (d > 0 || mbar_wait(vfull, static_cast<uint32_t>(seg & 1))) && mbar_wait(&wfull[hs], hparity) &&
+          ok = ok && (d > 0 || mbar_wait(vfull, static_cast<uint32_t>(seg & 1))) && mbar_wait(&wfull[hs], hparity) &&
                (done + d < kXpRing || mbar_wait(&dempty[hs], hparity ^ 1u));
-          if (!ok) break;
-          if (lane == 0) {
+          if (lane == 0 && ok) {
             fence_proxy_async_smem();  // for the other warps' copies and stores, which the barriers order before this
             tc_fence_after_sync();
             const uint32_t wa = base_v + L::kOffW + hs * L::kTileW;
@@ -1367,6 +1370,7 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 16 ? 3 : (RP <= 64 ? 2 : 1)
   __syncwarp();
   pdl_allow_dependents();
   pdl_wait_prior_grids();
+  const bool skip = skip_x_loads();  // failure-path test hook (no block of B is requested): never set in normal use
   const int rank = static_cast<int>(blockIdx.x);  // in the cluster
   const LoraTile chunk = lora_tile<kFewRows>(a.offsets, a.L, a.M, blockIdx.y);
   if (chunk.l == -2) return;  // (the whole cluster, as below)
@@ -1404,7 +1408,7 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 16 ? 3 : (RP <= 64 ? 2 : 1)
     mbar_arrive_expect_tx(&bars[s], bytes);
     bulk_load_1d(slots + s * L::kSlot, B + n0 * a.rank, bytes, &bars[s]);
   };
-  if (lane == 0)
+  if (lane == 0 && !skip)
     for (int i = 0; i < L::kSlots; ++i)
       if (b0 + warp + kFewWarps * i < b1) request(b0 + warp + kFewWarps * i, i);
 
@@ -1520,8 +1524,17 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 16 ? 3 : (RP <= 64 ? 2 : 1)
     const uint4 ycur = yv[0];
     yv[0] = yv[1];
     yv[1] = load_y(blk + kY * kFewWarps);
-    ok = mbar_wait(&bars[slot], parity);
-    if (!ok) break;
+    ok = warp_wait(&bars[slot], parity);
+    if (!ok) {  // (recorded) this copy and those requested ahead get one more bounded wait each before the CTA may end
+      for (int i = 0; i < L::kSlots && blk + kFewWarps * i < b1; ++i) {
+        (void)warp_wait(&bars[slot], parity);
+        if (++slot == L::kSlots) {
+          slot = 0;
+          parity ^= 1u;
+        }
+      }
+      break;
+    }
     float d[4][4] = {};
 #pragma unroll
     for (int q = 0; q < KG; ++q)

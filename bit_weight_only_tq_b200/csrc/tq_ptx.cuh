@@ -25,7 +25,8 @@ __device__ long long g_tq_wait_limit = kWaitLimitCycles;
 
 // Failure-path test hook (tq_debug_skip_activation_loads): when nonzero, the producers of the
 // GEMM kernels issue no activation (x) loads, so the stage barriers that count those bytes never
-// complete and the consumers' bounded waits run out.  Nothing in the library sets it.
+// complete and the consumers' bounded waits run out; the adapters' kernels issue no products or, for
+// few rows, request no block of B.  Nothing in the library sets it.
 __device__ int g_tq_skip_x_loads = 0;
 __device__ __forceinline__ bool skip_x_loads() { return *reinterpret_cast<volatile int*>(&g_tq_skip_x_loads) != 0; }
 

@@ -416,10 +416,12 @@ TQ_API int tq_device_status(void);
  * tq_debug_set_wait_limit -- every bounded wait (mbarrier polls of the GEMM kernels) gives up
  *   after `cycles` SM clock cycles instead of the default 4e9 (~2 s); cycles <= 0 restores the
  *   default.  A wait that gives up records TQ_ERR_TIMEOUT for tq_device_status(); the kernel
- *   then skips the rest of its work (its outputs are unspecified), frees what it holds and exits.
+ *   then skips the rest of its work or goes on without waiting (its outputs are unspecified),
+ *   frees what it holds and exits.
  * tq_debug_skip_activation_loads -- on != 0: the GEMM kernels' producers issue no activation
  *   (x) loads, so the stage barriers that count those bytes never complete and the consumers'
- *   waits run out; 0 restores normal operation.  Batch calls made while it is set leave their
+ *   waits run out (tq_lora.h's kernels: no products are issued, or no tile of dy or B is loaded);
+ *   0 restores normal operation.  Batch calls made while it is set leave their
  *   workspace counters untouched.
  * Returns TQ_OK or TQ_ERR_CUDA.
  * ------------------------------------------------------------------------------------------ */

@@ -1,18 +1,18 @@
-"""Adapters' calls at the edges of what they allow: operands of different alignment in one call, bounded waits that run out,
-non-finite numbers in the gradients, plans with foreign rows, long sums.  The bounds are in lora_util.py."""
-import numpy as np
+"""The adapters' calls and the products' gradient for x at the edges of what they allow: operands of different alignment in one
+call, bounded waits that run out."""
+import contextlib
+
 import pytest
 import torch
 
 import bit_weight_only_tq_b200 as tq
-import lora_util as O
 from gpu_util import gpu, need_cuda
-from test_gpu_lora import _backward64, _case, _forward64, _gen, _shifted
+from test_gpu_lora import _case, _gen, _shifted
+from test_gpu_lora_more import _backward, _weights
 
 pytestmark = gpu
-U, HALF, TINY, SPLIT = O.U, O.HALF, O.TINY, O.SPLIT
 H, B = torch.float16, torch.bfloat16
-ANY, TC, FEW = tq.PATH_GENERIC, tq.PATH_PREFILL, tq.PATH_DECODE
+TC, FEW = tq.PATH_PREFILL, tq.PATH_DECODE
 
 
 # ------------------------------------------------------------------------------------------ alignment
@@ -41,3 +41,69 @@ def test_some_operands_misaligned(moved, M, L, K, N, r, p):
                to("out", torch.empty_like(base)), to("out", torch.empty_like(x)))
     assert all(torch.equal(g, w) for g, w in zip(got, want))
     assert tq.tq_device_status() == 0
+
+
+# ------------------------------------------------------------------------------------------ waits
+@contextlib.contextmanager
+def _waits_run_out():
+    """The failure-path hooks: the adapters' kernels issue no products (few rows: no block of B is requested; the products'
+    gradient: no tile of dy is), so that every wait that depends on them gives up, after about a millisecond each.  No copy is
+    left in flight."""
+    assert tq.lib.tq_debug_set_wait_limit(2_000_000) == 0
+    assert tq.lib.tq_debug_skip_activation_loads(1) == 0
+    try:
+        yield
+    finally:
+        assert tq.lib.tq_debug_skip_activation_loads(0) == 0
+        assert tq.lib.tq_debug_set_wait_limit(0) == 0
+
+
+def _runs_out_then_recovers(run):
+    ref = [t.clone() for t in run()]
+    assert tq.tq_device_status() == 0
+    with _waits_run_out():
+        run()
+        assert tq.tq_device_status() == -6
+    assert tq.tq_device_status() == 0
+    assert all(torch.equal(g, w) for g, w in zip(run(), ref))
+    assert tq.tq_device_status() == 0
+
+
+# tiles of several sets of row indices (wgrad) and of several runs per CTA (expand); clusters of one and of several CTAs
+@pytest.mark.parametrize("M,L,K,N,r", [(40, 2, 4096, 512, 16), (5000, 3, 128, 384, 64), (3000, 1, 1000, 8200, 128),
+                                       (20000, 5, 1288, 264, 8)])
+@pytest.mark.parametrize("p", [0.0, 0.3])
+def test_waits_of_the_adapters_kernels_run_out(M, L, K, N, r, p):
+    """Warps whose waits ran out still come to every barrier: the call ends, says so once, and the next one is as before."""
+    need_cuda()
+    x, a, b, base, s, offsets, order = _case(M, L, K, N, r, H, M)
+    dy = 0.1 * base
+    rng = torch.tensor([1, 2], dtype=torch.int64, device="cuda")
+    v = torch.zeros(M, r, device="cuda")
+    kw = dict(order=order, scaling=s, p=p, rng=rng, path=TC)
+
+    def forward():
+        return (tq.tq_lora(x, a, b, base, offsets, v=v, **kw), v)
+
+    def backward():
+        return tq.tq_lora_backward(dy, x, a, b, w, None, offsets, **kw)
+
+    _runs_out_then_recovers(forward)
+    w = v.clone()
+    _runs_out_then_recovers(backward)
+
+
+@pytest.mark.parametrize("M,L,K,N,r", [(1, 2, 512, 4096, 16), (24, 5, 256, 8200, 64), (3, 1, 64, 8, 128)])
+def test_waits_of_the_kernel_for_few_rows_run_out(M, L, K, N, r):
+    need_cuda()
+    x, a, b, base, s, offsets, order = _case(M, L, K, N, r, H, M, "one")
+    _runs_out_then_recovers(lambda: (tq.tq_lora(x, a, b, base, offsets, order=order, scaling=s, path=FEW),))
+
+
+@pytest.mark.parametrize("fmt", ["ternary", "w4z"])
+@pytest.mark.parametrize("M,N,K", [(200, 1024, 384), (64, 4096, 256), (9, 72, 128), (2816, 1024, 1792)])
+def test_waits_of_the_gradient_for_x_run_out(fmt, M, N, K):
+    need_cuda()
+    w, _ = _weights(N, K, 3, fmt)
+    dy = torch.randn(M, N, generator=_gen(5), device="cuda").half()
+    _runs_out_then_recovers(lambda: (_backward(dy, w, fmt, K, path=TC),))
