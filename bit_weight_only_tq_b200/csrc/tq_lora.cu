@@ -45,7 +45,7 @@ struct LoraArgs {
   // tensor-core kernels: rows of P, of W and of base and O in whole, aligned 16-byte vectors (element by element
   // otherwise); wgrad: O aligned to them
   bool pvec, wvec, yvec;
-  // Tensor-core reduce: the largest magnitude that each CTA of a tile wrote to V (most) and found in V2 (most2),
+  // Tensor-core reduce: the largest finite magnitude that each CTA of a tile wrote to V (most) and found in V2 (most2),
   // kLoraMostPer slots per tile; null: not wanted
   const float* V2;
   float* most;

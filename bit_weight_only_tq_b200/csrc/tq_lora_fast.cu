@@ -81,6 +81,10 @@ __device__ __forceinline__ float split_scale(float most, float& inv) {
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
+// The magnitude of a number that is finite, else zero: what an adapter's power of two is made from, since an infinity in
+// one inner column must not leave the other columns without one.
+__device__ __forceinline__ float finite_abs(float x) { return fabsf(x) <= 3.402823466e38f ? fabsf(x) : 0.0f; }
+
 // Eight consecutive 16-bit elements of which `left` are there (zero past them), one by one; out of line, since what
 // runs beside it is slower for the code.
 __device__ __noinline__ uint4 load8_any(const uint16_t* p, int64_t left) {
@@ -576,8 +580,8 @@ lora_tc_kernel(const __grid_constant__ LoraSums sums_of, const int S) {
       const int64_t at = (pos0 + r) * a.rank + j;
       const float o = none ? 0.0f : f * v;
       a.V[at] = o;
-      most = fmaxf(most, fabsf(o));
-      if (a.most2) most2 = fmaxf(most2, fabsf(a.V2[at]));
+      most = fmaxf(most, finite_abs(o));
+      if (a.most2) most2 = fmaxf(most2, finite_abs(a.V2[at]));
     }
   };
   auto sums = [&](int j0, float (&v)[8]) {
@@ -609,10 +613,11 @@ lora_tc_kernel(const __grid_constant__ LoraSums sums_of, const int S) {
               float4 o = make_float4(f * v[4 * h], f * v[4 * h + 1], f * v[4 * h + 2], f * v[4 * h + 3]);
               if (none) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               *reinterpret_cast<float4*>(a.V + at) = o;
-              most = fmaxf(fmaxf(fmaxf(fabsf(o.x), fabsf(o.y)), fmaxf(fabsf(o.z), fabsf(o.w))), most);
+              most = fmaxf(fmaxf(fmaxf(finite_abs(o.x), finite_abs(o.y)), fmaxf(finite_abs(o.z), finite_abs(o.w))), most);
               if (a.most2) {
                 const float4 p = *reinterpret_cast<const float4*>(a.V2 + at);
-                most2 = fmaxf(fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(p.z), fabsf(p.w))), most2);
+                most2 =
+                    fmaxf(fmaxf(fmaxf(finite_abs(p.x), finite_abs(p.y)), fmaxf(finite_abs(p.z), finite_abs(p.w))), most2);
               }
             }
         } else if (kW && a.wj == 1 && (a.rank & 7) == 0 && yvec) {  // dB: eight consecutive elements of a row

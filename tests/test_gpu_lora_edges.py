@@ -1,18 +1,20 @@
 """The adapters' calls and the products' gradient for x at the edges of what they allow: operands of different alignment in one
-call, bounded waits that run out."""
+call, bounded waits that run out, non-finite numbers.  The bounds are in lora_util.py."""
 import contextlib
 
+import numpy as np
 import pytest
 import torch
 
 import bit_weight_only_tq_b200 as tq
+import lora_util as O
 from gpu_util import gpu, need_cuda
-from test_gpu_lora import _case, _gen, _shifted
+from test_gpu_lora import _backward64, _case, _gen, _shifted
 from test_gpu_lora_more import _backward, _weights
 
 pytestmark = gpu
 H, B = torch.float16, torch.bfloat16
-TC, FEW = tq.PATH_PREFILL, tq.PATH_DECODE
+ANY, TC, FEW = tq.PATH_GENERIC, tq.PATH_PREFILL, tq.PATH_DECODE
 
 
 # ------------------------------------------------------------------------------------------ alignment
@@ -107,3 +109,44 @@ def test_waits_of_the_gradient_for_x_run_out(fmt, M, N, K):
     w, _ = _weights(N, K, 3, fmt)
     dy = torch.randn(M, N, generator=_gen(5), device="cuda").half()
     _runs_out_then_recovers(lambda: (_backward(dy, w, fmt, K, path=TC),))
+
+
+# ------------------------------------------------------------------------------------------ non-finite numbers
+@pytest.mark.parametrize("path", [ANY, TC])
+@pytest.mark.parametrize("dtype", [H, B])
+@pytest.mark.parametrize("xs,as_,ds,bs", [(14, 3, -9, -8),       # v about 1e5
+                                          (-9, 0, 7, 11),        # dv about 4e5
+                                          (-13, -10, 6, 0),      # v about 1e-7
+                                          (0, 0, -13, -8)])      # dv about 1e-6
+def test_a_non_finite_inner_column_leaves_the_others_right(path, dtype, xs, as_, ds, bs):
+    """An infinity in one row of A (one column of B) makes one inner column of v (of dv) non-finite in all of an adapter's rows.
+    The other columns of dB (rows of dA), made of numbers that fp16 holds only with a power of two of their own, are as if it
+    were not there."""
+    need_cuda()
+    M, L, K, N, r, bad = 200, 2, 128, 72, 8, 3
+    x, a, b, base, s, offsets, order = _case(M, L, K, N, r, dtype, 44)
+    to = lambda t, e: (t.float().clamp(-3, 3) * 2.0 ** e).to(dtype)
+    x, a, b, dy = to(x, xs), to(a, as_), to(b, bs), to(base, ds)
+    assert all(torch.isfinite(t).all() for t in (x, a, b, dy))
+    rest = [j for j in range(r) if j != bad]
+    v = torch.zeros(M, r, device="cuda")
+    kw = dict(order=order, scaling=s, path=path)
+    for hit in ("none", "a", "b"):
+        a_, b_ = a.clone(), b.clone()
+        if hit == "a":
+            a_[0, bad, 5] = float("inf")
+        if hit == "b":
+            b_[0, 7, bad] = float("-inf")
+        tq.tq_lora(x, a_, b_, None, offsets, v=v, **kw)
+        _, da, db = tq.tq_lora_backward(dy, x, a_, b_, v, None, offsets, need_dx=False, **kw)
+        if hit == "none":
+            want = _backward64(dy, x, a, b, v, None, s, offsets, order, 0.0, 0, 0)
+            assert all(np.abs(w).max() < 60000 for w, _ in want[1:])
+        if hit == "a":
+            assert not torch.isfinite(db[0, :, bad]).any()
+        if hit == "b":
+            assert not torch.isfinite(da[0, bad]).any()
+        for l in range(L):
+            ja, jb = rest if (hit, l) == ("b", 0) else range(r), rest if (hit, l) == ("a", 0) else range(r)
+            for got, (w, t), at in ((da, want[1], (l, list(ja))), (db, want[2], (l, slice(None), list(jb)))):
+                O.check(O.f64(got)[at], w[at], t[at], f"{hit}, adapter {l}")
