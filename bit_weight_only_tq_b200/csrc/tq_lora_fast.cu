@@ -534,6 +534,8 @@ lora_tc_kernel(const __grid_constant__ LoraSums sums_of, const int S) {
     const uint32_t base = smem_u32(sm);
     int s = 0;
     uint32_t parity = 0u;
+    // as the loaders do: the limit of a wait is for this kernel's own stages, not for the kernels ahead
+    if (kW && a.behind) pdl_wait_prior_grids();
     for (int i = 0; i < ns && ok; ++i) {
       ok = mbar_wait(&full[s], parity);
       if (!ok) break;
@@ -1178,6 +1180,12 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
     int s = 0, hs = 0, seg = 0;
     uint32_t parity = 1u, hparity = 0u;
     int64_t done = 0;  // blocks requested in earlier runs
+    // Whatever waits for V, directly or through the stages of W, first waits for the kernels ahead, without a limit.
+    bool waited = false;
+    auto wait_ahead = [&]() {
+      if (!waited) pdl_wait_prior_grids();
+      waited = true;
+    };
     for (int64_t run = run0; run < run1;) {
       const int64_t tn = run / nblk, c_begin = (run - tn * nblk) * kXpCols;
       const int nb = static_cast<int>(run1 - run < nblk * (tn + 1) - run ? run1 - run : nblk * (tn + 1) - run);
@@ -1199,7 +1207,10 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
       if (kWA) load_a(0);
       for (int b = 0; b < nb + L::kLag; ++b) {
         if (b < nb) {
-          if (ok && done + b >= kXpRing) ok = mbar_wait(&wempty[s], parity);
+          if (done + b >= kXpRing) {
+            wait_ahead();
+            if (ok) ok = mbar_wait(&wempty[s], parity);
+          }
           uint8_t* st = sm + L::kOffW + s * L::kTileW;
           if (kWA) {
             // columns 8 u + 2 j + e of a block of 32 to 8 j + 2 u + e: piece j of the chunk to 16-byte chunk j of the
@@ -1245,6 +1256,7 @@ __global__ void __launch_bounds__(kXpThreads, 1) lora_expand_tc_kernel(const Lor
         if (warp == kXpEpi) {
           // the MMAs of the block handed over: four buffers of D keep the epilogue busy while this warp waits
           const int d = b - L::kLag;
+          wait_ahead();
           ok = ok && (d > 0 || mbar_wait(vfull, static_cast<uint32_t>(seg & 1))) && mbar_wait(&wfull[hs], hparity) &&
                (done + d < kXpRing || mbar_wait(&dempty[hs], hparity ^ 1u));
           if (lane == 0 && ok) {

@@ -111,6 +111,35 @@ def test_waits_of_the_gradient_for_x_run_out(fmt, M, N, K):
     _runs_out_then_recovers(lambda: (_backward(dy, w, fmt, K, path=TC),))
 
 
+@pytest.mark.parametrize("M,K,N,p", [(128, 1 << 22, 4096, 0.0), (1 << 22, 128, 64, 0.25)])
+def test_waits_do_not_count_the_kernels_ahead(M, K, N, p):
+    """Kernels of a call start before the ones ahead of them end: the limit of their waits (here 0.2 ms) is for their own
+    stages, however long the others take (here, with eight CTAs at work, more than a millisecond)."""
+    need_cuda()
+    r = 1
+    x = torch.zeros(M, K, dtype=H, device="cuda")
+    x[:, :128] = torch.randn(M, 128, generator=_gen(1), device="cuda").half()
+    a, b = torch.randn(1, r, K, generator=_gen(2), device="cuda").half(), torch.randn(1, N, r, generator=_gen(3), device="cuda").half()
+    dy = torch.randn(M, N, generator=_gen(4), device="cuda").half() * 0.01
+    offsets = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    rng = torch.tensor([5, 6], dtype=torch.int64, device="cuda")
+    v = torch.zeros(M, r, device="cuda")
+
+    def run():
+        out = tq.tq_lora(x, a, b, None, offsets, p=p, rng=rng, v=v, path=TC)
+        return (out, *tq.tq_lora_backward(dy, x, a, b, v, None, offsets, p=p, rng=rng, need_dx=False, path=TC)[1:])
+
+    want = run()
+    assert tq.tq_device_status() == 0
+    assert tq.lib.tq_debug_set_wait_limit(400_000) == 0
+    try:
+        got = run()
+        assert tq.tq_device_status() == 0
+    finally:
+        assert tq.lib.tq_debug_set_wait_limit(0) == 0
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
 # ------------------------------------------------------------------------------------------ non-finite numbers
 @pytest.mark.parametrize("path", [ANY, TC])
 @pytest.mark.parametrize("dtype", [H, B])
