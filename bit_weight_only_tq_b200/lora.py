@@ -200,7 +200,8 @@ def tq_gemm_backward(dy: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor
 def w4g_gemm_backward(dy: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros=None, dx=None,
                       path: int = PATH_AUTO, stream=None, rows=None) -> torch.Tensor:
     """Gradient for x of w4g_gemm (zeros: of w4g_gemm_zp): dx [M, K] = dy [M, N] What, fp16.  rows: as in
-    tq_gemm_backward."""
+    tq_gemm_backward.  With weights in activation order (w4g_repack_act_order) the columns of dx are those of
+    tq_permute_columns(x, perm): tq_permute_columns(dx, inverse of perm) is the gradient for x."""
     dev = _device()
     M, N = _shape2(dy, "dy")
     K = 8 * _shape2(qweight, "qweight")[1]

@@ -120,6 +120,8 @@ TQ_API int tq_dropout(const void* x, int dtype, void* out, double p, const int64
 /* --------------------------------------------------------------------------------------------
  * tq_gemm_backward / w4g_gemm_backward -- dx = dy What, the gradient for x of tq_gemm / w4g_gemm / w4g_gemm_zp
  * (that of bias is the sum of dy's rows; the packed weights have none).
+ * A matrix in activation order (w4g_repack_act_order) gives the gradient of the permuted columns x_out[m, j] = x[m,
+ * perm[j]]: tq_permute_columns with the inverse permutation (inv[perm[j]] = j) makes it that of x.
  *   dy       fp16 [M, N]
  *   packed, scale / qweight, scales, zeros   as in the products (zeros NULL: symmetric)
  *   dx       fp16 [M, K], written in full.  Must not overlap dy.

@@ -164,6 +164,25 @@ def test_gradient_for_x_of_many_weight_rows(M, N, K, fmt):
     assert tq.tq_device_status() == 0
 
 
+@pytest.mark.parametrize("zero_point", [False, True])
+def test_gradient_through_activation_order(zero_point):
+    need_cuda()
+    M, N, K = 70, 200, 384
+    w = 0.05 * torch.randn(N, K, generator=_gen(1), device="cuda")
+    perm = torch.randperm(K, generator=torch.Generator().manual_seed(2)).to(torch.int32).cuda()
+    q, sc, z, _ = tq.w4g_quantize_pack_ex(w, zero_point=zero_point, perm=perm)
+    q = tq.w4g_repack_act_order(q, perm)
+    dy = torch.randn(M, N, generator=_gen(3), device="cuda").half()
+    inverse = torch.empty_like(perm)
+    inverse[perm.long()] = torch.arange(K, dtype=torch.int32, device="cuda")
+    dx = tq.tq_permute_columns(tq.w4g_gemm_backward(dy, q, sc, zeros=z), inverse)
+    w64, d = np.empty((N, K)), O.f64(dy)
+    w64[:, perm.cpu().numpy()] = O.w4_values(q, sc, z)           # in the order of x
+    assert np.abs(w64 - O.f64(w)).max() < 0.05                   # the matrix that was packed
+    squares = d ** 2 @ w64 ** 2
+    O.check(dx, d @ w64, _rounded(d @ w64, _e(N, squares) + 6 * 2.0 ** -11 * np.sqrt(squares), H))
+
+
 # ------------------------------------------------------------------------------------------ one launch for dA and dB
 @pytest.mark.parametrize("shape", [(5, 2, 7, 3, 5), (70, 2, 33, 128, 33), (70, 2, 136, 67, 16), (300, 4, 1001, 264, 16),
                                    (260, 2, 128, 515, 64), (140, 3, 650, 1026, 128), (130, 2, 264, 129, 8)], ids=str)
