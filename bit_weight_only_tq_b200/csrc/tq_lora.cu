@@ -2,9 +2,10 @@
 // shape and alignment, and dropout.
 //
 // Forward and backward are four forms of three sums, over the rows m(r) of the sorted positions r of each adapter l:
-//   reduce   V[r, j]  = f sum_c P[m, c] W_l(c, j)        v: P = drop(x), W = A;     dv: P = dy, W = B
-//   expand   O[m, c]  = base[m, c] + f sum_j V[r, j] W_l(c, j)   out: V = v, W = B;  dx: V = dv, W = A, dropout of
-//   the result wgrad    G_l(c, j) = f sum_r P[m, c] V[r, j]         dA: P = drop(x), V = dv;   dB: P = dy, V = v
+//   reduce   V[r, j]   = f sum_c P[m, c] W_l(c, j)               v: P = drop(x), W = A;  dv: P = dy, W = B
+//   expand   O[m, c]   = base[m, c] + f sum_j V[r, j] W_l(c, j)  out: V = v, W = B;      dx: V = dv, W = A, the sum dropped
+//   wgrad    G_l(c, j) = f sum_r P[m, c] V[r, j]                 dA: P = drop(x), V = dv;  dB: P = dy, V = v
+//
 // with W(c, j) stored as A [rank, C] (column c of row j) or as B [C, rank].  The factors that do not depend on the
 // summation index (scaling, 1 / (1 - p)) are applied to the fp32 sum.
 #include <cuda_bf16.h>

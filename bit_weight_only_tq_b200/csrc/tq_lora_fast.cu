@@ -6,8 +6,11 @@
 // the offsets, so that one captured graph serves any plan.
 //
 // v and dv are fp32.  As operands of a 16-bit product they are split, v s = hi + lo with hi = round(v s), lo =
-// round(v s - hi) and s a power of two (fp16 only: bf16 has the exponents of fp32), which keeps 22 (fp16) or 16
-// (bf16) bits; hi and lo enter the same fp32 sum, and 1 / s is applied to it, exactly.
+// round(v s - hi) and s a power of two (fp16 only: bf16 has the exponents of fp32), which keeps them to 2^-22 (fp16) or
+// 2^-16 (bf16) of each; hi and lo enter the same fp32 sum, and 1 / s is applied to it, exactly.  s is a row's own in
+// expand and in the kernel for few rows.  In wgrad, which sums over rows, it is an adapter's: the last half
+// step of lo is 2^-25 beside a largest number of 2^14 or more, so that up to 2^-39 of that one is left out.  A third
+// part would keep 24 bits of bf16 too and cost half as many products again; the outputs' own rounding is far above.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -924,6 +927,9 @@ cudaError_t launch_lora_split(bool bf16, bool both, const LoraWorkspace& w, cons
 // fragment layout of m16n8 (16x256b), which gives a lane columns 2 t, 2 t + 1 of each n8 tile; W's columns are dealt
 // to four n8 tiles so that these are eight consecutive ones: column c = 8 u + 2 j + e of a block of 32 is column 2 u
 // + e of tile j.  base is requested two blocks ahead.
+// At 96 registers the forms with W as A spill where they drop, in bf16 (78 bytes stored and 180 loaded at ranks up to
+// 64, 104 and 216 at 128; dx of 8192 x 4096, rank 64, 54 us, and 40 without dropout), and at rank 128 in both types (72
+// and 160 without dropout); the other bf16 forms spill 8 bytes, the fp16 ones none up to rank 64.
 // Four loader warps bring W: as B [C, rank] a column's 16-byte pieces with cp.async, as A [rank, C] through
 // registers, since pairs of columns part ways (4-byte cp.async took 78 cycles an instruction).  Only barriers of
 // single stages tie the warps.

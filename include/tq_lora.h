@@ -26,11 +26,21 @@
  * Positions before offsets[0] and from offsets[L] on belong to no adapter: their rows get the base alone.
  * The rows that `order` names are distinct; an entry outside [0, M) names no row.
  *
- * Types: x, A, B, base, out, dy and the gradients have one dtype, TQ_F16 or TQ_BF16.  Sums are in fp32, v and dv
+ * Types: x, A, B, base, out, dy and the gradients have one dtype, TQ_F16 or TQ_BF16 (the packed products and their
+ * gradient for x are fp16: beside them bf16 adapters need base and base_dx as bf16 copies).  Sums are in fp32, v and dv
  * are kept in fp32, and every output is rounded once.  Where v and dv enter a tensor-core product, each is
- * the sum of two 16-bit numbers: 22 bits (fp16) or 16 bits (bf16) of it.  A tensor core cuts its fp32 sum off
- * after every 16 products instead of rounding it: on PREFILL a sum of n products comes out smaller by up to about
- * n 2^-29 of its value (v of 16384 columns: 2e-5; a split over CTAs divides that).
+ * the sum of two 16-bit numbers, off by at most 2^-22 (fp16) or 2^-16 (bf16) of it; in dA and dB of fp16, where one
+ * power of two serves all of an adapter's numbers, by 2^-39 of the largest finite one where that is more (what is
+ * below 2^-17 of the largest loses bits).
+ * A tensor core adds up to 16 products at a time and cuts the fp32 sum off instead of rounding it, by less than a unit
+ * in the last place: on PREFILL and DECODE a sum of n products is off by at most n 2^-27 of its largest partial sum,
+ * toward zero.  Measured on v, fp16, most of 4096 elements, of that partial sum: 2.8e-5 for n = 4096 terms of one sign,
+ * 3.5e-5 for 16384, 7.9e-5 for 65536 (a split over CTAs makes the parts shorter); of random sign 0.7e-5, 1.6e-5 and
+ * 4.1e-5.  GENERIC rounds each addition.
+ *
+ * Numbers that are not finite: an output element in whose formula they do not occur is as without them; one that the
+ * formula makes infinite or NaN is not finite, but an infinity may come as NaN (on PREFILL and DECODE an infinite
+ * operand meets both parts of v or dv, which may differ in sign or be zero).
  *
  * Dropout: element e = k % 8 of the group i = m ceil(K / 8) + k / 8 of x [M, K] takes the 16 bits
  *   (e even: low half, odd: high half) of word e / 2 of Philox4x32-10 (Salmon, Moraes, Dror, Shaw: Parallel
@@ -65,7 +75,8 @@ extern "C" {
  *   out      [M, N], written in full.  Must not overlap x, a or b.
  *   v        fp32 [M, rank], or NULL: drop(x) A^T by sorted position, without `scaling`, written for
  *            the positions of adapters; tq_lora_backward reads it.  PREFILL and GENERIC need it
- *            (TQ_ERR_NULL); AUTO without it takes DECODE where it can.
+ *            (TQ_ERR_NULL); AUTO without it takes DECODE where it can, however many rows there are: give
+ *            it for more than a few rows per adapter, since DECODE reads an adapter's weights once per eight.
  *            Calls (or captured graphs) that may run at once need one each.
  *   path     TQ_PATH_AUTO, or one path (tests): DECODE takes few rows (one launch, up to 8 rows of an
  *            adapter per pass over its weights), PREFILL many (tensor cores), GENERIC is the plain form.
@@ -131,7 +142,8 @@ TQ_API int tq_dropout(const void* x, int dtype, void* out, double p, const int64
  *   path     TQ_PATH_AUTO, PREFILL (tensor cores) or GENERIC (any shape and alignment; weights enter the sum
  *            exactly).  PREFILL needs K % 64 == 0 (TQ_ERR_PATH) and 16-byte aligned weights and dx (TQ_ERR_ALIGN).
  *            There a ternary weight enters exactly and an INT4 weight (u - z) s is rounded to fp16, as on that path
- *            of w4g_gemm (scales must keep it below 65520).
+ *            of w4g_gemm (scales must keep it below 65520): dx is 2.7e-4 off relative rms where its own
+ *            rounding alone makes 2.1e-4.
  * Shapes and errors as in tq_gemm / w4g_gemm.
  * ------------------------------------------------------------------------------------------ */
 TQ_API int tq_gemm_backward(const uint16_t* dy, const uint8_t* packed, const uint16_t* scale, uint16_t* dx,
