@@ -173,7 +173,8 @@ TQ_API int w4g_gemm_ex(const uint16_t* x, const int32_t* qweight, const uint16_t
  *
  * w4g_gemm_zp / w4g_gemm_zp_ex -- y = x . What^T (+ bias) with What[n,k] = s[n, k/128] *
  *   (u[n,k] - zeros[n, k/128]) (asymmetric, consecutive groups); shapes, paths and errors as
- *   w4g_gemm / w4g_gemm_ex; zeros must not be NULL.
+ *   w4g_gemm / w4g_gemm_ex; zeros must not be NULL and hold 0 .. 15, as the packer writes them (the
+ *   tensor-core paths make 64 + z from a bit pattern that is right up to 63).
  *
  * Activation order at run time, the way the Marlin path of [VQ] §4.3 takes it: the product is
  * summed over k in the quantisation order, x . What^T = (x P) . (What P)^T, where P is the

@@ -134,7 +134,7 @@ TQ_API int tq_dropout(const void* x, int dtype, void* out, double p, const int64
  * A matrix in activation order (w4g_repack_act_order) gives the gradient of the permuted columns x_out[m, j] = x[m,
  * perm[j]]: tq_permute_columns with the inverse permutation (inv[perm[j]] = j) makes it that of x.
  *   dy       fp16 [M, N]
- *   packed, scale / qweight, scales, zeros   as in the products (zeros NULL: symmetric)
+ *   packed, scale / qweight, scales, zeros   as in the products (zeros NULL: symmetric, else 0 .. 15)
  *   dx       fp16 [M, K], written in full.  Must not overlap dy.
  *   rows     fp16 [M, N rounded up to a multiple of 8] scratch, 16-byte aligned, or NULL: PREFILL copies the rows of
  *            dy there first where N % 8 != 0 or dy is not 16-byte aligned (without it: AUTO takes GENERIC, PREFILL
